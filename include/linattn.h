@@ -25,6 +25,9 @@
  *   - Performer:  random exponential features in place of elu + 1
  *                 ("Choosing the Feature Map"), the map alone and the
  *                 attention over it.
+ * Beside them stand the selective state space scan with its short causal
+ * convolution, and the norms before and after a mixing block (see "Selective
+ * state space scan" below).
  * eps is added to the denominator after the dot product, as in the NumPy
  * listing on "Linear Attention Mechanisms" (sadullah.online), "The linear
  * attention trick".
@@ -409,6 +412,166 @@ LA_API la_status_t la_forward_noncausal_static(const void *q, const void *k, con
 
 /* Size in bytes of the per-device scratch used by la_forward_noncausal_static. */
 LA_API size_t la_forward_noncausal_static_limit(void);
+
+/*
+ * Selective state space scan and the operators around its block.  "Linear
+ * Attention Mechanisms" (dileepadev.github.io) sets the state space form
+ * h_t = A_t h_(t-1) + B_t x_t beside the gated recurrence of "Gating and
+ * Selective State Updates"; here A_t and B_t are chosen per token through a
+ * step dt_t.  Conventions of this family, besides those at the top:
+ * - Token-major tensors: x, dt, z, y [B][L][E], B_t and C_t [B][L][G][N] (each
+ *   group of E / G consecutive channels shares one), of `dtype`; for a single
+ *   token [B][E] and [B][G][N].  Parameters (A [E][N], D, dt_bias, w, bias) and
+ *   scan states [B][E][N] are fp32.
+ * - ldx, lddt, ldz, ldb, ldc: elements between consecutive tokens of that
+ *   input (the batch stride is L times it), so that slices of a projection's
+ *   output are read in place; 0 means dense rows.  A stride is a multiple of 8
+ *   and at least the row's width; outputs are dense.
+ * - Sizes: E a multiple of 8 up to 65536, E / G a multiple of 8, N in {8, 16,
+ *   32, 64}, fewer than 2^31 tokens and B E < 2^31.
+ * - lens (optional, int32 [B] in DEVICE memory, 4-byte aligned): sequence b
+ *   has lens[b] tokens (clamped to [0, L]).  Rows behind it are neither read
+ *   nor written, and the final state is the one after the last token.
+ * - fp32 arithmetic; each output is rounded once to `dtype`.  Results do not
+ *   depend on scheduling (no atomics).  Workspaces are stream-ordered
+ *   allocations from a pool the library keeps per device (up to 512 MiB held
+ *   between calls).
+ * - No written buffer may overlap any other buffer of the call (strided inputs
+ *   count from their first to their last element).
+ */
+
+/*
+ * Selective scan of whole sequences: per channel e and state n
+ *   dt_t = softplus(dt_t + dt_bias)   (softplus = 0: the plain sum)
+ *   h_t  = exp(dt_t A) h_(t-1) + dt_t x_t B_t,      h_(-1) = h0 (NULL: zeros)
+ *   y_t  = (sum_n C_t h_t + D x_t) silu(z_t)
+ * D, z and dt_bias may be NULL (no such term).  hN (optional) receives the
+ * state after the last token (h0 for no tokens), the state
+ * la_decode_selective continues from; it may not be h0 itself.  Few channels
+ * split the tokens into up to 32 parts, with a workspace of about
+ * B*31*E*(N + 1)*4 bytes at most.
+ */
+LA_API la_status_t la_forward_selective(const void *x, const void *dt, const float *A,
+                                        const void *Bm, const void *Cm, const float *D,
+                                        const void *z, const float *dt_bias, const float *h0,
+                                        const int *lens, void *y, float *hN, int B, int L, int E,
+                                        int N, int G, long long ldx, long long lddt, long long ldz,
+                                        long long ldb, long long ldc, int softplus,
+                                        la_dtype_t dtype, void *stream);
+
+/*
+ * One token of the scan, in place on the state h [B][E][N] fp32: x, dt, z, y
+ * [B][E], Bm, Cm [B][G][N].  y must not be any input.
+ */
+LA_API la_status_t la_decode_selective(const void *x, const void *dt, const float *A,
+                                       const void *Bm, const void *Cm, const float *D,
+                                       const void *z, const float *dt_bias, float *h, void *y,
+                                       int B, int E, int N, int G, long long ldx, long long lddt,
+                                       long long ldz, long long ldb, long long ldc, int softplus,
+                                       la_dtype_t dtype, void *stream);
+
+/*
+ * Gradients of la_forward_selective (every sequence of L tokens) for the
+ * upstream gradients dy of y and, optionally, dhN of the final state.  With
+ * gy_t = dy_t silu(z_t) and the adjoint state g_t = C_t gy_t + exp(dt_(t+1) A)
+ * g_(t+1) (dhN behind the last token):
+ *   dC_t = sum_e h_t gy_t,  dB_t = sum_e g_t dt_t x_t    (over a group)
+ *   du_t = sum_n g_t B_t,   w_t = g_t exp(dt_t A) h_(t-1)
+ *   dx_t = du_t dt_t + D gy_t
+ *   ddt_t = (sum_n w_t A + du_t x_t) softplus'(.),  ddt_bias = sum_t ddt_t
+ *   dA = sum_t w_t dt_t,  dD = sum_t gy_t x_t,  dz_t = dy_t (y_t before the gate) silu'(z_t)
+ *   dh0 = exp(dt_0 A) g_0.
+ * States are recomputed (the caller keeps no forward state).  dx, ddt, dz
+ * [B][L][E] and dBm, dCm [B][L][G][N] are dense, of `dtype`; dA, dD, ddt_bias
+ * and dh0 fp32.  dD, ddt_bias and dh0 may be NULL and need their input; dz is
+ * given exactly when z is.  A batch padded at the end is handled by zero rows
+ * of dy (a later token does not reach an earlier one).  The workspace is about
+ * B*L*E*(2N + 3)/16 + 2*B*L*N*E*N/1024 floats (parts of 64 tokens, 32 for
+ * N = 8).
+ */
+LA_API la_status_t la_backward_selective(
+    const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
+    const void *z, const float *dt_bias, const float *h0, const void *dy, const float *dhN,
+    void *dx, void *ddt, float *dA, void *dBm, void *dCm, float *dD, void *dz, float *ddt_bias,
+    float *dh0, int B, int L, int E, int N, int G, long long ldx, long long lddt, long long ldz,
+    long long ldb, long long ldc, int softplus, la_dtype_t dtype, void *stream);
+
+/*
+ * Short causal depthwise convolution (ahead of the scan):
+ *   y_t[e] = act(bias[e] + sum_(k < W) w[e][k] x_(t - W + 1 + k)[e]),
+ * act = SiLU when silu is nonzero, W in 2..4.  The W - 1 rows before the first
+ * token come from state [B][W-1][E] (`dtype`, oldest first; NULL: zeros).
+ * state_out (optional, not `state` itself) receives the last W - 1 rows, the
+ * state la_decode_conv continues from.  w [E][W], bias [E] (optional) fp32.
+ */
+LA_API la_status_t la_forward_conv(const void *x, const float *w, const float *bias,
+                                   const void *state, const int *lens, void *y, void *state_out,
+                                   int B, int L, int E, int W, long long ldx, int silu,
+                                   la_dtype_t dtype, void *stream);
+
+/* One token of the convolution, in place on state [B][W-1][E]: x, y [B][E]. */
+LA_API la_status_t la_decode_conv(const void *x, const float *w, const float *bias, void *state,
+                                  void *y, int B, int E, int W, long long ldx, int silu,
+                                  la_dtype_t dtype, void *stream);
+
+/*
+ * Gradients of la_forward_conv (every sequence of L tokens) for the upstream
+ * gradient dy: dx [B][L][E] and dstate [B][W-1][E] (optional, needs state) of
+ * `dtype`, dw [E][W] and dbias [E] (optional, needs bias) fp32.  A gradient of
+ * state_out is one of x's last rows (or of state's): the caller adds it there.
+ */
+LA_API la_status_t la_backward_conv(const void *x, const float *w, const float *bias,
+                                    const void *state, const void *dy, void *dx, float *dw,
+                                    float *dbias, void *dstate, int B, int L, int E, int W,
+                                    long long ldx, int silu, la_dtype_t dtype, void *stream);
+
+/*
+ * RMS norm of a mixing form's output per head, with its gate:
+ *   gate_first = 0:  o = y rsqrt(mean y^2 + eps) w silu(gate)
+ *   gate_first = 1:  o = p rsqrt(mean p^2 + eps) w,   p = y silu(gate)
+ * over rows of D values, one per (b, h, token).  y is [B][H][L][D]
+ * (heads_first, as la_forward and la_forward_gated write o) or [B][L][H][D];
+ * gate and out are token-major [B][L][H*D], as the projections before and
+ * behind it hold them; all of `dtype`.  w [H][D] fp32 (NULL: ones).  D a
+ * multiple of 8 up to 8192, H*D up to 65536, fewer than 2^31 rows; eps finite
+ * and >= 0.  out may not overlap an input.
+ */
+LA_API la_status_t la_forward_norm_gate(const void *y, const void *gate, const float *w, void *out,
+                                        int B, int H, int L, int D, int heads_first,
+                                        int gate_first, float eps, la_dtype_t dtype, void *stream);
+
+/*
+ * Gradients of la_forward_norm_gate for the upstream gradient dout [B][L][H*D]:
+ * dy (laid out as y), dgate [B][L][H*D] of `dtype` and dw [H][D] fp32
+ * (optional, needs w).
+ */
+LA_API la_status_t la_backward_norm_gate(const void *y, const void *gate, const float *w,
+                                         const void *dout, void *dy, void *dgate, float *dw, int B,
+                                         int H, int L, int D, int heads_first, int gate_first,
+                                         float eps, la_dtype_t dtype, void *stream);
+
+/*
+ * Scaled residual sum and the RMS norm ahead of the next block, over rows of E
+ * values of `dtype`:
+ *   r = residual + scale x  (residual NULL: scale x),  o = r rsqrt(mean r^2 + eps) w.
+ * The norm takes the fp32 sum; r is also written, rounded.  w [E] fp32 (NULL:
+ * ones).  E a multiple of 8 up to 8192, fewer than 2^31 rows.  o and r may not
+ * overlap an input or each other.
+ */
+LA_API la_status_t la_forward_norm_residual(const void *x, const void *residual, const float *w,
+                                            void *o, void *r, long long rows, int E, float scale,
+                                            float eps, la_dtype_t dtype, void *stream);
+
+/*
+ * Gradients of la_forward_norm_residual at the written r, for the upstream
+ * gradients dout of o and dr of r (NULL: none): dresidual = dr + the norm's
+ * gradient, dx = scale dresidual (NULL when scale is 1, where the two are
+ * equal), dw [E] fp32 (optional, needs w).
+ */
+LA_API la_status_t la_backward_norm_residual(const void *r, const float *w, const void *dout,
+                                             const void *dr, void *dresidual, void *dx, float *dw,
+                                             long long rows, int E, float scale, float eps,
+                                             la_dtype_t dtype, void *stream);
 
 /* Static, NUL-terminated description of a status code. */
 LA_API const char *la_status_string(la_status_t s);

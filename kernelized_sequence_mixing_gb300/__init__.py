@@ -17,6 +17,22 @@ Functions (same names as the C entry points, minus the ``la_`` prefix):
   favor_features(x, W, out=None)
   forward_favor(q, k, v, W, causal=True, gamma=None, eps=1e-6, out=None)
   backward(q, k, v, do, gamma=None, eps=1e-6)
+
+The selective state space scan, its short convolution and the norms around a
+block:
+  forward_selective(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True,
+                    h0=None, lens=None, out=None, return_state=False, h=None)
+  decode_selective(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus=True, out=None)
+  backward_selective(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softplus=True,
+                     h0=None, dh=None)
+  forward_conv(x, w, bias=None, silu=True, state=None, lens=None, out=None,
+               return_state=False, state_out=None)
+  decode_conv(x, w, state, bias=None, silu=True, out=None)
+  backward_conv(x, w, dy, bias=None, silu=True, state=None)
+  forward_norm_gate(y, gate, w=None, eps=1e-5, gate_first=False, heads_first=True, out=None)
+  backward_norm_gate(y, gate, do, w=None, eps=1e-5, gate_first=False, heads_first=True)
+  forward_norm_residual(x, residual=None, w=None, scale=1.0, eps=1e-5, out=None, r=None)
+  backward_norm_residual(r, do, w=None, dr=None, scale=1.0, eps=1e-5)
 """
 from __future__ import annotations
 
@@ -30,6 +46,10 @@ from . import workloads  # noqa: F401  (seeded input generators)
 
 __all__ = ["forward", "prefill_state", "decode_step", "forward_state",
            "forward_gated", "decode_gated", "favor_features", "forward_favor", "backward",
+           "forward_selective", "decode_selective", "backward_selective",
+           "forward_conv", "decode_conv", "backward_conv",
+           "forward_norm_gate", "backward_norm_gate",
+           "forward_norm_residual", "backward_norm_residual",
            "status_string",
            "device_wait_timeouts", "causal_kernel", "backward_kernel",
            "load_library", "library_path", "LinAttnError", "workloads"]
@@ -99,6 +119,27 @@ def load_library() -> ctypes.CDLL:
             lib.la_backward_kernel.restype = I
             lib.la_causal_kernel.argtypes = [I, I, I, I, I, FP, I]
             lib.la_causal_kernel.restype = I
+            LL = ctypes.c_longlong
+            lib.la_forward_selective.argtypes = [P] * 12 + [I] * 5 + [LL] * 5 + [I, I, P]
+            lib.la_forward_selective.restype = I
+            lib.la_decode_selective.argtypes = [P] * 10 + [I] * 4 + [LL] * 5 + [I, I, P]
+            lib.la_decode_selective.restype = I
+            lib.la_backward_selective.argtypes = [P] * 20 + [I] * 5 + [LL] * 5 + [I, I, P]
+            lib.la_backward_selective.restype = I
+            lib.la_forward_conv.argtypes = [P] * 7 + [I] * 4 + [LL, I, I, P]
+            lib.la_forward_conv.restype = I
+            lib.la_decode_conv.argtypes = [P] * 5 + [I] * 3 + [LL, I, I, P]
+            lib.la_decode_conv.restype = I
+            lib.la_backward_conv.argtypes = [P] * 9 + [I] * 4 + [LL, I, I, P]
+            lib.la_backward_conv.restype = I
+            lib.la_forward_norm_gate.argtypes = [P] * 4 + [I] * 6 + [F, I, P]
+            lib.la_forward_norm_gate.restype = I
+            lib.la_backward_norm_gate.argtypes = [P] * 7 + [I] * 6 + [F, I, P]
+            lib.la_backward_norm_gate.restype = I
+            lib.la_forward_norm_residual.argtypes = [P] * 5 + [LL, I, F, F, I, P]
+            lib.la_forward_norm_residual.restype = I
+            lib.la_backward_norm_residual.argtypes = [P] * 7 + [LL, I, F, F, I, P]
+            lib.la_backward_norm_residual.restype = I
             lib.la_wait_selftest.argtypes = [ctypes.c_longlong, ctypes.POINTER(I)]
             lib.la_wait_selftest.restype = I
             lib.la_device_wait_timeouts.argtypes = [I]
@@ -514,3 +555,333 @@ def wait_selftest(cycles=2_000_000) -> bool:
     gave_up = ctypes.c_int(0)
     _check("la_wait_selftest", load_library().la_wait_selftest(int(cycles), ctypes.byref(gave_up)))
     return bool(gave_up.value)
+
+
+# --- selective state space scan, short convolution, norms around a block ---
+
+
+def _tokens(fn, name, t, lead, row, dtype):
+    """The token stride (0: dense) of an input [*lead, *row] of ``dtype`` whose
+    rows are contiguous; lead is (B, L), with L token strides between
+    sequences, or (B,): dense tensors and slices of a dense tensor's rows."""
+    if tuple(t.shape) != lead + row:
+        raise ValueError(f"{fn}: {name} must have shape {lead + row}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return 0
+    stride = t.stride()
+    width = 1
+    for size, st in zip(reversed(row), reversed(stride)):
+        if size > 1 and st != width:
+            raise ValueError(f"{fn}: the values of each token of {name} must be contiguous")
+        width *= size
+    ld = width
+    for i in range(len(lead) - 1, -1, -1):
+        if lead[i] > 1:
+            ld = stride[i]
+            break
+    if ld < width or ld % 8 or (len(lead) == 2 and lead[0] > 1 and lead[1] > 1
+                                and stride[0] != lead[1] * ld):
+        raise ValueError(f"{fn}: {name} must be dense or a slice of a dense tensor's rows, with a "
+                         f"multiple of 8 elements between tokens (strides {stride})")
+    return ld
+
+
+def _param(fn, name, t, shape):
+    """An optional fp32 parameter or state: exactly ``shape``, contiguous."""
+    if t is not None:
+        _expect(fn, name, t, shape, torch.float32)
+
+
+def _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, dims):
+    """Checks shared by the scan's entry points; ``dims`` is 3 for sequences,
+    2 for one token.  Returns (lead, E, N, G, token strides)."""
+    if x.dim() != dims or Bm.dim() != dims + 1 or A.dim() != 2:
+        tok = "B, L" if dims == 3 else "B"
+        raise ValueError(f"{fn}: expected x, dt: [{tok}, E], A: [E, N] and Bm, Cm: [{tok}, G, N]")
+    _dtype_code(x)
+    lead, E = tuple(x.shape[:-1]), x.shape[-1]
+    G, N = Bm.shape[-2:]
+    lds = (_tokens(fn, "x", x, lead, (E,), x.dtype), _tokens(fn, "dt", dt, lead, (E,), x.dtype),
+           _tokens(fn, "z", z, lead, (E,), x.dtype) if z is not None else 0,
+           _tokens(fn, "Bm", Bm, lead, (G, N), x.dtype),
+           _tokens(fn, "Cm", Cm, lead, (G, N), x.dtype))
+    _param(fn, "A", A, (E, N))
+    _param(fn, "D", D, (E,))
+    _param(fn, "dt_bias", dt_bias, (E,))
+    return lead, E, N, G, lds
+
+
+def _lens(fn, lens, B):
+    if lens is not None:
+        _expect(fn, "lens", lens, (B,), torch.int32)
+
+
+def forward_selective(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, h0=None,
+                      lens=None, out=None, return_state=False, h=None):
+    """Selective state space scan: dt_t = softplus(dt_t + dt_bias) (or the
+    sum), h_t = exp(dt_t A) h_(t-1) + dt_t x_t B_t, y_t = (C_t . h_t + D x_t)
+    silu(z_t).  x, dt, z: [B, L, E]; Bm, Cm: [B, L, G, N] CUDA tensors of one
+    dtype, dense or slices of a dense tensor's rows; A: [E, N], D, dt_bias: [E]
+    and h0: [B, E, N] float32; lens: [B] int32 tokens per sequence (rows behind
+    are neither read nor written).  Returns y, or (y, h [B, E, N] float32) with
+    the state after the last token when return_state is true (or h is given)."""
+    fn = "forward_selective"
+    (B, L), E, N, G, lds = _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    _param(fn, "h0", h0, (B, E, N))
+    _param(fn, "h", h, (B, E, N))
+    _lens(fn, lens, B)
+    if out is not None:
+        _expect(fn, "out", out, (B, L, E), x.dtype)
+    dev = _one_device(fn, (("x", x), ("dt", dt), ("A", A), ("Bm", Bm), ("Cm", Cm), ("D", D),
+                           ("z", z), ("dt_bias", dt_bias), ("h0", h0), ("lens", lens),
+                           ("out", out), ("h", h)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((B, L, E), dtype=x.dtype, device=dev)
+        if h is None and return_state:
+            h = torch.empty((B, E, N), dtype=torch.float32, device=dev)
+        _check("la_forward_selective", lib.la_forward_selective(
+            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+            _ptr(h0), _ptr(lens), _ptr(out), _ptr(h), B, L, E, N, G, *lds,
+            1 if softplus else 0, _DTYPES[x.dtype], _stream(dev)))
+    return out if h is None else (out, h)
+
+
+def decode_selective(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus=True, out=None):
+    """One token of the scan, in place on h [B, E, N] float32.  x, dt, z:
+    [B, E]; Bm, Cm: [B, G, N]; otherwise as forward_selective.  Returns
+    y: [B, E]."""
+    fn = "decode_selective"
+    (B,), E, N, G, lds = _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    _expect(fn, "h", h, (B, E, N), torch.float32)
+    if out is not None:
+        _expect(fn, "out", out, (B, E), x.dtype)
+    dev = _one_device(fn, (("x", x), ("dt", dt), ("A", A), ("Bm", Bm), ("Cm", Cm), ("h", h),
+                           ("D", D), ("z", z), ("dt_bias", dt_bias), ("out", out)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((B, E), dtype=x.dtype, device=dev)
+        _check("la_decode_selective", lib.la_decode_selective(
+            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+            _ptr(h), _ptr(out), B, E, N, G, *lds, 1 if softplus else 0, _DTYPES[x.dtype],
+            _stream(dev)))
+    return out
+
+
+def backward_selective(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softplus=True,
+                       h0=None, dh=None):
+    """Gradients of y (and the final state) = forward_selective(...) for the
+    upstream gradients dy [B, L, E] of y and, if given, dh [B, E, N] float32
+    of the final state.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0);
+    dD, dz, ddt_bias and dh0 are None where their input is."""
+    fn = "backward_selective"
+    (B, L), E, N, G, lds = _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    _expect(fn, "dy", dy, (B, L, E), x.dtype)
+    _param(fn, "h0", h0, (B, E, N))
+    _param(fn, "dh", dh, (B, E, N))
+    dev = _one_device(fn, (("x", x), ("dt", dt), ("A", A), ("Bm", Bm), ("Cm", Cm), ("dy", dy),
+                           ("D", D), ("z", z), ("dt_bias", dt_bias), ("h0", h0), ("dh", dh)))
+    lib = load_library()
+    f = torch.float32
+    with torch.cuda.device(dev):
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        dx, ddt = new((B, L, E), x.dtype), new((B, L, E), x.dtype)
+        dA, dB, dC = new((E, N), f), new((B, L, G, N), x.dtype), new((B, L, G, N), x.dtype)
+        dD = new((E,), f) if D is not None else None
+        dz = new((B, L, E), x.dtype) if z is not None else None
+        dbias = new((E,), f) if dt_bias is not None else None
+        dh0 = new((B, E, N), f) if h0 is not None else None
+        _check("la_backward_selective", lib.la_backward_selective(
+            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+            _ptr(h0), _ptr(dy), _ptr(dh), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC),
+            _ptr(dD), _ptr(dz), _ptr(dbias), _ptr(dh0), B, L, E, N, G, *lds,
+            1 if softplus else 0, _DTYPES[x.dtype], _stream(dev)))
+    return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
+
+
+def _conv_args(fn, x, w, bias, dims):
+    if x.dim() != dims or w.dim() != 2:
+        raise ValueError(f"{fn}: expected x: [{'B, L' if dims == 3 else 'B'}, E] and w: [E, W]")
+    _dtype_code(x)
+    lead, E = tuple(x.shape[:-1]), x.shape[-1]
+    W = w.shape[1]
+    _param(fn, "w", w, (E, W))
+    _param(fn, "bias", bias, (E,))
+    return lead, E, W, _tokens(fn, "x", x, lead, (E,), x.dtype)
+
+
+def forward_conv(x, w, bias=None, silu=True, state=None, lens=None, out=None,
+                 return_state=False, state_out=None):
+    """Short causal depthwise convolution: y_t = act(bias + sum_k w[:, k]
+    x_(t - W + 1 + k)), act = SiLU (or none).  x: [B, L, E] (dense, or a slice
+    of a dense tensor's rows), w: [E, W] float32 with W in 2..4, bias: [E]
+    float32, state: [B, W - 1, E] of x's dtype, the rows before the first
+    token (zeros without it), lens: [B] int32 tokens per sequence.  Returns y,
+    or (y, state after the last token) when return_state is true (or state_out
+    is given)."""
+    fn = "forward_conv"
+    (B, L), E, W, ld = _conv_args(fn, x, w, bias, 3)
+    for n, t in (("state", state), ("state_out", state_out)):
+        if t is not None:
+            _expect(fn, n, t, (B, W - 1, E), x.dtype)
+    _lens(fn, lens, B)
+    if out is not None:
+        _expect(fn, "out", out, (B, L, E), x.dtype)
+    dev = _one_device(fn, (("x", x), ("w", w), ("bias", bias), ("state", state), ("lens", lens),
+                           ("out", out), ("state_out", state_out)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((B, L, E), dtype=x.dtype, device=dev)
+        if state_out is None and return_state:
+            state_out = torch.empty((B, max(W - 1, 0), E), dtype=x.dtype, device=dev)
+        _check("la_forward_conv", lib.la_forward_conv(
+            _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(lens), _ptr(out), _ptr(state_out),
+            B, L, E, W, ld, 1 if silu else 0, _DTYPES[x.dtype], _stream(dev)))
+    return out if state_out is None else (out, state_out)
+
+
+def decode_conv(x, w, state, bias=None, silu=True, out=None):
+    """One token of the convolution, in place on state [B, W - 1, E]: x [B, E].
+    Returns y: [B, E]."""
+    fn = "decode_conv"
+    (B,), E, W, ld = _conv_args(fn, x, w, bias, 2)
+    _expect(fn, "state", state, (B, W - 1, E), x.dtype)
+    if out is not None:
+        _expect(fn, "out", out, (B, E), x.dtype)
+    dev = _one_device(fn, (("x", x), ("w", w), ("state", state), ("bias", bias), ("out", out)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((B, E), dtype=x.dtype, device=dev)
+        _check("la_decode_conv", lib.la_decode_conv(
+            _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(out), B, E, W, ld,
+            1 if silu else 0, _DTYPES[x.dtype], _stream(dev)))
+    return out
+
+
+def backward_conv(x, w, dy, bias=None, silu=True, state=None):
+    """Gradients (dx, dw, dbias, dstate) of forward_conv(x, w, bias, silu,
+    state) for the upstream gradient dy [B, L, E]; dbias and dstate are None
+    where their input is."""
+    fn = "backward_conv"
+    (B, L), E, W, ld = _conv_args(fn, x, w, bias, 3)
+    _expect(fn, "dy", dy, (B, L, E), x.dtype)
+    if state is not None:
+        _expect(fn, "state", state, (B, W - 1, E), x.dtype)
+    dev = _one_device(fn, (("x", x), ("w", w), ("dy", dy), ("bias", bias), ("state", state)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        dx = torch.empty((B, L, E), dtype=x.dtype, device=dev)
+        dw = torch.empty((E, W), dtype=torch.float32, device=dev)
+        dbias = torch.empty((E,), dtype=torch.float32, device=dev) if bias is not None else None
+        dstate = torch.empty_like(state) if state is not None else None
+        _check("la_backward_conv", lib.la_backward_conv(
+            _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(dbias),
+            _ptr(dstate), B, L, E, W, ld, 1 if silu else 0, _DTYPES[x.dtype], _stream(dev)))
+    return dx, dw, dbias, dstate
+
+
+def _norm_gate_args(fn, y, gate, w, heads_first, extra=()):
+    if y.dim() != 4:
+        raise ValueError(f"{fn}: expected y: [B, H, L, D] (heads_first) or [B, L, H, D]")
+    _contig("y", y)
+    _dtype_code(y)
+    B, H, L, D = y.shape
+    if not heads_first:
+        H, L = L, H
+    for n, t in (("gate", gate),) + tuple(extra):
+        if t is not None:
+            _expect(fn, n, t, (B, L, H * D), y.dtype)
+    _param(fn, "w", w, (H, D))
+    return B, H, L, D
+
+
+def forward_norm_gate(y, gate, w=None, eps=1e-5, gate_first=False, heads_first=True, out=None):
+    """RMS norm of each head's rows with a SiLU gate: norm(y) w silu(gate), or
+    norm(y silu(gate)) w when gate_first.  y: [B, H, L, D] as forward() returns
+    it, or [B, L, H, D] with heads_first=False; gate: [B, L, H*D]; one dtype;
+    w: [H, D] float32.  Returns o: [B, L, H*D]."""
+    fn = "forward_norm_gate"
+    B, H, L, D = _norm_gate_args(fn, y, gate, w, heads_first, (("out", out),))
+    dev = _one_device(fn, (("y", y), ("gate", gate), ("w", w), ("out", out)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((B, L, H * D), dtype=y.dtype, device=dev)
+        _check("la_forward_norm_gate", lib.la_forward_norm_gate(
+            _ptr(y), _ptr(gate), _ptr(w), _ptr(out), B, H, L, D, 1 if heads_first else 0,
+            1 if gate_first else 0, float(eps), _DTYPES[y.dtype], _stream(dev)))
+    return out
+
+
+def backward_norm_gate(y, gate, do, w=None, eps=1e-5, gate_first=False, heads_first=True):
+    """Gradients (dy, dgate, dw) of forward_norm_gate for the upstream gradient
+    do [B, L, H*D]; dy is laid out as y, dw is None without w."""
+    fn = "backward_norm_gate"
+    B, H, L, D = _norm_gate_args(fn, y, gate, w, heads_first, (("do", do),))
+    dev = _one_device(fn, (("y", y), ("gate", gate), ("do", do), ("w", w)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        dy, dgate = torch.empty_like(y), torch.empty_like(gate)
+        dw = torch.empty((H, D), dtype=torch.float32, device=dev) if w is not None else None
+        _check("la_backward_norm_gate", lib.la_backward_norm_gate(
+            _ptr(y), _ptr(gate), _ptr(w), _ptr(do), _ptr(dy), _ptr(dgate), _ptr(dw), B, H, L, D,
+            1 if heads_first else 0, 1 if gate_first else 0, float(eps), _DTYPES[y.dtype],
+            _stream(dev)))
+    return dy, dgate, dw
+
+
+def _rows(fn, name, t, others, w):
+    """Rows [..., E] of one dtype and shape; returns (rows, E)."""
+    if t.dim() < 1:
+        raise ValueError(f"{fn}: expected {name}: [..., E]")
+    _contig(name, t)
+    _dtype_code(t)
+    for n, o in others:
+        if o is not None:
+            _expect(fn, n, o, t.shape, t.dtype)
+    E = t.shape[-1]
+    _param(fn, "w", w, (E,))
+    return (t.numel() // E if E else 0), E
+
+
+def forward_norm_residual(x, residual=None, w=None, scale=1.0, eps=1e-5, out=None, r=None):
+    """r = residual + scale x (scale x without a residual) and its RMS norm
+    o = r rsqrt(mean r^2 + eps) w over the last dimension.  x, residual:
+    [..., E] of one dtype; w: [E] float32.  Returns (o, r)."""
+    fn = "forward_norm_residual"
+    rows, E = _rows(fn, "x", x, (("residual", residual), ("out", out), ("r", r)), w)
+    dev = _one_device(fn, (("x", x), ("residual", residual), ("w", w), ("out", out), ("r", r)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(x)
+        if r is None:
+            r = torch.empty_like(x)
+        _check("la_forward_norm_residual", lib.la_forward_norm_residual(
+            _ptr(x), _ptr(residual), _ptr(w), _ptr(out), _ptr(r), rows, E, float(scale),
+            float(eps), _DTYPES[x.dtype], _stream(dev)))
+    return out, r
+
+
+def backward_norm_residual(r, do, w=None, dr=None, scale=1.0, eps=1e-5):
+    """Gradients (dresidual, dx, dw) of forward_norm_residual at its r, for the
+    upstream gradients do of o and dr of r (None: none).  With scale = 1 dx is
+    dresidual itself; dw is None without w."""
+    fn = "backward_norm_residual"
+    rows, E = _rows(fn, "r", r, (("do", do), ("dr", dr)), w)
+    dev = _one_device(fn, (("r", r), ("do", do), ("dr", dr), ("w", w)))
+    lib = load_library()
+    with torch.cuda.device(dev):
+        dres = torch.empty_like(r)
+        dx = torch.empty_like(r) if scale != 1.0 else None
+        dw = torch.empty((E,), dtype=torch.float32, device=dev) if w is not None else None
+        _check("la_backward_norm_residual", lib.la_backward_norm_residual(
+            _ptr(r), _ptr(w), _ptr(do), _ptr(dr), _ptr(dres), _ptr(dx), _ptr(dw), rows, E,
+            float(scale), float(eps), _DTYPES[r.dtype], _stream(dev)))
+    return dres, (dres if dx is None else dx), dw

@@ -1,0 +1,44 @@
+// Sums of fp32 records over the record index, in a fixed order (the second
+// stage of the parameter gradients).
+#include "kernels.h"
+
+namespace linattn {
+namespace {
+
+constexpr int kCols = 32, kSlices = 32;
+
+// 32 columns per CTA; slice y adds records y, y + 32, ..., then the slices are
+// added in their order.
+__global__ void __launch_bounds__(kCols * kSlices)
+    column_sum_kernel(const float *__restrict__ rec, int n, int64_t C, float *__restrict__ out0,
+                      int64_t C0, float *__restrict__ out1) {
+  __shared__ float sh[kSlices][kCols];
+  const int tx = threadIdx.x % kCols, ty = threadIdx.x / kCols;
+  const int64_t c = (int64_t)blockIdx.x * kCols + tx;
+  float s = 0.f;
+  if (c < C) {
+#pragma unroll 4
+    for (int r = ty; r < n; r += kSlices) s += rec[r * C + c];
+  }
+  sh[ty][tx] = s;
+  __syncthreads();
+  if (ty == 0 && c < C) {
+    for (int j = 1; j < kSlices; ++j) s += sh[j][tx];
+    if (c < C0) {
+      if (out0) out0[c] = s;
+    } else if (out1) {
+      out1[c - C0] = s;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_column_sum(const float *rec, int n, int64_t C, float *out0, int64_t C0,
+                              float *out1, cudaStream_t s) {
+  column_sum_kernel<<<(unsigned)((C + kCols - 1) / kCols), kCols * kSlices, 0, s>>>(rec, n, C, out0,
+                                                                                    C0, out1);
+  return cudaGetLastError();
+}
+
+}  // namespace linattn

@@ -186,4 +186,110 @@ int backward_tc_launches();
 cudaError_t launch_backward_tc(const Problem &p, const void *dO, void *dq, void *dk, void *dv,
                                const Gammas &g, void *ws, cudaStream_t s);
 
+// out0[c] (c < C0) and out1[c - C0] (the rest; may be null) = sum of rec[r][c]
+// over the n records of C columns, in a fixed order (column_sum.cu).
+cudaError_t launch_column_sum(const float *rec, int n, int64_t C, float *out0, int64_t C0,
+                              float *out1, cudaStream_t s);
+
+// Selective state space scan (selective.cu, selective_bwd.cu).  x, dt, z, y
+// and the gradients: [B][L][E] (one step: [B][E]); Bm, Cm [B][L][G][N]; x,
+// dt, z, Bm, Cm with ld elements between tokens; parameters and states fp32:
+// A [E][N], D, dt_bias [E], h0, hN [B][E][N].  z, D, dt_bias, lens (int32
+// [B]), h0, hN may be null.  For a step hN is updated in place.
+struct ScanArgs {
+  const void *x, *dt, *z, *Bm, *Cm;
+  const float *A, *D, *dt_bias, *h0;
+  const int *lens;
+  void *y;
+  float *hN;
+  int B, L, E, N, G;
+  int64_t ldx, lddt, ldz, ldb, ldc;
+  bool softplus;
+};
+bool selective_states_supported(int N);
+// Sequence parts of the scan, tokens per part, and the workspace of the
+// parts' records (0 for one part).
+int selective_parts(int B, int L, int E, int N, int G);
+int selective_part_len(int L, int S);
+size_t selective_workspace_bytes(int B, int E, int N, int S);
+cudaError_t launch_selective(const ScanArgs &a, Dtype dt, void *ws, int S, cudaStream_t s);
+cudaError_t launch_selective_step(const ScanArgs &a, Dtype dt, cudaStream_t s);
+// Backward of the scan from h0 (null: zeros): gradients of every input from
+// dy and, when dhN is set, the upstream gradient of the final state.  dD,
+// dz, ddt_bias, dh0 are null where their input is.
+struct ScanGrads {
+  const void *dy;
+  const float *dhN;
+  void *dx, *ddt, *dz, *dBm, *dCm;
+  float *dA, *dD, *ddt_bias, *dh0;
+};
+size_t selective_backward_workspace_bytes(int B, int L, int E, int N, int G);
+cudaError_t launch_selective_backward(const ScanArgs &a, const ScanGrads &g, Dtype dt, void *ws,
+                                      cudaStream_t s);
+
+// Short causal depthwise convolution (short_conv.cu): x, y [B][L][E] (x with
+// ldx elements between tokens), w [E][W] and bias [E] fp32, W in 2..4, state
+// [B][W-1][E] (the rows before the first token; null: zeros).
+struct ConvArgs {
+  const void *x;
+  const float *w, *bias;
+  const void *state;
+  const int *lens;
+  void *y, *state_out;
+  int B, L, E, W;
+  int64_t ldx;
+  bool silu;
+};
+cudaError_t launch_conv(const ConvArgs &a, Dtype dt, cudaStream_t s);
+// One token, in place on state_out (a.state and a.lens unused).
+cudaError_t launch_conv_step(const ConvArgs &a, Dtype dt, cudaStream_t s);
+// dx [B][L][E], dw [E][W], dbias [E] (optional), dstate [B][W-1][E] (optional).
+struct ConvGrads {
+  const void *dy;
+  void *dx, *dstate;
+  float *dw, *dbias;
+};
+size_t conv_backward_workspace_bytes(int B, int L, int E, int W);
+cudaError_t launch_conv_backward(const ConvArgs &a, const ConvGrads &g, Dtype dt, void *ws,
+                                 cudaStream_t s);
+
+// RMS norms around a block (norms.cu).  Gated: rows of D values, one per
+// (b, t, h); y [B][H][L][D] (heads_first) or [B][L][H][D], gate and out
+// [B][L][H*D], w [H][D] fp32 or null.
+struct NormGateArgs {
+  const void *y, *gate;
+  const float *w;
+  void *out;
+  int B, H, L, D;
+  float eps;
+  bool heads_first, gate_first;
+};
+struct NormGateGrads {
+  const void *dout;
+  void *dy, *dgate;
+  float *dw;  // null when w is
+};
+cudaError_t launch_norm_gate(const NormGateArgs &a, Dtype dt, cudaStream_t s);
+size_t norm_gate_backward_workspace_bytes(int B, int H, int L, int D);
+cudaError_t launch_norm_gate_backward(const NormGateArgs &a, const NormGateGrads &g, Dtype dt,
+                                      void *ws, cudaStream_t s);
+// Residual: r = residual + scale x, o = norm(r) w; rows of E values.
+struct NormResidualArgs {
+  const void *x, *residual;  // residual null: r = scale x
+  const float *w;            // [E] or null
+  void *o, *r;               // backward: r is an input, o unused
+  int64_t rows;
+  int E;
+  float scale, eps;
+};
+struct NormResidualGrads {
+  const void *dout, *dr;     // dr null: no other gradient of r
+  void *dresidual, *dx;      // dx null when scale is 1
+  float *dw;                 // null when w is
+};
+cudaError_t launch_norm_residual(const NormResidualArgs &a, Dtype dt, cudaStream_t s);
+size_t norm_residual_backward_workspace_bytes(int64_t rows, int E);
+cudaError_t launch_norm_residual_backward(const NormResidualArgs &a, const NormResidualGrads &g,
+                                          Dtype dt, void *ws, cudaStream_t s);
+
 }  // namespace linattn

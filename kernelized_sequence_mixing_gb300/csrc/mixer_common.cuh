@@ -1,0 +1,190 @@
+// Device helpers of the state space, convolution and norm kernels: pairs of
+// fp32 values for the packed instructions, eight-element vectors of either
+// element type, softplus and SiLU.
+#pragma once
+#include "common.cuh"
+
+namespace linattn {
+
+// Dynamic shared memory above 48 KB has to be asked for.
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, int bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Two fp32 values in one 64-bit register pair.  One packed instruction does
+// two fp32 operations in one issue slot; each half rounds as the scalar
+// instruction does.
+struct f2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ f2 dup2(float x) { return pack2(x, x); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float sum2(f2 a) {
+  const float2 x = unpack2(a);
+  return x.x + x.y;
+}
+// 2^x on the special function unit (relative error about 2^-22)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 a) {
+  const float2 x = unpack2(a);
+  return pack2(ex2(x.x), ex2(x.y));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// softplus(x) = max(x, 0) + log1p(exp(-|x|)).  log1p(t)/t on [0, 1] is the
+// degree-7 Chebyshev interpolant (relative error 3.2e-7 in fp32 arithmetic,
+// evaluated on a grid of 200 001 points): the logarithm's own instruction is
+// only accurate absolutely, and steps of 1e-3 need it relatively.  NaN stays
+// NaN (through the exponential).
+__device__ __forceinline__ float softplus_f32(float x) {
+  const float t = ex2(-fabsf(x) * kLog2e);
+  float p = -0.00837115291506052f;
+  p = fmaf(p, t, 0.04349390044808388f);
+  p = fmaf(p, t, -0.1068500280380249f);
+  p = fmaf(p, t, 0.1768747717142105f);
+  p = fmaf(p, t, -0.24474774301052094f);
+  p = fmaf(p, t, 0.3327192962169647f);
+  p = fmaf(p, t, -0.49997174739837646f);
+  p = fmaf(p, t, 0.9999997615814209f);
+  return fmaf(p, t, fmaxf(x, 0.f));
+}
+
+// 1 / (1 + exp(-x)); exp(-x) = inf gives 0, NaN stays NaN
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  return __fdividef(1.f, 1.f + ex2(-x * kLog2e));
+}
+
+// Asynchronous copy of 16 bytes to shared memory (zeros where !valid: the
+// source is then not read).
+__device__ __forceinline__ void copy16_async(void *smem, const void *gmem, bool valid) {
+  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const int bytes = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(gmem), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Eight consecutive elements as fp32; `p` is 16-byte aligned.
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p);
+  const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void bf16x2_to_f32(uint32_t u, float &lo, float &hi) {
+  lo = __uint_as_float(u << 16);
+  hi = __uint_as_float(u & 0xffff0000u);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4 *>(p);
+  bf16x2_to_f32(a.x, x[0], x[1]);
+  bf16x2_to_f32(a.y, x[2], x[3]);
+  bf16x2_to_f32(a.z, x[4], x[5]);
+  bf16x2_to_f32(a.w, x[6], x[7]);
+}
+__device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+  *reinterpret_cast<uint4 *>(p) =
+      make_uint4(f32_to_bf16x2(x[0], x[1]), f32_to_bf16x2(x[2], x[3]), f32_to_bf16x2(x[4], x[5]),
+                 f32_to_bf16x2(x[6], x[7]));
+}
+
+// Four consecutive elements as fp32 (8- or 16-byte aligned).
+__device__ __forceinline__ float4 load4(const float *p) {
+  return *reinterpret_cast<const float4 *>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const uint2 a = *reinterpret_cast<const uint2 *>(p);
+  float4 r;
+  bf16x2_to_f32(a.x, r.x, r.y);
+  bf16x2_to_f32(a.y, r.z, r.w);
+  return r;
+}
+__device__ __forceinline__ void store4(float *p, const float4 &x) {
+  *reinterpret_cast<float4 *>(p) = x;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &x) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(x.x, x.y), f32_to_bf16x2(x.z, x.w));
+}
+
+// Eight elements as they lie in memory, for loads that are issued well ahead
+// of their use (bf16: four registers, fp32: eight).
+template <typename T> struct raw8;
+template <> struct raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    a = *reinterpret_cast<const uint4 *>(p);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+    *reinterpret_cast<uint4 *>(p) = a;
+  }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    bf16x2_to_f32(a.x, x[0], x[1]);
+    bf16x2_to_f32(a.y, x[2], x[3]);
+    bf16x2_to_f32(a.z, x[4], x[5]);
+    bf16x2_to_f32(a.w, x[6], x[7]);
+  }
+};
+template <> struct raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *reinterpret_cast<const float4 *>(p + 4);
+  }
+  __device__ __forceinline__ void store(float *p) const {
+    *reinterpret_cast<float4 *>(p) = a;
+    *reinterpret_cast<float4 *>(p + 4) = b;
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
+}  // namespace linattn

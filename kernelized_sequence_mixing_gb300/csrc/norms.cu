@@ -1,0 +1,409 @@
+// RMS norms around a mixing block, forward and backward (fp32 arithmetic).
+//
+// After the block, per (b, t, h) row of D values (the heads of a causal
+// linear-attention pass, or the groups of a state space block):
+//   gate after:  o = p rsqrt(mean p^2 + eps) w act(g),   p = y
+//   gate first:  o = p rsqrt(mean p^2 + eps) w,          p = y act(g)
+// with act = SiLU.  y is read where the block left it ([B][H][L][D] or
+// [B][L][H][D]) and o is written token-major, as the projection behind it
+// reads it.  Ahead of the next block, per row of E values:
+//   r = residual + scale x,   o = r rsqrt(mean r^2 + eps) w
+// (the norm takes the fp32 sum, not the rounded r that is written beside it).
+//
+// Backward.  With n = p rstd and dn = do w (act(g)):
+//   dp = rstd (dn - n mean(dn n)) = rstd dn - p rstd^3 sum(dn p) / D,
+// so one joint reduction of sum p^2 and sum dn p serves a row.
+//
+// Bound by memory: every value is read once into registers and written once.
+// A row belongs to a power of two of lanes, 8 values a lane at a time: part
+// of a warp up to D = 256, a warp up to 1024, a CTA beyond.  The backward
+// passes keep a row group on one head, so the weight gradient stays in
+// registers over all its rows and leaves as one record per CTA; the records
+// are added in their order.
+#include <type_traits>
+
+#include "kernels.h"
+#include "mixer_common.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kThreads = 256;
+
+enum { kGateAfter = 0, kGateFirst = 1, kResidual = 2 };
+
+struct RowArgs {
+  const void *in1, *in2;  // y and gate, or x and residual (backward: r and nothing)
+  const void *in3, *in4;  // backward: do; dr
+  const float *w;
+  void *out1, *out2;      // o and r; backward: dy and dgate, or dresidual and dx
+  float *rec;             // backward: [slots][H][D] weight gradients, or null
+  int64_t tokens;         // B L (residual: rows)
+  int H, D, L;
+  float eps, scale;
+  bool heads_first;
+};
+
+// Element offset of row (token j, head h) in y.
+__device__ __forceinline__ int64_t y_offset(const RowArgs &a, int64_t j, int h) {
+  if (!a.heads_first) return (j * a.H + h) * a.D;
+  const int64_t b = j / a.L, t = j - b * a.L;
+  return ((b * a.H + h) * a.L + t) * a.D;
+}
+
+// Sum over a row's LANES lanes (LANES = kThreads: the CTA; `sh` has room for
+// two rounds, `round` alternates so that one barrier per sum is enough).
+template <int LANES, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float (*sh)[K][kThreads / 32], int &round) {
+#pragma unroll
+  for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if constexpr (LANES > 32) {
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) sh[round][k][warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < LANES / 32; ++i) s += sh[round][k][i];
+      v[k] = s;
+    }
+    round ^= 1;
+  }
+}
+
+template <typename T, int MODE, int LANES, int VPT>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int GPC = kThreads / LANES;
+  __shared__ float sh[2][1][kThreads / 32];
+  int round = 0;
+  const int lane = threadIdx.x % LANES;
+  const int64_t rows = a.tokens * a.H;
+  const int64_t row = (int64_t)blockIdx.x * GPC + threadIdx.x / LANES;
+  const bool live = row < rows;
+  const int64_t j = live ? row / a.H : 0;
+  const int h = live ? static_cast<int>(row - j * a.H) : 0;
+  const int64_t off = live ? row * a.D : 0;
+  const T *in1 = static_cast<const T *>(a.in1) + (MODE == kResidual ? off : y_offset(a, j, h));
+  const T *in2 = a.in2 ? static_cast<const T *>(a.in2) + off : nullptr;
+  float p[VPT][8], g[VPT][8], s[1] = {0.f};
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (v * LANES + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[v][i] = g[v][i] = 0.f;
+    if (live && c < a.D) {
+      load8(in1 + c, p[v]);
+      if (in2) load8(in2 + c, g[v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (MODE == kResidual) {
+        p[v][i] = fmaf(a.scale, p[v][i], g[v][i]);
+      } else {
+        g[v][i] *= sigmoid_f32(g[v][i]);
+        if (MODE == kGateFirst) p[v][i] *= g[v][i];
+      }
+      s[0] = fmaf(p[v][i], p[v][i], s[0]);
+    }
+  row_sum<LANES, 1>(s, sh, round);
+  const float rstd = rsqrtf(s[0] / a.D + a.eps);
+  if (!live) return;
+  T *o = static_cast<T *>(a.out1) + off;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (v * LANES + lane) * 8;
+    if (c < a.D) {
+      if (MODE == kResidual) store8(static_cast<T *>(a.out2) + off + c, p[v]);
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      if (a.w) load8(a.w + (int64_t)h * a.D + c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] *= p[v][i] * rstd;
+        if (MODE == kGateAfter) w[i] *= g[v][i];
+      }
+      store8(o + c, w);
+    }
+  }
+}
+
+// One head per CTA (blockIdx.x % H); its row groups stride over the tokens.
+template <typename T, int MODE, int LANES, int VPT>
+__global__ void __launch_bounds__(kThreads)
+    norm_bwd_kernel(const __grid_constant__ RowArgs a, int slots) {
+  constexpr int GPC = kThreads / LANES;
+  __shared__ float sh[2][2][kThreads / 32];
+  int round = 0;
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+  float w[VPT][8], dw[VPT][8];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (v * LANES + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[v][i] = 1.f;
+      dw[v][i] = 0.f;
+    }
+    if (a.w && c < a.D) load8(a.w + (int64_t)h * a.D + c, w[v]);
+  }
+  const float invD = 1.f / a.D;
+  // every group of the CTA makes the same number of turns (the sums cross
+  // lanes of several groups)
+  for (int64_t j0 = (int64_t)slot * GPC; j0 < a.tokens; j0 += (int64_t)slots * GPC) {
+    const int64_t j = j0 + grp;
+    const bool live = j < a.tokens;
+    const int64_t jj = live ? j : 0;
+    const int64_t off = (jj * a.H + h) * a.D;
+    const int64_t yoff = MODE == kResidual ? off : y_offset(a, jj, h);
+    const T *in1 = static_cast<const T *>(a.in1) + yoff;
+    const T *in2 = static_cast<const T *>(a.in2) + off;
+    const T *in3 = static_cast<const T *>(a.in3) + off;
+    const T *in4 = static_cast<const T *>(a.in4) + off;
+    raw8<T> ry[VPT], rg[VPT], rd[VPT];  // rg: the gate, or dr
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * LANES + lane) * 8;
+      ry[v].zero();
+      rg[v].zero();
+      rd[v].zero();
+      if (live && c < a.D) {
+        ry[v].load(in1 + c);
+        rd[v].load(in3 + c);
+        if (MODE == kResidual) {
+          if (a.in4) rg[v].load(in4 + c);
+        } else {
+          rg[v].load(in2 + c);
+        }
+      }
+    }
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float y[8], g[8], d[8];
+      ry[v].get(y);
+      rg[v].get(g);
+      rd[v].get(d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float p = y[i], dn = d[i] * w[v][i];
+        if (MODE != kResidual) {
+          const float act = g[i] * sigmoid_f32(g[i]);
+          if (MODE == kGateFirst) p *= act;
+          else dn *= act;
+        }
+        s[0] = fmaf(p, p, s[0]);
+        s[1] = fmaf(dn, p, s[1]);
+      }
+    }
+    row_sum<LANES, 2>(s, sh, round);
+    const float rstd = rsqrtf(fmaf(s[0], invD, a.eps));
+    const float k = rstd * rstd * rstd * s[1] * invD;
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (v * LANES + lane) * 8;
+        if (c < a.D) {
+          float y[8], g[8], d[8], o1[8], o2[8];
+          ry[v].get(y);
+          rg[v].get(g);
+          rd[v].get(d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (MODE == kResidual) {
+              const float dp = fmaf(rstd, d[i] * w[v][i], -k * y[i]);
+              dw[v][i] = fmaf(d[i], y[i] * rstd, dw[v][i]);
+              o1[i] = g[i] + dp;
+              o2[i] = a.scale * o1[i];
+            } else {
+              const float sg = sigmoid_f32(g[i]);
+              const float act = g[i] * sg, dact = sg * fmaf(g[i], 1.f - sg, 1.f);
+              if (MODE == kGateFirst) {
+                const float p = y[i] * act;
+                const float dp = fmaf(rstd, d[i] * w[v][i], -k * p);
+                dw[v][i] = fmaf(d[i], p * rstd, dw[v][i]);
+                o1[i] = dp * act;
+                o2[i] = dp * y[i] * dact;
+              } else {
+                const float dn = d[i] * w[v][i] * act, n = y[i] * rstd;
+                dw[v][i] = fmaf(d[i] * act, n, dw[v][i]);
+                o1[i] = fmaf(rstd, dn, -k * y[i]);
+                o2[i] = d[i] * n * w[v][i] * dact;
+              }
+            }
+          }
+          store8(static_cast<T *>(a.out1) + yoff + c, o1);
+          if (MODE != kResidual || a.out2) store8(static_cast<T *>(a.out2) + off + c, o2);
+        }
+      }
+    }
+  }
+  if (!a.rec) return;
+  float *rec = a.rec + ((int64_t)slot * a.H + h) * a.D;
+  if constexpr (GPC == 1) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * LANES + lane) * 8;
+      if (c < a.D) store8(rec + c, dw[v]);
+    }
+  } else {
+    // the groups' sums, in group order
+    __shared__ float part[GPC][LANES * 8];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      __syncthreads();
+      store8(&part[grp][lane * 8], dw[v]);
+      __syncthreads();
+      for (int i = threadIdx.x; i < LANES * 8; i += kThreads) {
+        const int c = v * LANES * 8 + i;
+        if (c < a.D) {
+          float q = part[0][i];
+          for (int k = 1; k < GPC; ++k) q += part[k][i];
+          rec[c] = q;
+        }
+      }
+    }
+  }
+}
+
+// Lanes per row: 8 values each up to a warp, then up to 4 vectors per lane,
+// then the CTA.
+template <typename F>
+cudaError_t by_width(int D, F &&f) {
+  if (D <= 32) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  if (D <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+  if (D <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+  if (D <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+  if (D <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+  if (D <= 1024) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+  if (D <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  if (D <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+}
+
+int lanes_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 1024 ? 32 : 256; }
+
+// CTAs per head of a backward pass: about four per SM over all heads, no more
+// than there are rows for.
+int bwd_slots(int64_t tokens, int H, int D) {
+  const int gpc = kThreads / lanes_of(D);
+  const int64_t most = (tokens + gpc - 1) / gpc;
+  int64_t n = (152 * 4 + H - 1) / H;
+  if (n > most) n = most;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+template <typename T, int MODE>
+cudaError_t run_rows(const RowArgs &a, cudaStream_t s) {
+  return by_width(a.D, [&](auto lanes, auto vpt) {
+    constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
+    const int64_t rows = a.tokens * a.H;
+    constexpr int GPC = kThreads / LANES;
+    norm_kernel<T, MODE, LANES, VPT><<<(unsigned)((rows + GPC - 1) / GPC), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T, int MODE>
+cudaError_t run_rows_bwd(const RowArgs &a, float *dw, cudaStream_t s) {
+  const int slots = bwd_slots(a.tokens, a.H, a.D);
+  cudaError_t e = by_width(a.D, [&](auto lanes, auto vpt) {
+    constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
+    norm_bwd_kernel<T, MODE, LANES, VPT><<<(unsigned)(slots * a.H), kThreads, 0, s>>>(a, slots);
+    return cudaGetLastError();
+  });
+  if (e != cudaSuccess || !dw) return e;
+  return launch_column_sum(a.rec, slots, a.H * a.D, dw, a.H * a.D, nullptr, s);
+}
+
+RowArgs gate_rows(const NormGateArgs &n) {
+  RowArgs a = {};
+  a.in1 = n.y;
+  a.in2 = n.gate;
+  a.w = n.w;
+  a.out1 = n.out;
+  a.tokens = (int64_t)n.B * n.L;
+  a.H = n.H;
+  a.D = n.D;
+  a.L = n.L;
+  a.eps = n.eps;
+  a.heads_first = n.heads_first;
+  return a;
+}
+
+RowArgs residual_rows(const NormResidualArgs &n) {
+  RowArgs a = {};
+  a.w = n.w;
+  a.tokens = n.rows;
+  a.H = 1;
+  a.D = n.E;
+  a.L = 1;
+  a.eps = n.eps;
+  a.scale = n.scale;
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_norm_gate(const NormGateArgs &n, Dtype dt, cudaStream_t s) {
+  const RowArgs a = gate_rows(n);
+  if (dt == kF32)
+    return n.gate_first ? run_rows<float, kGateFirst>(a, s) : run_rows<float, kGateAfter>(a, s);
+  return n.gate_first ? run_rows<__nv_bfloat16, kGateFirst>(a, s)
+                      : run_rows<__nv_bfloat16, kGateAfter>(a, s);
+}
+
+size_t norm_gate_backward_workspace_bytes(int B, int H, int L, int D) {
+  return sizeof(float) * (size_t)bwd_slots((int64_t)B * L, H, D) * H * D;
+}
+
+cudaError_t launch_norm_gate_backward(const NormGateArgs &n, const NormGateGrads &g, Dtype dt,
+                                      void *ws, cudaStream_t s) {
+  RowArgs a = gate_rows(n);
+  a.in3 = g.dout;
+  a.out1 = g.dy;
+  a.out2 = g.dgate;
+  a.rec = g.dw ? static_cast<float *>(ws) : nullptr;
+  if (dt == kF32)
+    return n.gate_first ? run_rows_bwd<float, kGateFirst>(a, g.dw, s)
+                        : run_rows_bwd<float, kGateAfter>(a, g.dw, s);
+  return n.gate_first ? run_rows_bwd<__nv_bfloat16, kGateFirst>(a, g.dw, s)
+                      : run_rows_bwd<__nv_bfloat16, kGateAfter>(a, g.dw, s);
+}
+
+cudaError_t launch_norm_residual(const NormResidualArgs &n, Dtype dt, cudaStream_t s) {
+  RowArgs a = residual_rows(n);
+  a.in1 = n.x;
+  a.in2 = n.residual;
+  a.out1 = n.o;
+  a.out2 = n.r;
+  return dt == kF32 ? run_rows<float, kResidual>(a, s) : run_rows<__nv_bfloat16, kResidual>(a, s);
+}
+
+size_t norm_residual_backward_workspace_bytes(int64_t rows, int E) {
+  return sizeof(float) * (size_t)bwd_slots(rows, 1, E) * E;
+}
+
+cudaError_t launch_norm_residual_backward(const NormResidualArgs &n, const NormResidualGrads &g,
+                                          Dtype dt, void *ws, cudaStream_t s) {
+  RowArgs a = residual_rows(n);
+  a.in1 = n.r;
+  a.in3 = g.dout;
+  a.in4 = g.dr;
+  a.out1 = g.dresidual;
+  a.out2 = g.dx;
+  a.rec = g.dw ? static_cast<float *>(ws) : nullptr;
+  return dt == kF32 ? run_rows_bwd<float, kResidual>(a, g.dw, s)
+                    : run_rows_bwd<__nv_bfloat16, kResidual>(a, g.dw, s);
+}
+
+}  // namespace linattn
