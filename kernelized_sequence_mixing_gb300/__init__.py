@@ -36,6 +36,7 @@ block:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -194,11 +195,21 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return None if t is None else t.data_ptr()
+
+
+def _on(dev):
+    """The context of a call on ``dev``: nothing to do where it is the current
+    device already (the guard costs more than the rest of a short call)."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _check(fn, code):
@@ -221,12 +232,14 @@ def _one_device(fn, named, allow_host=False):
     """All tensors of ``named`` [(name, tensor or None)] on one device, of a
     type the kernels can address (or the host, where ``allow_host``: the
     forward copies host tensors itself)."""
-    present = [(n, t) for n, t in named if t is not None]
-    devs = {t.device for _, t in present}
-    if len(devs) > 1:
-        where = ", ".join(f"{n} on {t.device}" for n, t in present)
-        raise ValueError(f"{fn}: all tensors must be on one device ({where})")
-    dev = next(iter(devs))
+    dev = None
+    for _, t in named:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                where = ", ".join(f"{n} on {t.device}" for n, t in named if t is not None)
+                raise ValueError(f"{fn}: all tensors must be on one device ({where})")
     if dev.type not in _DEVICE_TYPES and not allow_host:
         raise ValueError(f"{fn}: tensors must be CUDA tensors, got {dev}")
     return dev
@@ -234,7 +247,7 @@ def _one_device(fn, named, allow_host=False):
 
 def _expect(fn, name, t, shape, dtype):
     """A caller-provided buffer: exactly ``shape`` and ``dtype``, contiguous."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
@@ -564,7 +577,7 @@ def _tokens(fn, name, t, lead, row, dtype):
     """The token stride (0: dense) of an input [*lead, *row] of ``dtype`` whose
     rows are contiguous; lead is (B, L), with L token strides between
     sequences, or (B,): dense tensors and slices of a dense tensor's rows."""
-    if tuple(t.shape) != lead + row:
+    if t.shape != lead + row:
         raise ValueError(f"{fn}: {name} must have shape {lead + row}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
@@ -638,7 +651,7 @@ def forward_selective(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=T
                            ("z", z), ("dt_bias", dt_bias), ("h0", h0), ("lens", lens),
                            ("out", out), ("h", h)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((B, L, E), dtype=x.dtype, device=dev)
         if h is None and return_state:
@@ -662,7 +675,7 @@ def decode_selective(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus
     dev = _one_device(fn, (("x", x), ("dt", dt), ("A", A), ("Bm", Bm), ("Cm", Cm), ("h", h),
                            ("D", D), ("z", z), ("dt_bias", dt_bias), ("out", out)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((B, E), dtype=x.dtype, device=dev)
         _check("la_decode_selective", lib.la_decode_selective(
@@ -687,7 +700,7 @@ def backward_selective(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softp
                            ("D", D), ("z", z), ("dt_bias", dt_bias), ("h0", h0), ("dh", dh)))
     lib = load_library()
     f = torch.float32
-    with torch.cuda.device(dev):
+    with _on(dev):
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
         dx, ddt = new((B, L, E), x.dtype), new((B, L, E), x.dtype)
         dA, dB, dC = new((E, N), f), new((B, L, G, N), x.dtype), new((B, L, G, N), x.dtype)
@@ -734,7 +747,7 @@ def forward_conv(x, w, bias=None, silu=True, state=None, lens=None, out=None,
     dev = _one_device(fn, (("x", x), ("w", w), ("bias", bias), ("state", state), ("lens", lens),
                            ("out", out), ("state_out", state_out)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((B, L, E), dtype=x.dtype, device=dev)
         if state_out is None and return_state:
@@ -755,7 +768,7 @@ def decode_conv(x, w, state, bias=None, silu=True, out=None):
         _expect(fn, "out", out, (B, E), x.dtype)
     dev = _one_device(fn, (("x", x), ("w", w), ("state", state), ("bias", bias), ("out", out)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((B, E), dtype=x.dtype, device=dev)
         _check("la_decode_conv", lib.la_decode_conv(
@@ -775,7 +788,7 @@ def backward_conv(x, w, dy, bias=None, silu=True, state=None):
         _expect(fn, "state", state, (B, W - 1, E), x.dtype)
     dev = _one_device(fn, (("x", x), ("w", w), ("dy", dy), ("bias", bias), ("state", state)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         dx = torch.empty((B, L, E), dtype=x.dtype, device=dev)
         dw = torch.empty((E, W), dtype=torch.float32, device=dev)
         dbias = torch.empty((E,), dtype=torch.float32, device=dev) if bias is not None else None
@@ -810,7 +823,7 @@ def forward_norm_gate(y, gate, w=None, eps=1e-5, gate_first=False, heads_first=T
     B, H, L, D = _norm_gate_args(fn, y, gate, w, heads_first, (("out", out),))
     dev = _one_device(fn, (("y", y), ("gate", gate), ("w", w), ("out", out)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((B, L, H * D), dtype=y.dtype, device=dev)
         _check("la_forward_norm_gate", lib.la_forward_norm_gate(
@@ -826,7 +839,7 @@ def backward_norm_gate(y, gate, do, w=None, eps=1e-5, gate_first=False, heads_fi
     B, H, L, D = _norm_gate_args(fn, y, gate, w, heads_first, (("do", do),))
     dev = _one_device(fn, (("y", y), ("gate", gate), ("do", do), ("w", w)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         dy, dgate = torch.empty_like(y), torch.empty_like(gate)
         dw = torch.empty((H, D), dtype=torch.float32, device=dev) if w is not None else None
         _check("la_backward_norm_gate", lib.la_backward_norm_gate(
@@ -858,7 +871,7 @@ def forward_norm_residual(x, residual=None, w=None, scale=1.0, eps=1e-5, out=Non
     rows, E = _rows(fn, "x", x, (("residual", residual), ("out", out), ("r", r)), w)
     dev = _one_device(fn, (("x", x), ("residual", residual), ("w", w), ("out", out), ("r", r)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty_like(x)
         if r is None:
@@ -877,7 +890,7 @@ def backward_norm_residual(r, do, w=None, dr=None, scale=1.0, eps=1e-5):
     rows, E = _rows(fn, "r", r, (("do", do), ("dr", dr)), w)
     dev = _one_device(fn, (("r", r), ("do", do), ("dr", dr), ("w", w)))
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         dres = torch.empty_like(r)
         dx = torch.empty_like(r) if scale != 1.0 else None
         dw = torch.empty((E,), dtype=torch.float32, device=dev) if w is not None else None

@@ -112,6 +112,11 @@ __device__ __forceinline__ void bf16x2_to_f32(uint32_t u, float &lo, float &hi) 
   lo = __uint_as_float(u << 16);
   hi = __uint_as_float(u & 0xffff0000u);
 }
+__device__ __forceinline__ f2 bf16x2_to_f2(uint32_t u) {
+  float lo, hi;
+  bf16x2_to_f32(u, lo, hi);
+  return pack2(lo, hi);
+}
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
   const uint4 a = *reinterpret_cast<const uint4 *>(p);
   bf16x2_to_f32(a.x, x[0], x[1]);

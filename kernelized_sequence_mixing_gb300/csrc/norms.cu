@@ -38,17 +38,18 @@ struct RowArgs {
   const float *w;
   void *out1, *out2;      // o and r; backward: dy and dgate, or dresidual and dx
   float *rec;             // backward: [slots][H][D] weight gradients, or null
-  int64_t tokens;         // B L (residual: rows)
+  unsigned tokens;        // B L (residual: rows); tokens x H < 2^31
   int H, D, L;
   float eps, scale;
   bool heads_first;
 };
 
-// Element offset of row (token j, head h) in y.
-__device__ __forceinline__ int64_t y_offset(const RowArgs &a, int64_t j, int h) {
-  if (!a.heads_first) return (j * a.H + h) * a.D;
-  const int64_t b = j / a.L, t = j - b * a.L;
-  return ((b * a.H + h) * a.L + t) * a.D;
+// Element offset of row (token j, head h) in y.  Rows count less than 2^31,
+// so that 32-bit divisions do.
+__device__ __forceinline__ int64_t y_offset(const RowArgs &a, unsigned j, int h) {
+  if (!a.heads_first) return (int64_t)(j * a.H + h) * a.D;
+  const unsigned b = j / (unsigned)a.L, t = j - b * a.L;
+  return ((int64_t)(b * a.H + h) * a.L + t) * a.D;
 }
 
 // Sum over a row's LANES lanes (LANES = kThreads: the CTA; `sh` has room for
@@ -82,12 +83,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   __shared__ float sh[2][1][kThreads / 32];
   int round = 0;
   const int lane = threadIdx.x % LANES;
-  const int64_t rows = a.tokens * a.H;
-  const int64_t row = (int64_t)blockIdx.x * GPC + threadIdx.x / LANES;
+  const unsigned rows = a.tokens * a.H;
+  const unsigned row = blockIdx.x * GPC + threadIdx.x / LANES;
   const bool live = row < rows;
-  const int64_t j = live ? row / a.H : 0;
-  const int h = live ? static_cast<int>(row - j * a.H) : 0;
-  const int64_t off = live ? row * a.D : 0;
+  const unsigned j = MODE == kResidual ? row : live ? row / (unsigned)a.H : 0u;
+  const int h = MODE == kResidual || !live ? 0 : static_cast<int>(row - j * a.H);
+  const int64_t off = live ? (int64_t)row * a.D : 0;
   const T *in1 = static_cast<const T *>(a.in1) + (MODE == kResidual ? off : y_offset(a, j, h));
   const T *in2 = a.in2 ? static_cast<const T *>(a.in2) + off : nullptr;
   float p[VPT][8], g[VPT][8], s[1] = {0.f};
@@ -159,11 +160,11 @@ __global__ void __launch_bounds__(kThreads)
   const float invD = 1.f / a.D;
   // every group of the CTA makes the same number of turns (the sums cross
   // lanes of several groups)
-  for (int64_t j0 = (int64_t)slot * GPC; j0 < a.tokens; j0 += (int64_t)slots * GPC) {
-    const int64_t j = j0 + grp;
+  for (unsigned j0 = slot * GPC; j0 < a.tokens; j0 += slots * GPC) {
+    const unsigned j = j0 + grp;
     const bool live = j < a.tokens;
-    const int64_t jj = live ? j : 0;
-    const int64_t off = (jj * a.H + h) * a.D;
+    const unsigned jj = live ? j : 0u;
+    const int64_t off = (int64_t)(jj * a.H + h) * a.D;
     const int64_t yoff = MODE == kResidual ? off : y_offset(a, jj, h);
     const T *in1 = static_cast<const T *>(a.in1) + yoff;
     const T *in2 = static_cast<const T *>(a.in2) + off;
@@ -306,7 +307,7 @@ template <typename T, int MODE>
 cudaError_t run_rows(const RowArgs &a, cudaStream_t s) {
   return by_width(a.D, [&](auto lanes, auto vpt) {
     constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
-    const int64_t rows = a.tokens * a.H;
+    const int64_t rows = (int64_t)a.tokens * a.H;
     constexpr int GPC = kThreads / LANES;
     norm_kernel<T, MODE, LANES, VPT><<<(unsigned)((rows + GPC - 1) / GPC), kThreads, 0, s>>>(a);
     return cudaGetLastError();
@@ -331,7 +332,7 @@ RowArgs gate_rows(const NormGateArgs &n) {
   a.in2 = n.gate;
   a.w = n.w;
   a.out1 = n.out;
-  a.tokens = (int64_t)n.B * n.L;
+  a.tokens = (unsigned)n.B * (unsigned)n.L;
   a.H = n.H;
   a.D = n.D;
   a.L = n.L;
@@ -343,7 +344,7 @@ RowArgs gate_rows(const NormGateArgs &n) {
 RowArgs residual_rows(const NormResidualArgs &n) {
   RowArgs a = {};
   a.w = n.w;
-  a.tokens = n.rows;
+  a.tokens = (unsigned)n.rows;
   a.H = 1;
   a.D = n.E;
   a.L = 1;

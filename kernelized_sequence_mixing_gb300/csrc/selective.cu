@@ -367,63 +367,68 @@ cudaError_t scan_states(const ScanArgs &a, void *ws, int S, cudaStream_t s) {
 
 // One token, in place on the fp32 state.  Bound by the state's bytes (8 per
 // element): N/4 lanes share a channel, each streams one 16-byte piece of its
-// states; U channels per thread keep several loads in flight.
+// states.  A thread keeps its channel's parameters for U sequences, whose
+// state loads are all in flight at once.
 template <typename T, int N, int U>
 __global__ void __launch_bounds__(256) scan_step_kernel(const __grid_constant__ ScanArgs a) {
   constexpr int LN = N / 4, PER = 256 / LN;
   const int tid = threadIdx.x, sl = tid & (LN - 1);
-  const unsigned rows = (unsigned)a.B * (unsigned)a.E;  // < 2^31
-  const unsigned r0 = blockIdx.x * (U * PER) + tid / LN;
-  float4 h[U];
+  const int e = blockIdx.x * PER + tid / LN;  // equal in all lanes of a channel
+  const bool in = e < a.E;
+  const int ec = in ? e : 0;
+  const int goff = (a.G == 1 ? 0 : ec / (a.E / a.G)) * N + sl * 4;
+  const float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)ec * N + sl * 4);
+  const float bias = a.dt_bias ? a.dt_bias[ec] : 0.f, skip = a.D ? a.D[ec] : 0.f;
+  for (int b0 = blockIdx.y * U; b0 < a.B; b0 += gridDim.y * U) {
+    float4 h[U];
+    float x[U], d[U], zv[U];
+    float4 Bv[U], Cv[U];
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const unsigned r = r0 + j * PER;
-    h[j] = r < rows ? __ldcs(reinterpret_cast<const float4 *>(a.hN + (int64_t)r * N) + sl)
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+    for (int j = 0; j < U; ++j) {
+      const int64_t b = min(b0 + j, a.B - 1);
+      h[j] = __ldcs(reinterpret_cast<const float4 *>(a.hN + (b * a.E + ec) * N) + sl);
+      x[j] = io<T>::load(static_cast<const T *>(a.x) + b * a.ldx + ec);
+      d[j] = io<T>::load(static_cast<const T *>(a.dt) + b * a.lddt + ec);
+      zv[j] = a.z ? io<T>::load(static_cast<const T *>(a.z) + b * a.ldz + ec) : 0.f;
+      Bv[j] = load4(static_cast<const T *>(a.Bm) + b * a.ldb + goff);
+      Cv[j] = load4(static_cast<const T *>(a.Cm) + b * a.ldc + goff);
+    }
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const unsigned r = r0 + j * PER;
-    const bool in = r < rows;  // equal in all lanes of a channel
-    const unsigned bb = in ? r / (unsigned)a.E : 0u;
-    const int e = in ? static_cast<int>(r - bb * (unsigned)a.E) : 0;
-    const int64_t b = bb;
-    const int g = a.G == 1 ? 0 : e / (a.E / a.G);
-    const float x = io<T>::load(static_cast<const T *>(a.x) + b * a.ldx + e);
-    float d = io<T>::load(static_cast<const T *>(a.dt) + b * a.lddt + e);
-    const float zv = a.z ? io<T>::load(static_cast<const T *>(a.z) + b * a.ldz + e) : 0.f;
-    const float4 Bv = load4(static_cast<const T *>(a.Bm) + b * a.ldb + g * N + sl * 4);
-    const float4 Cv = load4(static_cast<const T *>(a.Cm) + b * a.ldc + g * N + sl * 4);
-    const float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)e * N + sl * 4);
-    if (a.dt_bias) d += a.dt_bias[e];
-    if (a.softplus) d = softplus_f32(d);
-    const float dl = d * kLog2e, u = d * x;
-    h[j].x = fmaf(ex2(dl * A.x), h[j].x, u * Bv.x);
-    h[j].y = fmaf(ex2(dl * A.y), h[j].y, u * Bv.y);
-    h[j].z = fmaf(ex2(dl * A.z), h[j].z, u * Bv.z);
-    h[j].w = fmaf(ex2(dl * A.w), h[j].w, u * Bv.w);
-    if (in) __stcs(reinterpret_cast<float4 *>(a.hN + (int64_t)r * N) + sl, h[j]);
-    float y = h[j].x * Cv.x;
-    y = fmaf(h[j].y, Cv.y, y);
-    y = fmaf(h[j].z, Cv.z, y);
-    y = fmaf(h[j].w, Cv.w, y);
+    for (int j = 0; j < U; ++j) {
+      const bool live = in && b0 + j < a.B;
+      const int64_t row = (int64_t)(b0 + j) * a.E + e;
+      float dt = d[j] + bias;
+      if (a.softplus) dt = softplus_f32(dt);
+      const float dl = dt * kLog2e, u = dt * x[j];
+      h[j].x = fmaf(ex2(dl * A.x), h[j].x, u * Bv[j].x);
+      h[j].y = fmaf(ex2(dl * A.y), h[j].y, u * Bv[j].y);
+      h[j].z = fmaf(ex2(dl * A.z), h[j].z, u * Bv[j].z);
+      h[j].w = fmaf(ex2(dl * A.w), h[j].w, u * Bv[j].w);
+      if (live) __stcs(reinterpret_cast<float4 *>(a.hN + row * N) + sl, h[j]);
+      float y = h[j].x * Cv[j].x;
+      y = fmaf(h[j].y, Cv[j].y, y);
+      y = fmaf(h[j].z, Cv[j].z, y);
+      y = fmaf(h[j].w, Cv[j].w, y);
 #pragma unroll
-    for (int o = 1; o < LN; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (a.D) y = fmaf(a.D[e], x, y);
-    if (a.z) y *= zv * sigmoid_f32(zv);
-    if (in && sl == 0) io<T>::store(static_cast<T *>(a.y) + b * a.E + e, y);
+      for (int o = 1; o < LN; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      y = fmaf(skip, x[j], y);
+      if (a.z) y *= zv[j] * sigmoid_f32(zv[j]);
+      if (live && sl == 0) io<T>::store(static_cast<T *>(a.y) + row, y);
+    }
   }
 }
 
 template <typename T, int N>
 cudaError_t step_typed(const ScanArgs &a, cudaStream_t s) {
-  constexpr int PER = 256 / (N / 4);
-  const int64_t rows = (int64_t)a.B * a.E;
-  // four channels per thread once that still gives every SM eight CTAs
-  if (rows >= (int64_t)152 * 8 * 4 * PER)
-    scan_step_kernel<T, N, 4><<<(unsigned)((rows + 4 * PER - 1) / (4 * PER)), 256, 0, s>>>(a);
-  else
-    scan_step_kernel<T, N, 1><<<(unsigned)((rows + PER - 1) / PER), 256, 0, s>>>(a);
+  constexpr int PER = 256 / (N / 4), kMaxY = 65535;
+  const unsigned nx = (a.E + PER - 1) / PER;
+  // four sequences per thread once that still gives every SM four CTAs
+  if ((int64_t)nx * a.B >= 152 * 4 * 4) {
+    const int ny = (a.B + 3) / 4;
+    scan_step_kernel<T, N, 4><<<dim3(nx, ny < kMaxY ? ny : kMaxY), 256, 0, s>>>(a);
+  } else {
+    scan_step_kernel<T, N, 1><<<dim3(nx, a.B < kMaxY ? a.B : kMaxY), 256, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 

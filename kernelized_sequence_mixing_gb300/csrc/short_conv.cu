@@ -5,11 +5,12 @@
 //   y_t = silu(pre_t)  (or pre_t),
 // with the rows before the first token taken from `state` (or zeros).
 //
-// Bound by memory: x is read once and y written once.  A thread owns a vector
-// of channels (8 in the forward pass, 4 in the backward pass, whose
-// accumulators need the registers) and a run of consecutive tokens; the last
-// W - 1 rows stay in registers as a sliding window, so only the first W - 1
-// rows of a run are read twice (from L2).
+// Bound by memory: x is read once and y written once.  A thread owns a few
+// consecutive channels (4 in the forward pass, 2 in the backward pass: packed
+// pairs, so that 32 to 48 warps fit an SM) and a run of consecutive tokens;
+// the last W - 1 rows stay in registers as a sliding window, so only the
+// first W - 1 rows of a run are read twice (from L2), and the next tokens'
+// loads are issued a group ahead.
 #include "kernels.h"
 #include "mixer_common.cuh"
 
@@ -17,31 +18,111 @@ namespace linattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 16;  // tokens per thread of the forward pass
+constexpr int kRun = 32;  // tokens per thread of the forward pass
 
-// Row t of sequence b before its first token: state row t + W - 1, or zeros.
-template <typename T, int W>
-__device__ __forceinline__ void state_row8(const ConvArgs &a, int64_t b, int t, int e, float (&x)[8]) {
-  if (a.state) {
-    load8(static_cast<const T *>(a.state) + (b * (W - 1) + t + W - 1) * a.E + e, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+// Pairs of channels as they lie in memory.
+template <typename T, int P> struct rawp;  // P pairs
+template <> struct rawp<__nv_bfloat16, 2> {
+  uint2 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint2 *>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint2 *>(p) = a; }
+  __device__ __forceinline__ void zero() { a = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void get(f2 (&x)[2]) const {
+    x[0] = bf16x2_to_f2(a.x);
+    x[1] = bf16x2_to_f2(a.y);
   }
+};
+template <> struct rawp<float, 2> {
+  float4 a;
+  __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const float4 *>(p); }
+  __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = a; }
+  __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(f2 (&x)[2]) const {
+    x[0] = pack2(a.x, a.y);
+    x[1] = pack2(a.z, a.w);
+  }
+};
+template <> struct rawp<__nv_bfloat16, 1> {
+  uint32_t a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint32_t *>(p); }
+  __device__ __forceinline__ void zero() { a = 0u; }
+  __device__ __forceinline__ void get(f2 (&x)[1]) const { x[0] = bf16x2_to_f2(a); }
+};
+template <> struct rawp<float, 1> {
+  float2 a;
+  __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const float2 *>(p); }
+  __device__ __forceinline__ void zero() { a = make_float2(0.f, 0.f); }
+  __device__ __forceinline__ void get(f2 (&x)[1]) const { x[0] = pack2(a.x, a.y); }
+};
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, f2 v) {
+  const float2 q = unpack2(v);
+  *reinterpret_cast<uint32_t *>(p) = f32_to_bf16x2(q.x, q.y);
+}
+__device__ __forceinline__ void store_pair(float *p, f2 v) {
+  *reinterpret_cast<float2 *>(p) = unpack2(v);
+}
+__device__ __forceinline__ void store_pairs(__nv_bfloat16 *p, const f2 (&v)[2]) {
+  const float2 q = unpack2(v[0]), r = unpack2(v[1]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(q.x, q.y), f32_to_bf16x2(r.x, r.y));
+}
+__device__ __forceinline__ void store_pairs(float *p, const f2 (&v)[2]) {
+  const float2 q = unpack2(v[0]), r = unpack2(v[1]);
+  *reinterpret_cast<float4 *>(p) = make_float4(q.x, q.y, r.x, r.y);
+}
+__device__ __forceinline__ f2 silu2(f2 v) {
+  const float2 q = unpack2(v);
+  return pack2(q.x * sigmoid_f32(q.x), q.y * sigmoid_f32(q.y));
+}
+
+// Row t < 0 of a sequence (before its first token): state row t + W - 1, or
+// zeros.
+template <typename T, int W, int P>
+__device__ __forceinline__ rawp<T, P> early_row(const T *state, int t, int E) {
+  rawp<T, P> r;
+  if (state) r.load(state + (int64_t)(t + W - 1) * E);
+  else r.zero();
+  return r;
+}
+
+// The taps of 2P consecutive channels as pairs: w [E][W], from channel e.
+template <int W, int P>
+__device__ __forceinline__ void load_taps(const float *w, int e, f2 (&out)[W][P]) {
+  float q[2 * P * W];
+#pragma unroll
+  for (int i = 0; i < P * W; ++i) {  // 2 W floats per pair: 8-byte aligned
+    const float2 v = *reinterpret_cast<const float2 *>(w + (int64_t)e * W + 2 * i);
+    q[2 * i] = v.x;
+    q[2 * i + 1] = v.y;
+  }
+#pragma unroll
+  for (int k = 0; k < W; ++k)
+#pragma unroll
+    for (int p = 0; p < P; ++p) out[k][p] = pack2(q[2 * p * W + k], q[(2 * p + 1) * W + k]);
 }
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ ConvArgs a, int runs) {
-  const int cols = a.E / 8;
+  const unsigned cols = a.E / 4;
   const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (idx >= (int64_t)a.B * runs * cols) return;
-  const int e = static_cast<int>(idx % cols) * 8;
-  const int64_t br = idx / cols;
-  const int run = static_cast<int>(br % runs);
-  const int64_t b = br / runs;
+  const int64_t total = (int64_t)a.B * runs * cols;
+  if (idx >= total) return;
+  int e, run;
+  int64_t b;
+  if (total < ((int64_t)1 << 32)) {  // 32-bit divisions
+    const unsigned i = static_cast<unsigned>(idx), br = i / cols;
+    e = static_cast<int>(i - br * cols) * 4;
+    b = br / static_cast<unsigned>(runs);
+    run = static_cast<int>(br - static_cast<unsigned>(b) * runs);
+  } else {
+    const int64_t br = idx / cols;
+    e = static_cast<int>(idx - br * cols) * 4;
+    b = br / runs;
+    run = static_cast<int>(br - b * runs);
+  }
   const int len = a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
   const int t0 = run * kRun, t1 = min(len, t0 + kRun);
   const T *x = static_cast<const T *>(a.x) + b * a.L * a.ldx + e;
+  const T *st = a.state ? static_cast<const T *>(a.state) + b * (W - 1) * a.E + e : nullptr;
   T *y = static_cast<T *>(a.y) + b * a.L * a.E + e;
 
   if (run == runs - 1 && a.state_out) {
@@ -50,100 +131,101 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
       const int t = len - (W - 1) + k;
-      raw8<T> r;
+      rawp<T, 2> r;
       if (t >= 0) r.load(x + t * a.ldx);
-      else if (a.state) r.load(static_cast<const T *>(a.state) + (b * (W - 1) + t + W - 1) * a.E + e);
-      else r.zero();
+      else r = early_row<T, W, 2>(st, t, a.E);
       r.store(so + (int64_t)k * a.E);
     }
   }
   if (t0 >= t1) return;
 
-  float w[W][8], bias[8];
-  {
-    float q[8 * W];  // w rows of 8 consecutive channels are consecutive
+  constexpr int kAhead = 8;
+  const T *xp = x + t0 * a.ldx;
+  T *yp = y + (int64_t)t0 * a.E;
+  rawp<T, 2> nxt[kAhead];
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i) {
-      const float4 v = *reinterpret_cast<const float4 *>(a.w + (int64_t)e * W + 4 * i);
-      q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
-    }
-#pragma unroll
-    for (int k = 0; k < W; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[k][i] = q[i * W + k];
+  for (int j = 0; j < kAhead; ++j)
+    if (t0 + j < t1) nxt[j].load(xp + j * a.ldx);
+  f2 w[W][2], bias[2], win[W][2];  // win[k] = row t - W + 1 + k
+  load_taps<W, 2>(a.w, e, w);
+  bias[0] = bias[1] = dup2(0.f);
+  if (a.bias) {
+    const float4 q = *reinterpret_cast<const float4 *>(a.bias + e);
+    bias[0] = pack2(q.x, q.y);
+    bias[1] = pack2(q.z, q.w);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = 0.f;
-  if (a.bias) load8(a.bias + e, bias);
-
-  float win[W][8];  // win[k] = row t - W + 1 + k
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
     const int t = t0 - (W - 1) + k;
-    if (t >= 0) load8(x + t * a.ldx, win[k + 1]);
-    else state_row8<T, W>(a, b, t, e, win[k + 1]);
+    rawp<T, 2> r;
+    if (t >= 0) r.load(x + t * a.ldx);
+    else r = early_row<T, W, 2>(st, t, a.E);
+    r.get(win[k + 1]);
   }
-  constexpr int kAhead = 8;
   for (int tb = t0; tb < t1; tb += kAhead) {
-    raw8<T> nxt[kAhead];
+    rawp<T, 2> cur[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (tb + j < t1) nxt[j].load(x + (tb + j) * a.ldx);
+    for (int j = 0; j < kAhead; ++j) {
+      cur[j] = nxt[j];
+      if (tb + kAhead + j < t1) nxt[j].load(xp + (kAhead + j) * a.ldx);
+    }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (tb + j < t1) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) win[k][i] = win[k + 1][i];
-        nxt[j].get(win[W - 1]);
-        float o[8];
+          for (int p = 0; p < 2; ++p) win[k][p] = win[k + 1][p];
+        cur[j].get(win[W - 1]);
+        f2 o[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float p = bias[i];
+        for (int p = 0; p < 2; ++p) {
+          o[p] = bias[p];
 #pragma unroll
-          for (int k = 0; k < W; ++k) p = fmaf(w[k][i], win[k][i], p);
-          o[i] = a.silu ? p * sigmoid_f32(p) : p;
+          for (int k = 0; k < W; ++k) o[p] = fma2(w[k][p], win[k][p], o[p]);
+          if (a.silu) o[p] = silu2(o[p]);
         }
-        store8(y + (int64_t)(tb + j) * a.E, o);
+        store_pairs(yp + (int64_t)j * a.E, o);
       }
     }
+    xp += kAhead * a.ldx;
+    yp += (int64_t)kAhead * a.E;
   }
 }
 
+// One token: a thread keeps its channels' taps for the sequences of its slice.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_constant__ ConvArgs a) {
-  const int cols = a.E / 8;
-  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (idx >= (int64_t)a.B * cols) return;
-  const int e = static_cast<int>(idx % cols) * 8;
-  const int64_t b = idx / cols;
-  T *st = static_cast<T *>(a.state_out) + b * (W - 1) * a.E + e;
-  raw8<T> r[W];
-#pragma unroll
-  for (int k = 0; k < W - 1; ++k) r[k].load(st + (int64_t)k * a.E);
-  r[W - 1].load(static_cast<const T *>(a.x) + b * a.ldx + e);
-  float q[8 * W], o[8];
-#pragma unroll
-  for (int i = 0; i < 2 * W; ++i) {
-    const float4 v = *reinterpret_cast<const float4 *>(a.w + (int64_t)e * W + 4 * i);
-    q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
+__global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvArgs a) {
+  const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
+  if (e >= a.E) return;
+  f2 w[W][2], bias[2];
+  load_taps<W, 2>(a.w, e, w);
+  bias[0] = bias[1] = dup2(0.f);
+  if (a.bias) {
+    const float4 q = *reinterpret_cast<const float4 *>(a.bias + e);
+    bias[0] = pack2(q.x, q.y);
+    bias[1] = pack2(q.z, q.w);
   }
+  for (int64_t b = blockIdx.y; b < a.B; b += gridDim.y) {
+    T *st = static_cast<T *>(a.state_out) + b * (W - 1) * a.E + e;
+    rawp<T, 2> r[W];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  if (a.bias) load8(a.bias + e, o);
+    for (int k = 0; k < W - 1; ++k) r[k].load(st + (int64_t)k * a.E);
+    r[W - 1].load(static_cast<const T *>(a.x) + b * a.ldx + e);
+    f2 o[2] = {bias[0], bias[1]};
 #pragma unroll
-  for (int k = 0; k < W; ++k) {
-    float x[8];
-    r[k].get(x);
+    for (int k = 0; k < W; ++k) {
+      f2 x[2];
+      r[k].get(x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(q[i * W + k], x[i], o[i]);
-    if (k > 0) r[k].store(st + (int64_t)(k - 1) * a.E);
+      for (int p = 0; p < 2; ++p) o[p] = fma2(w[k][p], x[p], o[p]);
+      if (k > 0) r[k].store(st + (int64_t)(k - 1) * a.E);
+    }
+    if (a.silu)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) o[p] = silu2(o[p]);
+    store_pairs(static_cast<T *>(a.y) + b * a.E + e, o);
   }
-  if (a.silu)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= sigmoid_f32(o[i]);
-  store8(static_cast<T *>(a.y) + b * a.E + e, o);
 }
 
 // Backward.  With dpre_t = dy_t silu'(pre_t):
@@ -153,31 +235,25 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_consta
 // token t it knows dpre_(t-W+1..t), which is all that dx_(t-W+1) needs.  A run
 // of dx rows [s0, s1) reads W - 1 tokens of dpre beyond s1, recomputed by the
 // next run too; the sums count a token only in the run that owns it.  A CTA
-// is 32 vectors of channels x 8 runs at a time; its sums meet in shared
-// memory and leave as one record, and a second kernel adds the records in
-// their order, so the result does not depend on scheduling.
-constexpr int kBwdCols = 32, kBwdRows = 8, kBwdVec = 4, kBwdRun = 32;
+// is 32 pairs of channels x 8 runs at a time; its sums meet in shared memory
+// and leave as one record, and a second kernel adds the records in their
+// order, so the result does not depend on scheduling.
+constexpr int kBwdCols = 32, kBwdRows = 8, kBwdRun = 32;
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kBwdCols * kBwdRows)
     conv_bwd_kernel(const __grid_constant__ ConvArgs a, const __grid_constant__ ConvGrads g,
                     float *__restrict__ rec, int runs) {
   const int tx = threadIdx.x % kBwdCols, ty = threadIdx.x / kBwdCols;
-  const int e = (blockIdx.x * kBwdCols + tx) * kBwdVec;
+  const int e = (blockIdx.x * kBwdCols + tx) * 2;
   const bool in = e < a.E;
-  float w[W][4], bias[4], dw[W][4], db[4];
+  f2 w[W][1], bias = dup2(0.f), dw[W], db = dup2(0.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bias[i] = in && a.bias ? a.bias[e + i] : 0.f;
-    db[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      w[k][i] = in ? a.w[(int64_t)(e + i) * W + k] : 0.f;
-      dw[k][i] = 0.f;
-    }
+  for (int k = 0; k < W; ++k) w[k][0] = dw[k] = dup2(0.f);
+  if (in) {
+    load_taps<W, 1>(a.w, e, w);
+    if (a.bias) bias = pack2(a.bias[e], a.bias[e + 1]);
   }
-  // the first run of a sequence starts W - 1 rows early when the state has a
-  // gradient
   const int64_t total = (int64_t)a.B * runs;
   for (int64_t r = (int64_t)blockIdx.y * kBwdRows + ty; in && r < total;
        r += (int64_t)gridDim.y * kBwdRows) {
@@ -188,106 +264,108 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
     const T *dy = static_cast<const T *>(g.dy) + b * a.L * a.E + e;
     T *dx = static_cast<T *>(g.dx) + b * a.L * a.E + e;
     const T *st = a.state ? static_cast<const T *>(a.state) + b * (W - 1) * a.E + e : nullptr;
-    float xw[W][4], dp[W][4];  // xw[k] = row t-W+1+k; dp[k] = dpre of t-W+1+k
+    const int last = s1 + W - 1;        // tokens walked: [s0, last)
+    const int here = min(last, a.L);    // those that exist
+    constexpr int kAhead = 8;
+    rawp<T, 1> xn[kAhead], gn[kAhead];
+    auto fetch = [&](int j, int t) {
+      xn[j].zero();
+      gn[j].zero();
+      if (t < here) {
+        xn[j].load(x + t * a.ldx);
+        gn[j].load(dy + (int64_t)t * a.E);
+      }
+    };
 #pragma unroll
-    for (int k = 0; k < W; ++k)
+    for (int j = 0; j < kAhead; ++j) fetch(j, s0 + j);
+    f2 xw[W], dp[W];  // xw[k] = row t-W+1+k; dp[k] = dpre of t-W+1+k
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xw[k][i] = dp[k][i] = 0.f;
+    for (int k = 0; k < W; ++k) xw[k] = dp[k] = dup2(0.f);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
       const int t = s0 - (W - 1) + k;
-      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t >= 0) q = load4(x + t * a.ldx);
-      else if (st) q = load4(st + (int64_t)(t + W - 1) * a.E);
-      xw[k + 1][0] = q.x; xw[k + 1][1] = q.y; xw[k + 1][2] = q.z; xw[k + 1][3] = q.w;
+      rawp<T, 1> q;
+      if (t >= 0) q.load(x + t * a.ldx);
+      else q = early_row<T, W, 1>(st, t, a.E);
+      f2 v[1];
+      q.get(v);
+      xw[k + 1] = v[0];
     }
-    const int last = s1 + W - 1;  // tokens walked: [s0, last)
-    constexpr int kAhead = 4;
     for (int tb = s0; tb < last; tb += kAhead) {
-      float4 xq[kAhead], gq[kAhead];
+      rawp<T, 1> xq[kAhead], gq[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        xq[j] = gq[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (tb + j < min(last, a.L)) {
-          xq[j] = load4(x + (tb + j) * a.ldx);
-          gq[j] = load4(dy + (int64_t)(tb + j) * a.E);
-        }
+        xq[j] = xn[j];
+        gq[j] = gn[j];
+        fetch(j, tb + kAhead + j);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int t = tb + j;
-        if (t >= last) break;
+        if (t < last) {
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xw[k][i] = xw[k + 1][i];
-            dp[k][i] = dp[k + 1][i];
+          for (int k = 0; k < W - 1; ++k) {
+            xw[k] = xw[k + 1];
+            dp[k] = dp[k + 1];
           }
-        const float xv[4] = {xq[j].x, xq[j].y, xq[j].z, xq[j].w};
-        const float gv[4] = {gq[j].x, gq[j].y, gq[j].z, gq[j].w};
-        const bool own = t < s1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          xw[W - 1][i] = xv[i];
-          float d = gv[i];  // zero behind the last token
+          f2 v[1];
+          xq[j].get(v);
+          xw[W - 1] = v[0];
+          gq[j].get(v);
+          f2 d = v[0];
           if (a.silu) {
-            float p = bias[i];
+            f2 p2 = bias;
 #pragma unroll
-            for (int k = 0; k < W; ++k) p = fmaf(w[k][i], xw[k][i], p);
-            const float s = sigmoid_f32(p);
-            d *= s * fmaf(p, 1.f - s, 1.f);
+            for (int k = 0; k < W; ++k) p2 = fma2(w[k][0], xw[k], p2);
+            const float2 p = unpack2(p2), q = unpack2(d);
+            const float s = sigmoid_f32(p.x), u = sigmoid_f32(p.y);
+            d = pack2(q.x * (s * fmaf(p.x, 1.f - s, 1.f)), q.y * (u * fmaf(p.y, 1.f - u, 1.f)));
           }
-          if (t >= a.L) d = 0.f;
-          dp[W - 1][i] = d;
-          if (own) {
-            db[i] += d;
+          if (t >= a.L) d = dup2(0.f);
+          dp[W - 1] = d;
+          if (t < s1) {
+            db = add2(db, d);
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][i] = fmaf(d, xw[k][i], dw[k][i]);
+            for (int k = 0; k < W; ++k) dw[k] = fma2(d, xw[k], dw[k]);
           }
-        }
-        const int s = t - (W - 1);
-        if (s >= s0 || (run == 0 && g.dstate)) {
-          float4 q;
-          float *o = &q.x;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = 0.f;
+          const int s = t - (W - 1);
+          if (s >= s0 || (run == 0 && g.dstate)) {
             // dpre_(s + W - 1 - k) = dp[W - 1 - k]
+            f2 o = mul2(w[0][0], dp[W - 1]);
 #pragma unroll
-            for (int k = 0; k < W; ++k) v = fmaf(w[k][i], dp[W - 1 - k][i], v);
-            o[i] = v;
+            for (int k = 1; k < W; ++k) o = fma2(w[k][0], dp[W - 1 - k], o);
+            if (s >= 0) store_pair(dx + (int64_t)s * a.E, o);
+            else store_pair(static_cast<T *>(g.dstate) + (b * (W - 1) + s + W - 1) * a.E + e, o);
           }
-          if (s >= 0) store4(dx + (int64_t)s * a.E, q);
-          else store4(static_cast<T *>(g.dstate) + (b * (W - 1) + s + W - 1) * a.E + e, q);
         }
       }
     }
   }
   // sums of the CTA's runs, in row order; a record is dw [E][W], then dbias [E]
-  __shared__ float4 sh[kBwdRows][kBwdCols];
+  __shared__ float2 sh[kBwdRows][kBwdCols];
   float *out = rec + (int64_t)blockIdx.y * (W + 1) * a.E;
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
     __syncthreads();
-    sh[ty][tx] = k < W ? make_float4(dw[k % W][0], dw[k % W][1], dw[k % W][2], dw[k % W][3])
-                       : make_float4(db[0], db[1], db[2], db[3]);
+    sh[ty][tx] = unpack2(k < W ? dw[k % W] : db);
     __syncthreads();
     if (ty == 0 && in) {
-      float4 q = sh[0][tx];
+      float2 q = sh[0][tx];
       for (int j = 1; j < kBwdRows; ++j) {
-        q.x += sh[j][tx].x; q.y += sh[j][tx].y; q.z += sh[j][tx].z; q.w += sh[j][tx].w;
+        q.x += sh[j][tx].x;
+        q.y += sh[j][tx].y;
       }
       const int stride = k < W ? W : 1;
       float *o = k < W ? out + (int64_t)e * W + k : out + (int64_t)a.E * W + e;
-      o[0] = q.x; o[stride] = q.y; o[2 * stride] = q.z; o[3 * stride] = q.w;
+      o[0] = q.x;
+      o[stride] = q.y;
     }
   }
 }
 
 int conv_bwd_blocks(int B, int L, int E) {
   const int64_t rows = ((int64_t)B * ((L + kBwdRun - 1) / kBwdRun) + kBwdRows - 1) / kBwdRows;
-  const int colb = (E / kBwdVec + kBwdCols - 1) / kBwdCols;
+  const int colb = (E / 2 + kBwdCols - 1) / kBwdCols;
   int64_t y = (152 * 4 + colb - 1) / colb;  // about four CTAs per SM
   if (y > rows) y = rows;
   return y < 1 ? 1 : static_cast<int>(y);
@@ -296,21 +374,24 @@ int conv_bwd_blocks(int B, int L, int E) {
 template <typename T, int W>
 cudaError_t conv_fwd_typed(const ConvArgs &a, cudaStream_t s) {
   const int runs = a.L > 0 ? (a.L + kRun - 1) / kRun : 1;
-  const int64_t n = (int64_t)a.B * runs * (a.E / 8);
+  const int64_t n = (int64_t)a.B * runs * (a.E / 4);
   conv_kernel<T, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, runs);
   return cudaGetLastError();
 }
 template <typename T, int W>
 cudaError_t conv_step_typed(const ConvArgs &a, cudaStream_t s) {
-  const int64_t n = (int64_t)a.B * (a.E / 8);
-  conv_step_kernel<T, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+  const int nx = (a.E / 4 + 127) / 128;
+  // about eight CTAs per SM; beyond that a CTA takes several sequences
+  int ny = (152 * 8 + nx - 1) / nx;
+  if (ny > a.B) ny = a.B;
+  conv_step_kernel<T, W><<<dim3(nx, ny), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T, int W>
 cudaError_t conv_bwd_typed(const ConvArgs &a, const ConvGrads &g, void *ws, cudaStream_t s) {
   const int runs = (a.L + kBwdRun - 1) / kBwdRun;
   const int ny = conv_bwd_blocks(a.B, a.L, a.E);
-  const int nx = (a.E / kBwdVec + kBwdCols - 1) / kBwdCols;
+  const int nx = (a.E / 2 + kBwdCols - 1) / kBwdCols;
   float *rec = static_cast<float *>(ws);
   conv_bwd_kernel<T, W><<<dim3(nx, ny), kBwdCols * kBwdRows, 0, s>>>(a, g, rec, runs);
   cudaError_t e = cudaGetLastError();
