@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(kCols * kSlices)
   const int64_t c = (int64_t)blockIdx.x * kCols + tx;
   float s = 0.f;
   if (c < C) {
-#pragma unroll 4
+#pragma unroll 16
     for (int r = ty; r < n; r += kSlices) s += rec[r * C + c];
   }
   sh[ty][tx] = s;

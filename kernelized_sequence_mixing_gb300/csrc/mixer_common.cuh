@@ -69,18 +69,20 @@ constexpr float kLn2 = 0.6931471805599453f;
 // evaluated on a grid of 200 001 points): the logarithm's own instruction is
 // only accurate absolutely, and steps of 1e-3 need it relatively.  NaN stays
 // NaN (through the exponential).
-__device__ __forceinline__ float softplus_f32(float x) {
-  const float t = ex2(-fabsf(x) * kLog2e);
-  float p = -0.00837115291506052f;
-  p = fmaf(p, t, 0.04349390044808388f);
-  p = fmaf(p, t, -0.1068500280380249f);
-  p = fmaf(p, t, 0.1768747717142105f);
-  p = fmaf(p, t, -0.24474774301052094f);
-  p = fmaf(p, t, 0.3327192962169647f);
-  p = fmaf(p, t, -0.49997174739837646f);
-  p = fmaf(p, t, 0.9999997615814209f);
-  return fmaf(p, t, fmaxf(x, 0.f));
+__device__ __forceinline__ f2 softplus_f2(f2 x) {
+  const float2 q = unpack2(x);
+  const f2 t = pack2(ex2(-fabsf(q.x) * kLog2e), ex2(-fabsf(q.y) * kLog2e));
+  f2 p = dup2(-0.00837115291506052f);
+  p = fma2(p, t, dup2(0.04349390044808388f));
+  p = fma2(p, t, dup2(-0.1068500280380249f));
+  p = fma2(p, t, dup2(0.1768747717142105f));
+  p = fma2(p, t, dup2(-0.24474774301052094f));
+  p = fma2(p, t, dup2(0.3327192962169647f));
+  p = fma2(p, t, dup2(-0.49997174739837646f));
+  p = fma2(p, t, dup2(0.9999997615814209f));
+  return fma2(p, t, pack2(fmaxf(q.x, 0.f), fmaxf(q.y, 0.f)));
 }
+__device__ __forceinline__ float softplus_f32(float x) { return unpack2(softplus_f2(dup2(x))).x; }
 
 // 1 / (1 + exp(-x)); exp(-x) = inf gives 0, NaN stays NaN
 __device__ __forceinline__ float sigmoid_f32(float x) {
@@ -138,6 +140,32 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
                  f32_to_bf16x2(x[6], x[7]));
 }
 
+// The same as four pairs.
+__device__ __forceinline__ void load8p(const float *p, f2 (&x)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
+  const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(p + 4);
+  x[0] = {a.x};
+  x[1] = {a.y};
+  x[2] = {b.x};
+  x[3] = {b.y};
+}
+__device__ __forceinline__ void load8p(const __nv_bfloat16 *p, f2 (&x)[4]) {
+  const uint4 a = *reinterpret_cast<const uint4 *>(p);
+  x[0] = bf16x2_to_f2(a.x);
+  x[1] = bf16x2_to_f2(a.y);
+  x[2] = bf16x2_to_f2(a.z);
+  x[3] = bf16x2_to_f2(a.w);
+}
+__device__ __forceinline__ void store8p(float *p, const f2 (&x)[4]) {
+  *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(x[0].v, x[1].v);
+  *reinterpret_cast<ulonglong2 *>(p + 4) = make_ulonglong2(x[2].v, x[3].v);
+}
+__device__ __forceinline__ void store8p(__nv_bfloat16 *p, const f2 (&x)[4]) {
+  const float2 a = unpack2(x[0]), b = unpack2(x[1]), c = unpack2(x[2]), d = unpack2(x[3]);
+  *reinterpret_cast<uint4 *>(p) = make_uint4(f32_to_bf16x2(a.x, a.y), f32_to_bf16x2(b.x, b.y),
+                                             f32_to_bf16x2(c.x, c.y), f32_to_bf16x2(d.x, d.y));
+}
+
 // Four consecutive elements as fp32 (8- or 16-byte aligned).
 __device__ __forceinline__ float4 load4(const float *p) {
   return *reinterpret_cast<const float4 *>(p);
@@ -168,6 +196,12 @@ template <> struct raw8<__nv_bfloat16> {
     *reinterpret_cast<uint4 *>(p) = a;
   }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void getp(f2 (&x)[4]) const {
+    x[0] = bf16x2_to_f2(a.x);
+    x[1] = bf16x2_to_f2(a.y);
+    x[2] = bf16x2_to_f2(a.z);
+    x[3] = bf16x2_to_f2(a.w);
+  }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     bf16x2_to_f32(a.x, x[0], x[1]);
     bf16x2_to_f32(a.y, x[2], x[3]);
@@ -186,6 +220,12 @@ template <> struct raw8<float> {
     *reinterpret_cast<float4 *>(p + 4) = b;
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void getp(f2 (&x)[4]) const {
+    x[0] = pack2(a.x, a.y);
+    x[1] = pack2(a.z, a.w);
+    x[2] = pack2(b.x, b.y);
+    x[3] = pack2(b.z, b.w);
+  }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;

@@ -42,6 +42,7 @@ struct RowArgs {
   int H, D, L;
   float eps, scale;
   bool heads_first;
+  int hb;                 // heads of a CTA's rows: a power of two that divides H
 };
 
 // Element offset of row (token j, head h) in y.  Rows count less than 2^31,
@@ -77,67 +78,97 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*sh)[K][kThreads /
   }
 }
 
+// The row of group `grp` of this CTA, `turn` groups of rows on: its head and
+// token.  CTAs go over the head blocks first.
+struct Row {
+  int h;
+  unsigned j;
+};
+__device__ __forceinline__ Row first_row(const RowArgs &a, int grp, int rows_per_cta, int turn_rows,
+                                         unsigned block) {
+  Row r;
+  const unsigned hblocks = a.H / a.hb;
+  const unsigned tb = hblocks == 1 ? block : block / hblocks;
+  r.h = static_cast<int>(block - tb * hblocks) * a.hb + (grp & (a.hb - 1));
+  r.j = tb * (rows_per_cta / a.hb) + (grp / a.hb) + turn_rows;
+  return r;
+}
+
 template <typename T, int MODE, int LANES, int VPT>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ RowArgs a) {
   constexpr int GPC = kThreads / LANES;
+  constexpr int R = VPT == 1 && LANES < 256 ? 2 : 1;  // rows per group, loaded together
   __shared__ float sh[2][1][kThreads / 32];
   int round = 0;
-  const int lane = threadIdx.x % LANES;
-  const unsigned rows = a.tokens * a.H;
-  const unsigned row = blockIdx.x * GPC + threadIdx.x / LANES;
-  const bool live = row < rows;
-  const unsigned j = MODE == kResidual ? row : live ? row / (unsigned)a.H : 0u;
-  const int h = MODE == kResidual || !live ? 0 : static_cast<int>(row - j * a.H);
-  const int64_t off = live ? (int64_t)row * a.D : 0;
-  const T *in1 = static_cast<const T *>(a.in1) + (MODE == kResidual ? off : y_offset(a, j, h));
-  const T *in2 = a.in2 ? static_cast<const T *>(a.in2) + off : nullptr;
-  float p[VPT][8], g[VPT][8], s[1] = {0.f};
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  raw8<T> rp[R][VPT], rg[R][VPT];
+  int64_t off[R];
+  bool live[R];
+  int h = 0;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int c = (v * LANES + lane) * 8;
+  for (int r = 0; r < R; ++r) {
+    const Row row = first_row(a, grp, GPC * R, r * (GPC / a.hb), blockIdx.x);
+    h = row.h;
+    live[r] = row.j < a.tokens;
+    off[r] = live[r] ? (int64_t)(row.j * a.H + h) * a.D : 0;
+    const T *in1 = static_cast<const T *>(a.in1) +
+                   (MODE == kResidual || !live[r] ? off[r] : y_offset(a, row.j, h));
+    const T *in2 = static_cast<const T *>(a.in2) + off[r];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[v][i] = g[v][i] = 0.f;
-    if (live && c < a.D) {
-      load8(in1 + c, p[v]);
-      if (in2) load8(in2 + c, g[v]);
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * LANES + lane) * 8;
+      rp[r][v].zero();
+      rg[r][v].zero();
+      if (live[r] && c < a.D) {
+        rp[r][v].load(in1 + c);
+        if (MODE != kResidual || a.in2) rg[r][v].load(in2 + c);
+      }
     }
   }
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
+  for (int r = 0; r < R; ++r) {
+    float p[VPT][8], g[VPT][8], s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (MODE == kResidual) {
-        p[v][i] = fmaf(a.scale, p[v][i], g[v][i]);
-      } else {
-        g[v][i] *= sigmoid_f32(g[v][i]);
-        if (MODE == kGateFirst) p[v][i] *= g[v][i];
-      }
-      s[0] = fmaf(p[v][i], p[v][i], s[0]);
-    }
-  row_sum<LANES, 1>(s, sh, round);
-  const float rstd = rsqrtf(s[0] / a.D + a.eps);
-  if (!live) return;
-  T *o = static_cast<T *>(a.out1) + off;
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int c = (v * LANES + lane) * 8;
-    if (c < a.D) {
-      if (MODE == kResidual) store8(static_cast<T *>(a.out2) + off + c, p[v]);
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-      if (a.w) load8(a.w + (int64_t)h * a.D + c, w);
+    for (int v = 0; v < VPT; ++v) {
+      rp[r][v].get(p[v]);
+      rg[r][v].get(g[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        w[i] *= p[v][i] * rstd;
-        if (MODE == kGateAfter) w[i] *= g[v][i];
+        if (MODE == kResidual) {
+          p[v][i] = fmaf(a.scale, p[v][i], g[v][i]);
+        } else {
+          g[v][i] *= sigmoid_f32(g[v][i]);
+          if (MODE == kGateFirst) p[v][i] *= g[v][i];
+        }
+        s[0] = fmaf(p[v][i], p[v][i], s[0]);
       }
-      store8(o + c, w);
+    }
+    row_sum<LANES, 1>(s, sh, round);
+    const float rstd = rsqrtf(s[0] / a.D + a.eps);
+    if (!live[r]) continue;
+    T *o = static_cast<T *>(a.out1) + off[r];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * LANES + lane) * 8;
+      if (c < a.D) {
+        if (MODE == kResidual) store8(static_cast<T *>(a.out2) + off[r] + c, p[v]);
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        if (a.w) load8(a.w + (int64_t)h * a.D + c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[i] *= p[v][i] * rstd;
+          if (MODE == kGateAfter) w[i] *= g[v][i];
+        }
+        store8(o + c, w);
+      }
     }
   }
 }
 
-// One head per CTA (blockIdx.x % H); its row groups stride over the tokens.
+// hb heads per CTA (blockIdx.x % (H / hb)); its row groups stride over the
+// tokens.
 template <typename T, int MODE, int LANES, int VPT>
 __global__ void __launch_bounds__(kThreads)
     norm_bwd_kernel(const __grid_constant__ RowArgs a, int slots) {
@@ -145,7 +176,9 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float sh[2][2][kThreads / 32];
   int round = 0;
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+  const int hblocks = a.H / a.hb, slot = blockIdx.x / hblocks, h0 = blockIdx.x % hblocks * a.hb;
+  const int h = h0 + (grp & (a.hb - 1));
+  const int tpc = GPC / a.hb;  // tokens of a turn
   float w[VPT][8], dw[VPT][8];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -160,8 +193,8 @@ __global__ void __launch_bounds__(kThreads)
   const float invD = 1.f / a.D;
   // every group of the CTA makes the same number of turns (the sums cross
   // lanes of several groups)
-  for (unsigned j0 = slot * GPC; j0 < a.tokens; j0 += slots * GPC) {
-    const unsigned j = j0 + grp;
+  for (unsigned j0 = slot * tpc; j0 < a.tokens; j0 += slots * tpc) {
+    const unsigned j = j0 + grp / a.hb;
     const bool live = j < a.tokens;
     const unsigned jj = live ? j : 0u;
     const int64_t off = (int64_t)(jj * a.H + h) * a.D;
@@ -249,7 +282,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   if (!a.rec) return;
-  float *rec = a.rec + ((int64_t)slot * a.H + h) * a.D;
+  float *rec = a.rec + ((int64_t)slot * a.H + h0) * a.D;
   if constexpr (GPC == 1) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -257,19 +290,19 @@ __global__ void __launch_bounds__(kThreads)
       if (c < a.D) store8(rec + c, dw[v]);
     }
   } else {
-    // the groups' sums, in group order
+    // each head's groups, in group order
     __shared__ float part[GPC][LANES * 8];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       __syncthreads();
       store8(&part[grp][lane * 8], dw[v]);
       __syncthreads();
-      for (int i = threadIdx.x; i < LANES * 8; i += kThreads) {
-        const int c = v * LANES * 8 + i;
+      for (int i = threadIdx.x; i < a.hb * LANES * 8; i += kThreads) {
+        const int hh = i / (LANES * 8), k = i % (LANES * 8), c = v * LANES * 8 + k;
         if (c < a.D) {
-          float q = part[0][i];
-          for (int k = 1; k < GPC; ++k) q += part[k][i];
-          rec[c] = q;
+          float q = part[hh][k];
+          for (int g = hh + a.hb; g < GPC; g += a.hb) q += part[g][k];
+          rec[(int64_t)hh * a.D + c] = q;
         }
       }
     }
@@ -293,12 +326,20 @@ cudaError_t by_width(int D, F &&f) {
 
 int lanes_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 1024 ? 32 : 256; }
 
-// CTAs per head of a backward pass: about four per SM over all heads, no more
-// than there are rows for.
-int bwd_slots(int64_t tokens, int H, int D) {
+// Heads of a CTA's rows: up to four, as many as divide H and fit its groups.
+int head_block(int H, int D) {
   const int gpc = kThreads / lanes_of(D);
-  const int64_t most = (tokens + gpc - 1) / gpc;
-  int64_t n = (152 * 4 + H - 1) / H;
+  int hb = 4;
+  while (hb > gpc || H % hb) hb /= 2;
+  return hb;
+}
+
+// CTAs per head block of a backward pass: about four per SM over all blocks,
+// no more than there are rows for.
+int bwd_slots(int64_t tokens, int H, int D) {
+  const int hb = head_block(H, D), tpc = kThreads / lanes_of(D) / hb, blocks = H / hb;
+  const int64_t most = (tokens + tpc - 1) / tpc;
+  int64_t n = (152 * 4 + blocks - 1) / blocks;
   if (n > most) n = most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
@@ -307,9 +348,10 @@ template <typename T, int MODE>
 cudaError_t run_rows(const RowArgs &a, cudaStream_t s) {
   return by_width(a.D, [&](auto lanes, auto vpt) {
     constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
-    const int64_t rows = (int64_t)a.tokens * a.H;
-    constexpr int GPC = kThreads / LANES;
-    norm_kernel<T, MODE, LANES, VPT><<<(unsigned)((rows + GPC - 1) / GPC), kThreads, 0, s>>>(a);
+    constexpr int R = VPT == 1 && LANES < 256 ? 2 : 1;
+    const int tpc = kThreads / LANES * R / a.hb;  // tokens per CTA
+    const int64_t ctas = ((int64_t)a.tokens + tpc - 1) / tpc * (a.H / a.hb);
+    norm_kernel<T, MODE, LANES, VPT><<<(unsigned)ctas, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   });
 }
@@ -319,7 +361,7 @@ cudaError_t run_rows_bwd(const RowArgs &a, float *dw, cudaStream_t s) {
   const int slots = bwd_slots(a.tokens, a.H, a.D);
   cudaError_t e = by_width(a.D, [&](auto lanes, auto vpt) {
     constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
-    norm_bwd_kernel<T, MODE, LANES, VPT><<<(unsigned)(slots * a.H), kThreads, 0, s>>>(a, slots);
+    norm_bwd_kernel<T, MODE, LANES, VPT><<<(unsigned)(slots * (a.H / a.hb)), kThreads, 0, s>>>(a, slots);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !dw) return e;
@@ -336,6 +378,7 @@ RowArgs gate_rows(const NormGateArgs &n) {
   a.H = n.H;
   a.D = n.D;
   a.L = n.L;
+  a.hb = head_block(n.H, n.D);
   a.eps = n.eps;
   a.heads_first = n.heads_first;
   return a;
@@ -348,6 +391,7 @@ RowArgs residual_rows(const NormResidualArgs &n) {
   a.H = 1;
   a.D = n.E;
   a.L = 1;
+  a.hb = 1;
   a.eps = n.eps;
   a.scale = n.scale;
   return a;

@@ -11,16 +11,23 @@
 //
 // What bounds it: one exponential and four fp32 operations per (channel,
 // state, token) against 8 bytes per (channel, token) in bf16, so at 16 states
-// the special function unit and the fp32 pipe, not memory.  Hence:
+// the instructions issued, not memory: per warp and token (512 states) 16
+// exponentials (4 cycles each), 32 packed operations (2 cycles each) and what
+// feeds them.  Hence:
 //   - a thread owns 4 channels x 4 states in registers: per token it reads one
 //     16-byte vector of dt, of u = dt x, and two of B and of C from shared
-//     memory for 16 state updates, done as packed pairs of channels;
-//   - the sum over states crosses N/4 lanes by a transposing exchange (3
-//     shuffles per token for 16 states);
+//     memory (few distinct addresses per warp: one wavefront each) for 16
+//     state updates, done as packed pairs of channels; the next token's
+//     operands are read before this token's are used;
+//   - the sum over states crosses N/4 lanes: each lane stores its part of y
+//     (beyond four lanes after an exchange) and the threads that write y add
+//     the parts, a third of the instructions of a shuffle tree;
 //   - softplus, the D term and the gate are applied once per (channel, token)
 //     when a tile of tokens is staged and when it is stored.
-// A tile's inputs are copied asynchronously while the previous tile computes;
-// the copying thread also converts them, so the raw buffers need no barrier.
+// A tile's inputs come by TMA, one box per tensor, while the previous tile
+// computes (copies issued per thread cost a shared-memory wavefront per lane,
+// which made them the largest load on that pipe; bulk copies per row kept the
+// issuing warp behind the others).
 //
 // Few channels leave SMs idle, so the tokens split into S parts: the state
 // pass leaves every part but the last its end state from zero and its sum of
@@ -28,69 +35,125 @@
 // pass folds the records before its part in front of its own scan.
 #include "kernels.h"
 #include "mixer_common.cuh"
+#include "tc_common.cuh"
 
 namespace linattn {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 2048;  // (token, channel) pairs per tile: 16 per thread
 constexpr int kMaxParts = 32;
+constexpr int kTile = 2048;  // (token, channel) pairs of a tile, at most
+constexpr int kSlots = 2;    // parts of y, at most
 
 template <typename T, int N>
 struct Shape {
-  static constexpr int LN = N / 4;            // lanes that share a channel's states
-  static constexpr int LC = 32 / LN;          // channel quads per warp
-  static constexpr int CPW = LC * 4;          // channels per warp
-  static constexpr int CT = CPW * kWarps;     // channels per CTA
-  static constexpr int TT = kTile / CT;       // tokens per tile
-  static constexpr int VC = CT / 8;           // 8-channel vectors per token
-  static constexpr int NV = kTile / 8 / kThreads;  // vectors per thread (2)
-  static constexpr int BV = TT * N / 8;       // vectors of B (and of C) per tile
-  static constexpr int NBV = (2 * BV + kThreads - 1) / kThreads;
+  static constexpr int LN = N / 4;         // lanes that share a channel's states
+  static constexpr int LC = 32 / LN;       // channel quads per warp
+  static constexpr int CPW = LC * 4;       // channels per warp
+  static constexpr int CT = CPW * kWarps;  // channels per CTA
+  static constexpr int TT = kTile / CT < 32 ? kTile / CT : 32;  // tokens per tile
+  static constexpr int TILE = TT * CT;     // (token, channel) pairs per tile
+  static constexpr int QC = CT / 4;        // channel quads per token
+  static constexpr int NQ = TILE / 4 / kThreads;  // quads staged per thread
+  static constexpr int SLOTS = LN < kSlots ? LN : kSlots;  // parts of y in shared memory
+  // the parts of one quad fall into different banks
+  static constexpr int SLOT = TILE + 32 / SLOTS;
+  static constexpr int BQ = TT * N / 4;    // quads of B (and of C) per tile
+  static constexpr int NBQ = (2 * BQ + kThreads - 1) / kThreads;
 };
 
-template <typename T, int N>
+// A tile as loaded (the state pass needs no C and z).
+template <typename T, int N, bool OUT>
+struct Stage {
+  using S = Shape<T, N>;
+  alignas(128) T x[S::TILE];
+  alignas(128) T dt[S::TILE];
+  alignas(128) T B[S::TT * N];
+  alignas(128) T C[OUT ? S::TT * N : 1];
+  alignas(128) T z[OUT ? S::TILE : 1];
+};
+
+template <typename T, int N, bool OUT>
 struct Smem {
   using S = Shape<T, N>;
-  float dt[kTile];
-  float u[kTile];  // dt x; overwritten by y
-  float2 B[S::TT * N], C[S::TT * N];  // each value twice, for the packed pairs
-  alignas(16) T raw[3][kTile];        // x, dt, z as loaded
-  alignas(16) T rawBC[2 * S::TT * N];
+  Stage<T, N, OUT> stage[2];
+  alignas(16) float dt[S::TILE];
+  float u[(OUT ? S::SLOTS : 1) * S::SLOT];  // dt x; y's first parts take its place, then the others
+  float2 B[S::TT * N], C[OUT ? S::TT * N : 1];  // each value twice, for the packed pairs
+  uint64_t full[2];
+  int abort;
 };
 
-// The sum over a channel quad's state lanes.  After it, lane sl of a quad
-// holds channel 2 (sl & 1) + ((sl >> 1) & 1) in v[0] (LN >= 4), or channels
-// 2 sl, 2 sl + 1 in v[0], v[1] (LN = 2).
-template <int LN>
-__device__ __forceinline__ void reduce_states(float (&v)[4], int lane) {
+// TMA maps of x, dt, z, B, C.
+struct ScanMaps {
+  CUtensorMap x, dt, z, B, C;
+};
+
+// Stores a channel quad's y of one token from its LN state lanes as SLOTS
+// parts, after an exchange over lane bits that halves the channels of a lane
+// (or, with one left, adds) until that many parts are left.
+template <int LN, int SLOTS, int SLOT>
+__device__ __forceinline__ void store_parts(float *y, int sl, f2 y01, f2 y23) {
   constexpr unsigned all = 0xffffffffu;
-  {
-    const bool hi = lane & 1;
-    const float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
-    const float s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
-    v[0] = k0 + __shfl_xor_sync(all, s0, 1);
-    v[1] = k1 + __shfl_xor_sync(all, s1, 1);
+  if constexpr (LN == SLOTS) {
+    *reinterpret_cast<ulonglong2 *>(y + sl * SLOT) = make_ulonglong2(y01.v, y23.v);
+  } else {
+    const bool hi = sl & 1;
+    const float2 a = unpack2(hi ? y23 : y01), b = unpack2(hi ? y01 : y23);
+    const float k0 = a.x + __shfl_xor_sync(all, b.x, 1), k1 = a.y + __shfl_xor_sync(all, b.y, 1);
+    if constexpr (LN == 2 * SLOTS) {
+      *reinterpret_cast<float2 *>(y + (sl >> 1) * SLOT + 2 * (sl & 1)) = make_float2(k0, k1);
+    } else {
+      const bool h2 = sl & 2;
+      float k = (h2 ? k1 : k0) + __shfl_xor_sync(all, h2 ? k0 : k1, 2);
+      int slot = sl >> 2;
+      if constexpr (LN == 8 * SLOTS) {
+        k += __shfl_xor_sync(all, k, 4);
+        slot = sl >> 3;
+      }
+      static_assert(LN <= 8 * SLOTS, "");
+      y[slot * SLOT + 2 * (sl & 1) + ((sl >> 1) & 1)] = k;
+    }
   }
-  if constexpr (LN >= 4) {
-    const bool hi = lane & 2;
-    const float k = hi ? v[1] : v[0], s = hi ? v[0] : v[1];
-    v[0] = k + __shfl_xor_sync(all, s, 2);
-  }
-  if constexpr (LN >= 8) v[0] += __shfl_xor_sync(all, v[0], 4);
-  if constexpr (LN >= 16) v[0] += __shfl_xor_sync(all, v[0], 8);
+}
+
+// Four consecutive elements as two pairs.
+__device__ __forceinline__ void load4p(const float *p, f2 (&x)[2]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
+  x[0] = {a.x};
+  x[1] = {a.y};
+}
+__device__ __forceinline__ void load4p(const __nv_bfloat16 *p, f2 (&x)[2]) {
+  const uint2 a = *reinterpret_cast<const uint2 *>(p);
+  x[0] = bf16x2_to_f2(a.x);
+  x[1] = bf16x2_to_f2(a.y);
+}
+__device__ __forceinline__ void store4p(float *p, const f2 (&x)[2]) {
+  *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(x[0].v, x[1].v);
+}
+__device__ __forceinline__ void store4p(__nv_bfloat16 *p, const f2 (&x)[2]) {
+  const float2 a = unpack2(x[0]), b = unpack2(x[1]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(a.x, a.y), f32_to_bf16x2(b.x, b.y));
 }
 
 // OUT: the output pass; otherwise the state pass of the parts but the last.
 template <typename T, int N, bool OUT>
-__global__ void __launch_bounds__(kThreads)
-    scan_kernel(const __grid_constant__ ScanArgs a, float *__restrict__ rec_h,
-                float *__restrict__ rec_dt, int S, int part_len) {
+__global__ void __launch_bounds__(kThreads, 4)
+    scan_kernel(const __grid_constant__ ScanArgs a, const __grid_constant__ ScanMaps maps,
+                float *__restrict__ rec_h,
+                float *__restrict__ rec_dt, int S, int part_len, unsigned int *timeouts) {
   using Sh = Shape<T, N>;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  Smem<T, N> &sm = *reinterpret_cast<Smem<T, N> *>(smem_raw);
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  Smem<T, N, OUT> &sm = *reinterpret_cast<Smem<T, N, OUT> *>(smem_raw);
 
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&sm.full[0], 1);
+    tc::mbar_init(&sm.full[1], 1);
+    tc::mbar_init_fence();
+    sm.abort = 0;
+  }
+  __syncthreads();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sl = lane & (Sh::LN - 1), lc = lane / Sh::LN;
   const int Eg = a.E / a.G;  // channels per group
@@ -106,11 +169,7 @@ __global__ void __launch_bounds__(kThreads)
   const int len = a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
   const int t0 = part * part_len, t1 = min(len, t0 + part_len);
 
-  const T *x = static_cast<const T *>(a.x) + (int64_t)b * a.L * a.ldx + e0;
-  const T *dt = static_cast<const T *>(a.dt) + (int64_t)b * a.L * a.lddt + e0;
-  const T *z = a.z ? static_cast<const T *>(a.z) + (int64_t)b * a.L * a.ldz + e0 : nullptr;
-  const T *Bm = static_cast<const T *>(a.Bm) + (int64_t)b * a.L * a.ldb + grp * N;
-  const T *Cm = static_cast<const T *>(a.Cm) + (int64_t)b * a.L * a.ldc + grp * N;
+  const bool gated = OUT && a.z;
   T *y = OUT ? static_cast<T *>(a.y) + (int64_t)b * a.L * a.E + e0 : nullptr;
 
   // this thread's channels and states
@@ -162,146 +221,151 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  float dtsum[4] = {0.f, 0.f, 0.f, 0.f};
+  f2 dtsum[2] = {dup2(0.f), dup2(0.f)};
 
-  // per-channel parameters of the staged vectors (one column per thread:
-  // kThreads is a multiple of VC)
-  const int vcol = (tid % Sh::VC) * 8, vrow = tid / Sh::VC;
-  constexpr int kRowStep = kThreads / Sh::VC;
-  const bool vin = vcol < nch;
-  float bias[8], dskip[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = dskip[i] = 0.f;
-  if (vin && a.dt_bias) load8(a.dt_bias + e0 + vcol, bias);
-  if (OUT && vin && a.D) load8(a.D + e0 + vcol, dskip);
+  // per-channel parameters of the staged quads (one column per thread:
+  // kThreads is a multiple of QC)
+  const int qcol = (tid % Sh::QC) * 4, qrow = tid / Sh::QC;
+  constexpr int kRowStep = kThreads / Sh::QC;
+  const bool qin = qcol < nch;
+  f2 bias[2] = {dup2(0.f), dup2(0.f)}, dskip[2] = {dup2(0.f), dup2(0.f)};
+  if (qin && a.dt_bias) load4p(a.dt_bias + e0 + qcol, bias);
+  if (OUT && qin && a.D) load4p(a.D + e0 + qcol, dskip);
 
-  auto issue = [&](int tb) {
-#pragma unroll
-    for (int i = 0; i < Sh::NV; ++i) {
-      const int r = vrow + i * kRowStep, t = tb + r;
-      const bool ok = vin && t < t1;
-      const int64_t tt = ok ? t : 0;
-      const int col = ok ? vcol : 0;
-      constexpr int per = 16 / sizeof(T);  // elements per 16-byte copy
-#pragma unroll
-      for (int j = 0; j < 8; j += per) {
-        const int s = r * Sh::CT + vcol + j;
-        copy16_async(&sm.raw[0][s], x + tt * a.ldx + col + j, ok);
-        copy16_async(&sm.raw[1][s], dt + tt * a.lddt + col + j, ok);
-        if (OUT && z) copy16_async(&sm.raw[2][s], z + tt * a.ldz + col + j, ok);
-      }
+  // The tile at token tb.  A box may reach behind the part's end, the
+  // sequence's or the group's: those rows are cleared when staged, those
+  // channels belong to lanes that store nothing.
+  auto issue = [&](int tb, int st) {
+    if (tid != 0) return;
+    Stage<T, N, OUT> &g = sm.stage[st];
+    uint64_t *bar = &sm.full[st];
+    constexpr uint32_t rows = Sh::TILE * sizeof(T), bc = Sh::TT * N * sizeof(T);
+    tc::mbar_arrive_expect_tx(bar, (gated ? 3 : 2) * rows + (OUT ? 2 : 1) * bc);
+    tc::tma_load_3d(g.x, &maps.x, e0, tb, b, bar);
+    tc::tma_load_3d(g.dt, &maps.dt, e0, tb, b, bar);
+    tc::tma_load_3d(g.B, &maps.B, grp * N, tb, b, bar);
+    if constexpr (OUT) {
+      tc::tma_load_3d(g.C, &maps.C, grp * N, tb, b, bar);
+      if (gated) tc::tma_load_3d(g.z, &maps.z, e0, tb, b, bar);
     }
-#pragma unroll
-    for (int i = 0; i < Sh::NBV; ++i) {
-      const int v = tid + i * kThreads;
-      const int which = v / Sh::BV, r = v % Sh::BV;
-      const int row = r / (N / 8), col = (r % (N / 8)) * 8;
-      if (which < (OUT ? 2 : 1)) {
-        const bool ok = tb + row < t1;
-        const int64_t t = ok ? tb + row : 0;
-        const T *src = (which ? Cm + t * a.ldc : Bm + t * a.ldb) + col;
-        constexpr int per = 16 / sizeof(T);
-#pragma unroll
-        for (int j = 0; j < 8; j += per) copy16_async(&sm.rawBC[v * 8 + j], src + j, ok);
-      }
+  };
+  struct Operands {
+    f2 d[2], u[2], b[4], c[4];
+  };
+  auto fetch = [&](int t) {
+    Operands o;
+    const int s = t * Sh::CT + c0;
+    const ulonglong2 dq = *reinterpret_cast<const ulonglong2 *>(&sm.dt[s]);
+    const ulonglong2 uq = *reinterpret_cast<const ulonglong2 *>(&sm.u[s]);
+    const ulonglong2 b01 = *reinterpret_cast<const ulonglong2 *>(&sm.B[t * N + n0]);
+    const ulonglong2 b23 = *reinterpret_cast<const ulonglong2 *>(&sm.B[t * N + n0 + 2]);
+    o.d[0] = {dq.x}; o.d[1] = {dq.y};
+    o.u[0] = {uq.x}; o.u[1] = {uq.y};
+    o.b[0] = {b01.x}; o.b[1] = {b01.y}; o.b[2] = {b23.x}; o.b[3] = {b23.y};
+    if constexpr (OUT) {
+      const ulonglong2 c01 = *reinterpret_cast<const ulonglong2 *>(&sm.C[t * N + n0]);
+      const ulonglong2 c23 = *reinterpret_cast<const ulonglong2 *>(&sm.C[t * N + n0 + 2]);
+      o.c[0] = {c01.x}; o.c[1] = {c01.y}; o.c[2] = {c23.x}; o.c[3] = {c23.y};
     }
-    copies_commit();
+    return o;
   };
 
-  if (t0 < t1) issue(t0);
-  for (int tb = t0; tb < t1; tb += Sh::TT) {
-    copies_wait<0>();
-    raw8<T> rx[Sh::NV], rz[Sh::NV];
-#pragma unroll
-    for (int i = 0; i < Sh::NV; ++i) {
-      const int r = vrow + i * kRowStep, s = r * Sh::CT + vcol;
-      rx[i].load(&sm.raw[0][s]);
-      if (OUT && z) rz[i].load(&sm.raw[2][s]);
-      float xv[8], dv[8];
-      rx[i].get(xv);
-      load8(&sm.raw[1][s], dv);
-      const bool in = tb + r < t1;  // rows behind the end leave the state as it is
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float q = dv[k] + bias[k];
-        dv[k] = in ? (a.softplus ? softplus_f32(q) : q) : 0.f;
-        xv[k] *= dv[k];
-      }
-      store8(&sm.dt[s], dv);
-      store8(&sm.u[s], xv);
+  if (t0 < t1) issue(t0, 0);
+  int turn = 0;
+  for (int tb = t0; tb < t1; tb += Sh::TT, ++turn) {
+    const int st = turn & 1, rows = min(Sh::TT, t1 - tb);
+    const Stage<T, N, OUT> &g = sm.stage[st];
+    // a wait that gives up ends the CTA; the next tile's copies are only
+    // issued after this one, so none is in flight but the one that failed
+    if (!tc::mbar_wait(&sm.full[st], (turn >> 1) & 1, &sm.abort, timeouts)) {
+      tc::mbar_wait_drain(&sm.full[st], (turn >> 1) & 1);
+      sm.abort = 1;
     }
 #pragma unroll
-    for (int i = 0; i < Sh::NBV; ++i) {
-      const int v = tid + i * kThreads;
-      if (v < (OUT ? 2 : 1) * Sh::BV) {
-        float q[8];
-        load8(&sm.rawBC[v * 8], q);
-        float4 *d = reinterpret_cast<float4 *>(v < Sh::BV ? &sm.B[v * 8] : &sm.C[(v - Sh::BV) * 8]);
+    for (int i = 0; i < Sh::NQ; ++i) {
+      const int r = qrow + i * kRowStep, s = r * Sh::CT + qcol;
+      f2 xv[2], dv[2];
+      load4p(&g.x[s], xv);
+      load4p(&g.dt[s], dv);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          d[k] = make_float4(q[2 * k], q[2 * k], q[2 * k + 1], q[2 * k + 1]);
+      for (int k = 0; k < 2; ++k) {
+        dv[k] = add2(dv[k], bias[k]);
+        if (a.softplus) dv[k] = softplus_f2(dv[k]);
+        xv[k] = mul2(xv[k], dv[k]);
+        // rows behind the end hold nothing and leave the state as it is
+        if (r >= rows) dv[k] = xv[k] = dup2(0.f);
+      }
+      store4p(&sm.dt[s], dv);
+      store4p(&sm.u[s], xv);
+    }
+#pragma unroll
+    for (int i = 0; i < Sh::NBQ; ++i) {
+      const int v = tid + i * kThreads, which = v / Sh::BQ, q = v % Sh::BQ * 4;
+      if (which < (OUT ? 2 : 1)) {
+        float4 w = load4((which ? g.C : g.B) + q);
+        if (q / N >= rows) w = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 *d = reinterpret_cast<float4 *>((which ? sm.C : sm.B) + q);
+        d[0] = make_float4(w.x, w.x, w.y, w.y);
+        d[1] = make_float4(w.z, w.z, w.w, w.w);
       }
     }
-    if (tb + Sh::TT < t1) issue(tb + Sh::TT);
     __syncthreads();
-#pragma unroll 4
+    if (sm.abort) return;
+    // the other stage was last read before this barrier
+    if (tb + Sh::TT < t1) issue(tb + Sh::TT, st ^ 1);
+    Operands nxt = fetch(0);
+#pragma unroll 16
     for (int t = 0; t < Sh::TT; ++t) {
-      const int s = t * Sh::CT + c0;
-      const ulonglong2 dq = *reinterpret_cast<const ulonglong2 *>(&sm.dt[s]);
-      const ulonglong2 uq = *reinterpret_cast<const ulonglong2 *>(&sm.u[s]);
-      const ulonglong2 b01 = *reinterpret_cast<const ulonglong2 *>(&sm.B[t * N + n0]);
-      const ulonglong2 b23 = *reinterpret_cast<const ulonglong2 *>(&sm.B[t * N + n0 + 2]);
-      const f2 d2[2] = {{dq.x}, {dq.y}}, u2[2] = {{uq.x}, {uq.y}};
-      const f2 bn[4] = {{b01.x}, {b01.y}, {b23.x}, {b23.y}};
+      const Operands o = nxt;
+      nxt = fetch(t + 1 < Sh::TT ? t + 1 : t);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-          h[c][n] = fma2(ex2_2(mul2(d2[c], A[c][n])), h[c][n], mul2(u2[c], bn[n]));
+          h[c][n] = fma2(ex2_2(mul2(o.d[c], A[c][n])), h[c][n], mul2(o.u[c], o.b[n]));
       if constexpr (OUT) {
-        const ulonglong2 c01 = *reinterpret_cast<const ulonglong2 *>(&sm.C[t * N + n0]);
-        const ulonglong2 c23 = *reinterpret_cast<const ulonglong2 *>(&sm.C[t * N + n0 + 2]);
-        const f2 cn[4] = {{c01.x}, {c01.y}, {c23.x}, {c23.y}};
         f2 y2[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          y2[c] = mul2(h[c][0], cn[0]);
+          y2[c] = mul2(h[c][0], o.c[0]);
 #pragma unroll
-          for (int n = 1; n < 4; ++n) y2[c] = fma2(h[c][n], cn[n], y2[c]);
+          for (int n = 1; n < 4; ++n) y2[c] = fma2(h[c][n], o.c[n], y2[c]);
         }
-        const float2 ya = unpack2(y2[0]), yb = unpack2(y2[1]);
-        float v[4] = {ya.x, ya.y, yb.x, yb.y};
-        reduce_states<Sh::LN>(v, lane);
-        // every lane of the warp has read u of this token (the shuffles), so
-        // y takes its place
-        if constexpr (Sh::LN == 2) {
-          *reinterpret_cast<float2 *>(&sm.u[s + 2 * sl]) = make_float2(v[0], v[1]);
-        } else if (sl < 4) {
-          sm.u[s + 2 * (sl & 1) + (sl >> 1)] = v[0];
-        }
+        __syncwarp();  // every lane has read u of this token: y takes its place
+        store_parts<Sh::LN, Sh::SLOTS, Sh::SLOT>(&sm.u[t * Sh::CT + c0], sl, y2[0], y2[1]);
       } else {
-        const float2 p = unpack2(d2[0]), q = unpack2(d2[1]);
-        dtsum[0] += p.x; dtsum[1] += p.y; dtsum[2] += q.x; dtsum[3] += q.y;
+        dtsum[0] = add2(dtsum[0], o.d[0]);
+        dtsum[1] = add2(dtsum[1], o.d[1]);
       }
     }
     __syncthreads();
     if constexpr (OUT) {
 #pragma unroll
-      for (int i = 0; i < Sh::NV; ++i) {
-        const int r = vrow + i * kRowStep;
-        if (vin && tb + r < t1) {
-          float yv[8], xv[8];
-          load8(&sm.u[r * Sh::CT + vcol], yv);
-          rx[i].get(xv);
+      for (int i = 0; i < Sh::NQ; ++i) {
+        const int r = qrow + i * kRowStep, s = r * Sh::CT + qcol;
+        if (qin && r < rows) {
+          f2 yv[2], xv[2];
+          load4p(&sm.u[s], yv);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) yv[k] = fmaf(dskip[k], xv[k], yv[k]);
-          if (z) {
-            float zv[8];
-            rz[i].get(zv);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) yv[k] *= zv[k] * sigmoid_f32(zv[k]);
+          for (int k = 1; k < Sh::SLOTS; ++k) {
+            f2 q[2];
+            load4p(&sm.u[k * Sh::SLOT + s], q);
+            yv[0] = add2(yv[0], q[0]);
+            yv[1] = add2(yv[1], q[1]);
           }
-          store8(y + (int64_t)(tb + r) * a.E + vcol, yv);
+          load4p(&g.x[s], xv);
+          yv[0] = fma2(dskip[0], xv[0], yv[0]);
+          yv[1] = fma2(dskip[1], xv[1], yv[1]);
+          if (gated) {
+            f2 zv[2];
+            load4p(&g.z[s], zv);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 q = unpack2(zv[k]);
+              yv[k] = mul2(mul2(yv[k], zv[k]), pack2(sigmoid_f32(q.x), sigmoid_f32(q.y)));
+            }
+          }
+          store4p(y + (int64_t)(tb + r) * a.E + qcol, yv);
         }
       }
     }
@@ -314,10 +378,13 @@ __global__ void __launch_bounds__(kThreads)
   } else {
     const int64_t rc = ((int64_t)b * (S - 1) + part) * a.E + e0 + c0;
     hd = rec_h + rc * N + n0;
-    if (sl == 0)
+    if (sl == 0) {
+      const float2 p = unpack2(dtsum[0]), q = unpack2(dtsum[1]);
+      const float v[4] = {p.x, p.y, q.x, q.y};
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (c0 + c < nch) rec_dt[rc + c] = dtsum[c];
+        if (c0 + c < nch) rec_dt[rc + c] = v[c];
+    }
   }
   if (hd) {
 #pragma unroll
@@ -335,22 +402,35 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int N>
 cudaError_t scan_typed(const ScanArgs &a, void *ws, int S, cudaStream_t s) {
   using Sh = Shape<T, N>;
-  constexpr int smem = sizeof(Smem<T, N>);
+  constexpr int es = sizeof(T);
+  ScanMaps maps = {};
+  auto map = [&](CUtensorMap *m, const void *p, int64_t width, int64_t ld, int box) {
+    return make_tmap_rows(m, p, es, width, a.L, a.B, ld, box, Sh::TT);
+  };
+  const int64_t GN = (int64_t)a.G * N;
+  if (a.L > 0 && (!map(&maps.x, a.x, a.E, a.ldx, Sh::CT) || !map(&maps.dt, a.dt, a.E, a.lddt, Sh::CT) ||
+                  !map(&maps.B, a.Bm, GN, a.ldb, N) || !map(&maps.C, a.Cm, GN, a.ldc, N) ||
+                  (a.z && !map(&maps.z, a.z, a.E, a.ldz, Sh::CT))))
+    return cudaErrorInvalidValue;
   const int tiles = a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
   const int part_len = selective_part_len(a.L, S);
   float *rec_h = static_cast<float *>(ws);
   float *rec_dt = rec_h + (size_t)a.B * (S - 1) * a.E * N;
+  unsigned int *timeouts = wait_timeout_counter();
+  if (!timeouts) return cudaErrorUnknown;
   if (S > 1) {
+    constexpr int smem = sizeof(Smem<T, N, false>);
     cudaError_t e = allow_smem(scan_kernel<T, N, false>, smem);
     if (e != cudaSuccess) return e;
     scan_kernel<T, N, false><<<(unsigned)((int64_t)a.B * (S - 1) * tiles), kThreads, smem, s>>>(
-        a, rec_h, rec_dt, S, part_len);
+        a, maps, rec_h, rec_dt, S, part_len, timeouts);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  constexpr int smem = sizeof(Smem<T, N, true>);
   cudaError_t e = allow_smem(scan_kernel<T, N, true>, smem);
   if (e != cudaSuccess) return e;
   scan_kernel<T, N, true><<<(unsigned)((int64_t)a.B * S * tiles), kThreads, smem, s>>>(
-      a, rec_h, rec_dt, S, part_len);
+      a, maps, rec_h, rec_dt, S, part_len, timeouts);
   return cudaGetLastError();
 }
 
@@ -448,9 +528,8 @@ cudaError_t step_states(const ScanArgs &a, cudaStream_t s) {
 bool selective_states_supported(int N) { return N == 8 || N == 16 || N == 32 || N == 64; }
 
 int selective_part_len(int L, int S) {
-  // whole tiles of every state size (64 tokens at most)
   const int l = (L + S - 1) / S;
-  return (l + 63) / 64 * 64;
+  return (l + 15) / 16 * 16;
 }
 
 int selective_parts(int B, int L, int E, int N, int G) {

@@ -6,19 +6,18 @@
 // with the rows before the first token taken from `state` (or zeros).
 //
 // Bound by memory: x is read once and y written once.  A thread owns a few
-// consecutive channels (4 in the forward pass, 2 in the backward pass: packed
-// pairs, so that 32 to 48 warps fit an SM) and a run of consecutive tokens;
-// the last W - 1 rows stay in registers as a sliding window, so only the
-// first W - 1 rows of a run are read twice (from L2), and the next tokens'
-// loads are issued a group ahead.
+// consecutive channels (16 bytes of them in the forward pass, one packed pair
+// in the backward pass, whose windows and sums need the registers) and a run
+// of consecutive tokens; the last W - 1 rows stay in registers as a sliding
+// window, so only the first W - 1 rows of a run are read twice (from L2), and
+// the next tokens' loads are issued a group ahead.
 #include "kernels.h"
 #include "mixer_common.cuh"
 
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRun = 32;  // tokens per thread of the forward pass
+constexpr int kThreads = 128;
 
 // Pairs of channels as they lie in memory.
 template <typename T, int P> struct rawp;  // P pairs
@@ -30,6 +29,18 @@ template <> struct rawp<__nv_bfloat16, 2> {
   __device__ __forceinline__ void get(f2 (&x)[2]) const {
     x[0] = bf16x2_to_f2(a.x);
     x[1] = bf16x2_to_f2(a.y);
+  }
+};
+template <> struct rawp<__nv_bfloat16, 4> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(f2 (&x)[4]) const {
+    x[0] = bf16x2_to_f2(a.x);
+    x[1] = bf16x2_to_f2(a.y);
+    x[2] = bf16x2_to_f2(a.z);
+    x[3] = bf16x2_to_f2(a.w);
   }
 };
 template <> struct rawp<float, 2> {
@@ -69,6 +80,26 @@ __device__ __forceinline__ void store_pairs(float *p, const f2 (&v)[2]) {
   const float2 q = unpack2(v[0]), r = unpack2(v[1]);
   *reinterpret_cast<float4 *>(p) = make_float4(q.x, q.y, r.x, r.y);
 }
+__device__ __forceinline__ void store_pairs(__nv_bfloat16 *p, const f2 (&v)[4]) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = unpack2(v[i]);
+    x[2 * i] = q.x;
+    x[2 * i + 1] = q.y;
+  }
+  store8(p, x);
+}
+// Pairs of channels per thread of the forward pass: 16 bytes.
+template <typename T> constexpr int kPairs = 8 / sizeof(T);
+template <int P>
+__device__ __forceinline__ void load_bias(const float *bias, int e, f2 (&out)[P]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const float2 q = bias ? *reinterpret_cast<const float2 *>(bias + e + 2 * p) : make_float2(0.f, 0.f);
+    out[p] = pack2(q.x, q.y);
+  }
+}
 __device__ __forceinline__ f2 silu2(f2 v) {
   const float2 q = unpack2(v);
   return pack2(q.x * sigmoid_f32(q.x), q.y * sigmoid_f32(q.y));
@@ -88,11 +119,18 @@ __device__ __forceinline__ rawp<T, P> early_row(const T *state, int t, int E) {
 template <int W, int P>
 __device__ __forceinline__ void load_taps(const float *w, int e, f2 (&out)[W][P]) {
   float q[2 * P * W];
+  if constexpr (P >= 2) {  // 4 W floats per two pairs: 16-byte aligned
 #pragma unroll
-  for (int i = 0; i < P * W; ++i) {  // 2 W floats per pair: 8-byte aligned
-    const float2 v = *reinterpret_cast<const float2 *>(w + (int64_t)e * W + 2 * i);
-    q[2 * i] = v.x;
-    q[2 * i + 1] = v.y;
+    for (int i = 0; i < P * W / 2; ++i) {
+      const float4 v = *reinterpret_cast<const float4 *>(w + (int64_t)e * W + 4 * i);
+      q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float2 v = *reinterpret_cast<const float2 *>(w + (int64_t)e * W + 2 * i);
+      q[2 * i] = v.x; q[2 * i + 1] = v.y;
+    }
   }
 #pragma unroll
   for (int k = 0; k < W; ++k)
@@ -101,8 +139,10 @@ __device__ __forceinline__ void load_taps(const float *w, int e, f2 (&out)[W][P]
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ ConvArgs a, int runs) {
-  const unsigned cols = a.E / 4;
+__global__ void __launch_bounds__(kThreads)
+    conv_kernel(const __grid_constant__ ConvArgs a, int run_len, int runs) {
+  constexpr int P = kPairs<T>;
+  const unsigned cols = a.E / (2 * P);
   const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int64_t total = (int64_t)a.B * runs * cols;
   if (idx >= total) return;
@@ -110,17 +150,17 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
   int64_t b;
   if (total < ((int64_t)1 << 32)) {  // 32-bit divisions
     const unsigned i = static_cast<unsigned>(idx), br = i / cols;
-    e = static_cast<int>(i - br * cols) * 4;
+    e = static_cast<int>(i - br * cols) * 2 * P;
     b = br / static_cast<unsigned>(runs);
     run = static_cast<int>(br - static_cast<unsigned>(b) * runs);
   } else {
     const int64_t br = idx / cols;
-    e = static_cast<int>(idx - br * cols) * 4;
+    e = static_cast<int>(idx - br * cols) * 2 * P;
     b = br / runs;
     run = static_cast<int>(br - b * runs);
   }
   const int len = a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
-  const int t0 = run * kRun, t1 = min(len, t0 + kRun);
+  const int t0 = run * run_len, t1 = min(len, t0 + run_len);
   const T *x = static_cast<const T *>(a.x) + b * a.L * a.ldx + e;
   const T *st = a.state ? static_cast<const T *>(a.state) + b * (W - 1) * a.E + e : nullptr;
   T *y = static_cast<T *>(a.y) + b * a.L * a.E + e;
@@ -131,39 +171,34 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
       const int t = len - (W - 1) + k;
-      rawp<T, 2> r;
+      rawp<T, P> r;
       if (t >= 0) r.load(x + t * a.ldx);
-      else r = early_row<T, W, 2>(st, t, a.E);
+      else r = early_row<T, W, P>(st, t, a.E);
       r.store(so + (int64_t)k * a.E);
     }
   }
   if (t0 >= t1) return;
 
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 4;
   const T *xp = x + t0 * a.ldx;
   T *yp = y + (int64_t)t0 * a.E;
-  rawp<T, 2> nxt[kAhead];
+  rawp<T, P> nxt[kAhead];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j)
     if (t0 + j < t1) nxt[j].load(xp + j * a.ldx);
-  f2 w[W][2], bias[2], win[W][2];  // win[k] = row t - W + 1 + k
-  load_taps<W, 2>(a.w, e, w);
-  bias[0] = bias[1] = dup2(0.f);
-  if (a.bias) {
-    const float4 q = *reinterpret_cast<const float4 *>(a.bias + e);
-    bias[0] = pack2(q.x, q.y);
-    bias[1] = pack2(q.z, q.w);
-  }
+  f2 w[W][P], bias[P], win[W][P];  // win[k] = row t - W + 1 + k
+  load_taps<W, P>(a.w, e, w);
+  load_bias<P>(a.bias, e, bias);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
     const int t = t0 - (W - 1) + k;
-    rawp<T, 2> r;
+    rawp<T, P> r;
     if (t >= 0) r.load(x + t * a.ldx);
-    else r = early_row<T, W, 2>(st, t, a.E);
+    else r = early_row<T, W, P>(st, t, a.E);
     r.get(win[k + 1]);
   }
   for (int tb = t0; tb < t1; tb += kAhead) {
-    rawp<T, 2> cur[kAhead];
+    rawp<T, P> cur[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       cur[j] = nxt[j];
@@ -175,11 +210,11 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) win[k][p] = win[k + 1][p];
+          for (int p = 0; p < P; ++p) win[k][p] = win[k + 1][p];
         cur[j].get(win[W - 1]);
-        f2 o[2];
+        f2 o[P];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < P; ++p) {
           o[p] = bias[p];
 #pragma unroll
           for (int k = 0; k < W; ++k) o[p] = fma2(w[k][p], win[k][p], o[p]);
@@ -200,12 +235,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
   if (e >= a.E) return;
   f2 w[W][2], bias[2];
   load_taps<W, 2>(a.w, e, w);
-  bias[0] = bias[1] = dup2(0.f);
-  if (a.bias) {
-    const float4 q = *reinterpret_cast<const float4 *>(a.bias + e);
-    bias[0] = pack2(q.x, q.y);
-    bias[1] = pack2(q.z, q.w);
-  }
+  load_bias<2>(a.bias, e, bias);
   for (int64_t b = blockIdx.y; b < a.B; b += gridDim.y) {
     T *st = static_cast<T *>(a.state_out) + b * (W - 1) * a.E + e;
     rawp<T, 2> r[W];
@@ -235,15 +265,15 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 // token t it knows dpre_(t-W+1..t), which is all that dx_(t-W+1) needs.  A run
 // of dx rows [s0, s1) reads W - 1 tokens of dpre beyond s1, recomputed by the
 // next run too; the sums count a token only in the run that owns it.  A CTA
-// is 32 pairs of channels x 8 runs at a time; its sums meet in shared memory
+// is 32 pairs of channels x 4 runs at a time; its sums meet in shared memory
 // and leave as one record, and a second kernel adds the records in their
 // order, so the result does not depend on scheduling.
-constexpr int kBwdCols = 32, kBwdRows = 8, kBwdRun = 32;
+constexpr int kBwdCols = 32, kBwdRows = 4;
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kBwdCols * kBwdRows)
     conv_bwd_kernel(const __grid_constant__ ConvArgs a, const __grid_constant__ ConvGrads g,
-                    float *__restrict__ rec, int runs) {
+                    float *__restrict__ rec, int run_len, int runs) {
   const int tx = threadIdx.x % kBwdCols, ty = threadIdx.x / kBwdCols;
   const int e = (blockIdx.x * kBwdCols + tx) * 2;
   const bool in = e < a.E;
@@ -259,14 +289,14 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
        r += (int64_t)gridDim.y * kBwdRows) {
     const int64_t b = r / runs;
     const int run = static_cast<int>(r - b * runs);
-    const int s0 = run * kBwdRun, s1 = min(a.L, s0 + kBwdRun);
+    const int s0 = run * run_len, s1 = min(a.L, s0 + run_len);
     const T *x = static_cast<const T *>(a.x) + b * a.L * a.ldx + e;
     const T *dy = static_cast<const T *>(g.dy) + b * a.L * a.E + e;
     T *dx = static_cast<T *>(g.dx) + b * a.L * a.E + e;
     const T *st = a.state ? static_cast<const T *>(a.state) + b * (W - 1) * a.E + e : nullptr;
     const int last = s1 + W - 1;        // tokens walked: [s0, last)
     const int here = min(last, a.L);    // those that exist
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     rawp<T, 1> xn[kAhead], gn[kAhead];
     auto fetch = [&](int j, int t) {
       xn[j].zero();
@@ -363,19 +393,38 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
   }
 }
 
-int conv_bwd_blocks(int B, int L, int E) {
-  const int64_t rows = ((int64_t)B * ((L + kBwdRun - 1) / kBwdRun) + kBwdRows - 1) / kBwdRows;
-  const int colb = (E / 2 + kBwdCols - 1) / kBwdCols;
-  int64_t y = (152 * 4 + colb - 1) / colb;  // about four CTAs per SM
-  if (y > rows) y = rows;
-  return y < 1 ? 1 : static_cast<int>(y);
+// Backward pass: a run per warp row such that all the CTAs are resident at
+// once (about four per SM; a CTA has four rows), of at least 29 tokens (the
+// W - 1 walked twice are then a tenth at most).
+struct BwdPlan {
+  int run_len, runs, ny;
+};
+BwdPlan conv_bwd_plan(int B, int L, int E) {
+  const int nx = (E / 2 + kBwdCols - 1) / kBwdCols;
+  int rows = 152 * 4 / nx * kBwdRows;  // rows of runs that fit at once
+  if (rows < kBwdRows) rows = kBwdRows;
+  const int per = rows / B > 0 ? rows / B : 1;  // runs per sequence
+  BwdPlan p;
+  p.run_len = (L + per - 1) / per;
+  if (p.run_len < 29) p.run_len = 29;
+  p.runs = (L + p.run_len - 1) / p.run_len;
+  const int64_t need = ((int64_t)B * p.runs + kBwdRows - 1) / kBwdRows;
+  p.ny = need < rows ? static_cast<int>(need) : rows;
+  return p;
 }
 
 template <typename T, int W>
 cudaError_t conv_fwd_typed(const ConvArgs &a, cudaStream_t s) {
-  const int runs = a.L > 0 ? (a.L + kRun - 1) / kRun : 1;
-  const int64_t n = (int64_t)a.B * runs * (a.E / 4);
-  conv_kernel<T, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, runs);
+  // runs of 64 tokens (the taps and the W - 1 early rows cost a thread about
+  // five tokens' work), shorter ones, whole groups of 4, where that leaves
+  // fewer than 256 threads per SM
+  const int cols = a.E / (2 * kPairs<T>);
+  int64_t len = (int64_t)a.B * a.L * cols / (152 * 256) / 4 * 4;
+  len = len < 8 ? 8 : len > 64 ? 64 : len;
+  const int run_len = static_cast<int>(len);
+  const int runs = a.L > 0 ? (a.L + run_len - 1) / run_len : 1;
+  const int64_t n = (int64_t)a.B * runs * cols;
+  conv_kernel<T, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, run_len, runs);
   return cudaGetLastError();
 }
 template <typename T, int W>
@@ -389,14 +438,13 @@ cudaError_t conv_step_typed(const ConvArgs &a, cudaStream_t s) {
 }
 template <typename T, int W>
 cudaError_t conv_bwd_typed(const ConvArgs &a, const ConvGrads &g, void *ws, cudaStream_t s) {
-  const int runs = (a.L + kBwdRun - 1) / kBwdRun;
-  const int ny = conv_bwd_blocks(a.B, a.L, a.E);
+  const BwdPlan p = conv_bwd_plan(a.B, a.L, a.E);
   const int nx = (a.E / 2 + kBwdCols - 1) / kBwdCols;
   float *rec = static_cast<float *>(ws);
-  conv_bwd_kernel<T, W><<<dim3(nx, ny), kBwdCols * kBwdRows, 0, s>>>(a, g, rec, runs);
+  conv_bwd_kernel<T, W><<<dim3(nx, p.ny), kBwdCols * kBwdRows, 0, s>>>(a, g, rec, p.run_len, p.runs);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_column_sum(rec, ny, (int64_t)(W + 1) * a.E, g.dw, (int64_t)W * a.E, g.dbias, s);
+  return launch_column_sum(rec, p.ny, (int64_t)(W + 1) * a.E, g.dw, (int64_t)W * a.E, g.dbias, s);
 }
 
 template <typename T>
@@ -425,7 +473,7 @@ cudaError_t launch_conv_step(const ConvArgs &a, Dtype dt, cudaStream_t s) {
                     : conv_widths<__nv_bfloat16>(a, nullptr, true, nullptr, s);
 }
 size_t conv_backward_workspace_bytes(int B, int L, int E, int W) {
-  return sizeof(float) * (size_t)conv_bwd_blocks(B, L, E) * (W + 1) * E;
+  return sizeof(float) * (size_t)conv_bwd_plan(B, L, E).ny * (W + 1) * E;
 }
 cudaError_t launch_conv_backward(const ConvArgs &a, const ConvGrads &g, Dtype dt, void *ws,
                                  cudaStream_t s) {

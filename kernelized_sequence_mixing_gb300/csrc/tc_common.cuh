@@ -405,6 +405,12 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
 bool make_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t dim_x, uint64_t dim_y,
                        uint64_t dim_z, uint32_t box_x, uint32_t box_y, int swizzle_bytes);
 
+// Host: encode a rank-3 map over [batch][rows][width] elements of 2 bytes
+// (bf16) or 4 (fp32) with `ld` elements between rows (and rows * ld between
+// batches), box (box_x, box_y, 1), no swizzle, zero fill out of bounds.
+bool make_tmap_rows(CUtensorMap *map, const void *base, int elem_bytes, uint64_t width,
+                    uint64_t rows, uint64_t batch, uint64_t ld, uint32_t box_x, uint32_t box_y);
+
 // Host: device address of the wait-timeout counter on the current device
 // (nullptr if it cannot be obtained).
 unsigned int *wait_timeout_counter();

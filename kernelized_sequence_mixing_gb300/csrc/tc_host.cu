@@ -50,6 +50,21 @@ bool make_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t dim_x, uint6
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_rows(CUtensorMap *map, const void *base, int elem_bytes, uint64_t width,
+                    uint64_t rows, uint64_t batch, uint64_t ld, uint32_t box_x, uint32_t box_y) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {width, rows, batch};
+  const cuuint64_t strides[2] = {ld * elem_bytes, rows * ld * elem_bytes};
+  const cuuint32_t box[3] = {box_x, box_y, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType ty =
+      elem_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(map, ty, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 unsigned int *wait_timeout_counter() {
   constexpr int kMaxDev = 64;
   static unsigned int *addr[kMaxDev] = {};
