@@ -15,10 +15,11 @@
 // exponentials (4 cycles each), 32 packed operations (2 cycles each) and what
 // feeds them.  Hence:
 //   - a thread owns 4 channels x 4 states in registers: per token it reads one
-//     16-byte vector of dt, of u = dt x, and two of B and of C from shared
-//     memory (few distinct addresses per warp: one wavefront each) for 16
-//     state updates, done as packed pairs of channels; the next token's
-//     operands are read before this token's are used;
+//     16-byte vector of dt, of u = dt x, and four 8-byte pairs of B and of C
+//     from shared memory for 16 state updates, done as packed pairs of
+//     channels; the next token's operands are read before this token's are
+//     used (a 16-byte read whose addresses repeat every four lanes takes four
+//     wavefronts, an 8-byte one takes one: so B and C lie state-lane-minor);
 //   - the sum over states crosses N/4 lanes: each lane stores its part of y
 //     (beyond four lanes after an exchange) and the threads that write y add
 //     the parts, a third of the instructions of a shuffle tree;
@@ -80,7 +81,8 @@ struct Smem {
   Stage<T, N, OUT> stage[2];
   alignas(16) float dt[S::TILE];
   float u[(OUT ? S::SLOTS : 1) * S::SLOT];  // dt x; y's first parts take its place, then the others
-  float2 B[S::TT * N], C[OUT ? S::TT * N : 1];  // each value twice, for the packed pairs
+  // each value twice, for the packed pairs: state 4 l + n at n LN + l
+  f2 B[S::TT * N], C[OUT ? S::TT * N : 1];
   uint64_t full[2];
   int abort;
 };
@@ -257,15 +259,12 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int s = t * Sh::CT + c0;
     const ulonglong2 dq = *reinterpret_cast<const ulonglong2 *>(&sm.dt[s]);
     const ulonglong2 uq = *reinterpret_cast<const ulonglong2 *>(&sm.u[s]);
-    const ulonglong2 b01 = *reinterpret_cast<const ulonglong2 *>(&sm.B[t * N + n0]);
-    const ulonglong2 b23 = *reinterpret_cast<const ulonglong2 *>(&sm.B[t * N + n0 + 2]);
     o.d[0] = {dq.x}; o.d[1] = {dq.y};
     o.u[0] = {uq.x}; o.u[1] = {uq.y};
-    o.b[0] = {b01.x}; o.b[1] = {b01.y}; o.b[2] = {b23.x}; o.b[3] = {b23.y};
-    if constexpr (OUT) {
-      const ulonglong2 c01 = *reinterpret_cast<const ulonglong2 *>(&sm.C[t * N + n0]);
-      const ulonglong2 c23 = *reinterpret_cast<const ulonglong2 *>(&sm.C[t * N + n0 + 2]);
-      o.c[0] = {c01.x}; o.c[1] = {c01.y}; o.c[2] = {c23.x}; o.c[3] = {c23.y};
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      o.b[n] = sm.B[t * N + n * Sh::LN + sl];
+      if constexpr (OUT) o.c[n] = sm.C[t * N + n * Sh::LN + sl];
     }
     return o;
   };
@@ -304,9 +303,11 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (which < (OUT ? 2 : 1)) {
         float4 w = load4((which ? g.C : g.B) + q);
         if (q / N >= rows) w = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 *d = reinterpret_cast<float4 *>((which ? sm.C : sm.B) + q);
-        d[0] = make_float4(w.x, w.x, w.y, w.y);
-        d[1] = make_float4(w.z, w.z, w.w, w.w);
+        f2 *d = (which ? sm.C : sm.B) + q / N * N + q % N / 4;
+        d[0] = dup2(w.x);
+        d[Sh::LN] = dup2(w.y);
+        d[2 * Sh::LN] = dup2(w.z);
+        d[3 * Sh::LN] = dup2(w.w);
       }
     }
     __syncthreads();
