@@ -214,6 +214,18 @@ int selective_part_len(int L, int S);
 size_t selective_workspace_bytes(int B, int E, int N, int S);
 cudaError_t launch_selective(const ScanArgs &a, Dtype dt, void *ws, int S, cudaStream_t s);
 cudaError_t launch_selective_step(const ScanArgs &a, Dtype dt, cudaStream_t s);
+// Records of the scan's parts (S of them; the forward pass keeps S - 1), fp32:
+// end states from zero h [B][S][E][N] and sums of dt [B][S][E]; for the
+// backward pass also each part's adjoint contribution to the state before it
+// g [B][S][E][N], and every kScanCheckpoint tokens (not at the part's start)
+// the state ck [B][S][K][E][N] and the sum of dt so far ckdt [B][S][K][E],
+// K = part_len / kScanCheckpoint - 1.
+constexpr int kScanCheckpoint = 8;
+struct ScanRecords {
+  float *h, *dt, *g, *ck, *ckdt;
+};
+cudaError_t launch_selective_local(const ScanArgs &a, const void *dy, const ScanRecords &rec, int S,
+                                   int part_len, Dtype dt, cudaStream_t s);
 // Backward of the scan from h0 (null: zeros): gradients of every input from
 // dy and, when dhN is set, the upstream gradient of the final state.  dD,
 // dz, ddt_bias, dh0 are null where their input is.

@@ -184,6 +184,25 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &x) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(x.x, x.y), f32_to_bf16x2(x.z, x.w));
 }
 
+// Four consecutive elements as two pairs.
+__device__ __forceinline__ void load4p(const float *p, f2 (&x)[2]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
+  x[0] = {a.x};
+  x[1] = {a.y};
+}
+__device__ __forceinline__ void load4p(const __nv_bfloat16 *p, f2 (&x)[2]) {
+  const uint2 a = *reinterpret_cast<const uint2 *>(p);
+  x[0] = bf16x2_to_f2(a.x);
+  x[1] = bf16x2_to_f2(a.y);
+}
+__device__ __forceinline__ void store4p(float *p, const f2 (&x)[2]) {
+  *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(x[0].v, x[1].v);
+}
+__device__ __forceinline__ void store4p(__nv_bfloat16 *p, const f2 (&x)[2]) {
+  const float2 a = unpack2(x[0]), b = unpack2(x[1]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(a.x, a.y), f32_to_bf16x2(b.x, b.y));
+}
+
 // Eight elements as they lie in memory, for loads that are issued well ahead
 // of their use (bf16: four registers, fp32: eight).
 template <typename T> struct raw8;

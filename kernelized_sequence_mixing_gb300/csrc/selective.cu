@@ -36,7 +36,7 @@
 // pass folds the records before its part in front of its own scan.
 #include "kernels.h"
 #include "mixer_common.cuh"
-#include "tc_common.cuh"
+#include "scan_maps.cuh"
 
 namespace linattn {
 namespace {
@@ -44,16 +44,23 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxParts = 32;
-constexpr int kTile = 2048;  // (token, channel) pairs of a tile, at most
+constexpr int kCheckpoint = kScanCheckpoint;
+constexpr int kLocalTile = 1024;
 constexpr int kSlots = 2;    // parts of y, at most
 
-template <typename T, int N>
+// The passes over the tokens: a part's end state; y; or, for the backward
+// pass, a part's end state with checkpoints and its adjoint contribution.
+enum { kStates = 0, kOut = 1, kLocal = 2 };
+
+template <int N, int MODE>
 struct Shape {
+  // (token, channel) pairs of a tile, at most
+  static constexpr int kTile = MODE == kLocal ? kLocalTile : 2048;
   static constexpr int LN = N / 4;         // lanes that share a channel's states
   static constexpr int LC = 32 / LN;       // channel quads per warp
   static constexpr int CPW = LC * 4;       // channels per warp
   static constexpr int CT = CPW * kWarps;  // channels per CTA
-  static constexpr int TT = kTile / CT < 32 ? kTile / CT : 32;  // tokens per tile
+  static constexpr int TT = kTile / CT < 8 ? 8 : kTile / CT < 32 ? kTile / CT : 32;  // tokens per tile
   static constexpr int TILE = TT * CT;     // (token, channel) pairs per tile
   static constexpr int QC = CT / 4;        // channel quads per token
   static constexpr int NQ = TILE / 4 / kThreads;  // quads staged per thread
@@ -64,32 +71,30 @@ struct Shape {
   static constexpr int NBQ = (2 * BQ + kThreads - 1) / kThreads;
 };
 
-// A tile as loaded (the state pass needs no C and z).
-template <typename T, int N, bool OUT>
+// A tile as loaded.
+template <typename T, int N, int MODE>
 struct Stage {
-  using S = Shape<T, N>;
+  using S = Shape<N, MODE>;
   alignas(128) T x[S::TILE];
   alignas(128) T dt[S::TILE];
   alignas(128) T B[S::TT * N];
-  alignas(128) T C[OUT ? S::TT * N : 1];
-  alignas(128) T z[OUT ? S::TILE : 1];
+  alignas(128) T C[MODE != kStates ? S::TT * N : 1];
+  alignas(128) T z[MODE != kStates ? S::TILE : 1];
+  alignas(128) T dy[MODE == kLocal ? S::TILE : 1];
 };
 
-template <typename T, int N, bool OUT>
+template <typename T, int N, int MODE>
 struct Smem {
-  using S = Shape<T, N>;
-  Stage<T, N, OUT> stage[2];
+  using S = Shape<N, MODE>;
+  Stage<T, N, MODE> stage[2];
   alignas(16) float dt[S::TILE];
-  float u[(OUT ? S::SLOTS : 1) * S::SLOT];  // dt x; y's first parts take its place, then the others
+  // dt x; in the output pass y's first parts take its place, then the others
+  float u[(MODE == kOut ? S::SLOTS : 1) * S::SLOT];
+  alignas(16) float g[MODE == kLocal ? S::TILE : 4];  // dy silu(z)
   // each value twice, for the packed pairs: state 4 l + n at n LN + l
-  f2 B[S::TT * N], C[OUT ? S::TT * N : 1];
+  f2 B[S::TT * N], C[MODE != kStates ? S::TT * N : 1];
   uint64_t full[2];
   int abort;
-};
-
-// TMA maps of x, dt, z, B, C.
-struct ScanMaps {
-  CUtensorMap x, dt, z, B, C;
 };
 
 // Stores a channel quad's y of one token from its LN state lanes as SLOTS
@@ -120,34 +125,16 @@ __device__ __forceinline__ void store_parts(float *y, int sl, f2 y01, f2 y23) {
   }
 }
 
-// Four consecutive elements as two pairs.
-__device__ __forceinline__ void load4p(const float *p, f2 (&x)[2]) {
-  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
-  x[0] = {a.x};
-  x[1] = {a.y};
-}
-__device__ __forceinline__ void load4p(const __nv_bfloat16 *p, f2 (&x)[2]) {
-  const uint2 a = *reinterpret_cast<const uint2 *>(p);
-  x[0] = bf16x2_to_f2(a.x);
-  x[1] = bf16x2_to_f2(a.y);
-}
-__device__ __forceinline__ void store4p(float *p, const f2 (&x)[2]) {
-  *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(x[0].v, x[1].v);
-}
-__device__ __forceinline__ void store4p(__nv_bfloat16 *p, const f2 (&x)[2]) {
-  const float2 a = unpack2(x[0]), b = unpack2(x[1]);
-  *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(a.x, a.y), f32_to_bf16x2(b.x, b.y));
-}
-
-// OUT: the output pass; otherwise the state pass of the parts but the last.
-template <typename T, int N, bool OUT>
+// Parts: the last has no record in the state pass; kLocal runs them all.
+template <typename T, int N, int MODE>
 __global__ void __launch_bounds__(kThreads, 4)
     scan_kernel(const __grid_constant__ ScanArgs a, const __grid_constant__ ScanMaps maps,
-                float *__restrict__ rec_h,
-                float *__restrict__ rec_dt, int S, int part_len, unsigned int *timeouts) {
-  using Sh = Shape<T, N>;
+                const __grid_constant__ ScanRecords rec, int S, int part_len,
+                unsigned int *timeouts) {
+  constexpr bool OUT = MODE == kOut, LOCAL = MODE == kLocal;
+  using Sh = Shape<N, MODE>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  Smem<T, N, OUT> &sm = *reinterpret_cast<Smem<T, N, OUT> *>(smem_raw);
+  Smem<T, N, MODE> &sm = *reinterpret_cast<Smem<T, N, MODE> *>(smem_raw);
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&sm.full[0], 1);
@@ -160,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int sl = lane & (Sh::LN - 1), lc = lane / Sh::LN;
   const int Eg = a.E / a.G;  // channels per group
   const int gtiles = (Eg + Sh::CT - 1) / Sh::CT, tiles = gtiles * a.G;
-  const int nparts = OUT ? S : S - 1;
+  const int nparts = MODE == kStates ? S - 1 : S;
   const int tile = blockIdx.x % tiles;
   const int part = (blockIdx.x / tiles) % nparts;
   const int b = blockIdx.x / tiles / nparts;
@@ -171,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int len = a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
   const int t0 = part * part_len, t1 = min(len, t0 + part_len);
 
-  const bool gated = OUT && a.z;
+  const bool gated = MODE != kStates && a.z;
   T *y = OUT ? static_cast<T *>(a.y) + (int64_t)b * a.L * a.E + e0 : nullptr;
 
   // this thread's channels and states
@@ -208,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const bool in = c0 + c < nch;
-        r[c] = in ? *reinterpret_cast<const float4 *>(rec_h + (rc + c) * N + n0)
+        r[c] = in ? *reinterpret_cast<const float4 *>(rec.h + (rc + c) * N + n0)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
-        sd[c] = in ? rec_dt[rc + c] : 0.f;
+        sd[c] = in ? rec.dt[rc + c] : 0.f;
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -224,6 +211,34 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
   }
   f2 dtsum[2] = {dup2(0.f), dup2(0.f)};
+  // the product of the part's decays so far, and its adjoint contribution
+  f2 P[2][4], adj[2][4];
+  if constexpr (LOCAL)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        P[c][n] = dup2(1.f);
+        adj[c][n] = dup2(0.f);
+      }
+  // v of this thread's channels and states to p, its first channel's place
+  auto store_states = [&](float *p, const f2 (&v)[2][4]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float2 q0 = unpack2(v[c][0]), q1 = unpack2(v[c][1]), q2 = unpack2(v[c][2]),
+                   q3 = unpack2(v[c][3]);
+      if (c0 + 2 * c < nch) {  // widths are multiples of 8
+        *reinterpret_cast<float4 *>(p + 2 * c * N) = make_float4(q0.x, q1.x, q2.x, q3.x);
+        *reinterpret_cast<float4 *>(p + (2 * c + 1) * N) = make_float4(q0.y, q1.y, q2.y, q3.y);
+      }
+    }
+  };
+  auto store_dtsum = [&](float *p) {
+    if (sl == 0 && c0 < nch) {
+      const float2 q = unpack2(dtsum[0]), r = unpack2(dtsum[1]);
+      *reinterpret_cast<float4 *>(p) = make_float4(q.x, q.y, r.x, r.y);
+    }
+  };
 
   // per-channel parameters of the staged quads (one column per thread:
   // kThreads is a multiple of QC)
@@ -239,20 +254,22 @@ __global__ void __launch_bounds__(kThreads, 4)
   // channels belong to lanes that store nothing.
   auto issue = [&](int tb, int st) {
     if (tid != 0) return;
-    Stage<T, N, OUT> &g = sm.stage[st];
+    Stage<T, N, MODE> &g = sm.stage[st];
     uint64_t *bar = &sm.full[st];
     constexpr uint32_t rows = Sh::TILE * sizeof(T), bc = Sh::TT * N * sizeof(T);
-    tc::mbar_arrive_expect_tx(bar, (gated ? 3 : 2) * rows + (OUT ? 2 : 1) * bc);
+    tc::mbar_arrive_expect_tx(
+        bar, (2 + (gated ? 1 : 0) + (LOCAL ? 1 : 0)) * rows + (MODE != kStates ? 2 : 1) * bc);
     tc::tma_load_3d(g.x, &maps.x, e0, tb, b, bar);
     tc::tma_load_3d(g.dt, &maps.dt, e0, tb, b, bar);
     tc::tma_load_3d(g.B, &maps.B, grp * N, tb, b, bar);
-    if constexpr (OUT) {
+    if constexpr (MODE != kStates) {
       tc::tma_load_3d(g.C, &maps.C, grp * N, tb, b, bar);
       if (gated) tc::tma_load_3d(g.z, &maps.z, e0, tb, b, bar);
     }
+    if constexpr (LOCAL) tc::tma_load_3d(g.dy, &maps.dy, e0, tb, b, bar);
   };
   struct Operands {
-    f2 d[2], u[2], b[4], c[4];
+    f2 d[2], u[2], g[2], b[4], c[4];
   };
   auto fetch = [&](int t) {
     Operands o;
@@ -261,10 +278,14 @@ __global__ void __launch_bounds__(kThreads, 4)
     const ulonglong2 uq = *reinterpret_cast<const ulonglong2 *>(&sm.u[s]);
     o.d[0] = {dq.x}; o.d[1] = {dq.y};
     o.u[0] = {uq.x}; o.u[1] = {uq.y};
+    if constexpr (LOCAL) {
+      const ulonglong2 gq = *reinterpret_cast<const ulonglong2 *>(&sm.g[s]);
+      o.g[0] = {gq.x}; o.g[1] = {gq.y};
+    }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       o.b[n] = sm.B[t * N + n * Sh::LN + sl];
-      if constexpr (OUT) o.c[n] = sm.C[t * N + n * Sh::LN + sl];
+      if constexpr (MODE != kStates) o.c[n] = sm.C[t * N + n * Sh::LN + sl];
     }
     return o;
   };
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   int turn = 0;
   for (int tb = t0; tb < t1; tb += Sh::TT, ++turn) {
     const int st = turn & 1, rows = min(Sh::TT, t1 - tb);
-    const Stage<T, N, OUT> &g = sm.stage[st];
+    const Stage<T, N, MODE> &g = sm.stage[st];
     // a wait that gives up ends the CTA; the next tile's copies are only
     // issued after this one, so none is in flight but the one that failed
     if (!tc::mbar_wait(&sm.full[st], (turn >> 1) & 1, &sm.abort, timeouts)) {
@@ -296,11 +317,25 @@ __global__ void __launch_bounds__(kThreads, 4)
       }
       store4p(&sm.dt[s], dv);
       store4p(&sm.u[s], xv);
+      if constexpr (LOCAL) {
+        f2 gv[2], zv[2];
+        load4p(&g.dy[s], gv);
+        if (gated) load4p(&g.z[s], zv);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (gated) {
+            const float2 q = unpack2(zv[k]);
+            gv[k] = mul2(gv[k], mul2(zv[k], pack2(sigmoid_f32(q.x), sigmoid_f32(q.y))));
+          }
+          if (r >= rows) gv[k] = dup2(0.f);
+        }
+        store4p(&sm.g[s], gv);
+      }
     }
 #pragma unroll
     for (int i = 0; i < Sh::NBQ; ++i) {
       const int v = tid + i * kThreads, which = v / Sh::BQ, q = v % Sh::BQ * 4;
-      if (which < (OUT ? 2 : 1)) {
+      if (which < (MODE != kStates ? 2 : 1)) {
         float4 w = load4((which ? g.C : g.B) + q);
         if (q / N >= rows) w = make_float4(0.f, 0.f, 0.f, 0.f);
         f2 *d = (which ? sm.C : sm.B) + q / N * N + q % N / 4;
@@ -315,15 +350,20 @@ __global__ void __launch_bounds__(kThreads, 4)
     // the other stage was last read before this barrier
     if (tb + Sh::TT < t1) issue(tb + Sh::TT, st ^ 1);
     Operands nxt = fetch(0);
-#pragma unroll 16
-    for (int t = 0; t < Sh::TT; ++t) {
+    auto step = [&](int t) {
       const Operands o = nxt;
       nxt = fetch(t + 1 < Sh::TT ? t + 1 : t);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          h[c][n] = fma2(ex2_2(mul2(o.d[c], A[c][n])), h[c][n], mul2(o.u[c], o.b[n]));
+        for (int n = 0; n < 4; ++n) {
+          const f2 e = ex2_2(mul2(o.d[c], A[c][n]));
+          h[c][n] = fma2(e, h[c][n], mul2(o.u[c], o.b[n]));
+          if constexpr (LOCAL) {
+            P[c][n] = mul2(P[c][n], e);
+            adj[c][n] = fma2(P[c][n], mul2(o.g[c], o.c[n]), adj[c][n]);
+          }
+        }
       if constexpr (OUT) {
         f2 y2[2];
 #pragma unroll
@@ -338,6 +378,22 @@ __global__ void __launch_bounds__(kThreads, 4)
         dtsum[0] = add2(dtsum[0], o.d[0]);
         dtsum[1] = add2(dtsum[1], o.d[1]);
       }
+    };
+    if constexpr (LOCAL) {
+      static_assert(Sh::TT % kCheckpoint == 0, "");
+      for (int t8 = 0; t8 < Sh::TT; t8 += kCheckpoint) {
+        const int k = (tb - t0 + t8) / kCheckpoint;
+        if (k > 0 && tb + t8 < t1) {
+          const int64_t rc = (((int64_t)b * S + part) * (part_len / kCheckpoint - 1) + k - 1) * a.E + e0 + c0;
+          store_states(rec.ck + rc * N + n0, h);
+          store_dtsum(rec.ckdt + rc);
+        }
+#pragma unroll
+        for (int j = 0; j < kCheckpoint; ++j) step(t8 + j);
+      }
+    } else {
+#pragma unroll 16
+      for (int t = 0; t < Sh::TT; ++t) step(t);
     }
     __syncthreads();
     if constexpr (OUT) {
@@ -373,66 +429,44 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 
   // the state after this part: the record, or the final state
-  float *hd = nullptr;
   if constexpr (OUT) {
-    if (part == S - 1 && a.hN) hd = a.hN + ((int64_t)b * a.E + e0 + c0) * N + n0;
+    if (part == S - 1 && a.hN) store_states(a.hN + ((int64_t)b * a.E + e0 + c0) * N + n0, h);
   } else {
-    const int64_t rc = ((int64_t)b * (S - 1) + part) * a.E + e0 + c0;
-    hd = rec_h + rc * N + n0;
-    if (sl == 0) {
-      const float2 p = unpack2(dtsum[0]), q = unpack2(dtsum[1]);
-      const float v[4] = {p.x, p.y, q.x, q.y};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c0 + c < nch) rec_dt[rc + c] = v[c];
-    }
+    const int64_t rc = ((int64_t)b * nparts + part) * a.E + e0 + c0;
+    store_states(rec.h + rc * N + n0, h);
+    store_dtsum(rec.dt + rc);
+    if constexpr (LOCAL) store_states(rec.g + rc * N + n0, adj);
   }
-  if (hd) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float2 p = unpack2(h[c][0]), q = unpack2(h[c][1]), r = unpack2(h[c][2]),
-                   s = unpack2(h[c][3]);
-      if (c0 + 2 * c < nch)
-        *reinterpret_cast<float4 *>(hd + 2 * c * N) = make_float4(p.x, q.x, r.x, s.x);
-      if (c0 + 2 * c + 1 < nch)
-        *reinterpret_cast<float4 *>(hd + (2 * c + 1) * N) = make_float4(p.y, q.y, r.y, s.y);
-    }
-  }
+}
+
+template <typename T, int N, int MODE>
+cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &rec, int S,
+                        int part_len, cudaStream_t s) {
+  using Sh = Shape<N, MODE>;
+  ScanMaps maps;
+  if (!make_scan_maps(&maps, a, dy, sizeof(T), Sh::CT, Sh::TT)) return cudaErrorInvalidValue;
+  constexpr int smem = sizeof(Smem<T, N, MODE>);
+  unsigned int *timeouts = wait_timeout_counter();
+  if (!timeouts) return cudaErrorUnknown;
+  cudaError_t e = allow_smem(scan_kernel<T, N, MODE>, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
+  const int64_t ctas = a.B * (MODE == kStates ? S - 1 : S) * tiles;
+  scan_kernel<T, N, MODE><<<(unsigned)ctas, kThreads, smem, s>>>(a, maps, rec, S, part_len, timeouts);
+  return cudaGetLastError();
 }
 
 template <typename T, int N>
 cudaError_t scan_typed(const ScanArgs &a, void *ws, int S, cudaStream_t s) {
-  using Sh = Shape<T, N>;
-  constexpr int es = sizeof(T);
-  ScanMaps maps = {};
-  auto map = [&](CUtensorMap *m, const void *p, int64_t width, int64_t ld, int box) {
-    return make_tmap_rows(m, p, es, width, a.L, a.B, ld, box, Sh::TT);
-  };
-  const int64_t GN = (int64_t)a.G * N;
-  if (a.L > 0 && (!map(&maps.x, a.x, a.E, a.ldx, Sh::CT) || !map(&maps.dt, a.dt, a.E, a.lddt, Sh::CT) ||
-                  !map(&maps.B, a.Bm, GN, a.ldb, N) || !map(&maps.C, a.Cm, GN, a.ldc, N) ||
-                  (a.z && !map(&maps.z, a.z, a.E, a.ldz, Sh::CT))))
-    return cudaErrorInvalidValue;
-  const int tiles = a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
   const int part_len = selective_part_len(a.L, S);
-  float *rec_h = static_cast<float *>(ws);
-  float *rec_dt = rec_h + (size_t)a.B * (S - 1) * a.E * N;
-  unsigned int *timeouts = wait_timeout_counter();
-  if (!timeouts) return cudaErrorUnknown;
+  ScanRecords rec = {};
+  rec.h = static_cast<float *>(ws);
+  rec.dt = rec.h + (size_t)a.B * (S - 1) * a.E * N;
   if (S > 1) {
-    constexpr int smem = sizeof(Smem<T, N, false>);
-    cudaError_t e = allow_smem(scan_kernel<T, N, false>, smem);
+    const cudaError_t e = launch_scan<T, N, kStates>(a, nullptr, rec, S, part_len, s);
     if (e != cudaSuccess) return e;
-    scan_kernel<T, N, false><<<(unsigned)((int64_t)a.B * (S - 1) * tiles), kThreads, smem, s>>>(
-        a, maps, rec_h, rec_dt, S, part_len, timeouts);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  constexpr int smem = sizeof(Smem<T, N, true>);
-  cudaError_t e = allow_smem(scan_kernel<T, N, true>, smem);
-  if (e != cudaSuccess) return e;
-  scan_kernel<T, N, true><<<(unsigned)((int64_t)a.B * S * tiles), kThreads, smem, s>>>(
-      a, maps, rec_h, rec_dt, S, part_len, timeouts);
-  return cudaGetLastError();
+  return launch_scan<T, N, kOut>(a, nullptr, rec, S, part_len, s);
 }
 
 template <typename T>
@@ -442,6 +476,18 @@ cudaError_t scan_states(const ScanArgs &a, void *ws, int S, cudaStream_t s) {
     case 16: return scan_typed<T, 16>(a, ws, S, s);
     case 32: return scan_typed<T, 32>(a, ws, S, s);
     case 64: return scan_typed<T, 64>(a, ws, S, s);
+  }
+  return cudaErrorNotSupported;
+}
+
+template <typename T>
+cudaError_t local_states(const ScanArgs &a, const void *dy, const ScanRecords &rec, int S,
+                         int part_len, cudaStream_t s) {
+  switch (a.N) {
+    case 8: return launch_scan<T, 8, kLocal>(a, dy, rec, S, part_len, s);
+    case 16: return launch_scan<T, 16, kLocal>(a, dy, rec, S, part_len, s);
+    case 32: return launch_scan<T, 32, kLocal>(a, dy, rec, S, part_len, s);
+    case 64: return launch_scan<T, 64, kLocal>(a, dy, rec, S, part_len, s);
   }
   return cudaErrorNotSupported;
 }
@@ -551,6 +597,12 @@ size_t selective_workspace_bytes(int B, int E, int N, int S) {
 
 cudaError_t launch_selective(const ScanArgs &a, Dtype dt, void *ws, int S, cudaStream_t s) {
   return dt == kF32 ? scan_states<float>(a, ws, S, s) : scan_states<__nv_bfloat16>(a, ws, S, s);
+}
+
+cudaError_t launch_selective_local(const ScanArgs &a, const void *dy, const ScanRecords &rec, int S,
+                                   int part_len, Dtype dt, cudaStream_t s) {
+  return dt == kF32 ? local_states<float>(a, dy, rec, S, part_len, s)
+                    : local_states<__nv_bfloat16>(a, dy, rec, S, part_len, s);
 }
 
 cudaError_t launch_selective_step(const ScanArgs &a, Dtype dt, cudaStream_t s) {

@@ -12,195 +12,46 @@
 // Dividing h_t by a_t to walk the states back loses everything once a_t is
 // small, so states are recomputed from checkpoints instead.
 //
-// Passes (the first two only when there is more than one part of kPart
-// tokens):
-//   local   every part's end state from zero, its adjoint contribution to the
-//           state before it, sum_t (a_1..a_t) C_t gy_t, and its sum of dt;
+// Passes:
+//   local   (the forward kernel's third mode) every part's end state from zero
+//           with a checkpoint of it every 8 tokens, its adjoint contribution
+//           to the state before it, sum_t (a_1..a_t) C_t gy_t, and its sums
+//           of dt;
 //   carry   the parts in order: the state before and the adjoint behind each;
-//   main    a part in tiles of TT tokens: forward over all tiles but the last
-//           for the state in front of each, then the tiles from the end; in a
-//           tile forward again for a checkpoint every 4 tokens, then 4 tokens
-//           at a time from the end: their states again into registers, and
-//           the adjoint recurrence over them (decays are computed again:
-//           holding them too costs the registers of a fourth CTA);
+//   main    a part in tiles, and 8 tokens at a time from the end: the state in
+//           front of them is the checkpoint plus exp(A sum dt) times the state
+//           before the part; from it the 8 states into registers, and the
+//           adjoint recurrence over them;
 //   sums    dB and dC over the channel tiles, dA, dD and d(dt_bias) over the
 //           parts, in a fixed order.
-//
-// What bounds it: the instructions issued, 4 exponentials and about 15 packed
-// fp32 operations per two states and token, plus the sums.  A thread of the
-// main pass owns 2 channels x 4 states (packed pairs of channels): sums over
-// states cross N/4 lanes, sums over channels the other lanes by a transposing
-// exchange (7 shuffles for 16 states), then the CTA's warps in shared memory.
-// The two levels of checkpoints keep a CTA within 52 KB and 128 registers a
-// thread at 16 states, so that four share an SM; one level (8 tokens of
-// states and decays in registers, 104 KB) ran at two CTAs per SM and 366 us
-// for B2 L4096 E2048 N16 in bf16.
+// The checkpoints cost N / 2 bytes of memory traffic per (channel, token) each
+// way; computing them again in the main pass, in one level or two, cost 12% to
+// 25% of its instructions, and it is the instructions and the shared-memory
+// pipe that bound it: 2 exponentials (3 with the local pass) and about 13
+// packed fp32 operations per two states and token, plus the sums.  A thread of
+// the main pass owns 2 channels x 4 states (packed pairs of channels): sums
+// over states cross N/4 lanes two tokens at a time, sums over channels the
+// other lanes, both by transposing exchanges, then the CTA's warps in shared
+// memory.
 #include "kernels.h"
 #include "mixer_common.cuh"
+#include "scan_maps.cuh"
 
 namespace linattn {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSub = 4;  // tokens whose states a thread holds
+constexpr int kSub = kScanCheckpoint;  // tokens whose states a thread holds
 
 template <int N> constexpr int kPart = N == 8 ? 32 : 64;  // tokens per part
 
 struct BwdRecords {
-  float *h;     // [B][S][E][N]: end states, then the states before a part, then dA
-  float *g;     // [B][S][E][N]: adjoint contributions, then the adjoints behind a part
-  float *dt;    // [B][S][E]
-  float *cols;  // [B][S][2][E]: dD, d(dt_bias)
-  float *bc;    // [B][tiles][L][2N]: dB | dC of a channel tile
+  ScanRecords s;  // s.h: end states, then the states before a part; s.g: likewise behind it
+  float *dA;      // [B][S][E][N], in place of s.h
+  float *cols;    // [B][S][2][E]: dD, d(dt_bias)
+  float *bc;      // [B][tiles][L][2N]: dB | dC of a channel tile
 };
-
-// ------------------------------------------------------------------- local
-
-template <typename T, int N>
-struct LocalShape {
-  static constexpr int LN = N / 4, LC = 32 / LN, CPW = LC * 4, CT = CPW * kWarps;
-  static constexpr int TT = 2048 / CT, VC = CT / 8, NV = 2;
-  static constexpr int smem = sizeof(float) * (3 * 2048 + 4 * TT * N);
-};
-
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, 4)
-    scan_bwd_local_kernel(const __grid_constant__ ScanArgs a, const T *__restrict__ dout,
-                          const __grid_constant__ BwdRecords rec, int S) {
-  using Sh = LocalShape<T, N>;
-  extern __shared__ __align__(16) float smem_local[];
-  float *sdt = smem_local, *su = sdt + 2048, *sg = su + 2048;
-  f2 *sB = reinterpret_cast<f2 *>(sg + 2048), *sC = sB + Sh::TT * N;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int sl = lane & (Sh::LN - 1), lc = lane / Sh::LN;
-  const int Eg = a.E / a.G, gtiles = (Eg + Sh::CT - 1) / Sh::CT, tiles = gtiles * a.G;
-  const int tile = blockIdx.x % tiles, part = (blockIdx.x / tiles) % S, b = blockIdx.x / tiles / S;
-  const int grp = tile / gtiles, cg = (tile % gtiles) * Sh::CT, e0 = grp * Eg + cg;
-  const int nch = min(Sh::CT, Eg - cg);
-  const int t0 = part * kPart<N>, t1 = min(a.L, t0 + kPart<N>);
-  const T *x = static_cast<const T *>(a.x) + (int64_t)b * a.L * a.ldx + e0;
-  const T *dt = static_cast<const T *>(a.dt) + (int64_t)b * a.L * a.lddt + e0;
-  const T *z = a.z ? static_cast<const T *>(a.z) + (int64_t)b * a.L * a.ldz + e0 : nullptr;
-  const T *dy = dout + (int64_t)b * a.L * a.E + e0;
-  const T *Bm = static_cast<const T *>(a.Bm) + (int64_t)b * a.L * a.ldb + grp * N;
-  const T *Cm = static_cast<const T *>(a.Cm) + (int64_t)b * a.L * a.ldc + grp * N;
-  const int c0 = warp * Sh::CPW + lc * 4, n0 = sl * 4;
-  f2 A[2][4], h[2][4], P[2][4], r[2][4];
-  {
-    float av[4][4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 q = c0 + c < nch
-                           ? *reinterpret_cast<const float4 *>(a.A + (int64_t)(e0 + c0 + c) * N + n0)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-      av[c][0] = q.x * kLog2e; av[c][1] = q.y * kLog2e;
-      av[c][2] = q.z * kLog2e; av[c][3] = q.w * kLog2e;
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        A[c][n] = pack2(av[2 * c][n], av[2 * c + 1][n]);
-        h[c][n] = r[c][n] = dup2(0.f);
-        P[c][n] = dup2(1.f);
-      }
-  }
-  float dtsum[4] = {0.f, 0.f, 0.f, 0.f};
-  const int vcol = (tid % Sh::VC) * 8, vrow = tid / Sh::VC;
-  const bool vin = vcol < nch;
-  float bias[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = 0.f;
-  if (vin && a.dt_bias) load8(a.dt_bias + e0 + vcol, bias);
-
-  for (int tb = t0; tb < t1; tb += Sh::TT) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < Sh::NV; ++i) {
-      const int row = vrow + i * (kThreads / Sh::VC), s = row * Sh::CT + vcol;
-      const int64_t t = tb + row;
-      float dv[8], uv[8], gv[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dv[k] = uv[k] = gv[k] = 0.f;
-      if (vin && t < t1) {
-        load8(x + t * a.ldx + vcol, uv);
-        load8(dt + t * a.lddt + vcol, dv);
-        load8(dy + t * a.E + vcol, gv);
-        if (z) {
-          float zv[8];
-          load8(z + t * a.ldz + vcol, zv);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) gv[k] *= zv[k] * sigmoid_f32(zv[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float q = dv[k] + bias[k];
-          dv[k] = a.softplus ? softplus_f32(q) : q;
-          uv[k] *= dv[k];
-        }
-      }
-      store8(&sdt[s], dv);
-      store8(&su[s], uv);
-      store8(&sg[s], gv);
-    }
-    for (int v = tid; v < Sh::TT * N / 8; v += kThreads) {
-      const int row = v / (N / 8), col = (v % (N / 8)) * 8;
-      const int64_t t = tb + row;
-      float q[8], p[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = p[k] = 0.f;
-      if (t < t1) {
-        load8(Bm + t * a.ldb + col, q);
-        load8(Cm + t * a.ldc + col, p);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sB[row * N + k % 4 * Sh::LN + col / 4 + k / 4] = dup2(q[k]);
-        sC[row * N + k % 4 * Sh::LN + col / 4 + k / 4] = dup2(p[k]);
-      }
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int t = 0; t < Sh::TT; ++t) {
-      const int s = t * Sh::CT + c0;
-      const ulonglong2 dq = *reinterpret_cast<const ulonglong2 *>(&sdt[s]);
-      const ulonglong2 uq = *reinterpret_cast<const ulonglong2 *>(&su[s]);
-      const ulonglong2 gq = *reinterpret_cast<const ulonglong2 *>(&sg[s]);
-      const f2 d2[2] = {{dq.x}, {dq.y}}, u2[2] = {{uq.x}, {uq.y}}, g2[2] = {{gq.x}, {gq.y}};
-      f2 bn[4], cn[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        bn[n] = sB[t * N + n * Sh::LN + sl];
-        cn[n] = sC[t * N + n * Sh::LN + sl];
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const f2 e = ex2_2(mul2(d2[c], A[c][n]));
-          h[c][n] = fma2(e, h[c][n], mul2(u2[c], bn[n]));
-          P[c][n] = mul2(P[c][n], e);
-          r[c][n] = fma2(P[c][n], mul2(g2[c], cn[n]), r[c][n]);
-        }
-      const float2 p = unpack2(d2[0]), q = unpack2(d2[1]);
-      dtsum[0] += p.x; dtsum[1] += p.y; dtsum[2] += q.x; dtsum[3] += q.y;
-    }
-  }
-  const int64_t rc = ((int64_t)b * S + part) * a.E + e0 + c0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (c0 + c < nch) {
-      auto half = [&](const f2 &v) { const float2 q = unpack2(v); return c & 1 ? q.y : q.x; };
-      const int cp = c / 2;
-      *reinterpret_cast<float4 *>(rec.h + (rc + c) * N + n0) =
-          make_float4(half(h[cp][0]), half(h[cp][1]), half(h[cp][2]), half(h[cp][3]));
-      *reinterpret_cast<float4 *>(rec.g + (rc + c) * N + n0) =
-          make_float4(half(r[cp][0]), half(r[cp][1]), half(r[cp][2]), half(r[cp][3]));
-      if (sl == 0) rec.dt[rc + c] = dtsum[c];
-    }
-  }
-}
 
 // ------------------------------------------------------------------- carry
 
@@ -217,8 +68,8 @@ __global__ void __launch_bounds__(256)
   const int e = static_cast<int>(en / a.N);
   const float A = a.A[en] * kLog2e;
   const bool back = blockIdx.y == 1;
-  float *r = (back ? rec.g : rec.h) + b * S * EN + en;
-  const float *sd = rec.dt + b * S * a.E + e;
+  float *r = (back ? rec.s.g : rec.s.h) + b * S * EN + en;
+  const float *sd = rec.s.dt + b * S * a.E + e;
   float acc = back ? (dhN ? dhN[i] : 0.f) : (a.h0 ? a.h0[i] : 0.f);
   constexpr int kAhead = 8;
   for (int q0 = 0; q0 < S; q0 += kAhead) {
@@ -247,32 +98,48 @@ template <typename T, int N>
 struct MainShape {
   static constexpr int LN = N / 4, LC = 32 / LN, CPW = LC * 2, CT = CPW * kWarps;
   static constexpr int TT = 1024 / CT < 32 ? 1024 / CT : 32;  // tokens per tile
-  static constexpr int NT = kPart<N> / TT;                    // tiles per part
-  static constexpr int NSUB = TT / kSub;
-  static constexpr int VC = CT / 8;
-  static constexpr int VECS = TT * VC;  // 8-channel vectors of a tile: at most one per thread
+  static constexpr int QC = CT / 4;                           // channel quads per token
+  static constexpr int ROWS = kThreads / QC;                  // token rows staged at a time
+  static constexpr int NQ = TT / ROWS;                        // quads per thread
+  static constexpr int NP = N + LN;  // pairs per token of B and of C: rows in different banks
+  static constexpr int NBQ = (2 * TT * LN + kThreads - 1) / kThreads;  // quads of B and C per thread
+};
+
+// A tile as loaded; the epilogue reads it again.
+template <typename T, int N>
+struct MainStage {
+  using Sh = MainShape<T, N>;
+  alignas(128) T x[Sh::TT * Sh::CT];
+  alignas(128) T dt[Sh::TT * Sh::CT];
+  alignas(128) T z[Sh::TT * Sh::CT];
+  alignas(128) T dy[Sh::TT * Sh::CT];
+  alignas(128) T B[Sh::TT * N];
+  alignas(128) T C[Sh::TT * N];
 };
 
 template <typename T, int N>
 struct MainSmem {
   using Sh = MainShape<T, N>;
-  float dt[Sh::TT * Sh::CT];  // then sum_n w A
+  MainStage<T, N> stage[2];
+  uint64_t full[2];
+  int abort;
+  alignas(16) float dt[Sh::TT * Sh::CT];  // then sum_n w A
   float u[Sh::TT * Sh::CT];   // then du
   float g[Sh::TT * Sh::CT];   // gy, then y
-  f2 B[Sh::TT * N], C[Sh::TT * N];      // each value twice; state 4 l + n at n LN + l
-  f2 coarse[Sh::NT - 1][4][kThreads];   // states in front of tiles 1 ..
-  f2 fine[Sh::NSUB - 1][4][kThreads];   // states in front of a tile's groups 1 ..
-  float cols[2][Sh::VECS * 8];          // dD and d(dt_bias) of each vector's threads
+  // each value twice; state 4 l + n at n LN + l
+  f2 B[Sh::TT * Sh::NP], C[Sh::TT * Sh::NP];
+  float cols[2][kThreads * 4];  // dD and d(dt_bias) of each thread's quads
   float red[2][kWarps][kSub][2 * N];
 };
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, N <= 16 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, 3)
     scan_bwd_main_kernel(const __grid_constant__ ScanArgs a, const __grid_constant__ ScanGrads gr,
-                         const __grid_constant__ BwdRecords rec, int S) {
+                         const __grid_constant__ ScanMaps maps,
+                         const __grid_constant__ BwdRecords rec, int S, unsigned int *timeouts) {
   using Sh = MainShape<T, N>;
   constexpr int CT = Sh::CT, LN = Sh::LN, TT = Sh::TT;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   MainSmem<T, N> &sm = *reinterpret_cast<MainSmem<T, N> *>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sl = lane & (LN - 1), lc = lane / LN;
@@ -283,80 +150,75 @@ __global__ void __launch_bounds__(kThreads, N <= 16 ? 4 : 2)
   const int t0 = part * kPart<N>, t1 = min(a.L, t0 + kPart<N>);
   const bool gated = a.z != nullptr;
 
-  // this thread's vector of a staged tile
-  const int vcol = (tid % Sh::VC) * 8, vrow = tid / Sh::VC;
-  const bool vlive = tid < Sh::VECS, vin = vlive && vcol < nch;
-  const int vs = vrow * CT + vcol;
-  if (vlive)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sm.cols[0][tid * 8 + i] = sm.cols[1][tid * 8 + i] = 0.f;
+  // this thread's quads of a staged tile: one column
+  const int qcol = (tid % Sh::QC) * 4, qrow = tid / Sh::QC;
+  const bool qin = qcol < nch;
+  *reinterpret_cast<float4 *>(&sm.cols[0][tid * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
+  *reinterpret_cast<float4 *>(&sm.cols[1][tid * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  // The tile at token tb into shared memory (first = true: what the states
-  // need, otherwise everything).
-  auto stage = [&](int tb, bool all) {
-    const int64_t t = tb + vrow;
-    if (vlive) {
-      raw8<T> rx, rd, rg, rz;
-      rx.zero();
-      rd.zero();
-      rg.zero();
-      rz.zero();
-      const bool in = vin && t < t1;
-      if (in) {
-        const int64_t row = (int64_t)b * a.L + t;
-        rx.load(static_cast<const T *>(a.x) + row * a.ldx + e0 + vcol);
-        rd.load(static_cast<const T *>(a.dt) + row * a.lddt + e0 + vcol);
-        if (all) {
-          rg.load(static_cast<const T *>(gr.dy) + row * a.E + e0 + vcol);
-          if (gated) rz.load(static_cast<const T *>(a.z) + row * a.ldz + e0 + vcol);
-        }
-      }
-      f2 dv[4], uv[4], bias[4];
+  if (tid == 0) {
+    tc::mbar_init(&sm.full[0], 1);
+    tc::mbar_init(&sm.full[1], 1);
+    tc::mbar_init_fence();
+    sm.abort = 0;
+  }
+  __syncthreads();
+  // The tile at token tb.  A box may reach behind the part's end, the
+  // sequence's or the group's: those rows and channels are cleared when staged.
+  auto issue = [&](int tb, int st) {
+    if (tid != 0) return;
+    MainStage<T, N> &g = sm.stage[st];
+    uint64_t *bar = &sm.full[st];
+    constexpr uint32_t rows = TT * CT * sizeof(T), bc = TT * N * sizeof(T);
+    tc::mbar_arrive_expect_tx(bar, (gated ? 4 : 3) * rows + 2 * bc);
+    tc::tma_load_3d(g.x, &maps.x, e0, tb, b, bar);
+    tc::tma_load_3d(g.dt, &maps.dt, e0, tb, b, bar);
+    tc::tma_load_3d(g.dy, &maps.dy, e0, tb, b, bar);
+    if (gated) tc::tma_load_3d(g.z, &maps.z, e0, tb, b, bar);
+    tc::tma_load_3d(g.B, &maps.B, grp * N, tb, b, bar);
+    tc::tma_load_3d(g.C, &maps.C, grp * N, tb, b, bar);
+  };
+  f2 bias[2] = {dup2(0.f), dup2(0.f)};
+  if (qin && a.dt_bias) load4p(a.dt_bias + e0 + qcol, bias);
+  // Stage st, whose first `rows` rows count, as the main loop reads it.
+  auto convert = [&](int st, int rows) {
+    const MainStage<T, N> &g = sm.stage[st];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bias[i] = dup2(0.f);
-      if (vin && a.dt_bias) load8p(a.dt_bias + e0 + vcol, bias);
-      rx.getp(uv);
-      rd.getp(dv);
+    for (int i = 0; i < Sh::NQ; ++i) {
+      const int row = qrow + i * Sh::ROWS, s = row * CT + qcol;
+      const bool in = qin && row < rows;  // other channels would count in dB and dC
+      f2 xv[2], dv[2], gv[2], zv[2];
+      load4p(&g.x[s], xv);
+      load4p(&g.dt[s], dv);
+      load4p(&g.dy[s], gv);
+      if (gated) load4p(&g.z[s], zv);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         dv[k] = add2(dv[k], bias[k]);
         if (a.softplus) dv[k] = softplus_f2(dv[k]);
-        if (!in) dv[k] = dup2(0.f);
-        uv[k] = mul2(uv[k], dv[k]);
-      }
-      store8p(&sm.dt[vs], dv);
-      store8p(&sm.u[vs], uv);
-      if (all) {
-        f2 gv[4];
-        rg.getp(gv);
+        xv[k] = mul2(xv[k], dv[k]);
         if (gated) {
-          f2 zv[4];
-          rz.getp(zv);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 q = unpack2(zv[k]);
-            gv[k] = mul2(gv[k], mul2(zv[k], pack2(sigmoid_f32(q.x), sigmoid_f32(q.y))));
-          }
+          const float2 q = unpack2(zv[k]);
+          gv[k] = mul2(gv[k], mul2(zv[k], pack2(sigmoid_f32(q.x), sigmoid_f32(q.y))));
         }
-        store8p(&sm.g[vs], gv);
+        if (!in) dv[k] = xv[k] = gv[k] = dup2(0.f);
       }
+      store4p(&sm.dt[s], dv);
+      store4p(&sm.u[s], xv);
+      store4p(&sm.g[s], gv);
     }
-    constexpr int BV = TT * N / 8;
-    for (int v = tid; v < (all ? 2 : 1) * BV; v += kThreads) {
-      const bool second = v >= BV;
-      const int r = second ? v - BV : v;
-      const int row = r / (N / 8), col = (r % (N / 8)) * 8;
-      float q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = 0.f;
-      if (tb + row < t1) {
-        const int64_t tr = (int64_t)b * a.L + tb + row;
-        load8((second ? static_cast<const T *>(a.Cm) + tr * a.ldc
-                      : static_cast<const T *>(a.Bm) + tr * a.ldb) + grp * N + col, q);
+    for (int i = 0; i < Sh::NBQ; ++i) {
+      const int v = tid + i * kThreads, which = v / (TT * LN), q = v % (TT * LN);
+      if (which < 2) {
+        float4 w = load4((which ? g.C : g.B) + q * 4);
+        if (q / LN >= rows) w = make_float4(0.f, 0.f, 0.f, 0.f);
+        f2 *d = (which ? sm.C : sm.B) + q / LN * Sh::NP + q % LN;
+        d[0] = dup2(w.x);
+        d[LN] = dup2(w.y);
+        d[2 * LN] = dup2(w.z);
+        d[3 * LN] = dup2(w.w);
       }
-      f2 *d = (second ? sm.C : sm.B) + row * N + col / 4;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) d[k % 4 * LN + k / 4] = dup2(q[k]);
     }
   };
 
@@ -383,123 +245,87 @@ __global__ void __launch_bounds__(kThreads, N <= 16 ? 4 : 2)
     *reinterpret_cast<float4 *>(p) = make_float4(q0.x, q1.x, q2.x, q3.x);
     *reinterpret_cast<float4 *>(p + N) = make_float4(q0.y, q1.y, q2.y, q3.y);
   };
-  const float *start = S > 1 ? rec.h + pen : a.h0 ? a.h0 + ben : nullptr;
-  f2 A[4], h[4], gc[4], dA[4];
+  f2 A[4], hin[4], gc[4], dA[4];
   load_pair(a.A + en, A, kLog2e);
-  load_pair(start, h, 1.f);
-  load_pair(S > 1 ? rec.g + pen : gr.dhN ? gr.dhN + ben : nullptr, gc, 1.f);
+  load_pair(S > 1 ? rec.s.h + pen : a.h0 ? a.h0 + ben : nullptr, hin, 1.f);
+  load_pair(S > 1 ? rec.s.g + pen : gr.dhN ? gr.dhN + ben : nullptr, gc, 1.f);
 #pragma unroll
   for (int n = 0; n < 4; ++n) dA[n] = dup2(0.f);
+  // the checkpoint in front of token group k of the part (k > 0)
+  auto load_ck = [&](int k, f2 (&h)[4], f2 &sd) {
+    const int64_t rc = (((int64_t)b * S + part) * (kPart<N> / kSub - 1) + k - 1) * a.E + e0 + c0;
+    load_pair(rec.s.ck + rc * N + n0, h, 1.f);
+    sd = cin ? f2{*reinterpret_cast<const unsigned long long *>(rec.s.ckdt + rc)} : dup2(0.f);
+  };
 
   auto tok2 = [&](const float *arr, int t) {
     return f2{*reinterpret_cast<const unsigned long long *>(&arr[t * CT + c0])};
   };
   auto shared4 = [&](const f2 *arr, int t, f2 (&v)[4]) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) v[n] = arr[t * N + n * LN + sl];
-  };
-  // h one token on
-  auto advance = [&](int t) {
-    const f2 d2 = tok2(sm.dt, t), u2 = tok2(sm.u, t);
-    f2 bn[4];
-    shared4(sm.B, t, bn);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) h[n] = fma2(ex2_2(mul2(d2, A[n])), h[n], mul2(u2, bn[n]));
+    for (int n = 0; n < 4; ++n) v[n] = arr[t * Sh::NP + n * LN + sl];
   };
 
+  int grp8 = (t1 - t0 + kSub - 1) / kSub - 1;  // token group of the part, from the last
+  f2 ck[4], cksd = dup2(0.f);
+  if (grp8 > 0) load_ck(grp8, ck, cksd);
   const int ntiles = (t1 - t0 + TT - 1) / TT;
-  for (int q = 0; q + 1 < ntiles; ++q) {
-    stage(t0 + q * TT, false);
-    __syncthreads();
-#pragma unroll 4
-    for (int t = 0; t < TT; ++t) advance(t);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) sm.coarse[q][n][tid] = h[n];
-    __syncthreads();
-  }
-
+  if (ntiles > 0) issue(t0 + (ntiles - 1) * TT, 0);
   for (int q = ntiles - 1; q >= 0; --q) {
-    const int tb = t0 + q * TT;
-    const int nsub = (min(TT, t1 - tb) + kSub - 1) / kSub;
-    stage(tb, true);
-    if (q > 0) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) h[n] = sm.coarse[q - 1][n][tid];
-    } else {
-      load_pair(start, h, 1.f);
+    const int tb = t0 + q * TT, turn = ntiles - 1 - q, st = turn & 1;
+    // a wait that gives up ends the CTA; the next tile's copies are only
+    // issued after this one, so none is in flight but the one that failed
+    if (!tc::mbar_wait(&sm.full[st], (turn >> 1) & 1, &sm.abort, timeouts)) {
+      tc::mbar_wait_drain(&sm.full[st], (turn >> 1) & 1);
+      sm.abort = 1;
     }
-    f2 first[4] = {h[0], h[1], h[2], h[3]};
+    convert(st, min(TT, t1 - tb));
     __syncthreads();
-    for (int sub = 0; sub + 1 < nsub; ++sub) {
-#pragma unroll
-      for (int j = 0; j < kSub; ++j) advance(sub * kSub + j);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) sm.fine[sub][n][tid] = h[n];
-    }
-
+    if (sm.abort) return;
+    // the other stage was last read before this barrier
+    if (q > 0) issue(tb - TT, st ^ 1);
     float *bc = rec.bc + (((int64_t)b * tiles + tile) * a.L + tb) * (2 * N);
-    for (int sub = nsub - 1; sub >= 0; --sub) {
-      f2 hs[kSub + 1][4], ys[kSub];  // hs[j]: the state in front of token j
+    for (int sub = (min(TT, t1 - tb) + kSub - 1) / kSub - 1; sub >= 0; --sub, --grp8) {
+      f2 hs[kSub + 1][4];  // hs[j]: the state in front of token j of the group
 #pragma unroll
-      for (int n = 0; n < 4; ++n) hs[0][n] = sub > 0 ? sm.fine[sub > 0 ? sub - 1 : 0][n][tid] : first[n];
+      for (int n = 0; n < 4; ++n)
+        hs[0][n] = grp8 > 0 ? fma2(ex2_2(mul2(cksd, A[n])), hin[n], ck[n]) : hin[n];
+      if (grp8 > 1) load_ck(grp8 - 1, ck, cksd);
 #pragma unroll
       for (int j = 0; j < kSub; ++j) {
         const int t = sub * kSub + j;
         const f2 d2 = tok2(sm.dt, t), u2 = tok2(sm.u, t);
-        f2 bn[4], cn[4];
+        f2 bn[4];
         shared4(sm.B, t, bn);
-        shared4(sm.C, t, cn);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < 4; ++n)
           hs[j + 1][n] = fma2(ex2_2(mul2(d2, A[n])), hs[j][n], mul2(u2, bn[n]));
-          ys[j] = n ? fma2(hs[j + 1][n], cn[n], ys[j]) : mul2(hs[j + 1][n], cn[n]);
-        }
       }
 #pragma unroll
-      for (int j = kSub - 1; j >= 0; --j) {
-        const int t = sub * kSub + j;
-        const f2 d2 = tok2(sm.dt, t), u2 = tok2(sm.u, t), g2 = tok2(sm.g, t);
-        f2 bn[4], cn[4];
-        shared4(sm.B, t, bn);
-        shared4(sm.C, t, cn);
-        f2 du, dd;
-        float r[8];  // dB, dC of this thread's states, over its channel pair
+      for (int j2 = kSub - 2; j2 >= 0; j2 -= 2) {  // tokens j2 + 1, then j2
+        f2 sums[2][3];  // du, sum_n w A, y over this thread's states
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const f2 g = fma2(cn[n], g2, gc[n]);
-          r[n] = sum2(mul2(g, u2));
-          r[4 + n] = sum2(mul2(hs[j + 1][n], g2));
-          du = n ? fma2(g, bn[n], du) : mul2(g, bn[n]);
-          gc[n] = mul2(g, ex2_2(mul2(d2, A[n])));
-          const f2 w = mul2(gc[n], hs[j][n]);
-          dd = n ? fma2(w, A[n], dd) : mul2(w, A[n]);
-          dA[n] = fma2(w, d2, dA[n]);
-        }
-        // over the states: lane bit 0 takes one channel of the pair
-        {
-          const bool hi = lane & 1;
-          const float2 p0 = unpack2(du), p1 = unpack2(dd), p2 = unpack2(ys[j]);
-          float v0 = hi ? p0.y : p0.x, v1 = hi ? p1.y : p1.x, v2 = hi ? p2.y : p2.x;
-          v0 += __shfl_xor_sync(0xffffffffu, hi ? p0.x : p0.y, 1);
-          v1 += __shfl_xor_sync(0xffffffffu, hi ? p1.x : p1.y, 1);
-          v2 += __shfl_xor_sync(0xffffffffu, hi ? p2.x : p2.y, 1);
+        for (int i = 1; i >= 0; --i) {
+          const int j = j2 + i, t = sub * kSub + j;
+          const f2 d2 = tok2(sm.dt, t), u2 = tok2(sm.u, t), g2 = tok2(sm.g, t);
+          f2 bn[4], cn[4];
+          shared4(sm.B, t, bn);
+          shared4(sm.C, t, cn);
+          float r[8];  // dB, dC of this thread's states, over its channel pair
 #pragma unroll
-          for (int o = 2; o < LN; o <<= 1) {
-            v0 += __shfl_xor_sync(0xffffffffu, v0, o);
-            v1 += __shfl_xor_sync(0xffffffffu, v1, o);
-            v2 += __shfl_xor_sync(0xffffffffu, v2, o);
+          for (int n = 0; n < 4; ++n) {
+            const f2 g = fma2(cn[n], g2, gc[n]);
+            r[n] = sum2(mul2(g, u2));
+            r[4 + n] = sum2(mul2(hs[j + 1][n], g2));
+            sums[i][0] = n ? fma2(g, bn[n], sums[i][0]) : mul2(g, bn[n]);
+            sums[i][2] = n ? fma2(hs[j + 1][n], cn[n], sums[i][2]) : mul2(hs[j + 1][n], cn[n]);
+            gc[n] = mul2(g, ex2_2(mul2(d2, A[n])));
+            const f2 w = mul2(gc[n], hs[j][n]);
+            sums[i][1] = n ? fma2(w, A[n], sums[i][1]) : mul2(w, A[n]);
+            dA[n] = fma2(w, d2, dA[n]);
           }
-          __syncwarp();  // every lane has read this token's inputs
-          if (sl < 2) {
-            const int s = t * CT + c0 + sl;
-            sm.u[s] = v0;
-            sm.dt[s] = v1;
-            sm.g[s] = v2;
-          }
-        }
-        // over the channels: each lane bit keeps half of the eight values
-        float *rd = sm.red[sub & 1][warp][j];
-        {
+          // over the channels: each lane bit keeps half of the eight values
+          float *rd = sm.red[sub & 1][warp][j];
           const bool h1 = lane & LN;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -529,6 +355,40 @@ __global__ void __launch_bounds__(kThreads, N <= 16 ? 4 : 2)
             *reinterpret_cast<float4 *>(&rd[idx]) = make_float4(r[0], r[1], r[2], r[3]);
           }
         }
+        // over the states: lane bit 0 takes one of the two tokens, bit 1 one
+        // channel of the pair
+        const bool b0 = lane & 1;
+        const int s = (sub * kSub + j2 + (b0 ? 1 : 0)) * CT + c0;
+        float2 v[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const float2 keep = unpack2(b0 ? sums[1][k] : sums[0][k]);
+          const float2 send = unpack2(b0 ? sums[0][k] : sums[1][k]);
+          v[k].x = keep.x + __shfl_xor_sync(0xffffffffu, send.x, 1);
+          v[k].y = keep.y + __shfl_xor_sync(0xffffffffu, send.y, 1);
+        }
+        // the shuffles: every lane has read these tokens' inputs
+        __syncwarp();
+        if constexpr (LN == 2) {
+          *reinterpret_cast<float2 *>(&sm.u[s]) = v[0];
+          *reinterpret_cast<float2 *>(&sm.dt[s]) = v[1];
+          *reinterpret_cast<float2 *>(&sm.g[s]) = v[2];
+        } else {
+          const bool b1 = lane & 2;
+          float w[3];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            w[k] = (b1 ? v[k].y : v[k].x) + __shfl_xor_sync(0xffffffffu, b1 ? v[k].x : v[k].y, 2);
+#pragma unroll
+            for (int o = 4; o < LN; o <<= 1) w[k] += __shfl_xor_sync(0xffffffffu, w[k], o);
+          }
+          if (sl < 4) {
+            const int c = b1 ? 1 : 0;
+            sm.u[s + c] = w[0];
+            sm.dt[s + c] = w[1];
+            sm.g[s + c] = w[2];
+          }
+        }
       }
       // the other half of `red` is written before this half is again, with
       // this barrier in between
@@ -546,59 +406,58 @@ __global__ void __launch_bounds__(kThreads, N <= 16 ? 4 : 2)
     }
 
     // the tile's per-token gradients, and its share of the column sums
-    const int64_t t = tb + vrow;
-    if (vin && t < t1) {
-      const int64_t row = (int64_t)b * a.L + t, o = row * a.E + e0 + vcol;
-      f2 xv[4], dv[4], gv[4], du[4], dd[4], yv[4], dskip[4], bias[4];
-      load8p(static_cast<const T *>(a.x) + row * a.ldx + e0 + vcol, xv);
-      load8p(static_cast<const T *>(a.dt) + row * a.lddt + e0 + vcol, dv);
-      load8p(static_cast<const T *>(gr.dy) + o, gv);
+    const MainStage<T, N> &sg = sm.stage[st];
+    f2 dskip[2] = {dup2(0.f), dup2(0.f)};
+    if (qin && a.D) load4p(a.D + e0 + qcol, dskip);
+    f2 sD[2], sb[2];
+    load4p(&sm.cols[0][tid * 4], sD);
+    load4p(&sm.cols[1][tid * 4], sb);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dskip[i] = bias[i] = dup2(0.f);
-      if (a.D) load8p(a.D + e0 + vcol, dskip);
-      if (a.dt_bias) load8p(a.dt_bias + e0 + vcol, bias);
-      load8p(&sm.u[vs], du);
-      load8p(&sm.dt[vs], dd);
-      load8p(&sm.g[vs], yv);
-      if (gated) {
-        f2 zv[4];
-        load8p(static_cast<const T *>(a.z) + row * a.ldz + e0 + vcol, zv);
+    for (int i = 0; i < Sh::NQ; ++i) {
+      const int row = qrow + i * Sh::ROWS, s = row * CT + qcol, t = tb + row;
+      if (qin && t < t1) {
+        const int64_t o = ((int64_t)b * a.L + t) * a.E + e0 + qcol;
+        f2 du[2], dd[2], yv[2], xv[2], dv[2], gv[2], zv[2];
+        load4p(&sg.x[s], xv);
+        load4p(&sg.dt[s], dv);
+        load4p(&sg.dy[s], gv);
+        if (gated) load4p(&sg.z[s], zv);
+        load4p(&sm.u[s], du);
+        load4p(&sm.dt[s], dd);
+        load4p(&sm.g[s], yv);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 z2 = unpack2(zv[k]);
-          const f2 sg = pack2(sigmoid_f32(z2.x), sigmoid_f32(z2.y));
-          // silu'(z) = s (1 + z (1 - s))
-          const f2 slope = mul2(sg, fma2(zv[k], fma2(sg, dup2(-1.f), dup2(1.f)), dup2(1.f)));
-          yv[k] = mul2(mul2(gv[k], fma2(dskip[k], xv[k], yv[k])), slope);
-          gv[k] = mul2(gv[k], mul2(zv[k], sg));
+        for (int k = 0; k < 2; ++k) {
+          f2 g = gv[k];
+          if (gated) {
+            const float2 z2 = unpack2(zv[k]);
+            const f2 act = pack2(sigmoid_f32(z2.x), sigmoid_f32(z2.y));
+            // silu'(z) = s (1 + z (1 - s))
+            const f2 slope = mul2(act, fma2(zv[k], fma2(act, dup2(-1.f), dup2(1.f)), dup2(1.f)));
+            yv[k] = mul2(mul2(g, fma2(dskip[k], xv[k], yv[k])), slope);
+            g = mul2(g, mul2(zv[k], act));
+          }
+          const f2 v = add2(dv[k], bias[k]);
+          const f2 step = a.softplus ? softplus_f2(v) : v;
+          dd[k] = fma2(du[k], xv[k], mul2(dd[k], dup2(kLn2)));
+          if (a.softplus) {
+            const float2 r = unpack2(v);
+            dd[k] = mul2(dd[k], pack2(sigmoid_f32(r.x), sigmoid_f32(r.y)));
+          }
+          du[k] = fma2(du[k], step, mul2(dskip[k], g));
+          sD[k] = fma2(g, xv[k], sD[k]);
+          sb[k] = add2(sb[k], dd[k]);
         }
-        store8p(static_cast<T *>(gr.dz) + o, yv);
+        if (gated) store4p(static_cast<T *>(gr.dz) + o, yv);
+        store4p(static_cast<T *>(gr.dx) + o, du);
+        store4p(static_cast<T *>(gr.ddt) + o, dd);
       }
-      f2 sD[4], sb[4];
-      load8p(&sm.cols[0][tid * 8], sD);
-      load8p(&sm.cols[1][tid * 8], sb);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const f2 v = add2(dv[k], bias[k]);
-        dv[k] = a.softplus ? softplus_f2(v) : v;
-        dd[k] = fma2(du[k], xv[k], mul2(dd[k], dup2(kLn2)));
-        if (a.softplus) {
-          const float2 r = unpack2(v);
-          dd[k] = mul2(dd[k], pack2(sigmoid_f32(r.x), sigmoid_f32(r.y)));
-        }
-        du[k] = fma2(du[k], dv[k], mul2(dskip[k], gv[k]));
-        sD[k] = fma2(gv[k], xv[k], sD[k]);
-        sb[k] = add2(sb[k], dd[k]);
-      }
-      store8p(&sm.cols[0][tid * 8], sD);
-      store8p(&sm.cols[1][tid * 8], sb);
-      store8p(static_cast<T *>(gr.dx) + o, du);
-      store8p(static_cast<T *>(gr.ddt) + o, dd);
     }
+    store4p(&sm.cols[0][tid * 4], sD);
+    store4p(&sm.cols[1][tid * 4], sb);
     // the next tile's staging writes only what this thread itself has read
     // here, and B and C, which were last read before the barrier above
   }
-  store_pair(rec.h + pen, dA);
+  store_pair(rec.dA + pen, dA);
   if (part == 0 && gr.dh0) store_pair(gr.dh0 + ben, gc);
   __syncthreads();
   float *cols = rec.cols + ((int64_t)b * S + part) * 2 * a.E + e0;
@@ -606,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, N <= 16 ? 4 : 2)
     if (i % CT < nch) {
       const float *p = sm.cols[i / CT] + i % CT;  // [rows of threads][CT]
       float s = 0.f;
-      for (int r = 0; r < Sh::VECS / Sh::VC; ++r) s += p[r * CT];
+      for (int r = 0; r < Sh::ROWS; ++r) s += p[r * CT];
       cols[(i < CT ? 0 : a.E) + i % CT] = s;
     }
   }
@@ -640,18 +499,21 @@ int bwd_tiles(int E, int N, int G) {
   return G * ((E / G + CT - 1) / CT);
 }
 
+// The workspace: floats of each record.
 struct BwdSizes {
-  size_t h, g, dt, cols, bc;
+  size_t h, g, dt, ck, ckdt, cols, bc;
   int S;
 };
 BwdSizes bwd_sizes(int B, int L, int E, int N, int G) {
   BwdSizes z;
-  const int pt = bwd_part_tokens(N);
+  const int pt = bwd_part_tokens(N), K = pt / kScanCheckpoint - 1;
   z.S = L > pt ? (L + pt - 1) / pt : 1;
   const size_t bs = (size_t)B * z.S;
   z.h = bs * E * N;
-  z.g = z.S > 1 ? z.h : 0;
-  z.dt = z.S > 1 ? (bs * E + 3) / 4 * 4 : 0;
+  z.g = z.h;
+  z.dt = bs * E;
+  z.ck = L > kScanCheckpoint ? bs * K * E * N : 0;
+  z.ckdt = L > kScanCheckpoint ? bs * K * E : 0;
   z.cols = bs * 2 * E;
   z.bc = (size_t)B * bwd_tiles(E, N, G) * L * 2 * N;
   return z;
@@ -661,19 +523,20 @@ template <typename T, int N>
 cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStream_t s) {
   const BwdSizes z = bwd_sizes(a.B, a.L, a.E, N, a.G);
   BwdRecords rec;
-  rec.h = static_cast<float *>(ws);
-  rec.g = rec.h + z.h;
-  rec.dt = rec.g + z.g;
-  rec.cols = rec.dt + z.dt;
+  rec.s.h = rec.dA = static_cast<float *>(ws);
+  rec.s.g = rec.s.h + z.h;
+  rec.s.dt = rec.s.g + z.g;
+  rec.s.ck = rec.s.dt + z.dt;
+  rec.s.ckdt = rec.s.ck + z.ck;
+  rec.cols = rec.s.ckdt + z.ckdt;
   rec.bc = rec.cols + z.cols;
   cudaError_t e;
+  // one group of tokens needs neither checkpoints nor records
+  if (a.L > kScanCheckpoint) {
+    e = launch_selective_local(a, g.dy, rec.s, z.S, kPart<N>, sizeof(T) == 4 ? kF32 : kBF16, s);
+    if (e != cudaSuccess) return e;
+  }
   if (z.S > 1) {
-    using Sh = LocalShape<T, N>;
-    const int tiles = a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
-    if ((e = allow_smem(scan_bwd_local_kernel<T, N>, Sh::smem)) != cudaSuccess) return e;
-    scan_bwd_local_kernel<T, N><<<(unsigned)((int64_t)a.B * z.S * tiles), kThreads, Sh::smem, s>>>(
-        a, static_cast<const T *>(g.dy), rec, z.S);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t n = (int64_t)a.B * a.E * N;
     scan_bwd_carry_kernel<<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, s>>>(a, g.dhN, rec, z.S);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -681,8 +544,13 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   const int tiles = bwd_tiles(a.E, N, a.G);
   constexpr int smem = sizeof(MainSmem<T, N>);
   if ((e = allow_smem(scan_bwd_main_kernel<T, N>, smem)) != cudaSuccess) return e;
+  unsigned int *timeouts = wait_timeout_counter();
+  if (!timeouts) return cudaErrorUnknown;
+  using Sh = MainShape<T, N>;
+  ScanMaps maps;
+  if (!make_scan_maps(&maps, a, g.dy, sizeof(T), Sh::CT, Sh::TT)) return cudaErrorInvalidValue;
   scan_bwd_main_kernel<T, N><<<(unsigned)((int64_t)a.B * z.S * tiles), kThreads, smem, s>>>(
-      a, g, rec, z.S);
+      a, g, maps, rec, z.S, timeouts);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.L > 0) {
     const int64_t nbc = (int64_t)a.B * a.G * a.L * 2 * N;
@@ -690,7 +558,7 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
         rec.bc, static_cast<T *>(g.dBm), static_cast<T *>(g.dCm), a.B, a.L, a.G, N, tiles / a.G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  e = launch_column_sum(rec.h, a.B * z.S, (int64_t)a.E * N, g.dA, (int64_t)a.E * N, nullptr, s);
+  e = launch_column_sum(rec.dA, a.B * z.S, (int64_t)a.E * N, g.dA, (int64_t)a.E * N, nullptr, s);
   if (e != cudaSuccess || (!g.dD && !g.ddt_bias)) return e;
   return launch_column_sum(rec.cols, a.B * z.S, 2 * (int64_t)a.E, g.dD, a.E, g.ddt_bias, s);
 }
@@ -710,7 +578,7 @@ cudaError_t bwd_states(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStre
 
 size_t selective_backward_workspace_bytes(int B, int L, int E, int N, int G) {
   const BwdSizes z = bwd_sizes(B, L, E, N, G);
-  return sizeof(float) * (z.h + z.g + z.dt + z.cols + z.bc);
+  return sizeof(float) * (z.h + z.g + z.dt + z.ck + z.ckdt + z.cols + z.bc);
 }
 
 cudaError_t launch_selective_backward(const ScanArgs &a, const ScanGrads &g, Dtype dt, void *ws,
