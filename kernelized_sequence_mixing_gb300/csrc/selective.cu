@@ -15,11 +15,14 @@
 // exponentials (4 cycles each), 32 packed operations (2 cycles each) and what
 // feeds them.  Hence:
 //   - a thread owns 4 channels x 4 states in registers: per token it reads one
-//     16-byte vector of dt, of u = dt x, and four 8-byte pairs of B and of C
-//     from shared memory for 16 state updates, done as packed pairs of
+//     16-byte vector of dt, of u = dt x, and two of B and of C (each value
+//     twice) from shared memory for 16 state updates, done as packed pairs of
 //     channels; the next token's operands are read before this token's are
-//     used (a 16-byte read whose addresses repeat every four lanes takes four
-//     wavefronts, an 8-byte one takes one: so B and C lie state-lane-minor);
+//     used.  The backward pass's mode, which has more arithmetic per operand,
+//     reads B and C once each as 8-byte pairs instead and doubles them in
+//     registers: half the shared-memory wavefronts for 16 moves (441 against
+//     447 us for the whole backward pass at B2 L4096 E2048 N16 in bf16, but
+//     161 against 136 us for the forward pass);
 //   - the sum over states crosses N/4 lanes: each lane stores its part of y
 //     (beyond four lanes after an exchange) and the threads that write y add
 //     the parts, a third of the instructions of a shuffle tree;
@@ -91,8 +94,10 @@ struct Smem {
   // dt x; in the output pass y's first parts take its place, then the others
   float u[(MODE == kOut ? S::SLOTS : 1) * S::SLOT];
   alignas(16) float g[MODE == kLocal ? S::TILE : 4];  // dy silu(z)
-  // each value twice, for the packed pairs: state 4 l + n at n LN + l
-  f2 B[S::TT * N], C[MODE != kStates ? S::TT * N : 1];
+  // [token][N][2], each value twice; kLocal: [token][N], states 4 l and 4 l + 1
+  // at 2 l, 4 l + 2 and 4 l + 3 at 2 LN + 2 l
+  float B[S::TT * N * (MODE == kLocal ? 1 : 2)];
+  alignas(16) float C[MODE == kLocal ? S::TT * N : MODE == kOut ? S::TT * N * 2 : 4];
   uint64_t full[2];
   int abort;
 };
@@ -282,11 +287,21 @@ __global__ void __launch_bounds__(kThreads, 4)
       const ulonglong2 gq = *reinterpret_cast<const ulonglong2 *>(&sm.g[s]);
       o.g[0] = {gq.x}; o.g[1] = {gq.y};
     }
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      o.b[n] = sm.B[t * N + n * Sh::LN + sl];
-      if constexpr (MODE != kStates) o.c[n] = sm.C[t * N + n * Sh::LN + sl];
-    }
+    auto shared4 = [&](const float *arr, f2 (&v)[4]) {
+      if constexpr (LOCAL) {
+        const float *p = arr + t * N + 2 * sl;
+        const float2 lo = *reinterpret_cast<const float2 *>(p);
+        const float2 hi = *reinterpret_cast<const float2 *>(p + 2 * Sh::LN);
+        v[0] = dup2(lo.x); v[1] = dup2(lo.y);
+        v[2] = dup2(hi.x); v[3] = dup2(hi.y);
+      } else {
+        const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(arr + (t * N + n0) * 2);
+        v[0] = {p[0].x}; v[1] = {p[0].y};
+        v[2] = {p[1].x}; v[3] = {p[1].y};
+      }
+    };
+    shared4(sm.B, o.b);
+    if constexpr (MODE != kStates) shared4(sm.C, o.c);
     return o;
   };
 
@@ -338,11 +353,15 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (which < (MODE != kStates ? 2 : 1)) {
         float4 w = load4((which ? g.C : g.B) + q);
         if (q / N >= rows) w = make_float4(0.f, 0.f, 0.f, 0.f);
-        f2 *d = (which ? sm.C : sm.B) + q / N * N + q % N / 4;
-        d[0] = dup2(w.x);
-        d[Sh::LN] = dup2(w.y);
-        d[2 * Sh::LN] = dup2(w.z);
-        d[3 * Sh::LN] = dup2(w.w);
+        float *d = which ? sm.C : sm.B;
+        if constexpr (LOCAL) {
+          d += q / N * N + q % N / 2;
+          *reinterpret_cast<float2 *>(d) = make_float2(w.x, w.y);
+          *reinterpret_cast<float2 *>(d + 2 * Sh::LN) = make_float2(w.z, w.w);
+        } else {
+          *reinterpret_cast<float4 *>(d + 2 * q) = make_float4(w.x, w.x, w.y, w.y);
+          *reinterpret_cast<float4 *>(d + 2 * q + 4) = make_float4(w.z, w.z, w.w, w.w);
+        }
       }
     }
     __syncthreads();

@@ -101,7 +101,7 @@ struct MainShape {
   static constexpr int QC = CT / 4;                           // channel quads per token
   static constexpr int ROWS = kThreads / QC;                  // token rows staged at a time
   static constexpr int NQ = TT / ROWS;                        // quads per thread
-  static constexpr int NP = N + LN;  // pairs per token of B and of C: rows in different banks
+  static constexpr int NP = N + 8;  // floats per token of B and of C: rows in different banks
   static constexpr int NBQ = (2 * TT * LN + kThreads - 1) / kThreads;  // quads of B and C per thread
 };
 
@@ -126,8 +126,9 @@ struct MainSmem {
   alignas(16) float dt[Sh::TT * Sh::CT];  // then sum_n w A
   float u[Sh::TT * Sh::CT];   // then du
   float g[Sh::TT * Sh::CT];   // gy, then y
-  // each value twice; state 4 l + n at n LN + l
-  f2 B[Sh::TT * Sh::NP], C[Sh::TT * Sh::NP];
+  // states 4 l, 4 l + 1 at 2 l, states 4 l + 2, 4 l + 3 at 2 LN + 2 l: eight
+  // bytes a lane, whose repeats in the warp share a wavefront (sixteen do not)
+  float B[Sh::TT * Sh::NP], C[Sh::TT * Sh::NP];
   float cols[2][kThreads * 4];  // dD and d(dt_bias) of each thread's quads
   float red[2][kWarps][kSub][2 * N];
 };
@@ -178,6 +179,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     tc::tma_load_3d(g.B, &maps.B, grp * N, tb, b, bar);
     tc::tma_load_3d(g.C, &maps.C, grp * N, tb, b, bar);
   };
+  const int ntiles = (t1 - t0 + TT - 1) / TT;
+  if (ntiles > 0) issue(t0 + (ntiles - 1) * TT, 0);
   f2 bias[2] = {dup2(0.f), dup2(0.f)};
   if (qin && a.dt_bias) load4p(a.dt_bias + e0 + qcol, bias);
   // Stage st, whose first `rows` rows count, as the main loop reads it.
@@ -213,11 +216,9 @@ __global__ void __launch_bounds__(kThreads, 3)
       if (which < 2) {
         float4 w = load4((which ? g.C : g.B) + q * 4);
         if (q / LN >= rows) w = make_float4(0.f, 0.f, 0.f, 0.f);
-        f2 *d = (which ? sm.C : sm.B) + q / LN * Sh::NP + q % LN;
-        d[0] = dup2(w.x);
-        d[LN] = dup2(w.y);
-        d[2 * LN] = dup2(w.z);
-        d[3 * LN] = dup2(w.w);
+        float *d = (which ? sm.C : sm.B) + q / LN * Sh::NP + q % LN * 2;
+        *reinterpret_cast<float2 *>(d) = make_float2(w.x, w.y);
+        *reinterpret_cast<float2 *>(d + 2 * LN) = make_float2(w.z, w.w);
       }
     }
   };
@@ -261,16 +262,20 @@ __global__ void __launch_bounds__(kThreads, 3)
   auto tok2 = [&](const float *arr, int t) {
     return f2{*reinterpret_cast<const unsigned long long *>(&arr[t * CT + c0])};
   };
-  auto shared4 = [&](const f2 *arr, int t, f2 (&v)[4]) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) v[n] = arr[t * Sh::NP + n * LN + sl];
+  // this thread's four states of B or C, each twice
+  auto shared4 = [&](const float *arr, int t, f2 (&v)[4]) {
+    const float *p = arr + t * Sh::NP + 2 * sl;
+    const float2 lo = *reinterpret_cast<const float2 *>(p);
+    const float2 hi = *reinterpret_cast<const float2 *>(p + 2 * LN);
+    v[0] = dup2(lo.x);
+    v[1] = dup2(lo.y);
+    v[2] = dup2(hi.x);
+    v[3] = dup2(hi.y);
   };
 
   int grp8 = (t1 - t0 + kSub - 1) / kSub - 1;  // token group of the part, from the last
   f2 ck[4], cksd = dup2(0.f);
   if (grp8 > 0) load_ck(grp8, ck, cksd);
-  const int ntiles = (t1 - t0 + TT - 1) / TT;
-  if (ntiles > 0) issue(t0 + (ntiles - 1) * TT, 0);
   for (int q = ntiles - 1; q >= 0; --q) {
     const int tb = t0 + q * TT, turn = ntiles - 1 - q, st = turn & 1;
     // a wait that gives up ends the CTA; the next tile's copies are only
