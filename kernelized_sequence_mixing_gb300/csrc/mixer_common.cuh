@@ -84,9 +84,16 @@ __device__ __forceinline__ f2 softplus_f2(f2 x) {
 }
 __device__ __forceinline__ float softplus_f32(float x) { return unpack2(softplus_f2(dup2(x))).x; }
 
-// 1 / (1 + exp(-x)); exp(-x) = inf gives 0, NaN stays NaN
+// 1 / (1 + exp(-x)) on the special function unit (two roundings each of the
+// exponential and the reciprocal); exp(-x) = inf gives 0, NaN stays NaN
 __device__ __forceinline__ float sigmoid_f32(float x) {
-  return __fdividef(1.f, 1.f + ex2(-x * kLog2e));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-x * kLog2e)));
+  return r;
+}
+__device__ __forceinline__ f2 sigmoid_f2(f2 x) {
+  const float2 q = unpack2(x);
+  return pack2(sigmoid_f32(q.x), sigmoid_f32(q.y));
 }
 
 // Asynchronous copy of 16 bytes to shared memory (zeros where !valid: the

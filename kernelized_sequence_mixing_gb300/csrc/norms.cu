@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   constexpr int R = VPT == 1 && LANES < 256 ? 2 : 1;  // rows per group, loaded together
   __shared__ float sh[2][1][kThreads / 32];
   int round = 0;
+  const float invD = 1.f / a.D;
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
   raw8<T> rp[R][VPT], rg[R][VPT];
   int64_t off[R];
@@ -127,41 +128,42 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    float p[VPT][8], g[VPT][8], s[1] = {0.f};
+    f2 p[VPT][4], g[VPT][4], s2 = dup2(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      rp[r][v].get(p[v]);
-      rg[r][v].get(g[v]);
+      rp[r][v].getp(p[v]);
+      rg[r][v].getp(g[v]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         if (MODE == kResidual) {
-          p[v][i] = fmaf(a.scale, p[v][i], g[v][i]);
+          p[v][i] = fma2(dup2(a.scale), p[v][i], g[v][i]);
         } else {
-          g[v][i] *= sigmoid_f32(g[v][i]);
-          if (MODE == kGateFirst) p[v][i] *= g[v][i];
+          g[v][i] = mul2(g[v][i], sigmoid_f2(g[v][i]));
+          if (MODE == kGateFirst) p[v][i] = mul2(p[v][i], g[v][i]);
         }
-        s[0] = fmaf(p[v][i], p[v][i], s[0]);
+        s2 = fma2(p[v][i], p[v][i], s2);
       }
     }
+    float s[1] = {sum2(s2)};
     row_sum<LANES, 1>(s, sh, round);
-    const float rstd = rsqrtf(s[0] / a.D + a.eps);
+    const f2 rstd = dup2(rsqrtf(fmaf(s[0], invD, a.eps)));
     if (!live[r]) continue;
     T *o = static_cast<T *>(a.out1) + off[r];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (v * LANES + lane) * 8;
       if (c < a.D) {
-        if (MODE == kResidual) store8(static_cast<T *>(a.out2) + off[r] + c, p[v]);
-        float w[8];
+        if (MODE == kResidual) store8p(static_cast<T *>(a.out2) + off[r] + c, p[v]);
+        f2 w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        if (a.w) load8(a.w + (int64_t)h * a.D + c, w);
+        for (int i = 0; i < 4; ++i) w[i] = dup2(1.f);
+        if (a.w) load8p(a.w + (int64_t)h * a.D + c, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[i] *= p[v][i] * rstd;
-          if (MODE == kGateAfter) w[i] *= g[v][i];
+        for (int i = 0; i < 4; ++i) {
+          w[i] = mul2(w[i], mul2(p[v][i], rstd));
+          if (MODE == kGateAfter) w[i] = mul2(w[i], g[v][i]);
         }
-        store8(o + c, w);
+        store8p(o + c, w);
       }
     }
   }
@@ -179,104 +181,120 @@ __global__ void __launch_bounds__(kThreads)
   const int hblocks = a.H / a.hb, slot = blockIdx.x / hblocks, h0 = blockIdx.x % hblocks * a.hb;
   const int h = h0 + (grp & (a.hb - 1));
   const int tpc = GPC / a.hb;  // tokens of a turn
-  float w[VPT][8], dw[VPT][8];
+  f2 w[VPT][4], dw[VPT][4];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = (v * LANES + lane) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[v][i] = 1.f;
-      dw[v][i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      w[v][i] = dup2(1.f);
+      dw[v][i] = dup2(0.f);
     }
-    if (a.w && c < a.D) load8(a.w + (int64_t)h * a.D + c, w[v]);
+    if (a.w && c < a.D) load8p(a.w + (int64_t)h * a.D + c, w[v]);
   }
   const float invD = 1.f / a.D;
-  // every group of the CTA makes the same number of turns (the sums cross
-  // lanes of several groups)
-  for (unsigned j0 = slot * tpc; j0 < a.tokens; j0 += slots * tpc) {
+  // a turn's rows as they lie in memory, loaded one turn ahead where a row is
+  // one vector per lane
+  struct Rows {
+    raw8<T> y[VPT], g[VPT], d[VPT];  // g: the gate, or dr
+    int64_t off, yoff;
+    bool live;
+  };
+  auto fetch = [&](unsigned j0, Rows &r) {
     const unsigned j = j0 + grp / a.hb;
-    const bool live = j < a.tokens;
-    const unsigned jj = live ? j : 0u;
-    const int64_t off = (int64_t)(jj * a.H + h) * a.D;
-    const int64_t yoff = MODE == kResidual ? off : y_offset(a, jj, h);
-    const T *in1 = static_cast<const T *>(a.in1) + yoff;
-    const T *in2 = static_cast<const T *>(a.in2) + off;
-    const T *in3 = static_cast<const T *>(a.in3) + off;
-    const T *in4 = static_cast<const T *>(a.in4) + off;
-    raw8<T> ry[VPT], rg[VPT], rd[VPT];  // rg: the gate, or dr
+    r.live = j < a.tokens;
+    const unsigned jj = r.live ? j : 0u;
+    r.off = (int64_t)(jj * a.H + h) * a.D;
+    r.yoff = MODE == kResidual ? r.off : y_offset(a, jj, h);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (v * LANES + lane) * 8;
-      ry[v].zero();
-      rg[v].zero();
-      rd[v].zero();
-      if (live && c < a.D) {
-        ry[v].load(in1 + c);
-        rd[v].load(in3 + c);
+      r.y[v].zero();
+      r.g[v].zero();
+      r.d[v].zero();
+      if (r.live && c < a.D) {
+        r.y[v].load(static_cast<const T *>(a.in1) + r.yoff + c);
+        r.d[v].load(static_cast<const T *>(a.in3) + r.off + c);
         if (MODE == kResidual) {
-          if (a.in4) rg[v].load(in4 + c);
+          if (a.in4) r.g[v].load(static_cast<const T *>(a.in4) + r.off + c);
         } else {
-          rg[v].load(in2 + c);
+          r.g[v].load(static_cast<const T *>(a.in2) + r.off + c);
         }
       }
     }
-    float s[2] = {0.f, 0.f};
+  };
+  constexpr bool kPrefetch = VPT == 1;
+  const unsigned stride = slots * tpc;
+  Rows cur, nxt;
+  if (kPrefetch) fetch(slot * tpc, nxt);
+  // every group of the CTA makes the same number of turns (the sums cross
+  // lanes of several groups)
+  for (unsigned j0 = slot * tpc; j0 < a.tokens; j0 += stride) {
+    if (kPrefetch) {
+      cur = nxt;
+      fetch(j0 + stride, nxt);
+    } else {
+      fetch(j0, cur);
+    }
+    f2 s0 = dup2(0.f), s1 = dup2(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      float y[8], g[8], d[8];
-      ry[v].get(y);
-      rg[v].get(g);
-      rd[v].get(d);
+      f2 y[4], g[4], d[4];
+      cur.y[v].getp(y);
+      cur.g[v].getp(g);
+      cur.d[v].getp(d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float p = y[i], dn = d[i] * w[v][i];
+      for (int i = 0; i < 4; ++i) {
+        f2 p = y[i], dn = mul2(d[i], w[v][i]);
         if (MODE != kResidual) {
-          const float act = g[i] * sigmoid_f32(g[i]);
-          if (MODE == kGateFirst) p *= act;
-          else dn *= act;
+          const f2 act = mul2(g[i], sigmoid_f2(g[i]));
+          if (MODE == kGateFirst) p = mul2(p, act);
+          else dn = mul2(dn, act);
         }
-        s[0] = fmaf(p, p, s[0]);
-        s[1] = fmaf(dn, p, s[1]);
+        s0 = fma2(p, p, s0);
+        s1 = fma2(dn, p, s1);
       }
     }
+    float s[2] = {sum2(s0), sum2(s1)};
     row_sum<LANES, 2>(s, sh, round);
-    const float rstd = rsqrtf(fmaf(s[0], invD, a.eps));
-    const float k = rstd * rstd * rstd * s[1] * invD;
-    if (live) {
+    const float rs = rsqrtf(fmaf(s[0], invD, a.eps));
+    const f2 rstd = dup2(rs), k = dup2(-rs * rs * rs * s[1] * invD);
+    if (cur.live) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = (v * LANES + lane) * 8;
         if (c < a.D) {
-          float y[8], g[8], d[8], o1[8], o2[8];
-          ry[v].get(y);
-          rg[v].get(g);
-          rd[v].get(d);
+          f2 y[4], g[4], d[4], o1[4], o2[4];
+          cur.y[v].getp(y);
+          cur.g[v].getp(g);
+          cur.d[v].getp(d);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             if (MODE == kResidual) {
-              const float dp = fmaf(rstd, d[i] * w[v][i], -k * y[i]);
-              dw[v][i] = fmaf(d[i], y[i] * rstd, dw[v][i]);
-              o1[i] = g[i] + dp;
-              o2[i] = a.scale * o1[i];
+              const f2 n = mul2(y[i], rstd);
+              dw[v][i] = fma2(d[i], n, dw[v][i]);
+              o1[i] = add2(g[i], fma2(rstd, mul2(d[i], w[v][i]), mul2(k, y[i])));
+              o2[i] = mul2(dup2(a.scale), o1[i]);
             } else {
-              const float sg = sigmoid_f32(g[i]);
-              const float act = g[i] * sg, dact = sg * fmaf(g[i], 1.f - sg, 1.f);
+              const f2 sg = sigmoid_f2(g[i]), act = mul2(g[i], sg);
+              // silu'(g) = s (1 + g (1 - s))
+              const f2 dact = mul2(sg, fma2(g[i], fma2(sg, dup2(-1.f), dup2(1.f)), dup2(1.f)));
               if (MODE == kGateFirst) {
-                const float p = y[i] * act;
-                const float dp = fmaf(rstd, d[i] * w[v][i], -k * p);
-                dw[v][i] = fmaf(d[i], p * rstd, dw[v][i]);
-                o1[i] = dp * act;
-                o2[i] = dp * y[i] * dact;
+                const f2 p = mul2(y[i], act);
+                const f2 dp = fma2(rstd, mul2(d[i], w[v][i]), mul2(k, p));
+                dw[v][i] = fma2(d[i], mul2(p, rstd), dw[v][i]);
+                o1[i] = mul2(dp, act);
+                o2[i] = mul2(mul2(dp, y[i]), dact);
               } else {
-                const float dn = d[i] * w[v][i] * act, n = y[i] * rstd;
-                dw[v][i] = fmaf(d[i] * act, n, dw[v][i]);
-                o1[i] = fmaf(rstd, dn, -k * y[i]);
-                o2[i] = d[i] * n * w[v][i] * dact;
+                const f2 da = mul2(d[i], act), n = mul2(y[i], rstd);
+                dw[v][i] = fma2(da, n, dw[v][i]);
+                o1[i] = fma2(rstd, mul2(da, w[v][i]), mul2(k, y[i]));
+                o2[i] = mul2(mul2(d[i], n), mul2(w[v][i], dact));
               }
             }
           }
-          store8(static_cast<T *>(a.out1) + yoff + c, o1);
-          if (MODE != kResidual || a.out2) store8(static_cast<T *>(a.out2) + off + c, o2);
+          store8p(static_cast<T *>(a.out1) + cur.yoff + c, o1);
+          if (MODE != kResidual || a.out2) store8p(static_cast<T *>(a.out2) + cur.off + c, o2);
         }
       }
     }
@@ -287,7 +305,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (v * LANES + lane) * 8;
-      if (c < a.D) store8(rec + c, dw[v]);
+      if (c < a.D) store8p(rec + c, dw[v]);
     }
   } else {
     // each head's groups, in group order
@@ -295,7 +313,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       __syncthreads();
-      store8(&part[grp][lane * 8], dw[v]);
+      store8p(&part[grp][lane * 8], dw[v]);
       __syncthreads();
       for (int i = threadIdx.x; i < a.hb * LANES * 8; i += kThreads) {
         const int hh = i / (LANES * 8), k = i % (LANES * 8), c = v * LANES * 8 + k;
@@ -334,12 +352,13 @@ int head_block(int H, int D) {
   return hb;
 }
 
-// CTAs per head block of a backward pass: about four per SM over all blocks,
+// CTAs per head block of a backward pass: about three per SM over all blocks
+// (8191 rows of 2048 in bf16: 37 us, with two 39, four 42),
 // no more than there are rows for.
 int bwd_slots(int64_t tokens, int H, int D) {
   const int hb = head_block(H, D), tpc = kThreads / lanes_of(D) / hb, blocks = H / hb;
   const int64_t most = (tokens + tpc - 1) / tpc;
-  int64_t n = (152 * 4 + blocks - 1) / blocks;
+  int64_t n = (152 * 3 + blocks - 1) / blocks;
   if (n > most) n = most;
   return n < 1 ? 1 : static_cast<int>(n);
 }

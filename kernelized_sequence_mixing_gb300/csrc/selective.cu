@@ -568,10 +568,11 @@ template <typename T, int N>
 cudaError_t step_typed(const ScanArgs &a, cudaStream_t s) {
   constexpr int PER = 256 / (N / 4), kMaxY = 65535;
   const unsigned nx = (a.E + PER - 1) / PER;
-  // four sequences per thread once that still gives every SM four CTAs
-  if ((int64_t)nx * a.B >= 152 * 4 * 4) {
-    const int ny = (a.B + 3) / 4;
-    scan_step_kernel<T, N, 4><<<dim3(nx, ny < kMaxY ? ny : kMaxY), 256, 0, s>>>(a);
+  // two sequences per thread once that still gives every SM eight CTAs (256 x
+  // 4096 channels of 16 states in bf16: 28.9 us; four: 29.6)
+  if ((int64_t)nx * a.B >= 152 * 8 * 2) {
+    const int ny = (a.B + 1) / 2;
+    scan_step_kernel<T, N, 2><<<dim3(nx, ny < kMaxY ? ny : kMaxY), 256, 0, s>>>(a);
   } else {
     scan_step_kernel<T, N, 1><<<dim3(nx, a.B < kMaxY ? a.B : kMaxY), 256, 0, s>>>(a);
   }

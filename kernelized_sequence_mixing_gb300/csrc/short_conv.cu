@@ -100,10 +100,7 @@ __device__ __forceinline__ void load_bias(const float *bias, int e, f2 (&out)[P]
     out[p] = pack2(q.x, q.y);
   }
 }
-__device__ __forceinline__ f2 silu2(f2 v) {
-  const float2 q = unpack2(v);
-  return pack2(q.x * sigmoid_f32(q.x), q.y * sigmoid_f32(q.y));
-}
+__device__ __forceinline__ f2 silu2(f2 v) { return mul2(v, sigmoid_f2(v)); }
 
 // Row t < 0 of a sequence (before its first token): state row t + W - 1, or
 // zeros.
@@ -179,52 +176,68 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (t0 >= t1) return;
 
+  f2 w[W][P], bias[P], win[W][P];  // win[k] = row t - W + 1 + k
+  auto enter = [&](const rawp<T, P> &r) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+      for (int p = 0; p < P; ++p) win[k][p] = win[k + 1][p];
+    r.get(win[W - 1]);
+  };
+  auto out_row = [&](T *p) {
+    f2 o[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      o[i] = bias[i];
+#pragma unroll
+      for (int k = 0; k < W; ++k) o[i] = fma2(w[k][i], win[k][i], o[i]);
+      if (a.silu) o[i] = silu2(o[i]);
+    }
+    store_pairs(p, o);
+  };
   constexpr int kAhead = 4;
   const T *xp = x + t0 * a.ldx;
   T *yp = y + (int64_t)t0 * a.E;
+  int t = t0;
   rawp<T, P> nxt[kAhead];
+  auto fetch = [&] {
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j)
-    if (t0 + j < t1) nxt[j].load(xp + j * a.ldx);
-  f2 w[W][P], bias[P], win[W][P];  // win[k] = row t - W + 1 + k
+    for (int j = 0; j < kAhead; ++j) {
+      nxt[j].load(xp);
+      xp += a.ldx;
+    }
+  };
+  if (t + kAhead <= t1) fetch();
   load_taps<W, P>(a.w, e, w);
   load_bias<P>(a.bias, e, bias);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
-    const int t = t0 - (W - 1) + k;
+    const int s = t0 - (W - 1) + k;
     rawp<T, P> r;
-    if (t >= 0) r.load(x + t * a.ldx);
-    else r = early_row<T, W, P>(st, t, a.E);
+    if (s >= 0) r.load(x + s * a.ldx);
+    else r = early_row<T, W, P>(st, s, a.E);
     r.get(win[k + 1]);
   }
-  for (int tb = t0; tb < t1; tb += kAhead) {
+  for (; t + kAhead <= t1; t += kAhead) {
     rawp<T, P> cur[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      cur[j] = nxt[j];
-      if (tb + kAhead + j < t1) nxt[j].load(xp + (kAhead + j) * a.ldx);
-    }
+    for (int j = 0; j < kAhead; ++j) cur[j] = nxt[j];
+    if (t + 2 * kAhead <= t1) fetch();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (tb + j < t1) {
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-          for (int p = 0; p < P; ++p) win[k][p] = win[k + 1][p];
-        cur[j].get(win[W - 1]);
-        f2 o[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          o[p] = bias[p];
-#pragma unroll
-          for (int k = 0; k < W; ++k) o[p] = fma2(w[k][p], win[k][p], o[p]);
-          if (a.silu) o[p] = silu2(o[p]);
-        }
-        store_pairs(yp + (int64_t)j * a.E, o);
-      }
+      enter(cur[j]);
+      out_row(yp);
+      yp += a.E;
     }
-    xp += kAhead * a.ldx;
-    yp += (int64_t)kAhead * a.E;
+  }
+  xp = x + t * a.ldx;
+  for (; t < t1; ++t) {
+    rawp<T, P> r;
+    r.load(xp);
+    xp += a.ldx;
+    enter(r);
+    out_row(yp);
+    yp += a.E;
   }
 }
 
@@ -294,20 +307,6 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
     const T *dy = static_cast<const T *>(g.dy) + b * a.L * a.E + e;
     T *dx = static_cast<T *>(g.dx) + b * a.L * a.E + e;
     const T *st = a.state ? static_cast<const T *>(a.state) + b * (W - 1) * a.E + e : nullptr;
-    const int last = s1 + W - 1;        // tokens walked: [s0, last)
-    const int here = min(last, a.L);    // those that exist
-    constexpr int kAhead = 4;
-    rawp<T, 1> xn[kAhead], gn[kAhead];
-    auto fetch = [&](int j, int t) {
-      xn[j].zero();
-      gn[j].zero();
-      if (t < here) {
-        xn[j].load(x + t * a.ldx);
-        gn[j].load(dy + (int64_t)t * a.E);
-      }
-    };
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j, s0 + j);
     f2 xw[W], dp[W];  // xw[k] = row t-W+1+k; dp[k] = dpre of t-W+1+k
 #pragma unroll
     for (int k = 0; k < W; ++k) xw[k] = dp[k] = dup2(0.f);
@@ -321,53 +320,109 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
       q.get(v);
       xw[k + 1] = v[0];
     }
-    for (int tb = s0; tb < last; tb += kAhead) {
-      rawp<T, 1> xq[kAhead], gq[kAhead];
+    // one token on: its row and upstream gradient into the windows
+    auto enter = [&](const rawp<T, 1> &xr, const rawp<T, 1> &gr) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        xq[j] = xn[j];
-        gq[j] = gn[j];
-        fetch(j, tb + kAhead + j);
+      for (int k = 0; k < W - 1; ++k) {
+        xw[k] = xw[k + 1];
+        dp[k] = dp[k + 1];
       }
+      f2 v[1];
+      xr.get(v);
+      xw[W - 1] = v[0];
+      gr.get(v);
+      f2 d = v[0];
+      if (a.silu) {
+        f2 p = bias;
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int t = tb + j;
-        if (t < last) {
+        for (int k = 0; k < W; ++k) p = fma2(w[k][0], xw[k], p);
+        // silu'(p) = s (1 + p (1 - s))
+        const f2 s = sigmoid_f2(p);
+        d = mul2(d, mul2(s, fma2(p, fma2(s, dup2(-1.f), dup2(1.f)), dup2(1.f))));
+      }
+      dp[W - 1] = d;
+    };
+    auto add_sums = [&] {
+      db = add2(db, dp[W - 1]);
 #pragma unroll
-          for (int k = 0; k < W - 1; ++k) {
-            xw[k] = xw[k + 1];
-            dp[k] = dp[k + 1];
-          }
-          f2 v[1];
-          xq[j].get(v);
-          xw[W - 1] = v[0];
-          gq[j].get(v);
-          f2 d = v[0];
-          if (a.silu) {
-            f2 p2 = bias;
+      for (int k = 0; k < W; ++k) dw[k] = fma2(dp[W - 1], xw[k], dw[k]);
+    };
+    auto dx_row = [&] {  // of the window's first token
+      // dpre_(s + W - 1 - k) = dp[W - 1 - k]
+      f2 o = mul2(w[0][0], dp[W - 1]);
 #pragma unroll
-            for (int k = 0; k < W; ++k) p2 = fma2(w[k][0], xw[k], p2);
-            const float2 p = unpack2(p2), q = unpack2(d);
-            const float s = sigmoid_f32(p.x), u = sigmoid_f32(p.y);
-            d = pack2(q.x * (s * fmaf(p.x, 1.f - s, 1.f)), q.y * (u * fmaf(p.y, 1.f - u, 1.f)));
-          }
-          if (t >= a.L) d = dup2(0.f);
-          dp[W - 1] = d;
-          if (t < s1) {
-            db = add2(db, d);
+      for (int k = 1; k < W; ++k) o = fma2(w[k][0], dp[W - 1 - k], o);
+      return o;
+    };
+    // the first W - 1 tokens: their dx rows belong to the run before, or are
+    // the state's
+    int t = s0;
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k] = fma2(d, xw[k], dw[k]);
-          }
-          const int s = t - (W - 1);
-          if (s >= s0 || (run == 0 && g.dstate)) {
-            // dpre_(s + W - 1 - k) = dp[W - 1 - k]
-            f2 o = mul2(w[0][0], dp[W - 1]);
+    for (int k = 0; k < W - 1; ++k, ++t) {
+      rawp<T, 1> xr, gr;
+      xr.zero();
+      gr.zero();
+      if (t < a.L) {
+        xr.load(x + t * a.ldx);
+        gr.load(dy + (int64_t)t * a.E);
+      }
+      enter(xr, gr);
+      if (t >= a.L) dp[W - 1] = dup2(0.f);
+      if (t < s1) add_sums();
+      if (run == 0 && g.dstate) store_pair(static_cast<T *>(g.dstate) + (b * (W - 1) + k) * a.E + e, dx_row());
+    }
+    // whole groups of the run's own tokens, loads a group ahead
+    constexpr int kAhead = 2 * W;  // a multiple of W: the windows turn in place
+    const T *xp = x + t * a.ldx, *gp = dy + (int64_t)t * a.E;
+    T *op = dx + (int64_t)s0 * a.E;
+    if (t + kAhead <= s1) {
+      rawp<T, 1> xn[kAhead], gn[kAhead];
+      auto fetch = [&] {
 #pragma unroll
-            for (int k = 1; k < W; ++k) o = fma2(w[k][0], dp[W - 1 - k], o);
-            if (s >= 0) store_pair(dx + (int64_t)s * a.E, o);
-            else store_pair(static_cast<T *>(g.dstate) + (b * (W - 1) + s + W - 1) * a.E + e, o);
-          }
+        for (int j = 0; j < kAhead; ++j) {
+          xn[j].load(xp);
+          gn[j].load(gp);
+          xp += a.ldx;
+          gp += a.E;
         }
+      };
+      fetch();
+      for (; t + kAhead <= s1; t += kAhead) {
+        rawp<T, 1> xq[kAhead], gq[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          xq[j] = xn[j];
+          gq[j] = gn[j];
+        }
+        if (t + 2 * kAhead <= s1) fetch();
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          enter(xq[j], gq[j]);
+          add_sums();
+          store_pair(op, dx_row());
+          op += a.E;
+        }
+      }
+    }
+    // what is left, and the W - 1 tokens behind the run
+    xp = x + t * a.ldx;
+    gp = dy + (int64_t)t * a.E;
+    for (; t < s1 + W - 1; ++t) {
+      rawp<T, 1> xr, gr;
+      xr.zero();
+      gr.zero();
+      if (t < a.L) {
+        xr.load(xp);
+        gr.load(gp);
+        xp += a.ldx;
+        gp += a.E;
+      }
+      enter(xr, gr);
+      if (t >= a.L) dp[W - 1] = dup2(0.f);
+      if (t < s1) add_sums();
+      if (t - (W - 1) >= s0) {
+        store_pair(op, dx_row());
+        op += a.E;
       }
     }
   }
@@ -394,14 +449,14 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
 }
 
 // Backward pass: a run per warp row such that all the CTAs are resident at
-// once (about four per SM; a CTA has four rows), of at least 29 tokens (the
+// once (five per SM; a CTA has four rows), of at least 29 tokens (the
 // W - 1 walked twice are then a tenth at most).
 struct BwdPlan {
   int run_len, runs, ny;
 };
 BwdPlan conv_bwd_plan(int B, int L, int E) {
   const int nx = (E / 2 + kBwdCols - 1) / kBwdCols;
-  int rows = 152 * 4 / nx * kBwdRows;  // rows of runs that fit at once
+  int rows = 152 * 5 / nx * kBwdRows;  // rows of runs that fit at once
   if (rows < kBwdRows) rows = kBwdRows;
   const int per = rows / B > 0 ? rows / B : 1;  // runs per sequence
   BwdPlan p;
@@ -415,12 +470,12 @@ BwdPlan conv_bwd_plan(int B, int L, int E) {
 
 template <typename T, int W>
 cudaError_t conv_fwd_typed(const ConvArgs &a, cudaStream_t s) {
-  // runs of 64 tokens (the taps and the W - 1 early rows cost a thread about
+  // runs of 128 tokens (the taps and the W - 1 early rows cost a thread about
   // five tokens' work), shorter ones, whole groups of 4, where that leaves
   // fewer than 256 threads per SM
   const int cols = a.E / (2 * kPairs<T>);
   int64_t len = (int64_t)a.B * a.L * cols / (152 * 256) / 4 * 4;
-  len = len < 8 ? 8 : len > 64 ? 64 : len;
+  len = len < 8 ? 8 : len > 128 ? 128 : len;
   const int run_len = static_cast<int>(len);
   const int runs = a.L > 0 ? (a.L + run_len - 1) / run_len : 1;
   const int64_t n = (int64_t)a.B * runs * cols;
