@@ -486,8 +486,9 @@ LA_API la_status_t la_decode_selective(const void *x, const void *dt, const floa
  * and dh0 fp32.  dD, ddt_bias and dh0 may be NULL and need their input; dz is
  * given exactly when z is.  A batch padded at the end is handled by zero rows
  * of dy (a later token does not reach an earlier one).  The workspace is about
- * B*L*E*(2N + 3)/16 + 2*B*L*N*E*N/1024 floats (parts of 64 tokens, 32 for
- * N = 8).
+ * B*L*E*(N/8 + 2N/64 + N*N/512) floats (11 bytes per token and channel for
+ * N = 16): a state every 8 tokens, two per part of 64 tokens (32 for N = 8),
+ * and the channel tiles' sums of dB and dC.
  */
 LA_API la_status_t la_backward_selective(
     const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,

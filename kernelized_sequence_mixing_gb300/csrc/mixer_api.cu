@@ -83,17 +83,23 @@ cudaMemPool_t workspace_pool() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return nullptr;
   std::lock_guard<std::mutex> lock(mu);
   if (!pools[dev]) {
+    // the first call may be inside a stream capture, which creating a pool
+    // does not touch but a capture's stricter modes would end over
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
     cudaMemPoolProps props = {};
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
-    if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return nullptr;
     uint64_t keep = (uint64_t)1 << 29;
-    if (cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) {
+    bool ok = cudaMemPoolCreate(&pool, &props) == cudaSuccess;
+    if (ok && cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) {
       cudaMemPoolDestroy(pool);
-      return nullptr;
+      ok = false;
     }
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) ok = false;
+    if (!ok) return nullptr;
     pools[dev] = pool;
   }
   return pools[dev];

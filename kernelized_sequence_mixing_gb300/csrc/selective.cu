@@ -462,7 +462,7 @@ template <typename T, int N, int MODE>
 cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &rec, int S,
                         int part_len, cudaStream_t s) {
   using Sh = Shape<N, MODE>;
-  ScanMaps maps;
+  ScanMaps maps = {};
   if (!make_scan_maps(&maps, a, dy, sizeof(T), Sh::CT, Sh::TT)) return cudaErrorInvalidValue;
   constexpr int smem = sizeof(Smem<T, N, MODE>);
   unsigned int *timeouts = wait_timeout_counter();

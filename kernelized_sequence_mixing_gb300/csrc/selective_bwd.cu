@@ -552,7 +552,7 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   unsigned int *timeouts = wait_timeout_counter();
   if (!timeouts) return cudaErrorUnknown;
   using Sh = MainShape<T, N>;
-  ScanMaps maps;
+  ScanMaps maps = {};
   if (!make_scan_maps(&maps, a, g.dy, sizeof(T), Sh::CT, Sh::TT)) return cudaErrorInvalidValue;
   scan_bwd_main_kernel<T, N><<<(unsigned)((int64_t)a.B * z.S * tiles), kThreads, smem, s>>>(
       a, g, maps, rec, z.S, timeouts);

@@ -529,3 +529,105 @@ def test_long_offsets(la):
     assert torch.equal(y[1, -63:], part[0, 1:])
     o, r = la.forward_norm_residual(x.view(-1, E))
     assert torch.equal(r[-3:], x.view(-1, E)[-3:])
+
+
+@pytest.mark.parametrize("what", ["scan", "scan backward", "conv backward", "norm backward"])
+def test_first_call_inside_a_capture(la, what):
+    """A fresh process whose first call of all is captured, then replayed."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = f"""
+import torch
+import kernelized_sequence_mixing_gb300 as la
+f = lambda *s: torch.randn(*s, device="cuda")
+B, L, E, N = 1, 600, 64, 16
+x, dt, A, Bm, Cm, dy, w = f(B, L, E), f(B, L, E), -torch.rand(E, N, device="cuda"), f(B, L, 1, N), f(B, L, 1, N), \
+    f(B, L, E), f(E, 4)
+call = {{"scan": lambda: la.forward_selective(x, dt, A, Bm, Cm),
+        "scan backward": lambda: la.backward_selective(x, dt, A, Bm, Cm, dy)[0],
+        "conv backward": lambda: la.backward_conv(x, w, dy)[0],
+        "norm backward": lambda: la.backward_norm_residual(x, dy, w=A[:, 0].contiguous())[2]}}[{what!r}]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = call()
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(got, call())
+print("equal")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-1500:]
+
+
+def plain_step(a, more, h):
+    """One token in 64 bits on the GPU (many sequences)."""
+    d = {k: v.double() for k, v in {**a, **more}.items()}
+    E = d["x"].shape[1]
+    rep = lambda m: m.repeat_interleave(E // m.shape[1], 1)  # noqa: E731
+    step = torch.logaddexp(d["dt"] + d["dt_bias"], torch.zeros((), dtype=torch.float64, device="cuda"))
+    new = torch.exp(step[..., None] * d["A"]) * h.double() + (step * d["x"])[..., None] * rep(d["Bm"])
+    return ((new * rep(d["Cm"])).sum(-1) + d["D"] * d["x"]) * d["z"] * torch.sigmoid(d["z"]), new
+
+
+def test_many_sequences(la):
+    """More sequences than a grid has rows, for one token and for short prompts."""
+    B, E, N = 140000, 8, 8
+    a, more, d = scan_inputs(F32, (B,), E, N, 1, 4)
+    a, more = dev(a), dev(more)
+    h = torch.randn(B, E, N, device="cuda")
+    hc = h.clone()
+    y = la.decode_selective(**a, h=hc, **more)
+    ry, rh = plain_step(a, more, h)
+    assert float((hc - rh).abs().max()) < 400 * 2.0 ** -24 * float(rh.abs().max())
+    assert float((y - ry).abs().max()) < 400 * 2.0 ** -24 * float(ry.abs().max()) + 400 * 2.0 ** -24 * 30
+    seq = {k: (v[:, None] if k in ("x", "dt", "Bm", "Cm", "z") else v) for k, v in {**a, **more}.items()}
+    y2, h2 = la.forward_selective(**seq, h0=h, return_state=True)
+    assert float((h2 - rh).abs().max()) < 400 * 2.0 ** -24 * float(rh.abs().max())
+    w, st = torch.randn(E, 4, device="cuda"), torch.randn(B, 3, E, device="cuda")
+    full = (torch.cat((st, a["x"][:, None]), 1).double() * w.t().double()).sum(1)
+    yc = la.decode_conv(a["x"], w, st, silu=False)
+    assert float((yc - full).abs().max()) < 16 * 2.0 ** -24 * 60
+    assert torch.equal(st[:, 2], a["x"])
+
+
+@pytest.mark.parametrize("N", [8, 16, 64])
+def test_long_sequence(la, N):
+    """The largest number of parts, and its gradients."""
+    B, L, E = 1, 9001, 16
+    a, more, d = scan_inputs(F32, (B, L), E, N, 1, N)
+    y, h = la.forward_selective(**dev(a), **dev(more), return_state=True)
+    (ry, rh), (my, mh) = scan_ref(a, more, True)
+    # a state forgets: with decays of at most exp(-0.05 x 0.003) its memory is under 7000 tokens
+    close("scan long y", y, ry, my, 80 * 7000, F32)
+    close("scan long state", h, rh, mh, 80 * 7000, F32)
+    assert float((y.double() - torch.from_numpy(ry).cuda()).norm() / np.linalg.norm(ry)) < 2e-5
+    dy = d(B, L, E)
+    got = la.backward_selective(**dev(a), dy=dy.cuda(), **dev(more))
+    ref = osel.scan_backward(**host(a), **host(more), dy=dy.numpy())
+    for name, v in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias"), got):
+        assert np.linalg.norm(n64(v) - ref[name]) <= 2e-5 * np.linalg.norm(ref[name]), name
+
+
+def test_wide_batches_of_groups(la):
+    """Many channel tiles and groups, with tails, against the parts alone: a
+    group's channels give the same bits as that group on its own."""
+    B, L, E, N, G = 2, 100, 1200, 16, 3
+    a, more, d = scan_inputs(BF16, (B, L), E, N, G, 6)
+    a, more, dy = dev(a), dev(more), d(B, L, E).cuda()
+    y = la.forward_selective(**a, **more)
+    got = la.backward_selective(**a, dy=dy, **more)
+    for g in range(G):
+        c = slice(g * E // G, (g + 1) * E // G)
+        one = {k: (v[..., c].contiguous() if k in ("x", "dt", "D", "z", "dt_bias") else
+                   v[c].contiguous() if k == "A" else v[:, :, g:g + 1].contiguous())
+               for k, v in {**a, **more}.items()}
+        assert torch.equal(la.forward_selective(**one), y[..., c])
+        part = la.backward_selective(**one, dy=dy[..., c].contiguous())
+        for i, v in enumerate(part):
+            if v is None:
+                continue
+            whole = got[i][:, :, g:g + 1] if i in (3, 4) else got[i][c] if i in (2, 5, 7) else got[i][..., c]
+            assert torch.equal(v, whole), i
