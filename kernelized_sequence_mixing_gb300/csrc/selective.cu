@@ -46,19 +46,24 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 32;
+constexpr int kMaxParts = 128;
+// As many CTAs run whole sequences: 256 of them (B8 L2048 E4096 N16, bf16) take
+// 392 us and in parts 467, 192 of them 391 and 350.
+constexpr int kWhole = 224;
 constexpr int kCheckpoint = kScanCheckpoint;
-constexpr int kLocalTile = 1024;
 constexpr int kSlots = 2;    // parts of y, at most
 
 // The passes over the tokens: a part's end state; y; or, for the backward
 // pass, a part's end state with checkpoints and its adjoint contribution.
 enum { kStates = 0, kOut = 1, kLocal = 2 };
 
-template <int N, int MODE>
+template <typename T, int N, int MODE>
 struct Shape {
-  // (token, channel) pairs of a tile, at most
-  static constexpr int kTile = MODE == kLocal ? kLocalTile : 2048;
+  // (token, channel) pairs of a tile, at most.  The local pass has one more
+  // input to hold: with 2048 pairs two of its CTAs fewer fit an SM (472 us for
+  // the backward pass against 461).  The others gain by the larger tile (144
+  // against 135 us in bf16, 115 against 107 us in fp32).
+  static constexpr int kTile = MODE == kLocal ? 1024 : 2048;
   static constexpr int LN = N / 4;         // lanes that share a channel's states
   static constexpr int LC = 32 / LN;       // channel quads per warp
   static constexpr int CPW = LC * 4;       // channels per warp
@@ -77,7 +82,7 @@ struct Shape {
 // A tile as loaded.
 template <typename T, int N, int MODE>
 struct Stage {
-  using S = Shape<N, MODE>;
+  using S = Shape<T, N, MODE>;
   alignas(128) T x[S::TILE];
   alignas(128) T dt[S::TILE];
   alignas(128) T B[S::TT * N];
@@ -88,7 +93,7 @@ struct Stage {
 
 template <typename T, int N, int MODE>
 struct Smem {
-  using S = Shape<N, MODE>;
+  using S = Shape<T, N, MODE>;
   Stage<T, N, MODE> stage[2];
   alignas(16) float dt[S::TILE];
   // dt x; in the output pass y's first parts take its place, then the others
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                 const __grid_constant__ ScanRecords rec, int S, int part_len,
                 unsigned int *timeouts) {
   constexpr bool OUT = MODE == kOut, LOCAL = MODE == kLocal;
-  using Sh = Shape<N, MODE>;
+  using Sh = Shape<T, N, MODE>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Smem<T, N, MODE> &sm = *reinterpret_cast<Smem<T, N, MODE> *>(smem_raw);
 
@@ -192,26 +197,32 @@ __global__ void __launch_bounds__(kThreads, 4)
       }
   }
   if constexpr (OUT) {
-    // the state before this part: the records of the parts before it
-    for (int q = 0; q < part; ++q) {
-      const int64_t rc = ((int64_t)b * (S - 1) + q) * a.E + e0 + c0;
-      float4 r[4];
-      float sd[4];
+    // the state before this part: the records of the parts before it, four
+    // loaded at a time (one at a time each costs a memory latency)
+    constexpr int kFold = 4;
+    for (int q0 = 0; q0 < part; q0 += kFold) {
+      float4 r[kFold][4], sd[kFold];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool in = c0 + c < nch;
-        r[c] = in ? *reinterpret_cast<const float4 *>(rec.h + (rc + c) * N + n0)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        sd[c] = in ? rec.dt[rc + c] : 0.f;
+      for (int k = 0; k < kFold; ++k) {
+        const int64_t rc = ((int64_t)b * (S - 1) + q0 + k) * a.E + e0 + c0;
+        const bool in = q0 + k < part && c0 < nch;  // widths are multiples of 8
+        sd[k] = in ? *reinterpret_cast<const float4 *>(rec.dt + rc) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          r[k][c] = in ? *reinterpret_cast<const float4 *>(rec.h + (rc + c) * N + n0)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const f2 s2 = pack2(sd[2 * c], sd[2 * c + 1]);
-        const float4 lo = r[2 * c], hi = r[2 * c + 1];
-        h[c][0] = fma2(ex2_2(mul2(s2, A[c][0])), h[c][0], pack2(lo.x, hi.x));
-        h[c][1] = fma2(ex2_2(mul2(s2, A[c][1])), h[c][1], pack2(lo.y, hi.y));
-        h[c][2] = fma2(ex2_2(mul2(s2, A[c][2])), h[c][2], pack2(lo.z, hi.z));
-        h[c][3] = fma2(ex2_2(mul2(s2, A[c][3])), h[c][3], pack2(lo.w, hi.w));
+      for (int k = 0; k < kFold; ++k) {  // a record of zeros leaves h as it is
+        const f2 s2[2] = {pack2(sd[k].x, sd[k].y), pack2(sd[k].z, sd[k].w)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float4 lo = r[k][2 * c], hi = r[k][2 * c + 1];
+          h[c][0] = fma2(ex2_2(mul2(s2[c], A[c][0])), h[c][0], pack2(lo.x, hi.x));
+          h[c][1] = fma2(ex2_2(mul2(s2[c], A[c][1])), h[c][1], pack2(lo.y, hi.y));
+          h[c][2] = fma2(ex2_2(mul2(s2[c], A[c][2])), h[c][2], pack2(lo.z, hi.z));
+          h[c][3] = fma2(ex2_2(mul2(s2[c], A[c][3])), h[c][3], pack2(lo.w, hi.w));
+        }
       }
     }
   }
@@ -461,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 template <typename T, int N, int MODE>
 cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &rec, int S,
                         int part_len, cudaStream_t s) {
-  using Sh = Shape<N, MODE>;
+  using Sh = Shape<T, N, MODE>;
   ScanMaps maps = {};
   if (!make_scan_maps(&maps, a, dy, sizeof(T), Sh::CT, Sh::TT)) return cudaErrorInvalidValue;
   constexpr int smem = sizeof(Smem<T, N, MODE>);
@@ -509,6 +520,19 @@ cudaError_t local_states(const ScanArgs &a, const void *dy, const ScanRecords &r
     case 64: return launch_scan<T, 64, kLocal>(a, dy, rec, S, part_len, s);
   }
   return cudaErrorNotSupported;
+}
+
+// CTAs of the output pass that an SM holds: four by registers, fewer by
+// shared memory.
+template <typename T, int N>
+constexpr int resident_ctas() {
+  constexpr int n = 227 * 1024 / (sizeof(Smem<T, N, kOut>) + 1024);
+  return n < 4 ? n : 4;
+}
+template <typename T>
+int resident(int N) {
+  return N == 8 ? resident_ctas<T, 8>() : N == 16 ? resident_ctas<T, 16>()
+         : N == 32 ? resident_ctas<T, 32>() : resident_ctas<T, 64>();
 }
 
 // One token, in place on the fp32 state.  Bound by the state's bytes (8 per
@@ -599,11 +623,16 @@ int selective_part_len(int L, int S) {
   return (l + 15) / 16 * 16;
 }
 
-int selective_parts(int B, int L, int E, int N, int G) {
+int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged) {
   const int CT = 2048 / N;  // channels per CTA
   const int64_t ctas = (int64_t)B * G * ((E / G + CT - 1) / CT);
-  // about four CTAs per SM; parts of at least 128 tokens
-  int64_t S = (152 * 4) / (ctas > 0 ? ctas : 1);
+  if (ctas >= kWhole) return 1;
+  // one wave of the output pass; parts of at least 128 tokens
+  int64_t S = (int64_t)152 * (dt == kF32 ? resident<float>(N) : resident<__nv_bfloat16>(N)) /
+              (ctas > 0 ? ctas : 1);
+  // some parts of a ragged batch are empty: a third more of them (three fp32
+  // prompts of 8191, 5461 and 2731 tokens: 106 us against 117)
+  if (ragged) S = S * 4 / 3;
   const int most = L / 128 < kMaxParts ? L / 128 : kMaxParts;
   if (S > most) S = most;
   if (S < 2) return 1;
