@@ -33,6 +33,7 @@
 // over states cross N/4 lanes two tokens at a time, sums over channels the
 // other lanes, both by transposing exchanges, then the CTA's warps in shared
 // memory.
+#include "column_sum.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
 #include "scan_maps.cuh"
@@ -478,24 +479,45 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 // -------------------------------------------------------------------- sums
 
-// dB, dC of a token and group: the channel tiles' records in order.
+struct SumBlocks {
+  int64_t bc, dA;  // blocks of each kind, in this order; the rest are dD and d(dt_bias)
+};
+
+// All the sums in one launch, so that they share the machine: a block adds
+// either four values of dB or dC per thread over a group's channel tiles, or
+// 128 columns of dA, or of dD and d(dt_bias), over the parts.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    scan_bwd_bc_kernel(const float *__restrict__ bc, T *__restrict__ dB, T *__restrict__ dC, int B,
-                       int L, int G, int N, int gtiles) {
-  const int64_t per = (int64_t)L * 2 * N;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)B * G * per) return;
+    scan_bwd_sum_kernel(const __grid_constant__ ScanArgs a, const __grid_constant__ ScanGrads g,
+                        const __grid_constant__ BwdRecords rec, int S, int gtiles, SumBlocks nb) {
+  __shared__ float4 sh[kWideSlices][kWideVecs];
+  const int64_t block = blockIdx.x;
+  if (block >= nb.bc + nb.dA) {
+    column_sum_wide(rec.cols, a.B * S, 2 * (int64_t)a.E, g.dD, a.E, g.ddt_bias, block - nb.bc - nb.dA, sh);
+    return;
+  }
+  if (block >= nb.bc) {
+    const int64_t C = (int64_t)a.E * a.N;
+    column_sum_wide(rec.dA, a.B * S, C, g.dA, C, nullptr, block - nb.bc, sh);
+    return;
+  }
+  const int N = a.N;
+  const int64_t per = (int64_t)a.L * 2 * N;
+  const int64_t i = (block * 256 + threadIdx.x) * 4;
+  if (i >= (int64_t)a.B * a.G * per) return;
   const int64_t bg = i / per, tk = i - bg * per;
-  const float *p = bc + bg * gtiles * per + tk;
-  float s = 0.f;
+  const float *p = rec.bc + bg * gtiles * per + tk;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int k = 0; k < gtiles; ++k) s += p[k * per];
+  for (int k = 0; k < gtiles; ++k) {
+    const float4 v = *reinterpret_cast<const float4 *>(p + k * per);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
   const int64_t t = tk / (2 * N);
   const int k = static_cast<int>(tk - t * 2 * N);
-  const int64_t b = bg / G, g = bg - b * G;
-  const int64_t o = ((b * L + t) * G + g) * N + (k < N ? k : k - N);
-  io<T>::store((k < N ? dB : dC) + o, s);
+  const int64_t b = bg / a.G, gi = bg - b * a.G;
+  const int64_t o = ((b * a.L + t) * a.G + gi) * N + (k < N ? k : k - N);
+  store4(static_cast<T *>(k < N ? g.dBm : g.dCm) + o, s);
 }
 
 int bwd_part_tokens(int N) { return N == 8 ? 32 : 64; }
@@ -557,15 +579,12 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   scan_bwd_main_kernel<T, N><<<(unsigned)((int64_t)a.B * z.S * tiles), kThreads, smem, s>>>(
       a, g, maps, rec, z.S, timeouts);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.L > 0) {
-    const int64_t nbc = (int64_t)a.B * a.G * a.L * 2 * N;
-    scan_bwd_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, s>>>(
-        rec.bc, static_cast<T *>(g.dBm), static_cast<T *>(g.dCm), a.B, a.L, a.G, N, tiles / a.G);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  e = launch_column_sum(rec.dA, a.B * z.S, (int64_t)a.E * N, g.dA, (int64_t)a.E * N, nullptr, s);
-  if (e != cudaSuccess || (!g.dD && !g.ddt_bias)) return e;
-  return launch_column_sum(rec.cols, a.B * z.S, 2 * (int64_t)a.E, g.dD, a.E, g.ddt_bias, s);
+  SumBlocks nb;
+  nb.bc = ((int64_t)a.B * a.G * a.L * 2 * N / 4 + 255) / 256;
+  nb.dA = ((int64_t)a.E * N + kWideCols - 1) / kWideCols;
+  const int64_t cols = g.dD || g.ddt_bias ? (2 * (int64_t)a.E + kWideCols - 1) / kWideCols : 0;
+  scan_bwd_sum_kernel<T><<<(unsigned)(nb.bc + nb.dA + cols), 256, 0, s>>>(a, g, rec, z.S, tiles / a.G, nb);
+  return cudaGetLastError();
 }
 
 template <typename T>
