@@ -42,16 +42,21 @@ struct RowArgs {
   int H, D, L;
   float eps, scale;
   bool heads_first;
-  int hb;                 // heads of a CTA's rows: a power of two that divides H
+  int hs;                 // a CTA's rows are 2^hs heads (which divide H) of its tokens
 };
 
-// Element offset of row (token j, head h) in y.  Rows count less than 2^31,
-// so that 32-bit divisions do.
-__device__ __forceinline__ int64_t y_offset(const RowArgs &a, unsigned j, int h) {
-  if (!a.heads_first) return (int64_t)(j * a.H + h) * a.D;
-  const unsigned b = j / (unsigned)a.L, t = j - b * a.L;
-  return ((int64_t)(b * a.H + h) * a.L + t) * a.D;
-}
+// Where token j (of batch entry b, at t in it) of head h lies: in y, and in the
+// token-major tensors.  Rows count less than 2^31.
+struct Row {
+  unsigned j, b, t;
+  int h;
+  __device__ __forceinline__ int64_t off(const RowArgs &a) const {
+    return (int64_t)(j * a.H + h) * a.D;
+  }
+  __device__ __forceinline__ int64_t y_off(const RowArgs &a) const {
+    return a.heads_first ? ((int64_t)(b * a.H + h) * a.L + t) * a.D : off(a);
+  }
+};
 
 // Sum over a row's LANES lanes (LANES = kThreads: the CTA; `sh` has room for
 // two rounds, `round` alternates so that one barrier per sum is enough).
@@ -78,22 +83,8 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*sh)[K][kThreads /
   }
 }
 
-// The row of group `grp` of this CTA, `turn` groups of rows on: its head and
-// token.  CTAs go over the head blocks first.
-struct Row {
-  int h;
-  unsigned j;
-};
-__device__ __forceinline__ Row first_row(const RowArgs &a, int grp, int rows_per_cta, int turn_rows,
-                                         unsigned block) {
-  Row r;
-  const unsigned hblocks = a.H / a.hb;
-  const unsigned tb = hblocks == 1 ? block : block / hblocks;
-  r.h = static_cast<int>(block - tb * hblocks) * a.hb + (grp & (a.hb - 1));
-  r.j = tb * (rows_per_cta / a.hb) + (grp / a.hb) + turn_rows;
-  return r;
-}
-
+// CTAs go over the head blocks first.  The divisions are the CTA's: a thread
+// steps from its first token.
 template <typename T, int MODE, int LANES, int VPT>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ RowArgs a) {
   constexpr int GPC = kThreads / LANES;
@@ -105,15 +96,24 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   raw8<T> rp[R][VPT], rg[R][VPT];
   int64_t off[R];
   bool live[R];
-  int h = 0;
+  const unsigned hblocks = (unsigned)a.H >> a.hs;
+  const unsigned tb = hblocks == 1 ? blockIdx.x : blockIdx.x / hblocks;
+  const unsigned j0 = tb * (GPC * R >> a.hs);
+  const unsigned b0 = MODE == kResidual ? 0u : j0 / (unsigned)a.L, i0 = j0 - b0 * (unsigned)a.L;
+  const int h = static_cast<int>(((blockIdx.x - tb * hblocks) << a.hs) + (grp & ((1 << a.hs) - 1)));
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const Row row = first_row(a, grp, GPC * R, r * (GPC / a.hb), blockIdx.x);
-    h = row.h;
+    const unsigned step = (grp >> a.hs) + r * (GPC >> a.hs);
+    Row row = {j0 + step, b0, i0 + step, h};
+    if (MODE != kResidual)
+      while (row.t >= (unsigned)a.L) {
+        row.t -= a.L;
+        ++row.b;
+      }
     live[r] = row.j < a.tokens;
-    off[r] = live[r] ? (int64_t)(row.j * a.H + h) * a.D : 0;
+    off[r] = live[r] ? row.off(a) : 0;
     const T *in1 = static_cast<const T *>(a.in1) +
-                   (MODE == kResidual || !live[r] ? off[r] : y_offset(a, row.j, h));
+                   (MODE == kResidual || !live[r] ? off[r] : row.y_off(a));
     const T *in2 = static_cast<const T *>(a.in2) + off[r];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -169,8 +169,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   }
 }
 
-// hb heads per CTA (blockIdx.x % (H / hb)); its row groups stride over the
-// tokens.
+// 2^hs heads per CTA; its row groups stride over the tokens.
 template <typename T, int MODE, int LANES, int VPT>
 __global__ void __launch_bounds__(kThreads)
     norm_bwd_kernel(const __grid_constant__ RowArgs a, int slots) {
@@ -178,9 +177,10 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float sh[2][2][kThreads / 32];
   int round = 0;
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const int hblocks = a.H / a.hb, slot = blockIdx.x / hblocks, h0 = blockIdx.x % hblocks * a.hb;
-  const int h = h0 + (grp & (a.hb - 1));
-  const int tpc = GPC / a.hb;  // tokens of a turn
+  const unsigned hblocks = (unsigned)a.H >> a.hs, slot = blockIdx.x / hblocks;
+  const int h0 = static_cast<int>((blockIdx.x - slot * hblocks) << a.hs);
+  const int h = h0 + (grp & ((1 << a.hs) - 1));
+  const unsigned tpc = GPC >> a.hs;  // tokens of a turn
   f2 w[VPT][4], dw[VPT][4];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -200,12 +200,28 @@ __global__ void __launch_bounds__(kThreads)
     int64_t off, yoff;
     bool live;
   };
-  auto fetch = [&](unsigned j0, Rows &r) {
-    const unsigned j = j0 + grp / a.hb;
-    r.live = j < a.tokens;
-    const unsigned jj = r.live ? j : 0u;
-    r.off = (int64_t)(jj * a.H + h) * a.D;
-    r.yoff = MODE == kResidual ? r.off : y_offset(a, jj, h);
+  const unsigned stride = slots * tpc;
+  Row row = {slot * tpc + (grp >> a.hs), 0u, 0u, h};
+  unsigned stride_b = 0, stride_t = 0;
+  if (MODE != kResidual) {
+    row.b = row.j / (unsigned)a.L;
+    row.t = row.j - row.b * (unsigned)a.L;
+    stride_b = stride / (unsigned)a.L;
+    stride_t = stride - stride_b * (unsigned)a.L;
+  }
+  auto fetch = [&](Rows &r) {  // the next row of this group
+    r.live = row.j < a.tokens;
+    r.off = r.live ? row.off(a) : 0;
+    r.yoff = MODE == kResidual || !r.live ? r.off : row.y_off(a);
+    row.j += stride;
+    if (MODE != kResidual) {
+      row.b += stride_b;
+      row.t += stride_t;
+      if (row.t >= (unsigned)a.L) {
+        row.t -= a.L;
+        ++row.b;
+      }
+    }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (v * LANES + lane) * 8;
@@ -224,17 +240,16 @@ __global__ void __launch_bounds__(kThreads)
     }
   };
   constexpr bool kPrefetch = VPT == 1;
-  const unsigned stride = slots * tpc;
   Rows cur, nxt;
-  if (kPrefetch) fetch(slot * tpc, nxt);
+  if (kPrefetch) fetch(nxt);
   // every group of the CTA makes the same number of turns (the sums cross
   // lanes of several groups)
   for (unsigned j0 = slot * tpc; j0 < a.tokens; j0 += stride) {
     if (kPrefetch) {
       cur = nxt;
-      fetch(j0 + stride, nxt);
+      fetch(nxt);
     } else {
-      fetch(j0, cur);
+      fetch(cur);
     }
     f2 s0 = dup2(0.f), s1 = dup2(0.f);
 #pragma unroll
@@ -315,11 +330,12 @@ __global__ void __launch_bounds__(kThreads)
       __syncthreads();
       store8p(&part[grp][lane * 8], dw[v]);
       __syncthreads();
-      for (int i = threadIdx.x; i < a.hb * LANES * 8; i += kThreads) {
+      const int hb = 1 << a.hs;
+      for (int i = threadIdx.x; i < hb * LANES * 8; i += kThreads) {
         const int hh = i / (LANES * 8), k = i % (LANES * 8), c = v * LANES * 8 + k;
         if (c < a.D) {
           float q = part[hh][k];
-          for (int g = hh + a.hb; g < GPC; g += a.hb) q += part[g][k];
+          for (int g = hh + hb; g < GPC; g += hb) q += part[g][k];
           rec[(int64_t)hh * a.D + c] = q;
         }
       }
@@ -344,19 +360,20 @@ cudaError_t by_width(int D, F &&f) {
 
 int lanes_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 1024 ? 32 : 256; }
 
-// Heads of a CTA's rows: up to four, as many as divide H and fit its groups.
-int head_block(int H, int D) {
+// Heads of a CTA's rows, as a power of two: up to four, as many as divide H
+// and fit its groups.
+int head_shift(int H, int D) {
   const int gpc = kThreads / lanes_of(D);
-  int hb = 4;
-  while (hb > gpc || H % hb) hb /= 2;
-  return hb;
+  int s = 2;
+  while ((1 << s) > gpc || H % (1 << s)) --s;
+  return s;
 }
 
 // CTAs per head block of a backward pass: about three per SM over all blocks
 // (8191 rows of 2048 in bf16: 37 us, with two 39, four 42),
 // no more than there are rows for.
 int bwd_slots(int64_t tokens, int H, int D) {
-  const int hb = head_block(H, D), tpc = kThreads / lanes_of(D) / hb, blocks = H / hb;
+  const int hs = head_shift(H, D), tpc = (kThreads / lanes_of(D)) >> hs, blocks = H >> hs;
   const int64_t most = (tokens + tpc - 1) / tpc;
   int64_t n = (152 * 3 + blocks - 1) / blocks;
   if (n > most) n = most;
@@ -368,8 +385,8 @@ cudaError_t run_rows(const RowArgs &a, cudaStream_t s) {
   return by_width(a.D, [&](auto lanes, auto vpt) {
     constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
     constexpr int R = VPT == 1 && LANES < 256 ? 2 : 1;
-    const int tpc = kThreads / LANES * R / a.hb;  // tokens per CTA
-    const int64_t ctas = ((int64_t)a.tokens + tpc - 1) / tpc * (a.H / a.hb);
+    const int tpc = (kThreads / LANES * R) >> a.hs;  // tokens per CTA
+    const int64_t ctas = ((int64_t)a.tokens + tpc - 1) / tpc * (a.H >> a.hs);
     norm_kernel<T, MODE, LANES, VPT><<<(unsigned)ctas, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   });
@@ -380,7 +397,7 @@ cudaError_t run_rows_bwd(const RowArgs &a, float *dw, cudaStream_t s) {
   const int slots = bwd_slots(a.tokens, a.H, a.D);
   cudaError_t e = by_width(a.D, [&](auto lanes, auto vpt) {
     constexpr int LANES = decltype(lanes)::value, VPT = decltype(vpt)::value;
-    norm_bwd_kernel<T, MODE, LANES, VPT><<<(unsigned)(slots * (a.H / a.hb)), kThreads, 0, s>>>(a, slots);
+    norm_bwd_kernel<T, MODE, LANES, VPT><<<(unsigned)(slots * (a.H >> a.hs)), kThreads, 0, s>>>(a, slots);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !dw) return e;
@@ -397,7 +414,7 @@ RowArgs gate_rows(const NormGateArgs &n) {
   a.H = n.H;
   a.D = n.D;
   a.L = n.L;
-  a.hb = head_block(n.H, n.D);
+  a.hs = head_shift(n.H, n.D);
   a.eps = n.eps;
   a.heads_first = n.heads_first;
   return a;
@@ -410,7 +427,7 @@ RowArgs residual_rows(const NormResidualArgs &n) {
   a.H = 1;
   a.D = n.E;
   a.L = 1;
-  a.hb = 1;
+  a.hs = 0;
   a.eps = n.eps;
   a.scale = n.scale;
   return a;
