@@ -369,13 +369,14 @@ int head_shift(int H, int D) {
   return s;
 }
 
-// CTAs per head block of a backward pass: about three per SM over all blocks
-// (8191 rows of 2048 in bf16: 37 us, with two 39, four 42),
-// no more than there are rows for.
+// CTAs per head block of a backward pass: about two per SM over all blocks, no
+// more than there are rows for.  More of them hide more latency but leave more
+// records to add: B4 H8 L4096 D64 takes 16.0, 17.0 and 19.3 us with two, four
+// and six, 8191 rows of 2048 take 35.9, 37.8 and 35.2 (bf16, both kernels).
 int bwd_slots(int64_t tokens, int H, int D) {
   const int hs = head_shift(H, D), tpc = (kThreads / lanes_of(D)) >> hs, blocks = H >> hs;
   const int64_t most = (tokens + tpc - 1) / tpc;
-  int64_t n = (152 * 3 + blocks - 1) / blocks;
+  int64_t n = (152 * 2 + blocks - 1) / blocks;
   if (n > most) n = most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
