@@ -1,6 +1,7 @@
 // Sums of fp32 records over the record index, in a fixed order (the second
 // stage of the parameter gradients).
 #include "column_sum.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 
 namespace linattn {
@@ -16,6 +17,7 @@ __global__ void __launch_bounds__(kCols * kSlices)
   const int tx = threadIdx.x % kCols, ty = threadIdx.x / kCols;
   const int64_t c = (int64_t)blockIdx.x * kCols + tx;
   float s = 0.f;
+  wait_for_previous();
   if (c < C) {
 #pragma unroll 8
     for (int r = ty; r < n; r += kSlices) s += rec[r * C + c];
@@ -32,9 +34,8 @@ __global__ void __launch_bounds__(kCols * kSlices)
 
 cudaError_t launch_column_sum(const float *rec, int n, int64_t C, float *out0, int64_t C0,
                               float *out1, cudaStream_t s) {
-  column_sum_kernel<<<(unsigned)((C + kCols - 1) / kCols), kCols * kSlices, 0, s>>>(rec, n, C, out0,
-                                                                                    C0, out1);
-  return cudaGetLastError();
+  return launch_dependent(column_sum_kernel, (unsigned)((C + kCols - 1) / kCols), 1, kCols * kSlices, 0, s,
+                          rec, n, C, out0, C0, out1);
 }
 
 }  // namespace linattn

@@ -187,7 +187,8 @@ cudaError_t launch_backward_tc(const Problem &p, const void *dO, void *dq, void 
                                const Gammas &g, void *ws, cudaStream_t s);
 
 // out0[c] (c < C0) and out1[c - C0] (the rest; may be null) = sum of rec[r][c]
-// over the n records of C columns, in a fixed order (column_sum.cu).
+// over the n records of C columns, in a fixed order (column_sum.cu).  To be
+// launched right behind the kernel that writes the records.
 cudaError_t launch_column_sum(const float *rec, int n, int64_t C, float *out0, int64_t C0,
                               float *out1, cudaStream_t s);
 

@@ -22,6 +22,7 @@
 // are added in their order.
 #include <type_traits>
 
+#include "dependent.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
 
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 template <typename T, int MODE, int LANES, int VPT>
 __global__ void __launch_bounds__(kThreads)
     norm_bwd_kernel(const __grid_constant__ RowArgs a, int slots) {
+  let_next_start();
   constexpr int GPC = kThreads / LANES;
   __shared__ float sh[2][2][kThreads / 32];
   int round = 0;

@@ -37,6 +37,7 @@
 // pass leaves every part but the last its end state from zero and its sum of
 // dt (the part's decay is exp(A sum dt): no product is kept), and the output
 // pass folds the records before its part in front of its own scan.
+#include "dependent.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
 #include "scan_maps.cuh"
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                 const __grid_constant__ ScanRecords rec, int S, int part_len,
                 unsigned int *timeouts) {
   constexpr bool OUT = MODE == kOut, LOCAL = MODE == kLocal;
+  if constexpr (!OUT) let_next_start();
   using Sh = Shape<T, N, MODE>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Smem<T, N, MODE> &sm = *reinterpret_cast<Smem<T, N, MODE> *>(smem_raw);
@@ -170,6 +172,27 @@ __global__ void __launch_bounds__(kThreads, 4)
 
   const bool gated = MODE != kStates && a.z;
   T *y = OUT ? static_cast<T *>(a.y) + (int64_t)b * a.L * a.E + e0 : nullptr;
+
+  // The tile at token tb.  A box may reach behind the part's end, the
+  // sequence's or the group's: those rows are cleared when staged, those
+  // channels belong to lanes that store nothing.
+  auto issue = [&](int tb, int st) {
+    if (tid != 0) return;
+    Stage<T, N, MODE> &g = sm.stage[st];
+    uint64_t *bar = &sm.full[st];
+    constexpr uint32_t rows = Sh::TILE * sizeof(T), bc = Sh::TT * N * sizeof(T);
+    tc::mbar_arrive_expect_tx(
+        bar, (2 + (gated ? 1 : 0) + (LOCAL ? 1 : 0)) * rows + (MODE != kStates ? 2 : 1) * bc);
+    tc::tma_load_3d(g.x, &maps.x, e0, tb, b, bar);
+    tc::tma_load_3d(g.dt, &maps.dt, e0, tb, b, bar);
+    tc::tma_load_3d(g.B, &maps.B, grp * N, tb, b, bar);
+    if constexpr (MODE != kStates) {
+      tc::tma_load_3d(g.C, &maps.C, grp * N, tb, b, bar);
+      if (gated) tc::tma_load_3d(g.z, &maps.z, e0, tb, b, bar);
+    }
+    if constexpr (LOCAL) tc::tma_load_3d(g.dy, &maps.dy, e0, tb, b, bar);
+  };
+  if (t0 < t1) issue(t0, 0);
 
   // this thread's channels and states
   const int c0 = warp * Sh::CPW + lc * 4, n0 = sl * 4;
@@ -200,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     // the state before this part: the records of the parts before it, four
     // loaded at a time (one at a time each costs a memory latency)
     constexpr int kFold = 4;
+    if (part > 0) wait_for_previous();
     for (int q0 = 0; q0 < part; q0 += kFold) {
       float4 r[kFold][4], sd[kFold];
 #pragma unroll
@@ -265,25 +289,6 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (qin && a.dt_bias) load4p(a.dt_bias + e0 + qcol, bias);
   if (OUT && qin && a.D) load4p(a.D + e0 + qcol, dskip);
 
-  // The tile at token tb.  A box may reach behind the part's end, the
-  // sequence's or the group's: those rows are cleared when staged, those
-  // channels belong to lanes that store nothing.
-  auto issue = [&](int tb, int st) {
-    if (tid != 0) return;
-    Stage<T, N, MODE> &g = sm.stage[st];
-    uint64_t *bar = &sm.full[st];
-    constexpr uint32_t rows = Sh::TILE * sizeof(T), bc = Sh::TT * N * sizeof(T);
-    tc::mbar_arrive_expect_tx(
-        bar, (2 + (gated ? 1 : 0) + (LOCAL ? 1 : 0)) * rows + (MODE != kStates ? 2 : 1) * bc);
-    tc::tma_load_3d(g.x, &maps.x, e0, tb, b, bar);
-    tc::tma_load_3d(g.dt, &maps.dt, e0, tb, b, bar);
-    tc::tma_load_3d(g.B, &maps.B, grp * N, tb, b, bar);
-    if constexpr (MODE != kStates) {
-      tc::tma_load_3d(g.C, &maps.C, grp * N, tb, b, bar);
-      if (gated) tc::tma_load_3d(g.z, &maps.z, e0, tb, b, bar);
-    }
-    if constexpr (LOCAL) tc::tma_load_3d(g.dy, &maps.dy, e0, tb, b, bar);
-  };
   struct Operands {
     f2 d[2], u[2], g[2], b[4], c[4];
   };
@@ -316,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 4)
     return o;
   };
 
-  if (t0 < t1) issue(t0, 0);
   int turn = 0;
   for (int tb = t0; tb < t1; tb += Sh::TT, ++turn) {
     const int st = turn & 1, rows = min(Sh::TT, t1 - tb);
@@ -482,6 +486,9 @@ cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &re
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
   const int64_t ctas = a.B * (MODE == kStates ? S - 1 : S) * tiles;
+  if (MODE == kOut && S > 1)  // behind the state pass
+    return launch_dependent(scan_kernel<T, N, MODE>, (unsigned)ctas, 1, kThreads, smem, s, a, maps, rec, S,
+                            part_len, timeouts);
   scan_kernel<T, N, MODE><<<(unsigned)ctas, kThreads, smem, s>>>(a, maps, rec, S, part_len, timeouts);
   return cudaGetLastError();
 }

@@ -34,6 +34,7 @@
 // other lanes, both by transposing exchanges, then the CTA's warps in shared
 // memory.
 #include "column_sum.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
 #include "scan_maps.cuh"
@@ -62,6 +63,8 @@ struct BwdRecords {
 __global__ void __launch_bounds__(256)
     scan_bwd_carry_kernel(const __grid_constant__ ScanArgs a, const float *__restrict__ dhN,
                           const __grid_constant__ BwdRecords rec, int S) {
+  let_next_start();
+  wait_for_previous();
   const int64_t EN = (int64_t)a.E * a.N;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= a.B * EN) return;
@@ -158,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   *reinterpret_cast<float4 *>(&sm.cols[0][tid * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
   *reinterpret_cast<float4 *>(&sm.cols[1][tid * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
 
+  let_next_start();
   if (tid == 0) {
     tc::mbar_init(&sm.full[0], 1);
     tc::mbar_init(&sm.full[1], 1);
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   };
   f2 A[4], hin[4], gc[4], dA[4];
   load_pair(a.A + en, A, kLog2e);
+  wait_for_previous();
   load_pair(S > 1 ? rec.s.h + pen : a.h0 ? a.h0 + ben : nullptr, hin, 1.f);
   load_pair(S > 1 ? rec.s.g + pen : gr.dhN ? gr.dhN + ben : nullptr, gc, 1.f);
 #pragma unroll
@@ -491,6 +496,7 @@ __global__ void __launch_bounds__(256)
     scan_bwd_sum_kernel(const __grid_constant__ ScanArgs a, const __grid_constant__ ScanGrads g,
                         const __grid_constant__ BwdRecords rec, int S, int gtiles, SumBlocks nb) {
   __shared__ float4 sh[kWideSlices][kWideVecs];
+  wait_for_previous();
   const int64_t block = blockIdx.x;
   if (block >= nb.bc + nb.dA) {
     column_sum_wide(rec.cols, a.B * S, 2 * (int64_t)a.E, g.dD, a.E, g.ddt_bias, block - nb.bc - nb.dA, sh);
@@ -565,8 +571,8 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   }
   if (z.S > 1) {
     const int64_t n = (int64_t)a.B * a.E * N;
-    scan_bwd_carry_kernel<<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, s>>>(a, g.dhN, rec, z.S);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dependent(scan_bwd_carry_kernel, (unsigned)((n + 255) / 256), 2, 256, 0, s, a, g.dhN, rec, z.S);
+    if (e != cudaSuccess) return e;
   }
   const int tiles = bwd_tiles(a.E, N, a.G);
   constexpr int smem = sizeof(MainSmem<T, N>);
@@ -576,15 +582,20 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   using Sh = MainShape<T, N>;
   ScanMaps maps = {};
   if (!make_scan_maps(&maps, a, g.dy, sizeof(T), Sh::CT, Sh::TT)) return cudaErrorInvalidValue;
-  scan_bwd_main_kernel<T, N><<<(unsigned)((int64_t)a.B * z.S * tiles), kThreads, smem, s>>>(
-      a, g, maps, rec, z.S, timeouts);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const unsigned ctas = (unsigned)((int64_t)a.B * z.S * tiles);
+  if (a.L > kScanCheckpoint) {
+    e = launch_dependent(scan_bwd_main_kernel<T, N>, ctas, 1, kThreads, smem, s, a, g, maps, rec, z.S, timeouts);
+  } else {  // the kernel before is the caller's
+    scan_bwd_main_kernel<T, N><<<ctas, kThreads, smem, s>>>(a, g, maps, rec, z.S, timeouts);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   SumBlocks nb;
   nb.bc = ((int64_t)a.B * a.G * a.L * 2 * N / 4 + 255) / 256;
   nb.dA = ((int64_t)a.E * N + kWideCols - 1) / kWideCols;
   const int64_t cols = g.dD || g.ddt_bias ? (2 * (int64_t)a.E + kWideCols - 1) / kWideCols : 0;
-  scan_bwd_sum_kernel<T><<<(unsigned)(nb.bc + nb.dA + cols), 256, 0, s>>>(a, g, rec, z.S, tiles / a.G, nb);
-  return cudaGetLastError();
+  return launch_dependent(scan_bwd_sum_kernel<T>, (unsigned)(nb.bc + nb.dA + cols), 1, 256, 0, s, a, g, rec, z.S,
+                          tiles / a.G, nb);
 }
 
 template <typename T>

@@ -11,6 +11,7 @@
 // of consecutive tokens; the last W - 1 rows stay in registers as a sliding
 // window, so only the first W - 1 rows of a run are read twice (from L2), and
 // the next tokens' loads are issued a group ahead.
+#include "dependent.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
 
@@ -287,6 +288,7 @@ template <typename T, int W>
 __global__ void __launch_bounds__(kBwdCols * kBwdRows)
     conv_bwd_kernel(const __grid_constant__ ConvArgs a, const __grid_constant__ ConvGrads g,
                     float *__restrict__ rec, int run_len, int runs) {
+  let_next_start();
   const int tx = threadIdx.x % kBwdCols, ty = threadIdx.x / kBwdCols;
   const int e = (blockIdx.x * kBwdCols + tx) * 2;
   const bool in = e < a.E;
