@@ -78,6 +78,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load liblinattn.so; raises RuntimeError if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -206,7 +208,7 @@ def _ptr(t):
 def _on(dev):
     """The context of a call on ``dev``: nothing to do where it is the current
     device already (the guard costs more than the rest of a short call)."""
-    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
 
 
 _HERE = contextlib.nullcontext()
@@ -237,7 +239,8 @@ def _one_device(fn, named, allow_host=False):
         if t is not None:
             if dev is None:
                 dev = t.device
-            elif t.device != dev:
+                index = t.get_device()  # an integer: cheaper to compare; -1 is any other device
+            elif t.get_device() != index or (index < 0 and t.device != dev):
                 where = ", ".join(f"{n} on {t.device}" for n, t in named if t is not None)
                 raise ValueError(f"{fn}: all tensors must be on one device ({where})")
     if dev.type not in _DEVICE_TYPES and not allow_host:
@@ -613,13 +616,18 @@ def _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, dims):
     if x.dim() != dims or Bm.dim() != dims + 1 or A.dim() != 2:
         tok = "B, L" if dims == 3 else "B"
         raise ValueError(f"{fn}: expected x, dt: [{tok}, E], A: [E, N] and Bm, Cm: [{tok}, G, N]")
-    _dtype_code(x)
-    lead, E = tuple(x.shape[:-1]), x.shape[-1]
+    dtype = x.dtype
+    if dtype not in _DTYPES:
+        _dtype_code(x)
+    *lead, E = x.shape
+    lead = tuple(lead)
     G, N = Bm.shape[-2:]
-    lds = (_tokens(fn, "x", x, lead, (E,), x.dtype), _tokens(fn, "dt", dt, lead, (E,), x.dtype),
-           _tokens(fn, "z", z, lead, (E,), x.dtype) if z is not None else 0,
-           _tokens(fn, "Bm", Bm, lead, (G, N), x.dtype),
-           _tokens(fn, "Cm", Cm, lead, (G, N), x.dtype))
+    tok, grp = lead + (E,), lead + (G, N)
+    lds = []
+    for name, t, shape in (("x", x, tok), ("dt", dt, tok), ("z", z, tok), ("Bm", Bm, grp), ("Cm", Cm, grp)):
+        # dense rows need no stride; _tokens finds the others' and every fault
+        lds.append(0 if t is None or (t.shape == shape and t.dtype is dtype and t.is_contiguous())
+                   else _tokens(fn, name, t, lead, shape[len(lead):], dtype))
     _param(fn, "A", A, (E, N))
     _param(fn, "D", D, (E,))
     _param(fn, "dt_bias", dt_bias, (E,))
