@@ -12,7 +12,8 @@
 //
 // Backward.  With n = p rstd and dn = do w (act(g)):
 //   dp = rstd (dn - n mean(dn n)) = rstd dn - p rstd^3 sum(dn p) / D,
-// so one joint reduction of sum p^2 and sum dn p serves a row.
+// so one joint reduction of sum p^2 and sum dn p serves a row (rstd^3 alone
+// leaves the fp32 range long before its product with the sum does).
 //
 // Bound by memory: every value is read once into registers and written once.
 // A row belongs to a power of two of lanes, 8 values a lane at a time: part
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
     float s[2] = {sum2(s0), sum2(s1)};
     row_sum<LANES, 2>(s, sh, round);
     const float rs = rsqrtf(fmaf(s[0], invD, a.eps));
-    const f2 rstd = dup2(rs), k = dup2(-rs * rs * rs * s[1] * invD);
+    const f2 rstd = dup2(rs), k = dup2(-rs * (rs * (rs * (s[1] * invD))));
     if (cur.live) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
@@ -378,7 +379,7 @@ int head_shift(int H, int D) {
 int bwd_slots(int64_t tokens, int H, int D) {
   const int hs = head_shift(H, D), tpc = (kThreads / lanes_of(D)) >> hs, blocks = H >> hs;
   const int64_t most = (tokens + tpc - 1) / tpc;
-  int64_t n = (152 * 2 + blocks - 1) / blocks;
+  int64_t n = (kSMs * 2 + blocks - 1) / blocks;
   if (n > most) n = most;
   return n < 1 ? 1 : static_cast<int>(n);
 }

@@ -420,6 +420,74 @@ def test_special_values(la):
     assert torch.equal(bad, clean)
 
 
+@DT
+@pytest.mark.parametrize("gate_first", [False, True], ids=["after", "first"])
+def test_norms_of_extreme_rows(la, dtype, gate_first):
+    """Rows whose rstd cubed leaves the fp32 range: zeros and 2^-45 under a
+    small eps, 2^60 at the other end.  The same roundings as other rows."""
+    eps, D = 2.0 ** -100, 64
+    d = Draw(11, dtype)
+    size = torch.tensor([0, 2.0 ** -45, 2.0 ** 60, 1.0])[:, None]
+    y = (d(1, 2, 4, D, dtype=F32) * size).to(dtype)
+    gate, w, do = d(1, 4, 2 * D), d.f(2, D), d(1, 4, 2 * D)
+    kw = {"eps": eps, "gate_first": gate_first, "heads_first": True}
+    h = host({"y": y, "gate": gate, "w": w})
+    K = D / 8 + 32
+    ref = osel.norm_gate(**h, **kw)
+    close("norm gate extremes o", la.forward_norm_gate(y.cuda(), gate.cuda(), w.cuda(), **kw), ref, np.abs(ref), K, dtype)
+    got = la.backward_norm_gate(y.cuda(), gate.cuda(), do.cuda(), w.cuda(), **kw)
+    ref, mag = [osel.norm_gate_backward(**h, do=do.float().numpy(), **kw, mag=m) for m in (False, True)]
+    for name, v in zip(("dy", "dgate", "dw"), got):
+        close("norm gate extremes " + name, v, ref[name], mag[name], K + (4 if name == "dw" else 0), v.dtype)
+    r, do, w = y[0, 0].contiguous(), d(4, D), d.f(D)
+    got = la.backward_norm_residual(r.cuda(), do.cuda(), w.cuda(), eps=eps)
+    hb = host({"r": r, "do": do, "w": w, "dr": None})
+    ref, mag = [osel.norm_residual_backward(**hb, scale=1.0, eps=eps, mag=m) for m in (False, True)]
+    for name, v in zip(("dresidual", "dx", "dw"), got):
+        close("norm residual extremes " + name, v, ref[name], mag[name], K + (4 if name == "dw" else 0), v.dtype)
+
+
+def test_one_tensor_as_two_inputs(la):
+    """Inputs are only read: a tensor may stand for two of them."""
+    d = Draw(12, BF16)
+    x, bc, A = d(2, 70, 64).cuda(), d(2, 70, 1, 16).cuda(), -torch.rand(64, 16, generator=d.g).cuda()
+    same = {"x": x, "dt": x, "Bm": bc, "Cm": bc, "z": x, "A": A}
+    apart = {k: v.clone() for k, v in same.items()}
+    assert torch.equal(la.forward_selective(**same), la.forward_selective(**apart))
+    for u, v in zip(la.backward_selective(**same, dy=x), la.backward_selective(**apart, dy=x.clone())):
+        assert u is v is None or torch.equal(u, v)
+    assert torch.equal(la.forward_norm_residual(x, x)[0], la.forward_norm_residual(x, x.clone())[0])
+
+
+def test_two_threads(la):
+    """Calls from two host threads at once, each on a stream of its own."""
+    import threading
+    a, more, d = scan_inputs(BF16, (2, 300), 96, 16, 1, 13)
+    args, dy = {**dev(a), **dev(more)}, d(2, 300, 96).cuda()
+    want = la.backward_selective(**args, dy=dy)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got = la.backward_selective(**args, dy=dy)
+                    s.synchronize()
+                    if not all(u is v is None or torch.equal(u, v) for u, v in zip(got, want)):
+                        bad.append("other values")
+        except Exception as e:  # noqa: BLE001 (reported by the assertion)
+            bad.append(repr(e))
+
+    ts = [threading.Thread(target=work) for _ in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad, bad
+
+
 def test_block_prompt_then_tokens(la):
     """The operators together, as a block runs them: convolution, scan, gated
     norm, residual norm over a prompt with its states, then token by token; the
