@@ -7,6 +7,7 @@
 namespace linattn {
 
 constexpr int kMaxHeads = 256;
+constexpr int kSMs = 152;  // of a GB300, for the rules that size grids
 
 // Per-head decay values, passed to kernels by value.
 struct Gammas {

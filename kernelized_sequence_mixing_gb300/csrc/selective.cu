@@ -23,9 +23,10 @@
 //     registers: half the shared-memory wavefronts for 16 moves (441 against
 //     447 us for the whole backward pass at B2 L4096 E2048 N16 in bf16, but
 //     161 against 136 us for the forward pass);
-//   - the sum over states crosses N/4 lanes: each lane stores its part of y
-//     (beyond four lanes after an exchange) and the threads that write y add
-//     the parts, a third of the instructions of a shuffle tree;
+//   - the sum over states crosses N/4 lanes: exchanges that halve a lane's
+//     channels leave two parts of y, stored to shared memory, and the threads
+//     that write y add them (139 us for the forward pass; four parts, without
+//     an exchange at 16 states, cost an SM one of its four CTAs: 157 us);
 //   - softplus, the D term and the gate are applied once per (channel, token)
 //     when a tile of tokens is staged and when it is stored.
 // A tile's inputs come by TMA, one box per tensor, while the previous tile
@@ -61,8 +62,8 @@ enum { kStates = 0, kOut = 1, kLocal = 2 };
 template <typename T, int N, int MODE>
 struct Shape {
   // (token, channel) pairs of a tile, at most.  The local pass has one more
-  // input to hold: with 2048 pairs two of its CTAs fewer fit an SM (472 us for
-  // the backward pass against 461).  The others gain by the larger tile (144
+  // input to hold: with 2048 pairs one of its four CTAs less fits an SM (472 us
+  // for the backward pass against 461).  The others gain by the larger tile (144
   // against 135 us in bf16, 115 against 107 us in fp32).
   static constexpr int kTile = MODE == kLocal ? 1024 : 2048;
   static constexpr int LN = N / 4;         // lanes that share a channel's states
@@ -601,7 +602,7 @@ cudaError_t step_typed(const ScanArgs &a, cudaStream_t s) {
   const unsigned nx = (a.E + PER - 1) / PER;
   // two sequences per thread once that still gives every SM eight CTAs (256 x
   // 4096 channels of 16 states in bf16: 28.9 us; four: 29.6)
-  if ((int64_t)nx * a.B >= 152 * 8 * 2) {
+  if ((int64_t)nx * a.B >= kSMs * 8 * 2) {
     const int ny = (a.B + 1) / 2;
     scan_step_kernel<T, N, 2><<<dim3(nx, ny < kMaxY ? ny : kMaxY), 256, 0, s>>>(a);
   } else {
@@ -635,7 +636,7 @@ int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged) {
   const int64_t ctas = (int64_t)B * G * ((E / G + CT - 1) / CT);
   if (ctas >= kWhole) return 1;
   // one wave of the output pass; parts of at least 128 tokens
-  int64_t S = (int64_t)152 * (dt == kF32 ? resident<float>(N) : resident<__nv_bfloat16>(N)) /
+  int64_t S = (int64_t)kSMs * (dt == kF32 ? resident<float>(N) : resident<__nv_bfloat16>(N)) /
               (ctas > 0 ? ctas : 1);
   // some parts of a ragged batch are empty: a third more of them (three fp32
   // prompts of 8191, 5461 and 2731 tokens: 106 us against 117)

@@ -458,7 +458,7 @@ struct BwdPlan {
 };
 BwdPlan conv_bwd_plan(int B, int L, int E) {
   const int nx = (E / 2 + kBwdCols - 1) / kBwdCols;
-  int rows = 152 * 5 / nx * kBwdRows;  // rows of runs that fit at once
+  int rows = kSMs * 5 / nx * kBwdRows;  // rows of runs that fit at once
   if (rows < kBwdRows) rows = kBwdRows;
   const int per = rows / B > 0 ? rows / B : 1;  // runs per sequence
   BwdPlan p;
@@ -476,7 +476,7 @@ cudaError_t conv_fwd_typed(const ConvArgs &a, cudaStream_t s) {
   // five tokens' work), shorter ones, whole groups of 4, where that leaves
   // fewer than 256 threads per SM
   const int cols = a.E / (2 * kPairs<T>);
-  int64_t len = (int64_t)a.B * a.L * cols / (152 * 256) / 4 * 4;
+  int64_t len = (int64_t)a.B * a.L * cols / (kSMs * 256) / 4 * 4;
   len = len < 8 ? 8 : len > 128 ? 128 : len;
   const int run_len = static_cast<int>(len);
   const int runs = a.L > 0 ? (a.L + run_len - 1) / run_len : 1;
@@ -488,7 +488,7 @@ template <typename T, int W>
 cudaError_t conv_step_typed(const ConvArgs &a, cudaStream_t s) {
   const int nx = (a.E / 4 + 127) / 128;
   // about eight CTAs per SM; beyond that a CTA takes several sequences
-  int ny = (152 * 8 + nx - 1) / nx;
+  int ny = (kSMs * 8 + nx - 1) / nx;
   if (ny > a.B) ny = a.B;
   conv_step_kernel<T, W><<<dim3(nx, ny), 128, 0, s>>>(a);
   return cudaGetLastError();
