@@ -263,7 +263,7 @@ struct ConvGrads {
   void *dx, *dstate;
   float *dw, *dbias;
 };
-size_t conv_backward_workspace_bytes(int B, int L, int E, int W);
+size_t conv_backward_workspace_bytes(int B, int L, int E, int W, Dtype dt);
 cudaError_t launch_conv_backward(const ConvArgs &a, const ConvGrads &g, Dtype dt, void *ws,
                                  cudaStream_t s);
 

@@ -343,7 +343,7 @@ la_status_t la_backward_conv(const void *x, const float *w, const float *bias, c
   }
   const ConvArgs a = {x, w, bias, state, nullptr, nullptr, nullptr, B, L, E, W, ldx, silu != 0};
   const ConvGrads g = {dy, dx, dstate, dw, dbias};
-  return with_workspace(conv_backward_workspace_bytes(B, L, E, W), s, [&](void *ws) {
+  return with_workspace(conv_backward_workspace_bytes(B, L, E, W, to_dtype(dtype)), s, [&](void *ws) {
     return launch_conv_backward(a, g, to_dtype(dtype), ws, s);
   });
 }

@@ -86,14 +86,16 @@ __device__ __forceinline__ float softplus_f32(float x) { return unpack2(softplus
 
 // 1 / (1 + exp(-x)) on the special function unit (two roundings each of the
 // exponential and the reciprocal); exp(-x) = inf gives 0, NaN stays NaN
-__device__ __forceinline__ float sigmoid_f32(float x) {
+__device__ __forceinline__ float rcp_approx(float x) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-x * kLog2e)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_approx(1.f + ex2(-x * kLog2e)); }
 __device__ __forceinline__ f2 sigmoid_f2(f2 x) {
-  const float2 q = unpack2(x);
-  return pack2(sigmoid_f32(q.x), sigmoid_f32(q.y));
+  const float2 q = unpack2(mul2(x, dup2(-kLog2e)));
+  const float2 s = unpack2(add2(pack2(ex2(q.x), ex2(q.y)), dup2(1.f)));
+  return pack2(rcp_approx(s.x), rcp_approx(s.y));
 }
 
 // Asynchronous copy of 16 bytes to shared memory (zeros where !valid: the

@@ -354,10 +354,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         if (gated) load4p(&g.z[s], zv);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (gated) {
-            const float2 q = unpack2(zv[k]);
-            gv[k] = mul2(gv[k], mul2(zv[k], pack2(sigmoid_f32(q.x), sigmoid_f32(q.y))));
-          }
+          if (gated) gv[k] = mul2(gv[k], mul2(zv[k], sigmoid_f2(zv[k])));
           if (r >= rows) gv[k] = dup2(0.f);
         }
         store4p(&sm.g[s], gv);
@@ -452,10 +449,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             f2 zv[2];
             load4p(&g.z[s], zv);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 q = unpack2(zv[k]);
-              yv[k] = mul2(mul2(yv[k], zv[k]), pack2(sigmoid_f32(q.x), sigmoid_f32(q.y)));
-            }
+            for (int k = 0; k < 2; ++k) yv[k] = mul2(mul2(yv[k], zv[k]), sigmoid_f2(zv[k]));
           }
           store4p(y + (int64_t)(tb + r) * a.E + qcol, yv);
         }

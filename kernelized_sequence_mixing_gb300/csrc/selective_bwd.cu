@@ -205,10 +205,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         dv[k] = add2(dv[k], bias[k]);
         if (a.softplus) dv[k] = softplus_f2(dv[k]);
         xv[k] = mul2(xv[k], dv[k]);
-        if (gated) {
-          const float2 q = unpack2(zv[k]);
-          gv[k] = mul2(gv[k], mul2(zv[k], pack2(sigmoid_f32(q.x), sigmoid_f32(q.y))));
-        }
+        if (gated) gv[k] = mul2(gv[k], mul2(zv[k], sigmoid_f2(zv[k])));
         if (!in) dv[k] = xv[k] = gv[k] = dup2(0.f);
       }
       store4p(&sm.dt[s], dv);
@@ -440,8 +437,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int k = 0; k < 2; ++k) {
           f2 g = gv[k];
           if (gated) {
-            const float2 z2 = unpack2(zv[k]);
-            const f2 act = pack2(sigmoid_f32(z2.x), sigmoid_f32(z2.y));
+            const f2 act = sigmoid_f2(zv[k]);
             // silu'(z) = s (1 + z (1 - s))
             const f2 slope = mul2(act, fma2(zv[k], fma2(act, dup2(-1.f), dup2(1.f)), dup2(1.f)));
             yv[k] = mul2(mul2(g, fma2(dskip[k], xv[k], yv[k])), slope);
@@ -450,10 +446,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           const f2 v = add2(dv[k], bias[k]);
           const f2 step = a.softplus ? softplus_f2(v) : v;
           dd[k] = fma2(du[k], xv[k], mul2(dd[k], dup2(kLn2)));
-          if (a.softplus) {
-            const float2 r = unpack2(v);
-            dd[k] = mul2(dd[k], pack2(sigmoid_f32(r.x), sigmoid_f32(r.y)));
-          }
+          if (a.softplus) dd[k] = mul2(dd[k], sigmoid_f2(v));
           du[k] = fma2(du[k], step, mul2(dskip[k], g));
           sD[k] = fma2(g, xv[k], sD[k]);
           sb[k] = add2(sb[k], dd[k]);

@@ -136,8 +136,12 @@ __device__ __forceinline__ void load_taps(const float *w, int e, f2 (&out)[W][P]
     for (int p = 0; p < P; ++p) out[k][p] = pack2(q[2 * p * W + k], q[(2 * p + 1) * W + k]);
 }
 
+// CTAs of the forward pass that fit an SM; one more would spill (B4 L4096
+// E4096 W4 in bf16: 47 us at four, 79 at five; fp32: 85 at five, 87 at six).
+template <typename T> constexpr int kResident = sizeof(T) == 2 ? 4 : 5;
+
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kResident<T>)
     conv_kernel(const __grid_constant__ ConvArgs a, int run_len, int runs) {
   constexpr int P = kPairs<T>;
   const unsigned cols = a.E / (2 * P);
@@ -283,9 +287,13 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 // and leave as one record, and a second kernel adds the records in their
 // order, so the result does not depend on scheduling.
 constexpr int kBwdCols = 32, kBwdRows = 4;
+// CTAs that fit an SM: the loads ahead (2 W per thread) take the registers.
+// One more would spill (B4 L4096 E4096, W = 4, fp32: 128 us at four, 185 at
+// five; bf16: 89 at five, 95 at six), one less leaves a part of the SM idle.
+constexpr int bwd_resident(int elem_bytes, int W) { return (elem_bytes == 4 ? 8 : 9) - W; }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kBwdCols * kBwdRows)
+__global__ void __launch_bounds__(kBwdCols * kBwdRows, bwd_resident(sizeof(T), W))
     conv_bwd_kernel(const __grid_constant__ ConvArgs a, const __grid_constant__ ConvGrads g,
                     float *__restrict__ rec, int run_len, int runs) {
   let_next_start();
@@ -451,14 +459,14 @@ __global__ void __launch_bounds__(kBwdCols * kBwdRows)
 }
 
 // Backward pass: a run per warp row such that all the CTAs are resident at
-// once (five per SM; a CTA has four rows), of at least 29 tokens (the
+// once (a CTA has four rows), of at least 29 tokens (the
 // W - 1 walked twice are then a tenth at most).
 struct BwdPlan {
   int run_len, runs, ny;
 };
-BwdPlan conv_bwd_plan(int B, int L, int E) {
+BwdPlan conv_bwd_plan(int B, int L, int E, int W, int elem_bytes) {
   const int nx = (E / 2 + kBwdCols - 1) / kBwdCols;
-  int rows = kSMs * 5 / nx * kBwdRows;  // rows of runs that fit at once
+  int rows = kSMs * bwd_resident(elem_bytes, W) / nx * kBwdRows;  // rows of runs that fit at once
   if (rows < kBwdRows) rows = kBwdRows;
   const int per = rows / B > 0 ? rows / B : 1;  // runs per sequence
   BwdPlan p;
@@ -472,13 +480,16 @@ BwdPlan conv_bwd_plan(int B, int L, int E) {
 
 template <typename T, int W>
 cudaError_t conv_fwd_typed(const ConvArgs &a, cudaStream_t s) {
-  // runs of 128 tokens (the taps and the W - 1 early rows cost a thread about
-  // five tokens' work), shorter ones, whole groups of 4, where that leaves
-  // fewer than 256 threads per SM
+  // Runs of at most 128 tokens (the taps and the W - 1 early rows cost a thread
+  // about five tokens' work), in whole groups of 4, as many as fill the waves
+  // of CTAs that this takes.
   const int cols = a.E / (2 * kPairs<T>);
-  int64_t len = (int64_t)a.B * a.L * cols / (kSMs * 256) / 4 * 4;
-  len = len < 8 ? 8 : len > 128 ? 128 : len;
-  const int run_len = static_cast<int>(len);
+  const int64_t wave = (int64_t)kSMs * kResident<T> * kThreads, lanes = (int64_t)a.B * cols;
+  const int64_t least = lanes * ((a.L + 127) / 128), waves = least > wave ? (least + wave - 1) / wave : 1;
+  const int64_t per = waves * wave / lanes;  // runs per sequence
+  int64_t len = per > 0 ? (a.L + per - 1) / per : a.L;
+  len = (len + 3) / 4 * 4;
+  const int run_len = static_cast<int>(len < 8 ? 8 : len > 128 ? 128 : len);
   const int runs = a.L > 0 ? (a.L + run_len - 1) / run_len : 1;
   const int64_t n = (int64_t)a.B * runs * cols;
   conv_kernel<T, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, run_len, runs);
@@ -495,7 +506,7 @@ cudaError_t conv_step_typed(const ConvArgs &a, cudaStream_t s) {
 }
 template <typename T, int W>
 cudaError_t conv_bwd_typed(const ConvArgs &a, const ConvGrads &g, void *ws, cudaStream_t s) {
-  const BwdPlan p = conv_bwd_plan(a.B, a.L, a.E);
+  const BwdPlan p = conv_bwd_plan(a.B, a.L, a.E, W, sizeof(T));
   const int nx = (a.E / 2 + kBwdCols - 1) / kBwdCols;
   float *rec = static_cast<float *>(ws);
   conv_bwd_kernel<T, W><<<dim3(nx, p.ny), kBwdCols * kBwdRows, 0, s>>>(a, g, rec, p.run_len, p.runs);
@@ -529,8 +540,8 @@ cudaError_t launch_conv_step(const ConvArgs &a, Dtype dt, cudaStream_t s) {
   return dt == kF32 ? conv_widths<float>(a, nullptr, true, nullptr, s)
                     : conv_widths<__nv_bfloat16>(a, nullptr, true, nullptr, s);
 }
-size_t conv_backward_workspace_bytes(int B, int L, int E, int W) {
-  return sizeof(float) * (size_t)conv_bwd_plan(B, L, E).ny * (W + 1) * E;
+size_t conv_backward_workspace_bytes(int B, int L, int E, int W, Dtype dt) {
+  return sizeof(float) * (size_t)conv_bwd_plan(B, L, E, W, dt == kF32 ? 4 : 2).ny * (W + 1) * E;
 }
 cudaError_t launch_conv_backward(const ConvArgs &a, const ConvGrads &g, Dtype dt, void *ws,
                                  cudaStream_t s) {
