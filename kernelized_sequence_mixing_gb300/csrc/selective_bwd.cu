@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                          const __grid_constant__ BwdRecords rec, int S, unsigned int *timeouts) {
   using Sh = MainShape<T, N>;
   constexpr int CT = Sh::CT, LN = Sh::LN, TT = Sh::TT;
+  constexpr bool kOnce = TT <= 2 * kSub;  // one sum over the warps per tile
   extern __shared__ __align__(128) unsigned char smem_raw[];
   MainSmem<T, N> &sm = *reinterpret_cast<MainSmem<T, N> *>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -398,17 +399,21 @@ __global__ void __launch_bounds__(kThreads, 3)
           }
         }
       }
-      // the other half of `red` is written before this half is again, with
-      // this barrier in between
-      __syncthreads();
-      for (int i = tid; i < kSub * 2 * N; i += kThreads) {
-        const int t = sub * kSub + i / (2 * N);
-        if (tb + t < t1) {
-          const float *p = &sm.red[sub & 1][0][0][0] + i;
-          float s = p[0];
+      if (!kOnce || sub == 0) {
+        // kOnce: `red` holds the tile, and the barrier after the next staging
+        // is in front of its next use.  Otherwise the other half of `red` is
+        // written before this half is again, with this barrier in between.
+        __syncthreads();
+        const int subs = kOnce ? (min(TT, t1 - tb) + kSub - 1) / kSub : 1;
+        for (int i = tid; i < subs * kSub * 2 * N; i += kThreads) {
+          const int s1 = sub + i / (kSub * 2 * N), j = i % (kSub * 2 * N);
+          if (tb + s1 * kSub + j / (2 * N) < t1) {
+            const float *p = &sm.red[s1 & 1][0][0][0] + j;
+            float s = p[0];
 #pragma unroll
-          for (int w = 1; w < kWarps; ++w) s += p[w * kSub * 2 * N];
-          bc[(int64_t)sub * kSub * 2 * N + i] = s;
+            for (int w = 1; w < kWarps; ++w) s += p[w * kSub * 2 * N];
+            bc[(int64_t)sub * kSub * 2 * N + i] = s;
+          }
         }
       }
     }
