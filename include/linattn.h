@@ -430,8 +430,8 @@ LA_API size_t la_forward_noncausal_static_limit(void);
  * - Sizes: E a multiple of 8 up to 65536, E / G a multiple of 8, N in {8, 16,
  *   32, 64}, fewer than 2^31 tokens and B E < 2^31.
  * - lens (optional, int32 [B] in DEVICE memory, 4-byte aligned): sequence b
- *   has lens[b] tokens (clamped to [0, L]).  Rows behind it are neither read
- *   nor written, and the final state is the one after the last token.
+ *   has lens[b] tokens (clamped to [0, L]).  Rows behind it have no
+ *   effect and are left alone in the outputs, and the final state is the one after the last token.
  * - fp32 arithmetic; each output is rounded once to `dtype`.  Results do not
  *   depend on scheduling (no atomics).  Workspaces are stream-ordered
  *   allocations from a pool the library keeps per device (up to 512 MiB held

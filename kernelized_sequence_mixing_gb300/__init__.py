@@ -646,7 +646,7 @@ def forward_selective(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=T
     silu(z_t).  x, dt, z: [B, L, E]; Bm, Cm: [B, L, G, N] CUDA tensors of one
     dtype, dense or slices of a dense tensor's rows; A: [E, N], D, dt_bias: [E]
     and h0: [B, E, N] float32; lens: [B] int32 tokens per sequence (rows behind
-    are neither read nor written).  Returns y, or (y, h [B, E, N] float32) with
+    have no effect and stay unwritten).  Returns y, or (y, h [B, E, N] float32) with
     the state after the last token when return_state is true (or h is given)."""
     fn = "forward_selective"
     (B, L), E, N, G, lds = _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, 3)

@@ -144,7 +144,6 @@ __global__ void __launch_bounds__(kThreads, 4)
                 const __grid_constant__ ScanRecords rec, int S, int part_len,
                 unsigned int *timeouts) {
   constexpr bool OUT = MODE == kOut, LOCAL = MODE == kLocal;
-  if constexpr (!OUT) let_next_start();
   using Sh = Shape<T, N, MODE>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Smem<T, N, MODE> &sm = *reinterpret_cast<Smem<T, N, MODE> *>(smem_raw);
@@ -478,6 +477,7 @@ cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &re
   unsigned int *timeouts = wait_timeout_counter();
   if (!timeouts) return cudaErrorUnknown;
   cudaError_t e = allow_smem(scan_kernel<T, N, MODE>, smem);
+  if (e == cudaSuccess) e = most_shared(scan_kernel<T, N, MODE>);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
   const int64_t ctas = a.B * (MODE == kStates ? S - 1 : S) * tiles;

@@ -63,7 +63,6 @@ struct BwdRecords {
 __global__ void __launch_bounds__(256)
     scan_bwd_carry_kernel(const __grid_constant__ ScanArgs a, const float *__restrict__ dhN,
                           const __grid_constant__ BwdRecords rec, int S) {
-  let_next_start();
   wait_for_previous();
   const int64_t EN = (int64_t)a.E * a.N;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -107,7 +106,45 @@ struct MainShape {
   static constexpr int NQ = TT / ROWS;                        // quads per thread
   static constexpr int NP = N + 8;  // floats per token of B and of C: rows in different banks
   static constexpr int NBQ = (2 * TT * LN + kThreads - 1) / kThreads;  // quads of B and C per thread
+  // tokens whose dB and dC a warp sums at once: as many as cost an SM no CTA
+  static constexpr int BT = N == 64 ? 0 : sizeof(T) == 4 || N == 32 ? 2 : 4;
+  // in a warp's [channels][dB | dC] the halves change places such that eight
+  // lanes' 16 bytes fill the banks
+  static __device__ __forceinline__ int flip(int lc) {
+    return N == 8 ? (lc & 2) * 4 : N == 16 ? (lc & 1) * 16 : 0;
+  }
 };
+
+// s += p[0..V) (first: s = p).
+template <int V>
+__device__ __forceinline__ void add_vec(float (&s)[V], const float *p, bool first) {
+  float v[V];
+  if constexpr (V == 4) {
+    const float4 q = *reinterpret_cast<const float4 *>(p);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  } else if constexpr (V == 2) {
+    const float2 q = *reinterpret_cast<const float2 *>(p);
+    v[0] = q.x; v[1] = q.y;
+  } else {
+    v[0] = *p;
+  }
+  if constexpr (V == 1) {
+    s[0] = first ? v[0] : s[0] + v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 q = unpack2(add2(pack2(first ? 0.f : s[i], first ? 0.f : s[i + 1]), pack2(v[i], v[i + 1])));
+      s[i] = first ? v[i] : q.x;
+      s[i + 1] = first ? v[i + 1] : q.y;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_vec(float *p, const float (&s)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4 *>(p) = make_float4(s[0], s[1], s[2], s[3]);
+  else if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(s[0], s[1]);
+  else *p = s[0];
+}
 
 // A tile as loaded; the epilogue reads it again.
 template <typename T, int N>
@@ -134,6 +171,7 @@ struct MainSmem {
   // bytes a lane, whose repeats in the warp share a wavefront (sixteen do not)
   float B[Sh::TT * Sh::NP], C[Sh::TT * Sh::NP];
   float cols[2][kThreads * 4];  // dD and d(dt_bias) of each thread's quads
+  alignas(16) float part[kWarps][Sh::BT ? Sh::BT * 256 : 4];  // dB | dC of the warps' channels
   float red[2][kWarps][kSub][2 * N];
 };
 
@@ -150,10 +188,10 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sl = lane & (LN - 1), lc = lane / LN;
   const int Eg = a.E / a.G, gtiles = (Eg + CT - 1) / CT, tiles = gtiles * a.G;
-  const int tile = blockIdx.x % tiles, part = (blockIdx.x / tiles) % S, b = blockIdx.x / tiles / S;
+  const int tile = blockIdx.x % tiles, seg = (blockIdx.x / tiles) % S, b = blockIdx.x / tiles / S;
   const int grp = tile / gtiles, cg = (tile % gtiles) * CT, e0 = grp * Eg + cg;
   const int nch = min(CT, Eg - cg);
-  const int t0 = part * kPart<N>, t1 = min(a.L, t0 + kPart<N>);
+  const int t0 = seg * kPart<N>, t1 = min(a.L, t0 + kPart<N>);
   const bool gated = a.z != nullptr;
 
   // this thread's quads of a staged tile: one column
@@ -162,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, 3)
   *reinterpret_cast<float4 *>(&sm.cols[0][tid * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
   *reinterpret_cast<float4 *>(&sm.cols[1][tid * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  let_next_start();
   if (tid == 0) {
     tc::mbar_init(&sm.full[0], 1);
     tc::mbar_init(&sm.full[1], 1);
@@ -228,10 +265,11 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   // this thread's channel pair and states
   const int c0 = warp * Sh::CPW + lc * 2, n0 = sl * 4;
+  float *part = sm.part[warp];
   const bool cin = c0 < nch;  // pairs: widths are multiples of 8
   const int64_t en = (int64_t)(e0 + c0) * N + n0;            // within [E][N]
   const int64_t ben = (int64_t)b * a.E * N + en;             // within [B][E][N]
-  const int64_t pen = ((int64_t)b * S + part) * a.E * N + en;  // within the records
+  const int64_t pen = ((int64_t)b * S + seg) * a.E * N + en;  // within the records
   auto load_pair = [&](const float *p, f2 (&v)[4], float scale) {
     float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
     if (p && cin) {
@@ -258,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   for (int n = 0; n < 4; ++n) dA[n] = dup2(0.f);
   // the checkpoint in front of token group k of the part (k > 0)
   auto load_ck = [&](int k, f2 (&h)[4], f2 &sd) {
-    const int64_t rc = (((int64_t)b * S + part) * (kPart<N> / kSub - 1) + k - 1) * a.E + e0 + c0;
+    const int64_t rc = (((int64_t)b * S + seg) * (kPart<N> / kSub - 1) + k - 1) * a.E + e0 + c0;
     load_pair(rec.s.ck + rc * N + n0, h, 1.f);
     sd = cin ? f2{*reinterpret_cast<const unsigned long long *>(rec.s.ckdt + rc)} : dup2(0.f);
   };
@@ -333,35 +371,37 @@ __global__ void __launch_bounds__(kThreads, 3)
             sums[i][1] = n ? fma2(w, A[n], sums[i][1]) : mul2(w, A[n]);
             dA[n] = fma2(w, d2, dA[n]);
           }
-          // over the channels: each lane bit keeps half of the eight values
-          float *rd = sm.red[sub & 1][warp][j];
-          const bool h1 = lane & LN;
+          // over the warp's channels: through shared memory, several tokens at
+          // a time (shuffles and their selects took 29 instructions a token,
+          // this takes 10), or with two lanes to a state in one exchange
+          if constexpr (Sh::LC > 2) {
+            float *pd = part + (j % Sh::BT) * 256 + lc * 2 * N;
+            const int flip = Sh::flip(lc);
+            *reinterpret_cast<float4 *>(pd + (n0 ^ flip)) = make_float4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<float4 *>(pd + ((N + n0) ^ flip)) = make_float4(r[4], r[5], r[6], r[7]);
+            if (j % Sh::BT == 0) {
+              constexpr int V = Sh::BT * N / 16, VV = V < 4 ? V : 4;  // sums per lane, and at once
+              __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float keep = h1 ? r[4 + k] : r[k], send = h1 ? r[k] : r[4 + k];
-            r[k] = keep + __shfl_xor_sync(0xffffffffu, send, LN);
-          }
-          int idx = (h1 ? N : 0) + n0;
-          if constexpr (Sh::LC >= 4) {
-            const bool h2 = lane & (2 * LN);
+              for (int q = 0; q < V / VV; ++q) {
+                const int k = (q * 32 + lane) * VV, tk = k / (2 * N), o = k % (2 * N);
+                const float *ps = part + tk * 256;
+                float s[VV];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float keep = h2 ? r[2 + k] : r[k], send = h2 ? r[k] : r[2 + k];
-              r[k] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * LN);
-            }
-            idx += h2 ? 2 : 0;
-            if constexpr (Sh::LC >= 8) {
-              const bool h3 = lane & (4 * LN);
-              const float keep = h3 ? r[1] : r[0], send = h3 ? r[0] : r[1];
-              r[0] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * LN);
-              idx += h3 ? 1 : 0;
-              if constexpr (Sh::LC >= 16) r[0] += __shfl_xor_sync(0xffffffffu, r[0], 8 * LN);
-              if (Sh::LC < 16 || !(lane & (8 * LN))) rd[idx] = r[0];
-            } else {
-              *reinterpret_cast<float2 *>(&rd[idx]) = make_float2(r[0], r[1]);
+                for (int c = 0; c < Sh::LC; ++c) add_vec<VV>(s, ps + c * 2 * N + (o ^ Sh::flip(c)), c == 0);
+                store_vec<VV>(&sm.red[sub & 1][warp][j + tk][o], s);
+              }
+              __syncwarp();
             }
           } else {
-            *reinterpret_cast<float4 *>(&rd[idx]) = make_float4(r[0], r[1], r[2], r[3]);
+            const bool hi = lane & LN;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float keep = hi ? r[4 + k] : r[k], send = hi ? r[k] : r[4 + k];
+              r[k] = keep + __shfl_xor_sync(0xffffffffu, send, LN);
+            }
+            *reinterpret_cast<float4 *>(&sm.red[sub & 1][warp][j][(hi ? N : 0) + n0]) =
+                make_float4(r[0], r[1], r[2], r[3]);
           }
         }
         // over the states: lane bit 0 takes one of the two tokens, bit 1 one
@@ -467,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     // here, and B and C, which were last read before the barrier above
   }
   store_pair(rec.dA + pen, dA);
-  if (part == 0 && gr.dh0) store_pair(gr.dh0 + ben, gc);
+  if (seg == 0 && gr.dh0) store_pair(gr.dh0 + ben, gc);
   __syncthreads();
-  float *cols = rec.cols + ((int64_t)b * S + part) * 2 * a.E + e0;
+  float *cols = rec.cols + ((int64_t)b * S + seg) * 2 * a.E + e0;
   for (int i = tid; i < 2 * CT; i += kThreads) {
     if (i % CT < nch) {
       const float *p = sm.cols[i / CT] + i % CT;  // [rows of threads][CT]
