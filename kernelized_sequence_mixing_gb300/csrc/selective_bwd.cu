@@ -29,10 +29,11 @@
 // 25% of its instructions, and it is the instructions and the shared-memory
 // pipe that bound it: 2 exponentials (3 with the local pass) and about 13
 // packed fp32 operations per two states and token, plus the sums.  A thread of
-// the main pass owns 2 channels x 4 states (packed pairs of channels): sums
-// over states cross N/4 lanes two tokens at a time, sums over channels the
-// other lanes, both by transposing exchanges, then the CTA's warps in shared
-// memory.
+// the main pass owns 2 channels x 4 states (packed pairs of channels).  Sums over
+// states cross N/4 lanes by transposing exchanges, two tokens at a time; sums
+// over channels cross the other lanes and the CTA's warps in shared memory.
+// (B2 L4096 E2048 N16 in bf16, the whole backward pass: 407 us; both kinds by
+// exchanges 414, both in shared memory 431.)
 #include "column_sum.cuh"
 #include "dependent.cuh"
 #include "kernels.h"
@@ -48,6 +49,13 @@ constexpr int kSub = kScanCheckpoint;  // tokens whose states a thread holds
 
 template <int N> constexpr int kPart = N == 8 ? 32 : 64;  // tokens per part
 
+__device__ __forceinline__ f2 load_f2(const float *p) {
+  return f2{*reinterpret_cast<const unsigned long long *>(p)};
+}
+__device__ __forceinline__ void store_f2(float *p, f2 v) {
+  *reinterpret_cast<unsigned long long *>(p) = v.v;
+}
+
 struct BwdRecords {
   ScanRecords s;  // s.h: end states, then the states before a part; s.g: likewise behind it
   float *dA;      // [B][S][E][N], in place of s.h
@@ -57,41 +65,50 @@ struct BwdRecords {
 
 // ------------------------------------------------------------------- carry
 
-// One thread per (b, e, n) and direction: the records of the parts in order,
-// in place.  h: slot p <- the state before part p.  g: slot p <- the adjoint
-// behind part p.
-__global__ void __launch_bounds__(256)
+// One thread per two states of (b, e) and direction: the records of the parts
+// in order, in place.  h: slot p <- the state before part p.  g: slot p <- the
+// adjoint behind part p.
+constexpr int kCarryThreads = 128;
+__global__ void __launch_bounds__(kCarryThreads)
     scan_bwd_carry_kernel(const __grid_constant__ ScanArgs a, const float *__restrict__ dhN,
                           const __grid_constant__ BwdRecords rec, int S) {
   wait_for_previous();
   const int64_t EN = (int64_t)a.E * a.N;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = ((int64_t)blockIdx.x * kCarryThreads + threadIdx.x) * 2;
   if (i >= a.B * EN) return;
   const int64_t b = i / EN, en = i - b * EN;
   const int e = static_cast<int>(en / a.N);
-  const float A = a.A[en] * kLog2e;
+  const f2 A = mul2(load_f2(a.A + en), dup2(kLog2e));
   const bool back = blockIdx.y == 1;
-  float *r = (back ? rec.s.g : rec.s.h) + b * S * EN + en;
-  const float *sd = rec.s.dt + b * S * a.E + e;
-  float acc = back ? (dhN ? dhN[i] : 0.f) : (a.h0 ? a.h0[i] : 0.f);
+  const float *from = back ? dhN : a.h0;
+  f2 acc = from ? load_f2(from + i) : dup2(0.f);
+  // from the last part back: steps of the other sign
+  const int64_t rstep = back ? -EN : EN, sstep = back ? -a.E : a.E;
+  float *r = (back ? rec.s.g + (b * S + S - 1) * EN : rec.s.h + b * S * EN) + en;
+  const float *sd = rec.s.dt + (back ? b * S + S - 1 : b * S) * a.E + e;
   constexpr int kAhead = 8;
-  for (int q0 = 0; q0 < S; q0 += kAhead) {
-    float v[kAhead], d[kAhead];
+  for (int q = 0; q < S; q += kAhead) {
+    f2 v[kAhead];
+    float d[kAhead];
+    const int m = S - q;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int p = back ? S - 1 - (q0 + k) : q0 + k;
-      const bool in = q0 + k < S;
-      v[k] = in ? r[p * EN] : 0.f;
-      d[k] = in ? sd[(int64_t)p * a.E] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (q0 + k < S) {
-        const int p = back ? S - 1 - (q0 + k) : q0 + k;
-        r[p * EN] = acc;
-        acc = fmaf(ex2(d[k] * A), acc, v[k]);
+      v[k] = dup2(0.f);
+      d[k] = 0.f;
+      if (k < m) {
+        v[k] = load_f2(r + k * rstep);
+        d[k] = sd[k * sstep];
       }
     }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k < m) {
+        store_f2(r + k * rstep, acc);
+        acc = fma2(ex2_2(mul2(dup2(d[k]), A)), acc, v[k]);
+      }
+    }
+    r += kAhead * rstep;
+    sd += kAhead * sstep;
   }
 }
 
@@ -298,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 3)
   auto load_ck = [&](int k, f2 (&h)[4], f2 &sd) {
     const int64_t rc = (((int64_t)b * S + seg) * (kPart<N> / kSub - 1) + k - 1) * a.E + e0 + c0;
     load_pair(rec.s.ck + rc * N + n0, h, 1.f);
-    sd = cin ? f2{*reinterpret_cast<const unsigned long long *>(rec.s.ckdt + rc)} : dup2(0.f);
+    sd = cin ? load_f2(rec.s.ckdt + rc) : dup2(0.f);
   };
 
   auto tok2 = [&](const float *arr, int t) {
-    return f2{*reinterpret_cast<const unsigned long long *>(&arr[t * CT + c0])};
+    return load_f2(&arr[t * CT + c0]);
   };
   // this thread's four states of B or C, each twice
   auto shared4 = [&](const float *arr, int t, f2 (&v)[4]) {
@@ -609,7 +626,8 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   }
   if (z.S > 1) {
     const int64_t n = (int64_t)a.B * a.E * N;
-    e = launch_dependent(scan_bwd_carry_kernel, (unsigned)((n + 255) / 256), 2, 256, 0, s, a, g.dhN, rec, z.S);
+    e = launch_dependent(scan_bwd_carry_kernel, (unsigned)((n / 2 + kCarryThreads - 1) / kCarryThreads), 2,
+                         kCarryThreads, 0, s, a, g.dhN, rec, z.S);
     if (e != cudaSuccess) return e;
   }
   const int tiles = bwd_tiles(a.E, N, a.G);
