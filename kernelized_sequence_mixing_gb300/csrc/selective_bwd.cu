@@ -187,6 +187,7 @@ struct MainSmem {
   // states 4 l, 4 l + 1 at 2 l, states 4 l + 2, 4 l + 3 at 2 LN + 2 l: eight
   // bytes a lane, whose repeats in the warp share a wavefront (sixteen do not)
   float B[Sh::TT * Sh::NP], C[Sh::TT * Sh::NP];
+  alignas(16) float skip[Sh::CT], bias[Sh::CT];  // D and dt_bias
   float cols[2][kThreads * 4];  // dD and d(dt_bias) of each thread's quads
   alignas(16) float part[kWarps][Sh::BT ? Sh::BT * 256 : 4];  // dB | dC of the warps' channels
   float red[2][kWarps][kSub][2 * N];
@@ -241,11 +242,18 @@ __global__ void __launch_bounds__(kThreads, 3)
   };
   const int ntiles = (t1 - t0 + TT - 1) / TT;
   if (ntiles > 0) issue(t0 + (ntiles - 1) * TT, 0);
-  f2 bias[2] = {dup2(0.f), dup2(0.f)};
-  if (qin && a.dt_bias) load4p(a.dt_bias + e0 + qcol, bias);
+  {  // every thread of a column writes the same values, and reads its own
+    f2 v[2] = {dup2(0.f), dup2(0.f)}, w[2] = {v[0], v[1]};
+    if (qin && a.dt_bias) load4p(a.dt_bias + e0 + qcol, v);
+    if (qin && a.D) load4p(a.D + e0 + qcol, w);
+    store4p(&sm.bias[qcol], v);
+    store4p(&sm.skip[qcol], w);
+  }
   // Stage st, whose first `rows` rows count, as the main loop reads it.
   auto convert = [&](int st, int rows) {
     const MainStage<T, N> &g = sm.stage[st];
+    f2 bias[2];
+    load4p(&sm.bias[qcol], bias);
 #pragma unroll
     for (int i = 0; i < Sh::NQ; ++i) {
       const int row = qrow + i * Sh::ROWS, s = row * CT + qcol;
@@ -477,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     // the tile's per-token gradients, and its share of the column sums
     const MainStage<T, N> &sg = sm.stage[st];
-    f2 dskip[2] = {dup2(0.f), dup2(0.f)};
-    if (qin && a.D) load4p(a.D + e0 + qcol, dskip);
-    f2 sD[2], sb[2];
+    f2 dskip[2], bias[2], sD[2], sb[2];
+    load4p(&sm.skip[qcol], dskip);
+    load4p(&sm.bias[qcol], bias);
     load4p(&sm.cols[0][tid * 4], sD);
     load4p(&sm.cols[1][tid * 4], sb);
 #pragma unroll
