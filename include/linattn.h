@@ -448,8 +448,8 @@ LA_API size_t la_forward_noncausal_static_limit(void);
  * D, z and dt_bias may be NULL (no such term).  hN (optional) receives the
  * state after the last token (h0 for no tokens), the state
  * la_decode_selective continues from; it may not be h0 itself.  Few channels
- * split the tokens into up to 128 parts of 128 tokens or more, with a workspace
- * of B*E*(N + 1)*4 bytes for each part but one.
+ * split the tokens into up to 128 parts of 32 tokens or more, with a workspace of
+ * B*E*(N + 1)*4 bytes for each part but one.
  */
 LA_API la_status_t la_forward_selective(const void *x, const void *dt, const float *A,
                                         const void *Bm, const void *Cm, const float *D,
@@ -487,7 +487,7 @@ LA_API la_status_t la_decode_selective(const void *x, const void *dt, const floa
  * given exactly when z is.  A batch padded at the end is handled by zero rows
  * of dy (a later token does not reach an earlier one).  The workspace is about
  * B*L*E*(N/8 + 2N/64 + N*N/512) floats (11 bytes per token and channel for
- * N = 16): a state every 8 tokens, two per part of 64 tokens (32 for N = 8),
+ * N = 16): a state every 8 tokens, two per part of 64 tokens (32 or 48 for N = 8),
  * and the channel tiles' sums of dB and dC.
  */
 LA_API la_status_t la_backward_selective(

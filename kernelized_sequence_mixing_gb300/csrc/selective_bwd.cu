@@ -46,8 +46,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSub = kScanCheckpoint;  // tokens whose states a thread holds
-
-template <int N> constexpr int kPart = N == 8 ? 32 : 64;  // tokens per part
+constexpr int kPart = 64;              // tokens per part, of 16 states and more
 
 __device__ __forceinline__ f2 load_f2(const float *p) {
   return f2{*reinterpret_cast<const unsigned long long *>(p)};
@@ -61,6 +60,7 @@ struct BwdRecords {
   float *dA;      // [B][S][E][N], in place of s.h
   float *cols;    // [B][S][2][E]: dD, d(dt_bias)
   float *bc;      // [B][tiles][L][2N]: dB | dC of a channel tile
+  int part;       // tokens per part
 };
 
 // ------------------------------------------------------------------- carry
@@ -209,7 +209,9 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int tile = blockIdx.x % tiles, seg = (blockIdx.x / tiles) % S, b = blockIdx.x / tiles / S;
   const int grp = tile / gtiles, cg = (tile % gtiles) * CT, e0 = grp * Eg + cg;
   const int nch = min(CT, Eg - cg);
-  const int t0 = seg * kPart<N>, t1 = min(a.L, t0 + kPart<N>);
+  // a constant where it can be: as a parameter it cost 6 of 403 us
+  const int tokens = N > 8 ? kPart : rec.part;
+  const int t0 = seg * tokens, t1 = min(a.L, t0 + tokens);
   const bool gated = a.z != nullptr;
 
   // this thread's quads of a staged tile: one column
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   for (int n = 0; n < 4; ++n) dA[n] = dup2(0.f);
   // the checkpoint in front of token group k of the part (k > 0)
   auto load_ck = [&](int k, f2 (&h)[4], f2 &sd) {
-    const int64_t rc = (((int64_t)b * S + seg) * (kPart<N> / kSub - 1) + k - 1) * a.E + e0 + c0;
+    const int64_t rc = (((int64_t)b * S + seg) * (tokens / kSub - 1) + k - 1) * a.E + e0 + c0;
     load_pair(rec.s.ck + rc * N + n0, h, 1.f);
     sd = cin ? load_f2(rec.s.ckdt + rc) : dup2(0.f);
   };
@@ -589,20 +591,28 @@ __global__ void __launch_bounds__(256)
   store4(static_cast<T *>(k < N ? g.dBm : g.dCm) + o, s);
 }
 
-int bwd_part_tokens(int N) { return N == 8 ? 32 : 64; }
 int bwd_tiles(int E, int N, int G) {
   const int CT = 1024 / N;
   return G * ((E / G + CT - 1) / CT);
 }
 
+// Tokens per part.  With 8 states shorter ones, the shortest where they are
+// few (bf16, B2 L4096 E2048: 263 us at 48, 272 at 32; B1 L512 E2048: 32 us at
+// 32, 42 at 48).  With 16, 32 tokens differ from 64 by 5% either way in small
+// calls, and 96 are worse there (B1 L512 E2048: 62 us against 46).
+int bwd_part_tokens(int B, int L, int E, int N, int G) {
+  if (N > 8) return kPart;
+  return (int64_t)B * ((L + 47) / 48) * bwd_tiles(E, N, G) < kSMs * 3 ? 32 : 48;
+}
+
 // The workspace: floats of each record.
 struct BwdSizes {
   size_t h, g, dt, ck, ckdt, cols, bc;
-  int S;
+  int S, part;
 };
 BwdSizes bwd_sizes(int B, int L, int E, int N, int G) {
   BwdSizes z;
-  const int pt = bwd_part_tokens(N), K = pt / kScanCheckpoint - 1;
+  const int pt = z.part = bwd_part_tokens(B, L, E, N, G), K = pt / kScanCheckpoint - 1;
   z.S = L > pt ? (L + pt - 1) / pt : 1;
   const size_t bs = (size_t)B * z.S;
   z.h = bs * E * N;
@@ -626,10 +636,11 @@ cudaError_t bwd_typed(const ScanArgs &a, const ScanGrads &g, void *ws, cudaStrea
   rec.s.ckdt = rec.s.ck + z.ck;
   rec.cols = rec.s.ckdt + z.ckdt;
   rec.bc = rec.cols + z.cols;
+  rec.part = z.part;
   cudaError_t e;
   // one group of tokens needs neither checkpoints nor records
   if (a.L > kScanCheckpoint) {
-    e = launch_selective_local(a, g.dy, rec.s, z.S, kPart<N>, sizeof(T) == 4 ? kF32 : kBF16, s);
+    e = launch_selective_local(a, g.dy, rec.s, z.S, z.part, sizeof(T) == 4 ? kF32 : kBF16, s);
     if (e != cudaSuccess) return e;
   }
   if (z.S > 1) {

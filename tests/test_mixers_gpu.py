@@ -102,7 +102,7 @@ def scan_ref(a, more, sp, **kw):
 SCANS = [
     (1, 1, 8, 16, 1), (2, 3, 72, 8, 1), (1, 17, 136, 16, 1), (3, 65, 64, 32, 2), (1, 63, 40, 64, 1),
     (1, 333, 264, 16, 1), (2, 300, 48, 8, 2), (1, 520, 96, 64, 4), (1, 1000, 16, 32, 1),
-    (5, 2, 512, 16, 4),
+    (5, 2, 512, 16, 4), (1, 2800, 64, 8, 8), (2, 97, 40, 64, 1),
 ]
 sid = lambda s: "x".join(map(str, s))  # noqa: E731
 
