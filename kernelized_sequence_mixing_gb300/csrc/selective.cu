@@ -49,6 +49,10 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxParts = 128;
+// A tile's tokens are walked in groups of so many, which a part's last tile
+// may leave out (B2 L4096 E2048 N16 in bf16, parts of 216 tokens instead of
+// 224: 128.4 us against 131.4; without parts it costs 0.6%).
+constexpr int kSteps = 8;
 // As many CTAs run whole sequences: 256 of them (B8 L2048 E4096 N16, bf16) take
 // 392 us and in parts 467, 192 of them 391 and 350.
 constexpr int kWhole = 224;
@@ -423,8 +427,12 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int j = 0; j < kCheckpoint; ++j) step(t8 + j);
       }
     } else {
-#pragma unroll 16
-      for (int t = 0; t < Sh::TT; ++t) step(t);
+      #pragma unroll 2
+      for (int t8 = 0; t8 < Sh::TT; t8 += kSteps) {
+        if (t8 && t8 >= rows) break;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) step(t8 + j);
+      }
     }
     __syncthreads();
     if constexpr (OUT) {
@@ -490,7 +498,7 @@ cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &re
 
 template <typename T, int N>
 cudaError_t scan_typed(const ScanArgs &a, void *ws, int S, cudaStream_t s) {
-  const int part_len = selective_part_len(a.L, S, N);
+  const int part_len = selective_part_len(a.L, S);
   ScanRecords rec = {};
   rec.h = static_cast<float *>(ws);
   rec.dt = rec.h + (size_t)a.B * (S - 1) * a.E * N;
@@ -620,10 +628,9 @@ cudaError_t step_states(const ScanArgs &a, cudaStream_t s) {
 
 bool selective_states_supported(int N) { return N == 8 || N == 16 || N == 32 || N == 64; }
 
-// Whole tiles: a tile's steps run whether they hold tokens or not.
-int selective_part_len(int L, int S, int N) {
-  const int l = (L + S - 1) / S, tile = N < 16 ? 16 : N;
-  return (l + tile - 1) / tile * tile;
+int selective_part_len(int L, int S) {
+  const int l = (L + S - 1) / S;
+  return (l + kSteps - 1) / kSteps * kSteps;
 }
 
 int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged) {
@@ -643,7 +650,7 @@ int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged) {
   if (most < 3) return 1;
   if (S > most) S = most;
   if (S < 2) return 1;
-  const int len = selective_part_len(L, static_cast<int>(S), N);
+  const int len = selective_part_len(L, static_cast<int>(S));
   return (L + len - 1) / len;  // no part is empty
 }
 
