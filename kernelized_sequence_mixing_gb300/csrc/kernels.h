@@ -213,7 +213,7 @@ bool selective_states_supported(int N);
 // parts' records (0 for one part).
 int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged);
 int selective_part_len(int L, int S);
-size_t selective_workspace_bytes(int B, int E, int N, int S);
+size_t selective_workspace_bytes(int B, int E, int N, int S, bool ragged);
 cudaError_t launch_selective(const ScanArgs &a, Dtype dt, void *ws, int S, cudaStream_t s);
 cudaError_t launch_selective_step(const ScanArgs &a, Dtype dt, cudaStream_t s);
 // Records of the scan's parts (S of them; the forward pass keeps S - 1), fp32:

@@ -170,7 +170,7 @@ la_status_t la_forward_selective(const void *x, const void *dt, const float *A, 
                       ldx, lddt, ldz, ldb, ldc, softplus != 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int S = selective_parts(B, L, E, N, G, to_dtype(dtype), lens != nullptr);
-  return with_workspace(selective_workspace_bytes(B, E, N, S), s, [&](void *ws) {
+  return with_workspace(selective_workspace_bytes(B, E, N, S, lens != nullptr), s, [&](void *ws) {
     return launch_selective(a, to_dtype(dtype), ws, S, s);
   });
 }

@@ -141,6 +141,63 @@ __device__ __forceinline__ void store_parts(float *y, int sl, f2 y01, f2 y23) {
   }
 }
 
+// A part of a sequence, and the record of the sequence's first part.
+struct Place {
+  int b, part, len, part_len, first;
+  bool last;
+};
+
+// The place of `slot` among the parts of a ragged batch, which share one
+// length: the shortest (of four tried, and one that always fits) at which the
+// parts of all sequences, one at least for each, fit the slots.  Every warp
+// works it out.  With a part length from L alone, slots went empty or a second
+// wave was needed.  False for a slot without a part.
+__device__ __forceinline__ bool find_place(const int *__restrict__ lens, int B, int L, int slots,
+                                           int least, int slot, Place *p) {
+  const int lane = threadIdx.x & 31;
+  auto clamped = [&](int b) { return min(max(lens[b], 0), L); };
+  auto up = [](int n) { return (n + kSteps - 1) / kSteps * kSteps; };
+  int total = 0;  // B L < 2^31
+  for (int b = lane; b < B; b += 32) total += clamped(b);
+  total = __reduce_add_sync(0xffffffffu, total);
+  const int lo = max(least, up((total + slots - 1) / slots));
+  const int hi = max(lo, up((total + slots - B - 1) / (slots - B)));
+  int len = hi;
+  for (int k = 0; k < 4; ++k) {
+    const int l = up(lo + (hi - lo) / 4 * k);
+    int n = 0;
+    for (int b = lane; b < B; b += 32) n += max(1, (clamped(b) + l - 1) / l);
+    if (__reduce_add_sync(0xffffffffu, n) <= slots) {
+      len = l;
+      break;
+    }
+  }
+  int before = 0;  // parts of the sequences before
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    const int own = b < B ? max(1, (clamped(b) + len - 1) / len) : 0;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, slot < before + sum);
+    if (here) {
+      const int src = __ffs(here) - 1, q = __shfl_sync(0xffffffffu, own, src);
+      p->first = before + __shfl_sync(0xffffffffu, sum, src) - q;
+      p->b = b0 + src;
+      p->part = slot - p->first;
+      p->last = p->part == q - 1;
+      p->len = clamped(p->b);
+      p->part_len = len;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
 // Parts: the last has no record in the state pass; kLocal runs them all.
 template <typename T, int N, int MODE>
 __global__ void __launch_bounds__(kThreads, 4)
@@ -152,6 +209,23 @@ __global__ void __launch_bounds__(kThreads, 4)
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Smem<T, N, MODE> &sm = *reinterpret_cast<Smem<T, N, MODE> *>(smem_raw);
 
+  const int Eg = a.E / a.G;  // channels per group
+  const int gtiles = (Eg + Sh::CT - 1) / Sh::CT, tiles = gtiles * a.G;
+  const int tile = blockIdx.x % tiles;
+  Place at;
+  if (!LOCAL && a.lens && S > 1) {
+    if (!find_place(a.lens, a.B, a.L, a.B * S, part_len, blockIdx.x / tiles, &at)) return;
+    if (MODE == kStates && at.last) return;
+  } else {
+    const int nparts = MODE == kStates ? S - 1 : S;
+    at.part = (blockIdx.x / tiles) % nparts;
+    at.b = blockIdx.x / tiles / nparts;
+    at.first = at.b * (LOCAL ? S : S - 1);
+    at.len = a.lens ? min(max(a.lens[at.b], 0), a.L) : a.L;
+    at.part_len = part_len;
+    at.last = at.part == S - 1;
+  }
+  const int part = at.part, b = at.b;
   if (threadIdx.x == 0) {
     tc::mbar_init(&sm.full[0], 1);
     tc::mbar_init(&sm.full[1], 1);
@@ -161,18 +235,11 @@ __global__ void __launch_bounds__(kThreads, 4)
   __syncthreads();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sl = lane & (Sh::LN - 1), lc = lane / Sh::LN;
-  const int Eg = a.E / a.G;  // channels per group
-  const int gtiles = (Eg + Sh::CT - 1) / Sh::CT, tiles = gtiles * a.G;
-  const int nparts = MODE == kStates ? S - 1 : S;
-  const int tile = blockIdx.x % tiles;
-  const int part = (blockIdx.x / tiles) % nparts;
-  const int b = blockIdx.x / tiles / nparts;
   const int grp = tile / gtiles;
   const int cg = (tile % gtiles) * Sh::CT;      // first channel within the group
   const int e0 = grp * Eg + cg;                 // first channel
   const int nch = min(Sh::CT, Eg - cg);         // channels of this tile
-  const int len = a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
-  const int t0 = part * part_len, t1 = min(len, t0 + part_len);
+  const int t0 = part * at.part_len, t1 = min(at.len, t0 + at.part_len);
 
   const bool gated = MODE != kStates && a.z;
   T *y = OUT ? static_cast<T *>(a.y) + (int64_t)b * a.L * a.E + e0 : nullptr;
@@ -232,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       float4 r[kFold][4], sd[kFold];
 #pragma unroll
       for (int k = 0; k < kFold; ++k) {
-        const int64_t rc = ((int64_t)b * (S - 1) + q0 + k) * a.E + e0 + c0;
+        const int64_t rc = (int64_t)(at.first + q0 + k) * a.E + e0 + c0;
         const bool in = q0 + k < part && c0 < nch;  // widths are multiples of 8
         sd[k] = in ? *reinterpret_cast<const float4 *>(rec.dt + rc) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -419,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       for (int t8 = 0; t8 < Sh::TT; t8 += kCheckpoint) {
         const int k = (tb - t0 + t8) / kCheckpoint;
         if (k > 0 && tb + t8 < t1) {
-          const int64_t rc = (((int64_t)b * S + part) * (part_len / kCheckpoint - 1) + k - 1) * a.E + e0 + c0;
+          const int64_t rc = ((int64_t)(at.first + part) * (part_len / kCheckpoint - 1) + k - 1) * a.E + e0 + c0;
           store_states(rec.ck + rc * N + n0, h);
           store_dtsum(rec.ckdt + rc);
         }
@@ -466,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 
   // the state after this part: the record, or the final state
   if constexpr (OUT) {
-    if (part == S - 1 && a.hN) store_states(a.hN + ((int64_t)b * a.E + e0 + c0) * N + n0, h);
+    if (at.last && a.hN) store_states(a.hN + ((int64_t)b * a.E + e0 + c0) * N + n0, h);
   } else {
-    const int64_t rc = ((int64_t)b * nparts + part) * a.E + e0 + c0;
+    const int64_t rc = (int64_t)(at.first + part) * a.E + e0 + c0;
     store_states(rec.h + rc * N + n0, h);
     store_dtsum(rec.dt + rc);
     if constexpr (LOCAL) store_states(rec.g + rc * N + n0, adj);
@@ -488,7 +555,7 @@ cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &re
   if (e == cudaSuccess) e = most_shared(scan_kernel<T, N, MODE>);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)a.G * ((a.E / a.G + Sh::CT - 1) / Sh::CT);
-  const int64_t ctas = a.B * (MODE == kStates ? S - 1 : S) * tiles;
+  const int64_t ctas = (int64_t)a.B * (MODE == kStates && !a.lens ? S - 1 : S) * tiles;
   if (MODE == kOut && S > 1)  // behind the state pass
     return launch_dependent(scan_kernel<T, N, MODE>, (unsigned)ctas, 1, kThreads, smem, s, a, maps, rec, S,
                             part_len, timeouts);
@@ -496,12 +563,19 @@ cudaError_t launch_scan(const ScanArgs &a, const void *dy, const ScanRecords &re
   return cudaGetLastError();
 }
 
+// Tokens of a part, at least: kMaxParts of them hold any sequence.
+int max_parts_len(int L, int N) {
+  const int least = N > 32 ? N : 32, l = (L + kMaxParts - 1) / kMaxParts;
+  return l > least ? (l + kSteps - 1) / kSteps * kSteps : least;
+}
+
 template <typename T, int N>
 cudaError_t scan_typed(const ScanArgs &a, void *ws, int S, cudaStream_t s) {
-  const int part_len = selective_part_len(a.L, S);
+  // a ragged batch: the shortest part, the rest is decided on the device
+  const int part_len = a.lens && S > 1 ? max_parts_len(a.L, N) : selective_part_len(a.L, S);
   ScanRecords rec = {};
   rec.h = static_cast<float *>(ws);
-  rec.dt = rec.h + (size_t)a.B * (S - 1) * a.E * N;
+  rec.dt = rec.h + (size_t)a.B * (a.lens ? S : S - 1) * a.E * N;
   if (S > 1) {
     const cudaError_t e = launch_scan<T, N, kStates>(a, nullptr, rec, S, part_len, s);
     if (e != cudaSuccess) return e;
@@ -640,9 +714,6 @@ int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged) {
   // one wave of the output pass
   int64_t S = (int64_t)kSMs * (dt == kF32 ? resident<float>(N) : resident<__nv_bfloat16>(N)) /
               (ctas > 0 ? ctas : 1);
-  // some parts of a ragged batch are empty: a third more of them (three fp32
-  // prompts of 8191, 5461 and 2731 tokens: 106 us against 117)
-  if (ragged) S = S * 4 / 3;
   // parts of at least 32 tokens (B1 L512 E2048 N16 in bf16: 17.4 us; 64: 20.3,
   // 128: 32.9), and three of them: two walk as many tokens one after another
   // as one and its state pass (B16 L64 E1024 G4: 11.6 us, with two parts 14.1)
@@ -650,12 +721,13 @@ int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged) {
   if (most < 3) return 1;
   if (S > most) S = most;
   if (S < 2) return 1;
+  if (ragged) return static_cast<int>(S);  // parts, on average over the batch
   const int len = selective_part_len(L, static_cast<int>(S));
   return (L + len - 1) / len;  // no part is empty
 }
 
-size_t selective_workspace_bytes(int B, int E, int N, int S) {
-  return S > 1 ? sizeof(float) * (size_t)B * (S - 1) * E * (N + 1) : 0;
+size_t selective_workspace_bytes(int B, int E, int N, int S, bool ragged) {
+  return S > 1 ? sizeof(float) * (size_t)B * (ragged ? S : S - 1) * E * (N + 1) : 0;
 }
 
 cudaError_t launch_selective(const ScanArgs &a, Dtype dt, void *ws, int S, cudaStream_t s) {

@@ -152,6 +152,25 @@ def test_scan_ragged(la, dtype):
 
 
 @DT
+@pytest.mark.parametrize("B,L,E,N", [(3, 700, 64, 16), (40, 500, 8, 8), (100, 97, 16, 64), (2, 6000, 40, 32)])
+def test_scan_ragged_parts(la, dtype, B, L, E, N):
+    """Batches whose parts are laid out by the lengths: more sequences than a
+    warp has lanes, empty ones first and last, one long among short ones."""
+    a, more, d = scan_inputs(dtype, (B, L), E, N, 1, B)
+    lens = (torch.rand(B, generator=d.g) ** 3 * (L + 20)).to(torch.int32)
+    lens[0], lens[-1], lens[B // 2] = 0, -1, L
+    h0 = d.f(B, E, N)
+    y, h = la.forward_selective(**dev(a), **dev(more), h0=cuda(h0), lens=cuda(lens), return_state=True)
+    (ry, rh), (my, mh) = scan_ref(a, more, True, h0=h0.numpy(), lens=lens.numpy())
+    rows = np.arange(L)[None, :] < lens.numpy()[:, None]
+    close("scan ragged y", torch.where(torch.from_numpy(rows)[..., None].cuda(), y, 0), np.where(rows[..., None], ry, 0),
+          np.where(rows[..., None], my, 0), 80 * (L + 4), dtype)
+    close("scan ragged state", h, rh, mh, 80 * (L + 4), F32)
+    none = lens <= 0
+    assert torch.equal(h.cpu()[none], h0[none])
+
+
+@DT
 @pytest.mark.parametrize("shape", [(1, 8, 16, 1), (3, 72, 8, 1), (2, 64, 32, 2), (65, 96, 64, 4),
                                    (256, 4096, 16, 1)], ids=sid)
 def test_scan_step(la, dtype, shape):
