@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int cg = (tile % gtiles) * Sh::CT;      // first channel within the group
   const int e0 = grp * Eg + cg;                 // first channel
   const int nch = min(Sh::CT, Eg - cg);         // channels of this tile
-  const int t0 = part * at.part_len, t1 = min(at.len, t0 + at.part_len);
+  const int t0 = part * at.part_len, t1 = min(LOCAL ? a.L : at.len, t0 + at.part_len);
 
   const bool gated = MODE != kStates && a.z;
   T *y = OUT ? static_cast<T *>(a.y) + (int64_t)b * a.L * a.E + e0 : nullptr;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       for (int t8 = 0; t8 < Sh::TT; t8 += kCheckpoint) {
         const int k = (tb - t0 + t8) / kCheckpoint;
         if (k > 0 && tb + t8 < t1) {
-          const int64_t rc = ((int64_t)(at.first + part) * (part_len / kCheckpoint - 1) + k - 1) * a.E + e0 + c0;
+          const int64_t rc = (((int64_t)b * S + part) * (part_len / kCheckpoint - 1) + k - 1) * a.E + e0 + c0;
           store_states(rec.ck + rc * N + n0, h);
           store_dtsum(rec.ckdt + rc);
         }
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   if constexpr (OUT) {
     if (at.last && a.hN) store_states(a.hN + ((int64_t)b * a.E + e0 + c0) * N + n0, h);
   } else {
-    const int64_t rc = (int64_t)(at.first + part) * a.E + e0 + c0;
+    const int64_t rc = (LOCAL ? (int64_t)b * S + part : at.first + part) * a.E + e0 + c0;
     store_states(rec.h + rc * N + n0, h);
     store_dtsum(rec.dt + rc);
     if constexpr (LOCAL) store_states(rec.g + rc * N + n0, adj);
