@@ -449,7 +449,8 @@ LA_API size_t la_forward_noncausal_static_limit(void);
  * state after the last token (h0 for no tokens), the state
  * la_decode_selective continues from; it may not be h0 itself.  Few channels
  * split the tokens into up to 128 parts of 32 tokens or more, with a workspace of
- * B*E*(N + 1)*4 bytes for each part but one.
+ * B*E*(N + 1)*4 bytes for each part but one (each part of a ragged batch, whose
+ * parts are laid out over its sequences by their lengths).
  */
 LA_API la_status_t la_forward_selective(const void *x, const void *dt, const float *A,
                                         const void *Bm, const void *Cm, const float *D,

@@ -209,7 +209,8 @@ struct ScanArgs {
   bool softplus;
 };
 bool selective_states_supported(int N);
-// Sequence parts of the scan, tokens per part, and the workspace of the
+// Sequence parts of the scan (of a ragged batch: on average over its
+// sequences), tokens per part where they are not, and the workspace of the
 // parts' records (0 for one part).
 int selective_parts(int B, int L, int E, int N, int G, Dtype dt, bool ragged);
 int selective_part_len(int L, int S);

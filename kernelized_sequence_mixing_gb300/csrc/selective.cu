@@ -37,7 +37,9 @@
 // Few channels leave SMs idle, so the tokens split into S parts: the state
 // pass leaves every part but the last its end state from zero and its sum of
 // dt (the part's decay is exp(A sum dt): no product is kept), and the output
-// pass folds the records before its part in front of its own scan.
+// pass folds the records before its part in front of its own scan.  The parts
+// of a ragged batch are laid out over its sequences on the device, which knows
+// the lengths.
 #include "dependent.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
