@@ -603,6 +603,31 @@ def test_streams_and_graphs(la):
             assert (u is None and v is None) or torch.equal(u, v)
 
 
+def test_ragged_graph_replayed_with_other_lengths(la):
+    """The lengths are read when a graph runs, not when it was captured."""
+    B, L, E, N = 5, 900, 64, 16
+    a, more, d = scan_inputs(BF16, (B, L), E, N, 1, 17)
+    args = {**dev(a), **dev(more)}
+    x, w = d(B, L, E).cuda(), d.f(E, 4).cuda()
+    lens = torch.full((B,), L, dtype=torch.int32).cuda()
+    y, h = torch.zeros(B, L, E, dtype=BF16).cuda(), torch.zeros(B, E, N).cuda()
+    yc, sc = torch.zeros_like(y), torch.zeros(B, 3, E, dtype=BF16).cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        la.forward_selective(**args, lens=lens, out=y, h=h)
+        la.forward_conv(x, w, lens=lens, out=yc, state_out=sc)
+    for new in ([L] * B, [0, 1, 33, 900, 500], [900, 0, 0, 0, 2]):
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        for t in (y, h, yc, sc):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        want = la.forward_selective(**args, lens=lens, out=torch.zeros_like(y), return_state=True)
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+        want = la.forward_conv(x, w, lens=lens, out=torch.zeros_like(y), return_state=True)
+        assert torch.equal(yc, want[0]) and torch.equal(sc, want[1])
+
+
 def test_long_offsets(la):
     """Element offsets beyond 32 bits: the last sequence of a large batch."""
     B, L, E, W = 2, 1 << 20, 2048, 2
