@@ -524,8 +524,9 @@ __global__ void __launch_bounds__(kThreads, 4)
           if (gated) {
             f2 zv[2];
             load4p(&g.z[s], zv);
+            // silu(z) first: y z may overflow where silu(z) is zero
 #pragma unroll
-            for (int k = 0; k < 2; ++k) yv[k] = mul2(mul2(yv[k], zv[k]), sigmoid_f2(zv[k]));
+            for (int k = 0; k < 2; ++k) yv[k] = mul2(yv[k], mul2(zv[k], sigmoid_f2(zv[k])));
           }
           store4p(y + (int64_t)(tb + r) * a.E + qcol, yv);
         }
