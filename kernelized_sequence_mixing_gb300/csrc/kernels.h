@@ -9,6 +9,11 @@ namespace linattn {
 constexpr int kMaxHeads = 256;
 constexpr int kSMs = 152;  // of a GB300, for the rules that size grids
 
+// A runtime call that fails stays the thread's last error, where the check
+// behind a later launch would find it: whatever turns an error into a status
+// takes it away.
+inline void forget_error() { (void)cudaGetLastError(); }
+
 // Per-head decay values, passed to kernels by value.
 struct Gammas {
   float g[kMaxHeads];

@@ -55,10 +55,14 @@ la_status_t load_gammas(const float *gamma, int H, Gammas *g, bool *decay) {
   return LA_OK;
 }
 
+la_status_t failed() {
+  forget_error();
+  return LA_ERR_CUDA;
+}
+
 la_status_t from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return LA_OK;
-  if (e == cudaErrorNotSupported) return LA_ERR_UNSUPPORTED;
-  return LA_ERR_CUDA;
+  return e == cudaErrorNotSupported ? LA_ERR_UNSUPPORTED : failed();
 }
 
 la_status_t run_forward(const Problem &p, const Gammas &g, int causal, cudaStream_t s);
@@ -85,12 +89,13 @@ int la_causal_kernel(int B, int H, int N, int D, int Dv, const float *gamma,
 
 int la_device_wait_timeouts(int reset) {
   unsigned int *ctr = wait_timeout_counter();
-  if (!ctr) return -1;
+  if (!ctr) return forget_error(), -1;
   unsigned int v = 0;
-  if (cudaMemcpy(&v, ctr, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return -1;
+  if (cudaMemcpy(&v, ctr, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return forget_error(), -1;
   if (reset) {
     const unsigned int zero = 0;
-    if (cudaMemcpy(ctr, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return -1;
+    if (cudaMemcpy(ctr, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
+      return forget_error(), -1;
   }
   return static_cast<int>(v);
 }
@@ -172,7 +177,7 @@ la_status_t run_forward(const Problem &p, const Gammas &g, int causal, cudaStrea
       const int P = chunk128_parts(BH, N);
       const size_t wsb = chunk128_workspace_bytes(BH, P);
       void *ws = nullptr;
-      if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return LA_ERR_CUDA;
+      if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return failed();
       cudaError_t e = launch_causal_chunk128(p, g, ws, P, s);
       cudaError_t ef = ws ? cudaFreeAsync(ws, s) : cudaSuccess;
       if (e != cudaSuccess) return from_cuda(e);
@@ -184,7 +189,7 @@ la_status_t run_forward(const Problem &p, const Gammas &g, int causal, cudaStrea
       const int P = chunk_parts(BH, N);
       const size_t wsb = chunk_causal_workspace_bytes(BH, P, D, Dv);
       void *ws = nullptr;
-      if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return LA_ERR_CUDA;
+      if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return failed();
       cudaError_t e = launch_causal_chunk(p, g, ws, P, s);
       cudaError_t ef = ws ? cudaFreeAsync(ws, s) : cudaSuccess;
       if (e != cudaSuccess) return from_cuda(e);
@@ -196,7 +201,7 @@ la_status_t run_forward(const Problem &p, const Gammas &g, int causal, cudaStrea
   // apply them to every query (bf16: persistent tensor-core passes).
   if (noncausal_tc_supported(p)) {
     void *ws = nullptr;
-    if (cudaMallocAsync(&ws, noncausal_tc_workspace_bytes(p), s) != cudaSuccess) return LA_ERR_CUDA;
+    if (cudaMallocAsync(&ws, noncausal_tc_workspace_bytes(p), s) != cudaSuccess) return failed();
     cudaError_t e = launch_noncausal_tc(p, ws, s);
     cudaError_t ef = cudaFreeAsync(ws, s);
     if (e != cudaSuccess) return from_cuda(e);
@@ -206,7 +211,7 @@ la_status_t run_forward(const Problem &p, const Gammas &g, int causal, cudaStrea
   const size_t part_bytes = kv_state_workspace_bytes(BH, N, D, Dv);
   void *ws = nullptr;
   cudaError_t e = cudaMallocAsync(&ws, state_bytes + part_bytes, s);
-  if (e != cudaSuccess) return LA_ERR_CUDA;
+  if (e != cudaSuccess) return failed();
   float *S = static_cast<float *>(ws);
   float *z = S + (size_t)BH * D * Dv;
   float *part = part_bytes ? z + (size_t)BH * D : nullptr;
@@ -282,9 +287,9 @@ la_status_t run_forward_host(const void *q, const void *k, const void *v, void *
                              int N, int D, int Dv, int causal, const Gammas &g, float eps, Dtype dt,
                              cudaStream_t s) {
   cudaStream_t up = nullptr, down = nullptr;
-  if (!copy_streams(&up, &down)) return LA_ERR_CUDA;
+  if (!copy_streams(&up, &down)) return failed();
   cudaMemPool_t pool = host_path_pool();
-  if (!pool) return LA_ERR_CUDA;
+  if (!pool) return failed();
   const size_t es = dt == kF32 ? 4 : 2;
   const size_t head_qk = (size_t)N * D * es, head_v = (size_t)N * Dv * es;
   const size_t nqk = (size_t)B * H * head_qk, nvv = (size_t)B * H * head_v;
@@ -298,7 +303,7 @@ la_status_t run_forward_host(const void *q, const void *k, const void *v, void *
   const int G = B * gpb;
   uint8_t *dbuf = nullptr;
   if (cudaMallocFromPoolAsync(reinterpret_cast<void **>(&dbuf), 2 * nqk + 2 * nvv, pool, s) != cudaSuccess)
-    return LA_ERR_CUDA;
+    return failed();
   uint8_t *dq = dbuf, *dk = dq + nqk, *dv = dk + nqk, *dout = dv + nvv;
   std::vector<cudaEvent_t> ev(2 * G + 2, nullptr);
   la_status_t st = LA_OK;
@@ -357,6 +362,7 @@ la_status_t run_forward_host(const void *q, const void *k, const void *v, void *
   if (cudaFreeAsync(dbuf, s) != cudaSuccess && st == LA_OK) st = LA_ERR_CUDA;
   for (auto &e : ev)
     if (e) cudaEventDestroy(e);  // released once the work they mark is done
+  if (st != LA_OK) forget_error();
   return st;
 }
 
@@ -394,7 +400,7 @@ la_status_t la_prefill_state(const void *k, const void *v, float *S, float *z,
     const int P = chunk_state_parts(BH, N, D, Dv);
     void *ws = nullptr;
     if (cudaMallocAsync(&ws, chunk_workspace_bytes(BH, P, D, Dv), s) != cudaSuccess)
-      return LA_ERR_CUDA;
+      return failed();
     cudaError_t e = launch_prefill_chunk(k, v, S, z, B, H, N, D, Dv, decay, g, ws, P, s);
     cudaError_t ef = cudaFreeAsync(ws, s);
     if (e != cudaSuccess) return from_cuda(e);
@@ -403,7 +409,7 @@ la_status_t la_prefill_state(const void *k, const void *v, float *S, float *z,
   const size_t part_bytes = kv_state_workspace_bytes(BH, N, D, Dv);
   void *ws = nullptr;
   if (part_bytes) {
-    if (cudaMallocAsync(&ws, part_bytes, s) != cudaSuccess) return LA_ERR_CUDA;
+    if (cudaMallocAsync(&ws, part_bytes, s) != cudaSuccess) return failed();
   }
   cudaError_t e = launch_kv_state(k, v, S, z, static_cast<float *>(ws), B, H,
                                   N, D, Dv, decay, g,
@@ -431,7 +437,7 @@ la_status_t la_forward_state(const void *q, const void *k, const void *v, void *
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (N == 0) {
     if (cudaMemsetAsync(S, 0, nS, s) != cudaSuccess || cudaMemsetAsync(z, 0, nz, s) != cudaSuccess)
-      return LA_ERR_CUDA;
+      return failed();
     return LA_OK;
   }
   if (!q || !k || !v || !o) return LA_ERR_INVALID_ARG;
@@ -450,7 +456,7 @@ la_status_t la_forward_state(const void *q, const void *k, const void *v, void *
     const int P = chunk128_parts(BH, N);
     const size_t wsb = chunk128_workspace_bytes(BH, P);
     void *ws = nullptr;
-    if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return LA_ERR_CUDA;
+    if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return failed();
     cudaError_t e = launch_causal_chunk128(p, g, ws, P, s, S, z);
     cudaError_t ef = ws ? cudaFreeAsync(ws, s) : cudaSuccess;
     if (e != cudaSuccess) return from_cuda(e);
@@ -506,7 +512,7 @@ la_status_t la_forward_gated(const void *q, const void *k, const void *v, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (N == 0) {
     if (S && (cudaMemsetAsync(S, 0, nS, s) != cudaSuccess || cudaMemsetAsync(z, 0, nz, s) != cudaSuccess))
-      return LA_ERR_CUDA;
+      return failed();
     return LA_OK;
   }
   if (!q || !k || !v || !a || !o) return LA_ERR_INVALID_ARG;
@@ -529,7 +535,7 @@ la_status_t la_forward_gated(const void *q, const void *k, const void *v, const 
   const bool tc = gla_tc_supported(p);
   const size_t wsb = wsb_simt + (tc ? gla_tc_workspace_bytes(BH, N) : 0);
   void *ws = nullptr;
-  if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return LA_ERR_CUDA;
+  if (wsb && cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return failed();
   cudaError_t e = cudaSuccess;
   const int *hard = nullptr;
   if (tc) {
@@ -621,7 +627,7 @@ la_status_t la_forward_favor(const void *q, const void *k, const void *v, const 
   // the features of q and k, [B][H][N][r] each, in a stream-ordered workspace
   const size_t nf = (((size_t)rows * r * es) + 255) & ~(size_t)255;
   void *ws = nullptr;
-  if (cudaMallocAsync(&ws, 2 * nf, s) != cudaSuccess) return LA_ERR_CUDA;
+  if (cudaMallocAsync(&ws, 2 * nf, s) != cudaSuccess) return failed();
   void *fq = ws, *fk = static_cast<uint8_t *>(ws) + nf;
   la_status_t out = from_cuda(launch_favor_features(q, k, W, fq, fk, rows, D, r, dt, s));
   if (out == LA_OK) {
@@ -669,7 +675,7 @@ la_status_t la_backward(const void *q, const void *k, const void *v, const void 
   const bool tc = backward_tc_supported(p, g);
   void *ws = nullptr;
   const size_t wsb = tc ? backward_tc_workspace_bytes(B * H, N, D) : backward_workspace_bytes(B * H, N, D, Dv);
-  if (cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return LA_ERR_CUDA;
+  if (cudaMallocAsync(&ws, wsb, s) != cudaSuccess) return failed();
   const cudaError_t e = tc ? launch_backward_tc(p, dO, dq, dk, dv, g, ws, s)
                            : launch_backward(p, dO, dq, dk, dv, g, ws, s);
   const cudaError_t ef = cudaFreeAsync(ws, s);

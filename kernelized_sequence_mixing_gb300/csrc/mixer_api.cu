@@ -50,6 +50,7 @@ Dtype to_dtype(la_dtype_t dt) { return dt == LA_F32 ? kF32 : kBF16; }
 
 la_status_t status(cudaError_t e) {
   if (e == cudaSuccess) return LA_OK;
+  forget_error();
   return e == cudaErrorNotSupported ? LA_ERR_UNSUPPORTED : LA_ERR_CUDA;
 }
 
@@ -111,7 +112,8 @@ la_status_t with_workspace(size_t bytes, cudaStream_t s, F &&f) {
   if (bytes == 0) return status(f(nullptr));
   cudaMemPool_t pool = workspace_pool();
   void *ws = nullptr;
-  if (!pool || cudaMallocFromPoolAsync(&ws, bytes, pool, s) != cudaSuccess) return LA_ERR_CUDA;
+  if (!pool || cudaMallocFromPoolAsync(&ws, bytes, pool, s) != cudaSuccess)
+    return status(cudaErrorMemoryAllocation);
   const cudaError_t e = f(ws);
   const cudaError_t ef = cudaFreeAsync(ws, s);
   return status(e != cudaSuccess ? e : ef);

@@ -82,7 +82,10 @@ la_status_t la_forward_noncausal_static(const void *q, const void *k, const void
   while (nsplit > 1 && per_state * (1 + (size_t)nsplit) > kScratchBytes) --nsplit;
 
   float *scratch = scratch_on_current_device();  // first call on a device: one query
-  if (!scratch) return LA_ERR_CUDA;
+  if (!scratch) {
+    forget_error();
+    return LA_ERR_CUDA;
+  }
   float *S = scratch;
   float *z = S + (size_t)BH * D * Dv;
   float *part = nsplit > 1 ? z + (size_t)BH * D : nullptr;
@@ -94,8 +97,9 @@ la_status_t la_forward_noncausal_static(const void *q, const void *k, const void
   // this call, so nothing has to be cleared between calls
   cudaError_t e = launch_kv_state_splits(k, v, S, z, part, B, H, N, D, Dv, nsplit, g, dt, s);
   if (e == cudaSuccess) e = launch_noncausal_apply(q, S, z, o, BH, N, D, Dv, eps, dt, s);
-  if (e == cudaErrorNotSupported) return LA_ERR_UNSUPPORTED;
-  return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+  if (e == cudaSuccess) return LA_OK;
+  forget_error();
+  return e == cudaErrorNotSupported ? LA_ERR_UNSUPPORTED : LA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -76,3 +76,41 @@ def test_infinite_gates(la, dtype):
         assert torch.equal(g[i][..., other], g0[i][..., other])
     for i in (2, 5, 7):  # dA, dD, d(dt_bias)
         assert torch.equal(g[i][other], g0[i][other])
+
+
+@pytest.mark.parametrize("what", ["scan backward", "non-causal forward"])
+def test_calls_behind_a_failed_workspace(la, what):
+    """A call whose workspace is larger than the card reports it; the call
+    behind it, whatever it is, checks its own launches and is not affected."""
+    free, total = torch.cuda.mem_get_info()
+    if free < 20 << 30:
+        pytest.skip("needs 20 GB")
+    a, more, d = scan_inputs(F32, (2, 90), 64, 16, 1, 23)
+    args, dy, w = {**dev(a), **dev(more)}, d(2, 90, 64).cuda(), d.f(64, 4).cuda()
+    one = {k: v[:, 0].contiguous() if k in ("x", "dt", "Bm", "Cm", "z") else v for k, v in args.items()}
+    h, st, wn = torch.ones(2, 64, 16, device="cuda"), torch.ones(2, 3, 64, device="cuda"), w[:, 0].contiguous()
+    q, gates, S = d(1, 2, 70, 64).cuda(), torch.full((1, 2, 70, 64), 0.5, device="cuda"), torch.ones(1, 2, 64, 64, device="cuda")
+    q1 = q[:, :, 0].contiguous()
+    small = [lambda: [la.forward_selective(**args)], lambda: la.backward_selective(**args, dy=dy)[:8],
+             lambda: [la.decode_selective(**one, h=h.clone())], lambda: [la.forward_conv(dy, w)],
+             lambda: la.backward_conv(dy, w, dy)[:2], lambda: [la.decode_conv(dy[:, 0], w, st.clone())],
+             lambda: [la.forward_norm_gate(dy.view(2, 1, 90, 64), dy)], lambda: la.backward_norm_gate(dy.view(2, 1, 90, 64), dy, dy)[:2],
+             lambda: la.forward_norm_residual(dy), lambda: la.backward_norm_residual(dy, dy, wn),
+             lambda: [la.forward(q, q, q)], lambda: [la.forward(q, q, q, causal=False)], lambda: la.prefill_state(q, q),
+             lambda: [la.forward_gated(q, q, q, gates)], lambda: la.backward(q, q, q, q),
+             lambda: [la.decode_step(q1, q1, q1, S.clone(), S[..., 0].contiguous())], lambda: [dy + 1]]
+    want = [f() for f in small]
+    if what == "scan backward":  # two states of 64 fp32 per channel of 65536
+        E, N = 65536, 64
+        B = total // (E * N * 8) + 1000
+        x, m = torch.empty(B, 1, E, dtype=BF16, device="cuda"), torch.empty(B, 1, 1, N, dtype=BF16, device="cuda")
+        big = lambda: la.backward_selective(x, x, torch.empty(E, N, device="cuda"), m, m, x)  # noqa: E731
+    else:  # a state of 128 x 129 fp32 per head, of one token each
+        x = torch.empty(total // (256 * 128 * 129 * 4) + 1000, 256, 1, 128, device="cuda")
+        big = lambda: la.forward(x, x, x, causal=False)  # noqa: E731
+    for f, ref in zip(small, want):
+        with pytest.raises(la.LinAttnError) as e:
+            big()
+        assert e.value.code == 3
+        for u, v in zip(f(), ref):
+            assert torch.equal(u, v)
