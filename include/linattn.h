@@ -428,7 +428,7 @@ LA_API size_t la_forward_noncausal_static_limit(void);
  *   output are read in place; 0 means dense rows.  A stride is a multiple of 8
  *   and at least the row's width; outputs are dense.
  * - Sizes: E a multiple of 8 up to 65536, E / G a multiple of 8, N in {8, 16,
- *   32, 64}, fewer than 2^31 tokens and B E < 2^31.
+ *   32, 64}, B L < 2^31 - 2^16 tokens and B E < 2^31.
  * - lens (optional, int32 [B] in DEVICE memory, 4-byte aligned): sequence b
  *   has lens[b] tokens (clamped to [0, L]).  Rows behind it have no
  *   effect and are left alone in the outputs, and the final state is the one after the last token.

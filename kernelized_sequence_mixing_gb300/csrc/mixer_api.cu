@@ -15,6 +15,9 @@ using namespace linattn;
 namespace {
 
 constexpr int kMaxWidth = 65536;
+// Tokens of a batch: parts and runs are rounded up in 32 bits, by less than
+// 2^16 in all.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - (1 << 16);
 
 // A buffer of a call: where it is, how many bytes its elements span, and what
 // the call needs of it.
@@ -68,7 +71,7 @@ bool stride_ok(long long *ld, int64_t width) {
 la_status_t check_width(int B, int L, int E) {
   if (B < 0 || L < 0 || E < 0) return LA_ERR_INVALID_ARG;
   if (E % 8 != 0 || E > kMaxWidth) return LA_ERR_UNSUPPORTED;
-  if ((int64_t)B * (L > 0 ? L : 1) >= ((int64_t)1 << 31) || (int64_t)B * E >= ((int64_t)1 << 31))
+  if ((int64_t)B * (L > 0 ? L : 1) >= kMaxTokens || (int64_t)B * E >= ((int64_t)1 << 31))
     return LA_ERR_UNSUPPORTED;
   return LA_OK;
 }
