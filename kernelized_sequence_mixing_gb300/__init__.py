@@ -576,6 +576,13 @@ def wait_selftest(cycles=2_000_000) -> bool:
 # --- selective state space scan, short convolution, norms around a block ---
 
 
+def _c_ints(fn, *sizes):
+    """Sizes that reach the library as C ints, which ctypes cuts to 32 bits
+    without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"{fn}: sizes of 2^31 and more are not supported (got {sizes})")
+
+
 def _tokens(fn, name, t, lead, row, dtype):
     """The token stride (0: dense) of an input [*lead, *row] of ``dtype`` whose
     rows are contiguous; lead is (B, L), with L token strides between
@@ -622,6 +629,7 @@ def _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, dims):
     *lead, E = x.shape
     lead = tuple(lead)
     G, N = Bm.shape[-2:]
+    _c_ints(fn, *lead, E, G, N)
     tok, grp = lead + (E,), lead + (G, N)
     lds = []
     for name, t, shape in (("x", x, tok), ("dt", dt, tok), ("z", z, tok), ("Bm", Bm, grp), ("Cm", Cm, grp)):
@@ -730,6 +738,7 @@ def _conv_args(fn, x, w, bias, dims):
     _dtype_code(x)
     lead, E = tuple(x.shape[:-1]), x.shape[-1]
     W = w.shape[1]
+    _c_ints(fn, *lead, E, W)
     _param(fn, "w", w, (E, W))
     _param(fn, "bias", bias, (E,))
     return lead, E, W, _tokens(fn, "x", x, lead, (E,), x.dtype)
@@ -815,6 +824,7 @@ def _norm_gate_args(fn, y, gate, w, heads_first, extra=()):
     B, H, L, D = y.shape
     if not heads_first:
         H, L = L, H
+    _c_ints(fn, B, H, L, D)
     for n, t in (("gate", gate),) + tuple(extra):
         if t is not None:
             _expect(fn, n, t, (B, L, H * D), y.dtype)
@@ -867,6 +877,7 @@ def _rows(fn, name, t, others, w):
         if o is not None:
             _expect(fn, n, o, t.shape, t.dtype)
     E = t.shape[-1]
+    _c_ints(fn, E)
     _param(fn, "w", w, (E,))
     return (t.numel() // E if E else 0), E
 
