@@ -2,6 +2,8 @@
 // fp32 values for the packed instructions, eight-element vectors of either
 // element type, softplus and SiLU.
 #pragma once
+#include <float.h>
+
 #include "common.cuh"
 
 namespace linattn {
@@ -63,6 +65,11 @@ __device__ __forceinline__ f2 ex2_2(f2 a) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// A decay rate that is no lower than the lowest finite value: a step of zero
+// (of a row behind the end, for one) keeps the state, and zero times infinity
+// would not.  NaN stays NaN.
+__device__ __forceinline__ float finite_rate(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }
 
 // softplus(x) = max(x, 0) + log1p(exp(-|x|)).  log1p(t)/t on [0, 1] is the
 // degree-7 Chebyshev interpolant (relative error 3.2e-7 in fp32 arithmetic,

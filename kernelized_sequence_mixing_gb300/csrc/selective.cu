@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         if (OUT && a.h0)
           r = *reinterpret_cast<const float4 *>(a.h0 + ((int64_t)b * a.E + e0 + c0 + c) * N + n0);
       }
-      av[c][0] = q.x * kLog2e; av[c][1] = q.y * kLog2e;
-      av[c][2] = q.z * kLog2e; av[c][3] = q.w * kLog2e;
+      av[c][0] = finite_rate(q.x * kLog2e); av[c][1] = finite_rate(q.y * kLog2e);
+      av[c][2] = finite_rate(q.z * kLog2e); av[c][3] = finite_rate(q.w * kLog2e);
       hv[c][0] = r.x; hv[c][1] = r.y; hv[c][2] = r.z; hv[c][3] = r.w;
     }
 #pragma unroll
@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const __grid_constant__ 
   const bool in = e < a.E;
   const int ec = in ? e : 0;
   const int goff = (a.G == 1 ? 0 : ec / (a.E / a.G)) * N + sl * 4;
-  const float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)ec * N + sl * 4);
+  float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)ec * N + sl * 4);
+  A = make_float4(finite_rate(A.x), finite_rate(A.y), finite_rate(A.z), finite_rate(A.w));
   const float bias = a.dt_bias ? a.dt_bias[ec] : 0.f, skip = a.D ? a.D[ec] : 0.f;
   for (int b0 = blockIdx.y * U; b0 < a.B; b0 += gridDim.y * U) {
     float4 h[U];

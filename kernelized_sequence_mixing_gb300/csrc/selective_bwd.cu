@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kCarryThreads)
   if (i >= a.B * EN) return;
   const int64_t b = i / EN, en = i - b * EN;
   const int e = static_cast<int>(en / a.N);
-  const f2 A = mul2(load_f2(a.A + en), dup2(kLog2e));
+  const float2 rate = unpack2(mul2(load_f2(a.A + en), dup2(kLog2e)));
+  const f2 A = pack2(finite_rate(rate.x), finite_rate(rate.y));
   const bool back = blockIdx.y == 1;
   const float *from = back ? dhN : a.h0;
   f2 acc = from ? load_f2(from + i) : dup2(0.f);
@@ -300,16 +301,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int64_t en = (int64_t)(e0 + c0) * N + n0;            // within [E][N]
   const int64_t ben = (int64_t)b * a.E * N + en;             // within [B][E][N]
   const int64_t pen = ((int64_t)b * S + seg) * a.E * N + en;  // within the records
-  auto load_pair = [&](const float *p, f2 (&v)[4], float scale) {
+  auto load_pair = [&](const float *p, f2 (&v)[4]) {
     float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
     if (p && cin) {
       lo = *reinterpret_cast<const float4 *>(p);
       hi = *reinterpret_cast<const float4 *>(p + N);
     }
-    v[0] = pack2(lo.x * scale, hi.x * scale);
-    v[1] = pack2(lo.y * scale, hi.y * scale);
-    v[2] = pack2(lo.z * scale, hi.z * scale);
-    v[3] = pack2(lo.w * scale, hi.w * scale);
+    v[0] = pack2(lo.x, hi.x);
+    v[1] = pack2(lo.y, hi.y);
+    v[2] = pack2(lo.z, hi.z);
+    v[3] = pack2(lo.w, hi.w);
   };
   auto store_pair = [&](float *p, const f2 (&v)[4]) {
     if (!cin) return;
@@ -318,10 +319,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     *reinterpret_cast<float4 *>(p + N) = make_float4(q0.y, q1.y, q2.y, q3.y);
   };
   f2 A[4], hin[4], gc[4], dA[4];
-  load_pair(a.A + en, A, kLog2e);
+  load_pair(a.A + en, A);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const float2 q = unpack2(mul2(A[n], dup2(kLog2e)));
+    A[n] = pack2(finite_rate(q.x), finite_rate(q.y));
+  }
   wait_for_previous();
-  load_pair(S > 1 ? rec.s.h + pen : a.h0 ? a.h0 + ben : nullptr, hin, 1.f);
-  load_pair(S > 1 ? rec.s.g + pen : gr.dhN ? gr.dhN + ben : nullptr, gc, 1.f);
+  load_pair(S > 1 ? rec.s.h + pen : a.h0 ? a.h0 + ben : nullptr, hin);
+  load_pair(S > 1 ? rec.s.g + pen : gr.dhN ? gr.dhN + ben : nullptr, gc);
 #pragma unroll
   for (int n = 0; n < 4; ++n) dA[n] = dup2(0.f);
   // The checkpoint in front of token group k of the part (k > 0), asked for
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       copy8_async(&sm.ckdt[tid * 2], rec.s.ckdt + rc, cin);
       copies_commit();
     } else {
-      load_pair(rec.s.ck + rc * N + n0, ck, 1.f);
+      load_pair(rec.s.ck + rc * N + n0, ck);
       cksd = cin ? load_f2(rec.s.ckdt + rc) : dup2(0.f);
     }
   };

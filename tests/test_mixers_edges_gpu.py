@@ -114,3 +114,39 @@ def test_calls_behind_a_failed_workspace(la, what):
         assert e.value.code == 3
         for u, v in zip(f(), ref):
             assert torch.equal(u, v)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(1, 13, 64, 16, 1), (2, 70, 40, 8, 1), (1, 333, 264, 16, 3), (1, 333, 40, 64, 1)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_states_that_forget_at_once(la, dtype, shape):
+    """Rates at the lowest fp32 value: a decay of zero at every token, and
+    none at the rows behind a part's end, which hold no step."""
+    B, L, E, N, G = shape
+    a, more, d = scan_inputs(dtype, (B, L), E, N, G, L)
+    a["A"][:, ::3] = torch.finfo(F32).min
+    h0, dh, dy = d.f(B, E, N), d.f(B, E, N), d(B, L, E)
+    K = 80 * (L + 4) + N
+    y, h = la.forward_selective(**dev(a), **dev(more), h0=cuda(h0), return_state=True)
+    (ry, rh), (my, mh) = scan_ref(a, more, True, h0=h0.numpy())
+    close("scan lowest rates y", y, ry, my, K, dtype)
+    close("scan lowest rates state", h, rh, mh, K, F32)
+    got = la.backward_selective(**dev(a), dy=dy.cuda(), **dev(more), h0=cuda(h0), dh=cuda(dh))
+    kw = {**host(a), **host(more), "dy": dy.float().numpy(), **host({"h0": h0, "dh": dh})}
+    ref, mag = osel.scan_backward(**kw), osel.scan_backward(**kw, mag=True)
+    for name, v in zip(GRADS, got):
+        close("scan lowest rates " + name, v, ref[name], mag[name], 160 * (L + 8) + E + B * L, v.dtype)
+    # an infinite rate is the same decay; a ragged batch ends inside a tile
+    a["A"][:, ::3] = float("-inf")
+    assert torch.equal(la.forward_selective(**dev(a), **dev(more), h0=cuda(h0)), y)
+    lens = torch.full((B,), max(L - 5, 1), dtype=torch.int32)
+    y, h = la.forward_selective(**dev(a), **dev(more), h0=cuda(h0), lens=cuda(lens), out=torch.zeros_like(y), return_state=True)
+    (ry, rh), (my, mh) = scan_ref(a, more, True, h0=h0.numpy(), lens=lens.numpy())
+    close("scan infinite rates y", y, ry, my, K, dtype)
+    close("scan infinite rates state", h, rh, mh, K, F32)
+    one = {k: v[:, 0] if k in ("x", "dt", "Bm", "Cm", "z") else v for k, v in {**a, **more}.items()}
+    hs = cuda(h0).clone()
+    y = la.decode_selective(**dev(one), h=hs)
+    (ry, rh), (my, mh) = [osel.scan_step(**host(one), h=h0.numpy(), mag=m) for m in (False, True)]
+    close("scan infinite rates step y", y, ry, my, 80 * 5 + N, dtype)
+    close("scan infinite rates step state", hs, rh, mh, 80 * 5, F32)
