@@ -125,13 +125,6 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// Eight consecutive elements as fp32; `p` is 16-byte aligned.
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4 *>(p);
-  const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
 __device__ __forceinline__ void bf16x2_to_f32(uint32_t u, float &lo, float &hi) {
   lo = __uint_as_float(u << 16);
   hi = __uint_as_float(u & 0xffff0000u);
@@ -141,28 +134,18 @@ __device__ __forceinline__ f2 bf16x2_to_f2(uint32_t u) {
   bf16x2_to_f32(u, lo, hi);
   return pack2(lo, hi);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4 *>(p);
-  bf16x2_to_f32(a.x, x[0], x[1]);
-  bf16x2_to_f32(a.y, x[2], x[3]);
-  bf16x2_to_f32(a.z, x[4], x[5]);
-  bf16x2_to_f32(a.w, x[6], x[7]);
-}
 __device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-}
+// Eight consecutive elements, rounded once; `p` is 16-byte aligned.
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
   *reinterpret_cast<uint4 *>(p) =
       make_uint4(f32_to_bf16x2(x[0], x[1]), f32_to_bf16x2(x[2], x[3]), f32_to_bf16x2(x[4], x[5]),
                  f32_to_bf16x2(x[6], x[7]));
 }
 
-// The same as four pairs.
+// Eight consecutive elements as four pairs; `p` is 16-byte aligned.
 __device__ __forceinline__ void load8p(const float *p, f2 (&x)[4]) {
   const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
   const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(p + 4);
@@ -233,21 +216,12 @@ template <> struct raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
     a = *reinterpret_cast<const uint4 *>(p);
   }
-  __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
-    *reinterpret_cast<uint4 *>(p) = a;
-  }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void getp(f2 (&x)[4]) const {
     x[0] = bf16x2_to_f2(a.x);
     x[1] = bf16x2_to_f2(a.y);
     x[2] = bf16x2_to_f2(a.z);
     x[3] = bf16x2_to_f2(a.w);
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    bf16x2_to_f32(a.x, x[0], x[1]);
-    bf16x2_to_f32(a.y, x[2], x[3]);
-    bf16x2_to_f32(a.z, x[4], x[5]);
-    bf16x2_to_f32(a.w, x[6], x[7]);
   }
 };
 template <> struct raw8<float> {
@@ -256,20 +230,12 @@ template <> struct raw8<float> {
     a = *reinterpret_cast<const float4 *>(p);
     b = *reinterpret_cast<const float4 *>(p + 4);
   }
-  __device__ __forceinline__ void store(float *p) const {
-    *reinterpret_cast<float4 *>(p) = a;
-    *reinterpret_cast<float4 *>(p + 4) = b;
-  }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void getp(f2 (&x)[4]) const {
     x[0] = pack2(a.x, a.y);
     x[1] = pack2(a.z, a.w);
     x[2] = pack2(b.x, b.y);
     x[3] = pack2(b.z, b.w);
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
 };
 
