@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from helpers import record
 from oracle import selective as osel
 from test_mixers_gpu import BF16, DT, F32, Draw, close, cuda, dev, host, la, n64, scan_inputs, scan_ref  # noqa: F401
 
@@ -150,3 +151,49 @@ def test_states_that_forget_at_once(la, dtype, shape):
     (ry, rh), (my, mh) = [osel.scan_step(**host(one), h=h0.numpy(), mag=m) for m in (False, True)]
     close("scan infinite rates step y", y, ry, my, 80 * 5 + N, dtype)
     close("scan infinite rates step state", hs, rh, mh, 80 * 5, F32)
+
+
+def close_in_norm(name, got, ref, tol, dtype):
+    """||got - ref|| against tol and half a step of the output's type, both of
+    ||ref||."""
+    rel = np.linalg.norm(n64(got) - ref) / np.linalg.norm(ref)
+    bound = tol + (0 if dtype == F32 else torch.finfo(dtype).eps / 2)
+    record(f"{name} {str(dtype)[6:]} (norm)", rel, bound)
+    assert rel <= bound, f"{name}: {rel}, bound {bound}"
+
+
+# Several parts, groups, channel tiles, all numbers of states.
+MANY_PARTS = [(2, 400, 264, 8, 1), (1, 700, 528, 16, 2), (1, 500, 264, 32, 1), (2, 300, 72, 64, 1), (3, 1500, 16, 16, 1)]
+
+
+@DT
+@pytest.mark.parametrize("shape", MANY_PARTS, ids=lambda s: "x".join(map(str, s)))
+def test_many_parts_in_norm(la, dtype, shape):
+    """The scan over many parts, norm-wise: fewer bits in a record or a
+    checkpoint show here, where the element bounds are far wider.
+
+    A state remembers 1 / (dt |A|) tokens, at most about 1 / (0.01 x 0.05) =
+    2000 with these inputs, and takes about 5.5 roundings a token (the
+    exponential 4, the product and sum 1.5; the exponent of a state that
+    remembers long is near zero).  Independent roundings add up as
+    sqrt(2000) x 5.5 = 250 of 2^-24: 1.5e-5, 2e-5 with what stands around the
+    recurrence.  Gradients take a second recurrence: 4e-5.  A record in bf16
+    would be off by 2^-9 / sqrt(3) = 1.1e-3 of itself."""
+    B, L, E, N, G = shape
+    a, more, d = scan_inputs(dtype, (B, L), E, N, G, 3 * L + N)
+    h0, dh, dy = d.f(B, E, N), d.f(B, E, N), d(B, L, E)
+    p = {**dev(a), **dev(more), "h0": cuda(h0)}
+    y, h = la.forward_selective(**p, return_state=True)
+    hp = {**host(a), **host(more), "h0": h0.numpy()}
+    ry, rh = osel.scan(**hp)
+    close_in_norm("scan y", y, ry, 2e-5, dtype)
+    close_in_norm("scan state", h, rh, 2e-5, F32)
+    lens = (torch.rand(B, generator=d.g) * L).to(torch.int32) + 1
+    y, h = la.forward_selective(**p, lens=cuda(lens), out=torch.zeros_like(y), return_state=True)
+    ry, rh = osel.scan(**hp, lens=lens.numpy())
+    close_in_norm("scan ragged y", y, ry, 2e-5, dtype)
+    close_in_norm("scan ragged state", h, rh, 2e-5, F32)
+    got = la.backward_selective(**p, dy=dy.cuda(), dh=cuda(dh))
+    ref = osel.scan_backward(**hp, dy=dy.float().numpy(), dh=dh.numpy())
+    for name, v in zip(GRADS, got):
+        close_in_norm("scan " + name, v, ref[name], 4e-5, v.dtype)
