@@ -445,7 +445,10 @@ LA_API size_t la_forward_noncausal_static_limit(void);
  *   dt_t = softplus(dt_t + dt_bias)   (softplus = 0: the plain sum)
  *   h_t  = exp(dt_t A) h_(t-1) + dt_t x_t B_t,      h_(-1) = h0 (NULL: zeros)
  *   y_t  = (sum_n C_t h_t + D x_t) silu(z_t)
- * D, z and dt_bias may be NULL (no such term).  hN (optional) receives the
+ * D, z and dt_bias may be NULL (no such term).  States are meant to decay
+ * (dt_t A <= 0; any rate down to -inf): the tokens are worked in parts, and
+ * where exp(A sum dt) over a part leaves the fp32 range a result may be inf or
+ * NaN although its own token-by-token terms are finite.  hN (optional) receives the
  * state after the last token (h0 for no tokens), the state
  * la_decode_selective continues from; it may not be h0 itself.  Few channels
  * split the tokens into up to 128 parts of 32 tokens or more, with a workspace of
@@ -485,11 +488,14 @@ LA_API la_status_t la_decode_selective(const void *x, const void *dt, const floa
  * States are recomputed (the caller keeps no forward state).  dx, ddt, dz
  * [B][L][E] and dBm, dCm [B][L][G][N] are dense, of `dtype`; dA, dD, ddt_bias
  * and dh0 fp32.  dD, ddt_bias and dh0 may be NULL and need their input; dz is
- * given exactly when z is.  A batch padded at the end is handled by zero rows
- * of dy (a later token does not reach an earlier one).  The workspace is about
- * B*L*E*(N/8 + 2N/64 + N*N/512) floats (11 bytes per token and channel for
- * N = 16): a state every 8 tokens, two per part of 64 tokens (32 or 48 for N = 8),
- * and the channel tiles' sums of dB and dC.
+ * given exactly when z is.  A batch padded at the end is given zero rows of dy
+ * and finite values in the padding of the other inputs (a later token does not
+ * reach an earlier one, but zero times NaN is NaN); with dhN also steps of zero
+ * there (raw dt -inf under softplus), which carry the state to the end.  The
+ * workspace is about B*L*E*(9N/64 + N*N/512) floats (11 bytes per token and
+ * channel for N = 16): per part of 64 tokens (32 or 48 for N = 8) seven states
+ * within it, one in front and one adjoint behind, and the channel tiles' sums
+ * of dB and dC.
  */
 LA_API la_status_t la_backward_selective(
     const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
@@ -521,6 +527,7 @@ LA_API la_status_t la_decode_conv(const void *x, const float *w, const float *bi
  * gradient dy: dx [B][L][E] and dstate [B][W-1][E] (optional, needs state) of
  * `dtype`, dw [E][W] and dbias [E] (optional, needs bias) fp32.  A gradient of
  * state_out is one of x's last rows (or of state's): the caller adds it there.
+ * A batch padded at the end is given zero rows of dy and finite rows of x there.
  */
 LA_API la_status_t la_backward_conv(const void *x, const float *w, const float *bias,
                                     const void *state, const void *dy, void *dx, float *dw,
@@ -536,7 +543,9 @@ LA_API la_status_t la_backward_conv(const void *x, const float *w, const float *
  * gate and out are token-major [B][L][H*D], as the projections before and
  * behind it hold them; all of `dtype`.  w [H][D] fp32 (NULL: ones).  D a
  * multiple of 8 up to 8192, H*D up to 65536, fewer than 2^31 rows; eps finite
- * and >= 0.  out may not overlap an input.
+ * and >= 0.  All tensors are dense; out may not overlap an input.  The sum of
+ * squares is fp32: a row for which it overflows (values beyond 2^64 / sqrt(D))
+ * gives zeros.
  */
 LA_API la_status_t la_forward_norm_gate(const void *y, const void *gate, const float *w, void *out,
                                         int B, int H, int L, int D, int heads_first,
@@ -556,9 +565,9 @@ LA_API la_status_t la_backward_norm_gate(const void *y, const void *gate, const 
  * Scaled residual sum and the RMS norm ahead of the next block, over rows of E
  * values of `dtype`:
  *   r = residual + scale x  (residual NULL: scale x),  o = r rsqrt(mean r^2 + eps) w.
- * The norm takes the fp32 sum; r is also written, rounded.  w [E] fp32 (NULL:
- * ones).  E a multiple of 8 up to 8192, fewer than 2^31 rows.  o and r may not
- * overlap an input or each other.
+ * The norm takes the fp32 sum r (and an fp32 sum of squares, as above); r is
+ * also written, rounded.  w [E] fp32 (NULL: ones).  E a multiple of 8 up to
+ * 8192, fewer than 2^31 rows.  o and r may not overlap an input or each other.
  */
 LA_API la_status_t la_forward_norm_residual(const void *x, const void *residual, const float *w,
                                             void *o, void *r, long long rows, int E, float scale,

@@ -654,7 +654,8 @@ def forward_selective(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=T
     silu(z_t).  x, dt, z: [B, L, E]; Bm, Cm: [B, L, G, N] CUDA tensors of one
     dtype, dense or slices of a dense tensor's rows; A: [E, N], D, dt_bias: [E]
     and h0: [B, E, N] float32; lens: [B] int32 tokens per sequence (rows behind
-    have no effect and stay unwritten).  Returns y, or (y, h [B, E, N] float32) with
+    have no effect and stay unwritten).  States are meant to decay (steps times A
+    not positive).  Returns y, or (y, h [B, E, N] float32) with
     the state after the last token when return_state is true (or h is given)."""
     fn = "forward_selective"
     (B, L), E, N, G, lds = _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, 3)
@@ -706,7 +707,9 @@ def backward_selective(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softp
     """Gradients of y (and the final state) = forward_selective(...) for the
     upstream gradients dy [B, L, E] of y and, if given, dh [B, E, N] float32
     of the final state.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0);
-    dD, dz, ddt_bias and dh0 are None where their input is."""
+    dD, dz, ddt_bias and dh0 are None where their input is.  A batch padded at
+    the end takes zero rows of dy and finite padding, with dh also steps of zero
+    there (raw dt -inf under softplus)."""
     fn = "backward_selective"
     (B, L), E, N, G, lds = _scan_args(fn, x, dt, A, Bm, Cm, D, z, dt_bias, 3)
     _expect(fn, "dy", dy, (B, L, E), x.dtype)
@@ -797,7 +800,8 @@ def decode_conv(x, w, state, bias=None, silu=True, out=None):
 def backward_conv(x, w, dy, bias=None, silu=True, state=None):
     """Gradients (dx, dw, dbias, dstate) of forward_conv(x, w, bias, silu,
     state) for the upstream gradient dy [B, L, E]; dbias and dstate are None
-    where their input is."""
+    where their input is.  A batch padded at the end takes zero rows of dy and
+    finite rows of x there."""
     fn = "backward_conv"
     (B, L), E, W, ld = _conv_args(fn, x, w, bias, 3)
     _expect(fn, "dy", dy, (B, L, E), x.dtype)
@@ -835,8 +839,8 @@ def _norm_gate_args(fn, y, gate, w, heads_first, extra=()):
 def forward_norm_gate(y, gate, w=None, eps=1e-5, gate_first=False, heads_first=True, out=None):
     """RMS norm of each head's rows with a SiLU gate: norm(y) w silu(gate), or
     norm(y silu(gate)) w when gate_first.  y: [B, H, L, D] as forward() returns
-    it, or [B, L, H, D] with heads_first=False; gate: [B, L, H*D]; one dtype;
-    w: [H, D] float32.  Returns o: [B, L, H*D]."""
+    it, or [B, L, H, D] with heads_first=False; gate: [B, L, H*D]; one dtype,
+    contiguous; w: [H, D] float32.  Returns o: [B, L, H*D]."""
     fn = "forward_norm_gate"
     B, H, L, D = _norm_gate_args(fn, y, gate, w, heads_first, (("out", out),))
     dev = _one_device(fn, (("y", y), ("gate", gate), ("w", w), ("out", out)))

@@ -197,3 +197,34 @@ def test_many_parts_in_norm(la, dtype, shape):
     ref = osel.scan_backward(**hp, dy=dy.float().numpy(), dh=dh.numpy())
     for name, v in zip(GRADS, got):
         close_in_norm("scan " + name, v, ref[name], 4e-5, v.dtype)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(3, 75, 64, 16, 1), (2, 300, 72, 8, 1), (2, 130, 40, 64, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_backward_of_a_padded_batch(la, dtype, shape):
+    """Rows of padding with a raw step of -inf (softplus: a step of zero) and
+    zero rows of dy: every sequence gets the gradients that it has alone, also
+    through its final state, and the padding none but dz = 0."""
+    B, L, E, N, G = shape
+    a, more, d = scan_inputs(dtype, (B, L), E, N, G, 31)
+    h0, dh, dy = d.f(B, E, N), d.f(B, E, N), d(B, L, E)
+    lens = [L - 1 - (b * L) // (B + 1) for b in range(B)]
+    for b, n in enumerate(lens):
+        a["dt"][b, n:] = float("-inf")
+        dy[b, n:] = 0
+    got = la.backward_selective(**dev(a), dy=dy.cuda(), **dev(more), h0=cuda(h0), dh=cuda(dh))
+    parts = []
+    for b, n in enumerate(lens):
+        one = {k: v[b:b + 1, :n] if k in ("x", "dt", "Bm", "Cm", "z") else v for k, v in {**a, **more}.items()}
+        kw = {**host(one), "dy": dy[b:b + 1, :n].float().numpy(), **host({"h0": h0[b:b + 1], "dh": dh[b:b + 1]})}
+        parts.append([osel.scan_backward(**kw, mag=m) for m in (False, True)])
+    K = 160 * (L + 8) + E + B * L
+    for name, v in zip(GRADS, got):
+        if name in ("dA", "dD", "ddt_bias"):  # sums over the batch
+            close("scan padded " + name, v, sum(r[name] for r, _ in parts), sum(m[name] for _, m in parts), K, F32)
+            continue
+        for b, (ref, mag) in enumerate(parts):
+            own = v[b:b + 1] if name == "dh0" else v[b:b + 1, :lens[b]]
+            close("scan padded " + name, own, ref[name], mag[name], K, v.dtype)
+            if name != "dh0":
+                assert (v[b, lens[b]:] == 0).all(), name
