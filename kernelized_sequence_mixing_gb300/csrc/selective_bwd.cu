@@ -32,8 +32,8 @@
 // the main pass owns 2 channels x 4 states (packed pairs of channels).  Sums over
 // states cross N/4 lanes by transposing exchanges, two tokens at a time; sums
 // over channels cross the other lanes and the CTA's warps in shared memory.
-// (B2 L4096 E2048 N16 in bf16, the whole backward pass: 407 us; both kinds by
-// exchanges 414, both in shared memory 431.)
+// (B2 L4096 E2048 N16 in bf16, the whole backward pass: 399 us; when this was
+// chosen 407, both kinds by exchanges 414, both in shared memory 431.)
 #include "column_sum.cuh"
 #include "dependent.cuh"
 #include "kernels.h"
