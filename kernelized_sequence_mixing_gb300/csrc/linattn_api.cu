@@ -62,7 +62,8 @@ la_status_t failed() {
 
 la_status_t from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return LA_OK;
-  return e == cudaErrorNotSupported ? LA_ERR_UNSUPPORTED : failed();
+  const la_status_t st = failed();
+  return e == cudaErrorNotSupported ? LA_ERR_UNSUPPORTED : st;
 }
 
 la_status_t run_forward(const Problem &p, const Gammas &g, int causal, cudaStream_t s);
