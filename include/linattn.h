@@ -26,8 +26,9 @@
  *                 ("Choosing the Feature Map"), the map alone and the
  *                 attention over it.
  * Beside them stand the selective state space scan with its short causal
- * convolution, and the norms before and after a mixing block (see "Selective
- * state space scan" below).
+ * convolution, the norms before and after a mixing block (see "Selective
+ * state space scan" below), retention (the decayed form without feature map and
+ * normaliser) and beam search over decode states.
  * eps is added to the denominator after the dot product, as in the NumPy
  * listing on "Linear Attention Mechanisms" (sadullah.online), "The linear
  * attention trick".
@@ -583,6 +584,117 @@ LA_API la_status_t la_backward_norm_residual(const void *r, const float *w, cons
                                              const void *dr, void *dresidual, void *dx, float *dw,
                                              long long rows, int E, float scale, float eps,
                                              la_dtype_t dtype, void *stream);
+
+/*
+ * Retention: linear attention with one decay per head, q and k as they are (no
+ * feature map) and no normaliser (the retention of "Gating and Selective State
+ * Updates" and "Evolution: add decay/gating": RetNet, gamma^(t-j)):
+ *
+ *   S_t = gamma S_(t-1) + k_t v_t^T,   o_t = scale q_t^T S_t,   S_(-1) = S0.
+ *
+ * Conventions of this family, besides those at the top:
+ * - q [B][L][H][D], k [B][L][Hk][D], v [B][L][Hk][Dv], o [B][L][H][Dv] of
+ *   `dtype`; Hk divides H, and H / Hk consecutive heads of q share one of k and
+ *   v.  Each (b, h) has its own state [D][Dv], fp32, caller-owned.
+ * - strides (HOST array of 12, or NULL for dense tensors as above): elements
+ *   between batches, tokens and heads of q, k, v and o (la_backward_retention:
+ *   dO), so that slices of a projection's output and tensors laid out heads
+ *   first are read in place.  Multiples of 8, rows contiguous and apart from
+ *   one another; the stride of a dimension of size 1 is not looked at.
+ * - Sizes: D and Dv multiples of 8 up to 256, H <= 256, B L < 2^31 - 2^16
+ *   tokens, B H < 2^26.  scale is finite and not 0.
+ * - lens (optional, int32 [B] in DEVICE memory, 4-byte aligned): sequence b has
+ *   lens[b] tokens (clamped to [0, L]).  Rows behind it are not read and have no
+ *   effect; outputs there are left alone, gradients there are zero; the final
+ *   state is the one after the last token.
+ * - Arithmetic: fp32 states and sums, each output rounded once.  For LA_BF16
+ *   with D, Dv in {64, 128} (forward: Dv any multiple of 32) the products run on
+ *   tcgen05 tensor cores: there the weights of a chunk are rounded to bf16, the
+ *   states and the decayed rows that build them enter as sums of two bf16 values
+ *   (three where a state is returned, which then has fp32 accuracy).  Results do
+ *   not depend on scheduling (no atomics).
+ * - Within a chunk of up to 128 tokens a weight of zero times an infinity or NaN
+ *   of a later token is NaN: inputs are finite.
+ * - Few (batch, head) pairs split long sequences into parts that run side by
+ *   side, with a workspace of B*H*D*Dv*4 bytes for each part but one.
+ *   Workspaces as in the selective scan's family; no written buffer may overlap
+ *   any other buffer of the call.
+ */
+
+/*
+ * Whole sequences: o and, unless S is NULL, the state after the last token,
+ * which la_decode_retention continues from.  S0 [B][H][D][Dv] fp32 (NULL:
+ * zeros) may not be S itself.
+ */
+LA_API la_status_t la_forward_retention(const void *q, const void *k, const void *v, const float *S0,
+                                        const int *lens, void *o, float *S, int B, int L, int H,
+                                        int Hk, int D, int Dv, const long long *strides,
+                                        const float *gamma, float scale, la_dtype_t dtype,
+                                        void *stream);
+
+/*
+ * One token of each of B sequences, in place on states S [pool][H][D][Dv]:
+ * sequence b has state slots[b] (int32 [B] in DEVICE memory; NULL: state b,
+ * pool >= B).  A slot outside [0, pool) marks an idle row of a padded batch:
+ * nothing of it is read or written, its row of o is left alone.  No slot may
+ * occur twice.  q, o [B][H][*], k, v [B][Hk][*]; ldq, ldk, ldv: elements between
+ * consecutive sequences' rows, 0 for dense (as in the selective scan's family).
+ */
+LA_API la_status_t la_decode_retention(const void *q, const void *k, const void *v, float *S,
+                                       const int *slots, void *o, int B, int pool, int H, int Hk,
+                                       int D, int Dv, long long ldq, long long ldk, long long ldv,
+                                       const float *gamma, float scale, la_dtype_t dtype,
+                                       void *stream);
+
+/*
+ * Gradients of la_forward_retention for the upstream gradients dO of o and,
+ * unless NULL, dS [B][H][D][Dv] fp32 of the final state.  With
+ * U_t = dL/dS_t = gamma U_(t+1) + scale q_t dO_t^T (gamma U behind the last
+ * token: dS):
+ *   dq_t = scale S_t dO_t,  dk_t = U_t v_t,  dv_t = U_t^T k_t,  dS0 = gamma U_0,
+ * dk and dv summed over the heads that share them.  dq, dk, dv are dense, of
+ * `dtype`; dS0 fp32 (NULL: not wanted; needs S0).  Nothing of the forward pass
+ * is kept: the states are computed again.  Shared heads take a workspace of
+ * B*L*H*(D + Dv)*4 bytes more.
+ */
+LA_API la_status_t la_backward_retention(const void *q, const void *k, const void *v,
+                                         const void *dO, const float *S0, const float *dS,
+                                         const int *lens, void *dq, void *dk, void *dv, float *dS0,
+                                         int B, int L, int H, int Hk, int D, int Dv,
+                                         const long long *strides, const float *gamma, float scale,
+                                         la_dtype_t dtype, void *stream);
+
+/*
+ * Beam search between two decode steps.  For each of B requests the n best of
+ * its K beams' continuations: beam k with token v scores
+ *   scores[b][k] + logits[b][k][v] - log sum_u exp(logits[b][k][u]).
+ * out_scores fp32, parents and tokens int32, all [B][n], best first; equal
+ * scores in the order of k, then v.  finished (optional, bytes [B][K]): a beam
+ * that has ended, whose one continuation is `eos` at its own score.  A beam
+ * whose score or log-sum is not finite (a start's unused beams at -inf, a row
+ * with a NaN or +inf) offers nothing, nor does a logit of -inf (a forbidden
+ * token); places beyond the last continuation get score -inf, parent and token
+ * -1.  logits of `dtype` with ld elements between rows (0: V), scores fp32;
+ * no alignment beyond the elements' own.  K <= 32, n <= 64, V <= 2^30.  Scores
+ * are compared in 64 bits, sums of exponentials are fp32 within pieces of at
+ * most 8192 logits and 64-bit over them.  Workspace: 8 n + 8 bytes a piece.
+ */
+LA_API la_status_t la_select_beams(const void *logits, const float *scores,
+                                   const unsigned char *finished, float *out_scores, int *parents,
+                                   int *tokens, int B, int K, int V, int n, long long ld, int eos,
+                                   la_dtype_t dtype, void *stream);
+
+/*
+ * The beams' states after a selection: for each of `count` buffers, states[i]
+ * [B][K] records of bytes[i] bytes (HOST arrays of device pointers and sizes;
+ * the states of la_decode_retention, la_decode_step, la_decode_selective and
+ * la_decode_conv, tokens so far), record k of request b is replaced in place by
+ * record parents[b][k].  A parent outside [0, K) keeps the beam's own.  No two
+ * buffers may overlap.  K <= 32.  Buffers of 16-byte records on 16-byte
+ * boundaries move fastest.
+ */
+LA_API la_status_t la_reorder_states(void *const *states, const long long *bytes, int count,
+                                     const int *parents, int B, int K, void *stream);
 
 /* Static, NUL-terminated description of a status code. */
 LA_API const char *la_status_string(la_status_t s);

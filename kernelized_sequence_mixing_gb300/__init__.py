@@ -33,6 +33,15 @@ block:
   backward_norm_gate(y, gate, do, w=None, eps=1e-5, gate_first=False, heads_first=True)
   forward_norm_residual(x, residual=None, w=None, scale=1.0, eps=1e-5, out=None, r=None)
   backward_norm_residual(r, do, w=None, dr=None, scale=1.0, eps=1e-5)
+
+Retention (decayed linear attention without feature map and normaliser) and
+beam search over decode states:
+  forward_retention(q, k, v, gamma=None, scale=1.0, S0=None, lens=None, out=None,
+                    return_state=False, S=None)
+  decode_retention(q, k, v, S, gamma=None, scale=1.0, slots=None, out=None)
+  backward_retention(q, k, v, do, gamma=None, scale=1.0, S0=None, dS=None, lens=None)
+  select_beams(logits, scores, n=None, finished=None, eos=None)
+  reorder_states(states, parents)
 """
 from __future__ import annotations
 
@@ -51,6 +60,8 @@ __all__ = ["forward", "prefill_state", "decode_step", "forward_state",
            "forward_conv", "decode_conv", "backward_conv",
            "forward_norm_gate", "backward_norm_gate",
            "forward_norm_residual", "backward_norm_residual",
+           "forward_retention", "decode_retention", "backward_retention",
+           "select_beams", "reorder_states",
            "status_string",
            "device_wait_timeouts", "causal_kernel", "backward_kernel",
            "load_library", "library_path", "LinAttnError", "workloads"]
@@ -143,6 +154,17 @@ def load_library() -> ctypes.CDLL:
             lib.la_forward_norm_residual.restype = I
             lib.la_backward_norm_residual.argtypes = [P] * 7 + [LL, I, F, F, I, P]
             lib.la_backward_norm_residual.restype = I
+            LP = ctypes.POINTER(LL)
+            lib.la_forward_retention.argtypes = [P] * 7 + [I] * 6 + [LP, P, F, I, P]
+            lib.la_forward_retention.restype = I
+            lib.la_decode_retention.argtypes = [P] * 6 + [I] * 6 + [LL] * 3 + [P, F, I, P]
+            lib.la_decode_retention.restype = I
+            lib.la_backward_retention.argtypes = [P] * 11 + [I] * 6 + [LP, P, F, I, P]
+            lib.la_backward_retention.restype = I
+            lib.la_select_beams.argtypes = [P] * 6 + [I] * 4 + [LL, I, I, P]
+            lib.la_select_beams.restype = I
+            lib.la_reorder_states.argtypes = [ctypes.POINTER(P), LP, I, P, I, I, P]
+            lib.la_reorder_states.restype = I
             lib.la_wait_selftest.argtypes = [ctypes.c_longlong, ctypes.POINTER(I)]
             lib.la_wait_selftest.restype = I
             lib.la_device_wait_timeouts.argtypes = [I]
@@ -921,3 +943,221 @@ def backward_norm_residual(r, do, w=None, dr=None, scale=1.0, eps=1e-5):
             _ptr(r), _ptr(w), _ptr(do), _ptr(dr), _ptr(dres), _ptr(dx), _ptr(dw), rows, E,
             float(scale), float(eps), _DTYPES[r.dtype], _stream(dev)))
     return dres, (dres if dx is None else dx), dw
+
+
+# --- retention, beam search over decode states ---
+
+
+def _decays(gamma, H):
+    """gamma as the C calls take it, a host array of H floats: a contiguous
+    float32 host tensor as it is, anything else through _gamma_arg."""
+    if isinstance(gamma, torch.Tensor) and gamma.dtype is torch.float32 and gamma.device.type == "cpu" \
+            and gamma.shape == (H,) and gamma.is_contiguous():
+        return gamma.data_ptr()
+    return _gamma_arg(gamma, H)
+
+
+def _heads(fn, name, t, shape, dtype):
+    """The strides (batch, token, head) of t: ``shape`` [B, L, heads, width] and
+    ``dtype``, rows contiguous and apart from one another."""
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    *outer, last = t.stride()
+    sizes = t.shape
+    if last != 1 and sizes[3] > 1:
+        raise ValueError(f"{fn}: the rows of {name} must be contiguous (strides {t.stride()})")
+    inner = sizes[3]
+    for stride, size in sorted(zip(outer, sizes)):
+        if size > 1 and t.numel():
+            if stride % 8 or stride < inner:
+                raise ValueError(f"{fn}: rows of {name} must be apart from one another, a multiple of 8 "
+                                 f"elements each way (strides {t.stride()})")
+            inner += stride * (size - 1)
+    return outer
+
+
+def _retention_args(fn, q, k, v, gamma, scale, extra=()):
+    """Checks shared by the whole-sequence calls; ``extra`` [(name, tensor)] are
+    further tensors shaped like o.  Returns (B, L, H, Hk, D, Dv, the strides of
+    q, k, v and of the last of ``extra``)."""
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"{fn}: expected q: [B, L, H, D], k: [B, L, Hk, D] and v: [B, L, Hk, Dv]")
+    _dtype_code(q)
+    B, L, H, D = q.shape
+    Hk, Dv = v.shape[2:]
+    if H and (Hk == 0 or H % Hk):
+        raise ValueError(f"{fn}: the {Hk} heads of k and v must divide the {H} heads of q")
+    _c_ints(fn, B, L, H, D, Dv)
+    strides = (_heads(fn, "q", q, (B, L, H, D), q.dtype) + _heads(fn, "k", k, (B, L, Hk, D), q.dtype)
+               + _heads(fn, "v", v, (B, L, Hk, Dv), q.dtype))
+    last = [L * H * Dv, H * Dv, Dv]
+    for name, t in extra:
+        if t is not None:
+            last = _heads(fn, name, t, (B, L, H, Dv), q.dtype)
+    return B, L, H, Hk, D, Dv, (ctypes.c_longlong * 12)(*strides, *last)
+
+
+def forward_retention(q, k, v, gamma=None, scale=1.0, S0=None, lens=None, out=None,
+                      return_state=False, S=None):
+    """Retention: S_t = gamma S_(t-1) + k_t v_t^T, o_t = scale q_t^T S_t, with
+    one decay per head, no feature map and no normaliser.  q: [B, L, H, D]; k:
+    [B, L, Hk, D]; v: [B, L, Hk, Dv] with Hk dividing H (heads of q that share
+    one of k and v follow one another); CUDA tensors of one dtype with
+    contiguous rows and any strides (slices of a projection's output; tensors
+    [B, H, L, D] as t.transpose(1, 2)).  gamma: None, a float, or H decays in
+    [0, 1] (a float32 host tensor is passed on as it is); S0: [B, H, D, Dv]
+    float32; lens: [B] int32 tokens per sequence (rows behind have no effect and
+    stay unwritten).  Returns o [B, L, H, Dv], or (o, S [B, H, D, Dv] float32)
+    with the state after the last token when return_state is true (or S is
+    given)."""
+    fn = "forward_retention"
+    B, L, H, Hk, D, Dv, strides = _retention_args(fn, q, k, v, gamma, scale, (("out", out),))
+    _param(fn, "S0", S0, (B, H, D, Dv))
+    _param(fn, "S", S, (B, H, D, Dv))
+    _lens(fn, lens, B)
+    dev = _one_device(fn, (("q", q), ("k", k), ("v", v), ("S0", S0), ("lens", lens), ("out", out), ("S", S)))
+    lib = load_library()
+    with _on(dev):
+        if out is None:
+            out = torch.empty((B, L, H, Dv), dtype=q.dtype, device=dev)
+        if S is None and return_state:
+            S = torch.empty((B, H, D, Dv), dtype=torch.float32, device=dev)
+        _check("la_forward_retention", lib.la_forward_retention(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(S0), _ptr(lens), _ptr(out), _ptr(S), B, L, H, Hk, D, Dv,
+            strides, _decays(gamma, H), float(scale), _DTYPES[q.dtype], _stream(dev)))
+    return out if S is None else (out, S)
+
+
+def _step_rows(fn, name, t, B, heads, width, dtype):
+    if t.shape == (B, heads, width) and t.dtype is dtype and t.is_contiguous():
+        return 0
+    return _tokens(fn, name, t, (B,), (heads, width), dtype)
+
+
+def decode_retention(q, k, v, S, gamma=None, scale=1.0, slots=None, out=None):
+    """One token of retention, in place on S.  q: [B, H, D]; k: [B, Hk, D]; v:
+    [B, Hk, Dv] (dense, or slices of a dense tensor's rows); S: [B, H, D, Dv]
+    float32, or a pool [P, H, D, Dv] of states with slots: [B] int32, each
+    sequence's place in it (no place twice; a place outside the pool marks an
+    idle row, which stays unwritten).  Returns o: [B, H, Dv]."""
+    fn = "decode_retention"
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or S.dim() != 4:
+        raise ValueError(f"{fn}: expected q: [B, H, D], k: [B, Hk, D], v: [B, Hk, Dv] and S: [B, H, D, Dv]")
+    _dtype_code(q)
+    B, H, D = q.shape
+    Hk, Dv = v.shape[1:]
+    if H and (Hk == 0 or H % Hk):
+        raise ValueError(f"{fn}: the {Hk} heads of k and v must divide the {H} heads of q")
+    pool = S.shape[0]
+    _c_ints(fn, B, H, D, Dv, pool)
+    ldq = _step_rows(fn, "q", q, B, H, D, q.dtype)
+    ldk = _step_rows(fn, "k", k, B, Hk, D, q.dtype)
+    ldv = _step_rows(fn, "v", v, B, Hk, Dv, q.dtype)
+    _expect(fn, "S", S, (B if slots is None else pool, H, D, Dv), torch.float32)
+    if slots is not None:
+        _expect(fn, "slots", slots, (B,), torch.int32)
+    if out is not None:
+        _expect(fn, "out", out, (B, H, Dv), q.dtype)
+    dev = _one_device(fn, (("q", q), ("k", k), ("v", v), ("S", S), ("slots", slots), ("out", out)))
+    lib = load_library()
+    with _on(dev):
+        if out is None:
+            out = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
+        _check("la_decode_retention", lib.la_decode_retention(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(S), _ptr(slots), _ptr(out), B, pool, H, Hk, D, Dv,
+            ldq, ldk, ldv, _decays(gamma, H), float(scale), _DTYPES[q.dtype], _stream(dev)))
+    return out
+
+
+def backward_retention(q, k, v, do, gamma=None, scale=1.0, S0=None, dS=None, lens=None):
+    """Gradients (dq, dk, dv, dS0) of forward_retention for the upstream
+    gradients do [B, L, H, Dv] of o and, if given, dS [B, H, D, Dv] float32 of
+    the final state; dS0 is None without S0.  The gradients are dense tensors in
+    the shapes of q, k and v; rows behind a sequence's lens get zeros."""
+    fn = "backward_retention"
+    B, L, H, Hk, D, Dv, strides = _retention_args(fn, q, k, v, gamma, scale, (("do", do),))
+    _param(fn, "S0", S0, (B, H, D, Dv))
+    _param(fn, "dS", dS, (B, H, D, Dv))
+    _lens(fn, lens, B)
+    dev = _one_device(fn, (("q", q), ("k", k), ("v", v), ("do", do), ("S0", S0), ("dS", dS), ("lens", lens)))
+    lib = load_library()
+    with _on(dev):
+        new = lambda *shape: torch.empty(shape, dtype=q.dtype, device=dev)  # noqa: E731
+        dq, dk, dv = new(B, L, H, D), new(B, L, Hk, D), new(B, L, Hk, Dv)
+        dS0 = torch.empty_like(S0) if S0 is not None else None
+        _check("la_backward_retention", lib.la_backward_retention(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(do), _ptr(S0), _ptr(dS), _ptr(lens), _ptr(dq), _ptr(dk), _ptr(dv),
+            _ptr(dS0), B, L, H, Hk, D, Dv, strides, _decays(gamma, H), float(scale), _DTYPES[q.dtype],
+            _stream(dev)))
+    return dq, dk, dv, dS0
+
+
+def select_beams(logits, scores, n=None, finished=None, eos=None):
+    """The n (default K) best continuations of each request's beams: beam k with
+    token v scores scores[b, k] + log_softmax(logits[b, k])[v].  logits:
+    [B, K, V] float32 or bfloat16, rows contiguous, evenly apart (a slice of a
+    padded vocabulary); scores: [B, K] float32; finished: [B, K] bool, beams that
+    have ended (their one continuation is the token eos, at no cost).  Returns
+    (scores float32, parents int32, tokens int32), all [B, n], best first, equal
+    scores in the order of beam and token; places that no continuation fills
+    hold -inf, -1, -1."""
+    fn = "select_beams"
+    if logits.dim() != 3:
+        raise ValueError(f"{fn}: expected logits: [B, K, V]")
+    code = _dtype_code(logits)
+    B, K, V = logits.shape
+    n = K if n is None else int(n)
+    if K < 1 or V < 1 or not 1 <= n <= K * V:
+        raise ValueError(f"{fn}: n must be between 1 and K * V (got n = {n} of {K} * {V})")
+    _c_ints(fn, B, K, V)
+    ld = V
+    if not logits.is_contiguous():
+        sb, ld, last = logits.stride()
+        if K == 1:
+            ld = sb if B > 1 else V
+        if (last != 1 and V > 1) or ld < V or (B > 1 and K > 1 and sb != K * ld):
+            raise ValueError(f"{fn}: the rows of logits must be contiguous and evenly apart (strides {logits.stride()})")
+    _expect(fn, "scores", scores, (B, K), torch.float32)
+    if finished is not None:
+        _expect(fn, "finished", finished, (B, K), torch.bool)
+        if eos is None or not 0 <= int(eos) < V:
+            raise ValueError(f"{fn}: finished needs eos, a token in [0, {V})")
+    dev = _one_device(fn, (("logits", logits), ("scores", scores), ("finished", finished)))
+    lib = load_library()
+    with _on(dev):
+        best = torch.empty((B, n), dtype=torch.float32, device=dev)
+        parents, tokens = (torch.empty((B, n), dtype=torch.int32, device=dev) for _ in range(2))
+        _check("la_select_beams", lib.la_select_beams(
+            _ptr(logits), _ptr(scores), _ptr(finished), _ptr(best), _ptr(parents), _ptr(tokens), B, K, V, n, ld,
+            0 if eos is None else int(eos), code, _stream(dev)))
+    return best, parents, tokens
+
+
+def reorder_states(states, parents):
+    """The beams' states after a selection, in place: state[b, k] becomes
+    state[b, parents[b, k]] for every tensor of ``states`` (one tensor or a
+    sequence of them; [B, K, ...] or [B * K, ...], contiguous, any dtype: the
+    states of the decode calls, tokens so far).  parents: [B, K] int32; one
+    outside [0, K) keeps the beam's own state.  Returns ``states``."""
+    fn = "reorder_states"
+    tensors = (states,) if isinstance(states, torch.Tensor) else tuple(states)
+    if parents.dim() != 2:
+        raise ValueError(f"{fn}: expected parents: [B, K]")
+    B, K = parents.shape
+    _expect(fn, "parents", parents, (B, K), torch.int32)
+    for i, t in enumerate(tensors):
+        _contig(f"states[{i}]", t)
+        if t.shape[:2] != (B, K) and (t.dim() < 1 or t.shape[0] != B * K):
+            raise ValueError(f"{fn}: states[{i}] must be [{B}, {K}, ...] or [{B * K}, ...], got {tuple(t.shape)}")
+    _c_ints(fn, B, K)
+    dev = _one_device(fn, [("parents", parents)] + [(f"states[{i}]", t) for i, t in enumerate(tensors)])
+    lib = load_library()
+    count = len(tensors)
+    rows = max(1, B * K)
+    ptrs = (ctypes.c_void_p * count)(*[t.data_ptr() for t in tensors])
+    sizes = (ctypes.c_longlong * count)(*[t.numel() * t.element_size() // rows for t in tensors])
+    with _on(dev):
+        _check("la_reorder_states", lib.la_reorder_states(ptrs, sizes, count, _ptr(parents), B, K, _stream(dev)))
+    return states

@@ -1,0 +1,477 @@
+// Beam search over decode states: the n best continuations of each request,
+// and the states' reordering.
+//
+// Selection.  A continuation (k, v) of request b scores
+//   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]).
+// Within a beam the order of continuations is the order of its logits, so one
+// pass over the logits serves: each CTA takes a piece of a row that fits its
+// registers and leaves the piece's maximum, its sum of exponentials relative to
+// that, and its n largest logits in order (ties: lowest index first).  A second
+// kernel, one CTA per request, joins the sums in 64 bits and takes the n best
+// of the sorted lists.  Bound by HBM (the logits are read once) with one
+// exponential per logit beside it (16 a clock and SM).
+//
+// The n largest of a piece: the n-th largest of the threads' own maxima bounds
+// the n-th largest value from below (n <= threads), and what is not below that
+// bound is collected, in expectation little more than n values.  Many equal
+// logits can be more than the buffer holds; then the list is taken value by
+// value (n rounds of a maximum over the CTA).
+//
+// Reordering.  A thread has one position (16 bytes where sizes allow) of the
+// states of all K beams of a request: it loads the parents' before it stores
+// any, so the states move in place, without a second buffer and without a
+// barrier; beams that keep their own state are neither read nor written.
+#include <float.h>
+
+#include "common.cuh"
+#include "dependent.cuh"
+#include "kernels.h"
+#include "mixer_common.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKept = 512;  // values collected of a piece
+
+// Values in the order of their logits: larger keys first.  A NaN sorts anywhere
+// (its row has no continuations).
+__device__ __forceinline__ bool ahead(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+
+// What a piece leaves: its n largest logits and their places (n padded to an
+// even number), its maximum and its sum.
+struct Piece {
+  float *value;  // [pieces][n]
+  int *index;    // [pieces][n]
+  float2 *sum;   // [pieces] (maximum, sum of exp(x - maximum))
+};
+
+struct SelectParams {
+  BeamArgs a;
+  Piece out;
+  int pieces;  // of a row
+};
+
+template <typename T>
+struct vec16;
+template <>
+struct vec16<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void get(const float *p, float *x) {
+    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  }
+};
+template <>
+struct vec16<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void get(const __nv_bfloat16 *p, float *x) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+
+// A piece is VALUES values per thread, in 16-byte groups dealt out to the
+// threads in turn, from the row's first 16-byte boundary at or in front of it.
+template <typename T, int VALUES>
+__global__ void __launch_bounds__(kThreads) beams_piece_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kN = vec16<T>::kN, kGroups = VALUES / kN;
+  __shared__ float top[kThreads];
+  __shared__ float kept[kKept];
+  __shared__ int place[kKept];
+  __shared__ float warp_max[kThreads / 32], warp_sum[kThreads / 32], bound;
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int piece = blockIdx.x % p.pieces;
+  const int64_t row = blockIdx.x / p.pieces;
+  const T *x = static_cast<const T *>(p.a.logits) + row * p.a.ld;
+  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kN);  // values in front of the row
+  const int V = p.a.V, n = p.a.n;
+  const int64_t base = static_cast<int64_t>(piece) * kThreads * VALUES - skew;  // of this piece in the row
+  if (tid == 0) count = 0;
+  float v[VALUES];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int64_t at = base + (static_cast<int64_t>(g) * kThreads + tid) * kN;
+    if (at >= 0 && at + kN <= V) {
+      vec16<T>::get(x + at, v + g * kN);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[g * kN + i] = at + i >= 0 && at + i < V ? io<T>::load(x + at + i) : -INFINITY;
+    }
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VALUES; ++i) m = fmaxf(m, v[i]);
+  top[tid] = m;
+  float wm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(~0u, wm, o));
+  if (lane == 0) warp_max[warp] = wm;
+  __syncthreads();
+  float all = warp_max[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) all = fmaxf(all, warp_max[i]);
+  // rank of this thread's maximum among the threads'
+  int rank = 0;
+  for (int i = 0; i < kThreads; i += 4) {
+    const float4 o = *reinterpret_cast<const float4 *>(top + i);
+    rank += ahead(o.x, i, m, tid) + ahead(o.y, i + 1, m, tid) + ahead(o.z, i + 2, m, tid) + ahead(o.w, i + 3, m, tid);
+  }
+  if (rank == n - 1) bound = m;
+  float sum = 0.f;
+  if (all > -INFINITY) {
+    // the difference first: it is exact where it matters, near the maximum
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i) sum += exp2f((v[i] - all) * kLog2e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i)
+      if (v[i] != v[i]) sum = v[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (lane == 0) warp_sum[warp] = sum;
+  __syncthreads();
+  const float least = bound;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (v[g * kN + i] >= least && v[g * kN + i] > -INFINITY) {
+        const int to = atomicAdd(&count, 1);
+        if (to < kKept) {
+          kept[to] = v[g * kN + i];
+          place[to] = static_cast<int>(base + (static_cast<int64_t>(g) * kThreads + tid) * kN + i);
+        }
+      }
+  __syncthreads();
+  float *value = p.out.value + static_cast<int64_t>(blockIdx.x) * n;
+  int *index = p.out.index + static_cast<int64_t>(blockIdx.x) * n;
+  const int found = count;
+  if (found <= kKept) {
+    for (int i = tid; i < found; i += kThreads) {
+      const float a = kept[i];
+      const int ia = place[i];
+      int r = 0;
+      for (int j = 0; j < found; ++j) r += ahead(kept[j], place[j], a, ia);
+      if (r < n) {
+        value[r] = a;
+        index[r] = ia;
+      }
+    }
+    for (int i = found + tid; i < n; i += kThreads) {
+      value[i] = -INFINITY;
+      index[i] = -1;
+    }
+  } else {
+    // value by value: the largest behind the last one taken
+    float last = INFINITY;
+    int at_last = -1;
+    for (int r = 0; r < n; ++r) {
+      float best = -INFINITY;
+      int at_best = 0x7fffffff;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int at = static_cast<int>(base + (static_cast<int64_t>(g) * kThreads + tid) * kN + i);
+          const float a = v[g * kN + i];
+          if (ahead(last, at_last, a, at) && ahead(a, at, best, at_best)) best = a, at_best = at;
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float a = __shfl_xor_sync(~0u, best, o);
+        const int at = __shfl_xor_sync(~0u, at_best, o);
+        if (ahead(a, at, best, at_best)) best = a, at_best = at;
+      }
+      __syncthreads();
+      if (lane == 0) kept[warp] = best, place[warp] = at_best;
+      __syncthreads();
+      last = kept[0], at_last = place[0];
+#pragma unroll
+      for (int i = 1; i < kThreads / 32; ++i)
+        if (ahead(kept[i], place[i], last, at_last)) last = kept[i], at_last = place[i];
+      if (tid == 0) {
+        value[r] = last;
+        index[r] = last > -INFINITY ? at_last : -1;
+      }
+    }
+  }
+  if (tid == 0) {
+    float t = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) t += warp_sum[i];
+    p.out.sum[blockIdx.x] = make_float2(all, t);
+  }
+  let_next_start();
+}
+
+// A score as an integer of the same order (fp64 comparisons are slow here).
+__device__ __forceinline__ int64_t key_of(double v) {
+  const int64_t k = __double_as_longlong(v + 0.0);
+  return k < 0 ? k ^ INT64_MAX : k;
+}
+__device__ __forceinline__ double score_of(int64_t key) { return __longlong_as_double(key < 0 ? key ^ INT64_MAX : key); }
+
+constexpr int kCand = 1024;  // candidates of a request that are ranked at once
+constexpr int kMaxBeams = 32;
+
+// A continuation: its score's key, and beam and token as one number of the
+// order in which ties go.
+struct Cand {
+  int64_t key, at;
+};
+__device__ __forceinline__ bool ahead(const Cand &a, const Cand &b) {
+  return a.key > b.key || (a.key == b.key && a.at < b.at);
+}
+
+// The n best of a request's lists.  Rows first: the log of each row's sum, and
+// with it the offset score - lse in 64 bits (-inf for a row that offers
+// nothing).  Then the first entries of the lists, one per thread, of which the
+// n-th largest bounds the n-th best continuation; and the candidates that are
+// not below it, ranked.
+__global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ double offset[kMaxBeams];
+  __shared__ uint8_t done[kMaxBeams];
+  __shared__ Cand cand[kCand];
+  __shared__ int64_t heads[kThreads];
+  __shared__ Cand best[kThreads / 32];
+  __shared__ int64_t bound;
+  __shared__ int count;
+  const int K = p.a.K, n = p.a.n, pieces = p.pieces, lists = K * pieces;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t first = static_cast<int64_t>(b) * lists;
+  const int64_t nothing = key_of(-INFINITY);
+  if (tid == 0) count = 0;
+  wait_for_previous();
+  for (int k = warp; k < K; k += kThreads / 32) {
+    const float2 *s = p.out.sum + first + static_cast<int64_t>(k) * pieces;
+    float m = -INFINITY;
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, s[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    double t = 0.0;
+    for (int i = lane; i < pieces; i += 32) {
+      const float2 x = s[i];
+      // a piece of -inf alone adds nothing, one with NaN its NaN
+      t += x.x > -INFINITY ? x.y * expf(x.x - m) : x.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+    if (lane == 0) {
+      const float sc = p.a.scores[static_cast<int64_t>(b) * K + k];
+      const bool d = p.a.finished && p.a.finished[static_cast<int64_t>(b) * K + k];
+      const double lse = d ? 0.0 : m + log(t);
+      done[k] = d;
+      offset[k] = isfinite(sc) && isfinite(lse) ? sc - lse : -INFINITY;
+    }
+  }
+  __syncthreads();
+  // entry i of list l (a finished beam has one, its end token at no cost, in
+  // its first list)
+  auto entry = [&](int l, int i) -> Cand {
+    const int k = l / pieces;
+    const double off = offset[k];
+    if (!(off > -INFINITY)) return {nothing, INT64_MAX};
+    const int64_t row = static_cast<int64_t>(k) << 32;
+    if (done[k]) return l == k * pieces && i == 0 ? Cand{key_of(off), row | p.a.eos} : Cand{nothing, INT64_MAX};
+    const int64_t at = (first + l) * n + i;
+    const int v = p.out.index[at];
+    return v < 0 ? Cand{nothing, INT64_MAX} : Cand{key_of(off + p.out.value[at]), row | v};
+  };
+  // one entry per thread: as deep into the lists as there are threads for, or
+  // the best head of several lists
+  int64_t mine = nothing;
+  if (lists < kThreads) {
+    const int i = tid / lists;
+    if (i < n && i < kThreads / lists) mine = entry(tid % lists, i).key;
+  } else {
+    for (int l = tid; l < lists; l += kThreads) {
+      const int64_t h = entry(l, 0).key;
+      if (h > mine) mine = h;
+    }
+  }
+  heads[tid] = mine;
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < kThreads; ++i) rank += heads[i] > mine || (heads[i] == mine && i < tid);
+  if (rank == n - 1) bound = mine;
+  __syncthreads();
+  const int64_t least = bound;
+  for (int l = tid; l < lists; l += kThreads)
+    for (int i = 0; i < n; ++i) {
+      const Cand c = entry(l, i);
+      if (c.key == nothing || c.key < least) break;
+      const int to = atomicAdd(&count, 1);
+      if (to < kCand) cand[to] = c;
+    }
+  __syncthreads();
+  const int found = count;
+  const int64_t out = static_cast<int64_t>(b) * n;
+  auto put = [&](int r, const Cand &c) {
+    const bool any = c.key != nothing;
+    p.a.out_scores[out + r] = static_cast<float>(score_of(c.key));
+    p.a.parents[out + r] = any ? static_cast<int>(c.at >> 32) : -1;
+    p.a.tokens[out + r] = any ? static_cast<int>(c.at & 0xffffffff) : -1;
+  };
+  if (found <= kCand) {
+    for (int i = tid; i < found; i += kThreads) {
+      const Cand c = cand[i];
+      int r = 0;
+      for (int j = 0; j < found; ++j) r += ahead(cand[j], c);
+      if (r < n) put(r, c);
+    }
+    for (int i = found + tid; i < n; i += kThreads) put(i, {nothing, 0});
+    return;
+  }
+  // more equal scores than the buffer holds: one continuation after another
+  Cand last = {INT64_MAX, -1};
+  for (int r = 0; r < n; ++r) {
+    Cand mx = {nothing, INT64_MAX};
+    for (int l = tid; l < lists; l += kThreads)
+      for (int i = 0; i < n; ++i) {
+        const Cand c = entry(l, i);
+        if (c.key == nothing) break;
+        if (ahead(last, c) && ahead(c, mx)) mx = c;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Cand c = {__shfl_xor_sync(~0u, mx.key, o), __shfl_xor_sync(~0u, mx.at, o)};
+      if (ahead(c, mx)) mx = c;
+    }
+    __syncthreads();
+    if (lane == 0) best[warp] = mx;
+    __syncthreads();
+    last = best[0];
+    for (int i = 1; i < kThreads / 32; ++i)
+      if (ahead(best[i], last)) last = best[i];
+    if (tid == 0) put(r, last);
+  }
+}
+
+// Values per thread: long pieces where there are rows enough to fill the card,
+// short ones where the pieces of a few rows have to.
+int values_of(int64_t rows, int V) { return rows * ((V + 8191) / 8192) >= 2 * kSMs ? 32 : 8; }
+
+int pieces_of(int64_t rows, int V) {
+  const int piece = kThreads * values_of(rows, V);
+  return (V + 7 + piece - 1) / piece;  // 7: values in front of an unaligned row
+}
+
+// --- reordering ---
+
+struct ReorderParams {
+  void *state[kReorderStates];
+  int64_t words[kReorderStates];  // of a beam
+  const int *parents;
+  int B, K;
+};
+
+template <typename W, int KMAX>
+__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ ReorderParams p) {
+  __shared__ int parent[KMAX];
+  const int K = p.K;
+  const int64_t words = p.words[blockIdx.z];
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    int from = threadIdx.x;
+    if (threadIdx.x < K) {
+      const int named = p.parents[static_cast<int64_t>(b) * K + threadIdx.x];
+      if (named >= 0 && named < K) from = named;
+      parent[threadIdx.x] = from;
+    }
+    const bool moves = __syncthreads_or(from != threadIdx.x);
+    W *state = static_cast<W *>(p.state[blockIdx.z]) + static_cast<int64_t>(b) * K * words;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; moves && i < words;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
+      W v[KMAX];
+#pragma unroll
+      for (int k = 0; k < KMAX; ++k)
+        if (k < K && parent[k] != k) v[k] = state[parent[k] * words + i];
+#pragma unroll
+      for (int k = 0; k < KMAX; ++k)
+        if (k < K && parent[k] != k) state[k * words + i] = v[k];
+    }
+    __syncthreads();  // the next request's parents
+  }
+}
+
+template <typename W>
+cudaError_t reorder(const ReorderParams &p, int count, int B, int64_t most, cudaStream_t s) {
+  int64_t x = (most + kThreads - 1) / kThreads;
+  // a few waves of CTAs at most: a thread then walks several positions
+  const int64_t enough = (32 * kSMs + static_cast<int64_t>(B) * count - 1) / (static_cast<int64_t>(B) * count);
+  if (x > enough) x = enough;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(B < 65535 ? B : 65535), static_cast<unsigned>(count));
+  if (p.K <= 4) reorder_kernel<W, 4><<<grid, kThreads, 0, s>>>(p);
+  else if (p.K <= 8) reorder_kernel<W, 8><<<grid, kThreads, 0, s>>>(p);
+  else if (p.K <= 16) reorder_kernel<W, 16><<<grid, kThreads, 0, s>>>(p);
+  else reorder_kernel<W, 32><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t beams_workspace_bytes(int B, int K, int V, int n) {
+  const int64_t rows = static_cast<int64_t>(B) * K;
+  return static_cast<size_t>(rows * pieces_of(rows, V)) * (sizeof(float2) + 8 * static_cast<size_t>(n));
+}
+
+cudaError_t launch_select_beams(const BeamArgs &a, Dtype dt, void *ws, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.K;
+  SelectParams p = {a, {}, pieces_of(rows, a.V)};
+  const int64_t all = rows * p.pieces;
+  if (all >= (1LL << 31)) return cudaErrorNotSupported;
+  p.out.sum = static_cast<float2 *>(ws);
+  p.out.value = reinterpret_cast<float *>(p.out.sum + all);
+  p.out.index = reinterpret_cast<int *>(p.out.value + all * a.n);
+  const bool big = values_of(rows, a.V) == 32;
+  const unsigned grid = static_cast<unsigned>(all);
+  if (dt == kF32) {
+    if (big) beams_piece_kernel<float, 32><<<grid, kThreads, 0, s>>>(p);
+    else beams_piece_kernel<float, 8><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (big) beams_piece_kernel<__nv_bfloat16, 32><<<grid, kThreads, 0, s>>>(p);
+    else beams_piece_kernel<__nv_bfloat16, 8><<<grid, kThreads, 0, s>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(beams_join_kernel, static_cast<unsigned>(a.B), 1, kThreads, 0, s, p);
+}
+
+cudaError_t launch_reorder_states(void *const *states, const int64_t *bytes, int count, const int *parents, int B,
+                                  int K, cudaStream_t s) {
+  // 16-byte words where a state's size and place allow them, else 4-byte ones,
+  // else bytes; one launch for each of these that occurs
+  ReorderParams p = {};
+  p.parents = parents;
+  p.B = B;
+  p.K = K;
+  for (const int w : {16, 4, 1}) {
+    int m = 0;
+    int64_t most = 0;
+    for (int i = 0; i < count; ++i) {
+      int own = 16;
+      while (own > 1 && (bytes[i] % own != 0 || reinterpret_cast<uintptr_t>(states[i]) % own != 0))
+        own = own == 16 ? 4 : 1;
+      if (own != w || bytes[i] == 0) continue;
+      p.state[m] = states[i];
+      p.words[m] = bytes[i] / w;
+      if (p.words[m] > most) most = p.words[m];
+      ++m;
+    }
+    if (m) {
+      const cudaError_t e = w == 16  ? reorder<uint4>(p, m, B, most, s)
+                            : w == 4 ? reorder<uint32_t>(p, m, B, most, s)
+                                     : reorder<uint8_t>(p, m, B, most, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace linattn

@@ -312,4 +312,79 @@ size_t norm_residual_backward_workspace_bytes(int64_t rows, int E);
 cudaError_t launch_norm_residual_backward(const NormResidualArgs &a, const NormResidualGrads &g,
                                           Dtype dt, void *ws, cudaStream_t s);
 
+// Retention (retention.cuh): one product of rows x over the state that rows y
+// and w build, forward or backward in time.  Strides in elements between
+// batches, tokens and heads; head h of the call reads head h / xg of x (and so
+// on).  start, end: states [B][H][Dx][Dw] fp32 (start with its own row and
+// column strides, so that it may be stored transposed), each with a factor.
+// o_f32: o is fp32 whatever the inputs' type.
+struct RetStrides {
+  int64_t b, t, h;
+};
+struct RetRole {
+  const void *x, *y, *w;
+  void *o;
+  RetStrides xs, ys, ws, os;
+  int xg, yg, wg, Dx, Dw;
+  const float *start;
+  float *end, *rec;  // rec: [B][H][parts - 1][Dx][Dw]
+  int start_rs, start_cs;
+  float start_scale, end_scale, out_scale;
+  int reverse, o_f32;
+};
+constexpr int kRetRoles = 3;
+struct RetArgs {
+  RetRole role[kRetRoles];
+  int roles;
+  const int *lens;
+  int B, L, H;
+  bool fill;  // rows behind a sequence's end become zero (otherwise they are left)
+  Gammas lg;  // log2 of each head's decay
+};
+// Parts of the tokens that run side by side, and the records' size in floats
+// over all roles; the kernels take a.role[].rec as laid out by ret_layout.
+int ret_parts(const RetArgs &a, Dtype dt);
+size_t ret_record_floats(const RetArgs &a, int parts);
+void ret_layout(RetArgs *a, int parts, float *ws);
+cudaError_t launch_retention(const RetArgs &a, Dtype dt, int parts, cudaStream_t s);
+bool ret_tc_supported(const RetArgs &a, Dtype dt);
+cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStream_t s);
+cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s);
+int ret_parts_simt(const RetArgs &a);
+int ret_parts_tc(const RetArgs &a);
+// out[row][h][e] = sum over the g heads of each group of part[row][h g + i][e]
+cudaError_t launch_group_sum(const float *part, void *out, int64_t rows, int heads, int g, int width, Dtype dt,
+                             cudaStream_t s);
+
+// One token of retention in place on states [slots][H][D][Dv] fp32: sequence b
+// has the state slots[b] (null: b); one outside [0, pool) is passed over.
+struct RetStepArgs {
+  const void *q, *k, *v;
+  float *S;
+  const int *slots;
+  void *o;
+  int B, H, Hk, D, Dv, pool;
+  int64_t ldq, ldk, ldv;
+  float scale;
+  Gammas g;
+};
+cudaError_t launch_retention_step(const RetStepArgs &a, Dtype dt, cudaStream_t s);
+
+// Beam search (beams.cu): the n best of score[b][k] + log softmax(logits[b][k]).
+struct BeamArgs {
+  const void *logits;
+  const float *scores;
+  const uint8_t *finished;  // or null
+  float *out_scores;
+  int *parents, *tokens;
+  int B, K, V, n, eos;
+  int64_t ld;  // elements between rows of logits
+};
+size_t beams_workspace_bytes(int B, int K, int V, int n);
+cudaError_t launch_select_beams(const BeamArgs &a, Dtype dt, void *ws, cudaStream_t s);
+// states[i]: [B][K][bytes[i]], each beam's bytes replaced in place by its parent's.
+constexpr int kReorderStates = 64;  // of one launch
+cudaError_t launch_reorder_states(void *const *states, const int64_t *bytes, int count, const int *parents, int B,
+                                  int K, cudaStream_t s);
+
 }  // namespace linattn

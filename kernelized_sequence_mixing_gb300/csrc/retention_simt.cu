@@ -1,0 +1,333 @@
+// Retention on CUDA cores in fp32: fp32 inputs, and the widths that the
+// tensor-core kernel does not take.
+//
+// One CTA works a slice of SW columns of w over a part of the tokens, by
+// chunks of 64: x and y lie transposed in shared memory (feature-major), so
+// that every product reads float4 along the tokens; the state of the slice
+// stays in shared memory.  Bound by the fp32 pipe and by shared memory (two
+// 16-byte loads for 16 multiply-adds a thread).
+#include "common.cuh"
+#include "mixer_common.cuh"
+#include "retention.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kC = 64;
+constexpr int kLd = kC + 4;  // floats between feature rows
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float *p) {
+  return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+  const uint2 r = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                     __uint_as_float(r.y & 0xffff0000u));
+}
+
+// Rows [0, nv) of width W as feature-major columns; the rest of the chunk zero.
+template <typename T>
+__device__ __forceinline__ void load_turned(float *dst, const T *src, int64_t st, int W, int nv) {
+  const int t = threadIdx.x & (kC - 1), g = threadIdx.x >> 6;
+  for (int d = 4 * g; d < W; d += 4 * (kThreads / kC)) {
+    const float4 v = t < nv ? load4(src + t * st + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+    dst[d * kLd + t] = v.x;
+    dst[(d + 1) * kLd + t] = v.y;
+    dst[(d + 2) * kLd + t] = v.z;
+    dst[(d + 3) * kLd + t] = v.w;
+  }
+}
+
+template <int N>
+struct Cols {
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ Cols<N> cols(const float *p) {
+  Cols<N> r;
+  if constexpr (N == 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    r.v[0] = x.x, r.v[1] = x.y, r.v[2] = x.z, r.v[3] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    r.v[0] = x.x, r.v[1] = x.y;
+  }
+  return r;
+}
+
+struct SimtParams {
+  RetArgs a;
+  int parts, cpp, slices;  // cpp: chunks of a part; slices: of the widest role
+};
+
+int smem_floats(int Dx, int SW) { return 2 * Dx * kLd + Dx * SW + kC * SW + kC * kLd + 2 * kC; }
+
+// STATE: only the part's own state, into its record.
+template <typename T, int SW, bool STATE>
+__global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_constant__ SimtParams p) {
+  constexpr int CW = SW / 16;
+  extern __shared__ float sm[];
+  const RetRole &r = p.a.role[blockIdx.z];
+  const int np = STATE ? p.parts - 1 : p.parts;
+  const int slice = blockIdx.x % p.slices, part = blockIdx.x / p.slices % np;
+  const int64_t bh = blockIdx.x / p.slices / np;
+  const int e0 = slice * SW;
+  if (e0 >= r.Dw) return;
+  const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
+  const int Dx = r.Dx, Dw = r.Dw;
+  float *xt = sm, *yt = xt + Dx * kLd, *S = yt + Dx * kLd, *w = S + Dx * SW, *pt = w + kC * SW, *pw = pt + kC * kLd;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tokens = ret_tokens(p.a.lens, b, p.a.L);
+  const int n = (tokens + kC - 1) / kC;
+  const float lg = p.a.lg.g[h];
+  const T *x = static_cast<const T *>(r.x) + b * r.xs.b + (h / r.xg) * r.xs.h;
+  const T *y = static_cast<const T *>(r.y) + b * r.ys.b + (h / r.yg) * r.ys.h;
+  const T *wp = static_cast<const T *>(r.w) + b * r.ws.b + (h / r.wg) * r.ws.h + e0;
+  const float *rec = r.rec + bh * (p.parts - 1) * Dx * Dw;
+
+  if (tid <= kC) pw[tid] = exp2f(lg * static_cast<float>(tid));
+  for (int i = tid; i < Dx * SW; i += kThreads) {
+    const int d = i / SW, e = e0 + i % SW;
+    S[i] = STATE || e >= Dw ? 0.f : ret_start(r, rec, bh, part, p.cpp, n, tokens, kC, lg, d, e);
+  }
+  const int c0 = part * p.cpp, c1 = part == p.parts - 1 ? n : min(n, c0 + p.cpp);
+  const bool keep = STATE || (part == p.parts - 1 && r.end);  // the state behind the last chunk is wanted
+  for (int c = c0; c < c1; ++c) {
+    const int t0 = (r.reverse ? n - 1 - c : c) * kC;
+    const int nv = min(kC, tokens - t0);
+    if (!STATE) load_turned(xt, x + t0 * r.xs.t, r.xs.t, Dx, nv);
+    load_turned(yt, y + t0 * r.ys.t, r.ys.t, Dx, nv);
+    for (int i = tid; i < kC * SW / 4; i += kThreads) {
+      const int t = i / (SW / 4), e = 4 * (i % (SW / 4));
+      reinterpret_cast<float4 *>(w)[i] =
+          t < nv && e0 + e < Dw ? load4(wp + (t0 + t) * r.ws.t + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    if (!STATE) {
+      float a[4][4] = {};
+      for (int d = 0; d < Dx; ++d) {
+        const Cols<4> u = cols<4>(xt + d * kLd + 4 * ty), v = cols<4>(yt + d * kLd + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[i][j] = fmaf(u.v[i], v.v[j], a[i][j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float col[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int far = r.reverse ? 4 * tx + j - 4 * ty - i : 4 * ty + i - 4 * tx - j;
+          col[i] = far >= 0 ? a[i][j] * pw[far] : 0.f;
+        }
+        *reinterpret_cast<float4 *>(pt + (4 * tx + j) * kLd + 4 * ty) = make_float4(col[0], col[1], col[2], col[3]);
+      }
+      __syncthreads();
+      float o[4][CW] = {};
+      for (int d = 0; d < Dx; ++d) {
+        const Cols<4> u = cols<4>(xt + d * kLd + 4 * ty);
+        const Cols<CW> v = cols<CW>(S + d * SW + CW * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CW; ++j) o[i][j] = fmaf(u.v[i], v.v[j], o[i][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * ty + i;
+        const float f = t >= nv ? 0.f : pw[r.reverse ? nv - 1 - t : t + 1];
+#pragma unroll
+        for (int j = 0; j < CW; ++j) o[i][j] *= f;
+      }
+      for (int s = 0; s < kC; ++s) {
+        const Cols<4> u = cols<4>(pt + s * kLd + 4 * ty);
+        const Cols<CW> v = cols<CW>(w + s * SW + CW * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CW; ++j) o[i][j] = fmaf(u.v[i], v.v[j], o[i][j]);
+      }
+      if (e0 + CW * tx < Dw) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 4 * ty + i;
+          if (t >= nv) break;
+          const int64_t at = b * r.os.b + (t0 + t) * r.os.t + h * r.os.h + e0 + CW * tx;
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            const float v = o[i][j] * r.out_scale;
+            if (r.o_f32) static_cast<float *>(r.o)[at + j] = v;
+            else io<T>::store(static_cast<T *>(r.o) + at + j, v);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (keep || c + 1 < c1) {
+      const float gn = pw[nv];
+      for (int d = 4 * ty; d < Dx; d += 64) {
+        float s[4][CW] = {};
+        for (int j = 0; j < kC; j += 4) {
+          Cols<4> u[4];
+          Cols<CW> v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            u[i] = cols<4>(yt + (d + i) * kLd + j);
+            v[i] = cols<CW>(w + (j + i) * SW + CW * tx);
+            const int t = j + i;
+            const float f = t >= nv ? 0.f : pw[r.reverse ? t + 1 : nv - 1 - t];
+#pragma unroll
+            for (int k = 0; k < CW; ++k) v[i].v[k] *= f;
+          }
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < CW; ++k) s[i][k] = fmaf(u[i].v[jj], v[jj].v[k], s[i][k]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < CW; ++k) {
+            float *at = S + (d + i) * SW + CW * tx + k;
+            *at = fmaf(gn, *at, s[i][k]);
+          }
+      }
+    }
+    __syncthreads();
+  }
+  __syncthreads();
+  if (STATE || (part == p.parts - 1 && r.end)) {
+    float *out = STATE ? const_cast<float *>(rec) + static_cast<int64_t>(part) * Dx * Dw : r.end + bh * Dx * Dw;
+    const float f = STATE ? 1.f : r.end_scale;
+    for (int i = tid; i < Dx * SW; i += kThreads) {
+      const int d = i / SW, e = e0 + i % SW;
+      if (e < Dw) out[d * Dw + e] = f * S[i];
+    }
+  }
+  if (!STATE && p.a.fill && part == p.parts - 1) {
+    for (int64_t i = tid; i < static_cast<int64_t>(p.a.L - tokens) * SW; i += kThreads) {
+      const int e = e0 + static_cast<int>(i % SW);
+      if (e >= Dw) continue;
+      const int64_t at = b * r.os.b + (tokens + i / SW) * r.os.t + h * r.os.h + e;
+      if (r.o_f32) static_cast<float *>(r.o)[at] = 0.f;
+      else io<T>::store(static_cast<T *>(r.o) + at, 0.f);
+    }
+  }
+}
+
+template <typename T, int SW>
+cudaError_t run(const RetArgs &a, int parts, int widest, int Dx, cudaStream_t s) {
+  SimtParams p = {a, parts, 0, (widest + SW - 1) / SW};
+  const int chunks = (a.L + kC - 1) / kC;
+  p.cpp = (chunks + parts - 1) / parts;
+  const int bytes = smem_floats(Dx, SW) * 4;
+  const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
+  if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
+  if (parts > 1) {
+    auto k = retention_simt_kernel<T, SW, true>;
+    cudaError_t e = allow_smem(k, bytes);
+    if (e != cudaSuccess) return e;
+    k<<<dim3(static_cast<unsigned>(units * (parts - 1)), 1, a.roles), kThreads, bytes, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  auto k = retention_simt_kernel<T, SW, false>;
+  const cudaError_t e = allow_smem(k, bytes);
+  if (e != cudaSuccess) return e;
+  k<<<dim3(static_cast<unsigned>(units * parts), 1, a.roles), kThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+void widths(const RetArgs &a, int *Dx, int *Dw) {
+  *Dx = *Dw = 0;
+  for (int i = 0; i < a.roles; ++i) {
+    if (a.role[i].Dx > *Dx) *Dx = a.role[i].Dx;
+    if (a.role[i].Dw > *Dw) *Dw = a.role[i].Dw;
+  }
+}
+
+// Slices of 64 columns use each transposed load twice as often; above 128
+// features two tiles and the state no longer fit in shared memory with them.
+int slice_width(int Dx, int Dw) { return Dx > 128 || Dw <= 32 ? 32 : 64; }
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    group_sum_kernel(const float *part, T *out, int64_t total, int g, int width) {
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    // four columns of one (row, group): the g heads of it lie behind one another
+    const int64_t rh = i / (width / 4);
+    const int e = static_cast<int>(i % (width / 4)) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < g; ++j) {
+      const float4 v = __ldcs(reinterpret_cast<const float4 *>(part + (rh * g + j) * width + e));
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    T *o = out + rh * width + e;
+    io<T>::store(o, s.x), io<T>::store(o + 1, s.y), io<T>::store(o + 2, s.z), io<T>::store(o + 3, s.w);
+  }
+}
+
+}  // namespace
+
+int ret_parts_simt(const RetArgs &a) {
+  int Dx, Dw;
+  widths(a, &Dx, &Dw);
+  const int SW = slice_width(Dx, Dw);
+  const int64_t units = static_cast<int64_t>(a.B) * a.H * ((Dw + SW - 1) / SW) * a.roles;
+  const int chunks = (a.L + kC - 1) / kC;
+  // parts cost a second pass over y and w for their records (about a third of
+  // the work), so only where they at least double the CTAs at work
+  const int64_t room = 2 * kSMs / (units > 0 ? units : 1);
+  int parts = static_cast<int>(room < 32 ? room : 32);
+  if (parts > chunks / 4) parts = chunks / 4;
+  return parts < 2 ? 1 : parts;
+}
+
+cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStream_t s) {
+  int Dx, Dw;
+  widths(a, &Dx, &Dw);
+  const bool wide = slice_width(Dx, Dw) == 64;
+  if (dt == kF32) return wide ? run<float, 64>(a, parts, Dw, Dx, s) : run<float, 32>(a, parts, Dw, Dx, s);
+  return wide ? run<__nv_bfloat16, 64>(a, parts, Dw, Dx, s) : run<__nv_bfloat16, 32>(a, parts, Dw, Dx, s);
+}
+
+cudaError_t launch_group_sum(const float *part, void *out, int64_t rows, int heads, int g, int width, Dtype dt,
+                             cudaStream_t s) {
+  const int64_t total = rows * heads * (width / 4);
+  const int64_t want = (total + 255) / 256;
+  const unsigned grid = static_cast<unsigned>(want < 8 * kSMs ? want : 8 * kSMs);
+  if (dt == kF32) group_sum_kernel<float><<<grid, 256, 0, s>>>(part, static_cast<float *>(out), total, g, width);
+  else
+    group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16 *>(out), total, g, width);
+  return cudaGetLastError();
+}
+
+// ---- choice between the kernels, shared host code ----
+
+int ret_parts(const RetArgs &a, Dtype dt) { return ret_tc_supported(a, dt) ? ret_parts_tc(a) : ret_parts_simt(a); }
+
+size_t ret_record_floats(const RetArgs &a, int parts) {
+  size_t n = 0;
+  for (int i = 0; i < a.roles; ++i)
+    n += static_cast<size_t>(a.B) * a.H * (parts - 1) * a.role[i].Dx * a.role[i].Dw;
+  return n;
+}
+
+void ret_layout(RetArgs *a, int parts, float *ws) {
+  for (int i = 0; i < a->roles; ++i) {
+    a->role[i].rec = ws;
+    ws += static_cast<size_t>(a->B) * a->H * (parts - 1) * a->role[i].Dx * a->role[i].Dw;
+  }
+}
+
+cudaError_t launch_retention(const RetArgs &a, Dtype dt, int parts, cudaStream_t s) {
+  return ret_tc_supported(a, dt) ? launch_retention_tc(a, parts, s) : launch_retention_simt(a, dt, parts, s);
+}
+
+}  // namespace linattn

@@ -1,0 +1,503 @@
+"""GPU parity of retention and of beam search over its states against the fp64
+oracle.
+
+Tolerances, element by element, with mag the element's sums over absolute
+values (from the oracle):
+
+  half a step of the output's type, relative to the value, plus
+  K 2^-24 mag, K = 2 L + 2 D + 64 (group sums: + H / Hk): the fp32 roundings on
+  the longest path -- one multiplication by a power of the decay and one sum per
+  chunk at most and two per token, the D products of a weight, and a power
+  2^(e log2 g) that is off by e |log2 g| 2^-24 with |log2 g| <= 1 here (e <= L);
+  bf16 outputs of the tensor-core kernel also 2^-8 mag (the weights of a chunk,
+  rounded to bf16) + 2^-15 mag (states and decayed rows as sums of two bf16
+  values, 2^-16 each).
+
+States that are returned are fp32 (decayed rows as three bf16 values, 2^-24).
+"""
+import numpy as np
+import pytest
+import torch
+
+from helpers import record
+from oracle import retention as ort
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+DT = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+sid = lambda s: "x".join(map(str, s))  # noqa: E731
+
+
+@pytest.fixture(scope="module")
+def la():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kernelized_sequence_mixing_gb300 import build
+    build.build()
+    import kernelized_sequence_mixing_gb300 as m
+    return m
+
+
+def n64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def close(name, got, ref, mag, K, dtype, products=False):
+    got = n64(got)
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    assert np.isfinite(got).all(), name
+    if not got.size:
+        return
+    tol = torch.finfo(dtype).eps / 2 * np.abs(ref) + K * 2.0 ** -24 * mag + 1e-37
+    if products and dtype == BF16:
+        tol = tol + (2.0 ** -8 + 2.0 ** -15) * mag
+    worst = float((np.abs(got - ref) / tol).max())
+    record(f"retention {name} {str(dtype)[6:]} (share of its bound)", worst, 1)
+    assert worst <= 1, f"{name}: {worst} times its bound"
+
+
+def decays(H, seed=0):
+    """Between 1/2 and 1, both among them from three heads on."""
+    g = 1 - 2.0 ** -(1 + 8 * torch.rand(H, generator=torch.Generator().manual_seed(seed)))
+    if H > 1:
+        g[-1] = 1.0
+    if H > 2:
+        g[0] = 0.5
+    return g
+
+
+class Problem:
+    def __init__(self, shape, dtype, seed, start=True, lens=None):
+        B, L, H, Hk, D, Dv = self.shape = shape
+        self.g = torch.Generator().manual_seed(seed)
+        r = lambda *s, dtype=dtype: torch.randn(s, generator=self.g).to(dtype)  # noqa: E731
+        self.dtype, self.r = dtype, r
+        self.q, self.k, self.v, self.do = r(B, L, H, D), r(B, L, Hk, D), r(B, L, Hk, Dv), r(B, L, H, Dv)
+        self.S0 = r(B, H, D, Dv, dtype=F32) if start else None
+        self.dS = r(B, H, D, Dv, dtype=F32) if start else None
+        self.gamma, self.scale = decays(H, seed), 0.3
+        self.lens = lens
+        self.K = 2 * L + 2 * D + 64 + H // max(1, Hk)
+
+    def host(self):
+        return [n64(t) for t in (self.q, self.k, self.v)]
+
+    def dev(self):
+        return [t.cuda() for t in (self.q, self.k, self.v)]
+
+    def kw(self):
+        c = lambda t: None if t is None else t.cuda()  # noqa: E731
+        lens = None if self.lens is None else torch.tensor(self.lens, dtype=torch.int32).cuda()
+        return {"gamma": self.gamma, "scale": self.scale, "S0": c(self.S0), "lens": lens}
+
+    def ref(self, mag=False):
+        return ort.forward(*self.host(), n64(self.gamma), self.scale, n64(self.S0), self.lens, mag=mag)
+
+    def grads(self, mag=False):
+        return ort.backward(*self.host(), n64(self.do), n64(self.gamma), self.scale, n64(self.S0), n64(self.dS),
+                            self.lens, mag=mag)
+
+
+# (B, L, H, Hk, D, Dv): one token, lengths around the chunks of 64 and 128, both
+# widths of the tensor-core kernel and mixed ones, shared heads, odd widths,
+# few heads over many tokens (parts), one head
+SHAPES = [
+    (1, 1, 1, 1, 64, 64), (2, 3, 2, 1, 128, 128), (1, 63, 3, 3, 64, 128), (2, 64, 2, 2, 128, 64),
+    (1, 65, 4, 2, 64, 64), (3, 127, 2, 2, 128, 128), (1, 128, 3, 1, 128, 64), (1, 129, 2, 2, 64, 64),
+    (2, 257, 6, 2, 128, 128), (1, 1111, 2, 1, 64, 64), (1, 1500, 1, 1, 128, 128), (5, 200, 8, 4, 64, 64),
+    (2, 150, 2, 2, 8, 8), (1, 130, 3, 3, 96, 40), (1, 300, 2, 1, 256, 256), (2, 70, 2, 2, 32, 160),
+    (1, 400, 2, 2, 128, 192), (1, 520, 4, 1, 64, 32),
+]
+
+
+@DT
+@pytest.mark.parametrize("shape", SHAPES, ids=sid)
+def test_forward(la, dtype, shape):
+    p = Problem(shape, dtype, shape[1])
+    (ro, rS), (mo, mS) = p.ref(), p.ref(True)
+    o, S = la.forward_retention(*p.dev(), **p.kw(), return_state=True)
+    close("o", o, ro, mo, p.K, dtype, True)
+    close("state", S, rS, mS, p.K, F32)
+    # the same without the state, without a start
+    o2 = la.forward_retention(*p.dev(), **p.kw())
+    close("o alone", o2, ro, mo, p.K, dtype, True)
+    p.S0 = None
+    o3 = la.forward_retention(*p.dev(), **p.kw())
+    close("o from zero", o3, p.ref()[0], p.ref(True)[0], p.K, dtype, True)
+
+
+@DT
+@pytest.mark.parametrize("shape", SHAPES, ids=sid)
+def test_backward(la, dtype, shape):
+    p = Problem(shape, dtype, shape[1] + 1)
+    ref, mag = p.grads(), p.grads(True)
+    got = la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())
+    for name, x, r, m in zip(("dq", "dk", "dv"), got, ref, mag):
+        close(name, x, r, m, p.K, dtype, True)
+    close("dS0", got[3], ref[3], mag[3], p.K, F32)
+    # without states at the ends
+    p.S0 = p.dS = None
+    got = la.backward_retention(*p.dev(), p.do.cuda(), gamma=p.gamma, scale=p.scale)
+    assert got[3] is None
+    for name, x, r, m in zip(("dq", "dk", "dv"), got, p.grads(), p.grads(True)):
+        close(name + " from zero", x, r, m, p.K, dtype, True)
+
+
+RAGGED = [(6, 400, 2, 1, 64, 64), (6, 400, 2, 2, 128, 128), (6, 300, 1, 1, 40, 72)]
+LENS = [400, 0, 1, 257, 128, -3]
+
+
+@DT
+@pytest.mark.parametrize("shape", RAGGED, ids=sid)
+def test_ragged(la, dtype, shape):
+    """Rows behind a sequence's end: not read (NaN there), outputs left alone,
+    gradients zero."""
+    B, L, H, Hk, D, Dv = shape
+    lens = [min(n, L) for n in LENS]
+    p = Problem(shape, dtype, 5, lens=lens)
+    ref, mag, gref, gmag = p.ref(), p.ref(True), p.grads(), p.grads(True)
+    for b, n in enumerate(lens):
+        for t in (p.q, p.k, p.v, p.do):
+            t[b, max(n, 0):] = float("nan")
+    out = torch.full((B, L, H, Dv), -3.0, dtype=dtype).cuda()
+    o, S = la.forward_retention(*p.dev(), **p.kw(), out=out, return_state=True)
+    for b, n in enumerate(lens):
+        assert (o[b, max(n, 0):] == -3).all()
+        o[b, max(n, 0):] = 0
+    close("ragged o", o, ref[0], mag[0], p.K, dtype, True)
+    close("ragged state", S, ref[1], mag[1], p.K, F32)
+    got = la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())
+    for b, n in enumerate(lens):
+        for t in got[:3]:
+            assert not t[b, max(n, 0):].any()
+    for name, x, r, m in zip(("dq", "dk", "dv"), got, gref, gmag):
+        close("ragged " + name, x, r, m, p.K, dtype, True)
+    close("ragged dS0", got[3], gref[3], gmag[3], p.K, F32)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(2, 150, 4, 2, 64, 64), (2, 150, 4, 2, 128, 128), (2, 90, 4, 2, 24, 56)], ids=sid)
+def test_layouts(la, dtype, shape):
+    """Slices of one projection, heads first, padded rows: the dense results."""
+    B, L, H, Hk, D, Dv = shape
+    p = Problem(shape, dtype, 9)
+    q, k, v = p.dev()
+    do = p.do.cuda()
+    kw = p.kw()
+    o = la.forward_retention(q, k, v, **kw)
+    grads = la.backward_retention(q, k, v, do, **kw, dS=p.dS.cuda())
+    joint = torch.cat([t.flatten(2) for t in (q, k, v)], -1).split([H * D, Hk * D, Hk * Dv], -1)
+    joint = [t.unflatten(-1, (-1, w)) for t, w in zip(joint, (D, D, Dv))]
+    first = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in (q, k, v)]
+    padded = [torch.nn.functional.pad(t, (0, 8, 0, 1, 0, 2))[:, :L, :n, :w]
+              for t, n, w in ((q, H, D), (k, Hk, D), (v, Hk, Dv))]
+    tokens_first = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+    for args in (joint, first, padded, tokens_first):
+        assert torch.equal(la.forward_retention(*args, **kw), o)
+        out = torch.empty(B, H, L, Dv, dtype=dtype, device="cuda").transpose(1, 2)
+        assert la.forward_retention(*args, **kw, out=out) is out and torch.equal(out, o)
+        for x, y in zip(la.backward_retention(*args, do.transpose(1, 2).contiguous().transpose(1, 2), **kw, dS=p.dS.cuda()), grads):
+            assert torch.equal(x, y)
+
+
+@DT
+def test_zero_decay_and_none(la, dtype):
+    """A decay of zero keeps the newest token alone; no decay is one."""
+    p = Problem((1, 140, 2, 2, 64, 64), dtype, 3)
+    p.gamma = torch.tensor([0.0, 1.0])
+    (ro, rS), (mo, mS) = p.ref(), p.ref(True)
+    o, S = la.forward_retention(*p.dev(), **p.kw(), return_state=True)
+    close("o", o, ro, mo, p.K, dtype, True)
+    close("state", S, rS, mS, p.K, F32)
+    kw = p.kw()
+    kw["gamma"] = 1.0
+    a = la.forward_retention(*p.dev(), **kw)
+    kw["gamma"] = None
+    assert torch.equal(a, la.forward_retention(*p.dev(), **kw))
+
+
+def test_long_decay_far(la):
+    """Thousands of tokens at strong and weak decays stay finite and right."""
+    p = Problem((1, 4000, 4, 4, 64, 64), BF16, 4)
+    p.gamma = torch.tensor([0.5, 0.03, 0.999, 1.0])
+    (ro, rS), (mo, mS) = p.ref(), p.ref(True)
+    o, S = la.forward_retention(*p.dev(), **p.kw(), return_state=True)
+    # log2 0.03 = -5.06: powers that matter (above 2^-40) are off by 40 2^-24 more
+    close("o", o, ro, mo, p.K + 40, BF16, True)
+    close("state", S, rS, mS, p.K + 40, F32)
+
+
+STEPS = [(1, 2, 1, 64, 64), (3, 4, 4, 128, 128), (2, 3, 3, 8, 16), (2, 2, 1, 256, 256), (1, 3, 3, 96, 40),
+         (40, 16, 8, 64, 128), (40, 16, 16, 128, 64), (30, 16, 2, 136, 200)]
+
+
+@DT
+@pytest.mark.parametrize("shape", STEPS, ids=sid)
+def test_step(la, dtype, shape):
+    B, H, Hk, D, Dv = shape
+    p = Problem((B, 1, H, Hk, D, Dv), dtype, D)
+    (ro, rS), (mo, mS) = p.ref(), p.ref(True)
+    q, k, v = (t[:, 0] for t in p.dev())
+    S = p.S0.cuda()
+    o = la.decode_retention(q, k, v, S, gamma=p.gamma, scale=p.scale)
+    close("step o", o, ro[:, 0], mo[:, 0], D + 16, dtype)
+    close("step state", S, rS, mS, 4, F32)
+    # a pool, idle rows, strided inputs
+    pool = torch.randn(B + 3, H, D, Dv).cuda()
+    before = pool.clone()
+    slots = torch.randperm(B + 3)[:B].to(torch.int32)
+    for b in range(B):
+        pool[slots[b]] = p.S0[b].cuda()
+    idle = B > 1
+    if idle:
+        before[slots[0]] = pool[slots[0]]
+        slots[0], lost = (-1 if dtype == F32 else B + 3), int(slots[0])
+    joint = torch.cat([t.flatten(1) for t in (q, k, v)], -1).split([H * D, Hk * D, Hk * Dv], -1)
+    joint = [t.unflatten(-1, (-1, w)) for t, w in zip(joint, (D, D, Dv))]
+    out = torch.full_like(o, -3.0)
+    la.decode_retention(*joint, pool, gamma=p.gamma, scale=p.scale, slots=slots.cuda(), out=out)
+    for b in range(B):
+        if idle and b == 0:
+            assert (out[0] == -3).all() and torch.equal(pool[lost], before[lost])
+            continue
+        assert torch.equal(out[b], o[b]) and torch.equal(pool[slots[b]], S[b])
+        before[slots[b]] = S[b]
+    assert torch.equal(pool, before)
+
+
+@DT
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_then_tokens(la, dtype, D):
+    """A prompt in two segments and then tokens, against one call."""
+    B, L, H = 2, 300, 3
+    p = Problem((B, L, H, H, D, D), dtype, 21)
+    (ro, rS), (mo, mS) = p.ref(), p.ref(True)
+    q, k, v = p.dev()
+    kw = p.kw()
+    del kw["lens"]
+    o1, S = la.forward_retention(q[:, :170], k[:, :170], v[:, :170], **kw, return_state=True)
+    kw["S0"] = S
+    o2, S = la.forward_retention(q[:, 170:290], k[:, 170:290], v[:, 170:290], **kw, return_state=True)
+    del kw["S0"]
+    outs = [o1, o2]
+    for t in range(290, 300):
+        outs.append(la.decode_retention(q[:, t], k[:, t], v[:, t], S, **kw)[:, None])
+    close("o", torch.cat(outs, 1), ro, mo, p.K, dtype, True)
+    close("state", S, rS, mS, p.K, F32)
+
+
+def test_empty(la):
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    S0 = torch.randn(2, 3, 64, 64, device="cuda")
+    o, S = la.forward_retention(z(2, 0, 3, 64), z(2, 0, 3, 64), z(2, 0, 3, 64), S0=S0, return_state=True)
+    assert o.shape == (2, 0, 3, 64) and torch.equal(S, S0)
+    assert not la.forward_retention(z(2, 0, 3, 64), z(2, 0, 3, 64), z(2, 0, 3, 64), return_state=True)[1].any()
+    got = la.backward_retention(z(2, 0, 3, 64), z(2, 0, 3, 64), z(2, 0, 3, 64), z(2, 0, 3, 64), S0=S0, dS=S0)
+    assert torch.equal(got[3], S0)
+    assert la.forward_retention(z(0, 5, 3, 64), z(0, 5, 3, 64), z(0, 5, 3, 64)).shape == (0, 5, 3, 64)
+    assert la.decode_retention(z(0, 3, 64), z(0, 3, 64), z(0, 3, 64), z(0, 3, 64, 64)).shape == (0, 3, 64)
+
+
+@DT
+def test_captured_and_streams(la, dtype):
+    """Captured calls replay with other inputs and lengths; a call on another
+    stream; two graphs and an eager call interleaved."""
+    p = Problem((2, 700, 2, 1, 64, 64), dtype, 31, lens=[700, 300])
+    q, k, v = p.dev()
+    do, dS, kw = p.do.cuda(), p.dS.cuda(), p.kw()
+    forward = lambda: la.forward_retention(q, k, v, **kw, return_state=True)  # noqa: E731
+    backward = lambda: la.backward_retention(q, k, v, do, **kw, dS=dS)  # noqa: E731
+    side = torch.cuda.Stream()
+    graphs = []
+    for f in (forward, backward):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            held = f()
+        graphs.append((g, held, f))
+    for t in (q, k, v, do):
+        t.copy_(torch.randn(t.shape, generator=p.g).to(dtype))
+    kw["lens"].copy_(torch.tensor([130, 699], dtype=torch.int32))
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for g, held, f in graphs:
+            for t in held:
+                t.zero_()
+            g.replay()
+            for i, (x, y) in enumerate(zip(held, f())):
+                if f is forward and i == 0:
+                    for b, n in enumerate((130, 699)):
+                        assert torch.equal(x[b, :n], y[b, :n])
+                else:
+                    assert torch.equal(x, y)
+    with torch.cuda.stream(side):
+        again = forward()
+    side.synchronize()
+    assert torch.equal(again[1], forward()[1])
+
+
+# --- beams ---
+
+def check_select(la, logits, scores, n, finished=None, eos=None):
+    got = la.select_beams(logits.cuda(), scores.cuda(), n=n, finished=None if finished is None else finished.cuda(), eos=eos)
+    ref = ort.select(n64(logits), n64(scores), n, None if finished is None else finished.numpy(), eos)
+    assert got[1].cpu().tolist() == ref[1].tolist()
+    assert got[2].cpu().tolist() == ref[2].tolist()
+    s = n64(got[0])
+    live = np.isfinite(ref[0])
+    assert (np.isfinite(s) == live).all()
+    # the score's own rounding, and the sum of exponentials: each exponential and
+    # the sums of up to 32 in a thread, 8 over lanes and warps, 2^-24 each
+    tol = 2.0 ** -24 * np.abs(ref[0][live]) + 64 * 2.0 ** -24
+    assert (np.abs(s[live] - ref[0][live]) <= tol).all()
+    return got
+
+
+@DT
+@pytest.mark.parametrize("shape", [(1, 1, 5, 1), (2, 3, 7, 21), (3, 4, 1000, 8), (1, 4, 8191, 4), (1, 4, 30011, 8),
+                                   (70, 5, 9001, 10), (2, 16, 2047, 32), (1, 32, 333, 64), (200, 4, 64, 8)], ids=sid)
+def test_select(la, dtype, shape):
+    B, K, V, n = shape
+    g = torch.Generator().manual_seed(V)
+    logits = (torch.randn(B, K, V, generator=g) * 3).to(dtype)
+    scores = torch.randn(B, K, generator=g) * 2 - 5
+    check_select(la, logits, scores, n)
+    finished = torch.rand(B, K, generator=g) < 0.4
+    check_select(la, logits, scores, n, finished, 3)
+
+
+@DT
+def test_select_hard(la, dtype):
+    """Equal logits, rows that offer nothing, forbidden tokens, unused beams."""
+    inf, nan = float("inf"), float("nan")
+    V = 5000
+    flat = torch.zeros(1, 2, V, dtype=dtype)                 # all equal, over every piece's buffer
+    check_select(la, flat, torch.tensor([[-1.0, -1.0]]), 16)
+    check_select(la, torch.full((1, 3, V), -inf, dtype=dtype), torch.zeros(1, 3), 4)
+    x = torch.randn(1, 6, V, generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[0, 0, 17] = nan
+    x[0, 1, 4000] = inf
+    x[0, 2, :] = -inf
+    x[0, 2, 7] = 1.0                                         # one allowed token
+    x[0, 3, 100:] = -inf
+    x[0, 5] = -inf
+    x[0, 5, 9] = nan                                         # nothing but a NaN
+    scores = torch.tensor([[0.0, 0.0, -30.0, -1.0, -inf, 0.0]])
+    got = check_select(la, x, scores, 12)
+    assert set(got[1][0].tolist()) <= {2, 3}
+    got = check_select(la, x, scores, 64)
+    assert got[1][0].tolist().count(2) <= 1
+    # fewer continuations than asked for
+    x[0, 3] = -inf
+    x[0, 3, 50] = 0.0
+    got = check_select(la, x, scores, 5)
+    assert got[1][0].tolist() == [3, 2, -1, -1, -1]
+    # values far apart and large
+    y = torch.tensor([[[3e4, -3e4, 0.0] + [1e4] * 61]]).to(dtype)
+    check_select(la, y, torch.tensor([[2.0]]), 3)
+
+
+@DT
+@pytest.mark.parametrize("V,pad", [(1001, 0), (1000, 24), (1003, 5), (64, 1)])
+def test_select_rows(la, dtype, V, pad):
+    """Rows off the 16-byte boundary, inside a wider tensor of NaN."""
+    g = torch.Generator().manual_seed(V)
+    wide = torch.full((1 + 3 * 4 * (V + pad) + 16,), float("nan")).to(dtype).cuda()
+    for off in range(0, 9, 3):
+        x = wide[1 + off:1 + off + 12 * (V + pad)].view(3, 4, V + pad)[..., :V]
+        x.copy_(torch.randn(3, 4, V, generator=g))
+        scores = torch.randn(3, 4, generator=g)
+        got = la.select_beams(x, scores.cuda(), n=7)
+        ref = ort.select(n64(x), n64(scores), 7)
+        assert got[1].cpu().tolist() == ref[1].tolist() and got[2].cpu().tolist() == ref[2].tolist()
+        wide.fill_(float("nan"))
+
+
+@pytest.mark.parametrize("B,K", [(1, 1), (3, 2), (2, 4), (5, 7), (2, 16), (3, 32), (66000, 2)])
+def test_reorder(la, B, K):
+    """In place, over every word size; parents outside keep a beam's own."""
+    g = torch.Generator().manual_seed(B + K)
+    parents = torch.randint(-1, K + 1, (B, K), generator=g, dtype=torch.int32)
+    big = B > 1000
+    states = [torch.randn(B, K, 4 if big else 3000, generator=g), torch.randn(B * K, 3, 8, generator=g).bfloat16(),
+              torch.randint(0, 9, (B, K, 5), generator=g), torch.randint(0, 9, (B, K, 7), generator=g, dtype=torch.uint8),
+              torch.randn(B, K, 1, generator=g), torch.empty(B, K, 0)]
+    own = torch.where((parents < 0) | (parents >= K), torch.arange(K, dtype=torch.int32), parents).long()
+    rows = torch.arange(B)[:, None]
+    dev = [t.cuda() for t in states]
+    assert la.reorder_states(dev, parents.cuda()) is dev
+    for t, d in zip(states, dev):
+        want = t.view(B, K, -1)[rows, own] if t.numel() else t.view(B, K, 0)
+        assert torch.equal(d.cpu().view(B, K, -1) if t.numel() else d.cpu(), want)
+    one = states[0].cuda()
+    la.reorder_states(one, parents.cuda())
+    assert torch.equal(one, dev[0])
+    # more tensors than one launch takes, some of them off the 16-byte boundary
+    if not big:
+        many = [torch.randn(B * K * 12 + 1, generator=g).cuda() for _ in range(70)]
+        views = [t[i % 2:B * K * 12 + i % 2].view(B, K, 12) for i, t in enumerate(many)]
+        want = [t[rows.cuda(), own.cuda()] for t in views]
+        la.reorder_states(views, parents.cuda())
+        assert all(torch.equal(a, b) for a, b in zip(views, want))
+
+
+@DT
+def test_beam_search(la, dtype):
+    """Together as they are used: a prompt, then tokens with beams whose states,
+    convolution states and tokens follow the selection, captured as a graph and
+    eager, against a search that recomputes every beam from its tokens in fp64."""
+    B, K, H, D, V, steps = 2, 3, 2, 64, 50, 6
+    g = torch.Generator().manual_seed(11)
+    emb = torch.randn(V, 3 * H * D, generator=g).to(dtype)
+    head = (torch.randn(H * D, V, generator=g) * 0.02).to(dtype)
+    prompt = torch.randint(3, V, (B, 140), generator=g)
+    gamma = decays(H, 5)
+    emb_d, head_d = emb.cuda(), head.cuda()
+
+    def split(x):
+        return [t.unflatten(-1, (H, D)) for t in x.split(H * D, -1)]
+
+    _, S = la.forward_retention(*split(emb_d[prompt.cuda()]), gamma=gamma, scale=0.1, return_state=True)
+    S = S.repeat_interleave(K, 0)
+    tokens = torch.zeros(B, K, steps, dtype=torch.int32, device="cuda")
+    scores = torch.tensor([[0.0] + [-float("inf")] * (K - 1)] * B, device="cuda")
+    last = prompt[:, -1:].expand(B, K).cuda().to(torch.int32).contiguous()
+    at = torch.zeros(1, dtype=torch.long, device="cuda")
+
+    def step():
+        o = la.decode_retention(*split(emb_d[last.long().flatten()]), S, gamma=gamma, scale=0.1)
+        logits = (o.flatten(1).float() @ head_d.float()).view(B, K, V)
+        s, parents, chosen = la.select_beams(logits, scores)
+        la.reorder_states([S, tokens], parents)
+        scores.copy_(s)
+        last.copy_(chosen.clamp(min=0))
+        tokens.index_copy_(2, at, chosen[..., None])
+        at.add_(1)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(steps - 1):
+        graph.replay()
+    # fp64, from the tokens alone
+    e, w = n64(emb), n64(head)
+    for b in range(B):
+        beams = [(0.0, [])]
+        for _ in range(steps):
+            cand = []
+            for s, toks in beams:
+                seq = np.concatenate([prompt[b].numpy(), prompt[b, -1:].numpy(), np.array(toks, dtype=np.int64)])
+                x = e[seq][None]
+                q, k, v = (x[..., i * H * D:(i + 1) * H * D].reshape(1, -1, H, D) for i in range(3))
+                o = ort.forward(q, k, v, n64(gamma), 0.1)[0][0, -1].reshape(-1)
+                z = o @ w
+                lp = s + z - (z.max() + np.log(np.exp(z - z.max()).sum()))
+                cand += [(lp[t], toks + [t]) for t in range(V)]
+            beams = sorted(cand, key=lambda c: -c[0])[:K]
+        got = [(float(scores[b, i]), tokens[b, i].tolist()) for i in range(K)]
+        # bf16 rounds outputs of size about 1: their step times the head's weights
+        slack = 1e-4 if dtype == F32 else 0.05
+        for (gs, gt), (rs, rt) in zip(got, beams):
+            assert abs(gs - rs) < slack * steps
+            assert dtype == BF16 or gt == rt
