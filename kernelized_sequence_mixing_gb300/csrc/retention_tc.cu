@@ -1,6 +1,603 @@
+// Retention on tcgen05 tensor cores: bf16, Dx = 64 or 128 features, any
+// multiple of 32 columns of w.
+//
+// A CTA works a slice of 32 columns of w of one (batch, head) over a part of the
+// tokens, by chunks of 128 tokens.  Columns of the state do not meet, so slices
+// give few heads four times the CTAs without a second pass over the tokens; the
+// price is that the weights x y^T are computed once per slice.  Per chunk, M = 128
+// MMAs with operands as TMA leaves them (no pass over x or y):
+//
+//   R  = x y^T                      (K = Dx; raw weights, tensor memory)
+//   O1 = x [Shi | Slo]              (K = Dx; the state in front, two bf16 values)
+//   dS = y^T [w~1 | w~2 | w~3]      (K = tokens; w~ = decayed rows of w as a sum of
+//                                    two or three bf16 values side by side)
+//   O2 = P w                        (P = R times its powers of the decay, masked, in
+//                                    bf16, A operand in tensor memory)
+//   o  = scale (g^(.) (O1hi + O1lo) + O2),   S <- g^n S + dS1 + dS2 + dS3
+//
+// The state itself stays in fp32 registers (a thread has one row of the slice),
+// so dS needs nothing of the chunk before and only the sum S is a chain.  Values
+// side by side cost little: an MMA of N = 32 columns is bound by reading A from
+// shared memory (128 x 16 values for 128 x 32 x 16 products), not by the
+// products.
+//
+// Warp roles (18 warps):
+//   0-7    P: powers of the decay, mask, bf16 (a lane quadrant and two of its
+//          four blocks of 32 columns each)
+//   8-11   state: registers, its bf16 values for the MMA (thread = row)
+//   12-15  w~ of a chunk, and zeros behind a ragged sequence's end; then the
+//          output rows of the chunk before (thread = token)
+//   16     TMA: lane 0 the x ring, lane 1 the y ring, lane 2 the w ring
+//   17     TMEM owner and MMA issuer
+// Every wait is bounded; a CTA that gives up counts the failure in device
+// memory, drains its copies and MMAs, frees tensor memory and exits.
+#include "common.cuh"
+#include "mixer_common.cuh"
 #include "retention.cuh"
+#include "tc_common.cuh"
+
 namespace linattn {
-bool ret_tc_supported(const RetArgs &, Dtype) { return false; }
-int ret_parts_tc(const RetArgs &) { return 1; }
-cudaError_t launch_retention_tc(const RetArgs &, int, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+using namespace tc;
+
+constexpr int kC = 128;  // tokens per chunk
+constexpr int kSW = 32;  // columns of a slice
+constexpr int kThreads = 576;
+constexpr int kWarpS = 8, kWarpW = 12, kWarpTma = 16, kWarpMma = 17;
+constexpr int kBox = kC * 128;   // 128 tokens x 64 features, 128-byte swizzle
+constexpr int kWBox = kC * 64;   // 128 tokens x 32 columns, 64-byte swizzle
+
+// Shared memory, from a 1024-byte aligned base: two slots each of x, y and w,
+// w~ (one buffer; two in the pass that only sums states), the state's bf16
+// values, powers of the decay, barriers.
+template <int DX, bool STATE>
+struct Lay {
+  static constexpr int kTile = DX / 64 * kBox;
+  static constexpr int kX = 0;
+  static constexpr int kY = STATE ? 0 : 2 * kTile;
+  static constexpr int kW = kY + 2 * kTile;
+  static constexpr int kWt = kW + 2 * kWBox;
+  static constexpr int kWtBuf = 3 * kWBox;
+  static constexpr int kSop = kWt + (STATE ? 2 : 1) * kWtBuf;
+  static constexpr int kSopAtom = DX * 64;
+  static constexpr int kPow = kSop + (STATE ? 0 : 2 * kSopAtom);
+  static constexpr int kBar = kPow + (kC + 16) * 4;
+  static constexpr int kNumBars = 24;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+// Tensor memory columns: raw weights, P as bf16 pairs, dS (twice in the pass
+// that only sums states), O1, O2.
+constexpr uint32_t kColR = 0, kColP = 128, kColD = 192, kColD2 = 288, kColO1 = 288, kColO2 = 352;
+
+enum Bar : int {
+  kXFull = 0,    // [2] tile landed
+  kXEmpty = 2,   // [2] slot free (MMA commit)
+  kYFull = 4,    // [2]
+  kYEmpty = 6,   // [2]
+  kWFull = 8,    // [2]
+  kWEmpty = 10,  // [2]
+  kRFull = 12,   // raw weights computed (and P of the chunk before read)
+  kPReady = 13,  // P written
+  kOFull = 14,   // O1, O2 complete
+  kOFree = 15,   // O1, O2 read
+  kDFull = 16,   // [2] dS computed
+  // [2], of which the main pass uses one: there each chunk's hand-offs wait for
+  // the ones before; the pass that only sums states works two chunks at a time
+  kSReady = 18,  // the state's bf16 values written (dS of the chunk before read)
+  kWReady = 20,  // w~ written
+  kDrain = 22,
+};
+
+struct TcRole {
+  CUtensorMap m[3];  // x, y, w
+  uint8_t at[3][4];  // places of head, token and batch among each map's outer dimensions
+};
+struct TcParams {
+  RetArgs a;
+  TcRole map[kRetRoles];
+  int parts, cpp, slices;
+  unsigned int *timeouts;
+};
+
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+  tmem_st16(taddr, f);
+}
+
+// A pair of fp32 values as NS pairs of bf16 values that add up to them (each
+// remainder is exact).
+template <int NS>
+__device__ __forceinline__ void split2(float a, float b, uint32_t *out) {
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    out[s] = pack_bf16x2(a, b);
+    a -= __uint_as_float(out[s] << 16);
+    b -= __uint_as_float(out[s] & 0xffff0000u);
+  }
+}
+
+template <int DX, int NS, bool STATE>
+__global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_constant__ TcParams p) {
+  using Ly = Lay<DX, STATE>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~static_cast<uintptr_t>(1023));
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Ly::kBar);
+  float *pw = reinterpret_cast<float *>(sm + Ly::kPow);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Ly::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Ly::kMisc + 4);
+
+  const RetRole &r = p.a.role[blockIdx.z];
+  const TcRole &map = p.map[blockIdx.z];
+  const int np = STATE ? p.parts - 1 : p.parts;
+  const int slice = blockIdx.x % p.slices, part = blockIdx.x / p.slices % np;
+  const int64_t bh = blockIdx.x / p.slices / np;
+  const int e0 = slice * kSW;
+  if (e0 >= r.Dw) return;
+  const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tokens = ret_tokens(p.a.lens, b, p.a.L);
+  const int n = (tokens + kC - 1) / kC;
+  const bool last_part = part == p.parts - 1;
+  const int c0 = min(n, part * p.cpp), nc = (last_part ? n : min(n, c0 + p.cpp)) - c0;
+  const bool keep = STATE || (last_part && r.end);  // the state behind the last chunk is wanted
+  const float lg = p.a.lg.g[h];
+  // chunk c of the part: its first token and how many it has
+  auto first = [&](int c) { return (r.reverse ? n - 1 - c0 - c : c0 + c) * kC; };
+  auto size = [&](int c) { return min(kC, tokens - first(c)); };
+
+  if (tid < kC + 1) pw[tid] = exp2f(lg * static_cast<float>(tid));
+  if (tid == 32 * kWarpTma) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar[kXFull + s], 1);
+      mbar_init(&bar[kXEmpty + s], 1);
+      mbar_init(&bar[kYFull + s], 1);
+      mbar_init(&bar[kYEmpty + s], 1);
+      mbar_init(&bar[kWFull + s], 1);
+      mbar_init(&bar[kWEmpty + s], 1);
+      mbar_init(&bar[kDFull + s], 1);
+      mbar_init(&bar[kSReady + s], 4);
+      mbar_init(&bar[kWReady + s], 4);
+    }
+    mbar_init(&bar[kRFull], 1);
+    mbar_init(&bar[kPReady], 8);
+    mbar_init(&bar[kOFull], 1);
+    mbar_init(&bar[kOFree], 4);
+    mbar_init(&bar[kDrain], 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kWarpTma) {
+    if (lane < 3 && !(STATE && lane == 0)) {
+      const CUtensorMap *m = &map.m[lane];
+      const uint8_t *at = map.at[lane];
+      prefetch_tmap(m);
+      uint64_t *fullb = &bar[lane == 0 ? kXFull : (lane == 1 ? kYFull : kWFull)];
+      uint64_t *emptyb = &bar[lane == 0 ? kXEmpty : (lane == 1 ? kYEmpty : kWEmpty)];
+      const int head = h / (lane == 0 ? r.xg : (lane == 1 ? r.yg : r.wg));
+      int issued = 0;
+      for (int c = 0; c < nc; ++c) {
+        const int sl = c & 1;
+        if (!mbar_wait(&emptyb[sl], ((c >> 1) & 1) ^ 1, abort_flag, p.timeouts)) break;
+        const int t0 = first(c);
+        auto place = [&](int i) { return at[0] == i ? head : (at[1] == i ? t0 : b); };
+        const int y = place(0), z = place(1), w = place(2);
+        if (lane == 2) {
+          mbar_arrive_expect_tx(&fullb[sl], kWBox);
+          tma_load_4d(sm + Ly::kW + sl * kWBox, m, e0, y, z, w, &fullb[sl]);
+        } else {
+          uint8_t *dst = sm + (lane == 0 ? Ly::kX : Ly::kY) + sl * Ly::kTile;
+          mbar_arrive_expect_tx(&fullb[sl], Ly::kTile);
+#pragma unroll
+          for (int i = 0; i < DX / 64; ++i) tma_load_4d(dst + i * kBox, m, 64 * i, y, z, w, &fullb[sl]);
+        }
+        issued = c + 1;
+      }
+      if (*abort_flag)  // let every issued copy land before the CTA exits
+        for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c)
+          mbar_wait_drain(&fullb[c & 1], (c >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    const bool leader = lane == 0;
+    constexpr uint32_t ID_R = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * kSW, false, true);
+    constexpr uint32_t ID_D = idesc_bf16(DX, NS * kSW, true, true);
+    constexpr uint32_t ID_O2 = idesc_bf16(128, kSW, false, true);
+    const uint32_t base = smem_u32(sm);
+    // rows as K-major operands (K = features) and y^T as A (M = features in
+    // 64-wide atoms, K = tokens); w, w~ and the state with columns in atoms of 32
+    auto rows = [&](int at, int sl) { return smem_desc(base + at + sl * Ly::kTile, 16, 1024, kSw128); };
+    auto turned = [&](int sl) { return smem_desc(base + Ly::kY + sl * Ly::kTile, kBox, 1024, kSw128); };
+    const uint64_t dsop = smem_desc(base + Ly::kSop, Ly::kSopAtom, 512, kSw64);
+    for (int c = 0; c < nc; ++c) {
+      const int sl = c & 1;
+      const uint32_t ph = (c >> 1) & 1;
+      if (!STATE) {
+        if (!warp_wait(&bar[kXFull + sl], ph, abort_flag, p.timeouts) ||
+            !warp_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts))
+          break;
+        // rows behind the end have to be zero first
+        if (size(c) < kC && !warp_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts)) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t a = rows(Ly::kX, sl), bb = rows(Ly::kY, sl);
+#pragma unroll
+          for (int kk = 0; kk < DX / 16; ++kk) {
+            const uint64_t at = (kk >> 2) * (kBox >> 4) + (kk & 3) * 2;
+            mma_bf16(tmem + kColR, a + at, bb + at, ID_R, kk > 0);
+          }
+          mma_commit(&bar[kRFull]);
+        }
+        __syncwarp();
+        if (!warp_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts) ||
+            (c > 0 && !warp_wait(&bar[kOFree], (c - 1) & 1, abort_flag, p.timeouts)))
+          break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t a = rows(Ly::kX, sl);
+#pragma unroll
+          for (int kk = 0; kk < DX / 16; ++kk)
+            mma_bf16(tmem + kColO1, a + (kk >> 2) * (kBox >> 4) + (kk & 3) * 2, dsop + kk * 64, ID_O1, kk > 0);
+          mma_commit(&bar[kXEmpty + sl]);
+        }
+        __syncwarp();
+      } else if (c > 1 && !warp_wait(&bar[kSReady + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
+        break;  // dS of two chunks ago has been read
+      }
+      if (!warp_wait(&bar[kWReady + (STATE ? sl : 0)], STATE ? ph : c & 1, abort_flag, p.timeouts)) break;
+      if (STATE && !warp_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) break;
+      tc_fence_after();
+      if (leader) {
+        if (keep || c + 1 < nc) {
+          const uint64_t a = turned(sl);
+          const uint64_t bb = smem_desc(base + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kWBox, 512, kSw64);
+          const uint32_t d = tmem + (STATE && sl ? kColD2 : kColD);
+#pragma unroll
+          for (int kk = 0; kk < kC / 16; ++kk) mma_bf16(d, a + kk * 128, bb + kk * 64, ID_D, kk > 0);
+        }
+        mma_commit(&bar[kDFull + sl]);
+        mma_commit(&bar[kYEmpty + sl]);
+      }
+      __syncwarp();
+      if (!STATE) {
+        if (!warp_wait(&bar[kPReady], c & 1, abort_flag, p.timeouts)) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t bb = smem_desc(base + Ly::kW + sl * kWBox, kWBox, 512, kSw64);
+#pragma unroll
+          for (int kk = 0; kk < kC / 16; ++kk)
+            mma_bf16_ta(tmem + kColO2, tmem + kColP + 8 * kk, bb + kk * 64, ID_O2, kk > 0);
+          mma_commit(&bar[kOFull]);
+        }
+      }
+      if (leader) mma_commit(&bar[kWEmpty + sl]);
+      __syncwarp();
+    }
+    if (leader) {  // every MMA issued has completed before TMEM is released
+      mma_commit(&bar[kDrain]);
+      mbar_wait_drain(&bar[kDrain], 0);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpW) {
+    const int qd = warp - kWarpW, t = 32 * qd + lane;
+    uint8_t *out = static_cast<uint8_t *>(r.o);
+    const int64_t unit = b * r.os.b + h * r.os.h + e0;
+    for (int c = 0; c <= nc; ++c) {
+      if (c < nc) {
+        const int sl = c & 1, nv = size(c);
+        const uint32_t ph = (c >> 1) & 1;
+        const float f = t < nv ? exp2f(lg * static_cast<float>(r.reverse ? t + 1 : nv - 1 - t)) : 0.f;
+        // the buffer is free once the sum over the chunk that used it is done
+        const int before = c - (STATE ? 2 : 1);
+        if (!warp_wait(&bar[kWFull + sl], ph, abort_flag, p.timeouts) ||
+            (nv < kC && !warp_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) ||
+            (before >= 0 && !warp_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
+          break;
+        uint8_t *wrow = sm + Ly::kW + sl * kWBox;
+        uint8_t *wt = sm + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0);
+        if (t < nv) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(wrow + sw64_off(t, 16 * q));
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            uint32_t s[4][NS];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              split2<NS>(f * __uint_as_float(u[k] << 16), f * __uint_as_float(u[k] & 0xffff0000u), s[k]);
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+              *reinterpret_cast<uint4 *>(wt + j * kWBox + sw64_off(t, 16 * q)) =
+                  make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
+          }
+        } else {
+          const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            *reinterpret_cast<uint4 *>(wrow + sw64_off(t, 16 * q)) = z;
+#pragma unroll
+            for (int j = 0; j < NS; ++j) *reinterpret_cast<uint4 *>(wt + j * kWBox + sw64_off(t, 16 * q)) = z;
+          }
+#pragma unroll
+          for (int i = 0; i < DX / 64; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4 *>(sm + Ly::kY + sl * Ly::kTile + i * kBox + sw128_off(t, 16 * q)) = z;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kWReady + (STATE ? sl : 0)]);
+      }
+      if (!STATE && c > 0) {  // rows of chunk c - 1
+        const int l = c - 1, nv = size(l);
+        const float f = r.out_scale * exp2f(lg * static_cast<float>(r.reverse ? nv - 1 - t : t + 1));
+        if (!warp_wait(&bar[kOFull], l & 1, abort_flag, p.timeouts)) break;
+        tc_fence_after();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float hi[16], lo[16];
+          tmem_ld16(tmem_addr(tmem, 32 * qd, kColO1 + 16 * j), hi);
+          tmem_ld16(tmem_addr(tmem, 32 * qd, kColO1 + 32 + 16 * j), lo);
+          tmem_ld16(tmem_addr(tmem, 32 * qd, kColO2 + 16 * j), v + 16 * j);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[16 * j + e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[16 * j + e]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(&bar[kOFree]);
+        if (t < nv) {
+          const int64_t at = unit + (first(l) + t) * r.os.t;
+          if (r.o_f32) {
+            float4 *to = reinterpret_cast<float4 *>(out + at * 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else {
+            uint4 *to = reinterpret_cast<uint4 *>(out + at * 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                 pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          }
+        }
+      }
+    }
+    if (!STATE && p.a.fill && last_part)
+      for (int i = tokens + t; i < p.a.L; i += kC) {
+        const int64_t at = unit + i * r.os.t;
+        uint4 *to = reinterpret_cast<uint4 *>(out + at * (r.o_f32 ? 4 : 2));
+        for (int e = 0; e < (r.o_f32 ? 8 : 4); ++e) to[e] = make_uint4(0, 0, 0, 0);
+      }
+  } else if (warp >= kWarpS) {
+    // row d of the state: all 32 lanes of a quadrant, or (64 features) 16
+    const int qd = warp - kWarpS;
+    const int d = DX == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
+    const bool mine = DX == 128 || lane < 16;
+    const int64_t size_of = static_cast<int64_t>(DX) * r.Dw;
+    float *rec = r.rec + bh * (p.parts - 1) * size_of;
+    float S[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) S[e] = 0.f;
+    if (!STATE) {
+      const int here = ret_before(part * p.cpp, n, tokens, kC, r.reverse);
+      if (r.start) {
+        const float f = exp2f(lg * static_cast<float>(here)) * r.start_scale;
+        const float *from = r.start + bh * size_of + static_cast<int64_t>(d) * r.start_rs +
+                            static_cast<int64_t>(e0) * r.start_cs;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = f * from[static_cast<int64_t>(e) * r.start_cs];
+      }
+      for (int j = 0; j < part; ++j) {
+        const float f = exp2f(lg * static_cast<float>(here - ret_before((j + 1) * p.cpp, n, tokens, kC, r.reverse)));
+        const float4 *from = reinterpret_cast<const float4 *>(rec + j * size_of + d * r.Dw + e0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 v = from[e];
+          S[4 * e] = fmaf(f, v.x, S[4 * e]);
+          S[4 * e + 1] = fmaf(f, v.y, S[4 * e + 1]);
+          S[4 * e + 2] = fmaf(f, v.z, S[4 * e + 2]);
+          S[4 * e + 3] = fmaf(f, v.w, S[4 * e + 3]);
+        }
+      }
+    }
+    bool ok = true;
+    for (int c = 0; c <= nc; ++c) {
+      if (c > 0 && (c < nc || keep)) {  // S <- g^n S + dS of chunk c - 1
+        const int l = c - 1;
+        const float g = exp2f(lg * static_cast<float>(size(l)));
+        if (!warp_wait(&bar[kDFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = tmem_addr(tmem, 32 * qd, STATE && (l & 1) ? kColD2 : kColD);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x[NS][16];
+#pragma unroll
+          for (int k = 0; k < NS; ++k) tmem_ld16(at + 32 * k + 16 * j, x[k]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            S[16 * j + e] = fmaf(g, S[16 * j + e], NS == 3 ? x[0][e] + (x[1][e] + x[NS - 1][e]) : x[0][e] + x[1][e]);
+        }
+        tc_fence_before();
+      }
+      if (STATE) {
+        __syncwarp();
+        if (c > 0 && c < nc && lane == 0) mbar_arrive(&bar[kSReady + ((c - 1) & 1)]);
+      } else if (c < nc) {
+        if (mine) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) split2<2>(S[8 * q + 2 * k], S[8 * q + 2 * k + 1], s[k]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<uint4 *>(sm + Ly::kSop + j * Ly::kSopAtom + sw64_off(d, 16 * q)) =
+                  make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kSReady]);
+      }
+    }
+    if (keep && ok && mine) {
+      float4 *to = reinterpret_cast<float4 *>((STATE ? rec + part * size_of : r.end + bh * size_of) + d * r.Dw + e0);
+      const float f = STATE ? 1.f : r.end_scale;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        to[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
+    }
+  } else if (!STATE) {
+    // P: rows of quadrant qd, blocks of 32 columns h2 and h2 + 2
+    const int qd = warp & 3, h2 = warp >> 2, i = 32 * qd + lane;
+    const bool rev = r.reverse;
+    const uint32_t tr = tmem_addr(tmem, 32 * qd, kColR), tp = tmem_addr(tmem, 32 * qd, kColP);
+    // blocks without a weight are zero once and for all
+    float far[2];  // power of the decay between this row and the near end of the block
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int g = h2 + 2 * k;
+      const int gap = rev ? 32 * g - i : i - 32 * g - 31;
+      far[k] = gap >= 0 ? pw[gap] : 0.f;
+      if (rev ? g < qd : g > qd) {
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = 0u;
+        tmem_st16u(tp + 16 * g, z);
+      }
+    }
+    tmem_wait_st();
+    for (int c = 0; c < nc; ++c) {
+      if (!warp_wait(&bar[kRFull], c & 1, abort_flag, p.timeouts)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int g = h2 + 2 * k;
+        if (rev ? g < qd : g > qd) continue;
+        float a[32];
+        uint32_t pk[16];
+        tmem_ld32(tr + 32 * g, a);
+        tmem_wait_ld();
+        if (g == qd) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int gap = rev ? e - lane : lane - e;
+            a[e] = gap >= 0 ? a[e] * pw[gap >= 0 ? gap : 0] : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] *= far[k] * pw[rev ? e : 31 - e];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+        tmem_st16u(tp + 16 * g, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[kPReady]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int DX, int NS, bool STATE>
+cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
+  auto k = retention_tc_kernel<DX, NS, STATE>;
+  const int bytes = Lay<DX, STATE>::kAlloc;
+  const cudaError_t e = allow_smem(k, bytes);
+  if (e != cudaSuccess) return e;
+  const int np = STATE ? p.parts - 1 : p.parts;
+  k<<<dim3(static_cast<unsigned>(units * np), 1, p.a.roles), kThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DX>
+cudaError_t go_all(const TcParams &p, bool exact, int64_t units, cudaStream_t s) {
+  if (p.parts > 1) {
+    const cudaError_t e = exact ? go<DX, 3, true>(p, units, s) : go<DX, 2, true>(p, units, s);
+    if (e != cudaSuccess) return e;
+  }
+  return exact ? go<DX, 3, false>(p, units, s) : go<DX, 2, false>(p, units, s);
+}
+
+}  // namespace
+
+bool ret_tc_supported(const RetArgs &a, Dtype dt) {
+  if (dt != kBF16) return false;
+  for (int i = 0; i < a.roles; ++i)
+    if ((a.role[i].Dx != 64 && a.role[i].Dx != 128) || a.role[i].Dw % kSW != 0) return false;
+  return true;
+}
+
+int ret_parts_tc(const RetArgs &a) {
+  int64_t units = 0;
+  for (int i = 0; i < a.roles; ++i) units += static_cast<int64_t>(a.B) * a.H * (a.role[i].Dw / kSW);
+  const int chunks = (a.L + kC - 1) / kC;
+  // Parts cost a pass over y and w for their records (about half of a chunk's
+  // time) and a launch (about four chunks' time).
+  int64_t parts = kSMs / (units > 0 ? units : 1);
+  if (parts > 16) parts = 16;
+  if (parts > chunks / 4) parts = chunks / 4;
+  if (parts < 2 || 1.5 * chunks / parts + 4 > chunks) return 1;
+  return static_cast<int>(parts);
+}
+
+cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
+  const int chunks = (a.L + kC - 1) / kC;
+  unsigned int *timeouts = wait_timeout_counter();
+  if (!timeouts) return cudaErrorNotSupported;
+  // one launch for the roles of each number of features
+  for (const int DX : {64, 128}) {
+    TcParams p = {};
+    p.a = a;
+    p.a.roles = 0;
+    p.parts = parts;
+    p.cpp = (chunks + parts - 1) / parts;
+    p.timeouts = timeouts;
+    bool exact = false;
+    for (int i = 0; i < a.roles; ++i) {
+      const RetRole &r = a.role[i];
+      if (r.Dx != DX) continue;
+      TcRole &m = p.map[p.a.roles];
+      auto encode = [&](int i, const void *base, int width, int group, const RetStrides &s, int box) {
+        return make_tmap_heads(&m.m[i], base, width, a.H / group, a.L, a.B, s.h, s.t, s.b, box, kC, m.at[i]);
+      };
+      if (!encode(0, r.x, DX, r.xg, r.xs, 64) || !encode(1, r.y, DX, r.yg, r.ys, 64) ||
+          !encode(2, r.w, r.Dw, r.wg, r.ws, kSW))
+        return cudaErrorNotSupported;
+      p.a.role[p.a.roles++] = r;
+      if (r.Dw / kSW > p.slices) p.slices = r.Dw / kSW;
+      exact |= r.end != nullptr;
+    }
+    if (!p.a.roles) continue;
+    const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
+    if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
+    const cudaError_t e = DX == 64 ? go_all<64>(p, exact, units, s) : go_all<128>(p, exact, units, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace linattn

@@ -112,6 +112,14 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
 // TMA tile store from shared memory (bulk-group completion), and the
 // bulk-group bookkeeping of the issuing thread.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *smem_src, int x,
@@ -410,6 +418,15 @@ bool make_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t dim_x, uint6
 // batches), box (box_x, box_y, 1), no swizzle, zero fill out of bounds.
 bool make_tmap_rows(CUtensorMap *map, const void *base, int elem_bytes, uint64_t width,
                     uint64_t rows, uint64_t batch, uint64_t ld, uint32_t box_x, uint32_t box_y);
+
+// Host: encode a rank-4 bf16 map over rows of `width` elements per (head, token,
+// batch), strides in elements, box of box_x columns of box_t tokens, swizzle of
+// box_x * 2 bytes (64 or 128), zero fill out of bounds.  The map's outer
+// dimensions go by their strides; at[0..2] receive the places (0 to 2) of head,
+// token and batch among them.
+bool make_tmap_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t tokens,
+                     uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride,
+                     uint32_t box_x, uint32_t box_t, uint8_t *at);
 
 // Host: device address of the wait-timeout counter on the current device
 // (nullptr if it cannot be obtained).

@@ -228,6 +228,28 @@ def test_long_decay_far(la):
     close("state", S, rS, mS, p.K + 40, F32)
 
 
+@DT
+@pytest.mark.parametrize("shape", [(1, 3000, 1, 1, 128, 128), (1, 2817, 2, 1, 64, 64), (2, 2500, 1, 1, 128, 64),
+                                   (1, 2600, 1, 1, 72, 40)], ids=sid)
+def test_parts(la, dtype, shape):
+    """Few heads over many tokens, worked in parts that all reach the end: weak
+    decays and none; ragged lengths that end in front of the last parts."""
+    for gamma in (1.0, 0.9995):
+        p = Problem(shape, dtype, 77, lens=[shape[1] - 5, 900][:shape[0]])
+        p.gamma = torch.full((shape[2],), gamma)
+        (ro, rS), (mo, mS) = p.ref(), p.ref(True)
+        o, S = la.forward_retention(*p.dev(), **p.kw(), return_state=True)
+        for b, n in enumerate(p.lens):
+            o[b, n:] = 0
+        close("parts o", o, ro, mo, p.K, dtype, True)
+        close("parts state", S, rS, mS, p.K, F32)
+        ref, mag = p.grads(), p.grads(True)
+        got = la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())
+        for name, x, r, m in zip(("dq", "dk", "dv"), got, ref, mag):
+            close("parts " + name, x, r, m, p.K, dtype, True)
+        close("parts dS0", got[3], ref[3], mag[3], p.K, F32)
+
+
 STEPS = [(1, 2, 1, 64, 64), (3, 4, 4, 128, 128), (2, 3, 3, 8, 16), (2, 2, 1, 256, 256), (1, 3, 3, 96, 40),
          (40, 16, 8, 64, 128), (40, 16, 16, 128, 64), (30, 16, 2, 136, 200)]
 
