@@ -23,10 +23,10 @@
 //
 // Warp roles (18 warps):
 //   0-7    P: powers of the decay, mask, bf16 (a lane quadrant and two of its
-//          four blocks of 32 columns each)
+//          four blocks of 32 columns each); then half of the output columns of
+//          the quadrant's tokens
 //   8-11   state: registers, its bf16 values for the MMA (thread = row)
-//   12-15  w~ of a chunk, and zeros behind a ragged sequence's end; then the
-//          output rows of the chunk before (thread = token)
+//   12-15  w~ (thread = token), and zeros behind a ragged sequence's end
 //   16     TMA: lane 0 the x ring, lane 1 the y ring, lane 2 the w ring
 //   17     TMEM owner and MMA issuer
 // Every wait is bounded; a CTA that gives up counts the failure in device
@@ -50,7 +50,7 @@ constexpr int kWBox = kC * 64;   // 128 tokens x 32 columns, 64-byte swizzle
 
 // Shared memory, from a 1024-byte aligned base: two slots each of x, y and w,
 // w~ (one buffer; two in the pass that only sums states), the state's bf16
-// values, powers of the decay, barriers.
+// values, the weights of a chunk's blocks, barriers.
 template <int DX, bool STATE>
 struct Lay {
   static constexpr int kTile = DX / 64 * kBox;
@@ -61,8 +61,11 @@ struct Lay {
   static constexpr int kWtBuf = 3 * kWBox;
   static constexpr int kSop = kWt + (STATE ? 2 : 1) * kWtBuf;
   static constexpr int kSopAtom = DX * 64;
-  static constexpr int kPow = kSop + (STATE ? 0 : 2 * kSopAtom);
-  static constexpr int kBar = kPow + (kC + 16) * 4;
+  // weights of a block of 32 x 32, rows of kLdT floats, for each of the four
+  // distances of a block from the diagonal
+  static constexpr int kLdT = 36;
+  static constexpr int kTab = kSop + (STATE ? 0 : 2 * kSopAtom);
+  static constexpr int kBar = kTab + (STATE ? 0 : 4 * 32 * kLdT * 4);
   static constexpr int kNumBars = 24;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -103,6 +106,57 @@ struct TcParams {
   unsigned int *timeouts;
 };
 
+// warp_wait of tc_common.cuh for a kernel of many waiting warps: the hardware
+// holds the warp until the phase ends or the hint (nanoseconds) runs out, so that
+// waiting warps leave the issue slots and shared memory to the others.
+__device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *timeouts) {
+  auto held = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+  };
+  bool ok = held();
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = held()) && !*abort) {
+      if (clock64() - t0 > kWaitCycles) {
+        *abort = 1;
+        atomicAdd(timeouts, 1u);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// MMAs and commits issued by the warp as one: the predicate of the elected lane
+// inside, so that operands stay in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
   float f[16];
 #pragma unroll
@@ -129,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                             ~static_cast<uintptr_t>(1023));
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Ly::kBar);
-  float *pw = reinterpret_cast<float *>(sm + Ly::kPow);
+  float *tab = reinterpret_cast<float *>(sm + Ly::kTab);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Ly::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Ly::kMisc + 4);
 
@@ -141,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   const int e0 = slice * kSW;
   if (e0 >= r.Dw) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the shuffle tells the compiler that a warp agrees on its role
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int tokens = ret_tokens(p.a.lens, b, p.a.L);
   const int n = (tokens + kC - 1) / kC;
   const bool last_part = part == p.parts - 1;
@@ -152,7 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   auto first = [&](int c) { return (r.reverse ? n - 1 - c0 - c : c0 + c) * kC; };
   auto size = [&](int c) { return min(kC, tokens - first(c)); };
 
-  if (tid < kC + 1) pw[tid] = exp2f(lg * static_cast<float>(tid));
+  if (!STATE)
+    for (int i = tid; i < 4 * 32 * 32; i += kThreads) {
+      const int row = i >> 5 & 31, e = i & 31, gap = 32 * (i >> 10) + (r.reverse ? e - row : row - e);
+      tab[(i >> 5) * Ly::kLdT + e] = gap >= 0 ? exp2f(lg * static_cast<float>(gap)) : 0.f;
+    }
   if (tid == 32 * kWarpTma) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[kXFull + s], 1);
@@ -168,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     mbar_init(&bar[kRFull], 1);
     mbar_init(&bar[kPReady], 8);
     mbar_init(&bar[kOFull], 1);
-    mbar_init(&bar[kOFree], 4);
+    mbar_init(&bar[kOFree], 8);
     mbar_init(&bar[kDrain], 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -211,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
-    const bool leader = lane == 0;
     constexpr uint32_t ID_R = idesc_bf16(128, 128, false, false);
     constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * kSW, false, true);
     constexpr uint32_t ID_D = idesc_bf16(DX, NS * kSW, true, true);
@@ -226,85 +284,74 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       const int sl = c & 1;
       const uint32_t ph = (c >> 1) & 1;
       if (!STATE) {
-        if (!warp_wait(&bar[kXFull + sl], ph, abort_flag, p.timeouts) ||
-            !warp_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts))
+        if (!held_wait(&bar[kXFull + sl], ph, abort_flag, p.timeouts) ||
+            !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts))
           break;
         // rows behind the end have to be zero first
-        if (size(c) < kC && !warp_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts)) break;
+        if (size(c) < kC && !held_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
-        if (leader) {
+        {
           const uint64_t a = rows(Ly::kX, sl), bb = rows(Ly::kY, sl);
 #pragma unroll
           for (int kk = 0; kk < DX / 16; ++kk) {
             const uint64_t at = (kk >> 2) * (kBox >> 4) + (kk & 3) * 2;
-            mma_bf16(tmem + kColR, a + at, bb + at, ID_R, kk > 0);
+            mma_ss(tmem + kColR, a + at, bb + at, ID_R, kk > 0);
           }
-          mma_commit(&bar[kRFull]);
+          commit(&bar[kRFull]);
         }
-        __syncwarp();
-        if (!warp_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts) ||
-            (c > 0 && !warp_wait(&bar[kOFree], (c - 1) & 1, abort_flag, p.timeouts)))
+        if (!held_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts) ||
+            (c > 0 && !held_wait(&bar[kOFree], (c - 1) & 1, abort_flag, p.timeouts)))
           break;
         tc_fence_after();
-        if (leader) {
+        {
           const uint64_t a = rows(Ly::kX, sl);
 #pragma unroll
           for (int kk = 0; kk < DX / 16; ++kk)
-            mma_bf16(tmem + kColO1, a + (kk >> 2) * (kBox >> 4) + (kk & 3) * 2, dsop + kk * 64, ID_O1, kk > 0);
-          mma_commit(&bar[kXEmpty + sl]);
+            mma_ss(tmem + kColO1, a + (kk >> 2) * (kBox >> 4) + (kk & 3) * 2, dsop + kk * 64, ID_O1, kk > 0);
+          commit(&bar[kXEmpty + sl]);
         }
-        __syncwarp();
-      } else if (c > 1 && !warp_wait(&bar[kSReady + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
+      } else if (c > 1 && !held_wait(&bar[kSReady + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
         break;  // dS of two chunks ago has been read
       }
-      if (!warp_wait(&bar[kWReady + (STATE ? sl : 0)], STATE ? ph : c & 1, abort_flag, p.timeouts)) break;
-      if (STATE && !warp_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) break;
+      if (!held_wait(&bar[kWReady + (STATE ? sl : 0)], STATE ? ph : c & 1, abort_flag, p.timeouts)) break;
+      if (STATE && !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) break;
       tc_fence_after();
-      if (leader) {
-        if (keep || c + 1 < nc) {
-          const uint64_t a = turned(sl);
-          const uint64_t bb = smem_desc(base + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kWBox, 512, kSw64);
-          const uint32_t d = tmem + (STATE && sl ? kColD2 : kColD);
+      if (keep || c + 1 < nc) {
+        const uint64_t a = turned(sl);
+        const uint64_t bb = smem_desc(base + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kWBox, 512, kSw64);
+        const uint32_t d = tmem + (STATE && sl ? kColD2 : kColD);
 #pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk) mma_bf16(d, a + kk * 128, bb + kk * 64, ID_D, kk > 0);
-        }
-        mma_commit(&bar[kDFull + sl]);
-        mma_commit(&bar[kYEmpty + sl]);
+        for (int kk = 0; kk < kC / 16; ++kk) mma_ss(d, a + kk * 128, bb + kk * 64, ID_D, kk > 0);
       }
-      __syncwarp();
+      commit(&bar[kDFull + sl]);
+      commit(&bar[kYEmpty + sl]);
       if (!STATE) {
-        if (!warp_wait(&bar[kPReady], c & 1, abort_flag, p.timeouts)) break;
+        if (!held_wait(&bar[kPReady], c & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
-        if (leader) {
-          const uint64_t bb = smem_desc(base + Ly::kW + sl * kWBox, kWBox, 512, kSw64);
+        const uint64_t bb = smem_desc(base + Ly::kW + sl * kWBox, kWBox, 512, kSw64);
 #pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk)
-            mma_bf16_ta(tmem + kColO2, tmem + kColP + 8 * kk, bb + kk * 64, ID_O2, kk > 0);
-          mma_commit(&bar[kOFull]);
-        }
+        for (int kk = 0; kk < kC / 16; ++kk)
+          mma_ts(tmem + kColO2, tmem + kColP + 8 * kk, bb + kk * 64, ID_O2, kk > 0);
+        commit(&bar[kOFull]);
       }
-      if (leader) mma_commit(&bar[kWEmpty + sl]);
-      __syncwarp();
+      commit(&bar[kWEmpty + sl]);
     }
-    if (leader) {  // every MMA issued has completed before TMEM is released
-      mma_commit(&bar[kDrain]);
-      mbar_wait_drain(&bar[kDrain], 0);
-    }
+    // every MMA issued has completed before TMEM is released
+    commit(&bar[kDrain]);
+    mbar_wait_drain(&bar[kDrain], 0);
     __syncwarp();
   } else if (warp >= kWarpW) {
-    const int qd = warp - kWarpW, t = 32 * qd + lane;
-    uint8_t *out = static_cast<uint8_t *>(r.o);
-    const int64_t unit = b * r.os.b + h * r.os.h + e0;
-    for (int c = 0; c <= nc; ++c) {
-      if (c < nc) {
+    const int t = tid - 32 * kWarpW;
+    for (int c = 0; c < nc; ++c) {
+      {
         const int sl = c & 1, nv = size(c);
         const uint32_t ph = (c >> 1) & 1;
         const float f = t < nv ? exp2f(lg * static_cast<float>(r.reverse ? t + 1 : nv - 1 - t)) : 0.f;
         // the buffer is free once the sum over the chunk that used it is done
         const int before = c - (STATE ? 2 : 1);
-        if (!warp_wait(&bar[kWFull + sl], ph, abort_flag, p.timeouts) ||
-            (nv < kC && !warp_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) ||
-            (before >= 0 && !warp_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
+        if (!held_wait(&bar[kWFull + sl], ph, abort_flag, p.timeouts) ||
+            (nv < kC && !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) ||
+            (before >= 0 && !held_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
           break;
         uint8_t *wrow = sm + Ly::kW + sl * kWBox;
         uint8_t *wt = sm + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0);
@@ -340,47 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[kWReady + (STATE ? sl : 0)]);
       }
-      if (!STATE && c > 0) {  // rows of chunk c - 1
-        const int l = c - 1, nv = size(l);
-        const float f = r.out_scale * exp2f(lg * static_cast<float>(r.reverse ? nv - 1 - t : t + 1));
-        if (!warp_wait(&bar[kOFull], l & 1, abort_flag, p.timeouts)) break;
-        tc_fence_after();
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float hi[16], lo[16];
-          tmem_ld16(tmem_addr(tmem, 32 * qd, kColO1 + 16 * j), hi);
-          tmem_ld16(tmem_addr(tmem, 32 * qd, kColO1 + 32 + 16 * j), lo);
-          tmem_ld16(tmem_addr(tmem, 32 * qd, kColO2 + 16 * j), v + 16 * j);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[16 * j + e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[16 * j + e]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed(&bar[kOFree]);
-        if (t < nv) {
-          const int64_t at = unit + (first(l) + t) * r.os.t;
-          if (r.o_f32) {
-            float4 *to = reinterpret_cast<float4 *>(out + at * 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          } else {
-            uint4 *to = reinterpret_cast<uint4 *>(out + at * 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                 pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
-          }
-        }
-      }
     }
-    if (!STATE && p.a.fill && last_part)
-      for (int i = tokens + t; i < p.a.L; i += kC) {
-        const int64_t at = unit + i * r.os.t;
-        uint4 *to = reinterpret_cast<uint4 *>(out + at * (r.o_f32 ? 4 : 2));
-        for (int e = 0; e < (r.o_f32 ? 8 : 4); ++e) to[e] = make_uint4(0, 0, 0, 0);
-      }
   } else if (warp >= kWarpS) {
     // row d of the state: all 32 lanes of a quadrant, or (64 features) 16
     const int qd = warp - kWarpS;
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       if (c > 0 && (c < nc || keep)) {  // S <- g^n S + dS of chunk c - 1
         const int l = c - 1;
         const float g = exp2f(lg * static_cast<float>(size(l)));
-        if (!warp_wait(&bar[kDFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) {
+        if (!held_wait(&bar[kDFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) {
           ok = false;
           break;
         }
@@ -465,55 +472,87 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         to[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
     }
   } else if (!STATE) {
-    // P: rows of quadrant qd, blocks of 32 columns h2 and h2 + 2
-    const int qd = warp & 3, h2 = warp >> 2, i = 32 * qd + lane;
+    // P: rows of quadrant qd, blocks of 32 columns h2 and h2 + 2; output columns
+    // [16 h2, + 16)
+    const int qd = warp & 3, h2 = warp >> 2, t = 32 * qd + lane;
     const bool rev = r.reverse;
-    const uint32_t tr = tmem_addr(tmem, 32 * qd, kColR), tp = tmem_addr(tmem, 32 * qd, kColP);
+    const uint32_t quad = tmem_addr(tmem, 32 * qd, 0);
+    uint8_t *out = static_cast<uint8_t *>(r.o);
+    const int wide = r.o_f32 ? 4 : 2;  // bytes of an output
+    const int64_t unit = b * r.os.b + h * r.os.h + e0 + 16 * h2;
     // blocks without a weight are zero once and for all
-    float far[2];  // power of the decay between this row and the near end of the block
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int g = h2 + 2 * k;
-      const int gap = rev ? 32 * g - i : i - 32 * g - 31;
-      far[k] = gap >= 0 ? pw[gap] : 0.f;
       if (rev ? g < qd : g > qd) {
         uint32_t z[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) z[e] = 0u;
-        tmem_st16u(tp + 16 * g, z);
+        tmem_st16u(quad + kColP + 16 * g, z);
       }
     }
     tmem_wait_st();
     for (int c = 0; c < nc; ++c) {
-      if (!warp_wait(&bar[kRFull], c & 1, abort_flag, p.timeouts)) break;
+      if (!held_wait(&bar[kRFull], c & 1, abort_flag, p.timeouts)) break;
       tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int g = h2 + 2 * k;
-        if (rev ? g < qd : g > qd) continue;
+#pragma unroll 1
+      for (int g = h2; g < 4; g += 2) {
+        const int away = rev ? g - qd : qd - g;
+        if (away < 0) continue;
+        const float4 *w4 = reinterpret_cast<const float4 *>(tab + (32 * away + lane) * Ly::kLdT);
         float a[32];
         uint32_t pk[16];
-        tmem_ld32(tr + 32 * g, a);
+        tmem_ld32(quad + kColR + 32 * g, a);
         tmem_wait_ld();
-        if (g == qd) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int gap = rev ? e - lane : lane - e;
-            a[e] = gap >= 0 ? a[e] * pw[gap >= 0 ? gap : 0] : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) a[e] *= far[k] * pw[rev ? e : 31 - e];
+        for (int e = 0; e < 8; ++e) {
+          const float4 w = w4[e];
+          const float2 lo = unpack2(mul2(pack2(a[4 * e], a[4 * e + 1]), pack2(w.x, w.y)));
+          const float2 hi = unpack2(mul2(pack2(a[4 * e + 2], a[4 * e + 3]), pack2(w.z, w.w)));
+          pk[2 * e] = pack_bf16x2(lo.x, lo.y);
+          pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
-        tmem_st16u(tp + 16 * g, pk);
+        tmem_st16u(quad + kColP + 16 * g, pk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[kPReady]);
+      // output
+      const int nv = size(c);
+      const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
+      if (!held_wait(&bar[kOFull], c & 1, abort_flag, p.timeouts)) break;
+      tc_fence_after();
+      float hi[16], lo[16], v[16];
+      tmem_ld16(quad + kColO1 + 16 * h2, hi);
+      tmem_ld16(quad + kColO1 + 32 + 16 * h2, lo);
+      tmem_ld16(quad + kColO2 + 16 * h2, v);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(&bar[kOFree]);
+      if (t < nv) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
+        uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
+        if (r.o_f32) {
+          float4 *to = reinterpret_cast<float4 *>(at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else {
+          uint4 *to = reinterpret_cast<uint4 *>(at);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                               pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+        }
+      }
     }
+    if (p.a.fill && last_part)
+      for (int i = tokens + t; i < p.a.L; i += kC) {
+        uint4 *to = reinterpret_cast<uint4 *>(out + (unit + i * r.os.t) * wide);
+        for (int e = 0; e < wide; ++e) to[e] = make_uint4(0, 0, 0, 0);
+      }
   }
   __syncwarp();
   tc_fence_before();
