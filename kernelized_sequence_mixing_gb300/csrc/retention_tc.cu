@@ -42,39 +42,43 @@ namespace {
 using namespace tc;
 
 constexpr int kC = 128;  // tokens per chunk
-constexpr int kSW = 32;  // columns of a slice
 constexpr int kThreads = 576;
 constexpr int kWarpS = 8, kWarpW = 12, kWarpTma = 16, kWarpMma = 17;
-constexpr int kBox = kC * 128;   // 128 tokens x 64 features, 128-byte swizzle
-constexpr int kWBox = kC * 64;   // 128 tokens x 32 columns, 64-byte swizzle
+constexpr int kBox = kC * 128;  // 128 tokens x 64 features, 128-byte swizzle
+constexpr int kAtom = kC * 64;  // 128 tokens x 32 columns, 64-byte swizzle
 
-// Shared memory, from a 1024-byte aligned base: two slots each of x, y and w,
+// Shared memory, from a 1024-byte aligned base: slots of x, two slots each of y
+// and w,
 // w~ (one buffer; two in the pass that only sums states), the state's bf16
 // values, the weights of a chunk's blocks, barriers.
-template <int DX, bool STATE>
+template <int DX, int SW, int NS, bool STATE>
 struct Lay {
   static constexpr int kTile = DX / 64 * kBox;
+  static constexpr int kWTile = SW / 32 * kAtom;
   static constexpr int kX = 0;
-  static constexpr int kY = STATE ? 0 : 2 * kTile;
+  static constexpr int kXSlots = SW == 64 && NS == 3 ? 1 : 2;  // what fits
+  static constexpr int kY = STATE ? 0 : kXSlots * kTile;
   static constexpr int kW = kY + 2 * kTile;
-  static constexpr int kWt = kW + 2 * kWBox;
-  static constexpr int kWtBuf = 3 * kWBox;
+  static constexpr int kWt = kW + 2 * kWTile;
+  static constexpr int kWtBuf = NS * kWTile;
   static constexpr int kSop = kWt + (STATE ? 2 : 1) * kWtBuf;
   static constexpr int kSopAtom = DX * 64;
-  // weights of a block of 32 x 32, rows of kLdT floats, for each of the four
-  // distances of a block from the diagonal
+  // weights of a block of 32 x 32 on the diagonal and of the one beside it, rows
+  // of kLdT floats (16-byte accesses of 8 rows meet every bank once)
   static constexpr int kLdT = 36;
-  static constexpr int kTab = kSop + (STATE ? 0 : 2 * kSopAtom);
-  static constexpr int kBar = kTab + (STATE ? 0 : 4 * 32 * kLdT * 4);
+  static constexpr int kTab = kSop + (STATE ? 0 : 2 * (SW / 32) * kSopAtom);
+  static constexpr int kBar = kTab + (STATE ? 0 : 2 * 32 * kLdT * 4);
   static constexpr int kNumBars = 24;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
+  // Tensor memory columns: raw weights, in each block of 32 columns then P as
+  // bf16 pairs in the first 16; O1 with both values of the state side by side;
+  // O2; dS (twice in the pass that only sums states).
+  static constexpr uint32_t cR = 0, cO1 = 128, cO2 = cO1 + 2 * SW;
+  static constexpr uint32_t cD = STATE ? 0 : cO2 + SW, cD2 = NS * SW;
+  static_assert(cD + (STATE ? 2 : 1) * NS * SW <= 512, "tensor memory");
 };
-
-// Tensor memory columns: raw weights, P as bf16 pairs, dS (twice in the pass
-// that only sums states), O1, O2.
-constexpr uint32_t kColR = 0, kColP = 128, kColD = 192, kColD2 = 288, kColO1 = 288, kColO2 = 352;
 
 enum Bar : int {
   kXFull = 0,    // [2] tile landed
@@ -106,55 +110,68 @@ struct TcParams {
   unsigned int *timeouts;
 };
 
-// warp_wait of tc_common.cuh for a kernel of many waiting warps: the hardware
-// holds the warp until the phase ends or the hint (nanoseconds) runs out, so that
-// waiting warps leave the issue slots and shared memory to the others.
-__device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *timeouts) {
-  auto held = [&]() {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    return ok != 0;
-  };
-  bool ok = held();
-  if (!ok) {
-    const long long t0 = clock64();
-    while (!(ok = held()) && !*abort) {
-      if (clock64() - t0 > kWaitCycles) {
-        *abort = 1;
-        atomicAdd(timeouts, 1u);
-        break;
-      }
+// warp_wait of tc_common.cuh for a kernel of many waiting warps with much code:
+// the hardware holds the warp until the phase ends or the hint (nanoseconds) runs
+// out, so that waiting warps leave the issue slots to the others, and what follows
+// a hint that ran out is one function for all waits.
+__device__ __forceinline__ bool held(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool held_longer(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *timeouts) {
+  const long long t0 = clock64();
+  bool ok;
+  while (!(ok = held(bar, parity)) && !*abort) {
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+      atomicAdd(timeouts, 1u);
+      break;
     }
   }
+  return ok;
+}
+__device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *timeouts) {
+  const uint32_t at = smem_u32(bar);
+  bool ok = held(at, parity);
+  if (!ok) ok = held_longer(at, parity, abort, timeouts);
   return __all_sync(0xffffffffu, ok);
 }
 
-// MMAs and commits issued by the warp as one: the predicate of the elected lane
-// inside, so that operands stay in uniform registers.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Of a descriptor only the address in its low word changes from step to step.
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+};
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, const Desc &a, uint32_t a_off, const Desc &b, uint32_t b_off,
+                                       uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+      "r"(a.lo + a_off), "r"(a.hi), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "n"(ADD ? 1 : 0)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, const Desc &b, uint32_t b_off, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "n"(ADD ? 1 : 0)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t *bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
-      : "memory");
+// The lane that issues a group of MMAs, the same every time.  A branch around the
+// group, in a warp the compiler knows to agree on its role: 10 instructions an
+// MMA, against 35 with the election inside each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
@@ -167,18 +184,19 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
 // A pair of fp32 values as NS pairs of bf16 values that add up to them (each
 // remainder is exact).
 template <int NS>
-__device__ __forceinline__ void split2(float a, float b, uint32_t *out) {
+__device__ __forceinline__ void split2(f2 v, uint32_t *out) {
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-    out[s] = pack_bf16x2(a, b);
-    a -= __uint_as_float(out[s] << 16);
-    b -= __uint_as_float(out[s] & 0xffff0000u);
+    const float2 x = unpack2(v);
+    out[s] = pack_bf16x2(x.x, x.y);
+    if (s + 1 < NS)
+      v = add2(v, pack2(__uint_as_float((out[s] << 16) ^ 0x80000000u), __uint_as_float((out[s] & 0xffff0000u) ^ 0x80000000u)));
   }
 }
 
-template <int DX, int NS, bool STATE>
+template <int DX, int SW, int NS, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_constant__ TcParams p) {
-  using Ly = Lay<DX, STATE>;
+  using Ly = Lay<DX, SW, NS, STATE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                             ~static_cast<uintptr_t>(1023));
@@ -192,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   const int np = STATE ? p.parts - 1 : p.parts;
   const int slice = blockIdx.x % p.slices, part = blockIdx.x / p.slices % np;
   const int64_t bh = blockIdx.x / p.slices / np;
-  const int e0 = slice * kSW;
+  const int e0 = slice * SW;
   if (e0 >= r.Dw) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
   // the shuffle tells the compiler that a warp agrees on its role
@@ -208,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   auto size = [&](int c) { return min(kC, tokens - first(c)); };
 
   if (!STATE)
-    for (int i = tid; i < 4 * 32 * 32; i += kThreads) {
+    for (int i = tid; i < 2 * 32 * 32; i += kThreads) {
       const int row = i >> 5 & 31, e = i & 31, gap = 32 * (i >> 10) + (r.reverse ? e - row : row - e);
       tab[(i >> 5) * Ly::kLdT + e] = gap >= 0 ? exp2f(lg * static_cast<float>(gap)) : 0.f;
     }
@@ -248,14 +266,16 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       const int head = h / (lane == 0 ? r.xg : (lane == 1 ? r.yg : r.wg));
       int issued = 0;
       for (int c = 0; c < nc; ++c) {
-        const int sl = c & 1;
-        if (!mbar_wait(&emptyb[sl], ((c >> 1) & 1) ^ 1, abort_flag, p.timeouts)) break;
+        const int sl = lane == 0 ? c % Ly::kXSlots : c & 1, turn = lane == 0 ? c / Ly::kXSlots : c >> 1;
+        if (!mbar_wait(&emptyb[sl], (turn & 1) ^ 1, abort_flag, p.timeouts)) break;
         const int t0 = first(c);
         auto place = [&](int i) { return at[0] == i ? head : (at[1] == i ? t0 : b); };
         const int y = place(0), z = place(1), w = place(2);
         if (lane == 2) {
-          mbar_arrive_expect_tx(&fullb[sl], kWBox);
-          tma_load_4d(sm + Ly::kW + sl * kWBox, m, e0, y, z, w, &fullb[sl]);
+          mbar_arrive_expect_tx(&fullb[sl], Ly::kWTile);
+#pragma unroll
+          for (int i = 0; i < SW / 32; ++i)
+            tma_load_4d(sm + Ly::kW + sl * Ly::kWTile + i * kAtom, m, e0 + 32 * i, y, z, w, &fullb[sl]);
         } else {
           uint8_t *dst = sm + (lane == 0 ? Ly::kX : Ly::kY) + sl * Ly::kTile;
           mbar_arrive_expect_tx(&fullb[sl], Ly::kTile);
@@ -265,80 +285,93 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         issued = c + 1;
       }
       if (*abort_flag)  // let every issued copy land before the CTA exits
-        for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c)
-          mbar_wait_drain(&fullb[c & 1], (c >> 1) & 1);
+        for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) {
+          const int slots = lane == 0 ? Ly::kXSlots : 2;
+          mbar_wait_drain(&fullb[c % slots], (c / slots) & 1);
+        }
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     constexpr uint32_t ID_R = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * kSW, false, true);
-    constexpr uint32_t ID_D = idesc_bf16(DX, NS * kSW, true, true);
-    constexpr uint32_t ID_O2 = idesc_bf16(128, kSW, false, true);
+    constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * SW, false, true);
+    constexpr uint32_t ID_D = idesc_bf16(DX, NS * SW, true, true);
+    constexpr uint32_t ID_O2 = idesc_bf16(128, SW, false, true);
     const uint32_t base = smem_u32(sm);
     // rows as K-major operands (K = features) and y^T as A (M = features in
     // 64-wide atoms, K = tokens); w, w~ and the state with columns in atoms of 32
-    auto rows = [&](int at, int sl) { return smem_desc(base + at + sl * Ly::kTile, 16, 1024, kSw128); };
-    auto turned = [&](int sl) { return smem_desc(base + Ly::kY + sl * Ly::kTile, kBox, 1024, kSw128); };
-    const uint64_t dsop = smem_desc(base + Ly::kSop, Ly::kSopAtom, 512, kSw64);
+    auto rows = [&](int at) { return Desc(smem_desc(base + at, 16, 1024, kSw128)); };
+    auto atoms = [&](int at, int atom) { return Desc(smem_desc(base + at, atom, 512, kSw64)); };
+    auto step = [](int kk) { return static_cast<uint32_t>((kk >> 2) * (kBox >> 4) + (kk & 3) * 2); };
     for (int c = 0; c < nc; ++c) {
-      const int sl = c & 1;
+      const int sl = c & 1, xs = c % Ly::kXSlots;
       const uint32_t ph = (c >> 1) & 1;
       if (!STATE) {
-        if (!held_wait(&bar[kXFull + sl], ph, abort_flag, p.timeouts) ||
+        const Desc x = rows(Ly::kX + xs * Ly::kTile), y = rows(Ly::kY + sl * Ly::kTile);
+        if (!held_wait(&bar[kXFull + xs], (c / Ly::kXSlots) & 1, abort_flag, p.timeouts) ||
             !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts))
           break;
         // rows behind the end have to be zero first
         if (size(c) < kC && !held_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
-        {
-          const uint64_t a = rows(Ly::kX, sl), bb = rows(Ly::kY, sl);
+        if (elect_one()) {
+          mma_ss<false>(tmem + Ly::cR, x, 0, y, 0, ID_R);
 #pragma unroll
-          for (int kk = 0; kk < DX / 16; ++kk) {
-            const uint64_t at = (kk >> 2) * (kBox >> 4) + (kk & 3) * 2;
-            mma_ss(tmem + kColR, a + at, bb + at, ID_R, kk > 0);
-          }
-          commit(&bar[kRFull]);
+          for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(tmem + Ly::cR, x, step(kk), y, step(kk), ID_R);
+          mma_commit(&bar[kRFull]);
         }
+        __syncwarp();
         if (!held_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts) ||
             (c > 0 && !held_wait(&bar[kOFree], (c - 1) & 1, abort_flag, p.timeouts)))
           break;
         tc_fence_after();
-        {
-          const uint64_t a = rows(Ly::kX, sl);
+        const Desc sop = atoms(Ly::kSop, Ly::kSopAtom);
+        if (elect_one()) {
+          mma_ss<false>(tmem + Ly::cO1, x, 0, sop, 0, ID_O1);
 #pragma unroll
-          for (int kk = 0; kk < DX / 16; ++kk)
-            mma_ss(tmem + kColO1, a + (kk >> 2) * (kBox >> 4) + (kk & 3) * 2, dsop + kk * 64, ID_O1, kk > 0);
-          commit(&bar[kXEmpty + sl]);
+          for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(tmem + Ly::cO1, x, step(kk), sop, kk * 64, ID_O1);
+          mma_commit(&bar[kXEmpty + xs]);
         }
+        __syncwarp();
       } else if (c > 1 && !held_wait(&bar[kSReady + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
         break;  // dS of two chunks ago has been read
       }
       if (!held_wait(&bar[kWReady + (STATE ? sl : 0)], STATE ? ph : c & 1, abort_flag, p.timeouts)) break;
       if (STATE && !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) break;
       tc_fence_after();
-      if (keep || c + 1 < nc) {
-        const uint64_t a = turned(sl);
-        const uint64_t bb = smem_desc(base + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kWBox, 512, kSw64);
-        const uint32_t d = tmem + (STATE && sl ? kColD2 : kColD);
+      const Desc yt(smem_desc(base + Ly::kY + sl * Ly::kTile, kBox, 1024, kSw128));
+      const Desc wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
+      const uint32_t d = tmem + (STATE && sl ? Ly::cD2 : Ly::cD);
+      if (elect_one()) {
+        if (keep || c + 1 < nc) {
+          mma_ss<false>(d, yt, 0, wt, 0, ID_D);
 #pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk) mma_ss(d, a + kk * 128, bb + kk * 64, ID_D, kk > 0);
+          for (int kk = 1; kk < kC / 16; ++kk) mma_ss<true>(d, yt, kk * 128, wt, kk * 64, ID_D);
+        }
+        mma_commit(&bar[kDFull + sl]);
+        mma_commit(&bar[kYEmpty + sl]);
+        if (STATE) mma_commit(&bar[kWEmpty + sl]);
       }
-      commit(&bar[kDFull + sl]);
-      commit(&bar[kYEmpty + sl]);
+      __syncwarp();
       if (!STATE) {
         if (!held_wait(&bar[kPReady], c & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
-        const uint64_t bb = smem_desc(base + Ly::kW + sl * kWBox, kWBox, 512, kSw64);
+        const Desc w = atoms(Ly::kW + sl * Ly::kWTile, kAtom);
+        if (elect_one()) {
+          mma_ts<false>(tmem + Ly::cO2, tmem + Ly::cR, w, 0, ID_O2);
 #pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk)
-          mma_ts(tmem + kColO2, tmem + kColP + 8 * kk, bb + kk * 64, ID_O2, kk > 0);
-        commit(&bar[kOFull]);
+          for (int kk = 1; kk < kC / 16; ++kk)
+            mma_ts<true>(tmem + Ly::cO2, tmem + Ly::cR + 32 * (kk >> 1) + 8 * (kk & 1), w, kk * 64, ID_O2);
+          mma_commit(&bar[kOFull]);
+          mma_commit(&bar[kWEmpty + sl]);
+        }
+        __syncwarp();
       }
-      commit(&bar[kWEmpty + sl]);
     }
     // every MMA issued has completed before TMEM is released
-    commit(&bar[kDrain]);
-    mbar_wait_drain(&bar[kDrain], 0);
+    if (elect_one()) {
+      mma_commit(&bar[kDrain]);
+      mbar_wait_drain(&bar[kDrain], 0);
+    }
     __syncwarp();
   } else if (warp >= kWarpW) {
     const int t = tid - 32 * kWarpW;
@@ -353,33 +386,30 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
             (nv < kC && !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) ||
             (before >= 0 && !held_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
           break;
-        uint8_t *wrow = sm + Ly::kW + sl * kWBox;
+        uint8_t *wrow = sm + Ly::kW + sl * Ly::kWTile;
         uint8_t *wt = sm + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0);
         if (t < nv) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(wrow + sw64_off(t, 16 * q));
+#pragma unroll 2
+          for (int q = 0; q < SW / 8; ++q) {
+            const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
+            const uint4 x = *reinterpret_cast<const uint4 *>(wrow + at);
             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
             uint32_t s[4][NS];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              split2<NS>(f * __uint_as_float(u[k] << 16), f * __uint_as_float(u[k] & 0xffff0000u), s[k]);
+              split2<NS>(mul2(dup2(f), pack2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u))), s[k]);
 #pragma unroll
             for (int j = 0; j < NS; ++j)
-              *reinterpret_cast<uint4 *>(wt + j * kWBox + sw64_off(t, 16 * q)) =
-                  make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
+              *reinterpret_cast<uint4 *>(wt + j * Ly::kWTile + at) = make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
           }
         } else {
           const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            *reinterpret_cast<uint4 *>(wrow + sw64_off(t, 16 * q)) = z;
-#pragma unroll
-            for (int j = 0; j < NS; ++j) *reinterpret_cast<uint4 *>(wt + j * kWBox + sw64_off(t, 16 * q)) = z;
+          for (int q = 0; q < SW / 8; ++q) {
+            const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
+            *reinterpret_cast<uint4 *>(wrow + at) = z;
+            for (int j = 0; j < NS; ++j) *reinterpret_cast<uint4 *>(wt + j * Ly::kWTile + at) = z;
           }
-#pragma unroll
           for (int i = 0; i < DX / 64; ++i)
-#pragma unroll
             for (int q = 0; q < 8; ++q)
               *reinterpret_cast<uint4 *>(sm + Ly::kY + sl * Ly::kTile + i * kBox + sw128_off(t, 16 * q)) = z;
         }
@@ -395,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     const bool mine = DX == 128 || lane < 16;
     const int64_t size_of = static_cast<int64_t>(DX) * r.Dw;
     float *rec = r.rec + bh * (p.parts - 1) * size_of;
-    float S[32];
+    f2 S[SW / 2];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) S[e] = 0.f;
+    for (int e = 0; e < SW / 2; ++e) S[e] = dup2(0.f);
     if (!STATE) {
       const int here = ret_before(part * p.cpp, n, tokens, kC, r.reverse);
       if (r.start) {
@@ -405,18 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         const float *from = r.start + bh * size_of + static_cast<int64_t>(d) * r.start_rs +
                             static_cast<int64_t>(e0) * r.start_cs;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[e] = f * from[static_cast<int64_t>(e) * r.start_cs];
+        for (int e = 0; e < SW / 2; ++e)
+          S[e] = pack2(f * from[static_cast<int64_t>(2 * e) * r.start_cs], f * from[static_cast<int64_t>(2 * e + 1) * r.start_cs]);
       }
       for (int j = 0; j < part; ++j) {
-        const float f = exp2f(lg * static_cast<float>(here - ret_before((j + 1) * p.cpp, n, tokens, kC, r.reverse)));
+        const f2 f = dup2(exp2f(lg * static_cast<float>(here - ret_before((j + 1) * p.cpp, n, tokens, kC, r.reverse))));
         const float4 *from = reinterpret_cast<const float4 *>(rec + j * size_of + d * r.Dw + e0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < SW / 4; ++e) {
           const float4 v = from[e];
-          S[4 * e] = fmaf(f, v.x, S[4 * e]);
-          S[4 * e + 1] = fmaf(f, v.y, S[4 * e + 1]);
-          S[4 * e + 2] = fmaf(f, v.z, S[4 * e + 2]);
-          S[4 * e + 3] = fmaf(f, v.w, S[4 * e + 3]);
+          S[2 * e] = fma2(f, pack2(v.x, v.y), S[2 * e]);
+          S[2 * e + 1] = fma2(f, pack2(v.z, v.w), S[2 * e + 1]);
         }
       }
     }
@@ -424,22 +453,26 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     for (int c = 0; c <= nc; ++c) {
       if (c > 0 && (c < nc || keep)) {  // S <- g^n S + dS of chunk c - 1
         const int l = c - 1;
-        const float g = exp2f(lg * static_cast<float>(size(l)));
+        const f2 g = dup2(exp2f(lg * static_cast<float>(size(l))));
         if (!held_wait(&bar[kDFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = tmem_addr(tmem, 32 * qd, STATE && (l & 1) ? kColD2 : kColD);
+        const uint32_t at = tmem_addr(tmem, 32 * qd, STATE && (l & 1) ? Ly::cD2 : Ly::cD);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < SW / 16; ++j) {
           float x[NS][16];
 #pragma unroll
-          for (int k = 0; k < NS; ++k) tmem_ld16(at + 32 * k + 16 * j, x[k]);
+          for (int k = 0; k < NS; ++k) tmem_ld16(at + SW * k + 16 * j, x[k]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[16 * j + e] = fmaf(g, S[16 * j + e], NS == 3 ? x[0][e] + (x[1][e] + x[NS - 1][e]) : x[0][e] + x[1][e]);
+          for (int e = 0; e < 8; ++e) {
+            f2 v = pack2(x[NS - 1][2 * e], x[NS - 1][2 * e + 1]);
+#pragma unroll
+            for (int k = NS - 2; k >= 0; --k) v = add2(v, pack2(x[k][2 * e], x[k][2 * e + 1]));
+            S[8 * j + e] = fma2(g, S[8 * j + e], v);
+          }
         }
         tc_fence_before();
       }
@@ -449,14 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       } else if (c < nc) {
         if (mine) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < SW / 8; ++q) {
             uint32_t s[4][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) split2<2>(S[8 * q + 2 * k], S[8 * q + 2 * k + 1], s[k]);
+            for (int k = 0; k < 4; ++k) split2<2>(S[4 * q + k], s[k]);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<uint4 *>(sm + Ly::kSop + j * Ly::kSopAtom + sw64_off(d, 16 * q)) =
-                  make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
+              *reinterpret_cast<uint4 *>(sm + Ly::kSop + (j * (SW / 32) + (q >> 2)) * Ly::kSopAtom +
+                                         sw64_off(d, 16 * (q & 3))) = make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
           }
         }
         fence_async_smem();
@@ -466,53 +499,48 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     }
     if (keep && ok && mine) {
       float4 *to = reinterpret_cast<float4 *>((STATE ? rec + part * size_of : r.end + bh * size_of) + d * r.Dw + e0);
-      const float f = STATE ? 1.f : r.end_scale;
+      const f2 f = dup2(STATE ? 1.f : r.end_scale);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        to[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
+      for (int e = 0; e < SW / 4; ++e) {
+        const float2 lo = unpack2(mul2(f, S[2 * e])), hi = unpack2(mul2(f, S[2 * e + 1]));
+        to[e] = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
   } else if (!STATE) {
     // P: rows of quadrant qd, blocks of 32 columns h2 and h2 + 2; output columns
-    // [16 h2, + 16)
+    // [SW / 2 h2, + SW / 2)
     const int qd = warp & 3, h2 = warp >> 2, t = 32 * qd + lane;
     const bool rev = r.reverse;
     const uint32_t quad = tmem_addr(tmem, 32 * qd, 0);
     uint8_t *out = static_cast<uint8_t *>(r.o);
     const int wide = r.o_f32 ? 4 : 2;  // bytes of an output
-    const int64_t unit = b * r.os.b + h * r.os.h + e0 + 16 * h2;
-    // blocks without a weight are zero once and for all
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int g = h2 + 2 * k;
-      if (rev ? g < qd : g > qd) {
-        uint32_t z[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) z[e] = 0u;
-        tmem_st16u(quad + kColP + 16 * g, z);
-      }
-    }
-    tmem_wait_st();
+    const int64_t unit = b * r.os.b + h * r.os.h + e0 + SW / 2 * h2;
     for (int c = 0; c < nc; ++c) {
       if (!held_wait(&bar[kRFull], c & 1, abort_flag, p.timeouts)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int g = h2; g < 4; g += 2) {
         const int away = rev ? g - qd : qd - g;
-        if (away < 0) continue;
-        const float4 *w4 = reinterpret_cast<const float4 *>(tab + (32 * away + lane) * Ly::kLdT);
-        float a[32];
         uint32_t pk[16];
-        tmem_ld32(quad + kColR + 32 * g, a);
-        tmem_wait_ld();
+        if (away >= 0) {
+          const f2 far = dup2(away > 1 ? exp2f(lg * static_cast<float>(32 * (away - 1))) : 1.f);
+          const float4 *w4 = reinterpret_cast<const float4 *>(tab + ((away > 0 ? 32 : 0) + lane) * Ly::kLdT);
+          float a[32];
+          tmem_ld32(quad + Ly::cR + 32 * g, a);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 w = w4[e];
-          const float2 lo = unpack2(mul2(pack2(a[4 * e], a[4 * e + 1]), pack2(w.x, w.y)));
-          const float2 hi = unpack2(mul2(pack2(a[4 * e + 2], a[4 * e + 3]), pack2(w.z, w.w)));
-          pk[2 * e] = pack_bf16x2(lo.x, lo.y);
-          pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
+          for (int e = 0; e < 8; ++e) {
+            const float4 w = w4[e];
+            const float2 lo = unpack2(mul2(mul2(far, pack2(w.x, w.y)), pack2(a[4 * e], a[4 * e + 1])));
+            const float2 hi = unpack2(mul2(mul2(far, pack2(w.z, w.w)), pack2(a[4 * e + 2], a[4 * e + 3])));
+            pk[2 * e] = pack_bf16x2(lo.x, lo.y);
+            pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
         }
-        tmem_st16u(quad + kColP + 16 * g, pk);
+        tmem_st16u(quad + Ly::cR + 32 * g, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -523,35 +551,41 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
       if (!held_wait(&bar[kOFull], c & 1, abort_flag, p.timeouts)) break;
       tc_fence_after();
-      float hi[16], lo[16], v[16];
-      tmem_ld16(quad + kColO1 + 16 * h2, hi);
-      tmem_ld16(quad + kColO1 + 32 + 16 * h2, lo);
-      tmem_ld16(quad + kColO2 + 16 * h2, v);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(&bar[kOFree]);
-      if (t < nv) {
+      uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
-        uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
-        if (r.o_f32) {
-          float4 *to = reinterpret_cast<float4 *>(at);
+      for (int j = 0; j < SW / 32; ++j) {
+        float hi[16], lo[16], v[16];
+        const uint32_t col = SW / 2 * h2 + 16 * j;
+        tmem_ld16(quad + Ly::cO1 + col, hi);
+        tmem_ld16(quad + Ly::cO1 + SW + col, lo);
+        tmem_ld16(quad + Ly::cO2 + col, v);
+        tmem_wait_ld();
+        if (j == SW / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed(&bar[kOFree]);
+        }
+        if (t < nv) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        } else {
-          uint4 *to = reinterpret_cast<uint4 *>(at);
+          for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
+          if (r.o_f32) {
+            float4 *to = reinterpret_cast<float4 *>(at + 64 * j);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                               pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+            for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else {
+            uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                 pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          }
         }
       }
     }
     if (p.a.fill && last_part)
       for (int i = tokens + t; i < p.a.L; i += kC) {
         uint4 *to = reinterpret_cast<uint4 *>(out + (unit + i * r.os.t) * wide);
-        for (int e = 0; e < wide; ++e) to[e] = make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < wide * SW / 32; ++e) to[e] = make_uint4(0, 0, 0, 0);
       }
   }
   __syncwarp();
@@ -561,10 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-template <int DX, int NS, bool STATE>
+template <int DX, int SW, int NS, bool STATE>
 cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
-  auto k = retention_tc_kernel<DX, NS, STATE>;
-  const int bytes = Lay<DX, STATE>::kAlloc;
+  auto k = retention_tc_kernel<DX, SW, NS, STATE>;
+  const int bytes = Lay<DX, SW, NS, STATE>::kAlloc;
   const cudaError_t e = allow_smem(k, bytes);
   if (e != cudaSuccess) return e;
   const int np = STATE ? p.parts - 1 : p.parts;
@@ -572,13 +606,27 @@ cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int DX>
+template <int DX, int SW>
 cudaError_t go_all(const TcParams &p, bool exact, int64_t units, cudaStream_t s) {
   if (p.parts > 1) {
-    const cudaError_t e = exact ? go<DX, 3, true>(p, units, s) : go<DX, 2, true>(p, units, s);
+    const cudaError_t e = exact ? go<DX, SW, 3, true>(p, units, s) : go<DX, SW, 1, true>(p, units, s);
     if (e != cudaSuccess) return e;
   }
-  return exact ? go<DX, 3, false>(p, units, s) : go<DX, 2, false>(p, units, s);
+  return exact ? go<DX, SW, 3, false>(p, units, s) : go<DX, SW, 1, false>(p, units, s);
+}
+
+int64_t columns(const RetArgs &a) {
+  int64_t n = 0;
+  for (int i = 0; i < a.roles; ++i) n += static_cast<int64_t>(a.B) * a.H * a.role[i].Dw;
+  return n;
+}
+
+// Slices of 64 columns compute the raw weights half as often as slices of 32,
+// but are half as many.
+int slice_width(const RetArgs &a) {
+  for (int i = 0; i < a.roles; ++i)
+    if (a.role[i].Dw % 64 != 0) return 32;
+  return columns(a) / 64 >= kSMs - 24 ? 64 : 32;
 }
 
 }  // namespace
@@ -586,13 +634,12 @@ cudaError_t go_all(const TcParams &p, bool exact, int64_t units, cudaStream_t s)
 bool ret_tc_supported(const RetArgs &a, Dtype dt) {
   if (dt != kBF16) return false;
   for (int i = 0; i < a.roles; ++i)
-    if ((a.role[i].Dx != 64 && a.role[i].Dx != 128) || a.role[i].Dw % kSW != 0) return false;
+    if ((a.role[i].Dx != 64 && a.role[i].Dx != 128) || a.role[i].Dw % 32 != 0) return false;
   return true;
 }
 
 int ret_parts_tc(const RetArgs &a) {
-  int64_t units = 0;
-  for (int i = 0; i < a.roles; ++i) units += static_cast<int64_t>(a.B) * a.H * (a.role[i].Dw / kSW);
+  const int64_t units = columns(a) / slice_width(a);
   const int chunks = (a.L + kC - 1) / kC;
   // Parts cost a pass over y and w for their records (about half of a chunk's
   // time) and a launch (about four chunks' time).
@@ -604,7 +651,7 @@ int ret_parts_tc(const RetArgs &a) {
 }
 
 cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
-  const int chunks = (a.L + kC - 1) / kC;
+  const int chunks = (a.L + kC - 1) / kC, SW = slice_width(a);
   unsigned int *timeouts = wait_timeout_counter();
   if (!timeouts) return cudaErrorNotSupported;
   // one launch for the roles of each number of features
@@ -624,16 +671,18 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
         return make_tmap_heads(&m.m[i], base, width, a.H / group, a.L, a.B, s.h, s.t, s.b, box, kC, m.at[i]);
       };
       if (!encode(0, r.x, DX, r.xg, r.xs, 64) || !encode(1, r.y, DX, r.yg, r.ys, 64) ||
-          !encode(2, r.w, r.Dw, r.wg, r.ws, kSW))
+          !encode(2, r.w, r.Dw, r.wg, r.ws, 32))
         return cudaErrorNotSupported;
       p.a.role[p.a.roles++] = r;
-      if (r.Dw / kSW > p.slices) p.slices = r.Dw / kSW;
+      if (r.Dw / SW > p.slices) p.slices = r.Dw / SW;
       exact |= r.end != nullptr;
     }
     if (!p.a.roles) continue;
     const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
     if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
-    const cudaError_t e = DX == 64 ? go_all<64>(p, exact, units, s) : go_all<128>(p, exact, units, s);
+    cudaError_t e;
+    if (SW == 64) e = DX == 64 ? go_all<64, 64>(p, exact, units, s) : go_all<128, 64>(p, exact, units, s);
+    else e = DX == 64 ? go_all<64, 32>(p, exact, units, s) : go_all<128, 32>(p, exact, units, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
