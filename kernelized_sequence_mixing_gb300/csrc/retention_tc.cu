@@ -44,22 +44,24 @@ using namespace tc;
 constexpr int kC = 128;  // tokens per chunk
 constexpr int kThreads = 576;
 constexpr int kWarpS = 8, kWarpW = 12, kWarpTma = 16, kWarpMma = 17;
+constexpr int kAhead = 2;        // chunks between a tile's prefetch into L2 and its load
 constexpr int kBox = kC * 128;  // 128 tokens x 64 features, 128-byte swizzle
 constexpr int kAtom = kC * 64;  // 128 tokens x 32 columns, 64-byte swizzle
 
-// Shared memory, from a 1024-byte aligned base: slots of x, two slots each of y
-// and w,
+// Shared memory, from a 1024-byte aligned base: slots of x and y, slots of w,
 // w~ (one buffer; two in the pass that only sums states), the state's bf16
 // values, the weights of a chunk's blocks, barriers.
 template <int DX, int SW, int NS, bool STATE>
 struct Lay {
   static constexpr int kTile = DX / 64 * kBox;
   static constexpr int kWTile = SW / 32 * kAtom;
-  static constexpr int kX = 0;
-  static constexpr int kXSlots = SW == 64 && NS == 3 ? 1 : 2;  // what fits
-  static constexpr int kY = STATE ? 0 : kXSlots * kTile;
-  static constexpr int kW = kY + 2 * kTile;
-  static constexpr int kWt = kW + 2 * kWTile;
+  // a slot: x, then y
+  static constexpr int kYAt = STATE ? 0 : kTile, kSlot = kYAt + kTile;
+  // loads take 2000 cycles and more from issue to landing when all SMs stream, so
+  // as many slots as fit
+  static constexpr int kSlots = STATE ? 4 : 2, kWSlots = STATE || SW == 32 ? 4 : 2;
+  static constexpr int kW = kSlots * kSlot;
+  static constexpr int kWt = kW + kWSlots * kWTile;
   static constexpr int kWtBuf = NS * kWTile;
   static constexpr int kSop = kWt + (STATE ? 2 : 1) * kWtBuf;
   static constexpr int kSopAtom = DX * 64;
@@ -68,35 +70,33 @@ struct Lay {
   static constexpr int kLdT = 36;
   static constexpr int kTab = kSop + (STATE ? 0 : 2 * (SW / 32) * kSopAtom);
   static constexpr int kBar = kTab + (STATE ? 0 : 2 * 32 * kLdT * 4);
-  static constexpr int kNumBars = 24;
+  static constexpr int kNumBars = 32;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  // Tensor memory columns: raw weights, in each block of 32 columns then P as
-  // bf16 pairs in the first 16; O1 with both values of the state side by side;
-  // O2; dS (twice in the pass that only sums states).
-  static constexpr uint32_t cR = 0, cO1 = 128, cO2 = cO1 + 2 * SW;
+  // Tensor memory columns: two buffers of raw weights, in each block of 32
+  // columns then P as bf16 pairs in the first 16; O1 with both values of the state
+  // side by side; O2; dS (twice in the pass that only sums states).
+  static constexpr uint32_t cR = 0, cO1 = 256, cO2 = cO1 + 2 * SW;
   static constexpr uint32_t cD = STATE ? 0 : cO2 + SW, cD2 = NS * SW;
   static_assert(cD + (STATE ? 2 : 1) * NS * SW <= 512, "tensor memory");
 };
 
+// Where a barrier is one and not a pair, each of its phases is seen by every
+// waiter before the next can end.
 enum Bar : int {
-  kXFull = 0,    // [2] tile landed
-  kXEmpty = 2,   // [2] slot free (MMA commit)
-  kYFull = 4,    // [2]
-  kYEmpty = 6,   // [2]
-  kWFull = 8,    // [2]
-  kWEmpty = 10,  // [2]
-  kRFull = 12,   // raw weights computed (and P of the chunk before read)
-  kPReady = 13,  // P written
-  kOFull = 14,   // O1, O2 complete
-  kOFree = 15,   // O1, O2 read
-  kDFull = 16,   // [2] dS computed
-  // [2], of which the main pass uses one: there each chunk's hand-offs wait for
-  // the ones before; the pass that only sums states works two chunks at a time
-  kSReady = 18,  // the state's bf16 values written (dS of the chunk before read)
-  kWReady = 20,  // w~ written
-  kDrain = 22,
+  kXYFull = 0,    // [4] tiles of x and y landed
+  kXYEmpty = 4,   // [4] slot free (MMA commit)
+  kWFull = 8,     // [4]
+  kWEmpty = 12,   // [4]
+  kRFull = 16,    // [2] raw weights computed
+  kDFull = 18,    // [2] dS computed
+  kWReady = 20,   // [2] w~ written (main pass: one)
+  kDRead = 22,    // [2] the pass that only sums states: dS read
+  kOGo = 24,      // the state's bf16 values written, outputs of the chunk before read
+  kPReady = 25,   // P written
+  kOFull = 26,    // O1, O2 complete
+  kDrain = 27,
 };
 
 struct TcRole {
@@ -110,10 +110,11 @@ struct TcParams {
   unsigned int *timeouts;
 };
 
-// warp_wait of tc_common.cuh for a kernel of many waiting warps with much code:
-// the hardware holds the warp until the phase ends or the hint (nanoseconds) runs
-// out, so that waiting warps leave the issue slots to the others, and what follows
-// a hint that ran out is one function for all waits.
+// warp_wait of tc_common.cuh for a kernel of many waiting warps with much code: a
+// plain try first (15 cycles where the phase is over, 50 with a hint), then the
+// hardware holds the warp until the phase ends or the hint (nanoseconds) runs out,
+// so that waiting warps leave the issue slots to the others; one function for all
+// waits that take longer.
 __device__ __forceinline__ bool held(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -138,7 +139,7 @@ __device__ __noinline__ bool held_longer(uint32_t bar, uint32_t parity, volatile
 }
 __device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *timeouts) {
   const uint32_t at = smem_u32(bar);
-  bool ok = held(at, parity);
+  bool ok = mbar_try_wait(bar, parity);
   if (!ok) ok = held_longer(at, parity, abort, timeouts);
   return __all_sync(0xffffffffu, ok);
 }
@@ -231,21 +232,16 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       tab[(i >> 5) * Ly::kLdT + e] = gap >= 0 ? exp2f(lg * static_cast<float>(gap)) : 0.f;
     }
   if (tid == 32 * kWarpTma) {
+    for (int s = 0; s < 16; ++s) mbar_init(&bar[kXYFull + s], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar[kXFull + s], 1);
-      mbar_init(&bar[kXEmpty + s], 1);
-      mbar_init(&bar[kYFull + s], 1);
-      mbar_init(&bar[kYEmpty + s], 1);
-      mbar_init(&bar[kWFull + s], 1);
-      mbar_init(&bar[kWEmpty + s], 1);
+      mbar_init(&bar[kRFull + s], 1);
       mbar_init(&bar[kDFull + s], 1);
-      mbar_init(&bar[kSReady + s], 4);
-      mbar_init(&bar[kWReady + s], 4);
+      mbar_init(&bar[kWReady + s], STATE ? 12 : 4);
+      mbar_init(&bar[kDRead + s], 4);
     }
-    mbar_init(&bar[kRFull], 1);
+    mbar_init(&bar[kOGo], 12);
     mbar_init(&bar[kPReady], 8);
     mbar_init(&bar[kOFull], 1);
-    mbar_init(&bar[kOFree], 8);
     mbar_init(&bar[kDrain], 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -257,38 +253,55 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   const uint32_t tmem = *tmem_slot;
 
   if (warp == kWarpTma) {
-    if (lane < 3 && !(STATE && lane == 0)) {
-      const CUtensorMap *m = &map.m[lane];
-      const uint8_t *at = map.at[lane];
-      prefetch_tmap(m);
-      uint64_t *fullb = &bar[lane == 0 ? kXFull : (lane == 1 ? kYFull : kWFull)];
-      uint64_t *emptyb = &bar[lane == 0 ? kXEmpty : (lane == 1 ? kYEmpty : kWEmpty)];
-      const int head = h / (lane == 0 ? r.xg : (lane == 1 ? r.yg : r.wg));
+    if (lane < 2) {  // lane 0: x and y, lane 1: w
+      auto map_of = [&](int i) { return &map.m[i]; };
+      prefetch_tmap(map_of(lane == 0 ? 1 : 2));
+      if (lane == 0 && !STATE) prefetch_tmap(map_of(0));
+      uint64_t *fullb = &bar[lane == 0 ? kXYFull : kWFull], *emptyb = &bar[lane == 0 ? kXYEmpty : kWEmpty];
+      const int hx = h / r.xg, hy = h / r.yg, hw = h / r.wg;
+      const int sharers = r.Dw / SW;
+      // f(map, column, outer coordinates) for each box of a tile of tensor i
+      auto boxes = [&](int i, int head, int t, auto &&f) {
+        const uint8_t *at = map.at[i];
+        auto place = [&](int j) { return at[0] == j ? head : (at[1] == j ? t : b); };
+        const int y = place(0), z = place(1), w = place(2);
+#pragma unroll 1
+        for (int j = 0; j < (i == 2 ? SW / 32 : DX / 64); ++j) f(j, i == 2 ? e0 + 32 * j : 64 * j, y, z, w);
+      };
+      const int slots = lane == 0 ? Ly::kSlots : Ly::kWSlots;
       int issued = 0;
       for (int c = 0; c < nc; ++c) {
-        const int sl = lane == 0 ? c % Ly::kXSlots : c & 1, turn = lane == 0 ? c / Ly::kXSlots : c >> 1;
-        if (!mbar_wait(&emptyb[sl], (turn & 1) ^ 1, abort_flag, p.timeouts)) break;
-        const int t0 = first(c);
-        auto place = [&](int i) { return at[0] == i ? head : (at[1] == i ? t0 : b); };
-        const int y = place(0), z = place(1), w = place(2);
-        if (lane == 2) {
-          mbar_arrive_expect_tx(&fullb[sl], Ly::kWTile);
-#pragma unroll
-          for (int i = 0; i < SW / 32; ++i)
-            tma_load_4d(sm + Ly::kW + sl * Ly::kWTile + i * kAtom, m, e0 + 32 * i, y, z, w, &fullb[sl]);
+        const int sl = c % slots;
+        if (!mbar_wait(&emptyb[sl], ((c / slots) & 1) ^ 1, abort_flag, p.timeouts)) break;
+        // The slots hold less than the memory's latency: later tiles come into L2
+        // ahead, the boxes of x and y shared out among the slices that read them.
+        const int t0 = first(c), tp = first(c + kAhead);
+        const bool ahead = c + kAhead < nc;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&fullb[sl], Ly::kSlot);
+          for (int i = STATE ? 1 : 0; i < 2; ++i) {
+            uint8_t *dst = sm + sl * Ly::kSlot + (i == 0 ? 0 : Ly::kYAt);
+            boxes(i, i == 0 ? hx : hy, t0, [&](int j, int x, int y, int z, int w) {
+              tma_load_4d(dst + j * kBox, map_of(i), x, y, z, w, &fullb[sl]);
+            });
+          }
+          for (int i = STATE ? 1 : 0; ahead && i < 2; ++i)
+            boxes(i, i == 0 ? hx : hy, tp, [&](int j, int x, int y, int z, int w) {
+              if ((i * (DX / 64) + j) % sharers == slice) tma_prefetch_4d(map_of(i), x, y, z, w);
+            });
         } else {
-          uint8_t *dst = sm + (lane == 0 ? Ly::kX : Ly::kY) + sl * Ly::kTile;
-          mbar_arrive_expect_tx(&fullb[sl], Ly::kTile);
-#pragma unroll
-          for (int i = 0; i < DX / 64; ++i) tma_load_4d(dst + i * kBox, m, 64 * i, y, z, w, &fullb[sl]);
+          mbar_arrive_expect_tx(&fullb[sl], Ly::kWTile);
+          boxes(2, hw, t0, [&](int j, int x, int y, int z, int w) {
+            tma_load_4d(sm + Ly::kW + sl * Ly::kWTile + j * kAtom, map_of(2), x, y, z, w, &fullb[sl]);
+          });
+          if (ahead)
+            boxes(2, hw, tp, [&](int, int x, int y, int z, int w) { tma_prefetch_4d(map_of(2), x, y, z, w); });
         }
         issued = c + 1;
       }
       if (*abort_flag)  // let every issued copy land before the CTA exits
-        for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) {
-          const int slots = lane == 0 ? Ly::kXSlots : 2;
+        for (int c = issued > slots ? issued - slots : 0; c < issued; ++c)
           mbar_wait_drain(&fullb[c % slots], (c / slots) & 1);
-        }
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
@@ -302,43 +315,55 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     auto rows = [&](int at) { return Desc(smem_desc(base + at, 16, 1024, kSw128)); };
     auto atoms = [&](int at, int atom) { return Desc(smem_desc(base + at, atom, 512, kSw64)); };
     auto step = [](int kk) { return static_cast<uint32_t>((kk >> 2) * (kBox >> 4) + (kk & 3) * 2); };
-    for (int c = 0; c < nc; ++c) {
-      const int sl = c & 1, xs = c % Ly::kXSlots;
+    auto slot = [](int c) { return c % Ly::kSlots; };
+    auto landed = [&](int c) { return held_wait(&bar[kXYFull + slot(c)], (c / Ly::kSlots) & 1, abort_flag, p.timeouts); };
+    auto tiles = [&](int c) {  // x and y of chunk c have landed
+      return landed(c) &&
+             // rows behind the end have to be zero first
+             (size(c) == kC || held_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts));
+    };
+    auto tiles_state = [&](int c) {  // y has landed, dS of two chunks ago has been read
+      return landed(c) && (c < 2 || held_wait(&bar[kDRead + (c & 1)], ((c - 2) >> 1) & 1, abort_flag, p.timeouts));
+    };
+    auto weigh = [&](int c) {  // R of chunk c
+      const Desc x = rows(slot(c) * Ly::kSlot), y = rows(slot(c) * Ly::kSlot + Ly::kYAt);
+      const uint32_t d = tmem + Ly::cR + 128 * (c & 1);
+      if (elect_one()) {
+        mma_ss<false>(d, x, 0, y, 0, ID_R);
+#pragma unroll
+        for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(d, x, step(kk), y, step(kk), ID_R);
+        mma_commit(&bar[kRFull + (c & 1)]);
+      }
+      __syncwarp();
+    };
+    bool ok = true;
+    if (!STATE && nc > 0) {
+      ok = tiles(0);
+      tc_fence_after();
+      if (ok) weigh(0);
+    }
+    // Per chunk O1, dS, R of the next chunk and O2, so that each group's consumers
+    // work behind other groups: P behind O2 and O1 and dS of the next chunk, the
+    // state behind R and O2, the outputs' read (before the next O1) behind nothing.
+    for (int c = 0; ok && c < nc; ++c) {
+      const int sl = c & 1;
       const uint32_t ph = (c >> 1) & 1;
       if (!STATE) {
-        const Desc x = rows(Ly::kX + xs * Ly::kTile), y = rows(Ly::kY + sl * Ly::kTile);
-        if (!held_wait(&bar[kXFull + xs], (c / Ly::kXSlots) & 1, abort_flag, p.timeouts) ||
-            !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts))
-          break;
-        // rows behind the end have to be zero first
-        if (size(c) < kC && !held_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts)) break;
+        if (!held_wait(&bar[kOGo], c & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
-        if (elect_one()) {
-          mma_ss<false>(tmem + Ly::cR, x, 0, y, 0, ID_R);
-#pragma unroll
-          for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(tmem + Ly::cR, x, step(kk), y, step(kk), ID_R);
-          mma_commit(&bar[kRFull]);
-        }
-        __syncwarp();
-        if (!held_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts) ||
-            (c > 0 && !held_wait(&bar[kOFree], (c - 1) & 1, abort_flag, p.timeouts)))
-          break;
-        tc_fence_after();
-        const Desc sop = atoms(Ly::kSop, Ly::kSopAtom);
+        const Desc x = rows(slot(c) * Ly::kSlot), sop = atoms(Ly::kSop, Ly::kSopAtom);
         if (elect_one()) {
           mma_ss<false>(tmem + Ly::cO1, x, 0, sop, 0, ID_O1);
 #pragma unroll
           for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(tmem + Ly::cO1, x, step(kk), sop, kk * 64, ID_O1);
-          mma_commit(&bar[kXEmpty + xs]);
         }
         __syncwarp();
-      } else if (c > 1 && !held_wait(&bar[kSReady + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
-        break;  // dS of two chunks ago has been read
+      } else if (!tiles_state(c)) {
+        break;
       }
       if (!held_wait(&bar[kWReady + (STATE ? sl : 0)], STATE ? ph : c & 1, abort_flag, p.timeouts)) break;
-      if (STATE && !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) break;
       tc_fence_after();
-      const Desc yt(smem_desc(base + Ly::kY + sl * Ly::kTile, kBox, 1024, kSw128));
+      const Desc yt(smem_desc(base + slot(c) * Ly::kSlot + Ly::kYAt, kBox, 1024, kSw128));
       const Desc wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
       const uint32_t d = tmem + (STATE && sl ? Ly::cD2 : Ly::cD);
       if (elect_one()) {
@@ -348,21 +373,27 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           for (int kk = 1; kk < kC / 16; ++kk) mma_ss<true>(d, yt, kk * 128, wt, kk * 64, ID_D);
         }
         mma_commit(&bar[kDFull + sl]);
-        mma_commit(&bar[kYEmpty + sl]);
-        if (STATE) mma_commit(&bar[kWEmpty + sl]);
+        mma_commit(&bar[kXYEmpty + slot(c)]);
+        if (STATE) mma_commit(&bar[kWEmpty + c % Ly::kWSlots]);
       }
       __syncwarp();
       if (!STATE) {
+        if (c + 1 < nc) {
+          if (!tiles(c + 1)) break;
+          tc_fence_after();
+          weigh(c + 1);
+        }
         if (!held_wait(&bar[kPReady], c & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
-        const Desc w = atoms(Ly::kW + sl * Ly::kWTile, kAtom);
+        const Desc w = atoms(Ly::kW + c % Ly::kWSlots * Ly::kWTile, kAtom);
+        const uint32_t pr = tmem + Ly::cR + 128 * sl;
         if (elect_one()) {
-          mma_ts<false>(tmem + Ly::cO2, tmem + Ly::cR, w, 0, ID_O2);
+          mma_ts<false>(tmem + Ly::cO2, pr, w, 0, ID_O2);
 #pragma unroll
           for (int kk = 1; kk < kC / 16; ++kk)
-            mma_ts<true>(tmem + Ly::cO2, tmem + Ly::cR + 32 * (kk >> 1) + 8 * (kk & 1), w, kk * 64, ID_O2);
+            mma_ts<true>(tmem + Ly::cO2, pr + 32 * (kk >> 1) + 8 * (kk & 1), w, kk * 64, ID_O2);
           mma_commit(&bar[kOFull]);
-          mma_commit(&bar[kWEmpty + sl]);
+          mma_commit(&bar[kWEmpty + c % Ly::kWSlots]);
         }
         __syncwarp();
       }
@@ -373,50 +404,49 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       mbar_wait_drain(&bar[kDrain], 0);
     }
     __syncwarp();
-  } else if (warp >= kWarpW) {
-    const int t = tid - 32 * kWarpW;
+  } else if (warp >= kWarpW || (STATE && warp < kWarpS)) {
+    // a third of the columns each where the warps that weigh have nothing to do
+    const int t = tid & (kC - 1), group = STATE && warp >= kWarpW ? 2 : warp >> 2 & 1, groups = STATE ? 3 : 1;
     for (int c = 0; c < nc; ++c) {
-      {
-        const int sl = c & 1, nv = size(c);
-        const uint32_t ph = (c >> 1) & 1;
-        const float f = t < nv ? exp2f(lg * static_cast<float>(r.reverse ? t + 1 : nv - 1 - t)) : 0.f;
-        // the buffer is free once the sum over the chunk that used it is done
-        const int before = c - (STATE ? 2 : 1);
-        if (!held_wait(&bar[kWFull + sl], ph, abort_flag, p.timeouts) ||
-            (nv < kC && !held_wait(&bar[kYFull + sl], ph, abort_flag, p.timeouts)) ||
-            (before >= 0 && !held_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
-          break;
-        uint8_t *wrow = sm + Ly::kW + sl * Ly::kWTile;
-        uint8_t *wt = sm + Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0);
-        if (t < nv) {
+      const int ws = c % Ly::kWSlots, xs = c % Ly::kSlots, nv = size(c);
+      const float f = t < nv ? exp2f(lg * static_cast<float>(r.reverse ? t + 1 : nv - 1 - t)) : 0.f;
+      // the buffer is free once the sum over the chunk that used it is done
+      const int before = c - (STATE ? 2 : 1);
+      if (!held_wait(&bar[kWFull + ws], (c / Ly::kWSlots) & 1, abort_flag, p.timeouts) ||
+          (nv < kC && !held_wait(&bar[kXYFull + xs], (c / Ly::kSlots) & 1, abort_flag, p.timeouts)) ||
+          (before >= 0 && !held_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
+        break;
+      uint8_t *wrow = sm + Ly::kW + ws * Ly::kWTile;
+      uint8_t *wt = sm + Ly::kWt + (STATE ? (c & 1) * Ly::kWtBuf : 0);
+      if (t < nv) {
 #pragma unroll 2
-          for (int q = 0; q < SW / 8; ++q) {
-            const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
-            const uint4 x = *reinterpret_cast<const uint4 *>(wrow + at);
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            uint32_t s[4][NS];
+        for (int q = STATE ? group : 0; q < SW / 8; q += groups) {
+          const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
+          const uint4 x = *reinterpret_cast<const uint4 *>(wrow + at);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          uint32_t s[4][NS];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              split2<NS>(mul2(dup2(f), pack2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u))), s[k]);
+          for (int k = 0; k < 4; ++k)
+            split2<NS>(mul2(dup2(f), pack2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u))), s[k]);
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
-              *reinterpret_cast<uint4 *>(wt + j * Ly::kWTile + at) = make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
-          }
-        } else {
-          const uint4 z = make_uint4(0, 0, 0, 0);
-          for (int q = 0; q < SW / 8; ++q) {
-            const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
-            *reinterpret_cast<uint4 *>(wrow + at) = z;
-            for (int j = 0; j < NS; ++j) *reinterpret_cast<uint4 *>(wt + j * Ly::kWTile + at) = z;
-          }
-          for (int i = 0; i < DX / 64; ++i)
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<uint4 *>(sm + Ly::kY + sl * Ly::kTile + i * kBox + sw128_off(t, 16 * q)) = z;
+          for (int j = 0; j < NS; ++j)
+            *reinterpret_cast<uint4 *>(wt + j * Ly::kWTile + at) = make_uint4(s[0][j], s[1][j], s[2][j], s[3][j]);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kWReady + (STATE ? sl : 0)]);
+      } else {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int q = STATE ? group : 0; q < SW / 8; q += groups) {
+          const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
+          *reinterpret_cast<uint4 *>(wrow + at) = z;
+          for (int j = 0; j < NS; ++j) *reinterpret_cast<uint4 *>(wt + j * Ly::kWTile + at) = z;
+        }
+#pragma unroll 1
+        for (int q = STATE ? group : 0; q < DX / 8; q += groups)
+          *reinterpret_cast<uint4 *>(sm + xs * Ly::kSlot + Ly::kYAt + (q >> 3) * kBox + sw128_off(t, 16 * (q & 7))) = z;
       }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[kWReady + (STATE ? c & 1 : 0)]);
     }
   } else if (warp >= kWarpS) {
     // row d of the state: all 32 lanes of a quadrant, or (64 features) 16
@@ -478,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       }
       if (STATE) {
         __syncwarp();
-        if (c > 0 && c < nc && lane == 0) mbar_arrive(&bar[kSReady + ((c - 1) & 1)]);
+        if (c > 0 && c < nc && lane == 0) mbar_arrive(&bar[kDRead + ((c - 1) & 1)]);
       } else if (c < nc) {
         if (mine) {
 #pragma unroll
@@ -494,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kSReady]);
+        if (lane == 0) mbar_arrive(&bar[kOGo]);
       }
     }
     if (keep && ok && mine) {
@@ -515,24 +545,71 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     uint8_t *out = static_cast<uint8_t *>(r.o);
     const int wide = r.o_f32 ? 4 : 2;  // bytes of an output
     const int64_t unit = b * r.os.b + h * r.os.h + e0 + SW / 2 * h2;
-    for (int c = 0; c < nc; ++c) {
-      if (!held_wait(&bar[kRFull], c & 1, abort_flag, p.timeouts)) break;
+    if (lane == 0 && nc > 0) mbar_arrive(&bar[kOGo]);  // no outputs in front of the first chunk
+    for (int c = -1; c < nc; ++c) {
+      if (c >= 0) {  // outputs of chunk c
+        const int nv = size(c);
+        const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
+        uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
+        if (!held_wait(&bar[kOFull], c & 1, abort_flag, p.timeouts)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < SW / 32; ++j) {
+          float hi[16], lo[16], v[16];
+          const uint32_t col = SW / 2 * h2 + 16 * j;
+          tmem_ld16(quad + Ly::cO1 + col, hi);
+          tmem_ld16(quad + Ly::cO1 + SW + col, lo);
+          tmem_ld16(quad + Ly::cO2 + col, v);
+          tmem_wait_ld();
+          if (j == SW / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(&bar[kOGo]);
+          }
+          if (t < nv) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
+            if (r.o_f32) {
+              float4 *to = reinterpret_cast<float4 *>(at + 64 * j);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else {
+              uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                   pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+            }
+          }
+        }
+      }
+      const int l = c + 1;  // weights of the next chunk
+      if (l == nc) break;
+      if (!held_wait(&bar[kRFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) break;
       tc_fence_after();
+      const uint32_t raw = quad + Ly::cR + 128 * (l & 1);
 #pragma unroll 1
       for (int g = h2; g < 4; g += 2) {
         const int away = rev ? g - qd : qd - g;
         uint32_t pk[16];
         if (away >= 0) {
-          const f2 far = dup2(away > 1 ? exp2f(lg * static_cast<float>(32 * (away - 1))) : 1.f);
           const float4 *w4 = reinterpret_cast<const float4 *>(tab + ((away > 0 ? 32 : 0) + lane) * Ly::kLdT);
           float a[32];
-          tmem_ld32(quad + Ly::cR + 32 * g, a);
+          tmem_ld32(raw + 32 * g, a);
           tmem_wait_ld();
+          if (away > 1) {
+            const f2 far = dup2(exp2f(lg * static_cast<float>(32 * (away - 1))));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 v = unpack2(mul2(far, pack2(a[2 * e], a[2 * e + 1])));
+              a[2 * e] = v.x, a[2 * e + 1] = v.y;
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 w = w4[e];
-            const float2 lo = unpack2(mul2(mul2(far, pack2(w.x, w.y)), pack2(a[4 * e], a[4 * e + 1])));
-            const float2 hi = unpack2(mul2(mul2(far, pack2(w.z, w.w)), pack2(a[4 * e + 2], a[4 * e + 3])));
+            const float2 lo = unpack2(mul2(pack2(w.x, w.y), pack2(a[4 * e], a[4 * e + 1])));
+            const float2 hi = unpack2(mul2(pack2(w.z, w.w), pack2(a[4 * e + 2], a[4 * e + 3])));
             pk[2 * e] = pack_bf16x2(lo.x, lo.y);
             pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
           }
@@ -540,47 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = 0u;
         }
-        tmem_st16u(quad + Ly::cR + 32 * g, pk);
+        tmem_st16u(raw + 32 * g, pk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[kPReady]);
-      // output
-      const int nv = size(c);
-      const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
-      if (!held_wait(&bar[kOFull], c & 1, abort_flag, p.timeouts)) break;
-      tc_fence_after();
-      uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
-#pragma unroll
-      for (int j = 0; j < SW / 32; ++j) {
-        float hi[16], lo[16], v[16];
-        const uint32_t col = SW / 2 * h2 + 16 * j;
-        tmem_ld16(quad + Ly::cO1 + col, hi);
-        tmem_ld16(quad + Ly::cO1 + SW + col, lo);
-        tmem_ld16(quad + Ly::cO2 + col, v);
-        tmem_wait_ld();
-        if (j == SW / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_relaxed(&bar[kOFree]);
-        }
-        if (t < nv) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
-          if (r.o_f32) {
-            float4 *to = reinterpret_cast<float4 *>(at + 64 * j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          } else {
-            uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                 pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
-          }
-        }
-      }
     }
     if (p.a.fill && last_part)
       for (int i = tokens + t; i < p.a.L; i += kC) {
@@ -596,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
 }
 
 template <int DX, int SW, int NS, bool STATE>
-cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
+cudaError_t pass(const TcParams &p, int64_t units, cudaStream_t s) {
   auto k = retention_tc_kernel<DX, SW, NS, STATE>;
   const int bytes = Lay<DX, SW, NS, STATE>::kAlloc;
   const cudaError_t e = allow_smem(k, bytes);
@@ -606,13 +648,13 @@ cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int DX, int SW>
-cudaError_t go_all(const TcParams &p, bool exact, int64_t units, cudaStream_t s) {
+template <int DX, int SW, int NS>
+cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
   if (p.parts > 1) {
-    const cudaError_t e = exact ? go<DX, SW, 3, true>(p, units, s) : go<DX, SW, 1, true>(p, units, s);
+    const cudaError_t e = pass<DX, SW, NS, true>(p, units, s);
     if (e != cudaSuccess) return e;
   }
-  return exact ? go<DX, SW, 3, false>(p, units, s) : go<DX, SW, 1, false>(p, units, s);
+  return pass<DX, SW, NS, false>(p, units, s);
 }
 
 int64_t columns(const RetArgs &a) {
@@ -622,10 +664,10 @@ int64_t columns(const RetArgs &a) {
 }
 
 // Slices of 64 columns compute the raw weights half as often as slices of 32,
-// but are half as many.
+// but are half as many.  Three values of w~ do not fit beside them.
 int slice_width(const RetArgs &a) {
   for (int i = 0; i < a.roles; ++i)
-    if (a.role[i].Dw % 64 != 0) return 32;
+    if (a.role[i].Dw % 64 != 0 || a.role[i].end) return 32;
   return columns(a) / 64 >= kSMs - 24 ? 64 : 32;
 }
 
@@ -681,8 +723,9 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
     const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
     if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
     cudaError_t e;
-    if (SW == 64) e = DX == 64 ? go_all<64, 64>(p, exact, units, s) : go_all<128, 64>(p, exact, units, s);
-    else e = DX == 64 ? go_all<64, 32>(p, exact, units, s) : go_all<128, 32>(p, exact, units, s);
+    if (SW == 64) e = DX == 64 ? go<64, 64, 1>(p, units, s) : go<128, 64, 1>(p, units, s);
+    else if (exact) e = DX == 64 ? go<64, 32, 3>(p, units, s) : go<128, 32, 3>(p, units, s);
+    else e = DX == 64 ? go<64, 32, 1>(p, units, s) : go<128, 32, 1>(p, units, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
