@@ -327,7 +327,7 @@ struct RetRole {
   RetStrides xs, ys, ws, os;
   int xg, yg, wg, Dx, Dw;
   const float *start;
-  float *end, *rec;  // rec: [B][H][parts - 1][Dx][Dw]
+  float *end, *rec;  // rec: [B][H][records][Dx][Dw]
   int start_rs, start_cs;
   float start_scale, end_scale, out_scale;
   int reverse, o_f32;
@@ -341,9 +341,11 @@ struct RetArgs {
   bool fill;  // rows behind a sequence's end become zero (otherwise they are left)
   Gammas lg;  // log2 of each head's decay
 };
-// Parts of the tokens that run side by side, and the records' size in floats
+// Parts of the tokens that run side by side; records of a (batch, head) (the last
+// part has one too where some role wants its end state) and their size in floats
 // over all roles; the kernels take a.role[].rec as laid out by ret_layout.
 int ret_parts(const RetArgs &a, Dtype dt);
+int ret_records(const RetArgs &a, int parts);
 size_t ret_record_floats(const RetArgs &a, int parts);
 void ret_layout(RetArgs *a, int parts, float *ws);
 cudaError_t launch_retention(const RetArgs &a, Dtype dt, int parts, cudaStream_t s);

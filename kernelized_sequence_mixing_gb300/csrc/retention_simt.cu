@@ -312,17 +312,22 @@ cudaError_t launch_group_sum(const float *part, void *out, int64_t rows, int hea
 
 int ret_parts(const RetArgs &a, Dtype dt) { return ret_tc_supported(a, dt) ? ret_parts_tc(a) : ret_parts_simt(a); }
 
+int ret_records(const RetArgs &a, int parts) {
+  for (int i = 0; i < a.roles; ++i)
+    if (a.role[i].end) return parts;
+  return parts - 1;
+}
+
 size_t ret_record_floats(const RetArgs &a, int parts) {
   size_t n = 0;
-  for (int i = 0; i < a.roles; ++i)
-    n += static_cast<size_t>(a.B) * a.H * (parts - 1) * a.role[i].Dx * a.role[i].Dw;
-  return n;
+  for (int i = 0; i < a.roles; ++i) n += static_cast<size_t>(a.role[i].Dx) * a.role[i].Dw;
+  return n * a.B * a.H * ret_records(a, parts);
 }
 
 void ret_layout(RetArgs *a, int parts, float *ws) {
   for (int i = 0; i < a->roles; ++i) {
     a->role[i].rec = ws;
-    ws += static_cast<size_t>(a->B) * a->H * (parts - 1) * a->role[i].Dx * a->role[i].Dw;
+    ws += static_cast<size_t>(a->B) * a->H * ret_records(*a, parts) * a->role[i].Dx * a->role[i].Dw;
   }
 }
 

@@ -9,11 +9,10 @@
 //
 //   R  = x y^T                      (K = Dx; raw weights, tensor memory)
 //   O1 = x [Shi | Slo]              (K = Dx; the state in front, two bf16 values)
-//   dS = y^T [w~1 | w~2 | w~3]      (K = tokens; w~ = decayed rows of w as a sum of
-//                                    two or three bf16 values side by side)
+//   dS = y^T w~                     (K = tokens; w~ = decayed rows of w)
 //   O2 = P w                        (P = R times its powers of the decay, masked, in
 //                                    bf16, A operand in tensor memory)
-//   o  = scale (g^(.) (O1hi + O1lo) + O2),   S <- g^n S + dS1 + dS2 + dS3
+//   o  = scale (g^(.) (O1hi + O1lo) + O2),   S <- g^n S + dS
 //
 // The state itself stays in fp32 registers (a thread has one row of the slice),
 // so dS needs nothing of the chunk before and only the sum S is a chain.  Values
@@ -21,14 +20,16 @@
 // shared memory (128 x 16 values for 128 x 32 x 16 products), not by the
 // products.
 //
-// Warp roles (18 warps):
+// Warp roles (19 warps):
 //   0-7    P: powers of the decay, mask, bf16 (a lane quadrant and two of its
 //          four blocks of 32 columns each); then half of the output columns of
 //          the quadrant's tokens
 //   8-11   state: registers, its bf16 values for the MMA (thread = row)
 //   12-15  w~ (thread = token), and zeros behind a ragged sequence's end
 //   16     TMA: lane 0 the x ring, lane 1 the y ring, lane 2 the w ring
-//   17     TMEM owner and MMA issuer
+//   17     TMEM owner, issues R and O2
+//   18     issues O1 and dS: one warp's instructions for all four (some 500 a
+//          chunk) take longer than the products
 // Every wait is bounded; a CTA that gives up counts the failure in device
 // memory, drains its copies and MMAs, frees tensor memory and exits.
 #include "common.cuh"
@@ -42,8 +43,8 @@ namespace {
 using namespace tc;
 
 constexpr int kC = 128;  // tokens per chunk
-constexpr int kThreads = 576;
-constexpr int kWarpS = 8, kWarpW = 12, kWarpTma = 16, kWarpMma = 17;
+constexpr int kThreads = 608;
+constexpr int kWarpS = 8, kWarpW = 12, kWarpTma = 16, kWarpMma = 17;  // and 18
 constexpr int kAhead = 2;        // chunks between a tile's prefetch into L2 and its load
 constexpr int kBox = kC * 128;  // 128 tokens x 64 features, 128-byte swizzle
 constexpr int kAtom = kC * 64;  // 128 tokens x 32 columns, 64-byte swizzle
@@ -55,12 +56,14 @@ template <int DX, int SW, int NS, bool STATE>
 struct Lay {
   static constexpr int kTile = DX / 64 * kBox;
   static constexpr int kWTile = SW / 32 * kAtom;
-  // a slot: x, then y
-  static constexpr int kYAt = STATE ? 0 : kTile, kSlot = kYAt + kTile;
-  // loads take 2000 cycles and more from issue to landing when all SMs stream, so
-  // as many slots as fit
-  static constexpr int kSlots = STATE ? 4 : 2, kWSlots = STATE || SW == 32 ? 4 : 2;
-  static constexpr int kW = kSlots * kSlot;
+  // Loads take 2000 cycles and more from issue to landing when all SMs stream, so
+  // as many slots as fit; y is held longer than x, w longest.
+  static constexpr int kSumSlots = DX == 128 && SW == 64 && NS == 3 ? 2 : 4;
+  static constexpr int kXSlots = 2, kYSlots = STATE ? kSumSlots : (SW == 32 ? 3 : 2);
+  static constexpr int kWSlots = STATE ? kSumSlots : (SW == 32 ? 4 : 2);
+  static constexpr int kX = 0;
+  static constexpr int kY = STATE ? 0 : kXSlots * kTile;
+  static constexpr int kW = kY + kYSlots * kTile;
   static constexpr int kWt = kW + kWSlots * kWTile;
   static constexpr int kWtBuf = NS * kWTile;
   static constexpr int kSop = kWt + (STATE ? 2 : 1) * kWtBuf;
@@ -70,33 +73,39 @@ struct Lay {
   static constexpr int kLdT = 36;
   static constexpr int kTab = kSop + (STATE ? 0 : 2 * (SW / 32) * kSopAtom);
   static constexpr int kBar = kTab + (STATE ? 0 : 2 * 32 * kLdT * 4);
-  static constexpr int kNumBars = 32;
+  static constexpr int kNumBars = 44;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
   // Tensor memory columns: two buffers of raw weights, in each block of 32
-  // columns then P as bf16 pairs in the first 16; O1 with both values of the state
-  // side by side; O2; dS (twice in the pass that only sums states).
-  static constexpr uint32_t cR = 0, cO1 = 256, cO2 = cO1 + 2 * SW;
-  static constexpr uint32_t cD = STATE ? 0 : cO2 + SW, cD2 = NS * SW;
-  static_assert(cD + (STATE ? 2 : 1) * NS * SW <= 512, "tensor memory");
+  // columns then P as bf16 pairs in the first 16; kO buffers of O1, with both
+  // values of the state side by side, and O2; dS of w~1 and of the others (twice in
+  // the pass that only sums states).
+  static constexpr int kO = SW == 32 ? 2 : 1, kDParts = NS == 1 ? 1 : 2;
+  static constexpr uint32_t cR = 0, cO = 256, cOBuf = 3 * SW;
+  static constexpr uint32_t cD = STATE ? 0 : cO + kO * cOBuf, cD2 = kDParts * SW;
+  static_assert(cD + (STATE ? 2 : 1) * kDParts * SW <= 512, "tensor memory");
 };
 
-// Where a barrier is one and not a pair, each of its phases is seen by every
-// waiter before the next can end.
+// Each phase of a barrier is seen by every waiter before the phase after next of
+// the same barrier can end; the numbers of barriers follow from how far the roles
+// can run ahead of one another.
 enum Bar : int {
-  kXYFull = 0,    // [4] tiles of x and y landed
-  kXYEmpty = 4,   // [4] slot free (MMA commit)
-  kWFull = 8,     // [4]
-  kWEmpty = 12,   // [4]
-  kRFull = 16,    // [2] raw weights computed
-  kDFull = 18,    // [2] dS computed
-  kWReady = 20,   // [2] w~ written (main pass: one)
-  kDRead = 22,    // [2] the pass that only sums states: dS read
-  kOGo = 24,      // the state's bf16 values written, outputs of the chunk before read
-  kPReady = 25,   // P written
-  kOFull = 26,    // O1, O2 complete
-  kDrain = 27,
+  kXFull = 0,     // [4] tile landed
+  kXEmpty = 4,    // [4] slot free (commits of both issuing warps, of one where states are summed)
+  kYFull = 8,     // [4]
+  kYEmpty = 12,   // [4]
+  kWFull = 16,    // [4]
+  kWEmpty = 20,   // [4]
+  kRFull = 24,    // [2] raw weights computed
+  kDFull = 26,    // [2] dS computed
+  kWReady = 28,   // [4] w~ written: the warp that issues O2 waits for it late
+  kDRead = 32,    // [2] the pass that only sums states: dS read
+  kPReady = 34,   // [2] P written
+  kOFull = 36,    // [2] O1, O2 complete
+  kORead = 38,    // [2] O1, O2 read
+  kSReady = 40,   // the state's bf16 values written
+  kDrain = 41,    // [2]
 };
 
 struct TcRole {
@@ -106,7 +115,8 @@ struct TcRole {
 struct TcParams {
   RetArgs a;
   TcRole map[kRetRoles];
-  int parts, cpp, slices;
+  int parts, cpp, slices, records;  // records: of a (batch, head), parts - 1 or parts
+  bool sectors;
   unsigned int *timeouts;
 };
 
@@ -144,42 +154,52 @@ __device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// Of a descriptor only the address in its low word changes from step to step.
-struct Desc {
-  uint32_t lo, hi;
-  __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
-};
-template <bool ADD>
-__device__ __forceinline__ void mma_ss(uint32_t d, const Desc &a, uint32_t a_off, const Desc &b, uint32_t b_off,
-                                       uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
-      "r"(a.lo + a_off), "r"(a.hi), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "n"(ADD ? 1 : 0)
-      : "memory");
+// N MMAs along K, D[tmem] = (ADD: +=) sum of A[smem] B[smem]^T, the operands'
+// addresses (in the descriptors' low words, in units of 16 bytes) going on by a
+// step each; a step of 0: K-major rows of 64 features, by 2 and, behind each four,
+// to the next box.  Unrolled: a loop cannot feed the tensor pipe (220 us against
+// 191 for B2 L16384 H16 D128).
+template <int N, bool ADD, int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_group(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  const uint32_t alo = static_cast<uint32_t>(a), blo = static_cast<uint32_t>(b);
+  const uint32_t ahi = static_cast<uint32_t>(a >> 32), bhi = static_cast<uint32_t>(b >> 32);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t row = (i >> 2) * (kBox >> 4) + (i & 3) * 2;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+        "r"(alo + (A_STEP ? i * A_STEP : row)), "r"(ahi), "r"(blo + (B_STEP ? i * B_STEP : row)), "r"(bhi), "r"(idesc),
+        "r"(ADD || i > 0 ? 1u : 0u)
+        : "memory");
+  }
 }
-template <bool ADD>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, const Desc &b, uint32_t b_off, uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "n"(ADD ? 1 : 0)
-      : "memory");
+// The same with A in tensor memory, P: 16 values of K in 8 columns, 32 in the first
+// half of each 32 columns.
+template <int N, int B_STEP>
+__device__ __forceinline__ void mma_group_p(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  const uint32_t blo = static_cast<uint32_t>(b), bhi = static_cast<uint32_t>(b >> 32);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+        "r"(a + 32 * (i >> 1) + 8 * (i & 1)), "r"(blo + i * B_STEP), "r"(bhi), "r"(idesc), "r"(i > 0 ? 1u : 0u)
+        : "memory");
 }
 // The lane that issues a group of MMAs, the same every time.  A branch around the
-// group, in a warp the compiler knows to agree on its role: 10 instructions an
-// MMA, against 35 with the election inside each.
+// group, in a warp the compiler knows to agree on its role (an election inside
+// each MMA took 35 instructions).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
   return r != 0;
 }
 
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
-  float f[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
-  tmem_st16(taddr, f);
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t *v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // A pair of fp32 values as NS pairs of bf16 values that add up to them (each
@@ -208,11 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
 
   const RetRole &r = p.a.role[blockIdx.z];
   const TcRole &map = p.map[blockIdx.z];
-  const int np = STATE ? p.parts - 1 : p.parts;
+  const int np = STATE ? p.records : p.parts;
   const int slice = blockIdx.x % p.slices, part = blockIdx.x / p.slices % np;
   const int64_t bh = blockIdx.x / p.slices / np;
   const int e0 = slice * SW;
-  if (e0 >= r.Dw) return;
+  // the last part's record serves the end state alone
+  if (e0 >= r.Dw || (STATE && part == p.parts - 1 && !r.end)) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
   // the shuffle tells the compiler that a warp agrees on its role
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -220,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   const int n = (tokens + kC - 1) / kC;
   const bool last_part = part == p.parts - 1;
   const int c0 = min(n, part * p.cpp), nc = (last_part ? n : min(n, c0 + p.cpp)) - c0;
-  const bool keep = STATE || (last_part && r.end);  // the state behind the last chunk is wanted
   const float lg = p.a.lg.g[h];
   // chunk c of the part: its first token and how many it has
   auto first = [&](int c) { return (r.reverse ? n - 1 - c0 - c : c0 + c) * kC; };
@@ -232,17 +252,23 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       tab[(i >> 5) * Ly::kLdT + e] = gap >= 0 ? exp2f(lg * static_cast<float>(gap)) : 0.f;
     }
   if (tid == 32 * kWarpTma) {
-    for (int s = 0; s < 16; ++s) mbar_init(&bar[kXYFull + s], 1);
+    for (int s = 0; s < kRFull; ++s) {
+      const bool both = !STATE && ((s >= kXEmpty && s < kYFull) || (s >= kYEmpty && s < kWFull));
+      mbar_init(&bar[s], both ? 2 : 1);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[kRFull + s], 1);
       mbar_init(&bar[kDFull + s], 1);
       mbar_init(&bar[kWReady + s], STATE ? 12 : 4);
+      mbar_init(&bar[kWReady + 2 + s], STATE ? 12 : 4);
       mbar_init(&bar[kDRead + s], 4);
+      mbar_init(&bar[kPReady + s], 8);
+      mbar_init(&bar[kOFull + s], 2);
+      mbar_init(&bar[kORead + s], 8);
     }
-    mbar_init(&bar[kOGo], 12);
-    mbar_init(&bar[kPReady], 8);
-    mbar_init(&bar[kOFull], 1);
+    mbar_init(&bar[kSReady], 4);
     mbar_init(&bar[kDrain], 1);
+    mbar_init(&bar[kDrain + 1], 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -253,49 +279,35 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   const uint32_t tmem = *tmem_slot;
 
   if (warp == kWarpTma) {
-    if (lane < 2) {  // lane 0: x and y, lane 1: w
-      auto map_of = [&](int i) { return &map.m[i]; };
-      prefetch_tmap(map_of(lane == 0 ? 1 : 2));
-      if (lane == 0 && !STATE) prefetch_tmap(map_of(0));
-      uint64_t *fullb = &bar[lane == 0 ? kXYFull : kWFull], *emptyb = &bar[lane == 0 ? kXYEmpty : kWEmpty];
-      const int hx = h / r.xg, hy = h / r.yg, hw = h / r.wg;
-      const int sharers = r.Dw / SW;
-      // f(map, column, outer coordinates) for each box of a tile of tensor i
-      auto boxes = [&](int i, int head, int t, auto &&f) {
-        const uint8_t *at = map.at[i];
-        auto place = [&](int j) { return at[0] == j ? head : (at[1] == j ? t : b); };
-        const int y = place(0), z = place(1), w = place(2);
-#pragma unroll 1
-        for (int j = 0; j < (i == 2 ? SW / 32 : DX / 64); ++j) f(j, i == 2 ? e0 + 32 * j : 64 * j, y, z, w);
-      };
-      const int slots = lane == 0 ? Ly::kSlots : Ly::kWSlots;
+    if (lane < 3 && !(STATE && lane == 0)) {  // lane 0: x, 1: y, 2: w
+      const CUtensorMap *m = &map.m[lane];
+      const uint8_t *at = map.at[lane];
+      prefetch_tmap(m);
+      uint64_t *fullb = &bar[lane == 0 ? kXFull : (lane == 1 ? kYFull : kWFull)], *emptyb = fullb + 4;
+      const int head = h / (lane == 0 ? r.xg : (lane == 1 ? r.yg : r.wg));
+      const int slots = lane == 0 ? Ly::kXSlots : (lane == 1 ? Ly::kYSlots : Ly::kWSlots);
+      const int bytes = lane == 2 ? Ly::kWTile : Ly::kTile, box = lane == 2 ? kAtom : kBox;
+      const int boxes = bytes / box, x0 = lane == 2 ? e0 : 0, dx = lane == 2 ? 32 : 64;
+      const int sharers = lane == 2 ? 1 : r.Dw / SW, mine = lane == 2 ? 0 : slice;
+      uint8_t *ring = sm + (lane == 0 ? Ly::kX : (lane == 1 ? Ly::kY : Ly::kW));
+      auto place = [&](int j, int t) { return at[0] == j ? head : (at[1] == j ? t : b); };
       int issued = 0;
       for (int c = 0; c < nc; ++c) {
         const int sl = c % slots;
         if (!mbar_wait(&emptyb[sl], ((c / slots) & 1) ^ 1, abort_flag, p.timeouts)) break;
-        // The slots hold less than the memory's latency: later tiles come into L2
-        // ahead, the boxes of x and y shared out among the slices that read them.
-        const int t0 = first(c), tp = first(c + kAhead);
-        const bool ahead = c + kAhead < nc;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&fullb[sl], Ly::kSlot);
-          for (int i = STATE ? 1 : 0; i < 2; ++i) {
-            uint8_t *dst = sm + sl * Ly::kSlot + (i == 0 ? 0 : Ly::kYAt);
-            boxes(i, i == 0 ? hx : hy, t0, [&](int j, int x, int y, int z, int w) {
-              tma_load_4d(dst + j * kBox, map_of(i), x, y, z, w, &fullb[sl]);
-            });
-          }
-          for (int i = STATE ? 1 : 0; ahead && i < 2; ++i)
-            boxes(i, i == 0 ? hx : hy, tp, [&](int j, int x, int y, int z, int w) {
-              if ((i * (DX / 64) + j) % sharers == slice) tma_prefetch_4d(map_of(i), x, y, z, w);
-            });
-        } else {
-          mbar_arrive_expect_tx(&fullb[sl], Ly::kWTile);
-          boxes(2, hw, t0, [&](int j, int x, int y, int z, int w) {
-            tma_load_4d(sm + Ly::kW + sl * Ly::kWTile + j * kAtom, map_of(2), x, y, z, w, &fullb[sl]);
-          });
-          if (ahead)
-            boxes(2, hw, tp, [&](int, int x, int y, int z, int w) { tma_prefetch_4d(map_of(2), x, y, z, w); });
+        const int t0 = first(c);
+        mbar_arrive_expect_tx(&fullb[sl], bytes);
+#pragma unroll 1
+        for (int j = 0; j < boxes; ++j)
+          tma_load_4d(ring + sl * bytes + j * box, m, x0 + dx * j, place(0, t0), place(1, t0), place(2, t0), &fullb[sl]);
+        // Later tiles come into L2 ahead, the boxes of x and y shared out among the
+        // slices that read them.
+        if (c + kAhead < nc) {
+          const int tp = first(c + kAhead);
+#pragma unroll 1
+          for (int j = 0; j < boxes; ++j)
+            if ((lane * boxes + j) % sharers == mine)
+              tma_prefetch_4d(m, x0 + dx * j, place(0, tp), place(1, tp), place(2, tp));
         }
         issued = c + 1;
       }
@@ -304,122 +316,116 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           mbar_wait_drain(&fullb[c % slots], (c / slots) & 1);
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
-    constexpr uint32_t ID_R = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * SW, false, true);
-    constexpr uint32_t ID_D = idesc_bf16(DX, NS * SW, true, true);
-    constexpr uint32_t ID_O2 = idesc_bf16(128, SW, false, true);
+  } else if (warp >= kWarpMma) {
     const uint32_t base = smem_u32(sm);
     // rows as K-major operands (K = features) and y^T as A (M = features in
     // 64-wide atoms, K = tokens); w, w~ and the state with columns in atoms of 32
-    auto rows = [&](int at) { return Desc(smem_desc(base + at, 16, 1024, kSw128)); };
-    auto atoms = [&](int at, int atom) { return Desc(smem_desc(base + at, atom, 512, kSw64)); };
-    auto step = [](int kk) { return static_cast<uint32_t>((kk >> 2) * (kBox >> 4) + (kk & 3) * 2); };
-    auto slot = [](int c) { return c % Ly::kSlots; };
-    auto landed = [&](int c) { return held_wait(&bar[kXYFull + slot(c)], (c / Ly::kSlots) & 1, abort_flag, p.timeouts); };
-    auto tiles = [&](int c) {  // x and y of chunk c have landed
-      return landed(c) &&
-             // rows behind the end have to be zero first
-             (size(c) == kC || held_wait(&bar[kWReady], c & 1, abort_flag, p.timeouts));
+    auto rows = [&](int at) { return smem_desc(base + at, 16, 1024, kSw128); };
+    auto atoms = [&](int at, int atom) { return smem_desc(base + at, atom, 512, kSw64); };
+    auto xs = [](int c) { return c % Ly::kXSlots; };
+    auto ys = [](int c) { return c % Ly::kYSlots; };
+    auto x_landed = [&](int c) { return held_wait(&bar[kXFull + xs(c)], (c / Ly::kXSlots) & 1, abort_flag, p.timeouts); };
+    auto y_landed = [&](int c) { return held_wait(&bar[kYFull + ys(c)], (c / Ly::kYSlots) & 1, abort_flag, p.timeouts); };
+    auto w_ready = [&](int c) { return held_wait(&bar[kWReady + (c & 3)], (c >> 2) & 1, abort_flag, p.timeouts); };
+    // the outputs that were in the buffer have been read
+    auto o_free = [&](int c) {
+      const int l = c - Ly::kO;
+      return l < 0 || held_wait(&bar[kORead + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts);
     };
-    auto tiles_state = [&](int c) {  // y has landed, dS of two chunks ago has been read
-      return landed(c) && (c < 2 || held_wait(&bar[kDRead + (c & 1)], ((c - 2) >> 1) & 1, abort_flag, p.timeouts));
-    };
-    auto weigh = [&](int c) {  // R of chunk c
-      const Desc x = rows(slot(c) * Ly::kSlot), y = rows(slot(c) * Ly::kSlot + Ly::kYAt);
-      const uint32_t d = tmem + Ly::cR + 128 * (c & 1);
-      if (elect_one()) {
-        mma_ss<false>(d, x, 0, y, 0, ID_R);
-#pragma unroll
-        for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(d, x, step(kk), y, step(kk), ID_R);
-        mma_commit(&bar[kRFull + (c & 1)]);
-      }
-      __syncwarp();
-    };
-    bool ok = true;
-    if (!STATE && nc > 0) {
-      ok = tiles(0);
-      tc_fence_after();
-      if (ok) weigh(0);
-    }
-    // Per chunk O1, dS, R of the next chunk and O2, so that each group's consumers
-    // work behind other groups: P behind O2 and O1 and dS of the next chunk, the
-    // state behind R and O2, the outputs' read (before the next O1) behind nothing.
-    for (int c = 0; ok && c < nc; ++c) {
-      const int sl = c & 1;
-      const uint32_t ph = (c >> 1) & 1;
+    auto o_at = [&](int c) { return tmem + Ly::cO + (Ly::kO == 2 && (c & 1) ? Ly::cOBuf : 0u); };
+    if (warp == kWarpMma) {
+      // R of a chunk ahead of O2 of the one before, so that P works behind O2
       if (!STATE) {
-        if (!held_wait(&bar[kOGo], c & 1, abort_flag, p.timeouts)) break;
-        tc_fence_after();
-        const Desc x = rows(slot(c) * Ly::kSlot), sop = atoms(Ly::kSop, Ly::kSopAtom);
-        if (elect_one()) {
-          mma_ss<false>(tmem + Ly::cO1, x, 0, sop, 0, ID_O1);
-#pragma unroll
-          for (int kk = 1; kk < DX / 16; ++kk) mma_ss<true>(tmem + Ly::cO1, x, step(kk), sop, kk * 64, ID_O1);
+        constexpr uint32_t ID_R = idesc_bf16(128, 128, false, false), ID_O2 = idesc_bf16(128, SW, false, true);
+#pragma unroll 1
+        for (int c = 0; c <= nc; ++c) {
+          if (c < nc) {
+            // rows behind the end have to be zero first
+            if (!x_landed(c) || !y_landed(c) || (size(c) < kC && !w_ready(c))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_group<DX / 16, false, 0, 0>(tmem + Ly::cR + 128 * (c & 1), rows(Ly::kX + xs(c) * Ly::kTile),
+                                              rows(Ly::kY + ys(c) * Ly::kTile), ID_R);
+              mma_commit(&bar[kRFull + (c & 1)]);
+              mma_commit(&bar[kXEmpty + xs(c)]);
+              mma_commit(&bar[kYEmpty + ys(c)]);
+            }
+            __syncwarp();
+          }
+          if (c > 0) {
+            const int l = c - 1;
+            if (!w_ready(l) || !o_free(l) || !held_wait(&bar[kPReady + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts))
+              break;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_group_p<kC / 16, 64>(o_at(l) + 2 * SW, tmem + Ly::cR + 128 * (l & 1),
+                                       atoms(Ly::kW + l % Ly::kWSlots * Ly::kWTile, kAtom), ID_O2);
+              mma_commit(&bar[kOFull + (l & 1)]);
+              mma_commit(&bar[kWEmpty + l % Ly::kWSlots]);
+            }
+            __syncwarp();
+          }
         }
-        __syncwarp();
-      } else if (!tiles_state(c)) {
-        break;
       }
-      if (!held_wait(&bar[kWReady + (STATE ? sl : 0)], STATE ? ph : c & 1, abort_flag, p.timeouts)) break;
-      tc_fence_after();
-      const Desc yt(smem_desc(base + slot(c) * Ly::kSlot + Ly::kYAt, kBox, 1024, kSw128));
-      const Desc wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
-      const uint32_t d = tmem + (STATE && sl ? Ly::cD2 : Ly::cD);
-      if (elect_one()) {
-        if (keep || c + 1 < nc) {
-          mma_ss<false>(d, yt, 0, wt, 0, ID_D);
-#pragma unroll
-          for (int kk = 1; kk < kC / 16; ++kk) mma_ss<true>(d, yt, kk * 128, wt, kk * 64, ID_D);
-        }
-        mma_commit(&bar[kDFull + sl]);
-        mma_commit(&bar[kXYEmpty + slot(c)]);
-        if (STATE) mma_commit(&bar[kWEmpty + c % Ly::kWSlots]);
-      }
-      __syncwarp();
-      if (!STATE) {
-        if (c + 1 < nc) {
-          if (!tiles(c + 1)) break;
+    } else {
+      constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * SW, false, true);
+      constexpr uint32_t ID_D = idesc_bf16(DX, Ly::kDParts * SW, true, true), ID_D3 = idesc_bf16(DX, SW, true, true);
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c) {
+        const int sl = c & 1;
+        if (!STATE) {
+          if (!x_landed(c) || !o_free(c) || !held_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts)) break;
           tc_fence_after();
-          weigh(c + 1);
+          if (elect_one()) {
+            mma_group<DX / 16, false, 0, 64>(o_at(c), rows(Ly::kX + xs(c) * Ly::kTile), atoms(Ly::kSop, Ly::kSopAtom),
+                                             ID_O1);
+            mma_commit(&bar[kOFull + sl]);
+            mma_commit(&bar[kXEmpty + xs(c)]);
+          }
+          __syncwarp();
+        } else if (c > 1 && !held_wait(&bar[kDRead + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
+          break;  // dS of two chunks ago has been read
         }
-        if (!held_wait(&bar[kPReady], c & 1, abort_flag, p.timeouts)) break;
+        if (!y_landed(c) || !w_ready(c)) break;
         tc_fence_after();
-        const Desc w = atoms(Ly::kW + c % Ly::kWSlots * Ly::kWTile, kAtom);
-        const uint32_t pr = tmem + Ly::cR + 128 * sl;
         if (elect_one()) {
-          mma_ts<false>(tmem + Ly::cO2, pr, w, 0, ID_O2);
-#pragma unroll
-          for (int kk = 1; kk < kC / 16; ++kk)
-            mma_ts<true>(tmem + Ly::cO2, pr + 32 * (kk >> 1) + 8 * (kk & 1), w, kk * 64, ID_O2);
-          mma_commit(&bar[kOFull]);
-          mma_commit(&bar[kWEmpty + c % Ly::kWSlots]);
+          if (STATE || c + 1 < nc) {
+            const uint64_t yt = smem_desc(base + Ly::kY + ys(c) * Ly::kTile, kBox, 1024, kSw128);
+            const uint64_t wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
+            const uint32_t d = tmem + Ly::cD + (STATE && sl ? Ly::cD2 : 0u);
+            mma_group<kC / 16, false, 128, 64>(d, yt, wt, ID_D);
+            if (NS == 3)  // the smallest values into the same sums as the second
+              mma_group<kC / 16, true, 128, 64>(d + SW, yt, wt + (2 * Ly::kWTile >> 4), ID_D3);
+          }
+          mma_commit(&bar[kDFull + sl]);
+          mma_commit(&bar[kYEmpty + ys(c)]);
+          if (STATE) mma_commit(&bar[kWEmpty + c % Ly::kWSlots]);
         }
         __syncwarp();
       }
     }
     // every MMA issued has completed before TMEM is released
     if (elect_one()) {
-      mma_commit(&bar[kDrain]);
-      mbar_wait_drain(&bar[kDrain], 0);
+      mma_commit(&bar[kDrain + warp - kWarpMma]);
+      mbar_wait_drain(&bar[kDrain + warp - kWarpMma], 0);
     }
     __syncwarp();
   } else if (warp >= kWarpW || (STATE && warp < kWarpS)) {
     // a third of the columns each where the warps that weigh have nothing to do
     const int t = tid & (kC - 1), group = STATE && warp >= kWarpW ? 2 : warp >> 2 & 1, groups = STATE ? 3 : 1;
     for (int c = 0; c < nc; ++c) {
-      const int ws = c % Ly::kWSlots, xs = c % Ly::kSlots, nv = size(c);
+      const int ws = c % Ly::kWSlots, ys = c % Ly::kYSlots, nv = size(c);
       const float f = t < nv ? exp2f(lg * static_cast<float>(r.reverse ? t + 1 : nv - 1 - t)) : 0.f;
       // the buffer is free once the sum over the chunk that used it is done
       const int before = c - (STATE ? 2 : 1);
       if (!held_wait(&bar[kWFull + ws], (c / Ly::kWSlots) & 1, abort_flag, p.timeouts) ||
-          (nv < kC && !held_wait(&bar[kXYFull + xs], (c / Ly::kSlots) & 1, abort_flag, p.timeouts)) ||
+          (nv < kC && !held_wait(&bar[kYFull + ys], (c / Ly::kYSlots) & 1, abort_flag, p.timeouts)) ||
           (before >= 0 && !held_wait(&bar[kDFull + (before & 1)], (before >> 1) & 1, abort_flag, p.timeouts)))
         break;
       uint8_t *wrow = sm + Ly::kW + ws * Ly::kWTile;
       uint8_t *wt = sm + Ly::kWt + (STATE ? (c & 1) * Ly::kWtBuf : 0);
       if (t < nv) {
-#pragma unroll 2
+#pragma unroll 1
         for (int q = STATE ? group : 0; q < SW / 8; q += groups) {
           const int at = (q >> 2) * kAtom + sw64_off(t, 16 * (q & 3));
           const uint4 x = *reinterpret_cast<const uint4 *>(wrow + at);
@@ -442,11 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         }
 #pragma unroll 1
         for (int q = STATE ? group : 0; q < DX / 8; q += groups)
-          *reinterpret_cast<uint4 *>(sm + xs * Ly::kSlot + Ly::kYAt + (q >> 3) * kBox + sw128_off(t, 16 * (q & 7))) = z;
+          *reinterpret_cast<uint4 *>(sm + Ly::kY + ys * Ly::kTile + (q >> 3) * kBox + sw128_off(t, 16 * (q & 7))) = z;
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[kWReady + (STATE ? c & 1 : 0)]);
+      if (lane == 0) mbar_arrive(&bar[kWReady + (c & 3)]);
     }
   } else if (warp >= kWarpS) {
     // row d of the state: all 32 lanes of a quadrant, or (64 features) 16
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     const int d = DX == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
     const bool mine = DX == 128 || lane < 16;
     const int64_t size_of = static_cast<int64_t>(DX) * r.Dw;
-    float *rec = r.rec + bh * (p.parts - 1) * size_of;
+    float *rec = r.rec + bh * p.records * size_of;
     f2 S[SW / 2];
 #pragma unroll
     for (int e = 0; e < SW / 2; ++e) S[e] = dup2(0.f);
@@ -478,10 +484,24 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           S[2 * e + 1] = fma2(f, pack2(v.z, v.w), S[2 * e + 1]);
         }
       }
+      if (last_part && r.end && mine) {
+        // the end state: this part's start and its record, whose sums are exact to
+        // fp32 (w~ as three values), while this pass makes do with one
+        const f2 f = dup2(exp2f(lg * static_cast<float>(tokens - here)) * r.end_scale), one = dup2(r.end_scale);
+        const float4 *from = reinterpret_cast<const float4 *>(rec + part * size_of + d * r.Dw + e0);
+        float4 *to = reinterpret_cast<float4 *>(r.end + bh * size_of + d * r.Dw + e0);
+#pragma unroll
+        for (int e = 0; e < SW / 4; ++e) {
+          const float4 v = from[e];
+          const float2 lo = unpack2(fma2(one, pack2(v.x, v.y), mul2(f, S[2 * e])));
+          const float2 hi = unpack2(fma2(one, pack2(v.z, v.w), mul2(f, S[2 * e + 1])));
+          to[e] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+      }
     }
     bool ok = true;
     for (int c = 0; c <= nc; ++c) {
-      if (c > 0 && (c < nc || keep)) {  // S <- g^n S + dS of chunk c - 1
+      if (c > 0 && (c < nc || STATE)) {  // S <- g^n S + dS of chunk c - 1
         const int l = c - 1;
         const f2 g = dup2(exp2f(lg * static_cast<float>(size(l))));
         if (!held_wait(&bar[kDFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) {
@@ -489,18 +509,17 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           break;
         }
         tc_fence_after();
-        const uint32_t at = tmem_addr(tmem, 32 * qd, STATE && (l & 1) ? Ly::cD2 : Ly::cD);
+        const uint32_t at = tmem_addr(tmem, 32 * qd, Ly::cD + (STATE && (l & 1) ? Ly::cD2 : 0u));
 #pragma unroll
         for (int j = 0; j < SW / 16; ++j) {
-          float x[NS][16];
+          float x[Ly::kDParts][16];
 #pragma unroll
-          for (int k = 0; k < NS; ++k) tmem_ld16(at + SW * k + 16 * j, x[k]);
+          for (int k = 0; k < Ly::kDParts; ++k) tmem_ld16(at + SW * k + 16 * j, x[k]);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            f2 v = pack2(x[NS - 1][2 * e], x[NS - 1][2 * e + 1]);
-#pragma unroll
-            for (int k = NS - 2; k >= 0; --k) v = add2(v, pack2(x[k][2 * e], x[k][2 * e + 1]));
+            f2 v = pack2(x[0][2 * e], x[0][2 * e + 1]);
+            if (NS > 1) v = add2(v, pack2(x[Ly::kDParts - 1][2 * e], x[Ly::kDParts - 1][2 * e + 1]));
             S[8 * j + e] = fma2(g, S[8 * j + e], v);
           }
         }
@@ -524,15 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kOGo]);
+        if (lane == 0) mbar_arrive(&bar[kSReady]);
       }
     }
-    if (keep && ok && mine) {
-      float4 *to = reinterpret_cast<float4 *>((STATE ? rec + part * size_of : r.end + bh * size_of) + d * r.Dw + e0);
-      const f2 f = dup2(STATE ? 1.f : r.end_scale);
+    if (STATE && ok && mine) {
+      float4 *to = reinterpret_cast<float4 *>(rec + part * size_of + d * r.Dw + e0);
 #pragma unroll
       for (int e = 0; e < SW / 4; ++e) {
-        const float2 lo = unpack2(mul2(f, S[2 * e])), hi = unpack2(mul2(f, S[2 * e + 1]));
+        const float2 lo = unpack2(S[2 * e]), hi = unpack2(S[2 * e + 1]);
         to[e] = make_float4(lo.x, lo.y, hi.x, hi.y);
       }
     }
@@ -545,26 +563,25 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     uint8_t *out = static_cast<uint8_t *>(r.o);
     const int wide = r.o_f32 ? 4 : 2;  // bytes of an output
     const int64_t unit = b * r.os.b + h * r.os.h + e0 + SW / 2 * h2;
-    if (lane == 0 && nc > 0) mbar_arrive(&bar[kOGo]);  // no outputs in front of the first chunk
     for (int c = -1; c < nc; ++c) {
       if (c >= 0) {  // outputs of chunk c
         const int nv = size(c);
         const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
         uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
-        if (!held_wait(&bar[kOFull], c & 1, abort_flag, p.timeouts)) break;
+        if (!held_wait(&bar[kOFull + (c & 1)], (c >> 1) & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < SW / 32; ++j) {
           float hi[16], lo[16], v[16];
-          const uint32_t col = SW / 2 * h2 + 16 * j;
-          tmem_ld16(quad + Ly::cO1 + col, hi);
-          tmem_ld16(quad + Ly::cO1 + SW + col, lo);
-          tmem_ld16(quad + Ly::cO2 + col, v);
+          const uint32_t o = quad + Ly::cO + (Ly::kO == 2 && (c & 1) ? Ly::cOBuf : 0u) + SW / 2 * h2 + 16 * j;
+          tmem_ld16(o, hi);
+          tmem_ld16(o + SW, lo);
+          tmem_ld16(o + 2 * SW, v);
           tmem_wait_ld();
           if (j == SW / 32 - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_relaxed(&bar[kOGo]);
+            if (lane == 0) mbar_arrive_relaxed(&bar[kORead + (c & 1)]);
           }
           if (t < nv) {
 #pragma unroll
@@ -574,11 +591,17 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
 #pragma unroll
               for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             } else {
-              uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
+              uint32_t pk[8];
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                to[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                   pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+              for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+              // whole 32-byte sectors where the rows lie on them (191 us against 210)
+              if (p.sectors) {
+                st_global_v8(at + 32 * j, pk);
+              } else {
+                uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
+                to[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                to[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+              }
             }
           }
         }
@@ -589,40 +612,34 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       tc_fence_after();
       const uint32_t raw = quad + Ly::cR + 128 * (l & 1);
 #pragma unroll 1
-      for (int g = h2; g < 4; g += 2) {
-        const int away = rev ? g - qd : qd - g;
-        uint32_t pk[16];
+      for (int i = 0; i < 4; ++i) {  // half of a block: 16 columns
+        const int g = h2 + (i & 2), half = i & 1, away = rev ? g - qd : qd - g;
+        uint32_t pk[8];
         if (away >= 0) {
-          const float4 *w4 = reinterpret_cast<const float4 *>(tab + ((away > 0 ? 32 : 0) + lane) * Ly::kLdT);
-          float a[32];
-          tmem_ld32(raw + 32 * g, a);
+          const float4 *w4 = reinterpret_cast<const float4 *>(tab + ((away > 0 ? 32 : 0) + lane) * Ly::kLdT + 16 * half);
+          const f2 far = dup2(away > 1 ? exp2f(lg * static_cast<float>(32 * (away - 1))) : 1.f);
+          float a[16];
+          tmem_ld16(raw + 32 * g + 16 * half, a);
           tmem_wait_ld();
-          if (away > 1) {
-            const f2 far = dup2(exp2f(lg * static_cast<float>(32 * (away - 1))));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 v = unpack2(mul2(far, pack2(a[2 * e], a[2 * e + 1])));
-              a[2 * e] = v.x, a[2 * e + 1] = v.y;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < 4; ++e) {
             const float4 w = w4[e];
-            const float2 lo = unpack2(mul2(pack2(w.x, w.y), pack2(a[4 * e], a[4 * e + 1])));
-            const float2 hi = unpack2(mul2(pack2(w.z, w.w), pack2(a[4 * e + 2], a[4 * e + 3])));
+            const float2 lo = unpack2(mul2(mul2(far, pack2(w.x, w.y)), pack2(a[4 * e], a[4 * e + 1])));
+            const float2 hi = unpack2(mul2(mul2(far, pack2(w.z, w.w)), pack2(a[4 * e + 2], a[4 * e + 3])));
             pk[2 * e] = pack_bf16x2(lo.x, lo.y);
             pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          for (int e = 0; e < 8; ++e) pk[e] = 0u;
         }
-        tmem_st16u(raw + 32 * g, pk);
+        // the second half's P lies over the first half's raw weights, read already
+        tmem_st8u(raw + 32 * g + 8 * half, pk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[kPReady]);
+      if (lane == 0) mbar_arrive(&bar[kPReady + (l & 1)]);
     }
     if (p.a.fill && last_part)
       for (int i = tokens + t; i < p.a.L; i += kC) {
@@ -643,32 +660,50 @@ cudaError_t pass(const TcParams &p, int64_t units, cudaStream_t s) {
   const int bytes = Lay<DX, SW, NS, STATE>::kAlloc;
   const cudaError_t e = allow_smem(k, bytes);
   if (e != cudaSuccess) return e;
-  const int np = STATE ? p.parts - 1 : p.parts;
+  const int np = STATE ? p.records : p.parts;
   k<<<dim3(static_cast<unsigned>(units * np), 1, p.a.roles), kThreads, bytes, s>>>(p);
   return cudaGetLastError();
 }
 
-template <int DX, int SW, int NS>
-cudaError_t go(const TcParams &p, int64_t units, cudaStream_t s) {
-  if (p.parts > 1) {
-    const cudaError_t e = pass<DX, SW, NS, true>(p, units, s);
+template <int DX, int SW>
+cudaError_t go(const TcParams &p, bool exact, int64_t units, cudaStream_t s) {
+  if (p.records > 0) {
+    const cudaError_t e = exact ? pass<DX, SW, 3, true>(p, units, s) : pass<DX, SW, 1, true>(p, units, s);
     if (e != cudaSuccess) return e;
   }
-  return pass<DX, SW, NS, false>(p, units, s);
+  return pass<DX, SW, 1, false>(p, units, s);
 }
 
-int64_t columns(const RetArgs &a) {
-  int64_t n = 0;
-  for (int i = 0; i < a.roles; ++i) n += static_cast<int64_t>(a.B) * a.H * a.role[i].Dw;
-  return n;
-}
+// How a call is cut: slices of SW columns and parts of the tokens.
+struct Cut {
+  int SW, parts;
+};
 
-// Slices of 64 columns compute the raw weights half as often as slices of 32,
-// but are half as many.  Three values of w~ do not fit beside them.
-int slice_width(const RetArgs &a) {
-  for (int i = 0; i < a.roles; ++i)
-    if (a.role[i].Dw % 64 != 0 || a.role[i].end) return 32;
-  return columns(a) / 64 >= kSMs - 24 ? 64 : 32;
+// The cut that is done first by a model of one CTA per SM: a chunk takes 1 unit of
+// time with slices of 32 columns and 1.6 with 64 (2900 and 4700 cycles of 128
+// features), in the pass that sums states 0.4 and 0.5, and a CTA 4 units to begin
+// and end.
+Cut cut_of(const RetArgs &a) {
+  const int chunks = (a.L + kC - 1) / kC;
+  bool wide = true, end = false;
+  for (int i = 0; i < a.roles; ++i) {
+    wide &= a.role[i].Dw % 64 == 0;
+    end |= a.role[i].end != nullptr;
+  }
+  Cut best = {32, 1};
+  double least = 1e300;
+  for (int SW = 32; SW <= (wide ? 64 : 32); SW += 32) {
+    int64_t units = 0;
+    for (int i = 0; i < a.roles; ++i) units += static_cast<int64_t>(a.B) * a.H * (a.role[i].Dw / SW);
+    for (int parts = 1; parts <= 16 && (parts == 1 || parts * 4 <= chunks); ++parts) {
+      const int cpp = (chunks + parts - 1) / parts, sums = end ? parts : parts - 1;
+      auto waves = [&](int64_t n) { return static_cast<double>((n + kSMs - 1) / kSMs); };
+      double t = waves(units * parts) * (cpp * (SW == 32 ? 1.0 : 1.6) + 4);
+      if (sums > 0) t += waves(units * sums) * (cpp * (SW == 32 ? 0.4 : 0.5) + 4);
+      if (t < least) least = t, best = {SW, parts};
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -680,20 +715,10 @@ bool ret_tc_supported(const RetArgs &a, Dtype dt) {
   return true;
 }
 
-int ret_parts_tc(const RetArgs &a) {
-  const int64_t units = columns(a) / slice_width(a);
-  const int chunks = (a.L + kC - 1) / kC;
-  // Parts cost a pass over y and w for their records (about half of a chunk's
-  // time) and a launch (about four chunks' time).
-  int64_t parts = kSMs / (units > 0 ? units : 1);
-  if (parts > 16) parts = 16;
-  if (parts > chunks / 4) parts = chunks / 4;
-  if (parts < 2 || 1.5 * chunks / parts + 4 > chunks) return 1;
-  return static_cast<int>(parts);
-}
+int ret_parts_tc(const RetArgs &a) { return cut_of(a).parts; }
 
 cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
-  const int chunks = (a.L + kC - 1) / kC, SW = slice_width(a);
+  const int chunks = (a.L + kC - 1) / kC, SW = cut_of(a).SW;
   unsigned int *timeouts = wait_timeout_counter();
   if (!timeouts) return cudaErrorNotSupported;
   // one launch for the roles of each number of features
@@ -704,7 +729,8 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
     p.parts = parts;
     p.cpp = (chunks + parts - 1) / parts;
     p.timeouts = timeouts;
-    bool exact = false;
+    p.sectors = true;
+    bool end = false;
     for (int i = 0; i < a.roles; ++i) {
       const RetRole &r = a.role[i];
       if (r.Dx != DX) continue;
@@ -717,15 +743,16 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
         return cudaErrorNotSupported;
       p.a.role[p.a.roles++] = r;
       if (r.Dw / SW > p.slices) p.slices = r.Dw / SW;
-      exact |= r.end != nullptr;
+      end |= r.end != nullptr;
+      p.sectors &= reinterpret_cast<uintptr_t>(r.o) % 32 == 0 && (r.os.b | r.os.t | r.os.h) % 16 == 0;
     }
     if (!p.a.roles) continue;
+    p.records = ret_records(a, parts);
     const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
     if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
     cudaError_t e;
-    if (SW == 64) e = DX == 64 ? go<64, 64, 1>(p, units, s) : go<128, 64, 1>(p, units, s);
-    else if (exact) e = DX == 64 ? go<64, 32, 3>(p, units, s) : go<128, 32, 3>(p, units, s);
-    else e = DX == 64 ? go<64, 32, 1>(p, units, s) : go<128, 32, 1>(p, units, s);
+    if (SW == 64) e = DX == 64 ? go<64, 64>(p, end, units, s) : go<128, 64>(p, end, units, s);
+    else e = DX == 64 ? go<64, 32>(p, end, units, s) : go<128, 32>(p, end, units, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
