@@ -26,7 +26,7 @@
 //          the quadrant's tokens
 //   8-11   state: registers, its bf16 values for the MMA (thread = row)
 //   12-15  w~ (thread = token), and zeros behind a ragged sequence's end
-//   16     TMA: lane 0 the x ring, lane 1 the y ring, lane 2 the w ring
+//   16     TMA: rings of x, y and w
 //   17     TMEM owner, issues R and O2
 //   18     issues O1 and dS: one warp's instructions for all four (some 500 a
 //          chunk) take longer than the products
@@ -45,7 +45,6 @@ using namespace tc;
 constexpr int kC = 128;  // tokens per chunk
 constexpr int kThreads = 608;
 constexpr int kWarpS = 8, kWarpW = 12, kWarpTma = 16, kWarpMma = 17;  // and 18
-constexpr int kAhead = 2;        // chunks between a tile's prefetch into L2 and its load
 constexpr int kBox = kC * 128;  // 128 tokens x 64 features, 128-byte swizzle
 constexpr int kAtom = kC * 64;  // 128 tokens x 32 columns, 64-byte swizzle
 
@@ -157,44 +156,70 @@ __device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity, volati
 // N MMAs along K, D[tmem] = (ADD: +=) sum of A[smem] B[smem]^T, the operands'
 // addresses (in the descriptors' low words, in units of 16 bytes) going on by a
 // step each; a step of 0: K-major rows of 64 features, by 2 and, behind each four,
-// to the next box.  Unrolled: a loop cannot feed the tensor pipe (220 us against
-// 191 for B2 L16384 H16 D128).
+// to the next box.  All lanes come here and the leader issues, by predicate: with
+// a branch of one lane around them the operands go through vector registers and an
+// MMA takes 50 cycles to issue however small it is, against 16 (a loop, not
+// unrolled, cannot feed the tensor pipe either).
 template <int N, bool ADD, int A_STEP, int B_STEP>
-__device__ __forceinline__ void mma_group(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_group(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   const uint32_t alo = static_cast<uint32_t>(a), blo = static_cast<uint32_t>(b);
   const uint32_t ahi = static_cast<uint32_t>(a >> 32), bhi = static_cast<uint32_t>(b >> 32);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uint32_t row = (i >> 2) * (kBox >> 4) + (i & 3) * 2;
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+        "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+        " mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
         "r"(alo + (A_STEP ? i * A_STEP : row)), "r"(ahi), "r"(blo + (B_STEP ? i * B_STEP : row)), "r"(bhi), "r"(idesc),
-        "r"(ADD || i > 0 ? 1u : 0u)
+        "r"(ADD || i > 0 ? 1u : 0u), "r"(leader)
         : "memory");
   }
 }
 // The same with A in tensor memory, P: 16 values of K in 8 columns, 32 in the first
 // half of each 32 columns.
 template <int N, int B_STEP>
-__device__ __forceinline__ void mma_group_p(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_group_p(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   const uint32_t blo = static_cast<uint32_t>(b), bhi = static_cast<uint32_t>(b >> 32);
 #pragma unroll
   for (int i = 0; i < N; ++i)
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
-        "r"(a + 32 * (i >> 1) + 8 * (i & 1)), "r"(blo + i * B_STEP), "r"(bhi), "r"(idesc), "r"(i > 0 ? 1u : 0u)
+        "{\n .reg .pred p, e;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 e, %6, 0;\n mov.b64 y, {%2, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+        "r"(a + 32 * (i >> 1) + 8 * (i & 1)), "r"(blo + i * B_STEP), "r"(bhi), "r"(idesc), "r"(i > 0 ? 1u : 0u),
+        "r"(leader)
         : "memory");
 }
-// The lane that issues a group of MMAs, the same every time.  A branch around the
-// group, in a warp the compiler knows to agree on its role (an election inside
-// each MMA took 35 instructions).
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+      " @e mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                         uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %7, 0;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
-  return r != 0;
+  return r;
 }
+// A value that all lanes agree on, and the compiler knows it.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t *v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
@@ -235,9 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   // the last part's record serves the end state alone
   if (e0 >= r.Dw || (STATE && part == p.parts - 1 && !r.end)) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
-  // the shuffle tells the compiler that a warp agrees on its role
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int tokens = ret_tokens(p.a.lens, b, p.a.L);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int tokens = uniform(ret_tokens(p.a.lens, b, p.a.L));
   const int n = (tokens + kC - 1) / kC;
   const bool last_part = part == p.parts - 1;
   const int c0 = min(n, part * p.cpp), nc = (last_part ? n : min(n, c0 + p.cpp)) - c0;
@@ -276,45 +300,54 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   if (warp == kWarpTma) {
-    if (lane < 3 && !(STATE && lane == 0)) {  // lane 0: x, 1: y, 2: w
-      const CUtensorMap *m = &map.m[lane];
-      const uint8_t *at = map.at[lane];
-      prefetch_tmap(m);
-      uint64_t *fullb = &bar[lane == 0 ? kXFull : (lane == 1 ? kYFull : kWFull)], *emptyb = fullb + 4;
-      const int head = h / (lane == 0 ? r.xg : (lane == 1 ? r.yg : r.wg));
-      const int slots = lane == 0 ? Ly::kXSlots : (lane == 1 ? Ly::kYSlots : Ly::kWSlots);
-      const int bytes = lane == 2 ? Ly::kWTile : Ly::kTile, box = lane == 2 ? kAtom : kBox;
-      const int boxes = bytes / box, x0 = lane == 2 ? e0 : 0, dx = lane == 2 ? 32 : 64;
-      const int sharers = lane == 2 ? 1 : r.Dw / SW, mine = lane == 2 ? 0 : slice;
-      uint8_t *ring = sm + (lane == 0 ? Ly::kX : (lane == 1 ? Ly::kY : Ly::kW));
-      auto place = [&](int j, int t) { return at[0] == j ? head : (at[1] == j ? t : b); };
-      int issued = 0;
-      for (int c = 0; c < nc; ++c) {
-        const int sl = c % slots;
-        if (!mbar_wait(&emptyb[sl], ((c / slots) & 1) ^ 1, abort_flag, p.timeouts)) break;
-        const int t0 = first(c);
-        mbar_arrive_expect_tx(&fullb[sl], bytes);
+    // The warp as one for all rings, the leader's copies by predicate (see
+    // mma_group).  Each wait is for groups that need earlier loads alone: in turn x
+    // of chunk c and, where they have more slots, y and w of later chunks.
+    const uint32_t leader = elect_one();
+    struct Ring {
+      const CUtensorMap *m;
+      const uint8_t *at;
+      uint64_t *full;
+      int sm, head, slots, boxes, box, x0, dx, ahead;
+    };
+    const Ring rings[3] = {
+        {&map.m[0], map.at[0], &bar[kXFull], Ly::kX, h / r.xg, Ly::kXSlots, DX / 64, kBox, 0, 64, 0},
+        {&map.m[1], map.at[1], &bar[kYFull], Ly::kY, h / r.yg, Ly::kYSlots, DX / 64, kBox, 0, 64,
+         STATE ? 0 : Ly::kYSlots - Ly::kXSlots},
+        {&map.m[2], map.at[2], &bar[kWFull], Ly::kW, h / r.wg, Ly::kWSlots, SW / 32, kAtom, e0, 32,
+         STATE ? 0 : Ly::kWSlots - Ly::kXSlots}};
+    constexpr int kFirst = STATE ? 1 : 0;
+    int issued[3] = {0, 0, 0};
+    auto load = [&](const Ring &g, int c) {
+      const int sl = c % g.slots, t0 = first(c);
+      if (!held_wait(g.full + 4 + sl, ((c / g.slots) & 1) ^ 1, abort_flag, p.timeouts)) return false;
+      auto place = [&](int j) { return g.at[0] == j ? g.head : (g.at[1] == j ? t0 : b); };
+      const int y = place(0), z = place(1), w = place(2);
+      const uint32_t full = smem_u32(g.full + sl), dst = smem_u32(sm + g.sm + sl * g.boxes * g.box);
+      __syncwarp();
+      expect_tx(leader, full, g.boxes * g.box);
+#pragma unroll
+      for (int j = 0; j < g.boxes; ++j) load_box(leader, dst + j * g.box, g.m, g.x0 + g.dx * j, y, z, w, full);
+      return true;
+    };
+    bool ok = true;
+    for (int c = 0; ok && c < nc; ++c)
+#pragma unroll
+      for (int i = kFirst; i < 3; ++i)
 #pragma unroll 1
-        for (int j = 0; j < boxes; ++j)
-          tma_load_4d(ring + sl * bytes + j * box, m, x0 + dx * j, place(0, t0), place(1, t0), place(2, t0), &fullb[sl]);
-        // Later tiles come into L2 ahead, the boxes of x and y shared out among the
-        // slices that read them.
-        if (c + kAhead < nc) {
-          const int tp = first(c + kAhead);
-#pragma unroll 1
-          for (int j = 0; j < boxes; ++j)
-            if ((lane * boxes + j) % sharers == mine)
-              tma_prefetch_4d(m, x0 + dx * j, place(0, tp), place(1, tp), place(2, tp));
-        }
-        issued = c + 1;
-      }
-      if (*abort_flag)  // let every issued copy land before the CTA exits
-        for (int c = issued > slots ? issued - slots : 0; c < issued; ++c)
-          mbar_wait_drain(&fullb[c % slots], (c / slots) & 1);
-    }
+        for (; ok && issued[i] <= c + rings[i].ahead && issued[i] < nc; ++issued[i])
+          if (!load(rings[i], issued[i])) {
+            ok = false;
+            break;
+          }
+    if (*abort_flag)  // let every issued copy land before the CTA exits
+#pragma unroll
+      for (int i = kFirst; i < 3; ++i)
+        for (int c = max(0, issued[i] - rings[i].slots); c < issued[i]; ++c)
+          mbar_wait_drain(rings[i].full + c % rings[i].slots, (c / rings[i].slots) & 1);
     __syncwarp();
   } else if (warp >= kWarpMma) {
     const uint32_t base = smem_u32(sm);
@@ -333,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       return l < 0 || held_wait(&bar[kORead + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts);
     };
     auto o_at = [&](int c) { return tmem + Ly::cO + (Ly::kO == 2 && (c & 1) ? Ly::cOBuf : 0u); };
+    const uint32_t leader = elect_one();
     if (warp == kWarpMma) {
       // R of a chunk ahead of O2 of the one before, so that P works behind O2
       if (!STATE) {
@@ -343,27 +377,23 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
             // rows behind the end have to be zero first
             if (!x_landed(c) || !y_landed(c) || (size(c) < kC && !w_ready(c))) break;
             tc_fence_after();
-            if (elect_one()) {
-              mma_group<DX / 16, false, 0, 0>(tmem + Ly::cR + 128 * (c & 1), rows(Ly::kX + xs(c) * Ly::kTile),
-                                              rows(Ly::kY + ys(c) * Ly::kTile), ID_R);
-              mma_commit(&bar[kRFull + (c & 1)]);
-              mma_commit(&bar[kXEmpty + xs(c)]);
-              mma_commit(&bar[kYEmpty + ys(c)]);
-            }
             __syncwarp();
+            mma_group<DX / 16, false, 0, 0>(leader, tmem + Ly::cR + 128 * (c & 1), rows(Ly::kX + xs(c) * Ly::kTile),
+                                            rows(Ly::kY + ys(c) * Ly::kTile), ID_R);
+            commit(leader, &bar[kRFull + (c & 1)]);
+            commit(leader, &bar[kXEmpty + xs(c)]);
+            commit(leader, &bar[kYEmpty + ys(c)]);
           }
           if (c > 0) {
             const int l = c - 1;
             if (!w_ready(l) || !o_free(l) || !held_wait(&bar[kPReady + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts))
               break;
             tc_fence_after();
-            if (elect_one()) {
-              mma_group_p<kC / 16, 64>(o_at(l) + 2 * SW, tmem + Ly::cR + 128 * (l & 1),
-                                       atoms(Ly::kW + l % Ly::kWSlots * Ly::kWTile, kAtom), ID_O2);
-              mma_commit(&bar[kOFull + (l & 1)]);
-              mma_commit(&bar[kWEmpty + l % Ly::kWSlots]);
-            }
             __syncwarp();
+            mma_group_p<kC / 16, 64>(leader, o_at(l) + 2 * SW, tmem + Ly::cR + 128 * (l & 1),
+                                     atoms(Ly::kW + l % Ly::kWSlots * Ly::kWTile, kAtom), ID_O2);
+            commit(leader, &bar[kOFull + (l & 1)]);
+            commit(leader, &bar[kWEmpty + l % Ly::kWSlots]);
           }
         }
       }
@@ -376,39 +406,33 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         if (!STATE) {
           if (!x_landed(c) || !o_free(c) || !held_wait(&bar[kSReady], c & 1, abort_flag, p.timeouts)) break;
           tc_fence_after();
-          if (elect_one()) {
-            mma_group<DX / 16, false, 0, 64>(o_at(c), rows(Ly::kX + xs(c) * Ly::kTile), atoms(Ly::kSop, Ly::kSopAtom),
-                                             ID_O1);
-            mma_commit(&bar[kOFull + sl]);
-            mma_commit(&bar[kXEmpty + xs(c)]);
-          }
           __syncwarp();
+          mma_group<DX / 16, false, 0, 64>(leader, o_at(c), rows(Ly::kX + xs(c) * Ly::kTile), atoms(Ly::kSop, Ly::kSopAtom),
+                                           ID_O1);
+          commit(leader, &bar[kOFull + sl]);
+          commit(leader, &bar[kXEmpty + xs(c)]);
         } else if (c > 1 && !held_wait(&bar[kDRead + sl], ((c - 2) >> 1) & 1, abort_flag, p.timeouts)) {
           break;  // dS of two chunks ago has been read
         }
         if (!y_landed(c) || !w_ready(c)) break;
         tc_fence_after();
-        if (elect_one()) {
-          if (STATE || c + 1 < nc) {
-            const uint64_t yt = smem_desc(base + Ly::kY + ys(c) * Ly::kTile, kBox, 1024, kSw128);
-            const uint64_t wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
-            const uint32_t d = tmem + Ly::cD + (STATE && sl ? Ly::cD2 : 0u);
-            mma_group<kC / 16, false, 128, 64>(d, yt, wt, ID_D);
-            if (NS == 3)  // the smallest values into the same sums as the second
-              mma_group<kC / 16, true, 128, 64>(d + SW, yt, wt + (2 * Ly::kWTile >> 4), ID_D3);
-          }
-          mma_commit(&bar[kDFull + sl]);
-          mma_commit(&bar[kYEmpty + ys(c)]);
-          if (STATE) mma_commit(&bar[kWEmpty + c % Ly::kWSlots]);
-        }
         __syncwarp();
+        if (STATE || c + 1 < nc) {
+          const uint64_t yt = smem_desc(base + Ly::kY + ys(c) * Ly::kTile, kBox, 1024, kSw128);
+          const uint64_t wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
+          const uint32_t d = tmem + Ly::cD + (STATE && sl ? Ly::cD2 : 0u);
+          mma_group<kC / 16, false, 128, 64>(leader, d, yt, wt, ID_D);
+          if (NS == 3)  // the smallest values into the same sums as the second
+            mma_group<kC / 16, true, 128, 64>(leader, d + SW, yt, wt + (2 * Ly::kWTile >> 4), ID_D3);
+        }
+        commit(leader, &bar[kDFull + sl]);
+        commit(leader, &bar[kYEmpty + ys(c)]);
+        if (STATE) commit(leader, &bar[kWEmpty + c % Ly::kWSlots]);
       }
     }
     // every MMA issued has completed before TMEM is released
-    if (elect_one()) {
-      mma_commit(&bar[kDrain + warp - kWarpMma]);
-      mbar_wait_drain(&bar[kDrain + warp - kWarpMma], 0);
-    }
+    commit(leader, &bar[kDrain + warp - kWarpMma]);
+    mbar_wait_drain(&bar[kDrain + warp - kWarpMma], 0);
     __syncwarp();
   } else if (warp >= kWarpW || (STATE && warp < kWarpS)) {
     // a third of the columns each where the warps that weigh have nothing to do
