@@ -109,7 +109,6 @@ enum Bar : int {
 
 struct TcRole {
   CUtensorMap m[3];  // x, y, w
-  uint8_t at[3][4];  // places of head, token and batch among each map's outer dimensions
 };
 struct TcParams {
   RetArgs a;
@@ -204,13 +203,13 @@ __device__ __forceinline__ void expect_tx(uint32_t leader, uint32_t bar, uint32_
       "r"(bytes), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
-                                         uint32_t bar) {
+__device__ __forceinline__ void load_tile(uint32_t leader, uint32_t dst, const CUtensorMap *map, int token, int atom,
+                                          int head, int batch, uint32_t bar) {
   asm volatile(
       "{\n .reg .pred e;\n setp.ne.b32 e, %7, 0;\n"
-      " @e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(leader)
+      " @e cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {0, %2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(token), "r"(atom), "r"(head), "r"(batch), "r"(bar), "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ uint32_t elect_one() {
@@ -309,28 +308,23 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     const uint32_t leader = elect_one();
     struct Ring {
       const CUtensorMap *m;
-      const uint8_t *at;
       uint64_t *full;
-      int sm, head, slots, boxes, box, x0, dx, ahead;
+      int sm, head, slots, bytes, atom, ahead;
     };
     const Ring rings[3] = {
-        {&map.m[0], map.at[0], &bar[kXFull], Ly::kX, h / r.xg, Ly::kXSlots, DX / 64, kBox, 0, 64, 0},
-        {&map.m[1], map.at[1], &bar[kYFull], Ly::kY, h / r.yg, Ly::kYSlots, DX / 64, kBox, 0, 64,
-         STATE ? 0 : Ly::kYSlots - Ly::kXSlots},
-        {&map.m[2], map.at[2], &bar[kWFull], Ly::kW, h / r.wg, Ly::kWSlots, SW / 32, kAtom, e0, 32,
+        {&map.m[0], &bar[kXFull], Ly::kX, h / r.xg, Ly::kXSlots, Ly::kTile, 0, 0},
+        {&map.m[1], &bar[kYFull], Ly::kY, h / r.yg, Ly::kYSlots, Ly::kTile, 0, STATE ? 0 : Ly::kYSlots - Ly::kXSlots},
+        {&map.m[2], &bar[kWFull], Ly::kW, h / r.wg, Ly::kWSlots, Ly::kWTile, e0 / 32,
          STATE ? 0 : Ly::kWSlots - Ly::kXSlots}};
     constexpr int kFirst = STATE ? 1 : 0;
     int issued[3] = {0, 0, 0};
     auto load = [&](const Ring &g, int c) {
-      const int sl = c % g.slots, t0 = first(c);
+      const int sl = c % g.slots;
       if (!held_wait(g.full + 4 + sl, ((c / g.slots) & 1) ^ 1, abort_flag, p.timeouts)) return false;
-      auto place = [&](int j) { return g.at[0] == j ? g.head : (g.at[1] == j ? t0 : b); };
-      const int y = place(0), z = place(1), w = place(2);
-      const uint32_t full = smem_u32(g.full + sl), dst = smem_u32(sm + g.sm + sl * g.boxes * g.box);
+      const uint32_t full = smem_u32(g.full + sl);
       __syncwarp();
-      expect_tx(leader, full, g.boxes * g.box);
-#pragma unroll
-      for (int j = 0; j < g.boxes; ++j) load_box(leader, dst + j * g.box, g.m, g.x0 + g.dx * j, y, z, w, full);
+      expect_tx(leader, full, g.bytes);
+      load_tile(leader, smem_u32(sm + g.sm + sl * g.bytes), g.m, first(c), g.atom, g.head, b, full);
       return true;
     };
     bool ok = true;
@@ -587,7 +581,43 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     uint8_t *out = static_cast<uint8_t *>(r.o);
     const int wide = r.o_f32 ? 4 : 2;  // bytes of an output
     const int64_t unit = b * r.os.b + h * r.os.h + e0 + SW / 2 * h2;
+    // the next chunk's weights first: O2 of this one waits for its own
     for (int c = -1; c < nc; ++c) {
+      const int l = c + 1;  // weights of the next chunk
+      if (l < nc) {
+        if (!held_wait(&bar[kRFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) break;
+        tc_fence_after();
+        const uint32_t raw = quad + Ly::cR + 128 * (l & 1);
+  #pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // half of a block: 16 columns
+          const int g = h2 + (i & 2), half = i & 1, away = rev ? g - qd : qd - g;
+          uint32_t pk[8];
+          if (away >= 0) {
+            const float4 *w4 = reinterpret_cast<const float4 *>(tab + ((away > 0 ? 32 : 0) + lane) * Ly::kLdT + 16 * half);
+            const f2 far = dup2(away > 1 ? exp2f(lg * static_cast<float>(32 * (away - 1))) : 1.f);
+            float a[16];
+            tmem_ld16(raw + 32 * g + 16 * half, a);
+            tmem_wait_ld();
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 w = w4[e];
+              const float2 lo = unpack2(mul2(mul2(far, pack2(w.x, w.y)), pack2(a[4 * e], a[4 * e + 1])));
+              const float2 hi = unpack2(mul2(mul2(far, pack2(w.z, w.w)), pack2(a[4 * e + 2], a[4 * e + 3])));
+              pk[2 * e] = pack_bf16x2(lo.x, lo.y);
+              pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
+            }
+          } else {
+  #pragma unroll
+            for (int e = 0; e < 8; ++e) pk[e] = 0u;
+          }
+          // the second half's P lies over the first half's raw weights, read already
+          tmem_st8u(raw + 32 * g + 8 * half, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kPReady + (l & 1)]);
+      }
       if (c >= 0) {  // outputs of chunk c
         const int nv = size(c);
         const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
@@ -630,40 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           }
         }
       }
-      const int l = c + 1;  // weights of the next chunk
-      if (l == nc) break;
-      if (!held_wait(&bar[kRFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) break;
-      tc_fence_after();
-      const uint32_t raw = quad + Ly::cR + 128 * (l & 1);
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {  // half of a block: 16 columns
-        const int g = h2 + (i & 2), half = i & 1, away = rev ? g - qd : qd - g;
-        uint32_t pk[8];
-        if (away >= 0) {
-          const float4 *w4 = reinterpret_cast<const float4 *>(tab + ((away > 0 ? 32 : 0) + lane) * Ly::kLdT + 16 * half);
-          const f2 far = dup2(away > 1 ? exp2f(lg * static_cast<float>(32 * (away - 1))) : 1.f);
-          float a[16];
-          tmem_ld16(raw + 32 * g + 16 * half, a);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 w = w4[e];
-            const float2 lo = unpack2(mul2(mul2(far, pack2(w.x, w.y)), pack2(a[4 * e], a[4 * e + 1])));
-            const float2 hi = unpack2(mul2(mul2(far, pack2(w.z, w.w)), pack2(a[4 * e + 2], a[4 * e + 3])));
-            pk[2 * e] = pack_bf16x2(lo.x, lo.y);
-            pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pk[e] = 0u;
-        }
-        // the second half's P lies over the first half's raw weights, read already
-        tmem_st8u(raw + 32 * g + 8 * half, pk);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[kPReady + (l & 1)]);
     }
     if (p.a.fill && last_part)
       for (int i = tokens + t; i < p.a.L; i += kC) {
@@ -759,11 +755,11 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
       const RetRole &r = a.role[i];
       if (r.Dx != DX) continue;
       TcRole &m = p.map[p.a.roles];
-      auto encode = [&](int i, const void *base, int width, int group, const RetStrides &s, int box) {
-        return make_tmap_heads(&m.m[i], base, width, a.H / group, a.L, a.B, s.h, s.t, s.b, box, kC, m.at[i]);
+      auto encode = [&](int i, const void *base, int width, int group, const RetStrides &s, int atom, int atoms) {
+        return make_tmap_atoms(&m.m[i], base, width, a.H / group, a.L, a.B, s.h, s.t, s.b, atom, atoms, kC);
       };
-      if (!encode(0, r.x, DX, r.xg, r.xs, 64) || !encode(1, r.y, DX, r.yg, r.ys, 64) ||
-          !encode(2, r.w, r.Dw, r.wg, r.ws, 32))
+      if (!encode(0, r.x, DX, r.xg, r.xs, 64, DX / 64) || !encode(1, r.y, DX, r.yg, r.ys, 64, DX / 64) ||
+          !encode(2, r.w, r.Dw, r.wg, r.ws, 32, SW / 32))
         return cudaErrorNotSupported;
       p.a.role[p.a.roles++] = r;
       if (r.Dw / SW > p.slices) p.slices = r.Dw / SW;

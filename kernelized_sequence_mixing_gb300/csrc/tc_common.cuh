@@ -411,14 +411,14 @@ bool make_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t dim_x, uint6
 bool make_tmap_rows(CUtensorMap *map, const void *base, int elem_bytes, uint64_t width,
                     uint64_t rows, uint64_t batch, uint64_t ld, uint32_t box_x, uint32_t box_y);
 
-// Host: encode a rank-4 bf16 map over rows of `width` elements per (head, token,
-// batch), strides in elements, box of box_x columns of box_t tokens, swizzle of
-// box_x * 2 bytes (64 or 128), zero fill out of bounds.  The map's outer
-// dimensions go by their strides; at[0..2] receive the places (0 to 2) of head,
-// token and batch among them.
-bool make_tmap_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t tokens,
-                     uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride,
-                     uint32_t box_x, uint32_t box_t, uint8_t *at);
+// Host: encode a rank-5 bf16 map over rows of `width` elements per (head, token,
+// batch), strides in elements: coordinates (0, token, atom, head, batch) with atoms
+// of `atom` columns (32 or 64, the swizzle being as wide), boxes of `tokens_box`
+// tokens and `atoms_box` atoms, which land one atom behind the other.  Zero fill
+// out of bounds.
+bool make_tmap_atoms(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t tokens,
+                     uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride, uint32_t atom,
+                     uint32_t atoms_box, uint32_t tokens_box);
 
 // Host: device address of the wait-timeout counter on the current device
 // (nullptr if it cannot be obtained).

@@ -65,26 +65,18 @@ bool make_tmap_rows(CUtensorMap *map, const void *base, int elem_bytes, uint64_t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_tmap_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t tokens,
-                     uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride,
-                     uint32_t box_x, uint32_t box_t, uint8_t *at) {
+bool make_tmap_atoms(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t tokens,
+                     uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride, uint32_t atom,
+                     uint32_t atoms_box, uint32_t tokens_box) {
   auto fn = encode_fn();
-  if (!fn || (box_x != 32 && box_x != 64)) return false;
-  const uint64_t size[3] = {heads, tokens, batch};
-  const int64_t stride[3] = {head_stride, token_stride, batch_stride};
-  cuuint64_t dims[4] = {width}, strides[3];
-  cuuint32_t box[4] = {box_x, 1, 1, 1};
-  for (int i = 0; i < 3; ++i) {
-    int place = 0;
-    for (int j = 0; j < 3; ++j) place += stride[j] < stride[i] || (stride[j] == stride[i] && j < i);
-    at[i] = static_cast<uint8_t>(place);
-    dims[1 + place] = size[i];
-    strides[place] = static_cast<cuuint64_t>(stride[i]) * 2;
-    if (i == 1) box[1 + place] = box_t;
-  }
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+  if (!fn || (atom != 32 && atom != 64) || width % atom != 0) return false;
+  const cuuint64_t dims[5] = {atom, tokens, width / atom, heads, batch};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(token_stride) * 2, atom * 2,
+                                 static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(batch_stride) * 2};
+  const cuuint32_t box[5] = {atom, tokens_box, atoms_box, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, atom == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
