@@ -22,16 +22,19 @@
 //
 // Warp roles (19 warps):
 //   0-7    P: powers of the decay, mask, bf16 (a lane quadrant and two of its
-//          four blocks of 32 columns each); then half of the output columns of
-//          the quadrant's tokens
+//          four blocks of 32 columns each); with slices of 64 columns also the
+//          output rows, half the columns each
 //   8-11   state: registers, its bf16 values for the MMA (thread = row)
-//   12-15  w~ (thread = token), and zeros behind a ragged sequence's end
+//   12-15  w~ (thread = token), and zeros behind a ragged sequence's end; with
+//          slices of 32 columns also the output rows
 //   16     TMA: rings of x, y and w
 //   17     TMEM owner, issues R and O2
 //   18     issues O1 and dS: one warp's instructions for all four (some 500 a
 //          chunk) take longer than the products
 // Every wait is bounded; a CTA that gives up counts the failure in device
 // memory, drains its copies and MMAs, frees tensor memory and exits.
+#include <type_traits>
+
 #include "common.cuh"
 #include "mixer_common.cuh"
 #include "retention.cuh"
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       mbar_init(&bar[kDRead + s], 4);
       mbar_init(&bar[kPReady + s], 8);
       mbar_init(&bar[kOFull + s], 2);
-      mbar_init(&bar[kORead + s], 8);
+      mbar_init(&bar[kORead + s], SW == 32 ? 4 : 8);  // the warps that write outputs
     }
     mbar_init(&bar[kSReady], 4);
     mbar_init(&bar[kDrain], 1);
@@ -300,6 +303,65 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
+
+  // Output columns [col, col + 16 N) of the rows of a lane quadrant.
+  auto outputs = [&](int c, int qd, int col, auto pieces) {
+    constexpr int N = decltype(pieces)::value;
+    const int nv = size(c), t = 32 * qd + lane, wide = r.o_f32 ? 4 : 2;
+    const float f = r.out_scale * exp2f(lg * static_cast<float>(r.reverse ? nv - 1 - t : t + 1));
+    uint8_t *at = static_cast<uint8_t *>(r.o) + (b * r.os.b + h * r.os.h + e0 + col + (first(c) + t) * r.os.t) * wide;
+    if (!held_wait(&bar[kOFull + (c & 1)], (c >> 1) & 1, abort_flag, p.timeouts)) return false;
+    tc_fence_after();
+    const uint32_t o = tmem_addr(tmem, 32 * qd, Ly::cO + (Ly::kO == 2 && (c & 1) ? Ly::cOBuf : 0u) + col);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float hi[16], lo[16], v[16];
+      tmem_ld16(o + 16 * j, hi);
+      tmem_ld16(o + 16 * j + SW, lo);
+      tmem_ld16(o + 16 * j + 2 * SW, v);
+      tmem_wait_ld();
+      if (j == N - 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(&bar[kORead + (c & 1)]);
+      }
+      if (t < nv) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
+        if (r.o_f32) {
+          float4 *to = reinterpret_cast<float4 *>(at + 64 * j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else {
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+          // whole 32-byte sectors where the rows lie on them (191 us against 210)
+          if (p.sectors) {
+            st_global_v8(at + 32 * j, pk);
+          } else {
+            uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
+            to[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            to[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          }
+        }
+      }
+    }
+    return true;
+  };
+  // Zeros behind a sequence's end.
+  auto fill = [&](int t, int col, int cols) {
+    if (!p.a.fill || !last_part) return;
+    const int wide = r.o_f32 ? 4 : 2;
+    uint8_t *out = static_cast<uint8_t *>(r.o) + (b * r.os.b + h * r.os.h + e0 + col) * wide;
+    for (int i = tokens + t; i < p.a.L; i += kC) {
+      uint4 *to = reinterpret_cast<uint4 *>(out + i * r.os.t * wide);
+      for (int e = 0; e < cols * wide / 16; ++e) to[e] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  // Outputs are the work of the warps that have time for it: with slices of 32
+  // columns those of w~, with 64 those of P, half the columns each.
+  constexpr bool kOutW = SW == 32;
 
   if (warp == kWarpTma) {
     // The warp as one for all rings, the leader's copies by predicate (see
@@ -431,7 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   } else if (warp >= kWarpW || (STATE && warp < kWarpS)) {
     // a third of the columns each where the warps that weigh have nothing to do
     const int t = tid & (kC - 1), group = STATE && warp >= kWarpW ? 2 : warp >> 2 & 1, groups = STATE ? 3 : 1;
-    for (int c = 0; c < nc; ++c) {
+    for (int c = 0; c <= nc; ++c) {
+      if (c == nc) {
+        if (!STATE && kOutW && c > 0) outputs(c - 1, warp - kWarpW, 0, std::integral_constant<int, SW / 16>{});
+        break;
+      }
       const int ws = c % Ly::kWSlots, ys = c % Ly::kYSlots, nv = size(c);
       const float f = t < nv ? exp2f(lg * static_cast<float>(r.reverse ? t + 1 : nv - 1 - t)) : 0.f;
       // the buffer is free once the sum over the chunk that used it is done
@@ -471,7 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[kWReady + (c & 3)]);
+      if (!STATE && kOutW && c > 0 && !outputs(c - 1, warp - kWarpW, 0, std::integral_constant<int, SW / 16>{})) break;
     }
+    if (!STATE && kOutW) fill(t, 0, SW);
   } else if (warp >= kWarpS) {
     // row d of the state: all 32 lanes of a quadrant, or (64 features) 16
     const int qd = warp - kWarpS;
@@ -573,14 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       }
     }
   } else if (!STATE) {
-    // P: rows of quadrant qd, blocks of 32 columns h2 and h2 + 2; output columns
-    // [SW / 2 h2, + SW / 2)
+    // P: rows of quadrant qd, blocks of 32 columns h2 and h2 + 2
     const int qd = warp & 3, h2 = warp >> 2, t = 32 * qd + lane;
     const bool rev = r.reverse;
     const uint32_t quad = tmem_addr(tmem, 32 * qd, 0);
-    uint8_t *out = static_cast<uint8_t *>(r.o);
-    const int wide = r.o_f32 ? 4 : 2;  // bytes of an output
-    const int64_t unit = b * r.os.b + h * r.os.h + e0 + SW / 2 * h2;
     // the next chunk's weights first: O2 of this one waits for its own
     for (int c = -1; c < nc; ++c) {
       const int l = c + 1;  // weights of the next chunk
@@ -588,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         if (!held_wait(&bar[kRFull + (l & 1)], (l >> 1) & 1, abort_flag, p.timeouts)) break;
         tc_fence_after();
         const uint32_t raw = quad + Ly::cR + 128 * (l & 1);
-  #pragma unroll 1
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {  // half of a block: 16 columns
           const int g = h2 + (i & 2), half = i & 1, away = rev ? g - qd : qd - g;
           uint32_t pk[8];
@@ -598,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
             float a[16];
             tmem_ld16(raw + 32 * g + 16 * half, a);
             tmem_wait_ld();
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float4 w = w4[e];
               const float2 lo = unpack2(mul2(mul2(far, pack2(w.x, w.y)), pack2(a[4 * e], a[4 * e + 1])));
@@ -607,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
               pk[2 * e + 1] = pack_bf16x2(hi.x, hi.y);
             }
           } else {
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 8; ++e) pk[e] = 0u;
           }
           // the second half's P lies over the first half's raw weights, read already
@@ -618,54 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[kPReady + (l & 1)]);
       }
-      if (c >= 0) {  // outputs of chunk c
-        const int nv = size(c);
-        const float f = r.out_scale * exp2f(lg * static_cast<float>(rev ? nv - 1 - t : t + 1));
-        uint8_t *at = out + (unit + (first(c) + t) * r.os.t) * wide;
-        if (!held_wait(&bar[kOFull + (c & 1)], (c >> 1) & 1, abort_flag, p.timeouts)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < SW / 32; ++j) {
-          float hi[16], lo[16], v[16];
-          const uint32_t o = quad + Ly::cO + (Ly::kO == 2 && (c & 1) ? Ly::cOBuf : 0u) + SW / 2 * h2 + 16 * j;
-          tmem_ld16(o, hi);
-          tmem_ld16(o + SW, lo);
-          tmem_ld16(o + 2 * SW, v);
-          tmem_wait_ld();
-          if (j == SW / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_relaxed(&bar[kORead + (c & 1)]);
-          }
-          if (t < nv) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = fmaf(f, hi[e] + lo[e], r.out_scale * v[e]);
-            if (r.o_f32) {
-              float4 *to = reinterpret_cast<float4 *>(at + 64 * j);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            } else {
-              uint32_t pk[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-              // whole 32-byte sectors where the rows lie on them (191 us against 210)
-              if (p.sectors) {
-                st_global_v8(at + 32 * j, pk);
-              } else {
-                uint4 *to = reinterpret_cast<uint4 *>(at + 32 * j);
-                to[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                to[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-              }
-            }
-          }
-        }
-      }
+      if (!kOutW && c >= 0 && !outputs(c, qd, SW / 2 * h2, std::integral_constant<int, SW / 32>{})) break;
     }
-    if (p.a.fill && last_part)
-      for (int i = tokens + t; i < p.a.L; i += kC) {
-        uint4 *to = reinterpret_cast<uint4 *>(out + (unit + i * r.os.t) * wide);
-        for (int e = 0; e < wide * SW / 32; ++e) to[e] = make_uint4(0, 0, 0, 0);
-      }
+    if (!kOutW) fill(t, SW / 2 * h2, SW / 2);
   }
   __syncwarp();
   tc_fence_before();
