@@ -60,9 +60,9 @@ struct Lay {
   static constexpr int kWTile = SW / 32 * kAtom;
   // Loads take 2000 cycles and more from issue to landing when all SMs stream, so
   // as many slots as fit; y is held longer than x, w longest.
-  static constexpr int kSumSlots = DX == 128 && SW == 64 && NS == 3 ? 2 : 4;
-  static constexpr int kXSlots = 2, kYSlots = STATE ? kSumSlots : (SW == 32 ? 3 : 2);
-  static constexpr int kWSlots = STATE ? kSumSlots : (SW == 32 ? 4 : 2);
+  static constexpr bool kTight = DX == 128 && SW == 64 && NS == 3;
+  static constexpr int kXSlots = 2, kYSlots = STATE ? (kTight ? 3 : 4) : (SW == 32 ? 3 : 2);
+  static constexpr int kWSlots = STATE ? (kTight ? 2 : 4) : (SW == 32 ? 4 : 2);
   static constexpr int kX = 0;
   static constexpr int kY = STATE ? 0 : kXSlots * kTile;
   static constexpr int kW = kY + kYSlots * kTile;
@@ -81,12 +81,12 @@ struct Lay {
   static_assert(kAlloc <= 227 * 1024, "shared memory");
   // Tensor memory columns: two buffers of raw weights, in each block of 32
   // columns then P as bf16 pairs in the first 16; kO buffers of O1, with both
-  // values of the state side by side, and O2; dS of w~1 and of the others (twice in
-  // the pass that only sums states).
-  static constexpr int kO = SW == 32 ? 2 : 1, kDParts = NS == 1 ? 1 : 2;
+  // values of the state side by side, and O2; dS, of each value of w~ (twice in the
+  // pass that only sums states).
+  static constexpr int kO = SW == 32 ? 2 : 1;
   static constexpr uint32_t cR = 0, cO = 256, cOBuf = 3 * SW;
-  static constexpr uint32_t cD = STATE ? 0 : cO + kO * cOBuf, cD2 = kDParts * SW;
-  static_assert(cD + (STATE ? 2 : 1) * kDParts * SW <= 512, "tensor memory");
+  static constexpr uint32_t cD = STATE ? 0 : cO + kO * cOBuf, cD2 = NS * SW;
+  static_assert(cD + (STATE ? 2 : 1) * NS * SW <= 512, "tensor memory");
 };
 
 // Each phase of a barrier is seen by every waiter before the phase after next of
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       }
     } else {
       constexpr uint32_t ID_O1 = idesc_bf16(128, 2 * SW, false, true);
-      constexpr uint32_t ID_D = idesc_bf16(DX, Ly::kDParts * SW, true, true), ID_D3 = idesc_bf16(DX, SW, true, true);
+      constexpr uint32_t ID_D = idesc_bf16(DX, NS * SW, true, true);
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
         const int sl = c & 1;
@@ -478,8 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           const uint64_t wt = atoms(Ly::kWt + (STATE ? sl * Ly::kWtBuf : 0), kAtom);
           const uint32_t d = tmem + Ly::cD + (STATE && sl ? Ly::cD2 : 0u);
           mma_group<kC / 16, false, 128, 64>(leader, d, yt, wt, ID_D);
-          if (NS == 3)  // the smallest values into the same sums as the second
-            mma_group<kC / 16, true, 128, 64>(leader, d + SW, yt, wt + (2 * Ly::kWTile >> 4), ID_D3);
         }
         commit(leader, &bar[kDFull + sl]);
         commit(leader, &bar[kYEmpty + ys(c)]);
@@ -598,14 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         const uint32_t at = tmem_addr(tmem, 32 * qd, Ly::cD + (STATE && (l & 1) ? Ly::cD2 : 0u));
 #pragma unroll
         for (int j = 0; j < SW / 16; ++j) {
-          float x[Ly::kDParts][16];
+          float x[NS][16];
 #pragma unroll
-          for (int k = 0; k < Ly::kDParts; ++k) tmem_ld16(at + SW * k + 16 * j, x[k]);
+          for (int k = 0; k < NS; ++k) tmem_ld16(at + SW * k + 16 * j, x[k]);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            f2 v = pack2(x[0][2 * e], x[0][2 * e + 1]);
-            if (NS > 1) v = add2(v, pack2(x[Ly::kDParts - 1][2 * e], x[Ly::kDParts - 1][2 * e + 1]));
+            f2 v = pack2(x[NS - 1][2 * e], x[NS - 1][2 * e + 1]);
+#pragma unroll
+            for (int k = NS - 2; k >= 0; --k) v = add2(v, pack2(x[k][2 * e], x[k][2 * e + 1]));
             S[8 * j + e] = fma2(g, S[8 * j + e], v);
           }
         }
