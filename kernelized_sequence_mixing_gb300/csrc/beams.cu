@@ -11,9 +11,10 @@
 // of the sorted lists.  Bound by HBM (the logits are read once) with one
 // exponential per logit beside it (16 a clock and SM).
 //
-// The n largest of a piece: the n-th largest of the threads' own maxima bounds
-// the n-th largest value from below (n <= threads), and what is not below that
-// bound is collected, in expectation little more than n values.  Many equal
+// The n largest of a piece: the n-th largest of the maxima of 32 or 128 groups of
+// threads bounds the n-th largest value from below, and what is not below that
+// bound is collected, in expectation little more than n values (with the maxima of
+// all 256 threads, ranked by all of them, a piece took five times as long).  Many equal
 // logits can be more than the buffer holds; then the list is taken value by
 // value (n rounds of a maximum over the CTA).
 //
@@ -21,6 +22,8 @@
 // states of all K beams of a request: it loads the parents' before it stores
 // any, so the states move in place, without a second buffer and without a
 // barrier; beams that keep their own state are neither read nor written.
+#include <float.h>
+
 #include <float.h>
 
 #include "common.cuh"
@@ -52,21 +55,22 @@ struct SelectParams {
   int pieces;  // of a row
 };
 
+// 16 bytes of logits: how many, the pattern of -inf, and their values.
 template <typename T>
 struct vec16;
 template <>
 struct vec16<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void get(const float *p, float *x) {
-    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  static constexpr uint32_t kNone = 0xff800000u;
+  static __device__ __forceinline__ void get(const uint4 &v, float *x) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
 };
 template <>
 struct vec16<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void get(const __nv_bfloat16 *p, float *x) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ void get(const uint4 &v, float *x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -79,9 +83,9 @@ struct vec16<__nv_bfloat16> {
 // A piece is VALUES values per thread, in 16-byte groups dealt out to the
 // threads in turn, from the row's first 16-byte boundary at or in front of it.
 template <typename T, int VALUES>
-__global__ void __launch_bounds__(kThreads) beams_piece_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kN = vec16<T>::kN, kGroups = VALUES / kN;
-  __shared__ float top[kThreads];
+  __shared__ float top[128];
   __shared__ float kept[kKept];
   __shared__ int place[kKept];
   __shared__ float warp_max[kThreads / 32], warp_sum[kThreads / 32], bound;
@@ -94,42 +98,61 @@ __global__ void __launch_bounds__(kThreads) beams_piece_kernel(const __grid_cons
   const int V = p.a.V, n = p.a.n;
   const int64_t base = static_cast<int64_t>(piece) * kThreads * VALUES - skew;  // of this piece in the row
   if (tid == 0) count = 0;
+  // all loads under way before the first value is used; groups across the row's
+  // ends (only of rows off the 16-byte boundary) one by one behind them
+  uint4 raw[kGroups];
+  auto at = [&](int g) { return base + (static_cast<int64_t>(g) * kThreads + tid) * kN; };
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    raw[g] = make_uint4(vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone);
+    if (at(g) >= 0 && at(g) + kN <= V) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(x + at(g)));
+  }
   float v[VALUES];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    const int64_t at = base + (static_cast<int64_t>(g) * kThreads + tid) * kN;
-    if (at >= 0 && at + kN <= V) {
-      vec16<T>::get(x + at, v + g * kN);
-    } else {
+    vec16<T>::get(raw[g], v + g * kN);
+    if ((at(g) < 0 && at(g) + kN > 0) || (at(g) < V && at(g) + kN > V)) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[g * kN + i] = at + i >= 0 && at + i < V ? io<T>::load(x + at + i) : -INFINITY;
+      for (int i = 0; i < kN; ++i) v[g * kN + i] = at(g) + i >= 0 && at(g) + i < V ? io<T>::load(x + at(g) + i) : -INFINITY;
     }
   }
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VALUES; ++i) m = fmaxf(m, v[i]);
-  top[tid] = m;
-  float wm = m;
+  // maxima of groups of 8 threads (n up to 16) or 2: 32 or 128 groups
+  const int few = n <= 16, groups = few ? 32 : 128;
+  float gm = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+  if (few) {
+    gm = fmaxf(gm, __shfl_xor_sync(~0u, gm, 2));
+    gm = fmaxf(gm, __shfl_xor_sync(~0u, gm, 4));
+  }
+  if ((tid & (few ? 7 : 1)) == 0) top[tid >> (few ? 3 : 1)] = gm;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(~0u, wm, o));
-  if (lane == 0) warp_max[warp] = wm;
+  for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(~0u, gm, o));
+  if (lane == 0) warp_max[warp] = gm;
   __syncthreads();
   float all = warp_max[0];
 #pragma unroll
   for (int i = 1; i < kThreads / 32; ++i) all = fmaxf(all, warp_max[i]);
-  // rank of this thread's maximum among the threads'
-  int rank = 0;
-  for (int i = 0; i < kThreads; i += 4) {
-    const float4 o = *reinterpret_cast<const float4 *>(top + i);
-    rank += ahead(o.x, i, m, tid) + ahead(o.y, i + 1, m, tid) + ahead(o.z, i + 2, m, tid) + ahead(o.w, i + 3, m, tid);
+  if (tid < groups) {  // rank of a group's maximum among the groups'
+    const float own = top[tid];
+    int rank = 0;
+    for (int i = 0; i < groups; i += 4) {
+      const float4 o = *reinterpret_cast<const float4 *>(top + i);
+      rank += ahead(o.x, i, own, tid) + ahead(o.y, i + 1, own, tid) + ahead(o.z, i + 2, own, tid) +
+              ahead(o.w, i + 3, own, tid);
+    }
+    if (rank == n - 1) bound = fmaxf(own, -FLT_MAX);  // -inf is no continuation
   }
-  if (rank == n - 1) bound = m;
-  float sum = 0.f;
+  f2 sums = dup2(0.f);
   if (all > -INFINITY) {
     // the difference first: it is exact where it matters, near the maximum
+    const f2 off = dup2(-all), l2e = dup2(kLog2e);
 #pragma unroll
-    for (int i = 0; i < VALUES; ++i) sum += exp2f((v[i] - all) * kLog2e);
-  } else {
+    for (int i = 0; i < VALUES; i += 2) sums = add2(sums, ex2_2(mul2(add2(pack2(v[i], v[i + 1]), off), l2e)));
+  }
+  float sum = sum2(sums);
+  if (!(all > -INFINITY)) {
 #pragma unroll
     for (int i = 0; i < VALUES; ++i)
       if (v[i] != v[i]) sum = v[i];
@@ -139,17 +162,19 @@ __global__ void __launch_bounds__(kThreads) beams_piece_kernel(const __grid_cons
   if (lane == 0) warp_sum[warp] = sum;
   __syncthreads();
   const float least = bound;
+  if (m >= least) {  // few threads
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g)
+    for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (v[g * kN + i] >= least && v[g * kN + i] > -INFINITY) {
-        const int to = atomicAdd(&count, 1);
-        if (to < kKept) {
-          kept[to] = v[g * kN + i];
-          place[to] = static_cast<int>(base + (static_cast<int64_t>(g) * kThreads + tid) * kN + i);
+      for (int i = 0; i < kN; ++i)
+        if (v[g * kN + i] >= least) {
+          const int to = atomicAdd(&count, 1);
+          if (to < kKept) {
+            kept[to] = v[g * kN + i];
+            place[to] = static_cast<int>(at(g)) + i;
+          }
         }
-      }
+  }
   __syncthreads();
   float *value = p.out.value + static_cast<int64_t>(blockIdx.x) * n;
   int *index = p.out.index + static_cast<int64_t>(blockIdx.x) * n;
@@ -180,15 +205,15 @@ __global__ void __launch_bounds__(kThreads) beams_piece_kernel(const __grid_cons
       for (int g = 0; g < kGroups; ++g)
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const int at = static_cast<int>(base + (static_cast<int64_t>(g) * kThreads + tid) * kN + i);
+          const int here = static_cast<int>(at(g)) + i;
           const float a = v[g * kN + i];
-          if (ahead(last, at_last, a, at) && ahead(a, at, best, at_best)) best = a, at_best = at;
+          if (ahead(last, at_last, a, here) && ahead(a, here, best, at_best)) best = a, at_best = here;
         }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const float a = __shfl_xor_sync(~0u, best, o);
-        const int at = __shfl_xor_sync(~0u, at_best, o);
-        if (ahead(a, at, best, at_best)) best = a, at_best = at;
+        const int there = __shfl_xor_sync(~0u, at_best, o);
+        if (ahead(a, there, best, at_best)) best = a, at_best = there;
       }
       __syncthreads();
       if (lane == 0) kept[warp] = best, place[warp] = at_best;
@@ -284,12 +309,14 @@ __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_const
     const int v = p.out.index[at];
     return v < 0 ? Cand{nothing, INT64_MAX} : Cand{key_of(off + p.out.value[at]), row | v};
   };
-  // one entry per thread: as deep into the lists as there are threads for, or
-  // the best head of several lists
+  // one entry per thread: so deep into the lists that there are 4 n, or the best
+  // head of several lists
   int64_t mine = nothing;
+  int some = kThreads;
   if (lists < kThreads) {
-    const int i = tid / lists;
-    if (i < n && i < kThreads / lists) mine = entry(tid % lists, i).key;
+    const int deep = min(min(n, (4 * n + lists - 1) / lists), kThreads / lists);
+    some = max(lists * deep, n);
+    if (tid < lists * deep) mine = entry(tid % lists, tid / lists).key;
   } else {
     for (int l = tid; l < lists; l += kThreads) {
       const int64_t h = entry(l, 0).key;
@@ -298,9 +325,11 @@ __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_const
   }
   heads[tid] = mine;
   __syncthreads();
-  int rank = 0;
-  for (int i = 0; i < kThreads; ++i) rank += heads[i] > mine || (heads[i] == mine && i < tid);
-  if (rank == n - 1) bound = mine;
+  if (tid < some) {
+    int rank = 0;
+    for (int i = 0; i < some; ++i) rank += heads[i] > mine || (heads[i] == mine && i < tid);
+    if (rank == n - 1) bound = mine;
+  }
   __syncthreads();
   const int64_t least = bound;
   for (int l = tid; l < lists; l += kThreads)
