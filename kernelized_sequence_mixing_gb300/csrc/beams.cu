@@ -96,29 +96,36 @@ __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_c
   const T *x = static_cast<const T *>(p.a.logits) + row * p.a.ld;
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kN);  // values in front of the row
   const int V = p.a.V, n = p.a.n;
-  const int64_t base = static_cast<int64_t>(piece) * kThreads * VALUES - skew;  // of this piece in the row
+  const int base = piece * (kThreads * VALUES) - skew;  // of this piece in the row (V is at most 2^30)
   if (tid == 0) count = 0;
   // all loads under way before the first value is used; groups across the row's
   // ends (only of rows off the 16-byte boundary) one by one behind them
   uint4 raw[kGroups];
-  auto at = [&](int g) { return base + (static_cast<int64_t>(g) * kThreads + tid) * kN; };
+  auto at = [&](int g) { return base + (g * kThreads + tid) * kN; };
+  const bool inside = base >= 0 && base + kThreads * VALUES <= V;  // the whole piece
+  if (inside) {
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    raw[g] = make_uint4(vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone);
-    if (at(g) >= 0 && at(g) + kN <= V) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(x + at(g)));
+    for (int g = 0; g < kGroups; ++g) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(x + at(g)));
+  } else {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      raw[g] = make_uint4(vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone);
+      if (at(g) >= 0 && at(g) + kN <= V) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(x + at(g)));
+    }
   }
-  float v[VALUES];
+  float v[VALUES], most[kGroups], m = -INFINITY;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     vec16<T>::get(raw[g], v + g * kN);
-    if ((at(g) < 0 && at(g) + kN > 0) || (at(g) < V && at(g) + kN > V)) {
+    if (!inside && ((at(g) < 0 && at(g) + kN > 0) || (at(g) < V && at(g) + kN > V))) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) v[g * kN + i] = at(g) + i >= 0 && at(g) + i < V ? io<T>::load(x + at(g) + i) : -INFINITY;
     }
-  }
-  float m = -INFINITY;
+    most[g] = v[g * kN];
 #pragma unroll
-  for (int i = 0; i < VALUES; ++i) m = fmaxf(m, v[i]);
+    for (int i = 1; i < kN; ++i) most[g] = fmaxf(most[g], v[g * kN + i]);
+    m = fmaxf(m, most[g]);
+  }
   // maxima of groups of 8 threads (n up to 16) or 2: 32 or 128 groups
   const int few = n <= 16, groups = few ? 32 : 128;
   float gm = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
@@ -164,16 +171,18 @@ __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_c
   const float least = bound;
   if (m >= least) {  // few threads
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
+    for (int g = 0; g < kGroups; ++g) {
+      if (!(most[g] >= least)) continue;
 #pragma unroll
       for (int i = 0; i < kN; ++i)
         if (v[g * kN + i] >= least) {
           const int to = atomicAdd(&count, 1);
           if (to < kKept) {
             kept[to] = v[g * kN + i];
-            place[to] = static_cast<int>(at(g)) + i;
+            place[to] = at(g) + i;
           }
         }
+    }
   }
   __syncthreads();
   float *value = p.out.value + static_cast<int64_t>(blockIdx.x) * n;
@@ -205,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_c
       for (int g = 0; g < kGroups; ++g)
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const int here = static_cast<int>(at(g)) + i;
+          const int here = at(g) + i;
           const float a = v[g * kN + i];
           if (ahead(last, at_last, a, here) && ahead(a, here, best, at_best)) best = a, at_best = here;
         }
@@ -243,8 +252,16 @@ __device__ __forceinline__ int64_t key_of(double v) {
 }
 __device__ __forceinline__ double score_of(int64_t key) { return __longlong_as_double(key < 0 ? key ^ INT64_MAX : key); }
 
+// log t to about 2^-23, absolutely: the fp32 logarithm, off by its own rounding,
+// and one step of Newton's method (64-bit logarithms take microseconds here).
+__device__ __forceinline__ double log_of(double t) {
+  const float tf = static_cast<float>(t), y = logf(tf);
+  return static_cast<double>(y) + fmaf(tf, expf(-y), -1.f);
+}
+
 constexpr int kCand = 1024;  // candidates of a request that are ranked at once
 constexpr int kMaxBeams = 32;
+constexpr int kHeld = 2048;  // entries of lists that shared memory holds
 
 // A continuation: its score's key, and beam and token as one number of the
 // order in which ties go.
@@ -261,19 +278,31 @@ __device__ __forceinline__ bool ahead(const Cand &a, const Cand &b) {
 // n-th largest bounds the n-th best continuation; and the candidates that are
 // not below it, ranked.
 __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ double offset[kMaxBeams];
+  __shared__ double offset[kMaxBeams], lse[kMaxBeams];
   __shared__ uint8_t done[kMaxBeams];
   __shared__ Cand cand[kCand];
   __shared__ int64_t heads[kThreads];
   __shared__ Cand best[kThreads / 32];
   __shared__ int64_t bound;
   __shared__ int count;
+  __shared__ float held_value[kHeld];
+  __shared__ int held_index[kHeld];
   const int K = p.a.K, n = p.a.n, pieces = p.pieces, lists = K * pieces;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t first = static_cast<int64_t>(b) * lists;
   const int64_t nothing = key_of(-INFINITY);
   if (tid == 0) count = 0;
+  // what the pass before does not write, ahead of the wait for it
+  const float own_score = tid < K ? p.a.scores[static_cast<int64_t>(b) * K + tid] : 0.f;
+  const bool own_done = tid < K && p.a.finished && p.a.finished[static_cast<int64_t>(b) * K + tid];
   wait_for_previous();
+  const bool held = lists * n <= kHeld;
+  if (held)
+    for (int i = tid; i < lists * n; i += kThreads) {
+      held_value[i] = p.out.value[first * n + i];
+      held_index[i] = p.out.index[first * n + i];
+    }
+  if (tid < K) done[tid] = own_done;
   for (int k = warp; k < K; k += kThreads / 32) {
     const float2 *s = p.out.sum + first + static_cast<int64_t>(k) * pieces;
     float m = -INFINITY;
@@ -288,13 +317,12 @@ __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_const
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-    if (lane == 0) {
-      const float sc = p.a.scores[static_cast<int64_t>(b) * K + k];
-      const bool d = p.a.finished && p.a.finished[static_cast<int64_t>(b) * K + k];
-      const double lse = d ? 0.0 : m + log(t);
-      done[k] = d;
-      offset[k] = isfinite(sc) && isfinite(lse) ? sc - lse : -INFINITY;
-    }
+    if (lane == 0) lse[k] = m + log_of(t);
+  }
+  __syncthreads();
+  if (tid < K) {
+    const double l = own_done ? 0.0 : lse[tid];
+    offset[tid] = isfinite(own_score) && isfinite(l) ? own_score - l : -INFINITY;
   }
   __syncthreads();
   // entry i of list l (a finished beam has one, its end token at no cost, in
@@ -305,9 +333,10 @@ __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_const
     if (!(off > -INFINITY)) return {nothing, INT64_MAX};
     const int64_t row = static_cast<int64_t>(k) << 32;
     if (done[k]) return l == k * pieces && i == 0 ? Cand{key_of(off), row | p.a.eos} : Cand{nothing, INT64_MAX};
-    const int64_t at = (first + l) * n + i;
-    const int v = p.out.index[at];
-    return v < 0 ? Cand{nothing, INT64_MAX} : Cand{key_of(off + p.out.value[at]), row | v};
+    const int in = l * n + i;
+    const int v = held ? held_index[in] : p.out.index[first * n + in];
+    if (v < 0) return {nothing, INT64_MAX};
+    return {key_of(off + (held ? held_value[in] : p.out.value[first * n + in])), row | v};
   };
   // one entry per thread: so deep into the lists that there are 4 n, or the best
   // head of several lists
