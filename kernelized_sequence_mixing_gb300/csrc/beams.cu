@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_c
     for (int i = 1; i < kN; ++i) most[g] = fmaxf(most[g], v[g * kN + i]);
     m = fmaxf(m, most[g]);
   }
-  // maxima of groups of 8 threads (n up to 16) or 2: 32 or 128 groups
-  const int few = n <= 16, groups = few ? 32 : 128;
+  // maxima of groups of 8 threads (n up to 32) or 2: 32 or 128 groups
+  const bool few = n <= 32;
   float gm = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
   if (few) {
     gm = fmaxf(gm, __shfl_xor_sync(~0u, gm, 2));
@@ -141,16 +141,30 @@ __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_c
   float all = warp_max[0];
 #pragma unroll
   for (int i = 1; i < kThreads / 32; ++i) all = fmaxf(all, warp_max[i]);
-  if (tid < groups) {  // rank of a group's maximum among the groups'
-    const float own = top[tid];
-    int rank = 0;
-    for (int i = 0; i < groups; i += 4) {
-      const float4 o = *reinterpret_cast<const float4 *>(top + i);
-      rank += ahead(o.x, i, own, tid) + ahead(o.y, i + 1, own, tid) + ahead(o.z, i + 2, own, tid) +
-              ahead(o.w, i + 3, own, tid);
+  float least;
+  if (few) {
+    // every warp sorts the 32 maxima over its lanes: no warp waits for another
+    float own = top[lane];
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        const float other = __shfl_xor_sync(~0u, own, j);
+        const bool larger = ((lane & j) == 0) == ((lane & k) == 0 || k == 32);
+        own = larger ? fmaxf(own, other) : fminf(own, other);
+      }
+    least = __shfl_sync(~0u, own, n - 1);
+  } else {
+    if (tid < 128) {  // rank of a group's maximum among the groups'
+      const float own = top[tid];
+      int rank = 0;
+      for (int i = 0; i < 128; ++i) rank += ahead(top[i], i, own, tid);
+      if (rank == n - 1) bound = own;
     }
-    if (rank == n - 1) bound = fmaxf(own, -FLT_MAX);  // -inf is no continuation
+    __syncthreads();
+    least = bound;
   }
+  least = fmaxf(least, -FLT_MAX);  // -inf is no continuation
   f2 sums = dup2(0.f);
   if (all > -INFINITY) {
     // the difference first: it is exact where it matters, near the maximum
@@ -167,8 +181,6 @@ __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_c
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   if (lane == 0) warp_sum[warp] = sum;
-  __syncthreads();
-  const float least = bound;
   if (m >= least) {  // few threads
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
