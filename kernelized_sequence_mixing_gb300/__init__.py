@@ -1147,17 +1147,23 @@ def reorder_states(states, parents):
         raise ValueError(f"{fn}: expected parents: [B, K]")
     B, K = parents.shape
     _expect(fn, "parents", parents, (B, K), torch.int32)
+    index, rows = parents.get_device(), max(1, B * K)
+    ptrs, sizes, one = [], [], index >= 0
     for i, t in enumerate(tensors):
-        _contig(f"states[{i}]", t)
-        if t.shape[:2] != (B, K) and (t.dim() < 1 or t.shape[0] != B * K):
-            raise ValueError(f"{fn}: states[{i}] must be [{B}, {K}, ...] or [{B * K}, ...], got {tuple(t.shape)}")
+        shape = t.shape
+        if not t.is_contiguous() or not shape or (shape[0] != B * K and shape[:2] != parents.shape):
+            _contig(f"states[{i}]", t)
+            raise ValueError(f"{fn}: states[{i}] must be [{B}, {K}, ...] or [{B * K}, ...], got {tuple(shape)}")
+        one = one and t.get_device() == index
+        ptrs.append(t.data_ptr())
+        sizes.append(t.nbytes // rows)
     _c_ints(fn, B, K)
-    dev = _one_device(fn, [("parents", parents)] + [(f"states[{i}]", t) for i, t in enumerate(tensors)])
+    if not one:  # finds the tensor that is elsewhere
+        _one_device(fn, [("parents", parents)] + [(f"states[{i}]", t) for i, t in enumerate(tensors)])
+    dev, count = parents.device, len(tensors)
     lib = load_library()
-    count = len(tensors)
-    rows = max(1, B * K)
-    ptrs = (ctypes.c_void_p * count)(*[t.data_ptr() for t in tensors])
-    sizes = (ctypes.c_longlong * count)(*[t.numel() * t.element_size() // rows for t in tensors])
     with _on(dev):
-        _check("la_reorder_states", lib.la_reorder_states(ptrs, sizes, count, _ptr(parents), B, K, _stream(dev)))
+        _check("la_reorder_states", lib.la_reorder_states(
+            (ctypes.c_void_p * count)(*ptrs), (ctypes.c_longlong * count)(*sizes), count, parents.data_ptr(), B, K,
+            _stream(dev)))
     return states

@@ -30,16 +30,22 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
                      __uint_as_float(r.y & 0xffff0000u));
 }
 
-// Rows [0, nv) of width W as feature-major columns; the rest of the chunk zero.
+// Four columns of a row, zero behind the end.
 template <typename T>
-__device__ __forceinline__ void load_turned(float *dst, const T *src, int64_t st, int W, int nv) {
-  const int t = threadIdx.x & (kC - 1), g = threadIdx.x >> 6;
-  for (int d = 4 * g; d < W; d += 4 * (kThreads / kC)) {
-    const float4 v = t < nv ? load4(src + t * st + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-    dst[d * kLd + t] = v.x;
-    dst[(d + 1) * kLd + t] = v.y;
-    dst[(d + 2) * kLd + t] = v.z;
-    dst[(d + 3) * kLd + t] = v.w;
+__device__ __forceinline__ float4 load_if(bool in, const T *p) {
+  return in ? load4(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+// A thread's share of 64 feature columns from d on (4 of each 16), for one token,
+// feature-major.
+__device__ __forceinline__ void store_turned(float *dst, const float4 *v, int t, int g, int d, int W) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = d + 4 * g + 16 * k;
+    if (c >= W) break;
+    dst[c * kLd + t] = v[k].x;
+    dst[(c + 1) * kLd + t] = v[k].y;
+    dst[(c + 2) * kLd + t] = v[k].z;
+    dst[(c + 3) * kLd + t] = v[k].w;
   }
 }
 
@@ -100,16 +106,35 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   for (int c = c0; c < c1; ++c) {
     const int t0 = (r.reverse ? n - 1 - c : c) * kC;
     const int nv = min(kC, tokens - t0);
-    if (!STATE) load_turned(xt, x + t0 * r.xs.t, r.xs.t, Dx, nv);
-    load_turned(yt, y + t0 * r.ys.t, r.ys.t, Dx, nv);
-    for (int i = tid; i < kC * SW / 4; i += kThreads) {
-      const int t = i / (SW / 4), e = 4 * (i % (SW / 4));
-      reinterpret_cast<float4 *>(w)[i] =
-          t < nv && e0 + e < Dw ? load4(wp + (t0 + t) * r.ws.t + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    {
+      // the loads of a round under way together: one by one their latency took
+      // half of the time
+      const int t = tid & (kC - 1), g = tid >> 6;
+      constexpr int kRows = kC * SW / 4 / kThreads;
+      float4 wv[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int at = tid + i * kThreads, row = at / (SW / 4), e = 4 * (at % (SW / 4));
+        wv[i] = load_if(row < nv && e0 + e < Dw, wp + (t0 + row) * r.ws.t + e);
+      }
+      for (int d = 0; d < Dx; d += 64) {
+        float4 xv[4], yv[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = d + 4 * g + 16 * k;
+          if (!STATE) xv[k] = load_if(t < nv && c < Dx, x + (t0 + t) * r.xs.t + c);
+          yv[k] = load_if(t < nv && c < Dx, y + (t0 + t) * r.ys.t + c);
+        }
+        if (!STATE) store_turned(xt, xv, t, g, d, Dx);
+        store_turned(yt, yv, t, g, d, Dx);
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) reinterpret_cast<float4 *>(w)[tid + i * kThreads] = wv[i];
     }
     __syncthreads();
     if (!STATE) {
       float a[4][4] = {};
+#pragma unroll 8
       for (int d = 0; d < Dx; ++d) {
         const Cols<4> u = cols<4>(xt + d * kLd + 4 * ty), v = cols<4>(yt + d * kLd + 4 * tx);
 #pragma unroll
@@ -129,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
       }
       __syncthreads();
       float o[4][CW] = {};
+#pragma unroll 8
       for (int d = 0; d < Dx; ++d) {
         const Cols<4> u = cols<4>(xt + d * kLd + 4 * ty);
         const Cols<CW> v = cols<CW>(S + d * SW + CW * tx);
@@ -144,7 +170,10 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < CW; ++j) o[i][j] *= f;
       }
-      for (int s = 0; s < kC; ++s) {
+      // the weights that are not masked, for the two groups of rows of a warp
+      const int s0 = r.reverse ? 4 * (ty & ~1) : 0, s1 = r.reverse ? kC : 4 * (ty | 1) + 4;
+#pragma unroll 8
+      for (int s = s0; s < s1; ++s) {
         const Cols<4> u = cols<4>(pt + s * kLd + 4 * ty);
         const Cols<CW> v = cols<CW>(w + s * SW + CW * tx);
 #pragma unroll
@@ -172,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
       const float gn = pw[nv];
       for (int d = 4 * ty; d < Dx; d += 64) {
         float s[4][CW] = {};
+#pragma unroll 2
         for (int j = 0; j < kC; j += 4) {
           Cols<4> u[4];
           Cols<CW> v[4];
