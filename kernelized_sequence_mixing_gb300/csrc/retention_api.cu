@@ -282,7 +282,7 @@ la_status_t la_reorder_states(void *const *states, const long long *bytes, int c
   if (!parents || (reinterpret_cast<uintptr_t>(parents) & 3u)) return LA_ERR_INVALID_ARG;
   for (int i = 0; i < count; ++i) {
     if (bytes[i] < 0 || (bytes[i] > 0 && !states[i])) return LA_ERR_INVALID_ARG;
-    if (bytes[i] >= ((int64_t)1 << 40)) return LA_ERR_UNSUPPORTED;
+    if (bytes[i] > ((int64_t)1 << 46) / rows) return LA_ERR_UNSUPPORTED;
     const Buf s = {states[i], (size_t)(rows * bytes[i]), false, true};
     if (overlap(s, pb)) return LA_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)

@@ -71,7 +71,10 @@ struct SimtParams {
   int parts, cpp, slices;  // cpp: chunks of a part; slices: of the widest role
 };
 
-int smem_floats(int Dx, int SW) { return 2 * Dx * kLd + Dx * SW + kC * SW + kC * kLd + 2 * kC; }
+// The pass that only sums states has no x and no weights.
+int smem_bytes(int Dx, int SW, bool state) {
+  return 4 * (Dx * kLd + Dx * SW + kC * SW + 2 * kC + (state ? 0 : Dx * kLd + kC * kLd));
+}
 
 // STATE: only the part's own state, into its record.
 template <typename T, int SW, bool STATE>
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   if (e0 >= r.Dw) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
   const int Dx = r.Dx, Dw = r.Dw;
-  float *xt = sm, *yt = xt + Dx * kLd, *S = yt + Dx * kLd, *w = S + Dx * SW, *pt = w + kC * SW, *pw = pt + kC * kLd;
+  float *yt = sm, *S = yt + Dx * kLd, *w = S + Dx * SW, *pw = w + kC * SW, *xt = pw + 2 * kC, *pt = xt + Dx * kLd;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int tokens = ret_tokens(p.a.lens, b, p.a.L);
   const int n = (tokens + kC - 1) / kC;
@@ -257,17 +260,18 @@ cudaError_t run(const RetArgs &a, int parts, int widest, int Dx, cudaStream_t s)
   SimtParams p = {a, parts, 0, (widest + SW - 1) / SW};
   const int chunks = (a.L + kC - 1) / kC;
   p.cpp = (chunks + parts - 1) / parts;
-  const int bytes = smem_floats(Dx, SW) * 4;
   const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
   if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
   if (parts > 1) {
     auto k = retention_simt_kernel<T, SW, true>;
+    const int bytes = smem_bytes(Dx, SW, true);
     cudaError_t e = allow_smem(k, bytes);
     if (e != cudaSuccess) return e;
     k<<<dim3(static_cast<unsigned>(units * (parts - 1)), 1, a.roles), kThreads, bytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   auto k = retention_simt_kernel<T, SW, false>;
+  const int bytes = smem_bytes(Dx, SW, false);
   const cudaError_t e = allow_smem(k, bytes);
   if (e != cudaSuccess) return e;
   k<<<dim3(static_cast<unsigned>(units * parts), 1, a.roles), kThreads, bytes, s>>>(p);
@@ -282,9 +286,40 @@ void widths(const RetArgs &a, int *Dx, int *Dw) {
   }
 }
 
-// Slices of 64 columns use each transposed load twice as often; above 128
-// features two tiles and the state no longer fit in shared memory with them.
-int slice_width(int Dx, int Dw) { return Dx > 128 || Dw <= 32 ? 32 : 64; }
+// How a call is cut: slices of SW columns and parts of the tokens.
+struct Cut {
+  int SW, parts;
+};
+
+// The cut that is done first by a model of the CTAs that an SM holds (by shared
+// memory, up to three): a chunk takes 1 unit of time with slices of 64 columns and
+// 0.8 with 32 (14 and 12 us of 64 features, alone on an SM), half of that where
+// states are summed, 0.35 more for each further CTA on the SM, and a CTA 1 unit to
+// begin and end.  Above 128 features slices of 64 columns do not fit.
+Cut cut_of(const RetArgs &a) {
+  int Dx, Dw;
+  widths(a, &Dx, &Dw);
+  const int chunks = (a.L + kC - 1) / kC;
+  Cut best = {32, 1};
+  double least = 1e300;
+  for (int SW = 32; SW <= (Dx > 128 || Dw <= 32 ? 32 : 64); SW += 32) {
+    const int64_t units = static_cast<int64_t>(a.B) * a.H * ((Dw + SW - 1) / SW) * a.roles;
+    auto time = [&](int64_t n, double chunk, bool state) {
+      int held = 227 * 1024 / (smem_bytes(Dx, SW, state) + 1024);
+      if (held > 3) held = 3;
+      if (n < static_cast<int64_t>(kSMs) * held) held = static_cast<int>((n + kSMs - 1) / kSMs);
+      const int64_t slots = static_cast<int64_t>(kSMs) * (held > 0 ? held : 1);
+      return static_cast<double>((n + slots - 1) / slots) * (chunk * (1 + 0.35 * (held - 1)) + 1);
+    };
+    for (int parts = 1; parts <= 32 && (parts == 1 || parts * 2 <= chunks); ++parts) {
+      const double chunk = ((chunks + parts - 1) / parts) * (SW == 64 ? 1.0 : 0.8);
+      double t = time(units * parts, chunk, false);
+      if (parts > 1) t += time(units * (parts - 1), 0.5 * chunk, true);
+      if (t < least) least = t, best = {SW, parts};
+    }
+  }
+  return best;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -305,24 +340,12 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-int ret_parts_simt(const RetArgs &a) {
-  int Dx, Dw;
-  widths(a, &Dx, &Dw);
-  const int SW = slice_width(Dx, Dw);
-  const int64_t units = static_cast<int64_t>(a.B) * a.H * ((Dw + SW - 1) / SW) * a.roles;
-  const int chunks = (a.L + kC - 1) / kC;
-  // parts cost a second pass over y and w for their records (about a third of
-  // the work), so only where they at least double the CTAs at work
-  const int64_t room = 2 * kSMs / (units > 0 ? units : 1);
-  int parts = static_cast<int>(room < 32 ? room : 32);
-  if (parts > chunks / 4) parts = chunks / 4;
-  return parts < 2 ? 1 : parts;
-}
+int ret_parts_simt(const RetArgs &a) { return cut_of(a).parts; }
 
 cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStream_t s) {
   int Dx, Dw;
   widths(a, &Dx, &Dw);
-  const bool wide = slice_width(Dx, Dw) == 64;
+  const bool wide = cut_of(a).SW == 64;
   if (dt == kF32) return wide ? run<float, 64>(a, parts, Dw, Dx, s) : run<float, 32>(a, parts, Dw, Dx, s);
   return wide ? run<__nv_bfloat16, 64>(a, parts, Dw, Dx, s) : run<__nv_bfloat16, 32>(a, parts, Dw, Dx, s);
 }
