@@ -329,10 +329,11 @@ struct RetRole {
   const float *start;
   float *end, *rec;  // rec: [B][H][records][Dx][Dw]
   int start_rs, start_cs;
+  int64_t state;  // elements between the states of start and end (Dx Dw, or more for a role of some features)
   float start_scale, end_scale, out_scale;
   int reverse, o_f32;
 };
-constexpr int kRetRoles = 3;
+constexpr int kRetRoles = 6;
 struct RetArgs {
   RetRole role[kRetRoles];
   int roles;
@@ -354,9 +355,16 @@ cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStr
 cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s);
 int ret_parts_simt(const RetArgs &a);
 int ret_parts_tc(const RetArgs &a);
-// out[row][h][e] = sum over the g heads of each group of part[row][h g + i][e]
-cudaError_t launch_group_sum(const float *part, void *out, int64_t rows, int heads, int g, int width, Dtype dt,
-                             cudaStream_t s);
+// out[b][t][h][e] = sum over the g shares of part[b][t][h g + i][e]; out with
+// strides of its own, rows behind lens left alone (lens null: none).
+struct GroupSumArgs {
+  const float *part;
+  void *out;
+  RetStrides os;
+  const int *lens;
+  int B, L, heads, g, width;
+};
+cudaError_t launch_group_sum(const GroupSumArgs &a, Dtype dt, cudaStream_t s);
 
 // One token of retention in place on states [slots][H][D][Dv] fp32: sequence b
 // has the state slots[b] (null: b); one outside [0, pool) is passed over.

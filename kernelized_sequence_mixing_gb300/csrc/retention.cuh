@@ -15,14 +15,23 @@
 //   dk: x = v,  y = do, w = q,  backward in time    state U_t^T
 //   dv: x = k,  y = q,  w = do, backward in time    state U_t
 //
-// where U_t = dL/dS_t / scale = g U_(t+1) + q_(t+1).. do_(t+1)^T g ... starts
-// from dL/dS behind the last token.  By chunks of C tokens, the state in front
-// of the chunk (in the direction of time) is carried and the rest is a masked
-// matrix of weights:  forward  g^(i+1) x_i S + sum_(j <= i) g^(i-j) ..., state
-// g^n S + sum_j g^(n-1-j) y_j w_j^T over the n tokens of the chunk; backward
-// g^(n-1-i) x_i U + sum_(j >= i) g^(j-i) ..., state g^n U + sum_j g^(j+1) y_j w_j^T
-// (U holds the gradient of the state in front of the chunk's first token, so
-// that a gradient of the final state meets the last token undecayed).
+// where U_t = dL/dS_t / scale = g U_(t+1) + q_t do_t^T, with dL/dS / scale of the
+// final state behind the last token.  By chunks of C tokens, the state in front of
+// the chunk (in the order of the pass) is carried and the rest is a masked matrix
+// of weights.  Over the n tokens of a chunk, forward in time:
+//
+//   o_i = scale (g^(i+1) x_i S + sum_(j <= i) g^(i-j) (x_i . y_j) w_j)
+//   S  <- g^n S + sum_j g^(n-1-j) y_j w_j^T
+//
+// and backward in time, U being the gradient of the state in front of the tokens
+// done so far (so that a gradient of the final state meets the last token
+// undecayed):
+//
+//   o_i = scale (g^(n-1-i) x_i U + sum_(j >= i) g^(j-i) (x_i . y_j) w_j)
+//   U  <- g^n U + sum_j g^(j+1) y_j w_j^T
+//
+// The product is linear in the features of x and y: 256 of them are two roles of
+// 128 whose outputs are added.
 #pragma once
 #include "kernels.h"
 
@@ -52,7 +61,7 @@ __device__ __forceinline__ float ret_start(const RetRole &r, const float *rec, i
   float s = 0.f;
   if (r.start)
     s = exp2f(lg * static_cast<float>(here)) * r.start_scale *
-        r.start[bh * r.Dx * r.Dw + static_cast<int64_t>(d) * r.start_rs + static_cast<int64_t>(e) * r.start_cs];
+        r.start[bh * r.state + static_cast<int64_t>(d) * r.start_rs + static_cast<int64_t>(e) * r.start_cs];
   for (int j = 0; j < part; ++j) {
     const int end = ret_before((j + 1) * cpp, n, tokens, C, r.reverse);
     s = fmaf(exp2f(lg * static_cast<float>(here - end)), rec[static_cast<int64_t>(j) * r.Dx * r.Dw + d * r.Dw + e], s);

@@ -80,6 +80,64 @@ bool lens_ok(const int *lens, int B, std::initializer_list<Buf> written) {
   return true;
 }
 
+// A call's roles with their outputs' shares: where query heads share a head of the
+// output (group) or the features are worked in two halves, each share goes to the
+// workspace in fp32 and the sums follow.
+struct Plan {
+  RetArgs a = {};
+  GroupSumArgs sum[3] = {};
+  int sums = 0;
+  size_t share = 0;  // floats of the workspace in front of the records
+
+  // r: o and os are the output's own; head h of the call writes head h / group.
+  void add(RetRole r, int group, bool halves, size_t es) {
+    const int n = halves ? 2 : 1;
+    const bool shares = group * n > 1;
+    r.state = (int64_t)r.Dx * r.Dw;
+    const int H = a.H, Dw = r.Dw;
+    if (shares) {
+      sum[sums++] = {nullptr, r.o, r.os, a.fill ? nullptr : a.lens, a.B, a.L, H / group, group * n, Dw};
+      r.os = {(int64_t)a.L * H * n * Dw, (int64_t)H * n * Dw, (int64_t)n * Dw};
+      r.o_f32 = 1;
+    }
+    r.Dx /= n;
+    for (int i = 0; i < n; ++i) {
+      RetRole &to = a.role[a.roles++];
+      to = r;
+      to.x = static_cast<const char *>(r.x) + i * r.Dx * es;
+      to.y = static_cast<const char *>(r.y) + i * r.Dx * es;
+      if (r.start) to.start = r.start + (int64_t)i * r.Dx * r.start_rs;
+      if (r.end) to.end = r.end + (int64_t)i * r.Dx * Dw;
+      // until the workspace is there: where in it
+      if (shares) to.o = reinterpret_cast<void *>((share + (size_t)i * Dw) * sizeof(float));
+    }
+    if (shares) {
+      sum[sums - 1].part = reinterpret_cast<const float *>(share * sizeof(float));
+      share += (size_t)a.B * a.L * H * n * Dw;
+    }
+  }
+
+  la_status_t run(Dtype dt, cudaStream_t s) {
+    const int parts = ret_parts(a, dt);
+    return with_workspace(sizeof(float) * (share + ret_record_floats(a, parts)), s, [&](void *ws) {
+      char *base = static_cast<char *>(ws);
+      for (int i = 0; i < a.roles; ++i)
+        if (a.role[i].o_f32) a.role[i].o = base + reinterpret_cast<size_t>(a.role[i].o);
+      ret_layout(&a, parts, static_cast<float *>(ws) + share);
+      cudaError_t e = launch_retention(a, dt, parts, s);
+      for (int i = 0; i < sums && e == cudaSuccess; ++i) {
+        GroupSumArgs g = sum[i];
+        g.part = reinterpret_cast<const float *>(base + reinterpret_cast<size_t>(g.part));
+        e = launch_group_sum(g, dt, s);
+      }
+      return e;
+    });
+  }
+};
+
+// Roles of 256 features in halves: where the halves run on the tensor cores.
+bool in_halves(int Dx, int Dw, la_dtype_t dt) { return dt == LA_BF16 && Dx == 256 && Dw % 32 == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -117,20 +175,13 @@ la_status_t la_forward_retention(const void *q, const void *k, const void *v, co
     if (!S0) return zero(S, state, cs);
     return status(cudaMemcpyAsync(S, S0, state, cudaMemcpyDeviceToDevice, cs));
   }
-  RetArgs a = {};
-  a.roles = 1;
-  a.role[0] = {q, k, v, o, s[0], s[1], s[2], s[3], 1, H / Hk, H / Hk, D, Dv, S0, S, nullptr, Dv, 1,
-               1.f, 1.f, scale, 0, 0};
-  a.lens = lens;
-  a.B = B, a.L = L, a.H = H;
-  a.fill = false;
-  a.lg = logs(g);
-  const Dtype dt = to_dtype(dtype);
-  const int parts = ret_parts(a, dt);
-  return with_workspace(sizeof(float) * ret_record_floats(a, parts), cs, [&](void *ws) {
-    ret_layout(&a, parts, static_cast<float *>(ws));
-    return launch_retention(a, dt, parts, cs);
-  });
+  Plan p;
+  p.a.lens = lens;
+  p.a.B = B, p.a.L = L, p.a.H = H;
+  p.a.lg = logs(g);
+  p.add({q, k, v, o, s[0], s[1], s[2], s[3], 1, H / Hk, H / Hk, D, Dv, S0, S, nullptr, Dv, 1, 0, 1.f, 1.f, scale, 0, 0},
+        1, in_halves(D, Dv, dtype), es);
+  return p.run(to_dtype(dtype), cs);
 }
 
 la_status_t la_backward_retention(const void *q, const void *k, const void *v, const void *dO,
@@ -174,39 +225,25 @@ la_status_t la_backward_retention(const void *q, const void *k, const void *v, c
     return status(cudaMemcpyAsync(dS0, dS, state, cudaMemcpyDeviceToDevice, cs));
   }
   const int group = H / Hk;
-  RetArgs a = {};
-  a.roles = 3;
-  const RetStrides dqs = dense(L, H, D), dks = dense(L, H, D), dvs = dense(L, H, Dv);
+  Plan p;
+  p.a.lens = lens;
+  p.a.B = B, p.a.L = L, p.a.H = H;
+  p.a.fill = lens != nullptr;
+  p.a.lg = logs(g);
+  // halves only where every role then runs on the tensor cores
+  auto fits = [](int Dx, int Dw) { return (Dx == 64 || Dx == 128 || Dx == 256) && Dw % 32 == 0; };
+  const bool tc = dtype == LA_BF16 && fits(D, Dv) && fits(Dv, D);
   // states of dq and dk are the transposes of S and U
-  a.role[0] = {dO, v, k, dq, s[3], s[2], s[1], dqs, 1, group, group, Dv, D, S0, nullptr, nullptr, 1, Dv,
-               1.f, 1.f, scale, 0, 0};
-  a.role[1] = {v, dO, q, dk, s[2], s[3], s[0], dks, group, 1, 1, Dv, D, dS, nullptr, nullptr, 1, Dv,
-               1.f / scale, 1.f, scale, 1, 0};
-  a.role[2] = {k, q, dO, dv, s[1], s[0], s[3], dvs, group, 1, 1, D, Dv, dS, dS0, nullptr, Dv, 1,
-               1.f / scale, scale, scale, 1, 0};
-  a.lens = lens;
-  a.B = B, a.L = L, a.H = H;
-  a.fill = lens != nullptr;
-  a.lg = logs(g);
-  const Dtype dt = to_dtype(dtype);
-  const int parts = ret_parts(a, dt);
-  const size_t rec = ret_record_floats(a, parts);
-  // shared heads: each query head's share in fp32, then their sums
-  const size_t share = group > 1 ? (size_t)rows * H * (D + Dv) : 0;
-  return with_workspace(sizeof(float) * (rec + share), cs, [&](void *ws) {
-    float *f = static_cast<float *>(ws);
-    ret_layout(&a, parts, f + share);
-    if (group > 1) {
-      a.role[1].o = f;
-      a.role[2].o = f + (size_t)rows * H * D;
-      a.role[1].o_f32 = a.role[2].o_f32 = 1;
-    }
-    cudaError_t e = launch_retention(a, dt, parts, cs);
-    if (group > 1 && e == cudaSuccess) e = launch_group_sum(f, dk, rows, Hk, group, D, dt, cs);
-    if (group > 1 && e == cudaSuccess)
-      e = launch_group_sum(f + (size_t)rows * H * D, dv, rows, Hk, group, Dv, dt, cs);
-    return e;
-  });
+  p.add({dO, v, k, dq, s[3], s[2], s[1], dense(L, H, D), 1, group, group, Dv, D, S0, nullptr, nullptr, 1, Dv, 0, 1.f,
+         1.f, scale, 0, 0},
+        1, tc && Dv == 256, es);
+  p.add({v, dO, q, dk, s[2], s[3], s[0], dense(L, Hk, D), group, 1, 1, Dv, D, dS, nullptr, nullptr, 1, Dv, 0,
+         1.f / scale, 1.f, scale, 1, 0},
+        group, tc && Dv == 256, es);
+  p.add({k, q, dO, dv, s[1], s[0], s[3], dense(L, Hk, Dv), group, 1, 1, D, Dv, dS, dS0, nullptr, Dv, 1, 0, 1.f / scale,
+         scale, scale, 1, 0},
+        group, tc && D == 256, es);
+  return p.run(to_dtype(dtype), cs);
 }
 
 la_status_t la_decode_retention(const void *q, const void *k, const void *v, float *S,

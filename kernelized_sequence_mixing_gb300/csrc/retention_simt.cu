@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   }
   __syncthreads();
   if (STATE || (part == p.parts - 1 && r.end)) {
-    float *out = STATE ? const_cast<float *>(rec) + static_cast<int64_t>(part) * Dx * Dw : r.end + bh * Dx * Dw;
+    float *out = STATE ? const_cast<float *>(rec) + static_cast<int64_t>(part) * Dx * Dw : r.end + bh * r.state;
     const float f = STATE ? 1.f : r.end_scale;
     for (int i = tid; i < Dx * SW; i += kThreads) {
       const int d = i / SW, e = e0 + i % SW;
@@ -322,18 +322,21 @@ Cut cut_of(const RetArgs &a) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
-    group_sum_kernel(const float *part, T *out, int64_t total, int g, int width) {
+__global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ GroupSumArgs a, int64_t total) {
   for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-    // four columns of one (row, group): the g heads of it lie behind one another
-    const int64_t rh = i / (width / 4);
-    const int e = static_cast<int>(i % (width / 4)) * 4;
+    // four columns of one output head: its shares lie behind one another
+    const int e = static_cast<int>(i % (a.width / 4)) * 4;
+    const int64_t rh = i / (a.width / 4);
+    const int h = static_cast<int>(rh % a.heads);
+    const int64_t row = rh / a.heads;
+    const int t = static_cast<int>(row % a.L), b = static_cast<int>(row / a.L);
+    if (t >= ret_tokens(a.lens, b, a.L)) continue;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < g; ++j) {
-      const float4 v = __ldcs(reinterpret_cast<const float4 *>(part + (rh * g + j) * width + e));
+    for (int j = 0; j < a.g; ++j) {
+      const float4 v = __ldcs(reinterpret_cast<const float4 *>(a.part + (rh * a.g + j) * a.width + e));
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    T *o = out + rh * width + e;
+    T *o = static_cast<T *>(a.out) + b * a.os.b + t * a.os.t + h * a.os.h + e;
     io<T>::store(o, s.x), io<T>::store(o + 1, s.y), io<T>::store(o + 2, s.z), io<T>::store(o + 3, s.w);
   }
 }
@@ -350,14 +353,12 @@ cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStr
   return wide ? run<__nv_bfloat16, 64>(a, parts, Dw, Dx, s) : run<__nv_bfloat16, 32>(a, parts, Dw, Dx, s);
 }
 
-cudaError_t launch_group_sum(const float *part, void *out, int64_t rows, int heads, int g, int width, Dtype dt,
-                             cudaStream_t s) {
-  const int64_t total = rows * heads * (width / 4);
+cudaError_t launch_group_sum(const GroupSumArgs &a, Dtype dt, cudaStream_t s) {
+  const int64_t total = static_cast<int64_t>(a.B) * a.L * a.heads * (a.width / 4);
   const int64_t want = (total + 255) / 256;
   const unsigned grid = static_cast<unsigned>(want < 8 * kSMs ? want : 8 * kSMs);
-  if (dt == kF32) group_sum_kernel<float><<<grid, 256, 0, s>>>(part, static_cast<float *>(out), total, g, width);
-  else
-    group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16 *>(out), total, g, width);
+  if (dt == kF32) group_sum_kernel<float><<<grid, 256, 0, s>>>(a, total);
+  else group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, total);
   return cudaGetLastError();
 }
 

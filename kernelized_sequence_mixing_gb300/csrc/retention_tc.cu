@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
       const int here = ret_before(part * p.cpp, n, tokens, kC, r.reverse);
       if (r.start) {
         const float f = exp2f(lg * static_cast<float>(here)) * r.start_scale;
-        const float *from = r.start + bh * size_of + static_cast<int64_t>(d) * r.start_rs +
+        const float *from = r.start + bh * r.state + static_cast<int64_t>(d) * r.start_rs +
                             static_cast<int64_t>(e0) * r.start_cs;
 #pragma unroll
         for (int e = 0; e < SW / 2; ++e)
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         // fp32 (w~ as three values), while this pass makes do with one
         const f2 f = dup2(exp2f(lg * static_cast<float>(tokens - here)) * r.end_scale), one = dup2(r.end_scale);
         const float4 *from = reinterpret_cast<const float4 *>(rec + part * size_of + d * r.Dw + e0);
-        float4 *to = reinterpret_cast<float4 *>(r.end + bh * size_of + d * r.Dw + e0);
+        float4 *to = reinterpret_cast<float4 *>(r.end + bh * r.state + d * r.Dw + e0);
 #pragma unroll
         for (int e = 0; e < SW / 4; ++e) {
           const float4 v = from[e];
