@@ -30,8 +30,8 @@
 //   o_i = scale (g^(n-1-i) x_i U + sum_(j >= i) g^(j-i) (x_i . y_j) w_j)
 //   U  <- g^n U + sum_j g^(j+1) y_j w_j^T
 //
-// The product is linear in the features of x and y: 256 of them are two roles of
-// 128 whose outputs are added.
+// The product is linear in the features of x and y: more than 128 of them are two
+// roles whose outputs are added.
 #pragma once
 #include "kernels.h"
 

@@ -81,8 +81,8 @@ bool lens_ok(const int *lens, int B, std::initializer_list<Buf> written) {
 }
 
 // A call's roles with their outputs' shares: where query heads share a head of the
-// output (group) or the features are worked in two halves, each share goes to the
-// workspace in fp32 and the sums follow.
+// output (group) or there are more than 128 features (the kernels' most: 128 of them
+// and then the rest), each share goes to the workspace in fp32 and the sums follow.
 struct Plan {
   RetArgs a = {};
   GroupSumArgs sum[3] = {};
@@ -90,8 +90,8 @@ struct Plan {
   size_t share = 0;  // floats of the workspace in front of the records
 
   // r: o and os are the output's own; head h of the call writes head h / group.
-  void add(RetRole r, int group, bool halves, size_t es) {
-    const int n = halves ? 2 : 1;
+  void add(RetRole r, int group, size_t es) {
+    const int Dx = r.Dx, n = Dx > 128 ? 2 : 1;
     const bool shares = group * n > 1;
     r.state = (int64_t)r.Dx * r.Dw;
     const int H = a.H, Dw = r.Dw;
@@ -100,14 +100,15 @@ struct Plan {
       r.os = {(int64_t)a.L * H * n * Dw, (int64_t)H * n * Dw, (int64_t)n * Dw};
       r.o_f32 = 1;
     }
-    r.Dx /= n;
     for (int i = 0; i < n; ++i) {
       RetRole &to = a.role[a.roles++];
+      const int64_t d = 128 * i;
       to = r;
-      to.x = static_cast<const char *>(r.x) + i * r.Dx * es;
-      to.y = static_cast<const char *>(r.y) + i * r.Dx * es;
-      if (r.start) to.start = r.start + (int64_t)i * r.Dx * r.start_rs;
-      if (r.end) to.end = r.end + (int64_t)i * r.Dx * Dw;
+      to.Dx = n == 1 ? Dx : i ? Dx - 128 : 128;
+      to.x = static_cast<const char *>(r.x) + d * es;
+      to.y = static_cast<const char *>(r.y) + d * es;
+      if (r.start) to.start = r.start + d * r.start_rs;
+      if (r.end) to.end = r.end + d * Dw;
       // until the workspace is there: where in it
       if (shares) to.o = reinterpret_cast<void *>((share + (size_t)i * Dw) * sizeof(float));
     }
@@ -134,9 +135,6 @@ struct Plan {
     });
   }
 };
-
-// Roles of 256 features in halves: where the halves run on the tensor cores.
-bool in_halves(int Dx, int Dw, la_dtype_t dt) { return dt == LA_BF16 && Dx == 256 && Dw % 32 == 0; }
 
 }  // namespace
 
@@ -180,7 +178,7 @@ la_status_t la_forward_retention(const void *q, const void *k, const void *v, co
   p.a.B = B, p.a.L = L, p.a.H = H;
   p.a.lg = logs(g);
   p.add({q, k, v, o, s[0], s[1], s[2], s[3], 1, H / Hk, H / Hk, D, Dv, S0, S, nullptr, Dv, 1, 0, 1.f, 1.f, scale, 0, 0},
-        1, in_halves(D, Dv, dtype), es);
+        1, es);
   return p.run(to_dtype(dtype), cs);
 }
 
@@ -230,19 +228,16 @@ la_status_t la_backward_retention(const void *q, const void *k, const void *v, c
   p.a.B = B, p.a.L = L, p.a.H = H;
   p.a.fill = lens != nullptr;
   p.a.lg = logs(g);
-  // halves only where every role then runs on the tensor cores
-  auto fits = [](int Dx, int Dw) { return (Dx == 64 || Dx == 128 || Dx == 256) && Dw % 32 == 0; };
-  const bool tc = dtype == LA_BF16 && fits(D, Dv) && fits(Dv, D);
   // states of dq and dk are the transposes of S and U
   p.add({dO, v, k, dq, s[3], s[2], s[1], dense(L, H, D), 1, group, group, Dv, D, S0, nullptr, nullptr, 1, Dv, 0, 1.f,
          1.f, scale, 0, 0},
-        1, tc && Dv == 256, es);
+        1, es);
   p.add({v, dO, q, dk, s[2], s[3], s[0], dense(L, Hk, D), group, 1, 1, Dv, D, dS, nullptr, nullptr, 1, Dv, 0,
          1.f / scale, 1.f, scale, 1, 0},
-        group, tc && Dv == 256, es);
+        group, es);
   p.add({k, q, dO, dv, s[1], s[0], s[3], dense(L, Hk, Dv), group, 1, 1, D, Dv, dS, dS0, nullptr, Dv, 1, 0, 1.f / scale,
          scale, scale, 1, 0},
-        group, tc && D == 256, es);
+        group, es);
   return p.run(to_dtype(dtype), cs);
 }
 

@@ -1,11 +1,17 @@
 // Retention on CUDA cores in fp32: fp32 inputs, and the widths that the
-// tensor-core kernel does not take.
+// tensor-core kernel does not take.  Roles of up to 128 features.
 //
-// One CTA works a slice of SW columns of w over a part of the tokens, by
-// chunks of 64: x and y lie transposed in shared memory (feature-major), so
-// that every product reads float4 along the tokens; the state of the slice
-// stays in shared memory.  Bound by the fp32 pipe and by shared memory (two
-// 16-byte loads for 16 multiply-adds a thread).
+// One CTA works a slice of SW columns of w over a part of the tokens, by chunks of
+// 64 in the order of the pass (a pass backward in time loads its rows turned
+// round, so that every chunk looks forward).  Per chunk and thread:
+//
+//   weights x y^T and x S in one pass over the features (4 x 4 and 4 x CW of them
+//   from the same x), blocks of 16 x 16 behind the diagonal left out;
+//   weights times w from shared memory; the decayed y^T w into the state, which
+//   stays in registers and goes to shared memory once a chunk for x S.
+//
+// The next chunk's rows travel meanwhile (fp32 by cp.async, bf16 in registers).
+// Bound by the fp32 pipe and by the latency of shared memory at 8 or 16 warps an SM.
 #include "common.cuh"
 #include "mixer_common.cuh"
 #include "retention.cuh"
@@ -14,40 +20,8 @@ namespace linattn {
 namespace {
 
 constexpr int kC = 64;
-constexpr int kLd = kC + 4;  // floats between feature rows
+constexpr int kLdP = kC + 4;  // floats between rows of weights
 constexpr int kThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) {
-  return *reinterpret_cast<const float4 *>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-  const uint2 r = *reinterpret_cast<const uint2 *>(p);
-  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                     __uint_as_float(r.y & 0xffff0000u));
-}
-
-// Four columns of a row, zero behind the end.
-template <typename T>
-__device__ __forceinline__ float4 load_if(bool in, const T *p) {
-  return in ? load4(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-// A thread's share of 64 feature columns from d on (4 of each 16), for one token,
-// feature-major.
-__device__ __forceinline__ void store_turned(float *dst, const float4 *v, int t, int g, int d, int W) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = d + 4 * g + 16 * k;
-    if (c >= W) break;
-    dst[c * kLd + t] = v[k].x;
-    dst[(c + 1) * kLd + t] = v[k].y;
-    dst[(c + 2) * kLd + t] = v[k].z;
-    dst[(c + 3) * kLd + t] = v[k].w;
-  }
-}
 
 template <int N>
 struct Cols {
@@ -65,22 +39,84 @@ __device__ __forceinline__ Cols<N> cols(const float *p) {
   }
   return r;
 }
+template <int N>
+__device__ __forceinline__ void put(float *p, const float *v) {
+  if constexpr (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+template <int N>
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float *v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<__nv_bfloat162 *>(p + i) = __floats2bfloat162_rn(v[i], v[i + 1]);
+}
+
+// Rows of a chunk on their way to shared memory: 16 bytes a piece, 1 << sh pieces a
+// row (of those, the ones below width), rows from nv on zero.  N: pieces of a thread.
+template <typename T, int N>
+struct Rows;
+template <int N>
+struct Rows<float, N> {
+  __device__ __forceinline__ void begin(const float *from, int64_t stride, int t0, int nv, bool turned, int sh,
+                                        int width, float *to, int ld) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * kThreads, row = i >> sh, col = (i & ((1 << sh) - 1)) * 4;
+      if (row >= kC) break;
+      const bool in = row < nv && col < width;
+      const int t = t0 + (in ? (turned ? nv - 1 - row : row) : 0);
+      if (col < ld) copy16_async(to + row * ld + col, from + t * stride + (in ? col : 0), in);
+    }
+  }
+  __device__ __forceinline__ void settle(int, float *, int) {}
+};
+template <int N>
+struct Rows<__nv_bfloat16, N> {
+  uint4 v[N];
+  __device__ __forceinline__ void begin(const __nv_bfloat16 *from, int64_t stride, int t0, int nv, bool turned, int sh,
+                                        int width, float *, int) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * kThreads, row = i >> sh, col = (i & ((1 << sh) - 1)) * 8;
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < nv && col < width)
+        v[k] = *reinterpret_cast<const uint4 *>(from + (t0 + (turned ? nv - 1 - row : row)) * stride + col);
+    }
+  }
+  __device__ __forceinline__ void settle(int sh, float *to, int ld) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * kThreads, row = i >> sh, col = (i & ((1 << sh) - 1)) * 8;
+      if (row >= kC || col + 8 > ld) continue;
+      float *at = to + row * ld + col;
+      auto lo = [](uint32_t u) { return __uint_as_float(u << 16); };
+      auto hi = [](uint32_t u) { return __uint_as_float(u & 0xffff0000u); };
+      *reinterpret_cast<float4 *>(at) = make_float4(lo(v[k].x), hi(v[k].x), lo(v[k].y), hi(v[k].y));
+      *reinterpret_cast<float4 *>(at + 4) = make_float4(lo(v[k].z), hi(v[k].z), lo(v[k].w), hi(v[k].w));
+    }
+  }
+};
 
 struct SimtParams {
   RetArgs a;
   int parts, cpp, slices;  // cpp: chunks of a part; slices: of the widest role
+  int bufs;                // 2: the next chunk is loaded during this one
 };
 
-// The pass that only sums states has no x and no weights.
-int smem_bytes(int Dx, int SW, bool state) {
-  return 4 * (Dx * kLd + Dx * SW + kC * SW + 2 * kC + (state ? 0 : Dx * kLd + kC * kLd));
+// The pass that only sums states has no x, no weights and its state in registers.
+int smem_bytes(int Dx, int SW, bool state, int bufs) {
+  const int rows = kC * (Dx + 4);
+  return 4 * (bufs * ((state ? 1 : 2) * rows + kC * SW) + 2 * kC + (state ? 0 : Dx * SW + kC * kLdP));
 }
 
-// STATE: only the part's own state, into its record.
-template <typename T, int SW, bool STATE>
-__global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_constant__ SimtParams p) {
-  constexpr int CW = SW / 16;
-  extern __shared__ float sm[];
+// NI: 64 features each; STATE: only the part's own state, into its record.
+template <typename T, int NI, int SW, bool STATE>
+__global__ void __launch_bounds__(kThreads, NI == 1 ? 2 : 1)
+    retention_simt_kernel(const __grid_constant__ SimtParams p) {
+  constexpr int CW = SW / 16, kPer = 16 / sizeof(T);
+  constexpr int kShW = SW / kPer == 16 ? 4 : SW / kPer == 8 ? 3 : 2;  // pieces of a row of w, log2
+  constexpr int kNX = kC * 64 * NI / kPer / kThreads, kNW = kC * SW / kPer / kThreads;
+  extern __shared__ __align__(16) float sm[];
   const RetRole &r = p.a.role[blockIdx.z];
   const int np = STATE ? p.parts - 1 : p.parts;
   const int slice = blockIdx.x % p.slices, part = blockIdx.x / p.slices % np;
@@ -88,9 +124,12 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   const int e0 = slice * SW;
   if (e0 >= r.Dw) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
-  const int Dx = r.Dx, Dw = r.Dw;
-  float *yt = sm, *S = yt + Dx * kLd, *w = S + Dx * SW, *pw = w + kC * SW, *xt = pw + 2 * kC, *pt = xt + Dx * kLd;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int Dx = r.Dx, Dw = r.Dw, ld = Dx + 4;
+  float *pw = sm, *S = pw + 2 * kC, *pt = S + (STATE ? 0 : Dx * SW), *rows = pt + (STATE ? 0 : kC * kLdP);
+  const int per_buf = (STATE ? 1 : 2) * kC * ld + kC * SW;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // a warp covers 4 x 8 threads of 16 x 16: few distinct rows in each of its loads
+  const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3);
   const int tokens = ret_tokens(p.a.lens, b, p.a.L);
   const int n = (tokens + kC - 1) / kC;
   const float lg = p.a.lg.g[h];
@@ -98,151 +137,175 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   const T *y = static_cast<const T *>(r.y) + b * r.ys.b + (h / r.yg) * r.ys.h;
   const T *wp = static_cast<const T *>(r.w) + b * r.ws.b + (h / r.wg) * r.ws.h + e0;
   const float *rec = r.rec + bh * (p.parts - 1) * Dx * Dw;
+  const int after = r.reverse ? 0 : 1;  // o_0 meets the state in front of it decayed once, in time
+  int sh = 0;
+  while ((kPer << sh) < Dx) ++sh;
 
   if (tid <= kC) pw[tid] = exp2f(lg * static_cast<float>(tid));
-  for (int i = tid; i < Dx * SW; i += kThreads) {
-    const int d = i / SW, e = e0 + i % SW;
-    S[i] = STATE || e >= Dw ? 0.f : ret_start(r, rec, bh, part, p.cpp, n, tokens, kC, lg, d, e);
-  }
   const int c0 = part * p.cpp, c1 = part == p.parts - 1 ? n : min(n, c0 + p.cpp);
   const bool keep = STATE || (part == p.parts - 1 && r.end);  // the state behind the last chunk is wanted
+
+  Rows<T, kNX> xr, yr;
+  Rows<T, kNW> wr;
+  auto begin = [&](int c, float *to) {
+    const int t0 = (r.reverse ? n - 1 - c : c) * kC, nv = min(kC, tokens - t0);
+    yr.begin(y, r.ys.t, t0, nv, r.reverse, sh, Dx, to, ld);
+    wr.begin(wp, r.ws.t, t0, nv, r.reverse, kShW, min(SW, Dw - e0), to + kC * ld, SW);
+    if (!STATE) xr.begin(x, r.xs.t, t0, nv, r.reverse, sh, Dx, to + kC * ld + kC * SW, ld);
+    if constexpr (sizeof(T) == 4) copies_commit();
+  };
+  auto settle = [&](float *to) {
+    yr.settle(sh, to, ld);
+    wr.settle(kShW, to + kC * ld, SW);
+    if (!STATE) xr.settle(sh, to + kC * ld + kC * SW, ld);
+    if constexpr (sizeof(T) == 4) copies_wait<0>();
+  };
+  if (c0 < c1) begin(c0, rows);
+
+  // the thread's share of the state: features 64 i + 4 ty + u, columns CW tx + k
+  float s[NI][4][CW];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int k = 0; k < CW; ++k) {
+        const int d = 64 * i + 4 * ty + u, e = e0 + CW * tx + k;
+        s[i][u][k] = STATE || d >= Dx || e >= Dw ? 0.f : ret_start(r, rec, bh, part, p.cpp, n, tokens, kC, lg, d, e);
+      }
+  auto show = [&] {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int d = 64 * i + 4 * ty + u;
+        if (d < Dx) put<CW>(S + d * SW + CW * tx, s[i][u]);
+      }
+  };
+  if (!STATE) show();
+  if (c0 < c1) settle(rows);
+
+  int cur = 0;
   for (int c = c0; c < c1; ++c) {
     const int t0 = (r.reverse ? n - 1 - c : c) * kC;
     const int nv = min(kC, tokens - t0);
-    {
-      // the loads of a round under way together: one by one their latency took
-      // half of the time
-      const int t = tid & (kC - 1), g = tid >> 6;
-      constexpr int kRows = kC * SW / 4 / kThreads;
-      float4 wv[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int at = tid + i * kThreads, row = at / (SW / 4), e = 4 * (at % (SW / 4));
-        wv[i] = load_if(row < nv && e0 + e < Dw, wp + (t0 + row) * r.ws.t + e);
-      }
-      for (int d = 0; d < Dx; d += 64) {
-        float4 xv[4], yv[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = d + 4 * g + 16 * k;
-          if (!STATE) xv[k] = load_if(t < nv && c < Dx, x + (t0 + t) * r.xs.t + c);
-          yv[k] = load_if(t < nv && c < Dx, y + (t0 + t) * r.ys.t + c);
-        }
-        if (!STATE) store_turned(xt, xv, t, g, d, Dx);
-        store_turned(yt, yv, t, g, d, Dx);
-      }
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) reinterpret_cast<float4 *>(w)[tid + i * kThreads] = wv[i];
-    }
-    __syncthreads();
+    const bool more = c + 1 < c1;
+    const float *yb = rows + cur * per_buf, *wb = yb + kC * ld, *xb = wb + kC * SW;
+    cur ^= p.bufs - 1;
+    float *next = rows + cur * per_buf;
+    __syncthreads();  // chunk and state are there, the other buffer is read
+    if (more && p.bufs == 2) begin(c + 1, next);
     if (!STATE) {
-      float a[4][4] = {};
-#pragma unroll 8
-      for (int d = 0; d < Dx; ++d) {
-        const Cols<4> u = cols<4>(xt + d * kLd + 4 * ty), v = cols<4>(yt + d * kLd + 4 * tx);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) a[i][j] = fmaf(u.v[i], v.v[j], a[i][j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float col[4];
+      float a[4][4] = {}, o[4][CW] = {};
+#pragma unroll 2
+      for (int d = 0; d < Dx; d += 4) {
+        Cols<4> u[4], v[4];
+        Cols<CW> st[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int far = r.reverse ? 4 * tx + j - 4 * ty - i : 4 * ty + i - 4 * tx - j;
-          col[i] = far >= 0 ? a[i][j] * pw[far] : 0.f;
+          u[i] = cols<4>(xb + (ty + 16 * i) * ld + d);
+          v[i] = cols<4>(yb + (tx + 16 * i) * ld + d);
+          st[i] = cols<CW>(S + (d + i) * SW + CW * tx);
         }
-        *reinterpret_cast<float4 *>(pt + (4 * tx + j) * kLd + 4 * ty) = make_float4(col[0], col[1], col[2], col[3]);
-      }
-      __syncthreads();
-      float o[4][CW] = {};
-#pragma unroll 8
-      for (int d = 0; d < Dx; ++d) {
-        const Cols<4> u = cols<4>(xt + d * kLd + 4 * ty);
-        const Cols<CW> v = cols<CW>(S + d * SW + CW * tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int j = 0; j < CW; ++j) o[i][j] = fmaf(u.v[i], v.v[j], o[i][j]);
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j <= i; ++j) a[i][j] = fmaf(u[i].v[q], v[j].v[q], a[i][j]);
+#pragma unroll
+            for (int k = 0; k < CW; ++k) o[i][k] = fmaf(u[i].v[q], st[q].v[k], o[i][k]);
+          }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 4 * ty + i;
-        const float f = t >= nv ? 0.f : pw[r.reverse ? nv - 1 - t : t + 1];
 #pragma unroll
-        for (int j = 0; j < CW; ++j) o[i][j] *= f;
+        for (int j = 0; j <= i; ++j) {
+          const int far = ty - tx + 16 * (i - j);
+          pt[(ty + 16 * i) * kLdP + tx + 16 * j] = far >= 0 ? a[i][j] * pw[far] : 0.f;
+        }
+        const float f = pw[ty + 16 * i + after];
+#pragma unroll
+        for (int k = 0; k < CW; ++k) o[i][k] *= f;
       }
-      // the weights that are not masked, for the two groups of rows of a warp
-      const int s0 = r.reverse ? 4 * (ty & ~1) : 0, s1 = r.reverse ? kC : 4 * (ty | 1) + 4;
-#pragma unroll 8
-      for (int s = s0; s < s1; ++s) {
-        const Cols<4> u = cols<4>(pt + s * kLd + 4 * ty);
-        const Cols<CW> v = cols<CW>(w + s * SW + CW * tx);
+      __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j)
+#pragma unroll 2
+        for (int t = 16 * j; t < 16 * j + 16; t += 4) {
+          Cols<CW> v[4];
 #pragma unroll
-          for (int j = 0; j < CW; ++j) o[i][j] = fmaf(u.v[i], v.v[j], o[i][j]);
-      }
+          for (int q = 0; q < 4; ++q) v[q] = cols<CW>(wb + (t + q) * SW + CW * tx);
+#pragma unroll
+          for (int i = j; i < 4; ++i) {
+            const Cols<4> u = cols<4>(pt + (ty + 16 * i) * kLdP + t);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int k = 0; k < CW; ++k) o[i][k] = fmaf(u.v[q], v[q].v[k], o[i][k]);
+          }
+        }
       if (e0 + CW * tx < Dw) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = 4 * ty + i;
+          const int t = ty + 16 * i;
           if (t >= nv) break;
-          const int64_t at = b * r.os.b + (t0 + t) * r.os.t + h * r.os.h + e0 + CW * tx;
 #pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            const float v = o[i][j] * r.out_scale;
-            if (r.o_f32) static_cast<float *>(r.o)[at + j] = v;
-            else io<T>::store(static_cast<T *>(r.o) + at + j, v);
-          }
+          for (int k = 0; k < CW; ++k) o[i][k] *= r.out_scale;
+          const int64_t at = b * r.os.b + (t0 + (r.reverse ? nv - 1 - t : t)) * r.os.t + h * r.os.h + e0 + CW * tx;
+          if (r.o_f32) put<CW>(static_cast<float *>(r.o) + at, o[i]);
+          else put<CW>(static_cast<T *>(r.o) + at, o[i]);
         }
       }
-      __syncthreads();
     }
-    if (keep || c + 1 < c1) {
+    if (keep || more) {
       const float gn = pw[nv];
-      for (int d = 4 * ty; d < Dx; d += 64) {
-        float s[4][CW] = {};
-#pragma unroll 2
-        for (int j = 0; j < kC; j += 4) {
-          Cols<4> u[4];
-          Cols<CW> v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u[i] = cols<4>(yt + (d + i) * kLd + j);
-            v[i] = cols<CW>(w + (j + i) * SW + CW * tx);
-            const int t = j + i;
-            const float f = t >= nv ? 0.f : pw[r.reverse ? t + 1 : nv - 1 - t];
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int k = 0; k < CW; ++k) v[i].v[k] *= f;
-          }
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj)
+          for (int k = 0; k < CW; ++k) s[i][u][k] *= gn;
+#pragma unroll 4
+      for (int t = 0; t < nv; ++t) {
+        const float f = pw[nv - after - t];
+        Cols<CW> v = cols<CW>(wb + t * SW + CW * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int k = 0; k < CW; ++k) v.v[k] *= f;
 #pragma unroll
-              for (int k = 0; k < CW; ++k) s[i][k] = fmaf(u[i].v[jj], v[jj].v[k], s[i][k]);
+        for (int i = 0; i < NI; ++i) {
+          // behind the last feature: the first ones again, not kept
+          const int d = 64 * i + 4 * ty;
+          const Cols<4> yv = cols<4>(yb + t * ld + (d < Dx ? d : 0));
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int k = 0; k < CW; ++k) s[i][u][k] = fmaf(yv.v[u], v.v[k], s[i][u][k]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < CW; ++k) {
-            float *at = S + (d + i) * SW + CW * tx + k;
-            *at = fmaf(gn, *at, s[i][k]);
-          }
       }
     }
-    __syncthreads();
+    if (more) {
+      if (p.bufs == 1) {
+        __syncthreads();
+        begin(c + 1, next);
+      }
+      if (!STATE) show();
+      settle(next);
+    }
   }
-  __syncthreads();
-  if (STATE || (part == p.parts - 1 && r.end)) {
+  if (keep) {
     float *out = STATE ? const_cast<float *>(rec) + static_cast<int64_t>(part) * Dx * Dw : r.end + bh * r.state;
     const float f = STATE ? 1.f : r.end_scale;
-    for (int i = tid; i < Dx * SW; i += kThreads) {
-      const int d = i / SW, e = e0 + i % SW;
-      if (e < Dw) out[d * Dw + e] = f * S[i];
-    }
+    const int e = e0 + CW * tx;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int d = 64 * i + 4 * ty + u;
+#pragma unroll
+        for (int k = 0; k < CW; ++k) s[i][u][k] *= f;
+        if (d < Dx && e < Dw) put<CW>(out + d * Dw + e, s[i][u]);
+      }
   }
   if (!STATE && p.a.fill && part == p.parts - 1) {
     for (int64_t i = tid; i < static_cast<int64_t>(p.a.L - tokens) * SW; i += kThreads) {
@@ -255,27 +318,40 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   }
 }
 
-template <typename T, int SW>
+constexpr int kSmSmem = 227 * 1024;
+
+// CTAs that an SM holds, and whether the next chunk is loaded during this one:
+// not where its room would cost the second CTA.
+int held_of(int Dx, int SW, bool state, int *bufs) {
+  const int most = Dx <= 64 ? 2 : 1;
+  for (int held = most; held >= 1; --held)
+    for (*bufs = 2; *bufs >= 1; --*bufs)
+      if (held * (smem_bytes(Dx, SW, state, *bufs) + 1024) <= kSmSmem + 1024) return held;
+  return 0;
+}
+
+template <typename T, int NI, int SW, bool STATE>
+cudaError_t pass(SimtParams p, int64_t blocks, int Dx, cudaStream_t s) {
+  if (!held_of(Dx, SW, STATE, &p.bufs) || blocks >= (1LL << 31)) return cudaErrorNotSupported;
+  auto k = retention_simt_kernel<T, NI, SW, STATE>;
+  const int bytes = smem_bytes(Dx, SW, STATE, p.bufs);
+  const cudaError_t e = allow_smem(k, bytes);
+  if (e != cudaSuccess) return e;
+  k<<<dim3(static_cast<unsigned>(blocks), 1, p.a.roles), kThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int NI, int SW>
 cudaError_t run(const RetArgs &a, int parts, int widest, int Dx, cudaStream_t s) {
-  SimtParams p = {a, parts, 0, (widest + SW - 1) / SW};
+  SimtParams p = {a, parts, 0, (widest + SW - 1) / SW, 0};
   const int chunks = (a.L + kC - 1) / kC;
   p.cpp = (chunks + parts - 1) / parts;
   const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
-  if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
   if (parts > 1) {
-    auto k = retention_simt_kernel<T, SW, true>;
-    const int bytes = smem_bytes(Dx, SW, true);
-    cudaError_t e = allow_smem(k, bytes);
+    const cudaError_t e = pass<T, NI, SW, true>(p, units * (parts - 1), Dx, s);
     if (e != cudaSuccess) return e;
-    k<<<dim3(static_cast<unsigned>(units * (parts - 1)), 1, a.roles), kThreads, bytes, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  auto k = retention_simt_kernel<T, SW, false>;
-  const int bytes = smem_bytes(Dx, SW, false);
-  const cudaError_t e = allow_smem(k, bytes);
-  if (e != cudaSuccess) return e;
-  k<<<dim3(static_cast<unsigned>(units * parts), 1, a.roles), kThreads, bytes, s>>>(p);
-  return cudaGetLastError();
+  return pass<T, NI, SW, false>(p, units * parts, Dx, s);
 }
 
 void widths(const RetArgs &a, int *Dx, int *Dw) {
@@ -291,34 +367,41 @@ struct Cut {
   int SW, parts;
 };
 
-// The cut that is done first by a model of the CTAs that an SM holds (by shared
-// memory, up to three): a chunk takes 1 unit of time with slices of 64 columns and
-// 0.8 with 32 (14 and 12 us of 64 features, alone on an SM), half of that where
-// states are summed, 0.35 more for each further CTA on the SM, and a CTA 1 unit to
-// begin and end.  Above 128 features slices of 64 columns do not fit.
+// The cut that is done first by a model of the CTAs that an SM holds: a chunk takes
+// 1 unit of time with slices of 64 columns and 0.65 with 32, 0.4 of that where
+// states are summed, 0.6 more for a second CTA on the SM, and a CTA 1 unit to begin
+// and end.
 Cut cut_of(const RetArgs &a) {
   int Dx, Dw;
   widths(a, &Dx, &Dw);
   const int chunks = (a.L + kC - 1) / kC;
   Cut best = {32, 1};
   double least = 1e300;
-  for (int SW = 32; SW <= (Dx > 128 || Dw <= 32 ? 32 : 64); SW += 32) {
+  for (int SW = 32; SW <= (Dw <= 32 ? 32 : 64); SW += 32) {
     const int64_t units = static_cast<int64_t>(a.B) * a.H * ((Dw + SW - 1) / SW) * a.roles;
     auto time = [&](int64_t n, double chunk, bool state) {
-      int held = 227 * 1024 / (smem_bytes(Dx, SW, state) + 1024);
-      if (held > 3) held = 3;
+      int bufs, held = held_of(Dx, SW, state, &bufs);
       if (n < static_cast<int64_t>(kSMs) * held) held = static_cast<int>((n + kSMs - 1) / kSMs);
       const int64_t slots = static_cast<int64_t>(kSMs) * (held > 0 ? held : 1);
-      return static_cast<double>((n + slots - 1) / slots) * (chunk * (1 + 0.35 * (held - 1)) + 1);
+      return static_cast<double>((n + slots - 1) / slots) * (chunk * (1 + 0.6 * (held - 1)) + 1);
     };
     for (int parts = 1; parts <= 32 && (parts == 1 || parts * 2 <= chunks); ++parts) {
-      const double chunk = ((chunks + parts - 1) / parts) * (SW == 64 ? 1.0 : 0.8);
+      const double chunk = ((chunks + parts - 1) / parts) * (SW == 64 ? 1.0 : 0.65);
       double t = time(units * parts, chunk, false);
-      if (parts > 1) t += time(units * (parts - 1), 0.5 * chunk, true);
+      if (parts > 1) t += time(units * (parts - 1), 0.4 * chunk, true);
       if (t < least) least = t, best = {SW, parts};
     }
   }
   return best;
+}
+
+template <typename T>
+cudaError_t cut_and_run(const RetArgs &a, int parts, cudaStream_t s) {
+  int Dx, Dw;
+  widths(a, &Dx, &Dw);
+  if (Dx > 128) return cudaErrorNotSupported;
+  if (cut_of(a).SW == 64) return Dx > 64 ? run<T, 2, 64>(a, parts, Dw, Dx, s) : run<T, 1, 64>(a, parts, Dw, Dx, s);
+  return Dx > 64 ? run<T, 2, 32>(a, parts, Dw, Dx, s) : run<T, 1, 32>(a, parts, Dw, Dx, s);
 }
 
 template <typename T>
@@ -346,11 +429,7 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ 
 int ret_parts_simt(const RetArgs &a) { return cut_of(a).parts; }
 
 cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStream_t s) {
-  int Dx, Dw;
-  widths(a, &Dx, &Dw);
-  const bool wide = cut_of(a).SW == 64;
-  if (dt == kF32) return wide ? run<float, 64>(a, parts, Dw, Dx, s) : run<float, 32>(a, parts, Dw, Dx, s);
-  return wide ? run<__nv_bfloat16, 64>(a, parts, Dw, Dx, s) : run<__nv_bfloat16, 32>(a, parts, Dw, Dx, s);
+  return dt == kF32 ? cut_and_run<float>(a, parts, s) : cut_and_run<__nv_bfloat16>(a, parts, s);
 }
 
 cudaError_t launch_group_sum(const GroupSumArgs &a, Dtype dt, cudaStream_t s) {
