@@ -364,7 +364,7 @@ struct GroupSumArgs {
   const int *lens;
   int B, L, heads, g, width;
 };
-cudaError_t launch_group_sum(const GroupSumArgs &a, Dtype dt, cudaStream_t s);
+cudaError_t launch_group_sums(const GroupSumArgs *a, int n, Dtype dt, cudaStream_t s);  // n <= 3, one launch
 
 // One token of retention in place on states [slots][H][D][Dv] fp32: sequence b
 // has the state slots[b] (null: b); one outside [0, pool) is passed over.

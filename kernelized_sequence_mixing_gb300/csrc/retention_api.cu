@@ -125,13 +125,10 @@ struct Plan {
       for (int i = 0; i < a.roles; ++i)
         if (a.role[i].o_f32) a.role[i].o = base + reinterpret_cast<size_t>(a.role[i].o);
       ret_layout(&a, parts, static_cast<float *>(ws) + share);
-      cudaError_t e = launch_retention(a, dt, parts, s);
-      for (int i = 0; i < sums && e == cudaSuccess; ++i) {
-        GroupSumArgs g = sum[i];
-        g.part = reinterpret_cast<const float *>(base + reinterpret_cast<size_t>(g.part));
-        e = launch_group_sum(g, dt, s);
-      }
-      return e;
+      const cudaError_t e = launch_retention(a, dt, parts, s);
+      for (int i = 0; i < sums; ++i)
+        sum[i].part = reinterpret_cast<const float *>(base + reinterpret_cast<size_t>(sum[i].part));
+      return e == cudaSuccess ? launch_group_sums(sum, sums, dt, s) : e;
     });
   }
 };

@@ -420,23 +420,33 @@ cudaError_t cut_and_run(const RetArgs &a, int parts, cudaStream_t s) {
   return Dx > 64 ? run<T, 2, 32>(a, parts, Dw, Dx, s) : run<T, 1, 32>(a, parts, Dw, Dx, s);
 }
 
+struct Sums {
+  GroupSumArgs s[3];
+};
+
+// A block takes rows of about 1024 pieces of four columns; blockIdx.y: which output.
 template <typename T>
-__global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ GroupSumArgs a, int64_t total) {
-  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-    // four columns of one output head: its shares lie behind one another
-    const int e = static_cast<int>(i % (a.width / 4)) * 4;
-    const int64_t rh = i / (a.width / 4);
-    const int h = static_cast<int>(rh % a.heads);
-    const int64_t row = rh / a.heads;
-    const int t = static_cast<int>(row % a.L), b = static_cast<int>(row / a.L);
-    if (t >= ret_tokens(a.lens, b, a.L)) continue;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < a.g; ++j) {
-      const float4 v = __ldcs(reinterpret_cast<const float4 *>(a.part + (rh * a.g + j) * a.width + e));
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+__global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ Sums p) {
+  const GroupSumArgs &a = p.s[blockIdx.y];
+  const int quarter = a.width / 4, per = a.heads * quarter;
+  const int rows = max(1, 1024 / per);
+  const int64_t all = static_cast<int64_t>(a.B) * a.L;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows; r0 < all; r0 += static_cast<int64_t>(gridDim.x) * rows) {
+    for (int i = threadIdx.x; i < rows * per; i += 256) {
+      const int64_t row = r0 + i / per;
+      if (row >= all) break;
+      const int h = i % per / quarter, e = i % quarter * 4;
+      const int b = static_cast<int>(row) / a.L, t = static_cast<int>(row) % a.L;  // rows below 2^31
+      if (t >= ret_tokens(a.lens, b, a.L)) continue;
+      // the shares of an output head lie behind one another
+      const float *from = a.part + ((row * a.heads + h) * a.g) * a.width + e;
+      float s[4] = {};
+      for (int j = 0; j < a.g; ++j) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(from + static_cast<int64_t>(j) * a.width));
+        s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+      }
+      put<4>(static_cast<T *>(a.out) + b * a.os.b + t * a.os.t + h * a.os.h + e, s);
     }
-    T *o = static_cast<T *>(a.out) + b * a.os.b + t * a.os.t + h * a.os.h + e;
-    io<T>::store(o, s.x), io<T>::store(o + 1, s.y), io<T>::store(o + 2, s.z), io<T>::store(o + 3, s.w);
   }
 }
 
@@ -448,12 +458,18 @@ cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStr
   return dt == kF32 ? cut_and_run<float>(a, parts, s) : cut_and_run<__nv_bfloat16>(a, parts, s);
 }
 
-cudaError_t launch_group_sum(const GroupSumArgs &a, Dtype dt, cudaStream_t s) {
-  const int64_t total = static_cast<int64_t>(a.B) * a.L * a.heads * (a.width / 4);
-  const int64_t want = (total + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(want < 8 * kSMs ? want : 8 * kSMs);
-  if (dt == kF32) group_sum_kernel<float><<<grid, 256, 0, s>>>(a, total);
-  else group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, total);
+cudaError_t launch_group_sums(const GroupSumArgs *a, int n, Dtype dt, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
+  Sums p = {};
+  int64_t want = 1;
+  for (int i = 0; i < n; ++i) {
+    p.s[i] = a[i];
+    const int64_t blocks = (static_cast<int64_t>(a[i].B) * a[i].L * a[i].heads * (a[i].width / 4) + 1023) / 1024;
+    if (blocks > want) want = blocks;
+  }
+  const dim3 grid(static_cast<unsigned>(want < 8 * kSMs ? want : 8 * kSMs), n);
+  if (dt == kF32) group_sum_kernel<float><<<grid, 256, 0, s>>>(p);
+  else group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
