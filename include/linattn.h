@@ -602,21 +602,24 @@ LA_API la_status_t la_backward_norm_residual(const void *r, const float *w, cons
  *   first are read in place.  Multiples of 8, rows contiguous and apart from
  *   one another; the stride of a dimension of size 1 is not looked at.
  * - Sizes: D and Dv multiples of 8 up to 256, H <= 256, B L < 2^31 - 2^16
- *   tokens, B H < 2^26.  scale is finite and not 0.
+ *   tokens, B H < 2^26.  |scale| between 2^-64 and 2^64.
  * - lens (optional, int32 [B] in DEVICE memory, 4-byte aligned): sequence b has
  *   lens[b] tokens (clamped to [0, L]).  Rows behind it are not read and have no
  *   effect; outputs there are left alone, gradients there are zero; the final
  *   state is the one after the last token.
  * - Arithmetic: fp32 states and sums, each output rounded once.  For LA_BF16
- *   with D, Dv in {64, 128} (forward: Dv any multiple of 32) the products run on
- *   tcgen05 tensor cores: there the weights of a chunk are rounded to bf16, the
- *   states and the decayed rows that build them enter as sums of two bf16 values
- *   (three where a state is returned, which then has fp32 accuracy).  Results do
- *   not depend on scheduling (no atomics).
+ *   with D a multiple of 64 and Dv of 32 (gradients: both of 64) the products run
+ *   on tcgen05 tensor cores: there the weights of a chunk and the decayed rows
+ *   that build the states for outputs are rounded to bf16 once, and states enter
+ *   as sums of two bf16 values.  Returned states (S, dS0) are summed from decayed
+ *   rows as three bf16 values, to fp32 accuracy.  Results do not depend on
+ *   scheduling (no atomics).
  * - Within a chunk of up to 128 tokens a weight of zero times an infinity or NaN
  *   of a later token is NaN: inputs are finite.
  * - Few (batch, head) pairs split long sequences into parts that run side by
- *   side, with a workspace of B*H*D*Dv*4 bytes for each part but one.
+ *   side, with a workspace of B*H*D*Dv*4 bytes for each part but the last (for it
+ *   too where a state is returned).  More than 128 features are worked as 128 and
+ *   the rest, with a workspace of 2*B*L*H*Dv*4 bytes for the two shares of o.
  *   Workspaces as in the selective scan's family; no written buffer may overlap
  *   any other buffer of the call.
  */
@@ -655,7 +658,8 @@ LA_API la_status_t la_decode_retention(const void *q, const void *k, const void 
  * dk and dv summed over the heads that share them.  dq, dk, dv are dense, of
  * `dtype`; dS0 fp32 (NULL: not wanted; needs S0).  Nothing of the forward pass
  * is kept: the states are computed again.  Shared heads take a workspace of
- * B*L*H*(D + Dv)*4 bytes more.
+ * B*L*H*(D + Dv)*4 bytes for dk and dv before they are added; Dv above 128 takes
+ * room for two shares of dq and dk, D above 128 of dv.
  */
 LA_API la_status_t la_backward_retention(const void *q, const void *k, const void *v,
                                          const void *dO, const float *S0, const float *dS,

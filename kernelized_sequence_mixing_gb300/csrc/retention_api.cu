@@ -47,7 +47,8 @@ RetStrides dense(int64_t L, int64_t heads, int64_t width) { return {L * heads * 
 
 la_status_t check_sizes(int B, int L, int H, int Hk, int D, int Dv, float scale, la_dtype_t dt) {
   if (!dtype_ok(dt) || B < 0 || L < 0 || H < 0 || D <= 0 || Dv <= 0) return LA_ERR_INVALID_ARG;
-  if (!isfinite(scale) || scale == 0.f) return LA_ERR_INVALID_ARG;
+  // the backward pass divides by it
+  if (!(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return LA_ERR_INVALID_ARG;
   if (H > 0 && (Hk <= 0 || H % Hk != 0)) return LA_ERR_INVALID_ARG;
   if (H > kMaxHeads || D % 8 != 0 || Dv % 8 != 0 || D > 256 || Dv > 256) return LA_ERR_UNSUPPORTED;
   if ((int64_t)B * (L > 0 ? L : 1) >= kMaxTokens || (int64_t)B * H >= (1 << 26)) return LA_ERR_UNSUPPORTED;

@@ -58,6 +58,17 @@ def common_refusals(c, dims=True):
     assert c(**none, B=0) == OK and c(**none, H=0, Hk=0) == OK
 
 
+def test_scales_beyond_the_range(lib):
+    """The backward pass divides by the scale: both calls refuse one whose inverse
+    or whose products would leave fp32."""
+    for name, names in (("la_forward_retention", "q k v S0 lens o S"),
+                        ("la_backward_retention", "q k v dO S0 dS lens dq dk dv dS0")):
+        c = Call(getattr(lib, name), names, SIZES)
+        for bad in (1e-39, 2.0 ** -65, -2.0 ** -70, 2.0 ** 65, -3e38):
+            assert c(scale=bad) == INVALID
+        assert c(scale=2.0 ** -64, B=0) == OK and c(scale=-2.0 ** 64, B=0) == OK
+
+
 def test_forward_refusals(lib):
     c = Call(lib.la_forward_retention, "q k v S0 lens o S", SIZES)
     for name in ("q", "k", "v", "o"):
