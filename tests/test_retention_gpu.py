@@ -9,9 +9,10 @@ values (from the oracle):
   the longest path -- one multiplication by a power of the decay and one sum per
   chunk at most and two per token, the D products of a weight, and a power
   2^(e log2 g) that is off by e |log2 g| 2^-24 with |log2 g| <= 1 here (e <= L);
-  bf16 outputs of the tensor-core kernel also 2^-8 mag (the weights of a chunk,
-  rounded to bf16) + 2^-15 mag (states and decayed rows as sums of two bf16
-  values, 2^-16 each).
+  bf16 outputs of the tensor-core kernel also 2^-8 mag (each product meets one
+  factor that was rounded to bf16: within a chunk its weight, further back the
+  decayed row that built the state) + 2^-15 mag (states as sums of two bf16
+  values, 2^-16, and the second order).
 
 States that are returned are fp32 (decayed rows as three bf16 values, 2^-24).
 """
@@ -523,3 +524,211 @@ def test_beam_search(la, dtype):
         for (gs, gt), (rs, rt) in zip(got, beams):
             assert abs(gs - rs) < slack * steps
             assert dtype == BF16 or gt == rt
+
+
+# --- further uses ---
+
+# more than 128 features (two roles whose outputs are added) on both kernels
+BROAD = [(2, 260, 2, 1, 192, 64), (1, 140, 2, 2, 256, 64), (2, 300, 2, 2, 64, 256), (1, 200, 2, 1, 136, 32),
+         (1, 131, 1, 1, 256, 136), (1, 90, 3, 1, 200, 248)]
+
+
+@DT
+@pytest.mark.parametrize("shape", BROAD, ids=sid)
+def test_more_features(la, dtype, shape):
+    test_forward(la, dtype, shape)
+    test_backward(la, dtype, shape)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(6, 300, 2, 1, 256, 128), (6, 300, 2, 2, 136, 72)], ids=sid)
+def test_more_features_ragged(la, dtype, shape):
+    test_ragged(la, dtype, shape)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(1, 2600, 1, 1, 256, 64), (1, 2600, 2, 1, 72, 200)], ids=sid)
+def test_more_features_parts(la, dtype, shape):
+    test_parts(la, dtype, shape)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(2, 150, 4, 2, 256, 64), (2, 150, 2, 2, 64, 256)], ids=sid)
+def test_more_features_layouts(la, dtype, shape):
+    test_layouts(la, dtype, shape)
+
+
+@DT
+@pytest.mark.parametrize("D", [64, 256])
+def test_out_off_the_sectors(la, dtype, D):
+    """Outputs whose rows start 8 elements off the 32-byte sectors; what lies
+    between the rows stays."""
+    B, L, H = 2, 200, 2
+    p = Problem((B, L, H, H, D, 64), dtype, 13)
+    want = la.forward_retention(*p.dev(), **p.kw())
+    for off, width in ((8, 72), (8, 88), (0, 72), (16, 80)):
+        room = torch.full((B, L, H, width + 8), -3.0, dtype=dtype, device="cuda")
+        out = room[..., off:off + 64]
+        la.forward_retention(*p.dev(), **p.kw(), out=out)
+        assert torch.equal(out, want)
+        out.fill_(-3.0)
+        assert (room == -3).all()
+
+
+@DT
+@pytest.mark.parametrize("shape", [(2, 140, 2, 2, 64, 64), (1, 300, 1, 1, 40, 24)], ids=sid)
+def test_zero_decay_gradients(la, dtype, shape):
+    p = Problem(shape, dtype, 3)
+    p.gamma = torch.zeros(shape[2])
+    ref, mag = p.grads(), p.grads(True)
+    got = la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())
+    for name, x, r, m in zip(("dq", "dk", "dv"), got, ref, mag):
+        close("zero decay " + name, x, r, m, p.K, dtype, True)
+    close("zero decay dS0", got[3], ref[3], mag[3], p.K, F32)
+
+
+@DT
+@pytest.mark.parametrize("scale", [2.0 ** -64, -2.0 ** -20, 2.0 ** 20])
+def test_scales(la, dtype, scale):
+    """Scales far from one (powers of two: no rounding of their own)."""
+    p = Problem((1, 150, 2, 1, 64, 64), dtype, 17)
+    p.scale = scale
+    (ro, _), (mo, _) = p.ref(), p.ref(True)
+    close("scaled o", la.forward_retention(*p.dev(), **p.kw()), ro, mo, p.K, dtype, True)
+    ref, mag = p.grads(), p.grads(True)
+    got = la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())
+    for name, x, r, m in zip(("dq", "dk", "dv"), got, ref, mag):
+        # states of dk and dv are held divided by the scale: one rounding more
+        close("scaled " + name, x, r, m, p.K + 2, dtype, True)
+
+
+@pytest.mark.parametrize("shape", [(2, 150, 4, 2, 64, 128), (1, 700, 1, 1, 40, 24), (1, 100, 2, 1, 256, 64)], ids=sid)
+def test_gradients_are_differences(la, shape):
+    """The loss sum(o do) + sum(S dS) is linear in each input alone: its change
+    along a direction is the gradient's product with it, up to the roundings of
+    both, whose bounds are the outputs' own."""
+    p = Problem(shape, F32, 23)
+    do, dS = n64(p.do), n64(p.dS)
+    grads, gmag = [n64(t) for t in la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())], p.grads(True)
+
+    def loss():
+        o, S = la.forward_retention(*p.dev(), **p.kw(), return_state=True)
+        (mo, mS) = p.ref(True)
+        step = (p.K + 1) * 2.0 ** -24
+        return (n64(o) * do).sum() + (n64(S) * dS).sum(), step * ((mo * np.abs(do)).sum() + (mS * np.abs(dS)).sum())
+
+    for i, name in enumerate(("q", "k", "v", "S0")):
+        t = getattr(p, name)
+        way = torch.randint(-1, 2, t.shape, generator=p.g).float()
+        kept = t.clone()
+        t.copy_(kept + way)
+        up = t.clone()
+        a, ea = loss()
+        t.copy_(kept - way)
+        moved = n64(up) - n64(t)  # as rounded
+        b, eb = loss()
+        t.copy_(kept)
+        want = (grads[i] * moved).sum()
+        bound = ea + eb + (p.K + 1) * 2.0 ** -24 * (gmag[i] * np.abs(moved)).sum()
+        assert abs(a - b - want) <= bound, (name, a - b, want, bound)
+        # not an empty test: the gradient's terms together exceed the worst case of the roundings
+        assert bound < np.abs(grads[i] * moved).sum()
+
+
+@DT
+def test_offsets_beyond_32_bits(la, dtype):
+    """Rows, heads and sequences more than 2^31 elements apart, and a decode whose
+    places lie behind 2^31 elements of the pool."""
+    B, L, H, D = 2, 130, 2, 64
+    p = Problem((B, L, H, H, D, D), dtype, 19)
+    o, S = la.forward_retention(*p.dev(), **p.kw(), return_state=True)
+    grads = la.backward_retention(*p.dev(), p.do.cuda(), **p.kw(), dS=p.dS.cuda())
+    far = (1 << 31) + (1 << 12)
+    for order in ((0, 1, 2), (2, 1, 0)):  # the far stride: of sequences, of heads
+        room = torch.empty(far + 5 * L * H * D * B, dtype=dtype, device="cuda")
+        sizes = [(B, L, H)[i] for i in order]
+        strides = [0, 0, 0]
+        strides[order[0]], strides[order[1]], strides[order[2]] = far, sizes[2] * D, D
+        step = L * H * D
+        views = [room[i * step:].as_strided((B, L, H, D), (*strides, 1), i * step) for i in range(4)]
+        for view, t in zip(views, (*p.dev(), p.do.cuda())):
+            view.copy_(t)
+        out = torch.empty(far + step * B, dtype=dtype, device="cuda").as_strided((B, L, H, D), (*strides, 1))
+        got, gs = la.forward_retention(*views[:3], **p.kw(), out=out, return_state=True)
+        assert torch.equal(got, o) and torch.equal(gs, S)
+        for x, y in zip(la.backward_retention(*views[:4], **p.kw(), dS=p.dS.cuda()), grads):
+            assert torch.equal(x, y)
+        del room, views, got, out
+    slots = torch.tensor([(1 << 19) + 3, 2, (1 << 19) + 5], dtype=torch.int32)
+    p = Problem((3, 1, 1, 1, 64, 64), dtype, 2)
+    q, k, v = (t[:, 0] for t in p.dev())
+    near = p.S0.cuda()
+    want = la.decode_retention(q, k, v, near, gamma=p.gamma, scale=p.scale)
+    pool = torch.empty((1 << 19) + 6, 1, 64, 64, device="cuda")
+    pool[slots.long().cuda()] = p.S0.cuda()
+    got = la.decode_retention(q, k, v, pool, gamma=p.gamma, scale=p.scale, slots=slots.cuda())
+    assert torch.equal(got, want) and torch.equal(pool[slots.long().cuda()], near)
+
+
+@DT
+def test_two_at_once(la, dtype):
+    """Calls on two streams at the same time, each with its own workspace, and the
+    same calls again: the same bits."""
+    ps = [Problem((1, 3000, 2, 1, 128, 128), dtype, s) for s in (1, 2)]
+    logits = [torch.randn(8, 4, 30011, device="cuda").to(dtype) for _ in ps]
+    scores = torch.randn(8, 4, device="cuda")
+    args = [(p.dev(), p.do.cuda(), p.kw(), p.dS.cuda()) for p in ps]
+
+    def all_of(i):
+        x, do, kw, dS = args[i]
+        return (*la.forward_retention(*x, **kw, return_state=True), *la.backward_retention(*x, do, **kw, dS=dS),
+                *la.select_beams(logits[i], scores))
+
+    alone = [all_of(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [None, None]
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = all_of(i)
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@DT
+def test_beams_captured(la, dtype):
+    """A selection and the reordering after it, captured twice and replayed with
+    other inputs, interleaved with eager calls."""
+    B, K, V = 5, 4, 20011
+    g = torch.Generator().manual_seed(8)
+    logits, scores = torch.randn(B, K, V, generator=g).to(dtype).cuda(), torch.randn(B, K, generator=g).cuda()
+    finished = torch.zeros(B, K, dtype=torch.bool, device="cuda")
+    states = [torch.randn(B, K, 40, 64, generator=g).cuda(), torch.randn(B * K, 7, generator=g).to(dtype).cuda()]
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = la.select_beams(logits, scores, finished=finished, eos=2)
+            la.reorder_states(states, held[1])
+        graphs.append((graph, held))
+    for turn in range(4):
+        logits.copy_(torch.randn(B, K, V, generator=g).to(dtype))
+        finished.copy_(torch.rand(B, K, generator=g) < 0.3)
+        before = [t.clone() for t in states]
+        graph, held = graphs[turn % 2]
+        graph.replay()
+        want = check_select(la, logits.cpu(), scores.cpu(), K, finished.cpu(), 2)
+        assert all(torch.equal(x, y) for x, y in zip(held, want))
+        la.reorder_states(before, want[1])
+        assert all(torch.equal(x, y) for x, y in zip(states, before))
+
+
+def test_select_largest(la):
+    """The most beams and places; one token; a vocabulary of a million."""
+    g = torch.Generator().manual_seed(4)
+    check_select(la, torch.randn(2, 32, 2000, generator=g), torch.randn(2, 32, generator=g), 64)
+    check_select(la, torch.zeros(3, 1, 1), torch.zeros(3, 1), 1)
+    check_select(la, torch.randn(1, 2, 1 << 20, generator=g), torch.randn(1, 2, generator=g), 64)
+    check_select(la, torch.randn(1, 1, 64, generator=g), torch.zeros(1, 1), 64)
