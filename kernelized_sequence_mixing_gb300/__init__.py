@@ -958,12 +958,14 @@ def _decays(gamma, H):
 
 
 def _heads(fn, name, t, shape, dtype):
-    """The strides (batch, token, head) of t: ``shape`` [B, L, heads, width] and
-    ``dtype``, rows contiguous and apart from one another."""
+    """The strides (batch, token, head) of t, None where it is dense: ``shape`` [B, L,
+    heads, width] and ``dtype``, rows contiguous and apart from one another."""
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return None
     *outer, last = t.stride()
     sizes = t.shape
     if last != 1 and sizes[3] > 1:
@@ -981,7 +983,7 @@ def _heads(fn, name, t, shape, dtype):
 def _retention_args(fn, q, k, v, gamma, scale, extra=()):
     """Checks shared by the whole-sequence calls; ``extra`` [(name, tensor)] are
     further tensors shaped like o.  Returns (B, L, H, Hk, D, Dv, the strides of
-    q, k, v and of the last of ``extra``)."""
+    q, k, v and of the last of ``extra``, or None where all are dense)."""
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError(f"{fn}: expected q: [B, L, H, D], k: [B, L, Hk, D] and v: [B, L, Hk, Dv]")
     _dtype_code(q)
@@ -990,13 +992,18 @@ def _retention_args(fn, q, k, v, gamma, scale, extra=()):
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"{fn}: the {Hk} heads of k and v must divide the {H} heads of q")
     _c_ints(fn, B, L, H, D, Dv)
-    strides = (_heads(fn, "q", q, (B, L, H, D), q.dtype) + _heads(fn, "k", k, (B, L, Hk, D), q.dtype)
-               + _heads(fn, "v", v, (B, L, Hk, Dv), q.dtype))
-    last = [L * H * Dv, H * Dv, Dv]
+    dtype = q.dtype
+    strides = [_heads(fn, "q", q, (B, L, H, D), dtype), _heads(fn, "k", k, (B, L, Hk, D), dtype),
+               _heads(fn, "v", v, (B, L, Hk, Dv), dtype), None]
     for name, t in extra:
         if t is not None:
-            last = _heads(fn, name, t, (B, L, H, Dv), q.dtype)
-    return B, L, H, Hk, D, Dv, (ctypes.c_longlong * 12)(*strides, *last)
+            strides[3] = _heads(fn, name, t, (B, L, H, Dv), dtype)
+    if strides == [None] * 4:
+        return B, L, H, Hk, D, Dv, None
+    flat = []
+    for own, heads, width in zip(strides, (H, Hk, Hk, H), (D, D, Dv, Dv)):
+        flat += own or (L * heads * width, heads * width, width)
+    return B, L, H, Hk, D, Dv, (ctypes.c_longlong * 12)(*flat)
 
 
 def forward_retention(q, k, v, gamma=None, scale=1.0, S0=None, lens=None, out=None,

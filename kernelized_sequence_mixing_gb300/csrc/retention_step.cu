@@ -9,6 +9,10 @@
 // (LN = 32, whole 512-byte rows) where they fill the card; slices of 32 columns
 // where few sequences decode, so that the states of one sequence spread over
 // four times the SMs.
+//
+// Measured at H = 32, D = Dv = 128, bf16: 256 sequences 159 us (1.08 GB, the copy
+// rate); one sequence of 16 heads 2.4 us in a graph (22-25 launched one by one, the
+// host's time).
 #include "common.cuh"
 #include "kernels.h"
 #include "mixer_common.cuh"
