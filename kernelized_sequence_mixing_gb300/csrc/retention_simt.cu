@@ -14,6 +14,7 @@
 // The next chunk's rows travel meanwhile (fp32 by cp.async, bf16 in registers).
 // Bound by the fp32 pipe and by the latency of shared memory at 8 or 16 warps an SM.
 #include "common.cuh"
+#include "dependent.cuh"
 #include "mixer_common.cuh"
 #include "retention.cuh"
 
@@ -428,6 +429,7 @@ struct Sums {
 template <typename T>
 __global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ Sums p) {
   const GroupSumArgs &a = p.s[blockIdx.y];
+  wait_for_previous();
   const int quarter = a.width / 4, per = a.heads * quarter;
   const int rows = max(1, 1024 / per);
   const int64_t all = static_cast<int64_t>(a.B) * a.L;
@@ -467,10 +469,8 @@ cudaError_t launch_group_sums(const GroupSumArgs *a, int n, Dtype dt, cudaStream
     const int64_t blocks = (static_cast<int64_t>(a[i].B) * a[i].L * a[i].heads * (a[i].width / 4) + 1023) / 1024;
     if (blocks > want) want = blocks;
   }
-  const dim3 grid(static_cast<unsigned>(want < 8 * kSMs ? want : 8 * kSMs), n);
-  if (dt == kF32) group_sum_kernel<float><<<grid, 256, 0, s>>>(p);
-  else group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(want < 8 * kSMs ? want : 8 * kSMs);
+  return launch_dependent(dt == kF32 ? group_sum_kernel<float> : group_sum_kernel<__nv_bfloat16>, grid, n, 256, 0, s, p);
 }
 
 // ---- choice between the kernels, shared host code ----

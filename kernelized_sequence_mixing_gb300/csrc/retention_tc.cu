@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "mixer_common.cuh"
 #include "retention.cuh"
 #include "tc_common.cuh"
@@ -264,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Ly::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Ly::kMisc + 4);
 
-  const RetRole &r = p.a.role[blockIdx.z];
-  const TcRole &map = p.map[blockIdx.z];
+  const RetRole &r = p.a.role[blockIdx.y];
+  const TcRole &map = p.map[blockIdx.y];
   const int np = STATE ? p.records : p.parts;
   const int slice = blockIdx.x % p.slices, part = blockIdx.x / p.slices % np;
   const int64_t bh = blockIdx.x / p.slices / np;
@@ -311,6 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   }
   if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
+  // the pass behind comes up as this one's CTAs end; before the first bounded wait
+  // all of it waits for the records
+  if (STATE) let_next_start();
+  else wait_for_previous();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
@@ -709,8 +714,9 @@ cudaError_t pass(const TcParams &p, int64_t units, cudaStream_t s) {
   const int bytes = Lay<DX, SW, NS, STATE>::kAlloc;
   const cudaError_t e = allow_smem(k, bytes);
   if (e != cudaSuccess) return e;
-  const int np = STATE ? p.records : p.parts;
-  k<<<dim3(static_cast<unsigned>(units * np), 1, p.a.roles), kThreads, bytes, s>>>(p);
+  const unsigned grid = static_cast<unsigned>(units * (STATE ? p.records : p.parts));
+  if (!STATE && p.records > 0) return launch_dependent(k, grid, p.a.roles, kThreads, bytes, s, p);
+  k<<<dim3(grid, p.a.roles), kThreads, bytes, s>>>(p);
   return cudaGetLastError();
 }
 
