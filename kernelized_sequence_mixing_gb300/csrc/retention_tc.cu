@@ -43,7 +43,7 @@
 // staging of the state pass through it too), about 2400 cycles a chunk of 128
 // features and 32 columns against 700 of products.  Measured: B2 L16384 H16 D128
 // forward 162 us (3.3 TB/s of q, k, v, o; 0.49 of the copy rate); B1 L65536 H8|4 D128
-// with the final state 201 us; backward B4 L4096 H8 D64 63 us.
+// with the final state 199 us; backward B4 L4096 H8 D64 63 us.
 #include <type_traits>
 
 #include "common.cuh"
