@@ -1,5 +1,5 @@
-// Retention on tcgen05 tensor cores: bf16, Dx = 64 or 128 features, any
-// multiple of 32 columns of w.
+// Retention on tcgen05 tensor cores: bf16, Dx = 128 or up to 64 features (fewer are
+// filled up with zeros as they land), any multiple of 32 columns of w.
 //
 // A CTA works a slice of SW = 32 or 64 columns of w of one (batch, head) over a part
 // of the tokens, by chunks of 128 tokens.  Columns of the state do not meet, so
@@ -559,12 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     const int qd = warp - kWarpS;
     const int d = DX == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
     const bool mine = DX == 128 || lane < 16;
-    const int64_t size_of = static_cast<int64_t>(DX) * r.Dw;
+    const bool stored = mine && (DX == 128 || d < r.Dx);  // rows behind Dx stay zero
+    const int64_t size_of = static_cast<int64_t>(r.Dx) * r.Dw;
     float *rec = r.rec + bh * p.records * size_of;
     f2 S[SW / 2];
 #pragma unroll
     for (int e = 0; e < SW / 2; ++e) S[e] = dup2(0.f);
-    if (!STATE) {
+    if (!STATE && stored) {
       const int here = ret_before(part * p.cpp, n, tokens, kC, r.reverse);
       if (r.start) {
         const float f = exp2f(lg * static_cast<float>(here)) * r.start_scale;
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
           S[2 * e + 1] = fma2(f, pack2(v.z, v.w), S[2 * e + 1]);
         }
       }
-      if (last_part && r.end && mine) {
+      if (last_part && r.end) {
         // the end state: this part's start and its record, whose sums are exact to
         // fp32 (w~ as three values), while this pass makes do with one
         const f2 f = dup2(exp2f(lg * static_cast<float>(tokens - here)) * r.end_scale), one = dup2(r.end_scale);
@@ -599,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         }
       }
     }
+    __syncwarp();
     bool ok = true;
     for (int c = 0; c <= nc; ++c) {
       if (c > 0 && (c < nc || STATE)) {  // S <- g^n S + dS of chunk c - 1
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
         if (lane == 0) mbar_arrive(&bar[kSReady]);
       }
     }
-    if (STATE && ok && mine) {
+    if (STATE && ok && stored) {
       float4 *to = reinterpret_cast<float4 *>(rec + part * size_of + d * r.Dw + e0);
 #pragma unroll
       for (int e = 0; e < SW / 4; ++e) {
@@ -766,7 +768,7 @@ Cut cut_of(const RetArgs &a) {
 bool ret_tc_supported(const RetArgs &a, Dtype dt) {
   if (dt != kBF16) return false;
   for (int i = 0; i < a.roles; ++i)
-    if ((a.role[i].Dx != 64 && a.role[i].Dx != 128) || a.role[i].Dw % 32 != 0) return false;
+    if ((a.role[i].Dx > 64 && a.role[i].Dx != 128) || a.role[i].Dw % 32 != 0) return false;
   return true;
 }
 
@@ -788,12 +790,12 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
     bool end = false;
     for (int i = 0; i < a.roles; ++i) {
       const RetRole &r = a.role[i];
-      if (r.Dx != DX) continue;
+      if ((r.Dx <= 64 ? 64 : 128) != DX) continue;
       TcRole &m = p.map[p.a.roles];
       auto encode = [&](int i, const void *base, int width, int group, const RetStrides &s, int atom, int atoms) {
         return make_tmap_atoms(&m.m[i], base, width, a.H / group, a.L, a.B, s.h, s.t, s.b, atom, atoms, kC);
       };
-      if (!encode(0, r.x, DX, r.xg, r.xs, 64, DX / 64) || !encode(1, r.y, DX, r.yg, r.ys, 64, DX / 64) ||
+      if (!encode(0, r.x, r.Dx, r.xg, r.xs, 64, DX / 64) || !encode(1, r.y, r.Dx, r.yg, r.ys, 64, DX / 64) ||
           !encode(2, r.w, r.Dw, r.wg, r.ws, 32, SW / 32))
         return cudaErrorNotSupported;
       p.a.role[p.a.roles++] = r;

@@ -415,7 +415,7 @@ bool make_tmap_rows(CUtensorMap *map, const void *base, int elem_bytes, uint64_t
 // batch), strides in elements: coordinates (0, token, atom, head, batch) with atoms
 // of `atom` columns (32 or 64, the swizzle being as wide), boxes of `tokens_box`
 // tokens and `atoms_box` atoms, which land one atom behind the other.  Zero fill
-// out of bounds.
+// out of bounds, also behind rows narrower than an atom.
 bool make_tmap_atoms(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t tokens,
                      uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride, uint32_t atom,
                      uint32_t atoms_box, uint32_t tokens_box);

@@ -69,8 +69,8 @@ bool make_tmap_atoms(CUtensorMap *map, const void *base, uint64_t width, uint64_
                      uint64_t batch, int64_t head_stride, int64_t token_stride, int64_t batch_stride, uint32_t atom,
                      uint32_t atoms_box, uint32_t tokens_box) {
   auto fn = encode_fn();
-  if (!fn || (atom != 32 && atom != 64) || width % atom != 0) return false;
-  const cuuint64_t dims[5] = {atom, tokens, width / atom, heads, batch};
+  if (!fn || (atom != 32 && atom != 64) || (width > atom && width % atom != 0)) return false;
+  const cuuint64_t dims[5] = {width < atom ? width : atom, tokens, (width + atom - 1) / atom, heads, batch};
   const cuuint64_t strides[4] = {static_cast<cuuint64_t>(token_stride) * 2, atom * 2,
                                  static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(batch_stride) * 2};
   const cuuint32_t box[5] = {atom, tokens_box, atoms_box, 1, 1};

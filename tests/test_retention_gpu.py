@@ -558,6 +558,25 @@ def test_more_features_layouts(la, dtype, shape):
     test_layouts(la, dtype, shape)
 
 
+# fewer than 64 features (filled up with zeros on the tensor cores) and 128 and a few
+NARROW = [(2, 300, 2, 1, 32, 32), (1, 200, 2, 2, 8, 32), (1, 260, 3, 1, 40, 64), (2, 150, 2, 1, 160, 96),
+          (1, 1, 1, 1, 32, 32), (3, 129, 4, 2, 56, 128), (1, 140, 1, 1, 152, 160)]
+
+
+@DT
+@pytest.mark.parametrize("shape", NARROW, ids=sid)
+def test_fewer_features(la, dtype, shape):
+    test_forward(la, dtype, shape)
+    test_backward(la, dtype, shape)
+
+
+@DT
+def test_fewer_features_ragged_parts_layouts(la, dtype):
+    test_ragged(la, dtype, (6, 300, 2, 1, 32, 64))
+    test_parts(la, dtype, (1, 2600, 1, 1, 32, 32))
+    test_layouts(la, dtype, (2, 150, 4, 2, 32, 32))
+
+
 @DT
 @pytest.mark.parametrize("D", [64, 256])
 def test_out_off_the_sectors(la, dtype, D):
