@@ -608,11 +608,11 @@ LA_API la_status_t la_backward_norm_residual(const void *r, const float *w, cons
  *   effect; outputs there are left alone, gradients there are zero; the final
  *   state is the one after the last token.
  * - Arithmetic: fp32 states and sums, each output rounded once.  For LA_BF16
- *   with Dv a multiple of 32 and D up to 64, 128, up to 192 or 256 (gradients: the
- *   same of D and Dv in each other's place too) the products run on tcgen05
- *   tensor cores: there the weights of a chunk and the decayed rows
- *   that build the states for outputs are rounded to bf16 once, and states enter
- *   as sums of two bf16 values.  Returned states (S, dS0) are summed from decayed
+ *   with Dv a multiple of 32 and D at most 64, 128, at most 192 or 256 (gradients:
+ *   with D and Dv in each other's place too) the products run on tcgen05 tensor
+ *   cores: there the weights of a chunk and the decayed rows that build the states
+ *   for outputs are rounded to bf16 once, and states enter as sums of two bf16
+ *   values.  Returned states (S, dS0) are summed from decayed
  *   rows as three bf16 values, to fp32 accuracy.  Results do not depend on
  *   scheduling (no atomics).
  * - Within a chunk of up to 128 tokens a weight of zero times an infinity or NaN
