@@ -674,9 +674,9 @@ LA_API la_status_t la_backward_retention(const void *q, const void *k, const voi
  * its K beams' continuations: beam k with token v scores
  *   scores[b][k] + logits[b][k][v] - log sum_u exp(logits[b][k][u]).
  * out_scores fp32, parents and tokens int32, all [B][n], best first; equal
- * scores (as computed: rows that hold the same logits in another order, or all
- * moved by a constant, may differ by the roundings of their sums) in the order of
- * k, then v.  finished (optional, bytes [B][K]): a beam
+ * scores (as computed: rows of the same logits have the same sums wherever they
+ * lie; rows that hold them in another order, or all moved by a constant, may differ
+ * by the roundings of their sums) in the order of k, then v.  finished (optional, bytes [B][K]): a beam
  * that has ended, whose one continuation is `eos` at its own score.  A beam
  * whose score or log-sum is not finite (a start's unused beams at -inf, a row
  * with a NaN or +inf) offers nothing, nor does a logit of -inf (a forbidden

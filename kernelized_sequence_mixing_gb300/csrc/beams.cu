@@ -60,7 +60,11 @@ struct SelectParams {
   int pieces;  // of a row
 };
 
-// 16 bytes of logits: how many, the pattern of -inf, and their values.
+// 16 bytes of logits: how many, the pattern of -inf, their values, and how they are
+// loaded from where a row off the 16-byte boundary has them (each word of 4 bytes;
+// four lanes share a sector, which L1 holds between the loads).  over: the words
+// reach over the group's ends, by one value of the row each way.  some: the first n
+// values of a group alone, one by one.
 template <typename T>
 struct vec16;
 template <>
@@ -69,6 +73,16 @@ struct vec16<float> {
   static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void get(const uint4 &v, float *x) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ bool over(const float *) { return false; }
+  static __device__ __forceinline__ uint4 load(const float *p, bool aligned) {
+    if (aligned) return __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+    return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+  }
+  static __device__ __noinline__ uint4 some(const float *p, int n) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+    return make_uint4(w[0], n > 1 ? w[1] : kNone, n > 2 ? w[2] : kNone, n > 3 ? w[3] : kNone);
   }
 };
 template <>
@@ -83,49 +97,110 @@ struct vec16<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ bool over(const __nv_bfloat16 *p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; }
+  static __device__ __forceinline__ uint4 load(const __nv_bfloat16 *p, bool aligned) {
+    if (!over(p)) return vec16<float>::load(reinterpret_cast<const float *>(p), aligned);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p - 1);
+    uint32_t a[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) a[i] = __ldg(w + i);
+    return make_uint4(__funnelshift_r(a[0], a[1], 16), __funnelshift_r(a[1], a[2], 16),
+                      __funnelshift_r(a[2], a[3], 16), __funnelshift_r(a[3], a[4], 16));
+  }
+  static __device__ __noinline__ uint4 some(const __nv_bfloat16 *p, int n) {
+    const uint16_t *w = reinterpret_cast<const uint16_t *>(p);
+    uint32_t a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = (2 * i < n ? w[2 * i] : kNone & 0xffffu) | (2 * i + 1 < n ? w[2 * i + 1] : kNone & 0xffffu) << 16;
+    return make_uint4(a[0], a[1], a[2], a[3]);
+  }
 };
 
-// A piece is VALUES values per thread, in 16-byte groups dealt out to the
-// threads in turn, from the row's first 16-byte boundary at or in front of it.
+// The groups of a row off the 16-byte boundary, from the aligned 16 bytes in which
+// they begin: each lane takes what is missing from the next lane, lane 31 from the
+// first lane of the next warp (edge[8 g]).  WS whole words in front of the group and
+// `bits`, 0 or 16, more.
+template <int WS, int G>
+__device__ __forceinline__ void shift_groups(uint4 (&raw)[G], const uint4 *edge, int lane, int bits) {
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    uint32_t w[8] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+#pragma unroll
+    for (int j = 0; j <= WS; ++j) {
+      w[4 + j] = __shfl_down_sync(~0u, w[j], 1);
+      if (lane == 31) w[4 + j] = reinterpret_cast<const uint32_t *>(edge + 8 * g)[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[WS + j] = __funnelshift_r(w[WS + j], w[WS + j + 1], bits);
+    raw[g] = make_uint4(w[WS], w[WS + 1], w[WS + 2], w[WS + 3]);
+  }
+}
+
+// A piece is VALUES values per thread, in groups of 16 bytes dealt out to the
+// threads in turn from the row's first value on, wherever that lies: rows of the
+// same logits have the same sums to the last bit, so that equal beams tie.
 template <typename T, int VALUES>
 __global__ void __launch_bounds__(kThreads, 5) beams_piece_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kN = vec16<T>::kN, kGroups = VALUES / kN;
   __shared__ float top[128];
   __shared__ float kept[kKept];
   __shared__ int place[kKept];
+  // rows off the boundary: bf16 by aligned loads and a shift (64 x 16 x 50257: 64 us,
+  // in words 70, on the boundary 60), fp32 in words (73 and 66; the shift spills: 86)
+  constexpr bool kShift = sizeof(T) == 2;
+  __shared__ uint4 edges[kShift ? 8 * kGroups + 1 : 1];  // what each warp's first lane loads
   __shared__ float warp_max[kThreads / 32], warp_sum[kThreads / 32], bound;
   __shared__ int count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int piece = blockIdx.x % p.pieces;
   const int64_t row = blockIdx.x / p.pieces;
   const T *x = static_cast<const T *>(p.a.logits) + row * p.a.ld;
-  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kN);  // values in front of the row
+  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16);  // bytes behind the boundary
   const int V = p.a.V, n = p.a.n;
-  const int base = piece * (kThreads * VALUES) - skew;  // of this piece in the row (V is at most 2^30)
+  const int base = piece * (kThreads * VALUES);  // of this piece in the row (V is at most 2^30)
   if (tid == 0) count = 0;
-  // all loads under way before the first value is used; groups across the row's
-  // ends (only of rows off the 16-byte boundary) one by one behind them
+  // all loads under way before the first value is used
   uint4 raw[kGroups];
   auto at = [&](int g) { return base + (g * kThreads + tid) * kN; };
-  const bool inside = base >= 0 && base + kThreads * VALUES <= V;  // the whole piece
-  if (inside) {
+  if (skew == 0 && base + kThreads * VALUES <= V) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(x + at(g)));
+  } else if (kShift && skew != 0 && (base > 0 || row > 0) && base + kThreads * VALUES + kN <= V) {
+    // from the boundary in front of the piece to the one behind it: all of the tensor
+    if constexpr (kShift) {
+      const T *from = x - skew / static_cast<int>(sizeof(T));
+      if (tid == 0) edges[8 * kGroups] = __ldg(reinterpret_cast<const uint4 *>(from + base + kThreads * VALUES));
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(from + at(g)));
+      if (lane == 0)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) edges[8 * g + warp] = raw[g];
+      __syncthreads();
+      const int bits = skew % 4 * 8;
+      if (skew < 4) shift_groups<0>(raw, edges + warp + 1, lane, bits);
+      else if (skew < 8) shift_groups<1>(raw, edges + warp + 1, lane, bits);
+      else if (skew < 12) shift_groups<2>(raw, edges + warp + 1, lane, bits);
+      else shift_groups<3>(raw, edges + warp + 1, lane, bits);
+    }
   } else {
+    // a piece at the row's end, or in words: groups across the row's end (loaded in
+    // words that reach over theirs: at either end) value by value, behind the others
+    const bool over = vec16<T>::over(x);
+    auto whole = [&](int g) { return at(g) >= over && at(g) + kN + over <= V; };
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       raw[g] = make_uint4(vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone, vec16<T>::kNone);
-      if (at(g) >= 0 && at(g) + kN <= V) raw[g] = __ldcs(reinterpret_cast<const uint4 *>(x + at(g)));
+      if (whole(g)) raw[g] = vec16<T>::load(x + at(g), skew == 0);
     }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+      if (!whole(g) && at(g) < V) raw[g] = vec16<T>::some(x + at(g), V - at(g));
   }
   float v[VALUES], most[kGroups], m = -INFINITY;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     vec16<T>::get(raw[g], v + g * kN);
-    if (!inside && ((at(g) < 0 && at(g) + kN > 0) || (at(g) < V && at(g) + kN > V))) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) v[g * kN + i] = at(g) + i >= 0 && at(g) + i < V ? io<T>::load(x + at(g) + i) : -INFINITY;
-    }
     most[g] = v[g * kN];
 #pragma unroll
     for (int i = 1; i < kN; ++i) most[g] = fmaxf(most[g], v[g * kN + i]);
@@ -435,7 +510,7 @@ int values_of(int64_t rows, int V) { return rows * ((V + 8191) / 8192) >= 2 * kS
 
 int pieces_of(int64_t rows, int V) {
   const int piece = kThreads * values_of(rows, V);
-  return (V + 7 + piece - 1) / piece;  // 7: values in front of an unaligned row
+  return (V + piece - 1) / piece;
 }
 
 // --- reordering ---

@@ -751,3 +751,22 @@ def test_select_largest(la):
     check_select(la, torch.zeros(3, 1, 1), torch.zeros(3, 1), 1)
     check_select(la, torch.randn(1, 2, 1 << 20, generator=g), torch.randn(1, 2, generator=g), 64)
     check_select(la, torch.randn(1, 1, 64, generator=g), torch.zeros(1, 1), 64)
+
+
+@DT
+@pytest.mark.parametrize("B,K,V,n", [(3, 4, 1001, 9), (1, 4, 131071, 8), (1, 8, 5003, 40), (80, 4, 9001, 9), (2, 32, 63, 64)])
+def test_select_equal_rows(la, dtype, B, K, V, n):
+    """Beams of equal scores that hold the same logits: equal continuations go in the
+    order of the beams wherever their rows lie relative to a 16-byte boundary, and
+    the scores' bits do not depend on where the logits lie or how far apart the rows
+    are."""
+    g = torch.Generator().manual_seed(V)
+    row, scores = torch.randn(B, 1, V, generator=g) * 3, torch.randn(B, 1, generator=g).expand(B, K).contiguous()
+    logits = row.expand(B, K, V).to(dtype)
+    want = check_select(la, logits.contiguous(), scores, n)
+    for off, pad in ((0, 1), (1, 0), (2, 3), (3, 8), (5, 2), (7, 5)):
+        wide = torch.full((off + B * K * (V + pad),), float("nan"), dtype=dtype, device="cuda")
+        x = wide[off:].view(B, K, V + pad)[..., :V]
+        x.copy_(logits)
+        got = la.select_beams(x, scores.cuda(), n=n)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (off, pad)
