@@ -2,13 +2,14 @@
 // and the states' reordering.
 //
 // Selection.  A continuation (k, v) of request b scores
-//   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]).
-// Within a beam the order of continuations is the order of its logits, so one
-// pass over the logits serves: each CTA takes a piece of a row that fits its
-// registers and leaves the piece's maximum, its sum of exponentials relative to
-// that, and its n largest logits in order (ties: lowest index first).  A second
-// kernel, one CTA per request, joins the sums in 64 bits and takes the n best
-// of the sorted lists.  Bound by HBM (the logits are read once) with one
+//   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]),
+// computed as the score less the log of the sum relative to the row's maximum, plus
+// the logit's distance from the maximum.  Within a beam the order of continuations is
+// the order of its logits, so one pass over the logits serves: each CTA takes a piece
+// of a row that fits its registers and leaves the piece's maximum, its sum of
+// exponentials relative to that, and its n largest logits in order (ties: lowest index
+// first).  A second kernel, one CTA per request, joins the sums in 64 bits and takes the n
+// best of the sorted lists.  Bound by HBM (the logits are read once) with one
 // exponential per logit beside it (16 a clock and SM).
 //
 // The n largest of a piece: the n-th largest of the maxima of 32 or 128 groups of
@@ -364,13 +365,16 @@ __device__ __forceinline__ bool ahead(const Cand &a, const Cand &b) {
   return a.key > b.key || (a.key == b.key && a.at < b.at);
 }
 
-// The n best of a request's lists.  Rows first: the log of each row's sum, and
-// with it the offset score - lse in 64 bits (-inf for a row that offers
-// nothing).  Then the first entries of the lists, one per thread, of which the
+// The n best of a request's lists.  Rows first: the log of each row's sum relative
+// to its maximum, and with it the offset score - log in 64 bits (-inf for a row that
+// offers nothing), to which a logit's distance from the maximum is added (a row of
+// the type's lowest value would swallow score and log, were they added to the
+// logits).  Then the first entries of the lists, one per thread, of which the
 // n-th largest bounds the n-th best continuation; and the candidates that are
 // not below it, ranked.
 __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_constant__ SelectParams p) {
   __shared__ double offset[kMaxBeams], lse[kMaxBeams];
+  __shared__ float most[kMaxBeams];
   __shared__ uint8_t done[kMaxBeams];
   __shared__ Cand cand[kCand];
   __shared__ int64_t heads[kThreads];
@@ -409,12 +413,13 @@ __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_const
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-    if (lane == 0) lse[k] = m + log_of(t);
+    if (lane == 0) lse[k] = log_of(t), most[k] = m;
   }
   __syncthreads();
   if (tid < K) {
     const double l = own_done ? 0.0 : lse[tid];
-    offset[tid] = isfinite(own_score) && isfinite(l) ? own_score - l : -INFINITY;
+    if (own_done) most[tid] = 0.f;
+    offset[tid] = isfinite(own_score) && isfinite(l) && isfinite(most[tid]) ? own_score - l : -INFINITY;
   }
   __syncthreads();
   // entry i of list l (a finished beam has one, its end token at no cost, in
@@ -428,7 +433,8 @@ __global__ void __launch_bounds__(kThreads) beams_join_kernel(const __grid_const
     const int in = l * n + i;
     const int v = held ? held_index[in] : p.out.index[first * n + in];
     if (v < 0) return {nothing, INT64_MAX};
-    return {key_of(off + (held ? held_value[in] : p.out.value[first * n + in])), row | v};
+    const double below = static_cast<double>(held ? held_value[in] : p.out.value[first * n + in]) - most[k];
+    return {key_of(off + below), row | v};
   };
   // one entry per thread: so deep into the lists that there are 4 n, or the best
   // head of several lists

@@ -84,7 +84,7 @@ def select(logits, scores, n, finished=None, eos=None):
             m = x.max() if not np.isnan(x).any() else np.nan
             if not np.isfinite(m):
                 continue
-            total = s + (x - (m + np.log(np.exp(x - m).sum())))
+            total = s + ((x - m) - np.log(np.exp(x - m).sum()))
             # candidates behind the n-th of their own row never enter
             keep = np.lexsort((np.arange(V), -x))[:n]
             cand += [(-total[i], k, int(i)) for i in keep if np.isfinite(x[i])]

@@ -770,3 +770,26 @@ def test_select_equal_rows(la, dtype, B, K, V, n):
         x.copy_(logits)
         got = la.select_beams(x, scores.cuda(), n=n)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), (off, pad)
+
+
+@DT
+@pytest.mark.parametrize("B,K,V,n", [(1, 4, 333, 7), (2, 3, 5003, 40), (80, 4, 9001, 8)])
+def test_select_rows_of_the_lowest_value(la, dtype, B, K, V, n):
+    """A row whose logits are all masked with the type's lowest value, or all as large
+    as the type goes, is a uniform one: its scores are those of zeros."""
+    g = torch.Generator().manual_seed(V)
+    scores = torch.randn(B, K, generator=g)
+    flat = torch.zeros(B, K, V, dtype=dtype)
+    want = check_select(la, flat, scores, n)
+    for value in (torch.finfo(dtype).min, torch.finfo(dtype).max, -1e30, 3e4):
+        got = la.select_beams(torch.full_like(flat, value).cuda(), scores.cuda(), n=n)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), value
+    # a masked row beside others, masked values among a row's own
+    x = (torch.randn(B, K, V, generator=g) * 3).to(dtype)
+    x[:, 1] = torch.finfo(dtype).min
+    x[:, 2, ::3] = torch.finfo(dtype).min
+    got = la.select_beams(x.cuda(), scores.cuda(), n=n)
+    alike = x.clone()
+    alike[:, 1] = 0
+    ref = check_select(la, alike, scores, n)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
