@@ -793,3 +793,23 @@ def test_select_rows_of_the_lowest_value(la, dtype, B, K, V, n):
     alike[:, 1] = 0
     ref = check_select(la, alike, scores, n)
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@DT
+@pytest.mark.parametrize("B,K,V,n", [(1, 32, 100, 64), (2, 32, 5000, 64), (1, 20, 70001, 7), (80, 4, 9001, 8), (80, 4, 9001, 64)])
+def test_select_more_ties_than_buffers(la, dtype, B, K, V, n):
+    """Equal logits in all beams: more candidates than the joining pass ranks at once
+    (lists in and beyond shared memory), more values in a piece than it collects
+    (short and long pieces, few and many places); beams that have ended, rows that
+    offer nothing and beams without a score among them."""
+    flat = torch.full((B, K, V), 0.5, dtype=dtype)
+    scores = torch.full((B, K), -2.0)
+    check_select(la, flat, scores, n)
+    finished = torch.zeros(B, K, dtype=torch.bool)
+    finished[:, 1] = True
+    flat[:, 2] = float("-inf")
+    flat[0, 0, V // 2] = 0.75                        # one that is ahead, and one behind
+    flat[0, 0, 3] = 0.25
+    scores[:, 3] = float("-inf")
+    check_select(la, flat, scores, n, finished, V - 1)
+    check_select(la, torch.full((B, K, V), torch.finfo(dtype).min, dtype=dtype), scores, n)
