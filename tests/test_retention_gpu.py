@@ -813,3 +813,61 @@ def test_select_more_ties_than_buffers(la, dtype, B, K, V, n):
     scores[:, 3] = float("-inf")
     check_select(la, flat, scores, n, finished, V - 1)
     check_select(la, torch.full((B, K, V), torch.finfo(dtype).min, dtype=dtype), scores, n)
+
+
+def paired(g, *shape):
+    """fp32 values that differ by up to 2^-9 within each 2 x 2 block of their last two
+    dimensions: the first bf16 values of a pair are equal or a step apart."""
+    *lead, a, b = shape
+    base = (1 + torch.rand(*lead, a // 2, b // 2, generator=g)) * (2 * torch.randint(0, 2, (*lead, a // 2, b // 2), generator=g) - 1)
+    wide = base.repeat_interleave(2, -2).repeat_interleave(2, -1)
+    return wide * (1 + (2 * torch.rand(shape, generator=g) - 1) * 2.0 ** -9)
+
+
+def differences(g, B, L, H, W):
+    """Rows of bf16 that read the difference of one pair of a state's rows."""
+    x = torch.zeros(B, L, H, W // 2, 2)
+    v = torch.randn(B, L, H, generator=g)
+    pair = torch.arange(L) % (W // 2)
+    x[:, torch.arange(L), :, pair, 0] = v.permute(1, 0, 2)
+    x[:, torch.arange(L), :, pair, 1] = -v.permute(1, 0, 2)
+    return x.view(B, L, H, W).to(BF16)
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 2, 2, 64, 64), (2, 300, 2, 2, 128, 128), (1, 400, 4, 2, 128, 64),
+                                   (1, 3000, 2, 2, 64, 64), (1, 300, 2, 1, 256, 64), (1, 300, 2, 1, 64, 256),
+                                   (1, 300, 2, 2, 40, 32)], ids=sid)
+def test_both_values_of_a_state(la, shape):
+    """The states of the tensor-core kernel are sums of two bf16 values.  Here nothing
+    but a state enters (no k, v or no q, dO: no weight or decayed row is rounded) and
+    its rows are read as differences in which the first values nearly cancel, so
+    that what is left of the bound is 2^-16 of the state (2^-8 of what the first
+    value leaves, itself 2^-8), fp32 sums and the output's own rounding.  A state of
+    one value, or with the second of another chunk, is many times beyond it."""
+    B, L, H, Hk, D, Dv = shape
+    g = torch.Generator().manual_seed(D + Dv + L)
+    zk, zv = torch.zeros(B, L, Hk, D, dtype=BF16), torch.zeros(B, L, Hk, Dv, dtype=BF16)
+    zq, zo = torch.zeros(B, L, H, D, dtype=BF16), torch.zeros(B, L, H, Dv, dtype=BF16)
+    q, do = differences(g, B, L, H, D), differences(g, B, L, H, Dv)
+    k, v = differences(g, B, L, Hk, D), differences(g, B, L, Hk, Dv)
+    S = paired(g, B, H, D, Dv)
+    gamma, scale = torch.tensor([1.0] + [1 - 2.0 ** -8] * (H - 1)), 0.3
+    K = 2 * L + 2 * D + 2 * Dv + 64 + H // Hk
+    c = lambda *ts: [t.cuda() for t in ts]  # noqa: E731
+    rounded = S.to(BF16).float()
+
+    def check(name, got, call):
+        ref, mag, one = call(S, False), call(S, True), call(rounded, False)
+        tol = torch.finfo(BF16).eps / 2 * np.abs(ref) + (K * 2.0 ** -24 + 2.0 ** -16) * mag + 1e-37
+        worst = float((np.abs(n64(got) - ref) / tol).max())
+        record(f"retention {name} of a state alone bfloat16 (share of its bound)", worst, 1)
+        assert (np.abs(one - ref) / tol).max() > 8, "the first value alone has to be beyond the bound"
+        assert worst <= 1, f"{name}: {worst} times its bound"
+
+    r = lambda i, *a: lambda S, mag: ort.backward(*map(n64, a), n64(gamma), scale, *(n64(s) for s in ((S, None) if i == 0 else (None, S))), mag=mag)[i]  # noqa: E501,E731
+    check("o", la.forward_retention(*c(q, zk, v), gamma, scale, S.cuda()),
+          lambda S, mag: ort.forward(n64(q), n64(zk), n64(v), n64(gamma), scale, n64(S), mag=mag)[0])
+    check("dq", la.backward_retention(*c(zq, k, zv, do), gamma, scale, S.cuda())[0], r(0, zq, k, zv, do))
+    dq, dk, dv, _ = la.backward_retention(*c(zq, k, v, zo), gamma, scale, dS=S.cuda())
+    check("dk", dk, r(1, zq, k, v, zo))
+    check("dv", dv, r(2, zq, k, v, zo))
