@@ -604,8 +604,7 @@ LA_API la_status_t la_backward_norm_residual(const void *r, const float *w, cons
  * - Sizes: D and Dv multiples of 8 up to 256, H <= 256, B L < 2^31 - 2^16
  *   tokens, B H < 2^26.  |scale| between 2^-64 and 2^64.
  * - lens (optional, int32 [B] in DEVICE memory, 4-byte aligned): sequence b has
- *   lens[b] tokens (clamped to [0, L]).  Rows behind it are not read and have no
- *   effect; outputs there are left alone, gradients there are zero; the final
+ *   lens[b] tokens (clamped to [0, L]).  Rows behind it have no effect; outputs there are left alone, gradients there are zero; the final
  *   state is the one after the last token.
  * - Arithmetic: fp32 states and sums, each output rounded once.  For LA_BF16
  *   with Dv a multiple of 32 and D at most 64, 128, at most 192 or 256 (gradients:
@@ -618,8 +617,9 @@ LA_API la_status_t la_backward_norm_residual(const void *r, const float *w, cons
  * - Within a chunk of up to 128 tokens a weight of zero times an infinity or NaN
  *   of a later token is NaN: inputs are finite.
  * - Few (batch, head) pairs split long sequences into parts that run side by
- *   side, with a workspace of B*H*D*Dv*4 bytes for each part but the last (for it
- *   too where a state is returned).  More than 128 features are worked as 128 and
+ *   side, with a workspace of B*H*D*Dv*4 bytes for each part but the last
+ *   (gradients: three times that); where a state is returned from the tensor cores,
+ *   once more for the last part.  More than 128 features are worked as 128 and
  *   the rest, with a workspace of 2*B*L*H*Dv*4 bytes for the two shares of o.
  *   Workspaces as in the selective scan's family; no written buffer may overlap
  *   any other buffer of the call.

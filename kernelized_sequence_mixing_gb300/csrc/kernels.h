@@ -332,6 +332,7 @@ struct RetRole {
   int64_t state;  // elements between the states of start and end (Dx Dw, or more for a role of some features)
   float start_scale, end_scale, out_scale;
   int reverse, o_f32;
+  int records;  // one for each part but the last; on tensor cores one more where there is an end
 };
 constexpr int kRetRoles = 6;
 struct RetArgs {
@@ -342,13 +343,11 @@ struct RetArgs {
   bool fill;  // rows behind a sequence's end become zero (otherwise they are left)
   Gammas lg;  // log2 of each head's decay
 };
-// Parts of the tokens that run side by side; records of a (batch, head) (the last
-// part has one too where some role wants its end state) and their size in floats
-// over all roles; the kernels take a.role[].rec as laid out by ret_layout.
+// Parts of the tokens that run side by side; the size in floats of the records of all
+// roles; the kernels take a.role[].rec and records as laid out by ret_layout.
 int ret_parts(const RetArgs &a, Dtype dt);
-int ret_records(const RetArgs &a, int parts);
-size_t ret_record_floats(const RetArgs &a, int parts);
-void ret_layout(RetArgs *a, int parts, float *ws);
+size_t ret_record_floats(const RetArgs &a, Dtype dt, int parts);
+void ret_layout(RetArgs *a, Dtype dt, int parts, float *ws);
 cudaError_t launch_retention(const RetArgs &a, Dtype dt, int parts, cudaStream_t s);
 bool ret_tc_supported(const RetArgs &a, Dtype dt);
 cudaError_t launch_retention_simt(const RetArgs &a, Dtype dt, int parts, cudaStream_t s);

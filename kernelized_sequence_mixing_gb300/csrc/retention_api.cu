@@ -121,11 +121,11 @@ struct Plan {
 
   la_status_t run(Dtype dt, cudaStream_t s) {
     const int parts = ret_parts(a, dt);
-    return with_workspace(sizeof(float) * (share + ret_record_floats(a, parts)), s, [&](void *ws) {
+    return with_workspace(sizeof(float) * (share + ret_record_floats(a, dt, parts)), s, [&](void *ws) {
       char *base = static_cast<char *>(ws);
       for (int i = 0; i < a.roles; ++i)
         if (a.role[i].o_f32) a.role[i].o = base + reinterpret_cast<size_t>(a.role[i].o);
-      ret_layout(&a, parts, static_cast<float *>(ws) + share);
+      ret_layout(&a, dt, parts, static_cast<float *>(ws) + share);
       const cudaError_t e = launch_retention(a, dt, parts, s);
       for (int i = 0; i < sums; ++i)
         sum[i].part = reinterpret_cast<const float *>(base + reinterpret_cast<size_t>(sum[i].part));

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, NI == 1 ? 2 : 1)
   const T *x = static_cast<const T *>(r.x) + b * r.xs.b + (h / r.xg) * r.xs.h;
   const T *y = static_cast<const T *>(r.y) + b * r.ys.b + (h / r.yg) * r.ys.h;
   const T *wp = static_cast<const T *>(r.w) + b * r.ws.b + (h / r.wg) * r.ws.h + e0;
-  const float *rec = r.rec + bh * (p.parts - 1) * Dx * Dw;
+  const float *rec = r.rec + bh * r.records * Dx * Dw;
   const int after = r.reverse ? 0 : 1;  // o_0 meets the state in front of it decayed once, in time
   int sh = 0;
   while ((kPer << sh) < Dx) ++sh;
@@ -480,22 +480,25 @@ cudaError_t launch_group_sums(const GroupSumArgs *a, int n, Dtype dt, cudaStream
 
 int ret_parts(const RetArgs &a, Dtype dt) { return ret_tc_supported(a, dt) ? ret_parts_tc(a) : ret_parts_simt(a); }
 
-int ret_records(const RetArgs &a, int parts) {
-  for (int i = 0; i < a.roles; ++i)
-    if (a.role[i].end) return parts;
-  return parts - 1;
-}
+// The tensor-core kernel takes a returned state from a record of the last part too,
+// the other one from its registers.
+static int records_of(const RetRole &r, bool tc, int parts) { return tc && r.end ? parts : parts - 1; }
 
-size_t ret_record_floats(const RetArgs &a, int parts) {
+size_t ret_record_floats(const RetArgs &a, Dtype dt, int parts) {
+  const bool tc = ret_tc_supported(a, dt);
   size_t n = 0;
-  for (int i = 0; i < a.roles; ++i) n += static_cast<size_t>(a.role[i].Dx) * a.role[i].Dw;
-  return n * a.B * a.H * ret_records(a, parts);
+  for (int i = 0; i < a.roles; ++i)
+    n += static_cast<size_t>(a.role[i].Dx) * a.role[i].Dw * records_of(a.role[i], tc, parts);
+  return n * a.B * a.H;
 }
 
-void ret_layout(RetArgs *a, int parts, float *ws) {
+void ret_layout(RetArgs *a, Dtype dt, int parts, float *ws) {
+  const bool tc = ret_tc_supported(*a, dt);
   for (int i = 0; i < a->roles; ++i) {
-    a->role[i].rec = ws;
-    ws += static_cast<size_t>(a->B) * a->H * ret_records(*a, parts) * a->role[i].Dx * a->role[i].Dw;
+    RetRole &r = a->role[i];
+    r.rec = ws;
+    r.records = records_of(r, tc, parts);
+    ws += static_cast<size_t>(a->B) * a->H * r.records * r.Dx * r.Dw;
   }
 }
 

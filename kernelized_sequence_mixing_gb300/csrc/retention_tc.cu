@@ -37,7 +37,8 @@
 // Two passes where the tokens are cut into parts: one sums each part's own state
 // (no x, no weights, no outputs), the other starts from those sums.  A returned
 // state is the sum of all parts' records, built from decayed rows as three bf16
-// values (fp32 accuracy); states for outputs make do with one.
+// values (fp32 accuracy); states for outputs make do with one (but where the roles of
+// a launch share that pass with one that returns its state, all have three).
 //
 // Bound by shared memory: an MMA reads its A operand (and the table, w~ and the
 // staging of the state pass through it too), about 2400 cycles a chunk of 128
@@ -128,7 +129,7 @@ struct TcRole {
 struct TcParams {
   RetArgs a;
   TcRole map[kRetRoles];
-  int parts, cpp, slices, records;  // records: of a (batch, head), parts - 1 or parts
+  int parts, cpp, slices, records;  // records: of the role of this launch that has most
   bool sectors;
   unsigned int *timeouts;
 };
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
   const int64_t bh = blockIdx.x / p.slices / np;
   const int e0 = slice * SW;
   // the last part's record serves the end state alone
-  if (e0 >= r.Dw || (STATE && part == p.parts - 1 && !r.end)) return;
+  if (e0 >= r.Dw || (STATE && part >= r.records)) return;
   const int b = static_cast<int>(bh / p.a.H), h = static_cast<int>(bh % p.a.H);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int tokens = uniform(ret_tokens(p.a.lens, b, p.a.L));
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) retention_tc_kernel(const __grid_
     const bool mine = DX == 128 || lane < 16;
     const bool stored = mine && (DX == 128 || d < r.Dx);  // rows behind Dx stay zero
     const int64_t size_of = static_cast<int64_t>(r.Dx) * r.Dw;
-    float *rec = r.rec + bh * p.records * size_of;
+    float *rec = r.rec + bh * r.records * size_of;
     f2 S[SW / 2];
 #pragma unroll
     for (int e = 0; e < SW / 2; ++e) S[e] = dup2(0.f);
@@ -800,11 +801,11 @@ cudaError_t launch_retention_tc(const RetArgs &a, int parts, cudaStream_t s) {
         return cudaErrorNotSupported;
       p.a.role[p.a.roles++] = r;
       if (r.Dw / SW > p.slices) p.slices = r.Dw / SW;
+      if (r.records > p.records) p.records = r.records;
       end |= r.end != nullptr;
       p.sectors &= reinterpret_cast<uintptr_t>(r.o) % 32 == 0 && (r.os.b | r.os.t | r.os.h) % 16 == 0;
     }
     if (!p.a.roles) continue;
-    p.records = ret_records(a, parts);
     const int64_t units = static_cast<int64_t>(a.B) * a.H * p.slices;
     if (units * parts >= (1LL << 31)) return cudaErrorNotSupported;
     cudaError_t e;

@@ -871,3 +871,45 @@ def test_both_values_of_a_state(la, shape):
     dq, dk, dv, _ = la.backward_retention(*c(zq, k, v, zo), gamma, scale, dS=S.cuda())
     check("dk", dk, r(1, zq, k, v, zo))
     check("dv", dv, r(2, zq, k, v, zo))
+
+
+def nodes(call):
+    """(launches, allocations) of a call, from the graph that it is captured into."""
+    import ctypes
+    call()  # kernels are loaded outside the capture
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        out = call()  # noqa: F841
+    cu, count = ctypes.CDLL("libcuda.so.1"), ctypes.c_size_t(0)
+    raw = ctypes.c_void_p(graph.raw_cuda_graph())
+    assert cu.cuGraphGetNodes(raw, None, ctypes.byref(count)) == 0
+    all_nodes = (ctypes.c_void_p * count.value)()
+    assert cu.cuGraphGetNodes(raw, all_nodes, ctypes.byref(count)) == 0
+    kinds = []
+    for node in all_nodes:
+        kind = ctypes.c_int(-1)
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        kinds.append(kind.value)
+    return kinds.count(0), kinds.count(10)  # kernel, memory allocation
+
+
+def test_no_records_that_nothing_reads(la):
+    """Sequences of one part: a record is kept for a returned state of the tensor-core
+    kernel alone, and no pass that sums states runs for roles without one."""
+    def run(shape, dtype, backward, S0=True):
+        B, L, H, Hk, D, Dv = shape
+        p = Problem(shape, dtype, 1, start=S0)
+        q, k, v, do = *p.dev(), p.do.cuda()
+        kw = p.kw()
+        if backward:
+            return nodes(lambda: la.backward_retention(q, k, v, do, **kw))
+        out, S = torch.empty_like(do), torch.empty(B, H, D, Dv, device="cuda")
+        return nodes(lambda: la.forward_retention(q, k, v, **kw, out=out, S=S))
+
+    wide = (2, 60, 200, 200, 64, 64)
+    assert run(wide, F32, False) == (1, 0)
+    assert run(wide, F32, True) == (1, 0)
+    assert run((2, 60, 4, 4, 96, 40), BF16, False) == (1, 0)         # on CUDA cores
+    assert run((2, 300, 4, 4, 64, 64), BF16, False) == (2, 1)        # the state's pass and the outputs'
+    assert run((2, 300, 4, 4, 128, 64), BF16, True) == (3, 1)        # dq and dk of 64 features: no states to sum
+    assert run((2, 300, 4, 4, 128, 64), BF16, True, S0=False) == (2, 0)
