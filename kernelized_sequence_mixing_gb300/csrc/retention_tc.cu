@@ -40,9 +40,11 @@
 // values (fp32 accuracy); states for outputs make do with one (but where the roles of
 // a launch share that pass with one that returns its state, all have three).
 //
-// Bound by shared memory: an MMA reads its A operand (and the table, w~ and the
-// staging of the state pass through it too), about 2400 cycles a chunk of 128
-// features and 32 columns against 700 of products.  Measured: B2 L16384 H16 D128
+// Bound by no unit but by the chain of waits of one CTA an SM (weights, P, O2, outputs;
+// dS, state, O1): about 2400 cycles a chunk of 128 features and 32 columns against 700
+// of products.  On an SM that works (128 of 152 at B2 H16) the tensor pipe is busy 41%
+// of the time, its reading of operands 48%, the pipe of shared memory 49%, and half of
+// the issue slots are taken.  Measured: B2 L16384 H16 D128
 // forward 162 us (3.3 TB/s of q, k, v, o; 0.49 of the copy rate); B1 L65536 H8|4 D128
 // with the final state 199 us; backward B4 L4096 H8 D64 63 us.
 #include <type_traits>
